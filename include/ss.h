@@ -509,6 +509,213 @@ typedef struct {
 size_t ss_fused_scratch_bytes(int32_t batch);
 ss_status ss_fused_lmhead_sample(const ss_fused_args* args, ss_stream_t stream);
 
+/* ---------------------------------------------------------- paged cache --
+ * The keys and values that a target model's verification step attends to, in
+ * pages: token number t of request r lies in page page_table[r][t / page_size],
+ * slot t % page_size.  A verification step with this library is
+ *   ss_pages_reserve     pages for the step's new tokens
+ *   per layer            ss_cache_append, ss_cache_attention
+ *   ss_spec_verify or ss_tree_verify on the target's logits
+ *   ss_commit_accepted, ss_pages_compact (trees), ss_pages_trim
+ * The step's new tokens of a request are those its target rows belong to: the
+ * last emitted token (a tree's root) and the drafts, in the order of the
+ * target rows.  Throughout, kv_len[r] is the number of tokens in the cache
+ * before the step; new token i is cached at slot number kv_len[r] + i.
+ *
+ * All arrays are device memory, all calls asynchronous on `stream` and
+ * capturable in a CUDA graph; none allocates or synchronises.  Statuses are
+ * SS_ROW_* codes, one per request, 0 when all is well.  An entry of the page
+ * table outside [0, num_pages) is a hole: nothing is written to it and its
+ * tokens are invisible to attention. */
+typedef enum {
+  SS_CACHE_BF16 = 0,
+  SS_CACHE_INT4 = 1 /* per (token, kv head) row x[0 .. head_dim) of K and of V: a low value m = min x
+                       and a step s = the smallest bf16 >= (max x - m) / 15 (in fp32), both bf16, and
+                       per channel n = min(15, round-half-even((x - m) / s)), 0 when s = 0; the row
+                       stands for s * n + m.  A row with a NaN, an infinity or max x - m beyond fp32
+                       has s = m = NaN.  Packed little-endian, eight channels per 32-bit word: channel
+                       2i of the eight in bits 4i.. , channel 2i + 1 in bits 16 + 4i.. (i = 0..3).
+                       The scale arrays hold the pair (s, m) per row. */
+} ss_cache_format;
+
+/* One cache: [num_layers][num_pages][num_kv_heads][page_size] rows of K and of
+ * V in any order of those four (strides in bytes, the same for K and V). */
+typedef struct {
+  int32_t format;               /* ss_cache_format                                */
+  int32_t num_layers;
+  int32_t num_pages;
+  int32_t num_kv_heads;
+  int32_t page_size;            /* power of two in [8, 1024]                       */
+  int32_t head_dim;             /* bf16: multiple of 8 in [8, 128]; 4 bits:
+                                   multiple of 32 in [32, 128]                    */
+  void* k;                      /* 16-byte aligned                                 */
+  void* v;
+  int64_t layer_stride;         /* bytes, multiples of 16                          */
+  int64_t page_stride;
+  int64_t head_stride;
+  int64_t slot_stride;          /* >= the row's bytes: 2 head_dim, or head_dim / 2 */
+  void* k_scale;                /* 4 bits only: pairs, 16-byte aligned; the pairs  */
+  void* v_scale;                /* of a page's slots lie next to each other        */
+  int64_t scale_layer_stride;   /* bytes, multiples of 16                          */
+  int64_t scale_page_stride;
+  int64_t scale_head_stride;
+} ss_kv_cache;
+
+/* The page table and, for the ss_pages_* calls, the pages' bookkeeping. */
+typedef struct {
+  int32_t num_rows;             /* rows of the table                               */
+  int32_t max_pages;            /* entries per row                                 */
+  int64_t row_stride;           /* entries, >= max_pages                           */
+  int32_t* page_table;          /* [num_rows, row_stride]                          */
+  int32_t num_pages;            /* pages of the cache                              */
+  int32_t page_size;
+  int32_t* ref_count;           /* [num_pages] table entries that hold the page    */
+  int32_t* free_pages;          /* [num_pages] a stack: the pages that no entry
+                                   holds are its first free_count entries, taken
+                                   from the end                                   */
+  int32_t* free_count;          /* [1]                                             */
+} ss_page_pool;
+
+/* ss_cache_append writes the new tokens' keys and values of one layer (k and
+ * v are read); ss_cache_read reads the same rows back as bf16 (k and v are
+ * written; 4-bit values s * n + m rounded once).  Request r has the rows
+ * token_offsets[r] .. token_offsets[r + 1] - 1 of k and v, at the slots from
+ * kv_len[r].  out_status: SS_ROW_BAD_PARAM (a count outside [0, max_tokens],
+ * rows outside [0, total_tokens), a negative kv_len or a table row outside the
+ * table: nothing of the request is touched), SS_ROW_BAD_INDEX (a slot beyond
+ * the table or in a hole: those tokens are left out, the others done; rows
+ * read from there are zero). */
+typedef struct {
+  const ss_kv_cache* cache;
+  const ss_page_pool* pool;     /* only the page table's four fields are used      */
+  int32_t layer;
+  int32_t num_requests;
+  int32_t max_tokens;           /* >= every request's number of new tokens         */
+  int32_t total_tokens;         /* rows of k and v                                 */
+  const int32_t* token_offsets; /* [num_requests + 1], or NULL: one token each     */
+  const int32_t* table_rows;    /* [num_requests] each request's row of the page
+                                   table, or NULL: the request's index            */
+  const int32_t* kv_len;        /* [num_requests]                                  */
+  void* k;                      /* [total_tokens, num_kv_heads, head_dim] bf16,    */
+  void* v;                      /* 16-byte aligned, the same strides               */
+  int64_t token_stride;         /* elements, multiples of 8                        */
+  int64_t head_stride;
+  int32_t* out_status;          /* [num_requests]                                  */
+} ss_append_args;
+
+ss_status ss_cache_append(const ss_append_args* args, ss_stream_t stream);
+ss_status ss_cache_read(const ss_append_args* args, ss_stream_t stream);
+
+/* ss_cache_attention: attention of the new tokens (queries) over one layer of
+ * the cache, their own keys included (ss_cache_append comes first).
+ *   S = scale * q . k_j over the keys j that the query sees
+ *   out = sum_j softmax(S)_j v_j,  lse = log sum_j exp S_j
+ * Query head h reads kv head h / (num_heads / num_kv_heads).  Query i of
+ * request r stands at position p = kv_len[r] + i and sees the keys of slot
+ * numbers j <= p; with parents (a draft tree per request, as ss_tree_verify
+ * takes it: at most SS_TREE_MAX_NODES queries per request) at
+ * p = kv_len[r] + depth(i), and sees the keys before kv_len[r], those of the
+ * nodes on its path and its own.  With window > 0 it sees of these only the
+ * keys at positions > p - window or < sinks (a draft key of a tree is at its
+ * node's position).  A query that sees nothing (holes) gets out = 0 and
+ * lse = -infinity.  Keys and values that a query does not see never reach its
+ * result, whatever they hold.  A query that sees a NaN or an infinity gets
+ * results that are not finite or, for an infinite key, weights of 0 and 1.
+ *
+ * Sums and softmax statistics are held in fp32; the weights are rounded to
+ * bf16 before they meet the values.  The result does not depend on timing: the
+ * work is split over the SMs by the lengths alone and joined in a fixed order.
+ *
+ * out_status: SS_ROW_BAD_PARAM (a count outside [0, max_queries], with parents
+ * above SS_TREE_MAX_NODES, query rows outside [0, total_queries), a negative
+ * kv_len, a table row outside the table: the request's rows are not written;
+ * or a parent outside [0, i): the node is taken as a child of the root),
+ * SS_ROW_BAD_INDEX (slots beyond the table: they are holes), SS_ROW_TIMEOUT (a
+ * bounded wait gave up: the request's rows are undefined).
+ *
+ * The workspace (ss_attention_workspace_size() bytes, 256-byte aligned) must
+ * have been zeroed once (ss_workspace_init); calls that share one must not
+ * overlap in time. */
+typedef struct {
+  const ss_kv_cache* cache;
+  const ss_page_pool* pool;     /* only the page table's four fields are used      */
+  int32_t layer;
+  int32_t num_requests;
+  int32_t num_heads;            /* num_kv_heads times 1 .. 128                     */
+  int32_t max_queries;          /* >= every request's number of queries            */
+  int32_t total_queries;        /* rows of q and out                               */
+  const int32_t* query_offsets; /* [num_requests + 1], or NULL: one query each     */
+  const int32_t* table_rows;    /* as ss_append_args                               */
+  const int32_t* kv_len;        /* [num_requests]                                  */
+  const int32_t* parents;       /* [total_queries] local parent node, or NULL      */
+  const void* q;                /* [total_queries, num_heads, head_dim] bf16       */
+  int64_t q_token_stride;       /* elements, multiples of 8; q 16-byte aligned     */
+  int64_t q_head_stride;
+  void* out;                    /* [total_queries, num_heads, head_dim] bf16       */
+  int64_t out_token_stride;     /* elements                                        */
+  int64_t out_head_stride;
+  float* lse;                   /* [total_queries, num_heads], or NULL             */
+  float scale;                  /* finite                                          */
+  int32_t window;               /* 0: off                                          */
+  int32_t sinks;                /* >= 0                                            */
+  int32_t* out_status;          /* [num_requests]                                  */
+} ss_attention_args;
+
+size_t ss_attention_workspace_size(void);
+ss_status ss_cache_attention(const ss_attention_args* args, void* workspace, size_t workspace_bytes,
+                             ss_stream_t stream);
+
+/* ss_pages_reserve: for each i, table row r = table_rows[i] (NULL: i) gets a
+ * page from the pool in every hole among the entries that hold the slots
+ * [from_len[i], to_len[i]).  Pages are taken in the order of i and of the
+ * entries; from the first i whose pages no longer suffice on, those that need
+ * any get none and SS_ROW_LIMIT.  SS_ROW_BAD_PARAM: a table row outside the
+ * table or lengths that are not 0 <= from <= to <= max_pages * page_size.
+ *
+ * ss_pages_fork: table row child[i] becomes a copy of row parent[i]'s first
+ * length[i] slots: full pages are shared (their reference counts grow), the
+ * last one, when it is partly filled, is copied to a page from the pool, in
+ * every layer, so that both rows can go on writing.  Holes stay holes.
+ * SS_ROW_LIMIT as above; SS_ROW_BAD_PARAM: rows outside the table, a length
+ * outside [0, max_pages * page_size], or a child row that holds pages.  A row
+ * without a page of its own is left as it was.  The children must be distinct
+ * and none of them a parent of the same call.
+ *
+ * ss_pages_compact: after ss_tree_verify, moves the accepted nodes' rows (K, V
+ * and scales, in every layer) from slot kv_len[i] + path[i][j] to slot
+ * kv_len[i] + 1 + j, j < num_accepted[i], and writes new_len[i] =
+ * kv_len[i] + 1 + num_accepted[i] (the root, already in place, and the
+ * accepted nodes).  path is ss_tree_verify's out_path ([n, path_stride], each
+ * path increasing and >= 1).  A request whose verification status is not
+ * SS_ROW_OK keeps new_len = kv_len and that status.  SS_ROW_BAD_INDEX (nothing
+ * is moved and new_len = kv_len): a path that is not increasing, a slot beyond
+ * the table or in a hole.  SS_ROW_BAD_PARAM (the same): num_accepted outside
+ * [0, path_stride], a negative kv_len, a table row outside the table.  new_len
+ * must not be the array kv_len.
+ *
+ * ss_pages_trim: table row i keeps the pages that hold a slot < length[i] that
+ * is < sinks or, with window > 0, >= length[i] - window; every other entry
+ * becomes a hole and its page, when no entry holds it any more, goes back to
+ * the pool, the last entry first (so that pages given back are taken again in
+ * the order of the entries).  length 0 frees the row.  SS_ROW_BAD_PARAM: a
+ * table row outside the table or a negative length (nothing is done);
+ * SS_ROW_BAD_INDEX: an entry >= num_pages or whose page's count was already 0
+ * (the entry becomes a hole).
+ *
+ * In each call the table rows must be distinct.  Only ref_count, free_pages,
+ * free_count and the table are touched by reserve and trim; page_size and
+ * num_pages must be the cache's where a cache is given. */
+ss_status ss_pages_reserve(const ss_page_pool* pool, int32_t n, const int32_t* table_rows, const int32_t* from_len,
+                           const int32_t* to_len, int32_t* out_status, ss_stream_t stream);
+ss_status ss_pages_fork(const ss_page_pool* pool, const ss_kv_cache* cache, int32_t n, const int32_t* parent,
+                        const int32_t* child, const int32_t* length, int32_t* out_status, ss_stream_t stream);
+ss_status ss_pages_compact(const ss_page_pool* pool, const ss_kv_cache* cache, int32_t n, const int32_t* table_rows,
+                           const int32_t* kv_len, const int32_t* path, int32_t path_stride,
+                           const int32_t* num_accepted, const int32_t* verify_status, int32_t* new_len,
+                           int32_t* out_status, ss_stream_t stream);
+ss_status ss_pages_trim(const ss_page_pool* pool, int32_t n, const int32_t* table_rows, const int32_t* length,
+                        int32_t window, int32_t sinks, int32_t* out_status, ss_stream_t stream);
+
 /* Cluster size (CTAs per vocabulary row) the kernels use for this vocabulary
  * and dtype, or 0 if unsupported.  A row is split over at most 8 CTAs of at
  * most 61,440 tokens and 160 KiB each, whose slice and working tables must

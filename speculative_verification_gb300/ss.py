@@ -135,6 +135,88 @@ class ss_tree_args(C.Structure):
     ]
 
 
+class ss_kv_cache(C.Structure):
+    _fields_ = [
+        ("format", C.c_int32),
+        ("num_layers", C.c_int32),
+        ("num_pages", C.c_int32),
+        ("num_kv_heads", C.c_int32),
+        ("page_size", C.c_int32),
+        ("head_dim", C.c_int32),
+        ("k", C.c_void_p),
+        ("v", C.c_void_p),
+        ("layer_stride", C.c_int64),
+        ("page_stride", C.c_int64),
+        ("head_stride", C.c_int64),
+        ("slot_stride", C.c_int64),
+        ("k_scale", C.c_void_p),
+        ("v_scale", C.c_void_p),
+        ("scale_layer_stride", C.c_int64),
+        ("scale_page_stride", C.c_int64),
+        ("scale_head_stride", C.c_int64),
+    ]
+
+
+class ss_page_pool(C.Structure):
+    _fields_ = [
+        ("num_rows", C.c_int32),
+        ("max_pages", C.c_int32),
+        ("row_stride", C.c_int64),
+        ("page_table", C.c_void_p),
+        ("num_pages", C.c_int32),
+        ("page_size", C.c_int32),
+        ("ref_count", C.c_void_p),
+        ("free_pages", C.c_void_p),
+        ("free_count", C.c_void_p),
+    ]
+
+
+class ss_append_args(C.Structure):
+    _fields_ = [
+        ("cache", C.POINTER(ss_kv_cache)),
+        ("pool", C.POINTER(ss_page_pool)),
+        ("layer", C.c_int32),
+        ("num_requests", C.c_int32),
+        ("max_tokens", C.c_int32),
+        ("total_tokens", C.c_int32),
+        ("token_offsets", C.c_void_p),
+        ("table_rows", C.c_void_p),
+        ("kv_len", C.c_void_p),
+        ("k", C.c_void_p),
+        ("v", C.c_void_p),
+        ("token_stride", C.c_int64),
+        ("head_stride", C.c_int64),
+        ("out_status", C.c_void_p),
+    ]
+
+
+class ss_attention_args(C.Structure):
+    _fields_ = [
+        ("cache", C.POINTER(ss_kv_cache)),
+        ("pool", C.POINTER(ss_page_pool)),
+        ("layer", C.c_int32),
+        ("num_requests", C.c_int32),
+        ("num_heads", C.c_int32),
+        ("max_queries", C.c_int32),
+        ("total_queries", C.c_int32),
+        ("query_offsets", C.c_void_p),
+        ("table_rows", C.c_void_p),
+        ("kv_len", C.c_void_p),
+        ("parents", C.c_void_p),
+        ("q", C.c_void_p),
+        ("q_token_stride", C.c_int64),
+        ("q_head_stride", C.c_int64),
+        ("out", C.c_void_p),
+        ("out_token_stride", C.c_int64),
+        ("out_head_stride", C.c_int64),
+        ("lse", C.c_void_p),
+        ("scale", C.c_float),
+        ("window", C.c_int32),
+        ("sinks", C.c_int32),
+        ("out_status", C.c_void_p),
+    ]
+
+
 # Every symbol include/ss.h declares, with its ctypes signature.
 SIGNATURES = {
     "ss_workspace_size": ([C.c_int32, C.c_int32], C.c_size_t),
@@ -160,6 +242,16 @@ SIGNATURES = {
     "ss_commit_accepted": ([C.c_int32, C.c_int32] + [C.c_void_p] * 4 + [C.c_int32] + [C.c_void_p] * 5, C.c_int),
     "ss_sample_shard": ([C.POINTER(ss_sample_args), C.c_int32, C.c_int32, C.c_int32, C.c_void_p, C.c_void_p], C.c_int),
     "ss_merge_shards": ([C.POINTER(ss_sample_args), C.c_int32, C.POINTER(C.c_void_p), C.c_int32, C.c_void_p], C.c_int),
+    "ss_cache_append": ([C.POINTER(ss_append_args), C.c_void_p], C.c_int),
+    "ss_cache_read": ([C.POINTER(ss_append_args), C.c_void_p], C.c_int),
+    "ss_attention_workspace_size": ([], C.c_size_t),
+    "ss_cache_attention": ([C.POINTER(ss_attention_args), C.c_void_p, C.c_size_t, C.c_void_p], C.c_int),
+    "ss_pages_reserve": ([C.POINTER(ss_page_pool), C.c_int32] + [C.c_void_p] * 5, C.c_int),
+    "ss_pages_fork": ([C.POINTER(ss_page_pool), C.POINTER(ss_kv_cache), C.c_int32] + [C.c_void_p] * 5, C.c_int),
+    "ss_pages_compact": ([C.POINTER(ss_page_pool), C.POINTER(ss_kv_cache), C.c_int32] + [C.c_void_p] * 3 +
+                         [C.c_int32] + [C.c_void_p] * 5, C.c_int),
+    "ss_pages_trim": ([C.POINTER(ss_page_pool), C.c_int32, C.c_void_p, C.c_void_p, C.c_int32, C.c_int32,
+                       C.c_void_p, C.c_void_p], C.c_int),
 }
 
 _lib = None
@@ -451,6 +543,231 @@ def ss_tree_verify(target_logits, node_offsets, parents, node_tokens, draft_prob
     a.debug_processed = _ptr(debug_processed)
     _check(load().ss_tree_verify(C.byref(a), C.c_void_p(workspace.data_ptr()),
                                  workspace.numel() * workspace.element_size(), _stream_handle(stream)))
+
+
+# ---------------------------------------------------------- paged cache --
+
+
+def _want(t, name, dtype, shape=None):
+    """A device tensor's pointer, after the checks that the C entry cannot
+    make: its type, its shape and that it is contiguous."""
+    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or (shape is not None and tuple(t.shape) != shape):
+        raise SSError("%s: want a contiguous %s device tensor%s, got %s %s on %s" %
+                      (name, dtype, "" if shape is None else " of shape %s" % (shape,), t.dtype, tuple(t.shape), t.device))
+    return t.data_ptr()
+
+
+class KVCache:
+    """The keys and values of a model's layers in pages (ss_kv_cache).
+
+    k, v: [layers, pages, kv heads, page size, head dim] bf16; or, packed in
+    4 bits, [..., head dim / 2] uint8 with k_scale and v_scale
+    [layers, pages, kv heads, page size, 2] bf16 holding each row's (step,
+    low).  Any strides with contiguous rows, the same for k and v.
+    """
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        import torch
+        packed = k_scale is not None
+        want = torch.uint8 if packed else torch.bfloat16
+        for t in (k, v):
+            if t.dim() != 5 or t.dtype != want or t.shape != k.shape or t.stride() != k.stride() or t.stride(4) != 1:
+                raise SSError("KVCache: want k and v as [layers, pages, kv heads, page size, row] %s tensors of the same "
+                              "shape and strides with contiguous rows" % want)
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.format = "int4" if packed else "bf16"
+        layers, self.num_pages, self.num_kv_heads, self.page_size, row = k.shape
+        self.num_layers, self.head_dim = layers, row * 2 if packed else row
+        es = k.element_size()
+        c = ss_kv_cache(1 if packed else 0, layers, self.num_pages, self.num_kv_heads, self.page_size, self.head_dim,
+                        k.data_ptr(), v.data_ptr(), *(_span(k, i) * es for i in range(4)))
+        if packed:
+            for t in (k_scale, v_scale):
+                if t is None or t.dtype != torch.bfloat16 or t.shape != (*k.shape[:4], 2) or \
+                        t.stride() != k_scale.stride() or t.stride()[3:] != (2, 1):
+                    raise SSError("KVCache: want k_scale and v_scale as [layers, pages, kv heads, page size, 2] bf16 "
+                                  "tensors of the same strides, a page's pairs next to each other")
+            c.k_scale, c.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
+            c.scale_layer_stride, c.scale_page_stride, c.scale_head_stride = (_span(k_scale, i) * 2 for i in range(3))
+        self.struct = c
+        self.ref = C.pointer(c)
+
+
+def _span(t, i):
+    """The stride of dimension i; where it has one entry only, and its stride
+    means nothing, the extent of the dimensions inside it."""
+    if t.shape[i] > 1:
+        return t.stride(i)
+    return max([t.stride(j) * t.shape[j] for j in range(i + 1, t.dim())] + [t.stride(i)])
+
+
+def alloc_cache(layers, pages, kv_heads, page_size, head_dim, format="bf16", device="cuda"):
+    """A zeroed KVCache."""
+    import torch
+    shape = (layers, pages, kv_heads, page_size)
+    if format == "bf16":
+        return KVCache(*(torch.zeros(*shape, head_dim, dtype=torch.bfloat16, device=device) for _ in range(2)))
+    if format != "int4":
+        raise SSError("alloc_cache: format is 'bf16' or 'int4'")
+    return KVCache(*(torch.zeros(*shape, head_dim // 2, dtype=torch.uint8, device=device) for _ in range(2)),
+                   *(torch.zeros(*shape, 2, dtype=torch.bfloat16, device=device) for _ in range(2)))
+
+
+class PagePool:
+    """The page table and the pages' bookkeeping (ss_page_pool): page_table
+    [rows, entries], ref_count [pages], free_pages [pages], free_count [1],
+    all int32 on the device."""
+
+    def __init__(self, page_table, ref_count, free_pages, free_count, page_size):
+        import torch
+        pages = ref_count.numel()
+        if page_table.dim() != 2 or page_table.dtype != torch.int32 or page_table.stride(1) != 1:
+            raise SSError("PagePool: want page_table as [rows, entries] int32 with contiguous rows")
+        self.page_table, self.ref_count, self.free_pages, self.free_count = page_table, ref_count, free_pages, free_count
+        self.page_size = page_size
+        rows, entries = page_table.shape
+        self.struct = ss_page_pool(rows, entries, page_table.stride(0) if rows > 1 else entries, page_table.data_ptr(),
+                                   pages, page_size, _want(ref_count, "ref_count", torch.int32, (pages,)),
+                                   _want(free_pages, "free_pages", torch.int32, (pages,)),
+                                   _want(free_count, "free_count", torch.int32, (1,)))
+        self.ref = C.pointer(self.struct)
+
+
+def alloc_pool(rows, entries, pages, page_size, device="cuda"):
+    """A PagePool with every page free (page 0 is taken first) and an empty table."""
+    import torch
+    i32 = dict(dtype=torch.int32, device=device)
+    return PagePool(torch.full((rows, entries), -1, **i32), torch.zeros(pages, **i32),
+                    torch.arange(pages - 1, -1, -1, **i32), torch.full((1,), pages, **i32), page_size)
+
+
+def _table(page_table, cache):
+    """ss_page_pool of a bare page table (the calls that only read the table)."""
+    import torch
+    if isinstance(page_table, PagePool):
+        return page_table.ref
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.stride(1) != 1 or not page_table.is_cuda:
+        raise SSError("page_table: want a PagePool or a [rows, entries] int32 device tensor with contiguous rows")
+    rows, entries = page_table.shape
+    return C.pointer(ss_page_pool(rows, entries, page_table.stride(0) if rows > 1 else entries, page_table.data_ptr(),
+                                  cache.num_pages, cache.page_size))
+
+
+def _rows_args(cache, layer, k, v, page_table, kv_len, status, token_offsets, max_tokens, table_rows):
+    import torch
+    n = kv_len.numel()
+    for t in (k, v):
+        if t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() != 3 or t.shape != k.shape or \
+                t.stride() != k.stride() or t.stride(2) != 1 or tuple(t.shape[1:]) != (cache.num_kv_heads, cache.head_dim):
+            raise SSError("want k and v as [tokens, %d, %d] bf16 device tensors of the same strides with contiguous rows"
+                          % (cache.num_kv_heads, cache.head_dim))
+    i32 = torch.int32
+    return ss_append_args(cache.ref, _table(page_table, cache), layer, n, 1 if max_tokens is None else max_tokens,
+                          k.shape[0], None if token_offsets is None else _want(token_offsets, "token_offsets", i32, (n + 1,)),
+                          None if table_rows is None else _want(table_rows, "table_rows", i32, (n,)),
+                          _want(kv_len, "kv_len", i32), k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1),
+                          _want(status, "status", i32, (n,)))
+
+
+def ss_cache_append(cache, layer, k, v, page_table, kv_len, status, *, token_offsets=None, max_tokens=None,
+                    table_rows=None, stream=None):
+    """Write the new tokens' keys and values [tokens, kv heads, head dim] of
+    one layer into the cache at the slots from kv_len (see include/ss.h).
+    page_table: a PagePool or the table alone; token_offsets None: one token
+    per request."""
+    a = _rows_args(cache, layer, k, v, page_table, kv_len, status, token_offsets, max_tokens, table_rows)
+    _check(load().ss_cache_append(a, _stream_handle(stream)))
+
+
+def ss_cache_read(cache, layer, k, v, page_table, kv_len, status, *, token_offsets=None, max_tokens=None,
+                  table_rows=None, stream=None):
+    """The inverse of ss_cache_append: k and v are written."""
+    a = _rows_args(cache, layer, k, v, page_table, kv_len, status, token_offsets, max_tokens, table_rows)
+    _check(load().ss_cache_read(a, _stream_handle(stream)))
+
+
+def ss_attention_workspace_size():
+    return int(load().ss_attention_workspace_size())
+
+
+def alloc_attention_workspace(device="cuda"):
+    """A workspace for ss_cache_attention, zeroed as its first use needs it."""
+    import torch
+    return torch.zeros((ss_attention_workspace_size() + 3) // 4, dtype=torch.int32, device=device)
+
+
+def ss_cache_attention(cache, layer, q, out, page_table, kv_len, workspace, status, *, query_offsets=None,
+                       max_queries=None, parents=None, scale=None, window=0, sinks=0, lse=None, table_rows=None,
+                       stream=None):
+    """Attention of the new tokens' queries [tokens, heads, head dim] over one
+    layer of the cache, their own keys included (see include/ss.h).
+    query_offsets None: one query per request; parents: a draft tree per
+    request, as ss_tree_verify takes it; scale None: 1 / sqrt(head dim)."""
+    import torch
+    i32 = torch.int32
+    n, total, heads = kv_len.numel(), q.shape[0], q.shape[1]
+    for t in (q, out):
+        if t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() != 3 or t.shape != q.shape or t.stride(2) != 1 or \
+                t.shape[2] != cache.head_dim:
+            raise SSError("want q and out as [tokens, heads, %d] bf16 device tensors with contiguous rows" % cache.head_dim)
+    a = ss_attention_args(cache.ref, _table(page_table, cache), layer, n, heads,
+                          1 if max_queries is None else max_queries, total,
+                          None if query_offsets is None else _want(query_offsets, "query_offsets", i32, (n + 1,)),
+                          None if table_rows is None else _want(table_rows, "table_rows", i32, (n,)),
+                          _want(kv_len, "kv_len", i32),
+                          None if parents is None else _want(parents, "parents", i32, (total,)),
+                          q.data_ptr(), q.stride(0), q.stride(1), out.data_ptr(), out.stride(0), out.stride(1),
+                          None if lse is None else _want(lse, "lse", torch.float32, (total, heads)),
+                          cache.head_dim ** -0.5 if scale is None else scale, window, sinks,
+                          _want(status, "status", i32, (n,)))
+    _check(load().ss_cache_attention(a, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                     _stream_handle(stream)))
+
+
+def ss_pages_reserve(pool, from_len, to_len, status, *, table_rows=None, stream=None):
+    """Pages from the pool for the slots [from_len, to_len) of each row."""
+    import torch
+    i32, n = torch.int32, from_len.numel()
+    _check(load().ss_pages_reserve(pool.ref, n, None if table_rows is None else _want(table_rows, "table_rows", i32, (n,)),
+                                   _want(from_len, "from_len", i32), _want(to_len, "to_len", i32, (n,)),
+                                   _want(status, "status", i32, (n,)), _stream_handle(stream)))
+
+
+def ss_pages_fork(pool, cache, parent, child, length, status, *, stream=None):
+    """Table rows `child` become copies of rows `parent`: full pages shared,
+    the partly filled last one copied in every layer."""
+    import torch
+    i32, n = torch.int32, parent.numel()
+    _check(load().ss_pages_fork(pool.ref, cache.ref, n, _want(parent, "parent", i32), _want(child, "child", i32, (n,)),
+                                _want(length, "length", i32, (n,)), _want(status, "status", i32, (n,)),
+                                _stream_handle(stream)))
+
+
+def ss_pages_compact(pool, cache, kv_len, path, num_accepted, verify_status, new_len, status, *, table_rows=None,
+                     stream=None):
+    """After ss_tree_verify: the accepted nodes' rows to consecutive slots, in
+    every layer; new_len = kv_len + 1 + num_accepted.  path: out_path."""
+    import torch
+    i32, n = torch.int32, kv_len.numel()
+    if path.dim() != 2 or path.shape[0] != n:
+        raise SSError("path: want ss_tree_verify's out_path, [%d, nodes]" % n)
+    _check(load().ss_pages_compact(pool.ref, cache.ref, n,
+                                   None if table_rows is None else _want(table_rows, "table_rows", i32, (n,)),
+                                   _want(kv_len, "kv_len", i32), _want(path, "path", i32), path.shape[1],
+                                   _want(num_accepted, "num_accepted", i32, (n,)),
+                                   None if verify_status is None else _want(verify_status, "verify_status", i32, (n,)),
+                                   _want(new_len, "new_len", i32, (n,)), _want(status, "status", i32, (n,)),
+                                   _stream_handle(stream)))
+
+
+def ss_pages_trim(pool, length, status, *, window=0, sinks=0, table_rows=None, stream=None):
+    """Give back the rows' pages past `length`, and with a window those that
+    no later token sees; length 0 frees a row."""
+    import torch
+    i32, n = torch.int32, length.numel()
+    _check(load().ss_pages_trim(pool.ref, n, None if table_rows is None else _want(table_rows, "table_rows", i32, (n,)),
+                                _want(length, "length", i32), window, sinks, _want(status, "status", i32, (n,)),
+                                _stream_handle(stream)))
 
 
 # ------------------------------------------------------------ workloads --
