@@ -12,8 +12,9 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libss.so")
-SOURCES = ["ss_kernel.cu", "ss_hist.cu", "ss_shard.cu", "ss_fused.cu", "ss_cache.cu", "ss_attn.cu"]
-DEPS = SOURCES + ["ss_hist.h", "ss_cache.h", "ss_philox.cuh", "ss_ptx.cuh", "ss_nvtx.h"]
+SOURCES = ["ss_kernel.cu", "ss_hist.cu", "ss_shard.cu", "ss_fused.cu", "ss_cache.cu", "ss_attn.cu",
+           "ss_attn_bf16.cu", "ss_attn_int4.cu"]
+DEPS = SOURCES + ["ss_hist.h", "ss_cache.h", "ss_attn.cuh", "ss_philox.cuh", "ss_ptx.cuh", "ss_nvtx.h"]
 
 NVCC_FLAGS = [
     "-std=c++17", "-O3", "-lineinfo",

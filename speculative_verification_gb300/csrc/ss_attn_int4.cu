@@ -1,0 +1,17 @@
+// ss_attn_int4.cu -- the attention kernel (ss_attn.cuh) for 4-bit caches.
+#include "ss_attn.cuh"
+
+namespace ssa {
+
+template <int kHalves>
+static ss_status pick(const AttnArgs& a, cudaStream_t s) {
+  switch (a.block_rows) {
+    case 16: return launch<16, true, kHalves>(a, s);
+    case 32: return launch<32, true, kHalves>(a, s);
+    default: return launch<64, true, kHalves>(a, s);
+  }
+}
+
+ss_status launch_int4(const AttnArgs& a, cudaStream_t s) { return a.c.dim <= 64 ? pick<1>(a, s) : pick<2>(a, s); }
+
+}  // namespace ssa

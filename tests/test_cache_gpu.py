@@ -145,6 +145,7 @@ class Problem:
         out, lse, st = self.call(ss, workspace)
         torch.cuda.synchronize()
         assert st.cpu().tolist() == [0] * len(self.lens)
+        assert not bool(workspace[:256].any())  # the counters are left at zero
         got, gl = np32(out).astype(np.float64), lse.cpu().numpy().astype(np.float64)
         k, v, mv = dense(self.cache)
         pick = lambda pages, slots: tuple(x[pages, :, slots] for x in (k, v, mv))  # noqa: E731
@@ -232,6 +233,15 @@ def test_many_requests(ss, workspace, fmt):
     lens = [rng.choice([0, 1, rng.randint(0, 200), rng.randint(0, 600)]) for _ in range(333)]
     news = [rng.randint(1, 3) for _ in lens]
     Problem(ss, 21, fmt, lens, news, 2, 1, 64, 16).check(ss, workspace)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("group,dim", [(8, 128), (24, 128), (24, 64), (60, 128), (100, 64), (128, 128)])
+def test_many_items_for_every_block_of_rows(ss, workspace, fmt, group, dim):
+    # several items per SM, whole and in pieces, of 16 to 128 rows
+    rng = random.Random(group)
+    lens = [rng.randint(0, 500) for _ in range(160)]
+    Problem(ss, 40, fmt, lens, [1] * len(lens), 2 * group, 2, dim, 16).check(ss, workspace)
 
 
 @pytest.mark.parametrize("order", ["pshd", "hpsd", "shpd"])
