@@ -61,7 +61,7 @@ ss_status ss_cache_attention(const ss_attention_args* args, void* workspace, siz
   if (!args || !check_cache(args->cache) || !check_table(args->pool)) return SS_ERR_INVALID_ARG;
   const ss_attention_args& A = *args;
   const int32_t kv_heads = A.cache->num_kv_heads;
-  if (A.layer < 0 || A.layer >= A.cache->num_layers || A.num_requests < 0 || A.num_requests > 65535 ||
+  if (A.layer < 0 || A.layer >= A.cache->num_layers || A.num_requests < 0 || A.num_requests > 16384 ||
       A.max_queries < 0 || A.total_queries < 0 || A.num_heads < 1 || A.num_heads % kv_heads != 0 ||
       A.num_heads / kv_heads > 128 || static_cast<int64_t>(A.max_queries) * A.num_heads >= (1ll << 31) || A.window < 0 || A.sinks < 0 || !isfinite(A.scale))
     return SS_ERR_INVALID_ARG;
@@ -100,7 +100,7 @@ ss_status ss_cache_attention(const ss_attention_args* args, void* workspace, siz
   // tensor-core and softmax time.
   const int64_t rows = static_cast<int64_t>(a.max_queries) * a.group;
   const int32_t most = a.c.format == SS_CACHE_INT4 ? 64 : 128;
-  a.block_rows = 16;
+  a.block_rows = 8;
   while (a.block_rows < rows && a.block_rows < most) a.block_rows *= 2;
   a.counters = static_cast<int32_t*>(workspace);
   a.pieces = reinterpret_cast<float*>(a.counters + kMaxCtas);

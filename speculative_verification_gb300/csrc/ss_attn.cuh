@@ -22,9 +22,9 @@
 // and K and V enter the tensor cores exactly as they lie in the cache ([key]
 // [channel], K as a K-major and V as an M-major operand).
 //
-// 4 bits.  A row stands for s n + m, n = 0..15.  n - 8 is exact in bf16, so
-// the tensor cores multiply the exact integers, and s and m enter in fp32:
-//   q.k = s_k (q.(n - 8)) + (m_k + 8 s_k) sum(q)
+// 4 bits.  A row stands for s n + m, n = 0..15.  n + 16 and n - 8 are exact in
+// bf16, so the tensor cores multiply exact integers, and s and m enter in fp32:
+//   q.k = s_k (q.(n + 16)) + (m_k - 16 s_k) sum(q)
 //   sum_j p v = sum_j (p s_v) (n - 8) + sum_j p (m_v + 8 s_v),
 // the first in fp32 on the thread that owns the key, the second by rounding
 // p s_v to bf16 instead of p, plus one fp32 sum per row.
@@ -41,8 +41,8 @@
 //
 // Warps: 0 tensor copies (one box per page and 64 channels, straight from the
 // page table), 1 tcgen05.mma, 2-3 the next item's queries and masks, then the
-// softmax warps (128 threads per 64 rows or fewer) and for 4 bits four warps
-// that unpack.
+// softmax warps (128 threads per 8 to 32 rows) and for 4 bits eight warps that
+// unpack.
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -57,7 +57,8 @@ using namespace ss;
 
 constexpr int kTile = 128;                // keys per tile
 constexpr int kMaxCtas = 256;             // the workspace's limit on the grid
-constexpr uint32_t kPolls = 1u << 20;     // bounded waits
+constexpr uint32_t kPolls = 1u << 14;     // bounded waits: polls that each sleep up to kSleepNs
+constexpr uint32_t kSleepNs = 50000;
 constexpr int kInfo = 16;                 // tiles whose page masks are kept
 constexpr int kPairs = 8;                 // tiles whose (s, m) pairs are kept
 constexpr float kUnset = 3.0e38f;         // minus the reference of a row that has seen nothing
@@ -67,7 +68,7 @@ struct AttnArgs {
   CacheView c;
   TableView t;
   int32_t num_requests, num_heads, group, max_queries, total_queries;
-  int32_t block_rows;  // rows of an item (the kernel's kN)
+  int32_t block_rows;  // rows of an item (the kernel's kLive)
   const int32_t* offsets;
   const int32_t* kv_len;
   const int32_t* parents;
@@ -104,13 +105,14 @@ struct Item {
   const int32_t* row;
 };
 
-template <int kN, bool kPacked, int kHalves>
+// kN: rows of the MMAs; kLive: of these the softmax warps handle the first
+// kLive (8 of 16 for the requests with no more rows than that).
+template <int kN, int kLive, bool kPacked, int kHalves>
 struct Cfg {
-  static constexpr int kGroups = kN >= 64 ? 2 : 1;           // softmax warpgroups
-  static constexpr int kCols = kN / kGroups;                 // rows per softmax thread
-  static constexpr int kSub = kCols < 32 ? kCols : 32;       // handled at once
+  static constexpr int kGroups = kN <= 16 ? 1 : kN == 32 ? 2 : kPacked ? 2 : 4;  // softmax warpgroups
+  static constexpr int kCols = kLive / kGroups;              // rows per softmax thread
   static constexpr int kSoft = 128 * kGroups;
-  static constexpr int kUnpack = kPacked ? 128 : 0;
+  static constexpr int kUnpack = kPacked ? 256 : 0;          // K tiles by one warpgroup, V tiles by the other
   static constexpr int kThreads = 128 + kSoft + kUnpack;
   static constexpr int kStage = kHalves * 16384;             // 128 keys x 64 channels x 2 bytes per half
   static constexpr int kQ = kHalves * kN * 128;
@@ -119,14 +121,20 @@ struct Cfg {
   static constexpr int kP = kTile * kN * 2;
   static constexpr int kRawRow = 32 * kHalves;               // packed bytes per key
   static constexpr int kRaw = kPacked ? 2 * kTile * kRawRow + 2 * kTile * 4 : 0;
-  static constexpr int kRawStages = kPacked ? (kN >= 64 ? 3 : 4) : 1;
-  static constexpr int kMeta = kNQ * (static_cast<int>(sizeof(Item)) + kN * 16 + 64) + kN * 4 * 11 + 2048 +
-                               (kPacked ? 2 * kPairs * kTile * 4 : 0);
+  static constexpr int kRawStages = kPacked ? 4 : 1;
+  // the static arrays, rounded up
+  static constexpr int kMeta = kNQ * (static_cast<int>(sizeof(Item)) + kN * 28 + 64) + kN * 32 + 1536 +
+                               (kGroups > 1 ? kGroups * 256 : 0) + (kPacked ? 2 * kPairs * kTile * 4 : 0);
   static constexpr int kBudget = 232448 - 1024 - kNQ * kQ - 2 * kP - kRawStages * kRaw - kMeta;
-  static constexpr int kRing = kBudget / kStage < 8 ? kBudget / kStage : 8;
+  // bf16: tiles of K and V in one ring; 4 bits: V tiles only
+  static constexpr int kMost = kPacked ? 4 : 8;
+  static constexpr int kRing = kBudget / kStage < kMost ? kBudget / kStage : kMost;
   static constexpr int kSmem = 1024 + kRing * kStage + kNQ * kQ + 2 * kP + kRawStages * kRaw;
-  static constexpr uint32_t kTmem = 4 * kN;                  // columns: S x 2, O x 2
-  static_assert(kRing >= 3, "K, the next K and V are held at once");
+  // tensor-memory columns: S x 2, O x 2, and for 4 bits K x 2 (two channels per column)
+  static constexpr uint32_t kKCols = kPacked ? 32 * kHalves : 0;
+  static constexpr uint32_t kUsed = 4 * kN + 2 * kKCols;
+  static constexpr uint32_t kTmem = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
+  static_assert(kRing >= (kPacked ? 2 : 3), "K, the next K and V are held at once");
 };
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
@@ -138,7 +146,15 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 // nothing it computes then is used.
 __device__ __forceinline__ bool wait_or_dead(uint64_t* bar, uint32_t parity, volatile int32_t* dead) {
   for (uint32_t i = 0; i < kPolls; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(kSleepNs)
+        : "memory");
+    if (done) return true;
     if (*dead) return false;
   }
   *dead = 1;
@@ -179,6 +195,16 @@ __device__ __forceinline__ void umma(uint32_t d, uint64_t a, uint64_t b, uint32_
       : "memory");
 }
 
+// The same with A in tensor memory: lane m holds row m, two channels per column.
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 __device__ __forceinline__ void umma_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
                : "memory");
@@ -201,6 +227,23 @@ __device__ __forceinline__ void tmem_ld(uint32_t t, float (&v)[16]) {
       : "memory");
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
+__device__ __forceinline__ void tmem_ld(uint32_t t, float (&v)[8]) {
+  __syncwarp();
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(t)
+               : "memory");
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_st(uint32_t t, const float (&v)[8]) {
+  __syncwarp();
+  const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(t)
+               : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void tmem_ld(uint32_t t, float (&v)[32]) {
   __syncwarp();
   uint32_t* r = reinterpret_cast<uint32_t*>(v);
@@ -215,7 +258,8 @@ __device__ __forceinline__ void tmem_ld(uint32_t t, float (&v)[32]) {
       : "memory");
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void tmem_st(uint32_t t, const float (&v)[16]) {
+__device__ __forceinline__ void tmem_put_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_put(uint32_t t, const float (&v)[16]) {
   __syncwarp();
   const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
   asm volatile(
@@ -224,7 +268,10 @@ __device__ __forceinline__ void tmem_st(uint32_t t, const float (&v)[16]) {
       "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
       "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(t)
       : "memory");
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_st(uint32_t t, const float (&v)[16]) {
+  tmem_put(t, v);
+  tmem_put_wait();
 }
 __device__ __forceinline__ void tmem_st(uint32_t t, const float (&v)[32]) {
   __syncwarp();
@@ -334,32 +381,36 @@ __device__ __forceinline__ Span span_of(const AttnArgs& a, const Request& q, int
   return s;
 }
 
-__device__ __forceinline__ int32_t request_tiles(const AttnArgs& a, const Request& q) {
+// Tiles of one kv head of a request; the lanes of a warp share its blocks.
+__device__ __forceinline__ int32_t request_tiles(const AttnArgs& a, const Request& q, int32_t block0, int32_t step) {
   int32_t sum = 0;
-  for (int32_t row0 = 0; row0 < q.n * a.group; row0 += a.block_rows) sum += span_of(a, q, row0).tiles;
+  for (int32_t row0 = block0 * a.block_rows; row0 < q.n * a.group; row0 += step * a.block_rows)
+    sum += span_of(a, q, row0).tiles;
   return sum;
 }
 
-template <int kN, bool kPacked, int kHalves>
-__global__ void __launch_bounds__(Cfg<kN, kPacked, kHalves>::kThreads, 1)
+template <int kN, int kLive, bool kPacked, int kHalves>
+__global__ void __launch_bounds__(Cfg<kN, kLive, kPacked, kHalves>::kThreads, 1)
     attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const AttnArgs a) {
-  using F = Cfg<kN, kPacked, kHalves>;
-  constexpr int kRing = F::kRing, kNQ = F::kNQ, kSub = F::kSub, kCols = F::kCols;
+  using F = Cfg<kN, kLive, kPacked, kHalves>;
+  constexpr int kRing = F::kRing, kNQ = F::kNQ, kCols = F::kCols;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full[kRing], empty[kRing], sfull[2], sempty[2], pfull[2], pdone[2], oempty[2],
-      qfull[kNQ], qempty[kNQ], rfull[F::kRawStages], rempty[F::kRawStages], looked, drain;
+      qfull[kNQ], qempty[kNQ], rfull[F::kRawStages], rempty[F::kRawStages], kfull[2], kempty[2], looked, drain;
   __shared__ Item items[kNQ];
-  __shared__ int32_t row_pos[kNQ][kN];
-  __shared__ uint64_t row_path[kNQ][kN];
-  __shared__ float row_qsum[kPacked ? kNQ : 1][kPacked ? kN : 1];
+  __shared__ __align__(16) int32_t row_pos[kNQ][kN];
+  __shared__ __align__(16) uint64_t row_path[kNQ][kN];
+  __shared__ int64_t row_out[kNQ][kN];
+  __shared__ int32_t row_lse[kNQ][kN];
+  __shared__ __align__(16) float row_qsum[kPacked ? kNQ : 1][kPacked ? kN : 4];
   __shared__ uint8_t node_depth[kNQ][SS_TREE_MAX_NODES];
   __shared__ uint32_t info[kInfo];
   __shared__ uint32_t k_pair[kPacked ? kPairs : 1][kPacked ? kTile : 1], v_pair[kPacked ? kPairs : 1][kPacked ? kTile : 1];
+  __shared__ uint8_t key_bad[2][F::kGroups > 1 ? F::kGroups : 1][F::kGroups > 1 ? kTile : 1];
   __shared__ __align__(16) float nref[kN], corr[kN], sums[kN], csums[kN];
   __shared__ float part[4][kN];
   __shared__ uint32_t tmem_slot;
-  __shared__ int32_t s_dead, s_last, s_chunk0, s_chunk1, s_scan[32];
-  __shared__ int32_t s_before;
+  __shared__ int32_t s_dead, s_last, s_r0, s_r1, s_before, s_tiles0, s_scan[32];
 
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* pbuf = ring + kRing * F::kStage;
@@ -384,15 +435,19 @@ __global__ void __launch_bounds__(Cfg<kN, kPacked, kHalves>::kThreads, 1)
       mbar_init(qfull + i, 64);
       mbar_init(qempty + i, 1 + F::kSoft / 32);
     }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(kfull + i, 128);
+      mbar_init(kempty + i, 1);
+    }
     if (kPacked)
       for (int i = 0; i < F::kRawStages; ++i) {
         mbar_init(rfull + i, 1);
-        mbar_init(rempty + i, 128);
+        mbar_init(rempty + i, 256);
       }
     mbar_init(&looked, F::kSoft);
     mbar_init(&drain, 1);
     s_dead = 0;
-    s_chunk0 = s_chunk1 = -1;
+    s_r0 = s_r1 = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -402,26 +457,43 @@ __global__ void __launch_bounds__(Cfg<kN, kPacked, kHalves>::kThreads, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     tc_fence_before();
   }
-  // this CTA's part of the tiles: thread t weighs the requests of its chunk
-  const int32_t chunk = (a.num_requests + F::kThreads - 1) / F::kThreads;
-  int32_t mine = 0;
-  for (int32_t i = 0; i < chunk; ++i) {
-    const int32_t r = tid * chunk + i;
-    if (r < a.num_requests) {
+  // ---- this CTA's part of the tiles
+  // Tiles of each request, in the ring's memory before the ring is used: a
+  // thread per request when a request is one block, else a warp.
+  int32_t* weights = reinterpret_cast<int32_t*>(ring);
+  if (a.max_queries * a.group <= kLive) {
+    for (int32_t r = tid; r < a.num_requests; r += F::kThreads) {
       const Request q = request_of(a, r);
-      mine += request_tiles(a, q);
-      if (blockIdx.x == 0) {
-        int32_t st = q.ok ? SS_ROW_OK : SS_ROW_BAD_PARAM;
-        if (q.ok && q.n > 0 && ((q.base + q.n - 1) >> a.c.page_shift) >= a.t.max_pages) st = SS_ROW_BAD_INDEX;
-        if (q.ok && a.parents)
-          for (int32_t n = 1; n < q.n; ++n) {
-            const int32_t pa = a.parents[q.qbegin + n];
-            if (pa < 0 || pa >= n) st = SS_ROW_BAD_PARAM;
-          }
-        a.status[r] = st;
-      }
+      weights[r] = request_tiles(a, q, 0, 1);
+    }
+  } else {
+    for (int32_t r = warp; r < a.num_requests; r += F::kThreads / 32) {
+      const Request q = request_of(a, r);
+      const int32_t w = __reduce_add_sync(0xffffffffu, request_tiles(a, q, lane, 32));
+      if (lane == 0) weights[r] = w;
     }
   }
+  // The statuses: each by one warp of one CTA.
+  for (int64_t r = blockIdx.x + static_cast<int64_t>(gridDim.x) * warp; r < a.num_requests;
+       r += static_cast<int64_t>(gridDim.x) * (F::kThreads / 32)) {
+    const Request q = request_of(a, static_cast<int32_t>(r));
+    bool bad = !q.ok;
+    if (q.ok && a.parents)
+      for (int32_t n = 1 + lane; n < q.n; n += 32) {
+        const int32_t pa = a.parents[q.qbegin + n];
+        bad |= pa < 0 || pa >= n;
+      }
+    bad = __any_sync(0xffffffffu, bad);
+    const bool beyond = q.n > 0 && ((q.base + q.n - 1) >> a.c.page_shift) >= a.t.max_pages;
+    if (lane == 0) a.status[r] = bad ? SS_ROW_BAD_PARAM : beyond ? SS_ROW_BAD_INDEX : SS_ROW_OK;
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  const int32_t chunk = (a.num_requests + F::kThreads - 1) / F::kThreads;  // consecutive requests per thread
+  const int32_t r_from = min(a.num_requests, tid * chunk), r_to = min(a.num_requests, r_from + chunk);
+  int32_t mine = 0;
+  for (int32_t r = r_from; r < r_to; ++r) mine += weights[r];
   int32_t upto = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -430,9 +502,8 @@ __global__ void __launch_bounds__(Cfg<kN, kPacked, kHalves>::kThreads, 1)
   }
   if (lane == 31) s_scan[warp] = upto;
   __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = tmem_slot;
   int32_t all_tiles = 0;
+#pragma unroll
   for (int w = 0; w < F::kThreads / 32; ++w) {
     if (w == warp) upto += all_tiles;
     all_tiles += s_scan[w];
@@ -441,20 +512,28 @@ __global__ void __launch_bounds__(Cfg<kN, kPacked, kHalves>::kThreads, 1)
   const int32_t ctas = static_cast<int32_t>(min(total, static_cast<int64_t>(gridDim.x)));  // each has a tile or more
   const int64_t lo = ctas ? total * blockIdx.x / ctas : 0, hi = ctas ? total * (blockIdx.x + 1) / ctas : 0;
   const int32_t my_tiles = static_cast<int32_t>(blockIdx.x) < ctas ? static_cast<int32_t>(hi - lo) : 0;
-  if (my_tiles > 0) {
-    const int64_t from = static_cast<int64_t>(upto - mine) * a.c.heads, to = static_cast<int64_t>(upto) * a.c.heads;
-    if (lo >= from && lo < to) {
-      s_chunk0 = tid;
-      s_before = upto - mine;
+  if (my_tiles > 0 && mine > 0) {
+    const int64_t heads = a.c.heads;
+    int32_t before = upto - mine;
+    if (lo >= before * heads && lo < upto * heads) {
+      int32_t r = r_from;
+      while (lo >= (before + weights[r]) * heads) before += weights[r++];
+      s_r0 = r;
+      s_before = before;
+      s_tiles0 = weights[r];
     }
-    if (hi - 1 >= from && hi - 1 < to) s_chunk1 = tid;
+    before = upto - mine;
+    if (hi - 1 >= before * heads && hi - 1 < upto * heads) s_r1 = r_to - 1;  // at or past the last request
   }
+  proxy_fence();  // the weights' reads before the ring's copies
   __syncthreads();
   // The ring's order within an item whose first tile is the CTA's tile f and
   // that has m tiles: K0, K1, V0, K2, V1, .., K(m-1), V(m-2), V(m-1), as the
   // MMAs take them.
   const auto k_seq = [](int32_t f, int32_t t) { return 2 * f + (t == 0 ? 0 : 2 * t - 1); };
-  const auto v_seq = [](int32_t f, int32_t m, int32_t t) { return 2 * f + (t == m - 1 ? 2 * t + 1 : 2 * t + 2); };
+  const auto v_seq = [](int32_t f, int32_t m, int32_t t) {
+    return kPacked ? f + t : 2 * f + (t == m - 1 ? 2 * t + 1 : 2 * t + 2);  // 4 bits: only V is in the ring
+  };
 
   if (my_tiles == 0) {
     // fewer tiles than CTAs
@@ -574,16 +653,26 @@ __global__ void __launch_bounds__(Cfg<kN, kPacked, kHalves>::kThreads, 1)
         const uint32_t qa = smem_addr(qbuf + qb * F::kQ);
         for (int32_t t = 0; t < tiles && ok; ++t, ++at) {
           const int b = at & 1;
-          const int32_t seq = k_seq(f, t), s = seq % kRing;
-          ok = ok && wait_or_dead(full + s, (seq / kRing) & 1, dead);
           ok = ok && wait_or_dead(sempty + b, ((at >> 1) & 1) ^ 1u, dead);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t ka = smem_addr(ring + s * F::kStage);
-          for (int kk = 0; kk < k_steps; ++kk)
-            umma(tmem + b * kN, smem_desc(ka + (kk >> 2) * 16384 + (kk & 3) * 32, 16, 1024, 2),
-                 smem_desc(qa + (kk >> 2) * (kN * 128) + (kk & 3) * 32, 16, 1024, 2), kIdS, kk > 0 ? 1u : 0u);
-          umma_commit(empty + s);
+          if constexpr (kPacked) {
+            ok = ok && wait_or_dead(kfull + b, (at >> 1) & 1, dead);
+            if (!ok) break;
+            tc_fence_after();
+            for (int kk = 0; kk < k_steps; ++kk)
+              umma_ts(tmem + b * kN, tmem + 4 * kN + b * F::kKCols + kk * 8,
+                      smem_desc(qa + (kk >> 2) * (kN * 128) + (kk & 3) * 32, 16, 1024, 2), kIdS, kk > 0 ? 1u : 0u);
+            umma_commit(kempty + b);
+          } else {
+            const int32_t seq = k_seq(f, t), s = seq % kRing;
+            ok = ok && wait_or_dead(full + s, (seq / kRing) & 1, dead);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t ka = smem_addr(ring + s * F::kStage);
+            for (int kk = 0; kk < k_steps; ++kk)
+              umma(tmem + b * kN, smem_desc(ka + (kk >> 2) * 16384 + (kk & 3) * 32, 16, 1024, 2),
+                   smem_desc(qa + (kk >> 2) * (kN * 128) + (kk & 3) * 32, 16, 1024, 2), kIdS, kk > 0 ? 1u : 0u);
+            umma_commit(empty + s);
+          }
           umma_commit(sfull + b);
           if (at > 0 && !(kNQ == 1 && t == 0)) second(at - 1, prev_seq, prev_first, prev_item);
           prev_seq = v_seq(f, tiles, t);
@@ -601,30 +690,38 @@ __global__ void __launch_bounds__(Cfg<kN, kPacked, kHalves>::kThreads, 1)
   } else if (warp < 4) {
     // --------------------------------------------- the items' queries --
     const int lt = tid - 64;
-    int32_t r = s_chunk0 * chunk, left = my_tiles;
+    int32_t r = s_r0, left = my_tiles;
     Request q = request_of(a, r);
-    int32_t w = request_tiles(a, q);
-    int64_t before = static_cast<int64_t>(s_before) * a.c.heads;  // tiles before request r
-    while (lo >= before + static_cast<int64_t>(w) * a.c.heads) {
-      before += static_cast<int64_t>(w) * a.c.heads;
-      q = request_of(a, ++r);
-      w = request_tiles(a, q);
-    }
+    const int64_t before = static_cast<int64_t>(s_before) * a.c.heads;  // tiles before request r
+    const int32_t w = s_tiles0;
     int32_t head = static_cast<int32_t>((lo - before) / w);
     int32_t skip = static_cast<int32_t>((lo - before) - static_cast<int64_t>(head) * w);  // tiles of the head passed
-    int32_t row0 = 0;
-    Span s = span_of(a, q, 0);
     int64_t start = before + static_cast<int64_t>(head) * w;  // the item's first tile
-    while (skip >= s.tiles) {
-      skip -= s.tiles;
-      start += s.tiles;
-      row0 += kN;
-      s = span_of(a, q, row0);
+    int32_t row0 = 0;
+    for (;; row0 += 32 * kLive) {  // the block that holds it: 32 blocks at a time
+      const int32_t mine_row = row0 + lane * kLive;
+      const int32_t n = mine_row < q.n * a.group ? span_of(a, q, mine_row).tiles : 0;
+      int32_t sum = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int32_t y = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += y;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, skip < sum);
+      const int at = past ? __ffs(past) - 1 : 31;
+      const int32_t passed = __shfl_sync(0xffffffffu, past ? sum - n : sum, at);
+      skip -= passed;
+      start += passed;
+      if (past) {
+        row0 += at * kLive;
+        break;
+      }
     }
+    Span s = span_of(a, q, row0);
     for (int32_t k = 0; left > 0; ++k) {
       const int b = k % kNQ;
       if (!__all_sync(0xffffffffu, wait_or_dead(qempty + b, ((k / kNQ) & 1) ^ 1u, dead))) break;
-      const int32_t rows = min(kN, q.n * a.group - row0), take = min(left, s.tiles - skip);
+      const int32_t rows = min(kLive, q.n * a.group - row0), take = min(left, s.tiles - skip);
       if (lt == 0) {
         Item it;
         it.r = r;
@@ -648,10 +745,11 @@ __global__ void __launch_bounds__(Cfg<kN, kPacked, kHalves>::kThreads, 1)
         items[b] = it;
       }
       for (int n = lt; n < kN; n += 64) {
-        const int32_t token = (row0 + n) / a.group;
+        const int32_t token = (row0 + n) / a.group, h = head * a.group + (row0 + n - token * a.group);
+        const bool live = n < rows;
         int32_t depth = token;
-        uint64_t path = 0;
-        if (a.parents && n < rows) {
+        uint64_t path = ~0ull;
+        if (a.parents && live) {
           depth = 0;
           path = 1ull << token;
           for (int32_t u = token; u > 0; ++depth) {
@@ -661,8 +759,11 @@ __global__ void __launch_bounds__(Cfg<kN, kPacked, kHalves>::kThreads, 1)
           }
         }
         // rows without a query: a position past every key, their result is not used
-        row_pos[b][n] = n < rows ? q.base + depth : 0x7fffffff;
-        row_path[b][n] = n < rows ? path : ~0ull;
+        row_pos[b][n] = live ? q.base + depth : 0x7ffffffe;
+        row_path[b][n] = path;
+        const int64_t t = static_cast<int64_t>(q.qbegin) + token;
+        row_out[b][n] = t * a.out_token + h * a.out_head;
+        row_lse[b][n] = static_cast<int32_t>(t * a.num_heads + h);
       }
       if (a.parents && lt < q.n) {
         int32_t depth = 0;
@@ -672,22 +773,33 @@ __global__ void __launch_bounds__(Cfg<kN, kPacked, kHalves>::kThreads, 1)
         }
         node_depth[b][lt] = static_cast<uint8_t>(depth);
       }
-      // 16 lanes per row, 8 channels each
-      for (int n = lt >> 4; n < kN; n += 4) {
-        const int ch = lt & 15, token = (row0 + n) / a.group;
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (n < rows && ch * 8 < a.c.dim)
-          x = *reinterpret_cast<const uint4*>(
-              a.q + (static_cast<int64_t>(q.qbegin) + token) * a.q_token +
-              (static_cast<int64_t>(head) * a.group + (row0 + n - token * a.group)) * a.q_head + ch * 16);
-        if (ch < 8 * kHalves)
-          *reinterpret_cast<uint4*>(qbuf + b * F::kQ + (ch >> 3) * (kN * 128) + n * 128 + (((ch & 7) ^ (n & 7)) << 4)) = x;
-        if (kPacked) {
-          float sum = ((bf16_lo(x.x) + bf16_hi(x.x)) + (bf16_lo(x.y) + bf16_hi(x.y))) +
-                      ((bf16_lo(x.z) + bf16_hi(x.z)) + (bf16_lo(x.w) + bf16_hi(x.w)));
+      // 16 lanes per row, 8 channels each; eight rows in flight
+      const int ch = lt & 15;
+#pragma unroll 1
+      for (int n0 = lt >> 4; n0 < kN; n0 += 32) {
+        uint4 x[8];
 #pragma unroll
-          for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o, 16);
-          if (ch == 0) row_qsum[b][n] = sum;
+        for (int u = 0; u < 8; ++u) {
+          const int n = n0 + 4 * u, token = (row0 + n) / a.group;
+          x[u] = make_uint4(0u, 0u, 0u, 0u);
+          if (n < rows && ch * 8 < a.c.dim)
+            x[u] = *reinterpret_cast<const uint4*>(
+                a.q + (static_cast<int64_t>(q.qbegin) + token) * a.q_token +
+                (static_cast<int64_t>(head) * a.group + (row0 + n - token * a.group)) * a.q_head + ch * 16);
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int n = n0 + 4 * u;
+          if (n >= kN) break;
+          if (ch < 8 * kHalves)
+            *reinterpret_cast<uint4*>(qbuf + b * F::kQ + (ch >> 3) * (kN * 128) + n * 128 + (((ch & 7) ^ (n & 7)) << 4)) = x[u];
+          if (kPacked) {
+            float sum = ((bf16_lo(x[u].x) + bf16_hi(x[u].x)) + (bf16_lo(x[u].y) + bf16_hi(x[u].y))) +
+                        ((bf16_lo(x[u].z) + bf16_hi(x[u].z)) + (bf16_lo(x[u].w) + bf16_hi(x[u].w)));
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o, 16);
+            if (ch == 0) row_qsum[b][n] = sum;
+          }
         }
       }
       proxy_fence();
@@ -697,7 +809,7 @@ __global__ void __launch_bounds__(Cfg<kN, kPacked, kHalves>::kThreads, 1)
       if (left == 0) break;
       start += s.tiles;
       skip = 0;
-      row0 += kN;
+      row0 += kLive;
       if (row0 >= q.n * a.group) {
         row0 = 0;
         if (++head == a.c.heads) {
@@ -712,9 +824,12 @@ __global__ void __launch_bounds__(Cfg<kN, kPacked, kHalves>::kThreads, 1)
   } else if (!kPacked || tid < 128 + F::kSoft) {
     // ---------------------------------------------------------- softmax --
     const int st = tid - 128, wg = st >> 7, lt = st & 127, wq = warp & 3;
-    const int col0 = wg * kCols;                            // this warpgroup's rows
+    const int c0 = wg * kCols;                                    // this warpgroup's rows
     const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;  // this warp's tensor-memory lanes
-    const int bar = 1 + wg;                                 // its barrier
+    const int bar = 1 + wg;                                       // its barrier
+    const int32_t unit_shift = min(a.c.page_shift, 7);
+    const uint32_t every = static_cast<uint32_t>((1ull << (kTile >> unit_shift)) - 1);
+    const bool tree = a.parents != nullptr;
     int32_t at = 0;
     uint32_t looks = 0;
     for (int32_t k = 0; at < my_tiles; ++k) {
@@ -728,9 +843,8 @@ __global__ void __launch_bounds__(Cfg<kN, kPacked, kHalves>::kThreads, 1)
       if (kPacked)
 #pragma unroll
         for (int n = 0; n < kCols; ++n) cs[n] = 0.0f;
-      if (lt < kCols) nref[col0 + lt] = kUnset;
-      const uint32_t o_base = tmem + 2 * kN + (k & 1) * kN + col0 + lanes;
-      const bool tree = a.parents != nullptr;
+      if (lt < kCols) nref[c0 + lt] = kUnset;
+      const uint32_t o_base = tmem + 2 * kN + (k & 1) * kN + c0 + lanes;
       const int32_t f = at;
       const int32_t first_pos = it.base + (tree ? 0 : it.row0 / a.group);
       const int32_t last_pos = it.base + (it.row0 + it.rows - 1) / a.group;  // of a tree: at most
@@ -742,46 +856,69 @@ __global__ void __launch_bounds__(Cfg<kN, kPacked, kHalves>::kThreads, 1)
         wait_or_dead(sfull + sb, (at >> 1) & 1, dead);
         tc_fence_after();
         const uint32_t there = *reinterpret_cast<volatile uint32_t*>(info + at % kInfo);
-        const int32_t unit_shift = min(a.c.page_shift, 7);
-        const uint32_t every = (kTile >> unit_shift) == 16 ? 0xffffu : (1u << (kTile >> unit_shift)) - 1u;
         // does some row miss some key of the tile?
         const bool masked = sink || there != every || j0 + kTile - 1 > (tree ? it.base - 1 : first_pos) ||
                             (a.window > 0 && j0 <= last_pos - a.window);
         float ka = a.scale_log2, kb = 0.0f, sv = 0.0f, wv = 0.0f;
-        if (kPacked) {
+        if (kPacked) {  // the tensor cores multiplied 16 + n
           const uint32_t kp = k_pair[at % kPairs][lt];
           const float s = bf16_lo(kp);
           ka = a.scale_log2 * s;
-          kb = a.scale_log2 * __fmaf_rn(8.0f, s, bf16_hi(kp));
+          kb = a.scale_log2 * __fmaf_rn(-16.0f, s, bf16_hi(kp));
         }
-        bool seen_key = true, poison = false;
-        int32_t j = 0, place = 0;
+        uint32_t vis = 0xffffffffu;  // the rows that see this thread's key
+        bool poison = false;
         if (masked) {
-          j = j0 + lt;
-          place = j;
-          seen_key = ((there >> (lt >> unit_shift)) & 1u) && j < (sink ? it.sink_end : it.end);
-          if (tree && seen_key && j >= it.base) place = it.base + node_depth[b][j - it.base];
+          const int32_t j = j0 + lt;
+          const bool here = ((there >> (lt >> unit_shift)) & 1u) && j < (sink ? it.sink_end : it.end);
+          const bool draft = tree && here && j >= it.base;
+          const int32_t place = draft ? it.base + node_depth[b][j - it.base] : j;
+          // a row at position pos sees the key when 0 <= pos - place <= span
+          const bool always = a.window == 0 || place < a.sinks;
+          const uint32_t span = always ? 0x7fffffffu : static_cast<uint32_t>(a.window) - 1u;
+          const int32_t from = here ? place : 0x7fffffff;
+          vis = 0;
+#pragma unroll
+          for (int i = 0; i < kCols; i += 4) {
+            const int4 p4 = *reinterpret_cast<const int4*>(&row_pos[b][c0 + i]);
+            vis |= (static_cast<uint32_t>(static_cast<uint32_t>(p4.x - from) <= span) << i) |
+                   (static_cast<uint32_t>(static_cast<uint32_t>(p4.y - from) <= span) << (i + 1)) |
+                   (static_cast<uint32_t>(static_cast<uint32_t>(p4.z - from) <= span) << (i + 2)) |
+                   (static_cast<uint32_t>(static_cast<uint32_t>(p4.w - from) <= span) << (i + 3));
+          }
+          if (draft) {
+            const uint32_t* word = reinterpret_cast<const uint32_t*>(&row_path[b][c0]) + ((j - it.base) >> 5);
+            uint32_t on = 0;
+#pragma unroll
+            for (int i = 0; i < kCols; ++i) on |= ((word[2 * i] >> ((j - it.base) & 31)) & 1u) << i;
+            vis &= on;
+          }
           if (!kPacked) {
-            // A value that is not finite must not meet a weight of 0: such a
-            // key's row becomes 0, and the rows that see it NaN by its weight.
+            // A value that is not finite must not meet a weight of 0: the row
+            // of such a key, where not every query sees it, becomes 0, and the
+            // queries that do see it get a weight of NaN.
             const int32_t seq = v_seq(f, it.tiles, t), s = seq % kRing;
             wait_or_dead(full + s, (seq / kRing) & 1, dead);
+            const bool all = here && !draft && j <= first_pos && (always || j > last_pos - a.window);
             uint4* v = reinterpret_cast<uint4*>(ring + s * F::kStage + lt * 128);
-            uint32_t bad = 0;
-#pragma unroll
-            for (int h = 0; h < kHalves; ++h)
-#pragma unroll
-              for (int c = 0; c < 8; ++c) {
-                const uint4 x = v[h * 1024 + (c ^ (lt & 7))];
+            if (!all) {
+              uint32_t acc = 0;  // 0 times each channel, added up: NaN as soon as one is not finite
+#pragma unroll 4
+              for (int c = wg; c < 8 * kHalves; c += F::kGroups) {
+                const uint4 x = v[(c >> 3) * 1024 + ((c & 7) ^ (lt & 7))];
                 const uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  bad |= ((y[e] & 0x7f80u) == 0x7f80u) | ((y[e] & 0x7f800000u) == 0x7f800000u);
+                for (int e = 0; e < 4; ++e) asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(y[e]), "r"(0u));
               }
-            poison = bad != 0;
-            if (F::kGroups > 1) {  // both warpgroups have looked
+              poison = (acc & 0x7fff7fffu) != 0;
+            }
+            if (F::kGroups > 1) {  // each warpgroup has looked at a part of the channels
+              key_bad[looks & 1][wg][lt] = poison;
               mbar_arrive(&looked);
-              wait_or_dead(&looked, looks++ & 1, dead);
+              wait_or_dead(&looked, looks & 1, dead);
+#pragma unroll
+              for (int g = 0; g < F::kGroups; ++g) poison |= key_bad[looks & 1][g][lt] != 0;
+              ++looks;
             }
             if (poison && wg == 0) {
 #pragma unroll
@@ -791,122 +928,116 @@ __global__ void __launch_bounds__(Cfg<kN, kPacked, kHalves>::kThreads, 1)
             }
           }
         }
-#pragma unroll
-        for (int sub = 0; sub < kCols / kSub; ++sub) {
-          const int c0 = col0 + sub * kSub;
-          float x[kSub];
+        // x_nj - r_n of this key, every row
+        float x[kCols];
+        const auto scores = [&](bool with_ref) {
           tmem_ld(tmem + sb * kN + c0 + lanes, x);
-          if (sub == kCols / kSub - 1) {
-            tc_fence_before();
-            mbar_arrive(sempty + sb);
-          }
-          float mul = ka;
-          if (kPacked) {
-            mul = 1.0f;
 #pragma unroll
-            for (int i = 0; i < kSub; ++i) x[i] = __fmaf_rn(x[i], ka, kb * row_qsum[b][c0 + i]);
-          }
-          uint32_t vis = 0xffffffffu;
-          if (masked) {
-            vis = 0;
-#pragma unroll 4
-            for (int i = 0; i < kSub; ++i) {
-              const int32_t pos = row_pos[b][c0 + i];
-              bool see = tree && j >= it.base ? seen_key && ((row_path[b][c0 + i] >> (j - it.base)) & 1ull) != 0
-                                              : seen_key && j <= pos;
-              see = see && (a.window == 0 || place > pos - a.window || place < a.sinks);
-              vis |= static_cast<uint32_t>(see) << i;
+          for (int i = 0; i < kCols; i += 4) {
+            const float4 r4 = *reinterpret_cast<const float4*>(nref + c0 + i);
+            float y[4] = {r4.x, r4.y, r4.z, r4.w};
+            if (!with_ref) y[0] = y[1] = y[2] = y[3] = 0.0f;
+            if (kPacked) {
+              const float4 q4 = *reinterpret_cast<const float4*>(&row_qsum[b][c0 + i]);
+              y[0] = __fmaf_rn(kb, q4.x, y[0]);
+              y[1] = __fmaf_rn(kb, q4.y, y[1]);
+              y[2] = __fmaf_rn(kb, q4.z, y[2]);
+              y[3] = __fmaf_rn(kb, q4.w, y[3]);
             }
 #pragma unroll
-            for (int i = 0; i < kSub; ++i) x[i] = ((vis >> i) & 1u) ? x[i] * mul : -INFINITY;
-            mul = 1.0f;
+            for (int e = 0; e < 4; ++e) x[i + e] = __fmaf_rn(x[i + e], ka, y[e]);
           }
-          // does some row's score pass its reference by more than 8?
-          bool pass = true;
-          if (t > 0) {
-            float most = -INFINITY;
+          if (masked)
 #pragma unroll
-            for (int i = 0; i < kSub; ++i) most = fmaxf(most, __fmaf_rn(x[i], mul, nref[c0 + i]));
-            pass = most > 8.0f;
+            for (int i = 0; i < kCols; ++i) x[i] = ((vis >> i) & 1u) ? x[i] : -INFINITY;
+        };
+        bool pass = true;
+        if (t > 0) {
+          scores(true);
+          float most = x[0];
+#pragma unroll
+          for (int i = 1; i < kCols; ++i) most = fmaxf(most, x[i]);
+          pass = bar_any(bar, 128, most > 8.0f);
+        }
+        if (pass) {
+          // some row's score passes its reference by more than 8: the new
+          // reference is the row's largest score of the tile
+          scores(false);
+#pragma unroll
+          for (int i = 0; i < kCols; ++i) {
+            const float y = fmaxf(x[i], -INFINITY);  // a NaN counts as nothing
+            const float m = order_float(__reduce_max_sync(0xffffffffu, order_int(y)));
+            if (lane == i) part[wq][c0 + i] = m;
           }
-          if (bar_any(bar, 128, pass)) {
-            // new references: the largest score of the tile where it passes
-#pragma unroll
-            for (int i = 0; i < kSub; ++i) {
-              const float y = fmaxf(x[i] * mul, -INFINITY);  // a NaN counts as nothing
-              const float m = order_float(__reduce_max_sync(0xffffffffu, order_int(y)));
-              if (lane == (i & 31)) part[wq][c0 + i] = m;
+          bar_sync(bar, 128);
+          if (lt < kCols) {
+            const int c = c0 + lt;
+            const float m = fmaxf(fmaxf(part[0][c], part[1][c]), fmaxf(part[2][c], part[3][c]));
+            const float old = nref[c];
+            float g = 1.0f;
+            if (m + old > 8.0f) {
+              nref[c] = -m;
+              g = old == kUnset ? 0.0f : ex2(-m - old);  // 2^(old reference - new)
             }
-            bar_sync(bar, 128);
-            if (lt < kSub) {
-              const int c = c0 + lt;
-              const float m = fmaxf(fmaxf(part[0][c], part[1][c]), fmaxf(part[2][c], part[3][c]));
-              const float old = nref[c];
-              float f = 1.0f;
-              if (m + old > 8.0f) {
-                nref[c] = -m;
-                f = old == kUnset ? 0.0f : ex2(-m - old);  // 2^(old reference - new)
+            corr[c] = g;
+          }
+          bar_sync(bar, 128);
+          bool change = false;
+#pragma unroll
+          for (int i = 0; i < kCols; ++i) {
+            const float g = corr[c0 + i];
+            change |= g != 1.0f;
+            l[i] *= g;
+            if (kPacked) cs[i] *= g;
+          }
+          if (change && t > 0) {
+            wait_or_dead(pdone + ((at - 1) & 1), ((at - 1) >> 1) & 1, dead);
+            tc_fence_after();
+            tmem_ld(o_base, x);
+#pragma unroll
+            for (int i = 0; i < kCols; ++i) x[i] *= corr[c0 + i];
+            tmem_st(o_base, x);
+          }
+          scores(true);
+        }
+        tc_fence_before();
+        mbar_arrive(sempty + sb);
+        if (kPacked) {
+          const int32_t seq = v_seq(f, it.tiles, t), s = seq % kRing;
+          wait_or_dead(full + s, (seq / kRing) & 1, dead);  // V is unpacked, so its pairs are there
+          const uint32_t vp = v_pair[at % kPairs][lt];
+          sv = bf16_lo(vp);
+          wv = __fmaf_rn(8.0f, sv, bf16_hi(vp));
+          poison = !(fabsf(wv) <= 3.0e38f);  // as below; a step that is not finite makes wv so
+          if (poison) sv = wv = 0.0f;
+        }
+        if (poison)
+#pragma unroll
+          for (int i = 0; i < kCols; ++i) x[i] = ((vis >> i) & 1u) ? __int_as_float(0x7fffffff) : -INFINITY;
+        if (at >= 2) wait_or_dead(pdone + sb, ((at - 2) >> 1) & 1, dead);  // P's buffer is free
+        // powers, sums, and P^T [key][row], swizzled as the MMA reads it
+        uint8_t* pb = pbuf + sb * F::kP + (c0 >> 6) * (kTile * 128);
+#pragma unroll
+        for (int i8 = 0; i8 < kCols / 8; ++i8) {
+          uint32_t o4[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float p[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int i = i8 * 8 + e * 2 + h;
+              p[h] = ex2(x[i]);
+              l[i] += p[h];
+              if (kPacked) {
+                cs[i] = __fmaf_rn(p[h], wv, cs[i]);
+                p[h] *= sv;
               }
-              corr[c] = f;
             }
-            bar_sync(bar, 128);
-            bool change = false;
-#pragma unroll
-            for (int i = 0; i < kSub; ++i) {
-              const float f = corr[c0 + i];
-              change |= f != 1.0f;
-              l[sub * kSub + i] *= f;
-              if (kPacked) cs[sub * kSub + i] *= f;
-            }
-            if (change && t > 0) {
-              wait_or_dead(pdone + ((at - 1) & 1), ((at - 1) >> 1) & 1, dead);
-              tc_fence_after();
-              float o[kSub];
-              tmem_ld(o_base + sub * kSub, o);
-#pragma unroll
-              for (int i = 0; i < kSub; ++i) o[i] *= corr[c0 + i];
-              tmem_st(o_base + sub * kSub, o);
-              tc_fence_before();
-            }
+            o4[e] = bf16_pair(p[0], p[1]);
           }
-          if (sub == 0 && at >= 2) wait_or_dead(pdone + sb, ((at - 2) >> 1) & 1, dead);  // P's buffer is free
-          if (kPacked && sub == 0) {
-            const int32_t seq = v_seq(f, it.tiles, t), s = seq % kRing;
-            wait_or_dead(full + s, (seq / kRing) & 1, dead);  // V is unpacked, so its pairs are there
-            const uint32_t vp = v_pair[at % kPairs][lt];
-            sv = bf16_lo(vp);
-            wv = __fmaf_rn(8.0f, sv, bf16_hi(vp));
-          }
-          // powers, sums, and P^T [key][row], swizzled as the MMA reads it
-          uint8_t* pb = pbuf + sb * F::kP + (kN == 128 ? wg * (kTile * 128) : 0);
-          const int in_block = (kN == 128 ? 0 : col0) + sub * kSub;
-#pragma unroll
-          for (int i8 = 0; i8 < kSub / 8; ++i8) {
-            uint32_t o4[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float p[2];
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const int i = i8 * 8 + e * 2 + h, c = sub * kSub + i;
-                p[h] = ex2(__fmaf_rn(x[i], mul, nref[c0 + i]));
-                if (!kPacked && masked && poison && ((vis >> i) & 1u)) p[h] = __int_as_float(0x7fffffff);
-                l[c] += p[h];
-                if (kPacked) {
-                  if (masked && !((vis >> i) & 1u)) {
-                    p[h] = 0.0f;  // the pair may hold anything
-                  } else {
-                    cs[c] = __fmaf_rn(p[h], wv, cs[c]);
-                    p[h] *= sv;
-                  }
-                }
-              }
-              o4[e] = bf16_pair(p[0], p[1]);
-            }
-            const uint32_t off = lt * F::kPitch + (in_block + i8 * 8) * 2;
-            const uint32_t swz = kN >= 64 ? 0x70u : kN == 32 ? 0x30u : 0x10u;
-            *reinterpret_cast<uint4*>(pb + (off ^ ((off >> 3) & swz))) = make_uint4(o4[0], o4[1], o4[2], o4[3]);
-          }
+          const uint32_t off = lt * F::kPitch + ((c0 & 63) + i8 * 8) * 2;
+          const uint32_t swz = kN >= 64 ? 0x70u : kN == 32 ? 0x30u : 0x10u;
+          *reinterpret_cast<uint4*>(pb + (off ^ ((off >> 3) & swz))) = make_uint4(o4[0], o4[1], o4[2], o4[3]);
         }
         proxy_fence();
         tc_fence_before();
@@ -915,74 +1046,47 @@ __global__ void __launch_bounds__(Cfg<kN, kPacked, kHalves>::kThreads, 1)
       // ---- the item's end: sums over the keys, then the rows
       wait_or_dead(pdone + ((at - 1) & 1), ((at - 1) >> 1) & 1, dead);
       tc_fence_after();
-#pragma unroll
-      for (int sub = 0; sub < kCols / kSub; ++sub) {
-        float y[kSub];
-#pragma unroll
-        for (int i = 0; i < kSub; ++i) y[i] = l[sub * kSub + i];
-        const float s = warp_sums<kSub>(y);
-        if (lane < kSub) part[wq][col0 + sub * kSub + lane] = s;
+      {
+        const float s = warp_sums<kCols>(l);
+        if (lane < kCols) part[wq][c0 + lane] = s;
       }
       bar_sync(bar, 128);
-      if (lt < kCols) sums[col0 + lt] = (part[0][col0 + lt] + part[1][col0 + lt]) + (part[2][col0 + lt] + part[3][col0 + lt]);
-      if (kPacked) {
+      if (lt < kCols) sums[c0 + lt] = (part[0][c0 + lt] + part[1][c0 + lt]) + (part[2][c0 + lt] + part[3][c0 + lt]);
+      if constexpr (kPacked) {
         bar_sync(bar, 128);
-#pragma unroll
-        for (int sub = 0; sub < kCols / kSub; ++sub) {
-          float y[kSub];
-#pragma unroll
-          for (int i = 0; i < kSub; ++i) y[i] = cs[sub * kSub + i];
-          const float s = warp_sums<kSub>(y);
-          if (lane < kSub) part[wq][col0 + sub * kSub + lane] = s;
-        }
+        const float s = warp_sums<kCols>(cs);
+        if (lane < kCols) part[wq][c0 + lane] = s;
         bar_sync(bar, 128);
-        if (lt < kCols)
-          csums[col0 + lt] = (part[0][col0 + lt] + part[1][col0 + lt]) + (part[2][col0 + lt] + part[3][col0 + lt]);
+        if (lt < kCols) csums[c0 + lt] = (part[0][c0 + lt] + part[1][c0 + lt]) + (part[2][c0 + lt] + part[3][c0 + lt]);
       }
       bar_sync(bar, 128);
       const int32_t rows = it.rows;            // live rows
       const int ch = wq * 32 + lane;           // this lane's channel
       const bool whole = it.tiles == it.all;
-      const auto place_of = [&](int32_t c, int64_t& token, int32_t& head) {  // of row c of the block
-        const int32_t t = (it.row0 + c) / a.group;
-        token = static_cast<int64_t>(it.qbegin) + t;
-        head = it.head * a.group + (it.row0 + c - t * a.group);
-      };
-      int64_t token;
-      int32_t head;
       float* piece = a.pieces + (static_cast<int64_t>(blockIdx.x) * 2 + it.piece) * kSlotFloats;
-      if (wq * 32 < kHalves * 64) {
-#pragma unroll 1
-        for (int sub = 0; sub < kCols / kSub; ++sub) {
-          const int c0 = col0 + sub * kSub;
-          if (c0 >= rows) break;
-          float o[kSub];
-          tmem_ld(o_base + sub * kSub, o);
+      if (wq * 32 < kHalves * 64 && c0 < rows) {
+        float o[kCols];
+        tmem_ld(o_base, o);
 #pragma unroll
-          for (int i = 0; i < kSub; ++i) {
-            const int c = c0 + i;
-            if (kPacked) o[i] += csums[c];
-            if (c >= rows) continue;
-            if (whole) {
-              const float s = sums[c], y = s == 0.0f ? 0.0f : __fdividef(o[i], s);
-              place_of(c, token, head);
-              if (ch < a.c.dim)
-                a.out[token * a.out_token + head * a.out_head + ch] = static_cast<uint16_t>(bf16_pair(y, 0.0f));
-            } else {
-              __stcg(piece + c * 128 + ch, o[i]);
-            }
+        for (int i = 0; i < kCols; ++i) {
+          const int c = c0 + i;
+          if (c >= rows) continue;
+          if (kPacked) o[i] += csums[c];
+          if (whole) {
+            const float s = sums[c], y = s == 0.0f ? 0.0f : __fdividef(o[i], s);
+            if (ch < a.c.dim) a.out[row_out[b][c] + ch] = static_cast<uint16_t>(bf16_pair(y, 0.0f));
+          } else {
+            __stcg(piece + c * 128 + ch, o[i]);
           }
         }
       }
-      if (lt < kCols && col0 + lt < rows) {
-        const int c = col0 + lt;
+      if (lt < kCols && c0 + lt < rows) {
+        const int c = c0 + lt;
         if (!whole) {
           __stcg(piece + 128 * 128 + 2 * c, nref[c]);
           __stcg(piece + 128 * 128 + 2 * c + 1, sums[c]);
         } else if (a.lse) {
-          place_of(c, token, head);
-          a.lse[token * a.num_heads + head] =
-              sums[c] == 0.0f ? -INFINITY : 0.69314718055994531f * (log2f(sums[c]) - nref[c]);
+          a.lse[row_lse[b][c]] = sums[c] == 0.0f ? -INFINITY : 0.69314718055994531f * (log2f(sums[c]) - nref[c]);
         }
       }
       tc_fence_before();
@@ -998,19 +1102,20 @@ __global__ void __launch_bounds__(Cfg<kN, kPacked, kHalves>::kThreads, 1)
         }
         bar_sync(5, F::kSoft);
         if (s_last) {
-          // ---- the last CTA of the item joins the pieces, in the CTAs' order
+          // ---- the last CTA of the item joins the pieces, in the CTAs' order:
+          // piece p is CTA cta0 + p's first, but for the first CTA, whose
+          // second piece it is unless the item starts where the CTA starts
           __threadfence();
-          // piece p is CTA cta0 + p's first one, but the first CTA's, which may be its second
-          const int64_t s0 = total * it.cta0 / ctas;  // the first CTA's first tile
           const int64_t item_start = (it.piece == 0 ? lo : hi - it.tiles) - it.tile0;
-          const int32_t first_piece = item_start == s0 ? 0 : 1;
+          const int32_t first_piece = item_start == total * it.cta0 / ctas ? 0 : 1;
           const float* base = a.pieces + static_cast<int64_t>(it.cta0) * 2 * kSlotFloats;
-          for (int c = (st >> 5); c < rows; c += F::kSoft / 32) {
-            place_of(c, token, head);
+          const auto piece_at = [&](int32_t p) {
+            return base + (static_cast<int64_t>(p) * 2 + (p == 0 ? first_piece : 0)) * kSlotFloats;
+          };
+          for (int c = st >> 5; c < rows; c += F::kSoft / 32) {
             float top = -INFINITY;  // the largest reference
             for (int32_t p = lane; p < parts; p += 32) {
-              const float* pc = base + (static_cast<int64_t>(p) * 2 + (p == 0 ? first_piece : 0)) * kSlotFloats;
-              const float nr = __ldcg(pc + 128 * 128 + 2 * c);
+              const float nr = __ldcg(piece_at(p) + 128 * 128 + 2 * c);
               top = fmaxf(top, nr == kUnset ? -INFINITY : -nr);
             }
 #pragma unroll
@@ -1018,100 +1123,118 @@ __global__ void __launch_bounds__(Cfg<kN, kPacked, kHalves>::kThreads, 1)
             float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             float sum = 0.0f;
             for (int32_t p0 = 0; p0 < parts; p0 += 32) {
-              const int32_t p = p0 + lane;
-              float f = 0.0f, ls = 0.0f;
-              if (p < parts) {
-                const float* pc = base + (static_cast<int64_t>(p) * 2 + (p == 0 ? first_piece : 0)) * kSlotFloats;
+              float g = 0.0f, ls = 0.0f;
+              if (p0 + lane < parts) {
+                const float* pc = piece_at(p0 + lane);
                 const float nr = __ldcg(pc + 128 * 128 + 2 * c);
                 ls = __ldcg(pc + 128 * 128 + 2 * c + 1);
                 // a piece in which the row saw nothing has sum 0 (or NaN from a NaN score, which stays)
-                f = nr == kUnset ? (ls == 0.0f ? 0.0f : 1.0f) : ex2(-nr - top);
+                g = nr == kUnset ? (ls == 0.0f ? 0.0f : 1.0f) : ex2(-nr - top);
               }
               const int32_t m = min(32, parts - p0);
 #pragma unroll 4
               for (int32_t i = 0; i < m; ++i) {
-                const float fi = __shfl_sync(0xffffffffu, f, i), li = __shfl_sync(0xffffffffu, ls, i);
-                const int32_t pp = p0 + i;
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(
-                    base + (static_cast<int64_t>(pp) * 2 + (pp == 0 ? first_piece : 0)) * kSlotFloats + c * 128 + lane * 4));
-                sum = __fmaf_rn(fi, li, sum);
-                if (fi != 0.0f || li != 0.0f) {
-                  acc.x = __fmaf_rn(fi, v.x, acc.x);
-                  acc.y = __fmaf_rn(fi, v.y, acc.y);
-                  acc.z = __fmaf_rn(fi, v.z, acc.z);
-                  acc.w = __fmaf_rn(fi, v.w, acc.w);
+                const float gi = __shfl_sync(0xffffffffu, g, i), li = __shfl_sync(0xffffffffu, ls, i);
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(piece_at(p0 + i) + c * 128 + lane * 4));
+                sum = __fmaf_rn(gi, li, sum);
+                if (gi != 0.0f) {
+                  acc.x = __fmaf_rn(gi, v.x, acc.x);
+                  acc.y = __fmaf_rn(gi, v.y, acc.y);
+                  acc.z = __fmaf_rn(gi, v.z, acc.z);
+                  acc.w = __fmaf_rn(gi, v.w, acc.w);
                 }
               }
             }
             const float inv = sum == 0.0f ? 0.0f : __fdividef(1.0f, sum);
             if (lane * 4 < a.c.dim) {
-              uint16_t* o = a.out + token * a.out_token + head * a.out_head + lane * 4;
+              uint16_t* o = a.out + row_out[b][c] + lane * 4;
               const float y[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
 #pragma unroll
               for (int e = 0; e < 4; ++e) o[e] = static_cast<uint16_t>(bf16_pair(y[e], 0.0f));
             }
             if (lane == 0 && a.lse)
-              a.lse[token * a.num_heads + head] =
-                  sum == 0.0f ? -INFINITY : 0.69314718055994531f * (log2f(sum) + top);
+              a.lse[row_lse[b][c]] = sum == 0.0f ? -INFINITY : 0.69314718055994531f * (log2f(sum) + top);
           }
         }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(qempty + b);
     }
-  } else if (kPacked) {
+  } else if constexpr (kPacked) {
     // --------------------------------------------------------- unpacking --
-    const int key = tid - 128 - F::kSoft;
-    bool ok = true;
-    const auto unpack = [&](int32_t tile, bool is_v, int32_t seq) {
-      const int rs = tile % F::kRawStages, s = seq % kRing;
-      if (!is_v) ok = ok && wait_or_dead(rfull + rs, (tile / F::kRawStages) & 1, dead);
-      ok = ok && wait_or_dead(empty + s, ((seq / kRing) & 1) ^ 1u, dead);
-      if (!ok) return;
+    // A thread per key; one warpgroup the K tiles, the other the V tiles.
+    // K becomes 16 + n: the four bits at the top of the mantissa of 16.0 need
+    // no arithmetic; it goes to tensor memory (a key's lane is the thread's),
+    // which spares shared memory a write and the MMAs a read of the tile.
+    // V becomes n - 8, which keeps the rounding of its weights (p s_v in bf16)
+    // from being multiplied by the offset; as an M-major operand it has to be
+    // in shared memory.
+    const int key = (tid - 128 - F::kSoft) & 127;
+    const bool is_v = tid - 128 - F::kSoft >= 128;
+    for (int32_t at = 0; at < my_tiles; ++at) {
+      const int32_t rs = at % F::kRawStages;
+      if (!wait_or_dead(rfull + rs, (at / F::kRawStages) & 1, dead)) break;
       const uint8_t* src = raw + rs * F::kRaw + (is_v ? kTile * F::kRawRow : 0);
-      const uint32_t pair = reinterpret_cast<const uint32_t*>(raw + rs * F::kRaw + 2 * kTile * F::kRawRow)[(is_v ? kTile : 0) + key];
-      (is_v ? v_pair : k_pair)[tile % kPairs][key] = pair;
-      uint8_t* dst = ring + s * F::kStage + key * 128;
+      const uint32_t pair =
+          reinterpret_cast<const uint32_t*>(raw + rs * F::kRaw + 2 * kTile * F::kRawRow)[(is_v ? kTile : 0) + key];
+      uint4 w4[2 * kHalves];  // 16 packed bytes: 32 channels
 #pragma unroll
-      for (int c = 0; c < 2 * kHalves; ++c) {  // 16 packed bytes: 32 channels
+      for (int c = 0; c < 2 * kHalves; ++c) {
         const uint32_t off = key * F::kRawRow + c * 16;
-        const uint4 w4 = *reinterpret_cast<const uint4*>(src + (off ^ ((off >> 3) & (kHalves == 2 ? 0x30u : 0x10u))));
-        const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+        w4[c] = *reinterpret_cast<const uint4*>(src + (off ^ ((off >> 3) & (kHalves == 2 ? 0x30u : 0x10u))));
+      }
+      if (is_v) {
+        const int32_t s = at % kRing;
+        if (!wait_or_dead(empty + s, ((at / kRing) & 1) ^ 1u, dead)) break;
+        v_pair[at % kPairs][key] = pair;
+        uint8_t* dst = ring + s * F::kStage + key * 128;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t o[4];
+        for (int c = 0; c < 2 * kHalves; ++c) {
+          const uint32_t w[4] = {w4[c].x, w4[c].y, w4[c].z, w4[c].w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            // 128 + n in bf16 is 0x4300 | n; minus 136 leaves n - 8 exactly
-            uint32_t y = ((w[e] >> (4 * i)) & 0x000f000fu) | 0x43004300u;
-            asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(o[i]) : "r"(y), "r"(0x43084308u));
+          for (int e = 0; e < 4; ++e) {
+            uint32_t o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              // 128 + n in bf16 is 0x4300 | n; minus 136 leaves n - 8 exactly
+              const uint32_t y = ((w[e] >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+              asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(o[i]) : "r"(y), "r"(0x43084308u));
+            }
+            const int x = c * 4 + e;  // 8 channels
+            *reinterpret_cast<uint4*>(dst + (x >> 3) * 16384 + (((x & 7) ^ (key & 7)) << 4)) =
+                make_uint4(o[0], o[1], o[2], o[3]);
           }
-          const int chunk = c * 4 + e;  // 8 channels
-          *reinterpret_cast<uint4*>(dst + (chunk >> 3) * 16384 + (((chunk & 7) ^ (key & 7)) << 4)) =
-              make_uint4(o[0], o[1], o[2], o[3]);
         }
+        proxy_fence();
+        mbar_arrive(full + s);
+      } else {
+        if (!__all_sync(0xffffffffu, wait_or_dead(kempty + (at & 1), ((at >> 1) & 1) ^ 1u, dead))) break;
+        tc_fence_after();
+        k_pair[at % kPairs][key] = pair;
+        const uint32_t dst = tmem + 4 * kN + (at & 1) * F::kKCols + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+#pragma unroll
+        for (int c = 0; c < 2 * kHalves; ++c) {
+          const uint32_t w[4] = {w4[c].x, w4[c].y, w4[c].z, w4[c].w};
+          float o[16];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            o[4 * e] = __uint_as_float(((w[e] << 3) & 0x00780078u) | 0x41804180u);
+            o[4 * e + 1] = __uint_as_float(((w[e] >> 1) & 0x00780078u) | 0x41804180u);
+            o[4 * e + 2] = __uint_as_float(((w[e] >> 5) & 0x00780078u) | 0x41804180u);
+            o[4 * e + 3] = __uint_as_float(((w[e] >> 9) & 0x00780078u) | 0x41804180u);
+          }
+          tmem_put(dst + c * 16, o);
+        }
+        tmem_put_wait();
+        tc_fence_before();
+        mbar_arrive(kfull + (at & 1));
       }
-      proxy_fence();
-      mbar_arrive(full + s);
-      if (is_v) mbar_arrive(rempty + rs);
-    };
-    int32_t at = 0;
-    for (int32_t k = 0; at < my_tiles && ok; ++k) {
-      ok = wait_or_dead(qfull + k % kNQ, (k / kNQ) & 1, dead);
-      if (!ok) break;
-      const int32_t tiles = items[k % kNQ].tiles, f = at;
-      for (int32_t t = 0; t < tiles; ++t) {
-        unpack(f + t, false, k_seq(f, t));
-        if (t > 0) unpack(f + t - 1, true, v_seq(f, tiles, t - 1));
-      }
-      unpack(f + tiles - 1, true, v_seq(f, tiles, tiles - 1));
-      at += tiles;
+      mbar_arrive(rempty + rs);
     }
   }
   __syncthreads();
   if (s_dead && my_tiles > 0) {
-    const int32_t r0 = s_chunk0 * chunk, r1 = min(a.num_requests, (s_chunk1 + 1) * chunk);
-    for (int32_t r = r0 + tid; r < r1; r += F::kThreads) a.status[r] = SS_ROW_TIMEOUT;
+    for (int32_t r = s_r0 + tid; r <= s_r1; r += F::kThreads) a.status[r] = SS_ROW_TIMEOUT;
   }
   if (warp == 1) {
     __syncwarp();
@@ -1120,10 +1243,10 @@ __global__ void __launch_bounds__(Cfg<kN, kPacked, kHalves>::kThreads, 1)
   }
 }
 
-template <int kN, bool kPacked, int kHalves>
+template <int kN, int kLive, bool kPacked, int kHalves>
 ss_status launch(const AttnArgs& a, cudaStream_t s) {
-  using F = Cfg<kN, kPacked, kHalves>;
-  const void* fn = reinterpret_cast<const void*>(&attn_kernel<kN, kPacked, kHalves>);
+  using F = Cfg<kN, kLive, kPacked, kHalves>;
+  const void* fn = reinterpret_cast<const void*>(&attn_kernel<kN, kLive, kPacked, kHalves>);
   CUtensorMap mk, mv;
   const int unit = 1 << (a.c.page_shift < 7 ? a.c.page_shift : 7);
   if (!make_cache_map(&mk, a.c.k, a.c, unit) || !make_cache_map(&mv, a.c.v, a.c, unit)) return SS_ERR_UNSUPPORTED;
@@ -1133,7 +1256,7 @@ ss_status launch(const AttnArgs& a, cudaStream_t s) {
   if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, F::kSmem);
   if (e == cudaSuccess) {
     const int grid = sms < kMaxCtas ? sms : kMaxCtas;
-    attn_kernel<kN, kPacked, kHalves><<<grid, F::kThreads, F::kSmem, s>>>(mk, mv, a);
+    attn_kernel<kN, kLive, kPacked, kHalves><<<grid, F::kThreads, F::kSmem, s>>>(mk, mv, a);
   }
   return finish(e);
 }
