@@ -79,6 +79,10 @@ ss_status ss_cache_attention(const ss_attention_args* args, void* workspace, siz
   a.num_requests = A.num_requests;
   a.num_heads = A.num_heads;
   a.group = A.num_heads / kv_heads;
+  uint32_t log2 = 0;
+  while ((1 << log2) < a.group) ++log2;
+  a.group_mul = static_cast<uint32_t>((1ull << (31 + log2)) / a.group + 1);
+  a.group_shift = log2 ? log2 - 1 : 0;
   a.max_queries = A.query_offsets ? A.max_queries : 1;
   a.total_queries = A.total_queries;
   a.offsets = A.query_offsets;

@@ -61,13 +61,14 @@ constexpr uint32_t kPolls = 1u << 14;     // bounded waits: polls that each slee
 constexpr uint32_t kSleepNs = 50000;
 constexpr int kInfo = 16;                 // tiles whose page masks are kept
 constexpr int kPairs = 8;                 // tiles whose (s, m) pairs are kept
-constexpr float kUnset = 3.0e38f;         // minus the reference of a row that has seen nothing
+constexpr float kUnset = 3.0e38f;         // in a piece: minus the reference of a row that has seen nothing
 constexpr int kSlotFloats = 128 * 130;    // one piece: up to 128 rows of 128 channels, r and l
 
 struct AttnArgs {
   CacheView c;
   TableView t;
   int32_t num_requests, num_heads, group, max_queries, total_queries;
+  uint32_t group_mul, group_shift;  // n / group = (n * group_mul >> 32) >> group_shift, n < 2^31
   int32_t block_rows;  // rows of an item (the kernel's kLive)
   const int32_t* offsets;
   const int32_t* kv_len;
@@ -123,7 +124,7 @@ struct Cfg {
   static constexpr int kRaw = kPacked ? 2 * kTile * kRawRow + 2 * kTile * 4 : 0;
   static constexpr int kRawStages = kPacked ? 4 : 1;
   // the static arrays, rounded up
-  static constexpr int kMeta = kNQ * (static_cast<int>(sizeof(Item)) + kN * 28 + 64) + kN * 32 + 1536 +
+  static constexpr int kMeta = kNQ * (static_cast<int>(sizeof(Item)) + kN * 28 + 64) + kN * 36 + 1536 +
                                (kGroups > 1 ? kGroups * 256 : 0) + (kPacked ? 2 * kPairs * kTile * 4 : 0);
   static constexpr int kBudget = 232448 - 1024 - kNQ * kQ - 2 * kP - kRawStages * kRaw - kMeta;
   // bf16: tiles of K and V in one ring; 4 bits: V tiles only
@@ -145,6 +146,7 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 // the CTA has given up before.  The caller goes on (single-role warps stop);
 // nothing it computes then is used.
 __device__ __forceinline__ bool wait_or_dead(uint64_t* bar, uint32_t parity, volatile int32_t* dead) {
+#pragma unroll 1
   for (uint32_t i = 0; i < kPolls; ++i) {
     uint32_t done;
     asm volatile(
@@ -170,12 +172,17 @@ __device__ __forceinline__ void tma_4d(void* dst, const CUtensorMap* map, int32_
       : "memory");
 }
 
-// Shared-memory matrix descriptor: start, leading and stride byte offsets,
-// version 1, swizzle layout (2: 128 bytes, 4: 64, 6: 32).
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo, uint32_t layout) {
-  return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) | (static_cast<uint64_t>(lbo >> 4) << 16) |
-         (static_cast<uint64_t>(sbo >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
-         (static_cast<uint64_t>(layout) << 61);
+// Shared-memory matrix descriptor: low word the start address and the leading
+// byte offset, high word the stride byte offset, version 1 and the swizzle
+// layout (2: 128 bytes, 4: 64, 6: 32).
+__device__ __forceinline__ constexpr uint32_t desc_hi(uint32_t sbo, uint32_t layout) {
+  return (sbo >> 4) | (1u << 14) | (layout << 29);
+}
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) {
+  return ((addr & 0x3ffffu) >> 4) | ((lbo >> 4) << 16);
+}
+__device__ __forceinline__ uint64_t desc(uint32_t lo, uint32_t hi) {
+  return static_cast<uint64_t>(lo) | (static_cast<uint64_t>(hi) << 32);
 }
 
 // Instruction descriptor of kind::f16: fp32 accumulator, bf16 A and B, M = 128;
@@ -186,28 +193,37 @@ __device__ __forceinline__ constexpr uint32_t instr_desc(bool mn) {
          (static_cast<uint32_t>(128 >> 4) << 24);
 }
 
-__device__ __forceinline__ void umma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// `leader` is 1 in the one lane that issues.
+__device__ __forceinline__ void umma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate,
+                                     uint32_t leader) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
       : "memory");
 }
 
 // The same with A in tensor memory: lane m holds row m, two channels per column.
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate,
+                                        uint32_t leader) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
       : "memory");
 }
 
-__device__ __forceinline__ void umma_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
-               : "memory");
+__device__ __forceinline__ void umma_commit(uint64_t* bar, uint32_t leader) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar)),
+      "r"(leader)
+      : "memory");
 }
 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -341,6 +357,12 @@ __device__ __forceinline__ float warp_sums(float (&v)[kCount]) {
   return v[0];
 }
 
+// Row number to token (division by multiplication, after Granlund and
+// Montgomery: the multiplier is floor(2^(31+l) / group) + 1, l = ceil(log2 group)).
+__device__ __forceinline__ int32_t token_of(const AttnArgs& a, int32_t row) {
+  return a.group == 1 ? row : static_cast<int32_t>(__umulhi(static_cast<uint32_t>(row), a.group_mul) >> a.group_shift);
+}
+
 // What the scheduler knows of one request.
 struct Request {
   const int32_t* row;
@@ -371,10 +393,10 @@ struct Span {
 __device__ __forceinline__ Span span_of(const AttnArgs& a, const Request& q, int32_t row0) {
   Span s;
   const int32_t unit = min(1 << a.c.page_shift, kTile);
-  const int32_t first = q.base + (a.parents ? 0 : row0 / a.group);  // the lowest position of the block
+  const int32_t first = q.base + (a.parents ? 0 : token_of(a, row0));  // the lowest position of the block
   const int32_t low = (a.window > 0 && first >= a.window) ? first - a.window + 1 : 0;
   s.origin = low & ~(unit - 1);
-  s.end = q.base + (min(row0 + a.block_rows, q.n * a.group) - 1) / a.group + 1;
+  s.end = q.base + token_of(a, min(row0 + a.block_rows, q.n * a.group) - 1) + 1;
   s.sink_end = min(a.sinks, s.origin);
   s.nsink = (s.sink_end + kTile - 1) / kTile;
   s.tiles = s.nsink + (s.end - s.origin + kTile - 1) / kTile;
@@ -384,6 +406,7 @@ __device__ __forceinline__ Span span_of(const AttnArgs& a, const Request& q, int
 // Tiles of one kv head of a request; the lanes of a warp share its blocks.
 __device__ __forceinline__ int32_t request_tiles(const AttnArgs& a, const Request& q, int32_t block0, int32_t step) {
   int32_t sum = 0;
+#pragma unroll 1
   for (int32_t row0 = block0 * a.block_rows; row0 < q.n * a.group; row0 += step * a.block_rows)
     sum += span_of(a, q, row0).tiles;
   return sum;
@@ -407,7 +430,7 @@ __global__ void __launch_bounds__(Cfg<kN, kLive, kPacked, kHalves>::kThreads, 1)
   __shared__ uint32_t info[kInfo];
   __shared__ uint32_t k_pair[kPacked ? kPairs : 1][kPacked ? kTile : 1], v_pair[kPacked ? kPairs : 1][kPacked ? kTile : 1];
   __shared__ uint8_t key_bad[2][F::kGroups > 1 ? F::kGroups : 1][F::kGroups > 1 ? kTile : 1];
-  __shared__ __align__(16) float nref[kN], corr[kN], sums[kN], csums[kN];
+  __shared__ __align__(16) float nref[kN], corr[kN], shift[kN], sums[kN], csums[kN];
   __shared__ float part[4][kN];
   __shared__ uint32_t tmem_slot;
   __shared__ int32_t s_dead, s_last, s_r0, s_r1, s_before, s_tiles0, s_scan[32];
@@ -462,11 +485,13 @@ __global__ void __launch_bounds__(Cfg<kN, kLive, kPacked, kHalves>::kThreads, 1)
   // thread per request when a request is one block, else a warp.
   int32_t* weights = reinterpret_cast<int32_t*>(ring);
   if (a.max_queries * a.group <= kLive) {
+#pragma unroll 1
     for (int32_t r = tid; r < a.num_requests; r += F::kThreads) {
       const Request q = request_of(a, r);
       weights[r] = request_tiles(a, q, 0, 1);
     }
   } else {
+#pragma unroll 1
     for (int32_t r = warp; r < a.num_requests; r += F::kThreads / 32) {
       const Request q = request_of(a, r);
       const int32_t w = __reduce_add_sync(0xffffffffu, request_tiles(a, q, lane, 32));
@@ -474,11 +499,13 @@ __global__ void __launch_bounds__(Cfg<kN, kLive, kPacked, kHalves>::kThreads, 1)
     }
   }
   // The statuses: each by one warp of one CTA.
+#pragma unroll 1
   for (int64_t r = blockIdx.x + static_cast<int64_t>(gridDim.x) * warp; r < a.num_requests;
        r += static_cast<int64_t>(gridDim.x) * (F::kThreads / 32)) {
     const Request q = request_of(a, static_cast<int32_t>(r));
     bool bad = !q.ok;
     if (q.ok && a.parents)
+#pragma unroll 1
       for (int32_t n = 1 + lane; n < q.n; n += 32) {
         const int32_t pa = a.parents[q.qbegin + n];
         bad |= pa < 0 || pa >= n;
@@ -493,6 +520,7 @@ __global__ void __launch_bounds__(Cfg<kN, kLive, kPacked, kHalves>::kThreads, 1)
   const int32_t chunk = (a.num_requests + F::kThreads - 1) / F::kThreads;  // consecutive requests per thread
   const int32_t r_from = min(a.num_requests, tid * chunk), r_to = min(a.num_requests, r_from + chunk);
   int32_t mine = 0;
+#pragma unroll 1
   for (int32_t r = r_from; r < r_to; ++r) mine += weights[r];
   int32_t upto = mine;
 #pragma unroll
@@ -619,73 +647,88 @@ __global__ void __launch_bounds__(Cfg<kN, kLive, kPacked, kHalves>::kThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------- MMAs --
-    if (lane == 0) {
-      constexpr uint32_t kIdS = instr_desc<kN>(false), kIdO = instr_desc<kN>(true);
-      constexpr uint32_t kPLayout = kN >= 64 ? 2u : kN == 32 ? 4u : 6u;
-      const int k_steps = (a.c.dim + 15) / 16;
-      bool ok = true;
-      const auto second = [&](int32_t i, int32_t seq, bool first, int32_t item) {  // O^T += V^T P^T of tile i
-        const int b = i & 1;
-        const int32_t s = seq % kRing;
-        ok = ok && wait_or_dead(pfull + b, (i >> 1) & 1, dead);
-        ok = ok && wait_or_dead(full + s, (seq / kRing) & 1, dead);
-        if (first) ok = ok && wait_or_dead(oempty + (item & 1), ((item >> 1) & 1) ^ 1u, dead);
-        if (!ok) return;
-        tc_fence_after();
-        const uint32_t va = smem_addr(ring + s * F::kStage), pa = smem_addr(pbuf + b * F::kP);
-        const uint32_t d = tmem + 2 * kN + (item & 1) * kN;
+    // The whole warp runs the loop on values that are the same in every lane
+    // (so that descriptors stay in uniform registers); one lane issues.
+    constexpr uint32_t kIdS = instr_desc<kN>(false), kIdO = instr_desc<kN>(true);
+    constexpr uint32_t kPLayout = kN >= 64 ? 2u : kN == 32 ? 4u : 6u;
+    constexpr uint32_t kHiK = desc_hi(1024, 2), kHiP = desc_hi(8 * F::kPitch, kPLayout);
+    const uint32_t leader = lane == 0;
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const int32_t tiles_all = __shfl_sync(0xffffffffu, my_tiles, 0);
+    const uint32_t ring_a = __shfl_sync(0xffffffffu, smem_addr(ring), 0);
+    const uint32_t p_a = ring_a + kRing * F::kStage, q_a = p_a + 2 * F::kP;
+    const int k_steps = (a.c.dim + 15) / 16;
+    bool ok = true;
+    const auto wait = [&](uint64_t* bar, int32_t use) {
+      if (ok) ok = __all_sync(0xffffffffu, wait_or_dead(bar, use & 1, dead));
+    };
+    const auto second = [&](int32_t i, int32_t seq, bool first, int32_t item) {  // O^T += V^T P^T of tile i
+      const int b = i & 1;
+      const int32_t s = seq % kRing;
+      wait(pfull + b, i >> 1);
+      wait(full + s, seq / kRing);
+      if (first) wait(oempty + (item & 1), (item >> 1) + 1);
+      if (!ok) return;
+      tc_fence_after();
+      const uint32_t va = desc_lo(ring_a + s * F::kStage, kHalves == 2 ? 16384 : 0);
+      const uint32_t pa = desc_lo(p_a + b * F::kP, kTile * 128);
+      const uint32_t d = tm + 2 * kN + (item & 1) * kN;
 #pragma unroll
-        for (int kk = 0; kk < kTile / 16; ++kk)
-          umma(d, smem_desc(va + kk * 16 * 128, kHalves == 2 ? 16384 : 0, 1024, 2),
-               smem_desc(pa + kk * 16 * F::kPitch, kTile * 128, 8 * F::kPitch, kPLayout), kIdO, (!first || kk > 0) ? 1u : 0u);
-        umma_commit(empty + s);
-        umma_commit(pdone + b);
-      };
-      int32_t at = 0, k = 0;
-      bool prev_first = false;
-      int32_t prev_item = 0, prev_seq = 0;
-      while (at < my_tiles && ok) {
-        const int qb = k % kNQ;
-        if (kNQ == 1 && at > 0) second(at - 1, prev_seq, prev_first, prev_item);  // else the next item's queries cannot come
-        ok = ok && wait_or_dead(qfull + qb, (k / kNQ) & 1, dead);
-        if (!ok) break;
-        const int32_t tiles = items[qb].tiles, f = at;
-        const uint32_t qa = smem_addr(qbuf + qb * F::kQ);
-        for (int32_t t = 0; t < tiles && ok; ++t, ++at) {
-          const int b = at & 1;
-          ok = ok && wait_or_dead(sempty + b, ((at >> 1) & 1) ^ 1u, dead);
-          if constexpr (kPacked) {
-            ok = ok && wait_or_dead(kfull + b, (at >> 1) & 1, dead);
-            if (!ok) break;
-            tc_fence_after();
-            for (int kk = 0; kk < k_steps; ++kk)
-              umma_ts(tmem + b * kN, tmem + 4 * kN + b * F::kKCols + kk * 8,
-                      smem_desc(qa + (kk >> 2) * (kN * 128) + (kk & 3) * 32, 16, 1024, 2), kIdS, kk > 0 ? 1u : 0u);
-            umma_commit(kempty + b);
-          } else {
-            const int32_t seq = k_seq(f, t), s = seq % kRing;
-            ok = ok && wait_or_dead(full + s, (seq / kRing) & 1, dead);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t ka = smem_addr(ring + s * F::kStage);
-            for (int kk = 0; kk < k_steps; ++kk)
-              umma(tmem + b * kN, smem_desc(ka + (kk >> 2) * 16384 + (kk & 3) * 32, 16, 1024, 2),
-                   smem_desc(qa + (kk >> 2) * (kN * 128) + (kk & 3) * 32, 16, 1024, 2), kIdS, kk > 0 ? 1u : 0u);
-            umma_commit(empty + s);
-          }
-          umma_commit(sfull + b);
-          if (at > 0 && !(kNQ == 1 && t == 0)) second(at - 1, prev_seq, prev_first, prev_item);
-          prev_seq = v_seq(f, tiles, t);
-          prev_first = t == 0;
-          prev_item = k;
+      for (int kk = 0; kk < kTile / 16; ++kk)
+        umma(d, desc(va + kk * (16 * 128 >> 4), kHiK), desc(pa + kk * (16 * F::kPitch >> 4), kHiP), kIdO,
+             (!first || kk > 0) ? 1u : 0u, leader);
+      umma_commit(empty + s, leader);
+      umma_commit(pdone + b, leader);
+    };
+    int32_t at = 0;
+    bool prev_first = false;
+    int32_t prev_item = 0, prev_seq = 0;
+#pragma unroll 1
+    for (int32_t k = 0; at < tiles_all && ok; ++k) {
+      const int qb = k % kNQ;
+      if (kNQ == 1 && at > 0) second(at - 1, prev_seq, prev_first, prev_item);  // else the next item's queries cannot come
+      wait(qfull + qb, k / kNQ);
+      if (!ok) break;
+      const int32_t tiles = __shfl_sync(0xffffffffu, items[qb].tiles, 0), f = at;
+      const uint32_t qa = desc_lo(q_a + qb * F::kQ, 16);
+#pragma unroll 1
+      for (int32_t t = 0; t < tiles; ++t, ++at) {
+        const int b = at & 1;
+        wait(sempty + b, (at >> 1) + 1);
+        if constexpr (kPacked) {
+          wait(kfull + b, at >> 1);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 4 * kHalves; ++kk)
+            if (kk < k_steps)
+              umma_ts(tm + b * kN, tm + 4 * kN + b * F::kKCols + kk * 8,
+                      desc(qa + (kk >> 2) * (kN * 128 >> 4) + (kk & 3) * 2, kHiK), kIdS, kk > 0 ? 1u : 0u, leader);
+          umma_commit(kempty + b, leader);
+        } else {
+          const int32_t seq = k_seq(f, t), s = seq % kRing;
+          wait(full + s, seq / kRing);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t ka = desc_lo(ring_a + s * F::kStage, 16);
+#pragma unroll
+          for (int kk = 0; kk < 4 * kHalves; ++kk)
+            if (kk < k_steps)
+              umma(tm + b * kN, desc(ka + (kk >> 2) * (16384 >> 4) + (kk & 3) * 2, kHiK),
+                   desc(qa + (kk >> 2) * (kN * 128 >> 4) + (kk & 3) * 2, kHiK), kIdS, kk > 0 ? 1u : 0u, leader);
+          umma_commit(empty + s, leader);
         }
-        ++k;
+        umma_commit(sfull + b, leader);
+        if (at > 0 && !(kNQ == 1 && t == 0)) second(at - 1, prev_seq, prev_first, prev_item);
+        prev_seq = v_seq(f, tiles, t);
+        prev_first = t == 0;
+        prev_item = k;
       }
-      if (ok) second(my_tiles - 1, prev_seq, prev_first, prev_item);
-      if (!ok) {  // given up: the MMAs in flight end before tensor memory is freed
-        umma_commit(&drain);
-        mbar_wait_bounded(&drain, 0, 1u << 16);
-      }
+    }
+    if (ok) second(tiles_all - 1, prev_seq, prev_first, prev_item);
+    if (!ok && lane == 0) {  // given up: the MMAs in flight end before tensor memory is freed
+      umma_commit(&drain, 1);
+      mbar_wait_bounded(&drain, 0, 1u << 16);
     }
   } else if (warp < 4) {
     // --------------------------------------------- the items' queries --
@@ -698,6 +741,7 @@ __global__ void __launch_bounds__(Cfg<kN, kLive, kPacked, kHalves>::kThreads, 1)
     int32_t skip = static_cast<int32_t>((lo - before) - static_cast<int64_t>(head) * w);  // tiles of the head passed
     int64_t start = before + static_cast<int64_t>(head) * w;  // the item's first tile
     int32_t row0 = 0;
+#pragma unroll 1
     for (;; row0 += 32 * kLive) {  // the block that holds it: 32 blocks at a time
       const int32_t mine_row = row0 + lane * kLive;
       const int32_t n = mine_row < q.n * a.group ? span_of(a, q, mine_row).tiles : 0;
@@ -744,14 +788,16 @@ __global__ void __launch_bounds__(Cfg<kN, kLive, kPacked, kHalves>::kThreads, 1)
         it.row = q.row;
         items[b] = it;
       }
+#pragma unroll 1
       for (int n = lt; n < kN; n += 64) {
-        const int32_t token = (row0 + n) / a.group, h = head * a.group + (row0 + n - token * a.group);
+        const int32_t token = token_of(a, row0 + n), h = head * a.group + (row0 + n - token * a.group);
         const bool live = n < rows;
         int32_t depth = token;
         uint64_t path = ~0ull;
         if (a.parents && live) {
           depth = 0;
           path = 1ull << token;
+#pragma unroll 1
           for (int32_t u = token; u > 0; ++depth) {
             const int32_t pa = a.parents[q.qbegin + u];
             u = (pa < 0 || pa >= u) ? 0 : pa;
@@ -767,6 +813,7 @@ __global__ void __launch_bounds__(Cfg<kN, kLive, kPacked, kHalves>::kThreads, 1)
       }
       if (a.parents && lt < q.n) {
         int32_t depth = 0;
+#pragma unroll 1
         for (int32_t u = lt; u > 0; ++depth) {
           const int32_t pa = a.parents[q.qbegin + u];
           u = (pa < 0 || pa >= u) ? 0 : pa;
@@ -780,7 +827,7 @@ __global__ void __launch_bounds__(Cfg<kN, kLive, kPacked, kHalves>::kThreads, 1)
         uint4 x[8];
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-          const int n = n0 + 4 * u, token = (row0 + n) / a.group;
+          const int n = n0 + 4 * u, token = token_of(a, row0 + n);
           x[u] = make_uint4(0u, 0u, 0u, 0u);
           if (n < rows && ch * 8 < a.c.dim)
             x[u] = *reinterpret_cast<const uint4*>(
@@ -843,11 +890,14 @@ __global__ void __launch_bounds__(Cfg<kN, kLive, kPacked, kHalves>::kThreads, 1)
       if (kPacked)
 #pragma unroll
         for (int n = 0; n < kCols; ++n) cs[n] = 0.0f;
-      if (lt < kCols) nref[c0 + lt] = kUnset;
+      if (lt < kCols) nref[c0 + lt] = 0.0f;
+      bool unset = true;  // thread i of the warpgroup: row i has seen no key yet
+      bool fresh = true;  // some row has not
       const uint32_t o_base = tmem + 2 * kN + (k & 1) * kN + c0 + lanes;
       const int32_t f = at;
-      const int32_t first_pos = it.base + (tree ? 0 : it.row0 / a.group);
-      const int32_t last_pos = it.base + (it.row0 + it.rows - 1) / a.group;  // of a tree: at most
+      const int32_t first_pos = it.base + (tree ? 0 : token_of(a, it.row0));
+      const int32_t last_pos = it.base + token_of(a, it.row0 + it.rows - 1);  // of a tree: at most
+#pragma unroll 1
       for (int32_t t = 0; t < it.tiles; ++t, ++at) {
         const int sb = at & 1;
         const int32_t n = it.tile0 + t;
@@ -930,39 +980,37 @@ __global__ void __launch_bounds__(Cfg<kN, kLive, kPacked, kHalves>::kThreads, 1)
         }
         // x_nj - r_n of this key, every row
         float x[kCols];
-        const auto scores = [&](bool with_ref) {
-          tmem_ld(tmem + sb * kN + c0 + lanes, x);
+        tmem_ld(tmem + sb * kN + c0 + lanes, x);
+        tc_fence_before();
+        mbar_arrive(sempty + sb);
 #pragma unroll
-          for (int i = 0; i < kCols; i += 4) {
-            const float4 r4 = *reinterpret_cast<const float4*>(nref + c0 + i);
-            float y[4] = {r4.x, r4.y, r4.z, r4.w};
-            if (!with_ref) y[0] = y[1] = y[2] = y[3] = 0.0f;
-            if (kPacked) {
-              const float4 q4 = *reinterpret_cast<const float4*>(&row_qsum[b][c0 + i]);
-              y[0] = __fmaf_rn(kb, q4.x, y[0]);
-              y[1] = __fmaf_rn(kb, q4.y, y[1]);
-              y[2] = __fmaf_rn(kb, q4.z, y[2]);
-              y[3] = __fmaf_rn(kb, q4.w, y[3]);
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[i + e] = __fmaf_rn(x[i + e], ka, y[e]);
+        for (int i = 0; i < kCols; i += 4) {
+          const float4 r4 = *reinterpret_cast<const float4*>(nref + c0 + i);
+          float y[4] = {r4.x, r4.y, r4.z, r4.w};
+          if (kPacked) {
+            const float4 q4 = *reinterpret_cast<const float4*>(&row_qsum[b][c0 + i]);
+            y[0] = __fmaf_rn(kb, q4.x, y[0]);
+            y[1] = __fmaf_rn(kb, q4.y, y[1]);
+            y[2] = __fmaf_rn(kb, q4.z, y[2]);
+            y[3] = __fmaf_rn(kb, q4.w, y[3]);
           }
-          if (masked)
 #pragma unroll
-            for (int i = 0; i < kCols; ++i) x[i] = ((vis >> i) & 1u) ? x[i] : -INFINITY;
-        };
-        bool pass = true;
-        if (t > 0) {
-          scores(true);
+          for (int e = 0; e < 4; ++e) x[i + e] = __fmaf_rn(x[i + e], ka, y[e]);
+        }
+        if (masked)
+#pragma unroll
+          for (int i = 0; i < kCols; ++i) x[i] = ((vis >> i) & 1u) ? x[i] : -INFINITY;
+        bool pass = fresh;
+        if (!pass) {
           float most = x[0];
 #pragma unroll
           for (int i = 1; i < kCols; ++i) most = fmaxf(most, x[i]);
           pass = bar_any(bar, 128, most > 8.0f);
         }
         if (pass) {
-          // some row's score passes its reference by more than 8: the new
-          // reference is the row's largest score of the tile
-          scores(false);
+          // some row's score passes its reference by more than 8 (or the row
+          // has none yet): the new reference is the row's largest score of the
+          // tile
 #pragma unroll
           for (int i = 0; i < kCols; ++i) {
             const float y = fmaxf(x[i], -INFINITY);  // a NaN counts as nothing
@@ -973,15 +1021,14 @@ __global__ void __launch_bounds__(Cfg<kN, kLive, kPacked, kHalves>::kThreads, 1)
           if (lt < kCols) {
             const int c = c0 + lt;
             const float m = fmaxf(fmaxf(part[0][c], part[1][c]), fmaxf(part[2][c], part[3][c]));
-            const float old = nref[c];
-            float g = 1.0f;
-            if (m + old > 8.0f) {
-              nref[c] = -m;
-              g = old == kUnset ? 0.0f : ex2(-m - old);  // 2^(old reference - new)
-            }
-            corr[c] = g;
+            const bool move = m > (unset ? -INFINITY : 8.0f);
+            corr[c] = !move ? 1.0f : unset ? 0.0f : ex2(-m);  // 2^(old reference - new)
+            shift[c] = move ? m : 0.0f;
+            if (move) nref[c] -= m;
+            unset = unset && !move;
           }
-          bar_sync(bar, 128);
+          // is there a row left that has seen nothing?
+          fresh = bar_any(bar, 128, lt < kCols && c0 + lt < it.rows && unset);
           bool change = false;
 #pragma unroll
           for (int i = 0; i < kCols; ++i) {
@@ -989,19 +1036,18 @@ __global__ void __launch_bounds__(Cfg<kN, kLive, kPacked, kHalves>::kThreads, 1)
             change |= g != 1.0f;
             l[i] *= g;
             if (kPacked) cs[i] *= g;
+            x[i] -= shift[c0 + i];
           }
           if (change && t > 0) {
             wait_or_dead(pdone + ((at - 1) & 1), ((at - 1) >> 1) & 1, dead);
             tc_fence_after();
-            tmem_ld(o_base, x);
+            float o[kCols];
+            tmem_ld(o_base, o);
 #pragma unroll
-            for (int i = 0; i < kCols; ++i) x[i] *= corr[c0 + i];
-            tmem_st(o_base, x);
+            for (int i = 0; i < kCols; ++i) o[i] *= corr[c0 + i];
+            tmem_st(o_base, o);
           }
-          scores(true);
         }
-        tc_fence_before();
-        mbar_arrive(sempty + sb);
         if (kPacked) {
           const int32_t seq = v_seq(f, it.tiles, t), s = seq % kRing;
           wait_or_dead(full + s, (seq / kRing) & 1, dead);  // V is unpacked, so its pairs are there
@@ -1083,7 +1129,7 @@ __global__ void __launch_bounds__(Cfg<kN, kLive, kPacked, kHalves>::kThreads, 1)
       if (lt < kCols && c0 + lt < rows) {
         const int c = c0 + lt;
         if (!whole) {
-          __stcg(piece + 128 * 128 + 2 * c, nref[c]);
+          __stcg(piece + 128 * 128 + 2 * c, unset ? kUnset : nref[c]);
           __stcg(piece + 128 * 128 + 2 * c + 1, sums[c]);
         } else if (a.lse) {
           a.lse[row_lse[b][c]] = sums[c] == 0.0f ? -INFINITY : 0.69314718055994531f * (log2f(sums[c]) - nref[c]);
@@ -1112,8 +1158,10 @@ __global__ void __launch_bounds__(Cfg<kN, kLive, kPacked, kHalves>::kThreads, 1)
           const auto piece_at = [&](int32_t p) {
             return base + (static_cast<int64_t>(p) * 2 + (p == 0 ? first_piece : 0)) * kSlotFloats;
           };
+#pragma unroll 1
           for (int c = st >> 5; c < rows; c += F::kSoft / 32) {
             float top = -INFINITY;  // the largest reference
+#pragma unroll 1
             for (int32_t p = lane; p < parts; p += 32) {
               const float nr = __ldcg(piece_at(p) + 128 * 128 + 2 * c);
               top = fmaxf(top, nr == kUnset ? -INFINITY : -nr);
@@ -1122,6 +1170,7 @@ __global__ void __launch_bounds__(Cfg<kN, kLive, kPacked, kHalves>::kThreads, 1)
             for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
             float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             float sum = 0.0f;
+#pragma unroll 1
             for (int32_t p0 = 0; p0 < parts; p0 += 32) {
               float g = 0.0f, ls = 0.0f;
               if (p0 + lane < parts) {
@@ -1171,6 +1220,7 @@ __global__ void __launch_bounds__(Cfg<kN, kLive, kPacked, kHalves>::kThreads, 1)
     // in shared memory.
     const int key = (tid - 128 - F::kSoft) & 127;
     const bool is_v = tid - 128 - F::kSoft >= 128;
+#pragma unroll 1
     for (int32_t at = 0; at < my_tiles; ++at) {
       const int32_t rs = at % F::kRawStages;
       if (!wait_or_dead(rfull + rs, (at / F::kRawStages) & 1, dead)) break;
