@@ -22,9 +22,9 @@
 // and K and V enter the tensor cores exactly as they lie in the cache ([key]
 // [channel], K as a K-major and V as an M-major operand).
 //
-// 4 bits.  A row stands for s n + m, n = 0..15.  n + 16 and n - 8 are exact in
-// bf16, so the tensor cores multiply exact integers, and s and m enter in fp32:
-//   q.k = s_k (q.(n + 16)) + (m_k - 16 s_k) sum(q)
+// 4 bits.  A row stands for s n + m, n = 0..15.  The tensor cores multiply the
+// exact integers, and s and m enter in fp32:
+//   q.k = s_k (q.n) + m_k sum(q)
 //   sum_j p v = sum_j (p s_v) (n - 8) + sum_j p (m_v + 8 s_v),
 // the first in fp32 on the thread that owns the key, the second by rounding
 // p s_v to bf16 instead of p, plus one fp32 sum per row.
@@ -40,7 +40,7 @@
 // them up in the CTAs' order.
 //
 // Warps: 0 tensor copies (one box per page and 64 channels, straight from the
-// page table), 1 tcgen05.mma, 2-3 the next item's queries and masks, then the
+// page table), 1 and 2 tcgen05.mma, 3 the next item's queries and masks, then the
 // softmax warps (128 threads per 8 to 32 rows) and for 4 bits eight warps that
 // unpack.
 #pragma once
@@ -106,36 +106,43 @@ struct Item {
   const int32_t* row;
 };
 
-// kN: rows of the MMAs; kLive: of these the softmax warps handle the first
-// kLive (8 of 16 for the requests with no more rows than that).
-template <int kN, int kLive, bool kPacked, int kHalves>
+// kLive: rows of an item; kN: rows of the second product's MMAs (16 at least);
+// kNS: columns of the first product (4 bits: two per row).
+template <int kLive, bool kPacked, int kHalves>
 struct Cfg {
-  static constexpr int kGroups = kN <= 16 ? 1 : kN == 32 ? 2 : kPacked ? 2 : 4;  // softmax warpgroups
+  static constexpr int kN = kLive < 16 ? 16 : kLive;
+  static constexpr int kNS = kPacked ? 2 * kLive : kN;
+  static constexpr int kGroups = kLive <= 16 ? 1 : kLive == 32 ? 2 : kPacked ? 2 : 4;  // softmax warpgroups
   static constexpr int kCols = kLive / kGroups;              // rows per softmax thread
   static constexpr int kSoft = 128 * kGroups;
   static constexpr int kUnpack = kPacked ? 256 : 0;          // K tiles by one warpgroup, V tiles by the other
   static constexpr int kThreads = 128 + kSoft + kUnpack;
   static constexpr int kStage = kHalves * 16384;             // 128 keys x 64 channels x 2 bytes per half
-  static constexpr int kQ = kHalves * kN * 128;
-  static constexpr int kNQ = kN >= 128 || (kPacked && kN >= 64) ? 1 : 2;
+  static constexpr int kQ = kPacked ? kNS * 128 : kHalves * kN * 128;
+  static constexpr int kNQ = kLive >= 128 ? 1 : 2;
   static constexpr int kPitch = kN >= 64 ? 128 : kN * 2;     // bytes per key of a P block
   static constexpr int kP = kTile * kN * 2;
+  static constexpr int kPBufs = kLive >= 128 ? 1 : 2;
   static constexpr int kRawRow = 32 * kHalves;               // packed bytes per key
   static constexpr int kRaw = kPacked ? 2 * kTile * kRawRow + 2 * kTile * 4 : 0;
   static constexpr int kRawStages = kPacked ? 4 : 1;
   // the static arrays, rounded up
-  static constexpr int kMeta = kNQ * (static_cast<int>(sizeof(Item)) + kN * 28 + 64) + kN * 36 + 1536 +
+  static constexpr int kMeta = kNQ * (static_cast<int>(sizeof(Item)) + kN * 32 + 64) + kN * 36 + 1536 +
                                (kGroups > 1 ? kGroups * 256 : 0) + (kPacked ? 2 * kPairs * kTile * 4 : 0);
-  static constexpr int kBudget = 232448 - 1024 - kNQ * kQ - 2 * kP - kRawStages * kRaw - kMeta;
-  // bf16: tiles of K and V in one ring; 4 bits: V tiles only
+  static constexpr int kBudget = 232448 - 1024 - kNQ * kQ - kPBufs * kP - kRawStages * kRaw - kMeta;
+  // K and V have a ring each, so that whoever waits for a slot has used the
+  // slot's previous contents itself: a parity wait tells two phases apart, no
+  // more.  4 bits: only V's is in shared memory, K's two slots are columns.
   static constexpr int kMost = kPacked ? 4 : 8;
   static constexpr int kRing = kBudget / kStage < kMost ? kBudget / kStage : kMost;
-  static constexpr int kSmem = 1024 + kRing * kStage + kNQ * kQ + 2 * kP + kRawStages * kRaw;
-  // tensor-memory columns: S x 2, O x 2, and for 4 bits K x 2 (two channels per column)
-  static constexpr uint32_t kKCols = kPacked ? 32 * kHalves : 0;
-  static constexpr uint32_t kUsed = 4 * kN + 2 * kKCols;
+  static constexpr int kKs = kPacked ? 2 : kRing / 2, kVs = kPacked ? kRing : kRing - kKs;
+  static constexpr int kSmem = 1024 + kRing * kStage + kNQ * kQ + kPBufs * kP + kRawStages * kRaw;
+  // tensor-memory columns: S x 2, O x 2, and for 4 bits K x 2 (four channels per column)
+  static constexpr uint32_t kOCol = 2 * kNS, kKCol = kOCol + 2 * kN;
+  static constexpr uint32_t kKCols = kPacked ? 16 * kHalves : 0;
+  static constexpr uint32_t kUsed = kKCol + 2 * kKCols;
   static constexpr uint32_t kTmem = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
-  static_assert(kRing >= (kPacked ? 2 : 3), "K, the next K and V are held at once");
+  static_assert(kKs >= 1 && kVs >= 2, "a tile in use and one on its way");
 };
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
@@ -146,6 +153,7 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 // the CTA has given up before.  The caller goes on (single-role warps stop);
 // nothing it computes then is used.
 __device__ __forceinline__ bool wait_or_dead(uint64_t* bar, uint32_t parity, volatile int32_t* dead) {
+  if (mbar_try_wait(bar, parity)) return true;  // 41 clocks when complete; with a time limit 116
 #pragma unroll 1
   for (uint32_t i = 0; i < kPolls; ++i) {
     uint32_t done;
@@ -185,12 +193,17 @@ __device__ __forceinline__ uint64_t desc(uint32_t lo, uint32_t hi) {
   return static_cast<uint64_t>(lo) | (static_cast<uint64_t>(hi) << 32);
 }
 
-// Instruction descriptor of kind::f16: fp32 accumulator, bf16 A and B, M = 128;
-// `mn`: both operands M-/N-major instead of K-major.
+// Instruction descriptors: fp32 accumulator, M = 128.  kind::f16 with bf16 A
+// and B, `mn`: both M-/N-major instead of K-major; kind::f8f6f4 with e4m3.
 template <int kN>
 __device__ __forceinline__ constexpr uint32_t instr_desc(bool mn) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (mn ? (3u << 15) : 0u) | (static_cast<uint32_t>(kN >> 3) << 17) |
          (static_cast<uint32_t>(128 >> 4) << 24);
+}
+
+template <int kN>
+__device__ __forceinline__ constexpr uint32_t instr_desc_e4m3() {
+  return (1u << 4) | (static_cast<uint32_t>(kN >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
 }
 
 // `leader` is 1 in the one lane that issues.
@@ -205,14 +218,14 @@ __device__ __forceinline__ void umma(uint32_t d, uint64_t a, uint64_t b, uint32_
       : "memory");
 }
 
-// The same with A in tensor memory: lane m holds row m, two channels per column.
+// e4m3, A in tensor memory: lane m holds row m, four channels per column.
 __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate,
                                         uint32_t leader) {
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "setp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
       : "memory");
 }
@@ -307,6 +320,22 @@ __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
+}
+
+// Two fp32 values as e4m3 (a in the low byte; finite values saturate), and back.
+__device__ __forceinline__ uint32_t e4m3_pair(float a, float b) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
+__device__ __forceinline__ float2 e4m3_floats(uint32_t pair) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(pair)));
+  float2 f;
+  asm("{\n\t.reg .f16 l, u;\n\tmov.b32 {l, u}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, u;\n\t}"
+      : "=f"(f.x), "=f"(f.y)
+      : "r"(h));
+  return f;
 }
 
 // Barrier `id` over `n` threads; the second form also says whether any thread
@@ -412,20 +441,20 @@ __device__ __forceinline__ int32_t request_tiles(const AttnArgs& a, const Reques
   return sum;
 }
 
-template <int kN, int kLive, bool kPacked, int kHalves>
-__global__ void __launch_bounds__(Cfg<kN, kLive, kPacked, kHalves>::kThreads, 1)
+template <int kLive, bool kPacked, int kHalves>
+__global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
     attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const AttnArgs a) {
-  using F = Cfg<kN, kLive, kPacked, kHalves>;
-  constexpr int kRing = F::kRing, kNQ = F::kNQ, kCols = F::kCols;
+  using F = Cfg<kLive, kPacked, kHalves>;
+  constexpr int kRing = F::kRing, kKs = F::kKs, kVs = F::kVs, kNQ = F::kNQ, kCols = F::kCols, kN = F::kN, kNS = F::kNS;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t full[kRing], empty[kRing], sfull[2], sempty[2], pfull[2], pdone[2], oempty[2],
-      qfull[kNQ], qempty[kNQ], rfull[F::kRawStages], rempty[F::kRawStages], kfull[2], kempty[2], looked, drain;
+  __shared__ __align__(8) uint64_t kfull[kKs], kempty[kKs], vfull[kVs], vempty[kVs], sfull[2], sempty[2], pfull[2], pdone[2], oempty[2],
+      qfull[kNQ], qempty[kNQ], rfull[F::kRawStages], rempty[F::kRawStages], looked, drain[2];
   __shared__ Item items[kNQ];
   __shared__ __align__(16) int32_t row_pos[kNQ][kN];
   __shared__ __align__(16) uint64_t row_path[kNQ][kN];
   __shared__ int64_t row_out[kNQ][kN];
   __shared__ int32_t row_lse[kNQ][kN];
-  __shared__ __align__(16) float row_qsum[kPacked ? kNQ : 1][kPacked ? kN : 4];
+  __shared__ __align__(16) float row_qsum[kPacked ? kNQ : 1][kPacked ? kN : 4], row_unit[kPacked ? kNQ : 1][kPacked ? kN : 4];
   __shared__ uint8_t node_depth[kNQ][SS_TREE_MAX_NODES];
   __shared__ uint32_t info[kInfo];
   __shared__ uint32_t k_pair[kPacked ? kPairs : 1][kPacked ? kTile : 1], v_pair[kPacked ? kPairs : 1][kPacked ? kTile : 1];
@@ -437,15 +466,20 @@ __global__ void __launch_bounds__(Cfg<kN, kLive, kPacked, kHalves>::kThreads, 1)
 
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* pbuf = ring + kRing * F::kStage;
-  uint8_t* qbuf = pbuf + 2 * F::kP;
+  uint8_t* qbuf = pbuf + F::kPBufs * F::kP;
+  uint8_t* vring = ring + (kPacked ? 0 : kKs) * F::kStage;  // after K's slots
   uint8_t* raw = qbuf + kNQ * F::kQ;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int32_t* dead = &s_dead;
 
   if (tid == 0) {
-    for (int i = 0; i < kRing; ++i) {
-      mbar_init(full + i, kPacked ? 128 : 1);
-      mbar_init(empty + i, 1);
+    for (int i = 0; i < kKs; ++i) {
+      mbar_init(kfull + i, kPacked ? 128 : 1);
+      mbar_init(kempty + i, 1);
+    }
+    for (int i = 0; i < kVs; ++i) {
+      mbar_init(vfull + i, kPacked ? 128 : 1);
+      mbar_init(vempty + i, 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(sfull + i, 1);
@@ -455,12 +489,8 @@ __global__ void __launch_bounds__(Cfg<kN, kLive, kPacked, kHalves>::kThreads, 1)
       mbar_init(oempty + i, F::kSoft);
     }
     for (int i = 0; i < kNQ; ++i) {
-      mbar_init(qfull + i, 64);
+      mbar_init(qfull + i, 32);
       mbar_init(qempty + i, 1 + F::kSoft / 32);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(kfull + i, 128);
-      mbar_init(kempty + i, 1);
     }
     if (kPacked)
       for (int i = 0; i < F::kRawStages; ++i) {
@@ -468,7 +498,8 @@ __global__ void __launch_bounds__(Cfg<kN, kLive, kPacked, kHalves>::kThreads, 1)
         mbar_init(rempty + i, 256);
       }
     mbar_init(&looked, F::kSoft);
-    mbar_init(&drain, 1);
+    mbar_init(&drain[0], 1);
+    mbar_init(&drain[1], 1);
     s_dead = 0;
     s_r0 = s_r1 = 0;
     fence_barrier_init();
@@ -555,42 +586,35 @@ __global__ void __launch_bounds__(Cfg<kN, kLive, kPacked, kHalves>::kThreads, 1)
   }
   proxy_fence();  // the weights' reads before the ring's copies
   __syncthreads();
-  // The ring's order within an item whose first tile is the CTA's tile f and
-  // that has m tiles: K0, K1, V0, K2, V1, .., K(m-1), V(m-2), V(m-1), as the
-  // MMAs take them.
-  const auto k_seq = [](int32_t f, int32_t t) { return 2 * f + (t == 0 ? 0 : 2 * t - 1); };
-  const auto v_seq = [](int32_t f, int32_t m, int32_t t) {
-    return kPacked ? f + t : 2 * f + (t == m - 1 ? 2 * t + 1 : 2 * t + 2);  // 4 bits: only V is in the ring
-  };
-
   if (my_tiles == 0) {
     // fewer tiles than CTAs
   } else if (warp == 0) {
     // ---------------------------------------------------- tensor copies --
     const int32_t unit_shift = min(a.c.page_shift, 7), units = kTile >> unit_shift;
     int32_t at = 0, k = 0;  // tile, item
-    int32_t page_k = 0, slot_k = 0;
     bool ok = true;
-    int32_t last_seq = -1;
-    const auto issue = [&](const CUtensorMap* map, int32_t seq, int32_t page, int32_t slot, int32_t head) {
-      const int s = seq % kRing;
-      if (ok) ok = wait_or_dead(empty + s, ((seq / kRing) & 1) ^ 1u, dead);
+    int32_t k_tiles = 0, v_tiles = 0;  // issued
+    const auto issue = [&](const CUtensorMap* map, uint8_t* dst, uint64_t* filled, uint64_t* free, int32_t use, int32_t page,
+                           int32_t slot, int32_t head) {
+      if (ok) ok = wait_or_dead(free, (use & 1) ^ 1u, dead);
       ok = __all_sync(0xffffffffu, ok);
-      if (!ok) return;
-      if (lane == 0) mbar_arrive_expect_tx(full + s, F::kStage);
+      if (!ok) return false;
+      if (lane == 0) mbar_arrive_expect_tx(filled, F::kStage);
       __syncwarp();
       if (lane < units)
+#pragma unroll
         for (int h = 0; h < kHalves; ++h)
-          tma_4d(ring + s * F::kStage + h * 16384 + (lane << unit_shift) * 128, map, h * 64, slot, head, page, full + s);
-      last_seq = seq;
+          tma_4d(dst + h * 16384 + (lane << unit_shift) * 128, map, h * 64, slot, head, page, filled);
+      return true;
     };
+#pragma unroll 1
     while (at < my_tiles && ok) {
       const int b = k % kNQ;
       ok = wait_or_dead(qfull + b, (k / kNQ) & 1, dead);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       const Item it = items[b];
-      const int32_t f = at;
+#pragma unroll 1
       for (int32_t t = 0; t < it.tiles && ok; ++t, ++at) {
         const int32_t n = it.tile0 + t;
         const bool sink = n < it.nsink;
@@ -624,13 +648,11 @@ __global__ void __launch_bounds__(Cfg<kN, kLive, kPacked, kHalves>::kThreads, 1)
         } else {
           if (lane == 0) *reinterpret_cast<volatile uint32_t*>(info + at % kInfo) = there;
           const int32_t pg = page < 0 ? a.c.num_pages : page;
-          issue(&tm_k, k_seq(f, t), pg, slot, it.head);
-          if (t > 0) issue(&tm_v, v_seq(f, it.tiles, t - 1), page_k, slot_k, it.head);
-          page_k = pg;
-          slot_k = slot;
+          const int ks = at % kKs, vs = at % kVs;
+          k_tiles += issue(&tm_k, ring + ks * F::kStage, kfull + ks, kempty + ks, at / kKs, pg, slot, it.head);
+          v_tiles += issue(&tm_v, vring + vs * F::kStage, vfull + vs, vempty + vs, at / kVs, pg, slot, it.head);
         }
       }
-      if (!kPacked && ok) issue(&tm_v, v_seq(f, it.tiles, it.tiles - 1), page_k, slot_k, it.head);
       __syncwarp();
       if (lane == 0) mbar_arrive(qempty + b);
       ++k;
@@ -641,98 +663,113 @@ __global__ void __launch_bounds__(Cfg<kN, kLive, kPacked, kHalves>::kThreads, 1)
         for (int32_t i = max(0, at - F::kRawStages); i < at; ++i)
           mbar_wait_bounded(rfull + i % F::kRawStages, (i / F::kRawStages) & 1, 1u << 16);
       } else {
-        for (int32_t i = max(0, last_seq - kRing + 1); i <= last_seq; ++i)
-          mbar_wait_bounded(full + i % kRing, (i / kRing) & 1, 1u << 16);
+        for (int32_t i = max(0, k_tiles - kKs); i < k_tiles; ++i)
+          mbar_wait_bounded(kfull + i % kKs, (i / kKs) & 1, 1u << 16);
+        for (int32_t i = max(0, v_tiles - kVs); i < v_tiles; ++i)
+          mbar_wait_bounded(vfull + i % kVs, (i / kVs) & 1, 1u << 16);
       }
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------- MMAs --
+    // -------------------------------------------- first product, S^T = K Q^T --
     // The whole warp runs the loop on values that are the same in every lane
-    // (so that descriptors stay in uniform registers); one lane issues.
-    constexpr uint32_t kIdS = instr_desc<kN>(false), kIdO = instr_desc<kN>(true);
-    constexpr uint32_t kPLayout = kN >= 64 ? 2u : kN == 32 ? 4u : 6u;
-    constexpr uint32_t kHiK = desc_hi(1024, 2), kHiP = desc_hi(8 * F::kPitch, kPLayout);
+    // (so that descriptors stay in uniform registers); one lane issues.  An MMA
+    // takes 64 clocks for 128 keys or channels however few rows there are, and
+    // its warp waits that long to issue the next; the second product has a warp
+    // of its own, so that one's waits pass under the other's MMAs.
+    constexpr uint32_t kHi = desc_hi(1024, 2);
     const uint32_t leader = lane == 0;
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     const int32_t tiles_all = __shfl_sync(0xffffffffu, my_tiles, 0);
     const uint32_t ring_a = __shfl_sync(0xffffffffu, smem_addr(ring), 0);
-    const uint32_t p_a = ring_a + kRing * F::kStage, q_a = p_a + 2 * F::kP;
-    const int k_steps = (a.c.dim + 15) / 16;
+    const uint32_t q_a = ring_a + kRing * F::kStage + F::kPBufs * F::kP;
+    const int k_steps = kPacked ? (a.c.dim + 31) / 32 : (a.c.dim + 15) / 16;
     bool ok = true;
     const auto wait = [&](uint64_t* bar, int32_t use) {
       if (ok) ok = __all_sync(0xffffffffu, wait_or_dead(bar, use & 1, dead));
     };
-    const auto second = [&](int32_t i, int32_t seq, bool first, int32_t item) {  // O^T += V^T P^T of tile i
-      const int b = i & 1;
-      const int32_t s = seq % kRing;
-      wait(pfull + b, i >> 1);
-      wait(full + s, seq / kRing);
-      if (first) wait(oempty + (item & 1), (item >> 1) + 1);
-      if (!ok) return;
-      tc_fence_after();
-      const uint32_t va = desc_lo(ring_a + s * F::kStage, kHalves == 2 ? 16384 : 0);
-      const uint32_t pa = desc_lo(p_a + b * F::kP, kTile * 128);
-      const uint32_t d = tm + 2 * kN + (item & 1) * kN;
-#pragma unroll
-      for (int kk = 0; kk < kTile / 16; ++kk)
-        umma(d, desc(va + kk * (16 * 128 >> 4), kHiK), desc(pa + kk * (16 * F::kPitch >> 4), kHiP), kIdO,
-             (!first || kk > 0) ? 1u : 0u, leader);
-      umma_commit(empty + s, leader);
-      umma_commit(pdone + b, leader);
-    };
     int32_t at = 0;
-    bool prev_first = false;
-    int32_t prev_item = 0, prev_seq = 0;
 #pragma unroll 1
     for (int32_t k = 0; at < tiles_all && ok; ++k) {
       const int qb = k % kNQ;
-      if (kNQ == 1 && at > 0) second(at - 1, prev_seq, prev_first, prev_item);  // else the next item's queries cannot come
       wait(qfull + qb, k / kNQ);
       if (!ok) break;
-      const int32_t tiles = __shfl_sync(0xffffffffu, items[qb].tiles, 0), f = at;
+      const int32_t tiles = __shfl_sync(0xffffffffu, items[qb].tiles, 0);
       const uint32_t qa = desc_lo(q_a + qb * F::kQ, 16);
 #pragma unroll 1
       for (int32_t t = 0; t < tiles; ++t, ++at) {
         const int b = at & 1;
+        const int32_t s = at % kKs;
+        wait(kfull + s, at / kKs);
         wait(sempty + b, (at >> 1) + 1);
+        if (!ok) break;
+        tc_fence_after();
         if constexpr (kPacked) {
-          wait(kfull + b, at >> 1);
-          if (!ok) break;
-          tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < 4 * kHalves; ++kk)
+          for (int kk = 0; kk < 2 * kHalves; ++kk)
             if (kk < k_steps)
-              umma_ts(tm + b * kN, tm + 4 * kN + b * F::kKCols + kk * 8,
-                      desc(qa + (kk >> 2) * (kN * 128 >> 4) + (kk & 3) * 2, kHiK), kIdS, kk > 0 ? 1u : 0u, leader);
-          umma_commit(kempty + b, leader);
+              umma_ts(tm + b * kNS, tm + F::kKCol + s * F::kKCols + kk * 8, desc(qa + kk * 2, kHi), instr_desc_e4m3<kNS>(),
+                      kk > 0 ? 1u : 0u, leader);
         } else {
-          const int32_t seq = k_seq(f, t), s = seq % kRing;
-          wait(full + s, seq / kRing);
-          if (!ok) break;
-          tc_fence_after();
           const uint32_t ka = desc_lo(ring_a + s * F::kStage, 16);
 #pragma unroll
           for (int kk = 0; kk < 4 * kHalves; ++kk)
             if (kk < k_steps)
-              umma(tm + b * kN, desc(ka + (kk >> 2) * (16384 >> 4) + (kk & 3) * 2, kHiK),
-                   desc(qa + (kk >> 2) * (kN * 128 >> 4) + (kk & 3) * 2, kHiK), kIdS, kk > 0 ? 1u : 0u, leader);
-          umma_commit(empty + s, leader);
+              umma(tm + b * kNS, desc(ka + (kk >> 2) * (16384 >> 4) + (kk & 3) * 2, kHi),
+                   desc(qa + (kk >> 2) * (kN * 128 >> 4) + (kk & 3) * 2, kHi), instr_desc<kN>(false), kk > 0 ? 1u : 0u, leader);
         }
+        umma_commit(kempty + s, leader);
         umma_commit(sfull + b, leader);
-        if (at > 0 && !(kNQ == 1 && t == 0)) second(at - 1, prev_seq, prev_first, prev_item);
-        prev_seq = v_seq(f, tiles, t);
-        prev_first = t == 0;
-        prev_item = k;
       }
     }
-    if (ok) second(tiles_all - 1, prev_seq, prev_first, prev_item);
     if (!ok && lane == 0) {  // given up: the MMAs in flight end before tensor memory is freed
-      umma_commit(&drain, 1);
-      mbar_wait_bounded(&drain, 0, 1u << 16);
+      umma_commit(&drain[0], 1);
+      mbar_wait_bounded(&drain[0], 0, 1u << 16);
     }
-  } else if (warp < 4) {
+  } else if (warp == 2) {
+    // ---------------------------------------- second product, O^T += V^T P^T --
+    constexpr uint32_t kHiV = desc_hi(1024, 2), kHiP = desc_hi(8 * F::kPitch, kN >= 64 ? 2u : kN == 32 ? 4u : 6u);
+    const uint32_t leader = lane == 0;
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const int32_t tiles_all = __shfl_sync(0xffffffffu, my_tiles, 0);
+    const uint32_t ring_a = __shfl_sync(0xffffffffu, smem_addr(ring), 0);
+    const uint32_t p_a = ring_a + kRing * F::kStage, v_a = ring_a + (kPacked ? 0 : kKs) * F::kStage;
+    bool ok = true;
+    const auto wait = [&](uint64_t* bar, int32_t use) {
+      if (ok) ok = __all_sync(0xffffffffu, wait_or_dead(bar, use & 1, dead));
+    };
+    int32_t at = 0;
+#pragma unroll 1
+    for (int32_t k = 0; at < tiles_all && ok; ++k) {
+      const int qb = k % kNQ;
+      wait(qfull + qb, k / kNQ);
+      if (!ok) break;
+      const int32_t tiles = __shfl_sync(0xffffffffu, items[qb].tiles, 0);
+      wait(oempty + (k & 1), (k >> 1) + 1);
+      const uint32_t d = tm + F::kOCol + (k & 1) * kN;
+#pragma unroll 1
+      for (int32_t t = 0; t < tiles; ++t, ++at) {
+        const int b = at & 1;
+        const int32_t s = at % kVs;
+        wait(vfull + s, at / kVs);
+        wait(pfull + b, at >> 1);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t va = desc_lo(v_a + s * F::kStage, kHalves == 2 ? 16384 : 0);
+        const uint32_t pa = desc_lo(p_a + b % F::kPBufs * F::kP, kTile * 128);
+#pragma unroll
+        for (int kk = 0; kk < kTile / 16; ++kk)
+          umma(d, desc(va + kk * (16 * 128 >> 4), kHiV), desc(pa + kk * (16 * F::kPitch >> 4), kHiP), instr_desc<kN>(true),
+               (t > 0 || kk > 0) ? 1u : 0u, leader);
+        umma_commit(vempty + s, leader);
+        umma_commit(pdone + b, leader);
+      }
+    }
+    if (!ok && lane == 0) {
+      umma_commit(&drain[1], 1);
+      mbar_wait_bounded(&drain[1], 0, 1u << 16);
+    }
+  } else if (warp == 3) {
     // --------------------------------------------- the items' queries --
-    const int lt = tid - 64;
     int32_t r = s_r0, left = my_tiles;
     Request q = request_of(a, r);
     const int64_t before = static_cast<int64_t>(s_before) * a.c.heads;  // tiles before request r
@@ -766,7 +803,7 @@ __global__ void __launch_bounds__(Cfg<kN, kLive, kPacked, kHalves>::kThreads, 1)
       const int b = k % kNQ;
       if (!__all_sync(0xffffffffu, wait_or_dead(qempty + b, ((k / kNQ) & 1) ^ 1u, dead))) break;
       const int32_t rows = min(kLive, q.n * a.group - row0), take = min(left, s.tiles - skip);
-      if (lt == 0) {
+      if (lane == 0) {
         Item it;
         it.r = r;
         it.head = head;
@@ -789,7 +826,7 @@ __global__ void __launch_bounds__(Cfg<kN, kLive, kPacked, kHalves>::kThreads, 1)
         items[b] = it;
       }
 #pragma unroll 1
-      for (int n = lt; n < kN; n += 64) {
+      for (int n = lane; n < kN; n += 32) {
         const int32_t token = token_of(a, row0 + n), h = head * a.group + (row0 + n - token * a.group);
         const bool live = n < rows;
         int32_t depth = token;
@@ -811,23 +848,25 @@ __global__ void __launch_bounds__(Cfg<kN, kLive, kPacked, kHalves>::kThreads, 1)
         row_out[b][n] = t * a.out_token + h * a.out_head;
         row_lse[b][n] = static_cast<int32_t>(t * a.num_heads + h);
       }
-      if (a.parents && lt < q.n) {
-        int32_t depth = 0;
+      if (a.parents)
 #pragma unroll 1
-        for (int32_t u = lt; u > 0; ++depth) {
-          const int32_t pa = a.parents[q.qbegin + u];
-          u = (pa < 0 || pa >= u) ? 0 : pa;
+        for (int32_t n = lane; n < q.n; n += 32) {
+          int32_t depth = 0;
+#pragma unroll 1
+          for (int32_t u = n; u > 0; ++depth) {
+            const int32_t pa = a.parents[q.qbegin + u];
+            u = (pa < 0 || pa >= u) ? 0 : pa;
+          }
+          node_depth[b][n] = static_cast<uint8_t>(depth);
         }
-        node_depth[b][lt] = static_cast<uint8_t>(depth);
-      }
-      // 16 lanes per row, 8 channels each; eight rows in flight
-      const int ch = lt & 15;
+      // 16 lanes per row, 8 channels each; 16 rows in flight
+      const int ch = lane & 15;
 #pragma unroll 1
-      for (int n0 = lt >> 4; n0 < kN; n0 += 32) {
+      for (int n0 = lane >> 4; n0 < kN; n0 += 16) {
         uint4 x[8];
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-          const int n = n0 + 4 * u, token = token_of(a, row0 + n);
+          const int n = n0 + 2 * u, token = token_of(a, row0 + n);
           x[u] = make_uint4(0u, 0u, 0u, 0u);
           if (n < rows && ch * 8 < a.c.dim)
             x[u] = *reinterpret_cast<const uint4*>(
@@ -836,16 +875,57 @@ __global__ void __launch_bounds__(Cfg<kN, kLive, kPacked, kHalves>::kThreads, 1)
         }
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-          const int n = n0 + 4 * u;
-          if (n >= kN) break;
-          if (ch < 8 * kHalves)
-            *reinterpret_cast<uint4*>(qbuf + b * F::kQ + (ch >> 3) * (kN * 128) + n * 128 + (((ch & 7) ^ (n & 7)) << 4)) = x[u];
-          if (kPacked) {
-            float sum = ((bf16_lo(x[u].x) + bf16_hi(x[u].x)) + (bf16_lo(x[u].y) + bf16_hi(x[u].y))) +
-                        ((bf16_lo(x[u].z) + bf16_hi(x[u].z)) + (bf16_lo(x[u].w) + bf16_hi(x[u].w)));
+          const int n = n0 + 2 * u;
+          if constexpr (!kPacked) {
+            if (ch < 8 * kHalves)
+              *reinterpret_cast<uint4*>(qbuf + b * F::kQ + (ch >> 3) * (kN * 128) + n * 128 + (((ch & 7) ^ (n & 7)) << 4)) = x[u];
+          } else {
+            // q as unit (hi + lo / 32), both e4m3, unit a power of two by the
+            // row's largest channel: q's 8 bits are 4 + 4, so this is exact but
+            // for channels below 2^-15 of the largest
+            const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+            float v[8], sum = 0.0f, top = 0.0f;
 #pragma unroll
-            for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o, 16);
-            if (ch == 0) row_qsum[b][n] = sum;
+            for (int i = 0; i < 4; ++i) {
+              v[2 * i] = bf16_lo(w[i]);
+              v[2 * i + 1] = bf16_hi(w[i]);
+              sum += v[2 * i] + v[2 * i + 1];
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const bool finite = fabsf(v[i]) <= 3.4e38f;
+              if (finite) top = fmaxf(top, fabsf(v[i]));
+              else v[i] = __int_as_float(0x7fffffff);
+            }
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) {
+              sum += __shfl_xor_sync(0xffffffffu, sum, o, 16);
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o, 16));
+            }
+            // top * scale is in [128, 256)
+            const int e = max((__float_as_int(top) >> 23) & 0xff, 16);
+            const float scale = __int_as_float((261 - e) << 23);
+            uint32_t hi[2] = {0u, 0u}, lo[2] = {0u, 0u};
+            // the unpacked keys' order of eight channels: 0 4 1 5, 2 6 3 7
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int c = (i & 1) + (i >> 1) * 2;  // pairs (0, 4), (1, 5), (2, 6), (3, 7)
+              const float p0 = v[c] * scale, p1 = v[c + 4] * scale;
+              const uint32_t h = e4m3_pair(p0, p1);
+              const float2 back = e4m3_floats(h);
+              const uint32_t r = e4m3_pair((p0 - back.x) * 32.0f, (p1 - back.y) * 32.0f);
+              hi[i >> 1] |= h << (16 * (i & 1));
+              lo[i >> 1] |= r << (16 * (i & 1));
+            }
+            uint8_t* at = qbuf + b * F::kQ + (((ch >> 1) ^ (n & 7)) << 4) + (ch & 1) * 8;  // kLive is a multiple of 8
+            if (n < kLive) {
+              *reinterpret_cast<uint2*>(at + n * 128) = make_uint2(hi[0], hi[1]);
+              *reinterpret_cast<uint2*>(at + (kLive + n) * 128) = make_uint2(lo[0], lo[1]);
+            }
+            if (ch == 0) {
+              row_qsum[b][n] = sum;
+              row_unit[b][n] = __int_as_float((e - 7) << 23);
+            }
           }
         }
       }
@@ -868,7 +948,7 @@ __global__ void __launch_bounds__(Cfg<kN, kLive, kPacked, kHalves>::kThreads, 1)
       }
       s = span_of(a, q, row0);
     }
-  } else if (!kPacked || tid < 128 + F::kSoft) {
+  } else if (!kPacked || warp < 4 + F::kSoft / 32) {
     // ---------------------------------------------------------- softmax --
     const int st = tid - 128, wg = st >> 7, lt = st & 127, wq = warp & 3;
     const int c0 = wg * kCols;                                    // this warpgroup's rows
@@ -893,8 +973,7 @@ __global__ void __launch_bounds__(Cfg<kN, kLive, kPacked, kHalves>::kThreads, 1)
       if (lt < kCols) nref[c0 + lt] = 0.0f;
       bool unset = true;  // thread i of the warpgroup: row i has seen no key yet
       bool fresh = true;  // some row has not
-      const uint32_t o_base = tmem + 2 * kN + (k & 1) * kN + c0 + lanes;
-      const int32_t f = at;
+      const uint32_t o_base = tmem + F::kOCol + (k & 1) * kN + c0 + lanes;
       const int32_t first_pos = it.base + (tree ? 0 : token_of(a, it.row0));
       const int32_t last_pos = it.base + token_of(a, it.row0 + it.rows - 1);  // of a tree: at most
 #pragma unroll 1
@@ -910,11 +989,10 @@ __global__ void __launch_bounds__(Cfg<kN, kLive, kPacked, kHalves>::kThreads, 1)
         const bool masked = sink || there != every || j0 + kTile - 1 > (tree ? it.base - 1 : first_pos) ||
                             (a.window > 0 && j0 <= last_pos - a.window);
         float ka = a.scale_log2, kb = 0.0f, sv = 0.0f, wv = 0.0f;
-        if (kPacked) {  // the tensor cores multiplied 16 + n
+        if (kPacked) {  // the tensor cores multiplied n / 512
           const uint32_t kp = k_pair[at % kPairs][lt];
-          const float s = bf16_lo(kp);
-          ka = a.scale_log2 * s;
-          kb = a.scale_log2 * __fmaf_rn(-16.0f, s, bf16_hi(kp));
+          ka = a.scale_log2 * 512.0f * bf16_lo(kp);
+          kb = a.scale_log2 * bf16_hi(kp);
         }
         uint32_t vis = 0xffffffffu;  // the rows that see this thread's key
         bool poison = false;
@@ -947,10 +1025,11 @@ __global__ void __launch_bounds__(Cfg<kN, kLive, kPacked, kHalves>::kThreads, 1)
             // A value that is not finite must not meet a weight of 0: the row
             // of such a key, where not every query sees it, becomes 0, and the
             // queries that do see it get a weight of NaN.
-            const int32_t seq = v_seq(f, it.tiles, t), s = seq % kRing;
-            wait_or_dead(full + s, (seq / kRing) & 1, dead);
+            const int32_t s = at % kVs;
+            if (at >= 2) wait_or_dead(pdone + sb, ((at - 2) >> 1) & 1, dead);  // V's slot has moved on to this tile
+            wait_or_dead(vfull + s, (at / kVs) & 1, dead);
             const bool all = here && !draft && j <= first_pos && (always || j > last_pos - a.window);
-            uint4* v = reinterpret_cast<uint4*>(ring + s * F::kStage + lt * 128);
+            uint4* v = reinterpret_cast<uint4*>(vring + s * F::kStage + lt * 128);
             if (!all) {
               uint32_t acc = 0;  // 0 times each channel, added up: NaN as soon as one is not finite
 #pragma unroll 4
@@ -980,7 +1059,17 @@ __global__ void __launch_bounds__(Cfg<kN, kLive, kPacked, kHalves>::kThreads, 1)
         }
         // x_nj - r_n of this key, every row
         float x[kCols];
-        tmem_ld(tmem + sb * kN + c0 + lanes, x);
+        tmem_ld(tmem + sb * kNS + c0 + lanes, x);
+        if constexpr (kPacked) {
+          constexpr int kPart = kCols < 16 ? kCols : 16;
+#pragma unroll
+          for (int i0 = 0; i0 < kCols; i0 += kPart) {
+            float low[kPart];
+            tmem_ld(tmem + sb * kNS + kLive + c0 + i0 + lanes, low);
+#pragma unroll
+            for (int i = 0; i < kPart; ++i) x[i0 + i] = __fmaf_rn(low[i], 0.03125f, x[i0 + i]);
+          }
+        }
         tc_fence_before();
         mbar_arrive(sempty + sb);
 #pragma unroll
@@ -989,10 +1078,15 @@ __global__ void __launch_bounds__(Cfg<kN, kLive, kPacked, kHalves>::kThreads, 1)
           float y[4] = {r4.x, r4.y, r4.z, r4.w};
           if (kPacked) {
             const float4 q4 = *reinterpret_cast<const float4*>(&row_qsum[b][c0 + i]);
+            const float4 u4 = *reinterpret_cast<const float4*>(&row_unit[b][c0 + i]);
             y[0] = __fmaf_rn(kb, q4.x, y[0]);
             y[1] = __fmaf_rn(kb, q4.y, y[1]);
             y[2] = __fmaf_rn(kb, q4.z, y[2]);
             y[3] = __fmaf_rn(kb, q4.w, y[3]);
+            x[i] *= u4.x;
+            x[i + 1] *= u4.y;
+            x[i + 2] *= u4.z;
+            x[i + 3] *= u4.w;
           }
 #pragma unroll
           for (int e = 0; e < 4; ++e) x[i + e] = __fmaf_rn(x[i + e], ka, y[e]);
@@ -1041,16 +1135,20 @@ __global__ void __launch_bounds__(Cfg<kN, kLive, kPacked, kHalves>::kThreads, 1)
           if (change && t > 0) {
             wait_or_dead(pdone + ((at - 1) & 1), ((at - 1) >> 1) & 1, dead);
             tc_fence_after();
-            float o[kCols];
-            tmem_ld(o_base, o);
+#pragma unroll 1
+            for (int i0 = 0; i0 < kCols; i0 += 8) {
+              float o[8];
+              tmem_ld(o_base + i0, o);
 #pragma unroll
-            for (int i = 0; i < kCols; ++i) o[i] *= corr[c0 + i];
-            tmem_st(o_base, o);
+              for (int i = 0; i < 8; ++i) o[i] *= corr[c0 + i0 + i];
+              tmem_st(o_base + i0, o);
+            }
           }
         }
+        // P's buffer is free, and V's slot has moved on to this tile
+        if (at >= F::kPBufs) wait_or_dead(pdone + ((at - F::kPBufs) & 1), ((at - F::kPBufs) >> 1) & 1, dead);
         if (kPacked) {
-          const int32_t seq = v_seq(f, it.tiles, t), s = seq % kRing;
-          wait_or_dead(full + s, (seq / kRing) & 1, dead);  // V is unpacked, so its pairs are there
+          wait_or_dead(vfull + at % kVs, (at / kVs) & 1, dead);  // V is unpacked, so its pairs are there
           const uint32_t vp = v_pair[at % kPairs][lt];
           sv = bf16_lo(vp);
           wv = __fmaf_rn(8.0f, sv, bf16_hi(vp));
@@ -1060,9 +1158,8 @@ __global__ void __launch_bounds__(Cfg<kN, kLive, kPacked, kHalves>::kThreads, 1)
         if (poison)
 #pragma unroll
           for (int i = 0; i < kCols; ++i) x[i] = ((vis >> i) & 1u) ? __int_as_float(0x7fffffff) : -INFINITY;
-        if (at >= 2) wait_or_dead(pdone + sb, ((at - 2) >> 1) & 1, dead);  // P's buffer is free
         // powers, sums, and P^T [key][row], swizzled as the MMA reads it
-        uint8_t* pb = pbuf + sb * F::kP + (c0 >> 6) * (kTile * 128);
+        uint8_t* pb = pbuf + sb % F::kPBufs * F::kP + (c0 >> 6) * (kTile * 128);
 #pragma unroll
         for (int i8 = 0; i8 < kCols / 8; ++i8) {
           uint32_t o4[4];
@@ -1212,12 +1309,11 @@ __global__ void __launch_bounds__(Cfg<kN, kLive, kPacked, kHalves>::kThreads, 1)
   } else if constexpr (kPacked) {
     // --------------------------------------------------------- unpacking --
     // A thread per key; one warpgroup the K tiles, the other the V tiles.
-    // K becomes 16 + n: the four bits at the top of the mantissa of 16.0 need
-    // no arithmetic; it goes to tensor memory (a key's lane is the thread's),
-    // which spares shared memory a write and the MMAs a read of the tile.
-    // V becomes n - 8, which keeps the rounding of its weights (p s_v in bf16)
-    // from being multiplied by the offset; as an M-major operand it has to be
-    // in shared memory.
+    // A byte n = 0..15 is the e4m3 number n / 512 (0..7 its subnormals, 8..15
+    // the first binade), so K only takes its bits apart; it goes to tensor
+    // memory (a key's lane is the thread's), which spares shared memory a write
+    // and the MMAs a read of the tile.  V becomes n - 8 in bf16: its weights
+    // need bf16's range, and as an M-major operand it is in shared memory.
     const int key = (tid - 128 - F::kSoft) & 127;
     const bool is_v = tid - 128 - F::kSoft >= 128;
 #pragma unroll 1
@@ -1234,10 +1330,10 @@ __global__ void __launch_bounds__(Cfg<kN, kLive, kPacked, kHalves>::kThreads, 1)
         w4[c] = *reinterpret_cast<const uint4*>(src + (off ^ ((off >> 3) & (kHalves == 2 ? 0x30u : 0x10u))));
       }
       if (is_v) {
-        const int32_t s = at % kRing;
-        if (!wait_or_dead(empty + s, ((at / kRing) & 1) ^ 1u, dead)) break;
+        const int32_t s = at % kVs;
+        if (!wait_or_dead(vempty + s, ((at / kVs) & 1) ^ 1u, dead)) break;
         v_pair[at % kPairs][key] = pair;
-        uint8_t* dst = ring + s * F::kStage + key * 128;
+        uint8_t* dst = vring + s * F::kStage + key * 128;
 #pragma unroll
         for (int c = 0; c < 2 * kHalves; ++c) {
           const uint32_t w[4] = {w4[c].x, w4[c].y, w4[c].z, w4[c].w};
@@ -1256,22 +1352,21 @@ __global__ void __launch_bounds__(Cfg<kN, kLive, kPacked, kHalves>::kThreads, 1)
           }
         }
         proxy_fence();
-        mbar_arrive(full + s);
+        mbar_arrive(vfull + s);
       } else {
         if (!__all_sync(0xffffffffu, wait_or_dead(kempty + (at & 1), ((at >> 1) & 1) ^ 1u, dead))) break;
         tc_fence_after();
         k_pair[at % kPairs][key] = pair;
-        const uint32_t dst = tmem + 4 * kN + (at & 1) * F::kKCols + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        const uint32_t dst = tmem + F::kKCol + (at & 1) * F::kKCols + (static_cast<uint32_t>((warp & 3) * 32) << 16);
 #pragma unroll
-        for (int c = 0; c < 2 * kHalves; ++c) {
-          const uint32_t w[4] = {w4[c].x, w4[c].y, w4[c].z, w4[c].w};
+        for (int c = 0; c < kHalves; ++c) {
+          const uint32_t w[8] = {w4[2 * c].x,     w4[2 * c].y,     w4[2 * c].z,     w4[2 * c].w,
+                                 w4[2 * c + 1].x, w4[2 * c + 1].y, w4[2 * c + 1].z, w4[2 * c + 1].w};
           float o[16];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            o[4 * e] = __uint_as_float(((w[e] << 3) & 0x00780078u) | 0x41804180u);
-            o[4 * e + 1] = __uint_as_float(((w[e] >> 1) & 0x00780078u) | 0x41804180u);
-            o[4 * e + 2] = __uint_as_float(((w[e] >> 5) & 0x00780078u) | 0x41804180u);
-            o[4 * e + 3] = __uint_as_float(((w[e] >> 9) & 0x00780078u) | 0x41804180u);
+          for (int e = 0; e < 8; ++e) {
+            o[2 * e] = __uint_as_float(w[e] & 0x0f0f0f0fu);
+            o[2 * e + 1] = __uint_as_float((w[e] >> 4) & 0x0f0f0f0fu);
           }
           tmem_put(dst + c * 16, o);
         }
@@ -1293,10 +1388,10 @@ __global__ void __launch_bounds__(Cfg<kN, kLive, kPacked, kHalves>::kThreads, 1)
   }
 }
 
-template <int kN, int kLive, bool kPacked, int kHalves>
+template <int kLive, bool kPacked, int kHalves>
 ss_status launch(const AttnArgs& a, cudaStream_t s) {
-  using F = Cfg<kN, kLive, kPacked, kHalves>;
-  const void* fn = reinterpret_cast<const void*>(&attn_kernel<kN, kLive, kPacked, kHalves>);
+  using F = Cfg<kLive, kPacked, kHalves>;
+  const void* fn = reinterpret_cast<const void*>(&attn_kernel<kLive, kPacked, kHalves>);
   CUtensorMap mk, mv;
   const int unit = 1 << (a.c.page_shift < 7 ? a.c.page_shift : 7);
   if (!make_cache_map(&mk, a.c.k, a.c, unit) || !make_cache_map(&mv, a.c.v, a.c, unit)) return SS_ERR_UNSUPPORTED;
@@ -1306,7 +1401,7 @@ ss_status launch(const AttnArgs& a, cudaStream_t s) {
   if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, F::kSmem);
   if (e == cudaSuccess) {
     const int grid = sms < kMaxCtas ? sms : kMaxCtas;
-    attn_kernel<kN, kLive, kPacked, kHalves><<<grid, F::kThreads, F::kSmem, s>>>(mk, mv, a);
+    attn_kernel<kLive, kPacked, kHalves><<<grid, F::kThreads, F::kSmem, s>>>(mk, mv, a);
   }
   return finish(e);
 }

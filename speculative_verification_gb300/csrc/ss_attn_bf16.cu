@@ -6,11 +6,11 @@ namespace ssa {
 template <int kHalves>
 static ss_status pick(const AttnArgs& a, cudaStream_t s) {
   switch (a.block_rows) {
-    case 8: return launch<16, 8, false, kHalves>(a, s);
-    case 16: return launch<16, 16, false, kHalves>(a, s);
-    case 32: return launch<32, 32, false, kHalves>(a, s);
-    case 64: return launch<64, 64, false, kHalves>(a, s);
-    default: return launch<128, 128, false, kHalves>(a, s);
+    case 8: return launch<8, false, kHalves>(a, s);
+    case 16: return launch<16, false, kHalves>(a, s);
+    case 32: return launch<32, false, kHalves>(a, s);
+    case 64: return launch<64, false, kHalves>(a, s);
+    default: return launch<128, false, kHalves>(a, s);
   }
 }
 

@@ -6,10 +6,10 @@ namespace ssa {
 template <int kHalves>
 static ss_status pick(const AttnArgs& a, cudaStream_t s) {
   switch (a.block_rows) {
-    case 8: return launch<16, 8, true, kHalves>(a, s);
-    case 16: return launch<16, 16, true, kHalves>(a, s);
-    case 32: return launch<32, 32, true, kHalves>(a, s);
-    default: return launch<64, 64, true, kHalves>(a, s);
+    case 8: return launch<8, true, kHalves>(a, s);
+    case 16: return launch<16, true, kHalves>(a, s);
+    case 32: return launch<32, true, kHalves>(a, s);
+    default: return launch<64, true, kHalves>(a, s);
   }
 }
 
