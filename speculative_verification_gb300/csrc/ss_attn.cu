@@ -46,6 +46,23 @@ bool make_cache_map(CUtensorMap* m, void* base, const CacheView& c, int box_slot
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_query_map(CUtensorMap* m, const AttnArgs& a, int rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const bool boxes = rows % a.group == 0;
+  // the stride of a dimension of one entry is never used
+  const int64_t head = a.num_heads > 1 ? a.q_head : 256, token = a.total_queries > 1 ? a.q_token : 256;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(a.c.dim), static_cast<cuuint64_t>(a.num_heads),
+                              static_cast<cuuint64_t>(a.total_queries)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(head), static_cast<cuuint64_t>(token)};
+  const cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(boxes ? a.group : 1),
+                             static_cast<cuuint32_t>(boxes ? rows / a.group : 1)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint8_t*>(a.q), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace ssa
 
 extern "C" {

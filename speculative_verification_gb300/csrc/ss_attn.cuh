@@ -7,10 +7,10 @@
 //   lse_n = ln 2 (r_n + log2 sum_j p_nj).
 // Any r_n gives the same result; it only has to keep the powers in range.  The
 // running maximum is the usual choice; here r_n moves only when some x_nj
-// passes it by more than 8, so the accumulated sums are rescaled a few times
-// per row instead of at every tile and a tile needs no maximum over its keys
-// at all (p <= 2^8 stays exact enough in fp32 and bf16 alike, as both are
-// relative).
+// passes it by more than 32, so the accumulated sums are rescaled once or
+// twice per row instead of at every tile and a tile needs no maximum over its
+// keys at all.  p up to 2^32 and what lies 2^-126 below rounds no worse: bf16
+// and fp32 are relative and have the same range.
 //
 // The transposed product.  A tile is 128 keys of one kv head; the rows are the
 // new tokens of one request times the query heads that share the kv head,
@@ -62,6 +62,7 @@ constexpr uint32_t kSleepNs = 50000;
 constexpr int kInfo = 16;                 // tiles whose page masks are kept
 constexpr int kPairs = 8;                 // tiles whose (s, m) pairs are kept
 constexpr float kUnset = 3.0e38f;         // in a piece: minus the reference of a row that has seen nothing
+constexpr float kSlack = 32.0f;           // how far a score (log2) may pass its row's reference
 constexpr int kSlotFloats = 128 * 130;    // one piece: up to 128 rows of 128 channels, r and l
 
 struct AttnArgs {
@@ -91,6 +92,11 @@ ss_status launch_int4(const AttnArgs& a, cudaStream_t s);
 // Rank-4 tensor map (channel bytes, slot, head, page) of K or V.
 bool make_cache_map(CUtensorMap* m, void* base, const CacheView& c, int box_slots);
 
+// Rank-3 tensor map (channels, head, token) of the queries: boxes of a block's
+// tokens times a group's heads where blocks of `rows` rows start at tokens,
+// else of one row.
+bool make_query_map(CUtensorMap* m, const AttnArgs& a, int rows);
+
 #ifdef __CUDACC__
 
 // One work item of a CTA: consecutive tiles of one (request, kv head, block).
@@ -119,7 +125,8 @@ struct Cfg {
   static constexpr int kThreads = 128 + kSoft + kUnpack;
   static constexpr int kStage = kHalves * 16384;             // 128 keys x 64 channels x 2 bytes per half
   static constexpr int kQ = kPacked ? kNS * 128 : kHalves * kN * 128;
-  static constexpr int kNQ = kLive >= 128 ? 1 : 2;
+  static constexpr int kNQ = 2;                              // items prepared ahead
+  static constexpr int kQBufs = kLive >= 128 ? 1 : 2;        // of which with their queries
   static constexpr int kPitch = kN >= 64 ? 128 : kN * 2;     // bytes per key of a P block
   static constexpr int kP = kTile * kN * 2;
   static constexpr int kPBufs = kLive >= 128 ? 1 : 2;
@@ -127,16 +134,16 @@ struct Cfg {
   static constexpr int kRaw = kPacked ? 2 * kTile * kRawRow + 2 * kTile * 4 : 0;
   static constexpr int kRawStages = kPacked ? 4 : 1;
   // the static arrays, rounded up
-  static constexpr int kMeta = kNQ * (static_cast<int>(sizeof(Item)) + kN * 32 + 64) + kN * 36 + 1536 +
+  static constexpr int kMeta = kNQ * (static_cast<int>(sizeof(Item)) + kN * 32 + 64 + 512) + kN * 36 + 1536 +
                                (kGroups > 1 ? kGroups * 256 : 0) + (kPacked ? 2 * kPairs * kTile * 4 : 0);
-  static constexpr int kBudget = 232448 - 1024 - kNQ * kQ - kPBufs * kP - kRawStages * kRaw - kMeta;
+  static constexpr int kBudget = 232448 - 1024 - kQBufs * kQ - kPBufs * kP - kRawStages * kRaw - kMeta;
   // K and V have a ring each, so that whoever waits for a slot has used the
   // slot's previous contents itself: a parity wait tells two phases apart, no
   // more.  4 bits: only V's is in shared memory, K's two slots are columns.
   static constexpr int kMost = kPacked ? 4 : 8;
   static constexpr int kRing = kBudget / kStage < kMost ? kBudget / kStage : kMost;
   static constexpr int kKs = kPacked ? 2 : kRing / 2, kVs = kPacked ? kRing : kRing - kKs;
-  static constexpr int kSmem = 1024 + kRing * kStage + kNQ * kQ + kPBufs * kP + kRawStages * kRaw;
+  static constexpr int kSmem = 1024 + kRing * kStage + kQBufs * kQ + kPBufs * kP + kRawStages * kRaw;
   // tensor-memory columns: S x 2, O x 2, and for 4 bits K x 2 (four channels per column)
   static constexpr uint32_t kOCol = 2 * kNS, kKCol = kOCol + 2 * kN;
   static constexpr uint32_t kKCols = kPacked ? 16 * kHalves : 0;
@@ -144,6 +151,10 @@ struct Cfg {
   static constexpr uint32_t kTmem = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
   static_assert(kKs >= 1 && kVs >= 2, "a tile in use and one on its way");
 };
+
+__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(bytes) : "memory");
+}
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
@@ -169,6 +180,22 @@ __device__ __forceinline__ bool wait_or_dead(uint64_t* bar, uint32_t parity, vol
   }
   *dead = 1;
   return false;
+}
+
+// Two barriers at once: the polls' latencies overlap.
+__device__ __forceinline__ void wait_both(uint64_t* bar0, uint32_t parity0, uint64_t* bar1, uint32_t parity1,
+                                          volatile int32_t* dead) {
+  const bool d0 = mbar_try_wait(bar0, parity0), d1 = mbar_try_wait(bar1, parity1);
+  if (!d0) wait_or_dead(bar0, parity0, dead);
+  if (!d1) wait_or_dead(bar1, parity1, dead);
+}
+
+__device__ __forceinline__ void tma_3d(void* dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+      : "memory");
 }
 
 __device__ __forceinline__ void tma_4d(void* dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z, int32_t w,
@@ -244,7 +271,8 @@ __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::
 __device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // Consecutive fp32 columns of this warp's 32 tensor-memory lanes.
-__device__ __forceinline__ void tmem_ld(uint32_t t, float (&v)[16]) {
+// tmem_get starts the load; tmem_wait ends it.
+__device__ __forceinline__ void tmem_get(uint32_t t, float (&v)[16]) {
   __syncwarp();  // the loads and stores of tensor memory are the whole warp's
   uint32_t* r = reinterpret_cast<uint32_t*>(v);
   asm volatile(
@@ -254,16 +282,14 @@ __device__ __forceinline__ void tmem_ld(uint32_t t, float (&v)[16]) {
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(t)
       : "memory");
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void tmem_ld(uint32_t t, float (&v)[8]) {
+__device__ __forceinline__ void tmem_get(uint32_t t, float (&v)[8]) {
   __syncwarp();
   uint32_t* r = reinterpret_cast<uint32_t*>(v);
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                : "r"(t)
                : "memory");
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void tmem_st(uint32_t t, const float (&v)[8]) {
   __syncwarp();
@@ -273,7 +299,7 @@ __device__ __forceinline__ void tmem_st(uint32_t t, const float (&v)[8]) {
                : "memory");
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void tmem_ld(uint32_t t, float (&v)[32]) {
+__device__ __forceinline__ void tmem_get(uint32_t t, float (&v)[32]) {
   __syncwarp();
   uint32_t* r = reinterpret_cast<uint32_t*>(v);
   asm volatile(
@@ -285,7 +311,6 @@ __device__ __forceinline__ void tmem_ld(uint32_t t, float (&v)[32]) {
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(t)
       : "memory");
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void tmem_put_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_put(uint32_t t, const float (&v)[16]) {
@@ -314,6 +339,18 @@ __device__ __forceinline__ void tmem_st(uint32_t t, const float (&v)[32]) {
       "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(t)
       : "memory");
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+template <int kCount>
+__device__ __forceinline__ void tmem_wait(float (&v)[kCount]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < kCount; ++i) asm volatile("" : "+f"(v[i]));  // no use of v moves above the wait
+}
+template <int kCount>
+__device__ __forceinline__ void tmem_ld(uint32_t t, float (&v)[kCount]) {
+  tmem_get(t, v);
+  tmem_wait(v);
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -443,12 +480,13 @@ __device__ __forceinline__ int32_t request_tiles(const AttnArgs& a, const Reques
 
 template <int kLive, bool kPacked, int kHalves>
 __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
-    attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const AttnArgs a) {
+    attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                const __grid_constant__ CUtensorMap tm_q, const AttnArgs a) {
   using F = Cfg<kLive, kPacked, kHalves>;
   constexpr int kRing = F::kRing, kKs = F::kKs, kVs = F::kVs, kNQ = F::kNQ, kCols = F::kCols, kN = F::kN, kNS = F::kNS;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t kfull[kKs], kempty[kKs], vfull[kVs], vempty[kVs], sfull[2], sempty[2], pfull[2], pdone[2], oempty[2],
-      qfull[kNQ], qempty[kNQ], rfull[F::kRawStages], rempty[F::kRawStages], looked, drain[2];
+      qfull[kNQ], qempty[kNQ], qfree[F::kQBufs], rfull[F::kRawStages], rempty[F::kRawStages], looked, drain[2];
   __shared__ Item items[kNQ];
   __shared__ __align__(16) int32_t row_pos[kNQ][kN];
   __shared__ __align__(16) uint64_t row_path[kNQ][kN];
@@ -456,6 +494,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
   __shared__ int32_t row_lse[kNQ][kN];
   __shared__ __align__(16) float row_qsum[kPacked ? kNQ : 1][kPacked ? kN : 4], row_unit[kPacked ? kNQ : 1][kPacked ? kN : 4];
   __shared__ uint8_t node_depth[kNQ][SS_TREE_MAX_NODES];
+  __shared__ uint64_t node_sees[kNQ][SS_TREE_MAX_NODES];
   __shared__ uint32_t info[kInfo];
   __shared__ uint32_t k_pair[kPacked ? kPairs : 1][kPacked ? kTile : 1], v_pair[kPacked ? kPairs : 1][kPacked ? kTile : 1];
   __shared__ uint8_t key_bad[2][F::kGroups > 1 ? F::kGroups : 1][F::kGroups > 1 ? kTile : 1];
@@ -468,7 +507,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
   uint8_t* pbuf = ring + kRing * F::kStage;
   uint8_t* qbuf = pbuf + F::kPBufs * F::kP;
   uint8_t* vring = ring + (kPacked ? 0 : kKs) * F::kStage;  // after K's slots
-  uint8_t* raw = qbuf + kNQ * F::kQ;
+  uint8_t* raw = qbuf + F::kQBufs * F::kQ;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int32_t* dead = &s_dead;
 
@@ -492,6 +531,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
       mbar_init(qfull + i, 32);
       mbar_init(qempty + i, 1 + F::kSoft / 32);
     }
+    for (int i = 0; i < F::kQBufs; ++i) mbar_init(qfree + i, 1);
     if (kPacked)
       for (int i = 0; i < F::kRawStages; ++i) {
         mbar_init(rfull + i, 1);
@@ -694,7 +734,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
       wait(qfull + qb, k / kNQ);
       if (!ok) break;
       const int32_t tiles = __shfl_sync(0xffffffffu, items[qb].tiles, 0);
-      const uint32_t qa = desc_lo(q_a + qb * F::kQ, 16);
+      const uint32_t qa = desc_lo(q_a + k % F::kQBufs * F::kQ, 16);
 #pragma unroll 1
       for (int32_t t = 0; t < tiles; ++t, ++at) {
         const int b = at & 1;
@@ -720,6 +760,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
         umma_commit(kempty + s, leader);
         umma_commit(sfull + b, leader);
       }
+      umma_commit(qfree + k % F::kQBufs, leader);  // the queries are read
     }
     if (!ok && lane == 0) {  // given up: the MMAs in flight end before tensor memory is freed
       umma_commit(&drain[0], 1);
@@ -799,6 +840,9 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
       }
     }
     Span s = span_of(a, q, row0);
+    int32_t tree_of = -1, node_deep[2];
+    uint64_t node_path[2];
+#pragma unroll 1
     for (int32_t k = 0; left > 0; ++k) {
       const int b = k % kNQ;
       if (!__all_sync(0xffffffffu, wait_or_dead(qempty + b, ((k / kNQ) & 1) ^ 1u, dead))) break;
@@ -825,40 +869,76 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
         it.row = q.row;
         items[b] = it;
       }
+      if (a.parents) {
+        // the request's tree: lane i walks up from nodes i and i + 32, all at once
+        if (tree_of != r) {
+          tree_of = r;
+          int32_t up[2], pa[2];
+          const auto parent_of = [&](int32_t n) {
+            const int32_t p = (n > 0 && n < q.n) ? a.parents[q.qbegin + n] : 0;
+            return (p < 0 || p >= n) ? 0 : p;
+          };
+          pa[0] = parent_of(lane);
+          pa[1] = parent_of(lane + 32);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            up[h] = lane + 32 * h;
+            node_path[h] = 1ull << up[h];
+            node_deep[h] = 0;
+          }
+#pragma unroll 1
+          while (__any_sync(0xffffffffu, up[0] > 0 || up[1] > 0)) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int32_t p0 = __shfl_sync(0xffffffffu, pa[0], up[h] & 31), p1 = __shfl_sync(0xffffffffu, pa[1], up[h] & 31);
+              if (up[h] > 0) {
+                up[h] = up[h] < 32 ? p0 : p1;
+                node_path[h] |= 1ull << up[h];
+                ++node_deep[h];
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          node_depth[b][lane + 32 * h] = static_cast<uint8_t>(node_deep[h]);
+          node_sees[b][lane + 32 * h] = node_path[h];
+        }
+        __syncwarp();
+      }
 #pragma unroll 1
       for (int n = lane; n < kN; n += 32) {
         const int32_t token = token_of(a, row0 + n), h = head * a.group + (row0 + n - token * a.group);
         const bool live = n < rows;
-        int32_t depth = token;
-        uint64_t path = ~0ull;
-        if (a.parents && live) {
-          depth = 0;
-          path = 1ull << token;
-#pragma unroll 1
-          for (int32_t u = token; u > 0; ++depth) {
-            const int32_t pa = a.parents[q.qbegin + u];
-            u = (pa < 0 || pa >= u) ? 0 : pa;
-            path |= 1ull << u;
-          }
-        }
         // rows without a query: a position past every key, their result is not used
-        row_pos[b][n] = live ? q.base + depth : 0x7ffffffe;
-        row_path[b][n] = path;
+        row_pos[b][n] = live ? q.base + (a.parents ? node_depth[b][token] : token) : 0x7ffffffe;
+        if (a.parents) row_path[b][n] = live ? node_sees[b][token] : ~0ull;
         const int64_t t = static_cast<int64_t>(q.qbegin) + token;
         row_out[b][n] = t * a.out_token + h * a.out_head;
         row_lse[b][n] = static_cast<int32_t>(t * a.num_heads + h);
       }
-      if (a.parents)
+      const int qb = k % F::kQBufs;
+      if (!__all_sync(0xffffffffu, wait_or_dead(qfree + qb, ((k / F::kQBufs) & 1) ^ 1u, dead))) break;
+      if constexpr (!kPacked) {
+        // by tensor copies: the block's tokens times the group's heads in one
+        // box where blocks start at tokens, else row by row
+        uint8_t* dst = qbuf + qb * F::kQ;
+        const bool boxes = kLive % a.group == 0;
+        if (lane == 0) mbar_expect_tx(qfull + b, static_cast<uint32_t>((boxes ? kLive : rows) * 128 * kHalves));
+        __syncwarp();
+        if (boxes) {
+          if (lane < kHalves)
+            tma_3d(dst + lane * (kN * 128), &tm_q, lane * 64, head * a.group, q.qbegin + token_of(a, row0), qfull + b);
+        } else {
 #pragma unroll 1
-        for (int32_t n = lane; n < q.n; n += 32) {
-          int32_t depth = 0;
-#pragma unroll 1
-          for (int32_t u = n; u > 0; ++depth) {
-            const int32_t pa = a.parents[q.qbegin + u];
-            u = (pa < 0 || pa >= u) ? 0 : pa;
+          for (int n = lane; n < rows; n += 32) {
+            const int32_t token = token_of(a, row0 + n), h = head * a.group + (row0 + n - token * a.group);
+#pragma unroll
+            for (int x = 0; x < kHalves; ++x)
+              tma_3d(dst + x * (kN * 128) + n * 128, &tm_q, x * 64, h, q.qbegin + token, qfull + b);
           }
-          node_depth[b][n] = static_cast<uint8_t>(depth);
         }
+      } else {
       // 16 lanes per row, 8 channels each; 16 rows in flight
       const int ch = lane & 15;
 #pragma unroll 1
@@ -876,10 +956,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
           const int n = n0 + 2 * u;
-          if constexpr (!kPacked) {
-            if (ch < 8 * kHalves)
-              *reinterpret_cast<uint4*>(qbuf + b * F::kQ + (ch >> 3) * (kN * 128) + n * 128 + (((ch & 7) ^ (n & 7)) << 4)) = x[u];
-          } else {
+          {
             // q as unit (hi + lo / 32), both e4m3, unit a power of two by the
             // row's largest channel: q's 8 bits are 4 + 4, so this is exact but
             // for channels below 2^-15 of the largest
@@ -917,7 +994,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
               hi[i >> 1] |= h << (16 * (i & 1));
               lo[i >> 1] |= r << (16 * (i & 1));
             }
-            uint8_t* at = qbuf + b * F::kQ + (((ch >> 1) ^ (n & 7)) << 4) + (ch & 1) * 8;  // kLive is a multiple of 8
+            uint8_t* at = qbuf + qb * F::kQ + (((ch >> 1) ^ (n & 7)) << 4) + (ch & 1) * 8;  // kLive is a multiple of 8
             if (n < kLive) {
               *reinterpret_cast<uint2*>(at + n * 128) = make_uint2(hi[0], hi[1]);
               *reinterpret_cast<uint2*>(at + (kLive + n) * 128) = make_uint2(lo[0], lo[1]);
@@ -929,7 +1006,8 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
           }
         }
       }
-      proxy_fence();
+        proxy_fence();
+      }
       mbar_arrive(qfull + b);
       // the next item
       left -= take;
@@ -982,20 +1060,30 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
         const int32_t n = it.tile0 + t;
         const bool sink = n < it.nsink;
         const int32_t j0 = sink ? n * kTile : it.origin + (n - it.nsink) * kTile;
-        wait_or_dead(sfull + sb, (at >> 1) & 1, dead);
+        if (F::kPBufs == 2 && at >= 2)  // and P's buffer is free, V's slot has moved on to this tile
+          wait_both(sfull + sb, (at >> 1) & 1, pdone + sb, ((at - 2) >> 1) & 1, dead);
+        else
+          wait_or_dead(sfull + sb, (at >> 1) & 1, dead);
         tc_fence_after();
+        float x[kCols], low[kPacked ? kCols : 1];
+        tmem_get(tmem + sb * kNS + c0 + lanes, x);
+        if constexpr (kPacked) tmem_get(tmem + sb * kNS + kLive + c0 + lanes, low);
         const uint32_t there = *reinterpret_cast<volatile uint32_t*>(info + at % kInfo);
         // does some row miss some key of the tile?
         const bool masked = sink || there != every || j0 + kTile - 1 > (tree ? it.base - 1 : first_pos) ||
                             (a.window > 0 && j0 <= last_pos - a.window);
         float ka = a.scale_log2, kb = 0.0f, sv = 0.0f, wv = 0.0f;
-        if (kPacked) {  // the tensor cores multiplied n / 512
-          const uint32_t kp = k_pair[at % kPairs][lt];
+        bool poison = false;
+        if (kPacked) {  // the tensor cores multiplied n / 512 and n - 8
+          const uint32_t kp = k_pair[at % kPairs][lt], vp = v_pair[at % kPairs][lt];
           ka = a.scale_log2 * 512.0f * bf16_lo(kp);
           kb = a.scale_log2 * bf16_hi(kp);
+          sv = bf16_lo(vp);
+          wv = __fmaf_rn(8.0f, sv, bf16_hi(vp));
+          poison = !(fabsf(wv) <= 3.0e38f);  // as below; a step that is not finite makes wv so
+          if (poison) sv = wv = 0.0f;
         }
         uint32_t vis = 0xffffffffu;  // the rows that see this thread's key
-        bool poison = false;
         if (masked) {
           const int32_t j = j0 + lt;
           const bool here = ((there >> (lt >> unit_shift)) & 1u) && j < (sink ? it.sink_end : it.end);
@@ -1026,7 +1114,6 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
             // of such a key, where not every query sees it, becomes 0, and the
             // queries that do see it get a weight of NaN.
             const int32_t s = at % kVs;
-            if (at >= 2) wait_or_dead(pdone + sb, ((at - 2) >> 1) & 1, dead);  // V's slot has moved on to this tile
             wait_or_dead(vfull + s, (at / kVs) & 1, dead);
             const bool all = here && !draft && j <= first_pos && (always || j > last_pos - a.window);
             uint4* v = reinterpret_cast<uint4*>(vring + s * F::kStage + lt * 128);
@@ -1058,17 +1145,11 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
           }
         }
         // x_nj - r_n of this key, every row
-        float x[kCols];
-        tmem_ld(tmem + sb * kNS + c0 + lanes, x);
+        tmem_wait(x);
         if constexpr (kPacked) {
-          constexpr int kPart = kCols < 16 ? kCols : 16;
+          tmem_wait(low);
 #pragma unroll
-          for (int i0 = 0; i0 < kCols; i0 += kPart) {
-            float low[kPart];
-            tmem_ld(tmem + sb * kNS + kLive + c0 + i0 + lanes, low);
-#pragma unroll
-            for (int i = 0; i < kPart; ++i) x[i0 + i] = __fmaf_rn(low[i], 0.03125f, x[i0 + i]);
-          }
+          for (int i = 0; i < kCols; ++i) x[i] = __fmaf_rn(low[i], 0.03125f, x[i]);
         }
         tc_fence_before();
         mbar_arrive(sempty + sb);
@@ -1099,10 +1180,10 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
           float most = x[0];
 #pragma unroll
           for (int i = 1; i < kCols; ++i) most = fmaxf(most, x[i]);
-          pass = bar_any(bar, 128, most > 8.0f);
+          pass = bar_any(bar, 128, most > kSlack);
         }
         if (pass) {
-          // some row's score passes its reference by more than 8 (or the row
+          // some row's score passes its reference by too much (or the row
           // has none yet): the new reference is the row's largest score of the
           // tile
 #pragma unroll
@@ -1115,7 +1196,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
           if (lt < kCols) {
             const int c = c0 + lt;
             const float m = fmaxf(fmaxf(part[0][c], part[1][c]), fmaxf(part[2][c], part[3][c]));
-            const bool move = m > (unset ? -INFINITY : 8.0f);
+            const bool move = m > (unset ? -INFINITY : kSlack);
             corr[c] = !move ? 1.0f : unset ? 0.0f : ex2(-m);  // 2^(old reference - new)
             shift[c] = move ? m : 0.0f;
             if (move) nref[c] -= m;
@@ -1145,16 +1226,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
             }
           }
         }
-        // P's buffer is free, and V's slot has moved on to this tile
-        if (at >= F::kPBufs) wait_or_dead(pdone + ((at - F::kPBufs) & 1), ((at - F::kPBufs) >> 1) & 1, dead);
-        if (kPacked) {
-          wait_or_dead(vfull + at % kVs, (at / kVs) & 1, dead);  // V is unpacked, so its pairs are there
-          const uint32_t vp = v_pair[at % kPairs][lt];
-          sv = bf16_lo(vp);
-          wv = __fmaf_rn(8.0f, sv, bf16_hi(vp));
-          poison = !(fabsf(wv) <= 3.0e38f);  // as below; a step that is not finite makes wv so
-          if (poison) sv = wv = 0.0f;
-        }
+        if (F::kPBufs == 1 && at >= 1) wait_or_dead(pdone + ((at - 1) & 1), ((at - 1) >> 1) & 1, dead);  // P's buffer is free
         if (poison)
 #pragma unroll
           for (int i = 0; i < kCols; ++i) x[i] = ((vis >> i) & 1u) ? __int_as_float(0x7fffffff) : -INFINITY;
@@ -1321,8 +1393,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
       const int32_t rs = at % F::kRawStages;
       if (!wait_or_dead(rfull + rs, (at / F::kRawStages) & 1, dead)) break;
       const uint8_t* src = raw + rs * F::kRaw + (is_v ? kTile * F::kRawRow : 0);
-      const uint32_t pair =
-          reinterpret_cast<const uint32_t*>(raw + rs * F::kRaw + 2 * kTile * F::kRawRow)[(is_v ? kTile : 0) + key];
+      const uint32_t* pairs = reinterpret_cast<const uint32_t*>(raw + rs * F::kRaw + 2 * kTile * F::kRawRow) + key;
       uint4 w4[2 * kHalves];  // 16 packed bytes: 32 channels
 #pragma unroll
       for (int c = 0; c < 2 * kHalves; ++c) {
@@ -1332,7 +1403,6 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
       if (is_v) {
         const int32_t s = at % kVs;
         if (!wait_or_dead(vempty + s, ((at / kVs) & 1) ^ 1u, dead)) break;
-        v_pair[at % kPairs][key] = pair;
         uint8_t* dst = vring + s * F::kStage + key * 128;
 #pragma unroll
         for (int c = 0; c < 2 * kHalves; ++c) {
@@ -1356,7 +1426,8 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
       } else {
         if (!__all_sync(0xffffffffu, wait_or_dead(kempty + (at & 1), ((at >> 1) & 1) ^ 1u, dead))) break;
         tc_fence_after();
-        k_pair[at % kPairs][key] = pair;
+        k_pair[at % kPairs][key] = pairs[0];
+        v_pair[at % kPairs][key] = pairs[kTile];
         const uint32_t dst = tmem + F::kKCol + (at & 1) * F::kKCols + (static_cast<uint32_t>((warp & 3) * 32) << 16);
 #pragma unroll
         for (int c = 0; c < kHalves; ++c) {
@@ -1392,16 +1463,17 @@ template <int kLive, bool kPacked, int kHalves>
 ss_status launch(const AttnArgs& a, cudaStream_t s) {
   using F = Cfg<kLive, kPacked, kHalves>;
   const void* fn = reinterpret_cast<const void*>(&attn_kernel<kLive, kPacked, kHalves>);
-  CUtensorMap mk, mv;
+  CUtensorMap mk, mv, mq{};
   const int unit = 1 << (a.c.page_shift < 7 ? a.c.page_shift : 7);
   if (!make_cache_map(&mk, a.c.k, a.c, unit) || !make_cache_map(&mv, a.c.v, a.c, unit)) return SS_ERR_UNSUPPORTED;
+  if (!kPacked && !make_query_map(&mq, a, kLive)) return SS_ERR_UNSUPPORTED;
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, F::kSmem);
   if (e == cudaSuccess) {
     const int grid = sms < kMaxCtas ? sms : kMaxCtas;
-    attn_kernel<kLive, kPacked, kHalves><<<grid, F::kThreads, F::kSmem, s>>>(mk, mv, a);
+    attn_kernel<kLive, kPacked, kHalves><<<grid, F::kThreads, F::kSmem, s>>>(mk, mv, mq, a);
   }
   return finish(e);
 }
