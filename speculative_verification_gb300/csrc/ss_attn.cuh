@@ -123,6 +123,15 @@ struct Cfg {
   static constexpr int kSoft = 128 * kGroups;
   static constexpr int kUnpack = kPacked ? 256 : 0;          // K tiles by one warpgroup, V tiles by the other
   static constexpr int kThreads = 128 + kSoft + kUnpack;
+  // Registers per thread by warpgroup where one size does not fit all: the
+  // launch's kThreads x kRegs are shared out again (all or none of them).
+  static constexpr int kRegs = kThreads > 512 ? 96 : kThreads > 384 ? 128 : 168;
+  static constexpr bool kSplit = (!kPacked && kLive == 128) || (kPacked && kLive >= 32);
+  static constexpr int kRegs0 = 64;                                   // copies, MMAs, queries
+  static constexpr int kRegsSoft = !kPacked ? 104 : kLive >= 64 ? 152 : 136;
+  static constexpr int kRegsUnpack = kLive >= 64 ? 56 : 72;
+  static_assert(!kSplit || kRegs0 + kGroups * kRegsSoft + (kPacked ? 2 * kRegsUnpack : 0) <= kThreads / 128 * kRegs,
+                "a warpgroup would wait for registers for ever");
   static constexpr int kStage = kHalves * 16384;             // 128 keys x 64 channels x 2 bytes per half
   static constexpr int kQ = kPacked ? kNS * 128 : kHalves * kN * 128;
   static constexpr int kNQ = 2;                              // items prepared ahead
@@ -135,7 +144,7 @@ struct Cfg {
   static constexpr int kRawStages = kPacked ? 4 : 1;
   // the static arrays, rounded up
   static constexpr int kMeta = kNQ * (static_cast<int>(sizeof(Item)) + kN * 32 + 64 + 512) + kN * 36 + 1536 +
-                               (kGroups > 1 ? kGroups * 256 : 0) + (kPacked ? 2 * kPairs * kTile * 4 : 0);
+                               (kPacked ? 2 * kPairs * kTile * 4 : 0);
   static constexpr int kBudget = 232448 - 1024 - kQBufs * kQ - kPBufs * kP - kRawStages * kRaw - kMeta;
   // K and V have a ring each, so that whoever waits for a slot has used the
   // slot's previous contents itself: a parity wait tells two phases apart, no
@@ -341,6 +350,15 @@ __device__ __forceinline__ void tmem_st(uint32_t t, const float (&v)[32]) {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+template <int kRegs>
+__device__ __forceinline__ void regs_fewer() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_more() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
 template <int kCount>
 __device__ __forceinline__ void tmem_wait(float (&v)[kCount]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
@@ -393,12 +411,21 @@ __device__ __forceinline__ bool bar_any(int id, int n, bool p) {
   return any != 0;
 }
 
-// Order-preserving signed integer of a float that is not NaN, and back.
-__device__ __forceinline__ int32_t order_int(float f) {
-  const int32_t i = __float_as_int(f);
-  return i ^ ((i >> 31) & 0x7fffffff);
+// Largest value of the warp's lanes that is a number (-infinity if none).
+__device__ __forceinline__ float warp_max(float x) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return fmaxf(r, -INFINITY);
 }
-__device__ __forceinline__ float order_float(int32_t i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
+
+__device__ __forceinline__ void store_pair(uint16_t* p, uint32_t pair, bool wide) {
+  if (wide) {
+    *reinterpret_cast<uint32_t*>(p) = pair;
+  } else {
+    p[0] = static_cast<uint16_t>(pair);
+    p[1] = static_cast<uint16_t>(pair >> 16);
+  }
+}
 
 // Sums of kCount values over the warp's 32 lanes; lane i gets the sum of
 // value i % kCount (a butterfly that halves the values at each step).
@@ -486,7 +513,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
   constexpr int kRing = F::kRing, kKs = F::kKs, kVs = F::kVs, kNQ = F::kNQ, kCols = F::kCols, kN = F::kN, kNS = F::kNS;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t kfull[kKs], kempty[kKs], vfull[kVs], vempty[kVs], sfull[2], sempty[2], pfull[2], pdone[2], oempty[2],
-      qfull[kNQ], qempty[kNQ], qfree[F::kQBufs], rfull[F::kRawStages], rempty[F::kRawStages], looked, drain[2];
+      qfull[kNQ], qempty[kNQ], qfree[F::kQBufs], rfull[F::kRawStages], rempty[F::kRawStages], written[2], drain[2];
   __shared__ Item items[kNQ];
   __shared__ __align__(16) int32_t row_pos[kNQ][kN];
   __shared__ __align__(16) uint64_t row_path[kNQ][kN];
@@ -497,7 +524,6 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
   __shared__ uint64_t node_sees[kNQ][SS_TREE_MAX_NODES];
   __shared__ uint32_t info[kInfo];
   __shared__ uint32_t k_pair[kPacked ? kPairs : 1][kPacked ? kTile : 1], v_pair[kPacked ? kPairs : 1][kPacked ? kTile : 1];
-  __shared__ uint8_t key_bad[2][F::kGroups > 1 ? F::kGroups : 1][F::kGroups > 1 ? kTile : 1];
   __shared__ __align__(16) float nref[kN], corr[kN], shift[kN], sums[kN], csums[kN];
   __shared__ float part[4][kN];
   __shared__ uint32_t tmem_slot;
@@ -537,7 +563,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
         mbar_init(rfull + i, 1);
         mbar_init(rempty + i, 256);
       }
-    mbar_init(&looked, F::kSoft);
+    for (int i = 0; i < 2; ++i) mbar_init(written + i, F::kGroups > 1 ? F::kSoft - 128 : 1);
     mbar_init(&drain[0], 1);
     mbar_init(&drain[1], 1);
     s_dead = 0;
@@ -628,7 +654,9 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
   __syncthreads();
   if (my_tiles == 0) {
     // fewer tiles than CTAs
-  } else if (warp == 0) {
+  } else if (warp < 4) {
+    if constexpr (F::kSplit) regs_fewer<F::kRegs0>();
+    if (warp == 0) {
     // ---------------------------------------------------- tensor copies --
     const int32_t unit_shift = min(a.c.page_shift, 7), units = kTile >> unit_shift;
     int32_t at = 0, k = 0;  // tile, item
@@ -939,13 +967,13 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
           }
         }
       } else {
-      // 16 lanes per row, 8 channels each; 16 rows in flight
+      // 16 lanes per row, 8 channels each; 8 rows in flight
       const int ch = lane & 15;
 #pragma unroll 1
-      for (int n0 = lane >> 4; n0 < kN; n0 += 16) {
-        uint4 x[8];
+      for (int n0 = lane >> 4; n0 < kN; n0 += 8) {
+        uint4 x[4];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
+        for (int u = 0; u < 4; ++u) {
           const int n = n0 + 2 * u, token = token_of(a, row0 + n);
           x[u] = make_uint4(0u, 0u, 0u, 0u);
           if (n < rows && ch * 8 < a.c.dim)
@@ -954,7 +982,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
                 (static_cast<int64_t>(head) * a.group + (row0 + n - token * a.group)) * a.q_head + ch * 16);
         }
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
+        for (int u = 0; u < 4; ++u) {
           const int n = n0 + 2 * u;
           {
             // q as unit (hi + lo / 32), both e4m3, unit a power of two by the
@@ -1026,7 +1054,9 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
       }
       s = span_of(a, q, row0);
     }
+  }
   } else if (!kPacked || warp < 4 + F::kSoft / 32) {
+    if constexpr (F::kSplit) regs_more<F::kRegsSoft>();
     // ---------------------------------------------------------- softmax --
     const int st = tid - 128, wg = st >> 7, lt = st & 127, wq = warp & 3;
     const int c0 = wg * kCols;                                    // this warpgroup's rows
@@ -1035,8 +1065,11 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
     const int32_t unit_shift = min(a.c.page_shift, 7);
     const uint32_t every = static_cast<uint32_t>((1ull << (kTile >> unit_shift)) - 1);
     const bool tree = a.parents != nullptr;
+    // two channels per store where the rows of out allow it
+    const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 3) == 0 && ((a.out_token | a.out_head) & 1) == 0;
+    constexpr uint32_t kSwz = kN >= 64 ? 0x70u : kN == 32 ? 0x30u : 0x10u;  // P's swizzle
     int32_t at = 0;
-    uint32_t looks = 0;
+    uint32_t uses[2] = {0, 0};  // of written
     for (int32_t k = 0; at < my_tiles; ++k) {
       const int b = k % kNQ;
       const bool in = wait_or_dead(qfull + b, (k / kNQ) & 1, dead);
@@ -1065,7 +1098,8 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
         else
           wait_or_dead(sfull + sb, (at >> 1) & 1, dead);
         tc_fence_after();
-        float x[kCols], low[kPacked ? kCols : 1];
+        constexpr int kPart = !kPacked ? 8 : kCols < 16 ? kCols : 16;
+        float x[kCols], low[kPart];
         tmem_get(tmem + sb * kNS + c0 + lanes, x);
         if constexpr (kPacked) tmem_get(tmem + sb * kNS + kLive + c0 + lanes, low);
         const uint32_t there = *reinterpret_cast<volatile uint32_t*>(info + at % kInfo);
@@ -1084,6 +1118,11 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
           if (poison) sv = wv = 0.0f;
         }
         uint32_t vis = 0xffffffffu;  // the rows that see this thread's key
+        int32_t from = 0, node = -1;
+        uint32_t span = 0x7fffffffu;
+        const auto sees = [&](int c) {
+          return static_cast<uint32_t>(row_pos[b][c] - from) <= span && (node < 0 || ((row_path[b][c] >> node) & 1ull) != 0);
+        };
         if (masked) {
           const int32_t j = j0 + lt;
           const bool here = ((there >> (lt >> unit_shift)) & 1u) && j < (sink ? it.sink_end : it.end);
@@ -1091,8 +1130,9 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
           const int32_t place = draft ? it.base + node_depth[b][j - it.base] : j;
           // a row at position pos sees the key when 0 <= pos - place <= span
           const bool always = a.window == 0 || place < a.sinks;
-          const uint32_t span = always ? 0x7fffffffu : static_cast<uint32_t>(a.window) - 1u;
-          const int32_t from = here ? place : 0x7fffffff;
+          span = always ? 0x7fffffffu : static_cast<uint32_t>(a.window) - 1u;
+          from = here ? place : 0x7fffffff;
+          if (draft) node = j - it.base;
           vis = 0;
 #pragma unroll
           for (int i = 0; i < kCols; i += 4) {
@@ -1109,47 +1149,41 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
             for (int i = 0; i < kCols; ++i) on |= ((word[2 * i] >> ((j - it.base) & 31)) & 1u) << i;
             vis &= on;
           }
-          if (!kPacked) {
+          if (!kPacked && wg == 0) {
             // A value that is not finite must not meet a weight of 0: the row
-            // of such a key, where not every query sees it, becomes 0, and the
-            // queries that do see it get a weight of NaN.
+            // of such a key, where not every query sees it, becomes 0 in
+            // shared memory, and the queries that do see it get a weight of NaN.
             const int32_t s = at % kVs;
             wait_or_dead(vfull + s, (at / kVs) & 1, dead);
             const bool all = here && !draft && j <= first_pos && (always || j > last_pos - a.window);
-            uint4* v = reinterpret_cast<uint4*>(vring + s * F::kStage + lt * 128);
             if (!all) {
+              uint4* v = reinterpret_cast<uint4*>(vring + s * F::kStage + lt * 128);
               uint32_t acc = 0;  // 0 times each channel, added up: NaN as soon as one is not finite
 #pragma unroll 4
-              for (int c = wg; c < 8 * kHalves; c += F::kGroups) {
+              for (int c = 0; c < 8 * kHalves; ++c) {
                 const uint4 x = v[(c >> 3) * 1024 + ((c & 7) ^ (lt & 7))];
                 const uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(y[e]), "r"(0u));
               }
               poison = (acc & 0x7fff7fffu) != 0;
-            }
-            if (F::kGroups > 1) {  // each warpgroup has looked at a part of the channels
-              key_bad[looks & 1][wg][lt] = poison;
-              mbar_arrive(&looked);
-              wait_or_dead(&looked, looks & 1, dead);
-#pragma unroll
-              for (int g = 0; g < F::kGroups; ++g) poison |= key_bad[looks & 1][g][lt] != 0;
-              ++looks;
-            }
-            if (poison && wg == 0) {
-#pragma unroll
-              for (int h = 0; h < kHalves; ++h)
-#pragma unroll
-                for (int c = 0; c < 8; ++c) v[h * 1024 + c] = make_uint4(0u, 0u, 0u, 0u);
+              if (poison) {
+#pragma unroll 1
+                for (int c = 0; c < 8 * kHalves; ++c) v[(c >> 3) * 1024 + (c & 7)] = make_uint4(0u, 0u, 0u, 0u);
+              }
             }
           }
         }
         // x_nj - r_n of this key, every row
         tmem_wait(x);
         if constexpr (kPacked) {
-          tmem_wait(low);
 #pragma unroll
-          for (int i = 0; i < kCols; ++i) x[i] = __fmaf_rn(low[i], 0.03125f, x[i]);
+          for (int i0 = 0; i0 < kCols; i0 += kPart) {
+            if (i0 > 0) tmem_get(tmem + sb * kNS + kLive + c0 + i0 + lanes, low);
+            tmem_wait(low);
+#pragma unroll
+            for (int i = 0; i < kPart; ++i) x[i0 + i] = __fmaf_rn(low[i], 0.03125f, x[i0 + i]);
+          }
         }
         tc_fence_before();
         mbar_arrive(sempty + sb);
@@ -1188,8 +1222,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
           // tile
 #pragma unroll
           for (int i = 0; i < kCols; ++i) {
-            const float y = fmaxf(x[i], -INFINITY);  // a NaN counts as nothing
-            const float m = order_float(__reduce_max_sync(0xffffffffu, order_int(y)));
+            const float m = warp_max(x[i]);  // a NaN counts as nothing
             if (lane == i) part[wq][c0 + i] = m;
           }
           bar_sync(bar, 128);
@@ -1227,9 +1260,6 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
           }
         }
         if (F::kPBufs == 1 && at >= 1) wait_or_dead(pdone + ((at - 1) & 1), ((at - 1) >> 1) & 1, dead);  // P's buffer is free
-        if (poison)
-#pragma unroll
-          for (int i = 0; i < kCols; ++i) x[i] = ((vis >> i) & 1u) ? __int_as_float(0x7fffffff) : -INFINITY;
         // powers, sums, and P^T [key][row], swizzled as the MMA reads it
         uint8_t* pb = pbuf + sb % F::kPBufs * F::kP + (c0 >> 6) * (kTile * 128);
 #pragma unroll
@@ -1251,8 +1281,23 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
             o4[e] = bf16_pair(p[0], p[1]);
           }
           const uint32_t off = lt * F::kPitch + ((c0 & 63) + i8 * 8) * 2;
-          const uint32_t swz = kN >= 64 ? 0x70u : kN == 32 ? 0x30u : 0x10u;
-          *reinterpret_cast<uint4*>(pb + (off ^ ((off >> 3) & swz))) = make_uint4(o4[0], o4[1], o4[2], o4[3]);
+          *reinterpret_cast<uint4*>(pb + (off ^ ((off >> 3) & kSwz))) = make_uint4(o4[0], o4[1], o4[2], o4[3]);
+        }
+        if (!kPacked && F::kGroups > 1 && masked) {
+          // warpgroup 0 writes into the others' weights (below) once they are there
+          if (wg != 0) mbar_arrive(&written[sb]);
+          else if (poison) wait_or_dead(&written[sb], uses[sb] & 1, dead);
+          uses[sb] += 1;
+        }
+        if (poison) {
+          const int from = kPacked ? c0 : 0, upto = kPacked ? c0 + kCols : kLive;
+#pragma unroll 1
+          for (int c = from; c < upto; ++c) {
+            const bool see = kPacked ? ((vis >> (c - c0)) & 1u) != 0 : sees(c);
+            const uint32_t off = lt * F::kPitch + (c & 63) * 2;
+            uint8_t* p = pbuf + sb % F::kPBufs * F::kP + (c >> 6) * (kTile * 128);
+            if (see) *reinterpret_cast<uint16_t*>(p + (off ^ ((off >> 3) & kSwz))) = 0x7fffu;
+          }
         }
         proxy_fence();
         tc_fence_before();
@@ -1266,7 +1311,11 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
         if (lane < kCols) part[wq][c0 + lane] = s;
       }
       bar_sync(bar, 128);
-      if (lt < kCols) sums[c0 + lt] = (part[0][c0 + lt] + part[1][c0 + lt]) + (part[2][c0 + lt] + part[3][c0 + lt]);
+      float sum = 0.0f;  // thread i: row i's
+      if (lt < kCols) {
+        sum = (part[0][c0 + lt] + part[1][c0 + lt]) + (part[2][c0 + lt] + part[3][c0 + lt]);
+        sums[c0 + lt] = sum == 0.0f ? 0.0f : __fdividef(1.0f, sum);
+      }
       if constexpr (kPacked) {
         bar_sync(bar, 128);
         const float s = warp_sums<kCols>(cs);
@@ -1282,26 +1331,34 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
       if (wq * 32 < kHalves * 64 && c0 < rows) {
         float o[kCols];
         tmem_ld(o_base, o);
+        if (whole) {
+          // even lanes take two channels of the even row, odd lanes of the odd one
+          const bool odd = lane & 1;
+          const bool in = (ch & ~1) < a.c.dim;
 #pragma unroll
-        for (int i = 0; i < kCols; ++i) {
-          const int c = c0 + i;
-          if (c >= rows) continue;
-          if (kPacked) o[i] += csums[c];
-          if (whole) {
-            const float s = sums[c], y = s == 0.0f ? 0.0f : __fdividef(o[i], s);
-            if (ch < a.c.dim) a.out[row_out[b][c] + ch] = static_cast<uint16_t>(bf16_pair(y, 0.0f));
-          } else {
-            __stcg(piece + c * 128 + ch, o[i]);
+          for (int i = 0; i < kCols; i += 2) {
+            const int c = c0 + i + odd;
+            float2 y = make_float2(o[i], o[i + 1]);
+            if (kPacked) y = make_float2(y.x + csums[c0 + i], y.y + csums[c0 + i + 1]);
+            y.x *= sums[c0 + i];
+            y.y *= sums[c0 + i + 1];
+            const float other = __shfl_xor_sync(0xffffffffu, odd ? y.x : y.y, 1);
+            const uint32_t pair = odd ? bf16_pair(other, y.y) : bf16_pair(y.x, other);
+            if (c < rows && in) store_pair(a.out + row_out[b][c] + (ch & ~1), pair, wide);
           }
+        } else {
+#pragma unroll
+          for (int i = 0; i < kCols; ++i)
+            if (c0 + i < rows) __stcg(piece + (c0 + i) * 128 + ch, kPacked ? o[i] + csums[c0 + i] : o[i]);
         }
       }
       if (lt < kCols && c0 + lt < rows) {
         const int c = c0 + lt;
         if (!whole) {
           __stcg(piece + 128 * 128 + 2 * c, unset ? kUnset : nref[c]);
-          __stcg(piece + 128 * 128 + 2 * c + 1, sums[c]);
+          __stcg(piece + 128 * 128 + 2 * c + 1, sum);
         } else if (a.lse) {
-          a.lse[row_lse[b][c]] = sums[c] == 0.0f ? -INFINITY : 0.69314718055994531f * (log2f(sums[c]) - nref[c]);
+          a.lse[row_lse[b][c]] = sum == 0.0f ? -INFINITY : 0.69314718055994531f * (log2f(sum) - nref[c]);
         }
       }
       tc_fence_before();
@@ -1366,9 +1423,8 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
             const float inv = sum == 0.0f ? 0.0f : __fdividef(1.0f, sum);
             if (lane * 4 < a.c.dim) {
               uint16_t* o = a.out + row_out[b][c] + lane * 4;
-              const float y[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
-#pragma unroll
-              for (int e = 0; e < 4; ++e) o[e] = static_cast<uint16_t>(bf16_pair(y[e], 0.0f));
+              store_pair(o, bf16_pair(acc.x * inv, acc.y * inv), wide);
+              store_pair(o + 2, bf16_pair(acc.z * inv, acc.w * inv), wide);
             }
             if (lane == 0 && a.lse)
               a.lse[row_lse[b][c]] = sum == 0.0f ? -INFINITY : 0.69314718055994531f * (log2f(sum) + top);
@@ -1379,6 +1435,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
       if (lane == 0) mbar_arrive(qempty + b);
     }
   } else if constexpr (kPacked) {
+    if constexpr (F::kSplit) regs_fewer<F::kRegsUnpack>();
     // --------------------------------------------------------- unpacking --
     // A thread per key; one warpgroup the K tiles, the other the V tiles.
     // A byte n = 0..15 is the e4m3 number n / 512 (0..7 its subnormals, 8..15
@@ -1413,7 +1470,8 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               // 128 + n in bf16 is 0x4300 | n; minus 136 leaves n - 8 exactly
-              const uint32_t y = ((w[e] >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+              uint32_t y;  // (w >> 4 i) & 0x000f000f | 0x43004300 in one instruction after the shift
+              asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(y) : "r"(w[e] >> (4 * i)), "r"(0x000f000fu), "r"(0x43004300u));
               asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(o[i]) : "r"(y), "r"(0x43084308u));
             }
             const int x = c * 4 + e;  // 8 channels
@@ -1472,6 +1530,13 @@ ss_status launch(const AttnArgs& a, cudaStream_t s) {
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, F::kSmem);
   if (e == cudaSuccess) {
+    if constexpr (F::kSplit) {  // the shares are of what the launch brings
+      static const int regs = [&] {
+        cudaFuncAttributes at{};
+        return cudaFuncGetAttributes(&at, fn) == cudaSuccess ? at.numRegs : 0;
+      }();
+      if (regs != F::kRegs) return SS_ERR_UNSUPPORTED;
+    }
     const int grid = sms < kMaxCtas ? sms : kMaxCtas;
     attn_kernel<kLive, kPacked, kHalves><<<grid, F::kThreads, F::kSmem, s>>>(mk, mv, mq, a);
   }
