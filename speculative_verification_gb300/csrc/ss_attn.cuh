@@ -121,16 +121,19 @@ struct Cfg {
   static constexpr int kGroups = kLive <= 16 ? 1 : kLive == 32 ? 2 : kPacked ? 2 : 4;  // softmax warpgroups
   static constexpr int kCols = kLive / kGroups;              // rows per softmax thread
   static constexpr int kSoft = 128 * kGroups;
-  static constexpr int kUnpack = kPacked ? 256 : 0;          // K tiles by one warpgroup, V tiles by the other
+  // 4 bits: one warpgroup unpacks K; V, twice the work, has two that take turns
+  // where the softmax leaves the registers
+  static constexpr int kVGroups = kLive <= 16 ? 2 : 1;
+  static constexpr int kUnpack = kPacked ? 128 * (1 + kVGroups) : 0;
   static constexpr int kThreads = 128 + kSoft + kUnpack;
   // Registers per thread by warpgroup where one size does not fit all: the
   // launch's kThreads x kRegs are shared out again (all or none of them).
   static constexpr int kRegs = kThreads > 512 ? 96 : kThreads > 384 ? 128 : 168;
-  static constexpr bool kSplit = (!kPacked && kLive == 128) || (kPacked && kLive >= 32);
+  static constexpr bool kSplit = kPacked || kLive == 128;
   static constexpr int kRegs0 = 64;                                   // copies, MMAs, queries
   static constexpr int kRegsSoft = !kPacked ? 104 : kLive >= 64 ? 152 : 136;
   static constexpr int kRegsUnpack = kLive >= 64 ? 56 : 72;
-  static_assert(!kSplit || kRegs0 + kGroups * kRegsSoft + (kPacked ? 2 * kRegsUnpack : 0) <= kThreads / 128 * kRegs,
+  static_assert(!kSplit || kRegs0 + kGroups * kRegsSoft + kUnpack / 128 * kRegsUnpack <= kThreads / 128 * kRegs,
                 "a warpgroup would wait for registers for ever");
   static constexpr int kStage = kHalves * 16384;             // 128 keys x 64 channels x 2 bytes per half
   static constexpr int kQ = kPacked ? kNS * 128 : kHalves * kN * 128;
@@ -159,6 +162,7 @@ struct Cfg {
   static constexpr uint32_t kUsed = kKCol + 2 * kKCols;
   static constexpr uint32_t kTmem = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
   static_assert(kKs >= 1 && kVs >= 2, "a tile in use and one on its way");
+  static_assert(!kPacked || (kVs % kVGroups == 0 && kRawStages % kVGroups == 0), "a warpgroup's slots are its own");
 };
 
 __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
@@ -1437,16 +1441,16 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
   } else if constexpr (kPacked) {
     if constexpr (F::kSplit) regs_fewer<F::kRegsUnpack>();
     // --------------------------------------------------------- unpacking --
-    // A thread per key; one warpgroup the K tiles, the other the V tiles.
+    // A thread per key; one warpgroup the K tiles, the others the V tiles.
     // A byte n = 0..15 is the e4m3 number n / 512 (0..7 its subnormals, 8..15
     // the first binade), so K only takes its bits apart; it goes to tensor
     // memory (a key's lane is the thread's), which spares shared memory a write
     // and the MMAs a read of the tile.  V becomes n - 8 in bf16: its weights
     // need bf16's range, and as an M-major operand it is in shared memory.
-    const int key = (tid - 128 - F::kSoft) & 127;
-    const bool is_v = tid - 128 - F::kSoft >= 128;
+    const int key = (tid - 128 - F::kSoft) & 127, turn = ((tid - 128 - F::kSoft) >> 7) - 1;
+    const bool is_v = turn >= 0;
 #pragma unroll 1
-    for (int32_t at = 0; at < my_tiles; ++at) {
+    for (int32_t at = is_v ? turn : 0; at < my_tiles; at += is_v ? F::kVGroups : 1) {
       const int32_t rs = at % F::kRawStages;
       if (!wait_or_dead(rfull + rs, (at / F::kRawStages) & 1, dead)) break;
       const uint8_t* src = raw + rs * F::kRaw + (is_v ? kTile * F::kRawRow : 0);
