@@ -686,13 +686,33 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       const Item it = items[b];
+      // 64 entries of the page table from the next tile's on, two per lane,
+      // loaded a tile or more before their use: a load per tile, waited for,
+      // would take longer than the tile
+      const int32_t last = min((it.end - 1) >> a.c.page_shift, a.t.max_pages - 1);
+      const auto entry = [&](int32_t e) { return e <= last ? it.row[e] : -1; };
+      int32_t e0 = (it.origin + max(it.tile0 - it.nsink, 0) * kTile) >> a.c.page_shift;
+      int32_t near = entry(e0 + lane), far = entry(e0 + 32 + lane);
 #pragma unroll 1
       for (int32_t t = 0; t < it.tiles && ok; ++t, ++at) {
         const int32_t n = it.tile0 + t;
         const bool sink = n < it.nsink;
         const int32_t u = (sink ? n * kTile : it.origin + (n - it.nsink) * kTile) + (lane << unit_shift);
         int32_t page = -1;
-        if (lane < units && u < (sink ? it.sink_end : it.end)) page = page_of(a.t, a.c, it.row, u);
+        if (sink) {
+          if (lane < units && u < it.sink_end) page = page_of(a.t, a.c, it.row, u);
+        } else {
+          const int32_t first = (it.origin + (n - it.nsink) * kTile) >> a.c.page_shift;
+          if (first - e0 >= 32) {
+            e0 += 32;
+            near = far;
+            far = entry(e0 + 32 + lane);
+          }
+          const int32_t e = (u >> a.c.page_shift) - e0;
+          const int32_t p0 = __shfl_sync(0xffffffffu, near, e & 31), p1 = __shfl_sync(0xffffffffu, far, e & 31);
+          page = e < 32 ? p0 : p1;
+          if (lane >= units || u >= it.end || page >= a.c.num_pages) page = -1;
+        }
         const uint32_t there = __ballot_sync(0xffffffffu, page >= 0);
         const int32_t slot = u & ((1 << a.c.page_shift) - 1);
         if (kPacked) {
