@@ -211,13 +211,22 @@ __device__ __forceinline__ void tma_3d(void* dst, const CUtensorMap* map, int32_
       : "memory");
 }
 
-__device__ __forceinline__ void tma_4d(void* dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z, int32_t w,
+__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z, int32_t w,
                                        uint64_t* bar) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
-          smem_addr(dst)),
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
       : "memory");
+}
+
+// 16 bytes by the thread's own asynchronous copy (zeros where `there` is
+// false), and an arrival on `bar` once the thread's copies so far are done.
+__device__ __forceinline__ void async_load16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16u : 0u) : "memory");
+}
+__device__ __forceinline__ void async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
 // Shared-memory matrix descriptor: low word the start address and the leading
@@ -564,7 +573,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
     for (int i = 0; i < F::kQBufs; ++i) mbar_init(qfree + i, 1);
     if (kPacked)
       for (int i = 0; i < F::kRawStages; ++i) {
-        mbar_init(rfull + i, 1);
+        mbar_init(rfull + i, 33);  // the copies' bytes, and the lanes' own copies
         mbar_init(rempty + i, 256);
       }
     for (int i = 0; i < 2; ++i) mbar_init(written + i, F::kGroups > 1 ? F::kSoft - 128 : 1);
@@ -663,47 +672,44 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
     if (warp == 0) {
     // ---------------------------------------------------- tensor copies --
     const int32_t unit_shift = min(a.c.page_shift, 7), units = kTile >> unit_shift;
+    const int32_t tiles_all = __shfl_sync(0xffffffffu, my_tiles, 0);
+    const uint32_t ring_a = __shfl_sync(0xffffffffu, smem_addr(ring), 0);
+    const uint32_t vring_a = ring_a + (kPacked ? 0 : kKs) * F::kStage;
+    const uint32_t raw_a = ring_a + kRing * F::kStage + F::kPBufs * F::kP + F::kQBufs * F::kQ;
     int32_t at = 0, k = 0;  // tile, item
     bool ok = true;
     int32_t k_tiles = 0, v_tiles = 0;  // issued
-    const auto issue = [&](const CUtensorMap* map, uint8_t* dst, uint64_t* filled, uint64_t* free, int32_t use, int32_t page,
-                           int32_t slot, int32_t head) {
-      if (ok) ok = wait_or_dead(free, (use & 1) ^ 1u, dead);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) return false;
-      if (lane == 0) mbar_arrive_expect_tx(filled, F::kStage);
-      __syncwarp();
-      if (lane < units)
-#pragma unroll
-        for (int h = 0; h < kHalves; ++h)
-          tma_4d(dst + h * 16384 + (lane << unit_shift) * 128, map, h * 64, slot, head, page, filled);
-      return true;
+    const auto wait = [&](uint64_t* bar, int32_t use) {
+      if (ok) ok = __all_sync(0xffffffffu, wait_or_dead(bar, use & 1, dead));
     };
 #pragma unroll 1
-    while (at < my_tiles && ok) {
+    while (at < tiles_all && ok) {
       const int b = k % kNQ;
-      ok = wait_or_dead(qfull + b, (k / kNQ) & 1, dead);
-      ok = __all_sync(0xffffffffu, ok);
+      wait(qfull + b, k / kNQ);
       if (!ok) break;
-      const Item it = items[b];
+      const Item& it = items[b];
+      const auto same = [](int32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
+      const int32_t tiles = same(it.tiles), tile0 = same(it.tile0), nsink = same(it.nsink), sink_end = same(it.sink_end);
+      const int32_t origin = same(it.origin), end = same(it.end), head = same(it.head);
+      const int32_t* row = it.row;
       // 64 entries of the page table from the next tile's on, two per lane,
       // loaded a tile or more before their use: a load per tile, waited for,
       // would take longer than the tile
-      const int32_t last = min((it.end - 1) >> a.c.page_shift, a.t.max_pages - 1);
-      const auto entry = [&](int32_t e) { return e <= last ? it.row[e] : -1; };
-      int32_t e0 = (it.origin + max(it.tile0 - it.nsink, 0) * kTile) >> a.c.page_shift;
+      const int32_t last = min((end - 1) >> a.c.page_shift, a.t.max_pages - 1);
+      const auto entry = [&](int32_t e) { return e <= last ? row[e] : -1; };
+      int32_t e0 = (origin + max(tile0 - nsink, 0) * kTile) >> a.c.page_shift;
       int32_t near = entry(e0 + lane), far = entry(e0 + 32 + lane);
 #pragma unroll 1
-      for (int32_t t = 0; t < it.tiles && ok; ++t, ++at) {
-        const int32_t n = it.tile0 + t;
-        const bool sink = n < it.nsink;
-        const int32_t u = (sink ? n * kTile : it.origin + (n - it.nsink) * kTile) + (lane << unit_shift);
+      for (int32_t t = 0; t < tiles && ok; ++t, ++at) {
+        const int32_t n = tile0 + t;
+        const bool sink = n < nsink;
+        const int32_t j0 = sink ? n * kTile : origin + (n - nsink) * kTile;
+        const int32_t u = j0 + (lane << unit_shift);
         int32_t page = -1;
         if (sink) {
-          if (lane < units && u < it.sink_end) page = page_of(a.t, a.c, it.row, u);
+          if (lane < units && u < sink_end) page = page_of(a.t, a.c, row, u);
         } else {
-          const int32_t first = (it.origin + (n - it.nsink) * kTile) >> a.c.page_shift;
-          if (first - e0 >= 32) {
+          if ((j0 >> a.c.page_shift) - e0 >= 32) {
             e0 += 32;
             near = far;
             far = entry(e0 + 32 + lane);
@@ -711,38 +717,52 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
           const int32_t e = (u >> a.c.page_shift) - e0;
           const int32_t p0 = __shfl_sync(0xffffffffu, near, e & 31), p1 = __shfl_sync(0xffffffffu, far, e & 31);
           page = e < 32 ? p0 : p1;
-          if (lane >= units || u >= it.end || page >= a.c.num_pages) page = -1;
+          if (lane >= units || u >= end || page >= a.c.num_pages) page = -1;
         }
         const uint32_t there = __ballot_sync(0xffffffffu, page >= 0);
-        const int32_t slot = u & ((1 << a.c.page_shift) - 1);
-        if (kPacked) {
-          const int s = at % F::kRawStages;
-          ok = wait_or_dead(rempty + s, ((at / F::kRawStages) & 1) ^ 1u, dead);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          uint8_t* dst = raw + s * F::kRaw;
-          if (lane == 0) {
-            *reinterpret_cast<volatile uint32_t*>(info + at % kInfo) = there;
-            mbar_arrive_expect_tx(rfull + s, 2 * kTile * F::kRawRow + 2 * __popc(there) * (4 << unit_shift));
-          }
-          __syncwarp();
+        if (lane == 0) *reinterpret_cast<volatile uint32_t*>(info + at % kInfo) = there;
+        const auto copies = [&](const CUtensorMap* map, uint32_t dst, uint64_t* bar) {  // of K or V, a lane per page
           if (lane < units) {
-            const int32_t pg = page < 0 ? a.c.num_pages : page;  // out of range: filled with zeros
-            tma_4d(dst + (lane << unit_shift) * F::kRawRow, &tm_k, 0, slot, it.head, pg, rfull + s);
-            tma_4d(dst + kTile * F::kRawRow + (lane << unit_shift) * F::kRawRow, &tm_v, 0, slot, it.head, pg, rfull + s);
-            if (page >= 0) {
-              const int64_t off = page * a.c.s_page_stride + it.head * a.c.s_head_stride + slot * 4;
-              uint8_t* pair = dst + 2 * kTile * F::kRawRow + (lane << unit_shift) * 4;
-              bulk_load(pair, a.c.ks + off, 4u << unit_shift, rfull + s);
-              bulk_load(pair + kTile * 4, a.c.vs + off, 4u << unit_shift, rfull + s);
-            }
+            const int32_t slot = u & ((1 << a.c.page_shift) - 1);
+            // a page out of range is filled with zeros
+#pragma unroll
+            for (int h = 0; h < (kPacked ? 1 : kHalves); ++h)
+              tma_4d(dst + h * 16384 + (lane << unit_shift) * (kPacked ? F::kRawRow : 128), map, h * 64, slot, head,
+                     page < 0 ? a.c.num_pages : page, bar);
           }
+        };
+        if constexpr (kPacked) {
+          const int s = at % F::kRawStages;
+          wait(rempty + s, at / F::kRawStages + 1);
+          if (!ok) break;
+          const uint32_t dst = raw_a + s * F::kRaw;
+          if (lane == 0) mbar_arrive_expect_tx(rfull + s, 2 * kTile * F::kRawRow);
+          __syncwarp();
+          copies(&tm_k, dst, rfull + s);
+          copies(&tm_v, dst + kTile * F::kRawRow, rfull + s);
+          // the (s, m) pairs, four slots per lane (a bulk copy per page and
+          // array is too small to be worth one: 256 bytes for 64 slots)
+          const int32_t p = __shfl_sync(0xffffffffu, page, (4 * lane) >> unit_shift);
+          const int32_t slot = (j0 + 4 * lane) & ((1 << a.c.page_shift) - 1);
+          const int64_t off = max(p, 0) * a.c.s_page_stride + head * a.c.s_head_stride + slot * 4;
+          const uint32_t to = dst + 2 * kTile * F::kRawRow + lane * 16;
+          async_load16(to, a.c.ks + off, p >= 0);
+          async_load16(to + kTile * 4, a.c.vs + off, p >= 0);
+          async_arrive(rfull + s);
         } else {
-          if (lane == 0) *reinterpret_cast<volatile uint32_t*>(info + at % kInfo) = there;
-          const int32_t pg = page < 0 ? a.c.num_pages : page;
           const int ks = at % kKs, vs = at % kVs;
-          k_tiles += issue(&tm_k, ring + ks * F::kStage, kfull + ks, kempty + ks, at / kKs, pg, slot, it.head);
-          v_tiles += issue(&tm_v, vring + vs * F::kStage, vfull + vs, vempty + vs, at / kVs, pg, slot, it.head);
+          wait(kempty + ks, at / kKs + 1);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(kfull + ks, F::kStage);
+          __syncwarp();
+          copies(&tm_k, ring_a + ks * F::kStage, kfull + ks);
+          ++k_tiles;
+          wait(vempty + vs, at / kVs + 1);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(vfull + vs, F::kStage);
+          __syncwarp();
+          copies(&tm_v, vring_a + vs * F::kStage, vfull + vs);
+          ++v_tiles;
         }
       }
       __syncwarp();
