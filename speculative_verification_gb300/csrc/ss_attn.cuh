@@ -120,7 +120,12 @@ struct Cfg {
   static constexpr int kNS = kPacked ? 2 * kLive : kN;
   static constexpr int kGroups = kLive <= 16 ? 1 : kLive == 32 ? 2 : kPacked ? 2 : 4;  // softmax warpgroups
   static constexpr int kCols = kLive / kGroups;              // rows per softmax thread
-  static constexpr int kSoft = 128 * kGroups;
+  // 4 bits, few rows: two warpgroups take turns at the tiles, each with a sum
+  // and an accumulator of its own, joined at the item's end.  What a tile asks
+  // of one is mostly latency then (1300 clocks, where copying it takes 750).
+  static constexpr int kStreams = kPacked && kLive <= 16 ? 2 : 1;
+  static constexpr int kSoft = 128 * kGroups * kStreams;
+  static constexpr int kPerTile = kSoft / kStreams;          // softmax threads of one tile
   // 4 bits: one warpgroup unpacks K; V, twice the work, has two that take turns
   // where the softmax leaves the registers
   static constexpr int kVGroups = kLive <= 16 ? 2 : 1;
@@ -128,12 +133,12 @@ struct Cfg {
   static constexpr int kThreads = 128 + kSoft + kUnpack;
   // Registers per thread by warpgroup where one size does not fit all: the
   // launch's kThreads x kRegs are shared out again (all or none of them).
-  static constexpr int kRegs = kThreads > 512 ? 96 : kThreads > 384 ? 128 : 168;
+  static constexpr int kRegs = kThreads > 640 ? 80 : kThreads > 512 ? 96 : kThreads > 384 ? 128 : 168;
   static constexpr bool kSplit = kPacked || kLive == 128;
-  static constexpr int kRegs0 = 64;                                   // copies, MMAs, queries
-  static constexpr int kRegsSoft = !kPacked ? 104 : kLive >= 64 ? 152 : 136;
+  static constexpr int kRegs0 = kStreams == 2 ? 56 : 64;                                   // copies, MMAs, queries
+  static constexpr int kRegsSoft = !kPacked || kStreams == 2 ? 104 : kLive >= 64 ? 152 : 136;
   static constexpr int kRegsUnpack = kLive >= 64 ? 56 : 72;
-  static_assert(!kSplit || kRegs0 + kGroups * kRegsSoft + kUnpack / 128 * kRegsUnpack <= kThreads / 128 * kRegs,
+  static_assert(!kSplit || kRegs0 + kSoft / 128 * kRegsSoft + kUnpack / 128 * kRegsUnpack <= kThreads / 128 * kRegs,
                 "a warpgroup would wait for registers for ever");
   static constexpr int kStage = kHalves * 16384;             // 128 keys x 64 channels x 2 bytes per half
   static constexpr int kQ = kPacked ? kNS * 128 : kHalves * kN * 128;
@@ -146,7 +151,7 @@ struct Cfg {
   static constexpr int kRaw = kPacked ? 2 * kTile * kRawRow + 2 * kTile * 4 : 0;
   static constexpr int kRawStages = kPacked ? 4 : 1;
   // the static arrays, rounded up
-  static constexpr int kMeta = kNQ * (static_cast<int>(sizeof(Item)) + kN * 32 + 64 + 512) + kN * 36 + 1536 +
+  static constexpr int kMeta = kNQ * (static_cast<int>(sizeof(Item)) + kN * 32 + 64 + 512) + kStreams * kN * 36 + 1536 +
                                (kPacked ? 2 * kPairs * kTile * 4 : 0);
   static constexpr int kBudget = 232448 - 1024 - kQBufs * kQ - kPBufs * kP - kRawStages * kRaw - kMeta;
   // K and V have a ring each, so that whoever waits for a slot has used the
@@ -157,7 +162,7 @@ struct Cfg {
   static constexpr int kKs = kPacked ? 2 : kRing / 2, kVs = kPacked ? kRing : kRing - kKs;
   static constexpr int kSmem = 1024 + kRing * kStage + kQBufs * kQ + kPBufs * kP + kRawStages * kRaw;
   // tensor-memory columns: S x 2, O x 2, and for 4 bits K x 2 (four channels per column)
-  static constexpr uint32_t kOCol = 2 * kNS, kKCol = kOCol + 2 * kN;
+  static constexpr uint32_t kOCol = 2 * kNS, kKCol = kOCol + 2 * kStreams * kN;
   static constexpr uint32_t kKCols = kPacked ? 16 * kHalves : 0;
   static constexpr uint32_t kUsed = kKCol + 2 * kKCols;
   static constexpr uint32_t kTmem = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
@@ -255,37 +260,41 @@ __device__ __forceinline__ constexpr uint32_t instr_desc_e4m3() {
   return (1u << 4) | (static_cast<uint32_t>(kN >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
 }
 
-// `leader` is 1 in the one lane that issues.
-__device__ __forceinline__ void umma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate,
-                                     uint32_t leader) {
+// True in one lane of the warp.  Inside `if (elect_one())` the compiler knows
+// that one lane runs and keeps descriptors in uniform registers: 6 instructions
+// per MMA, where a test of the lane number takes 14.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t is;
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(is));
+  return is != 0;
+}
+
+__device__ __forceinline__ void umma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "setp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 
 // e4m3, A in tensor memory: lane m holds row m, four channels per column.
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate,
-                                        uint32_t leader) {
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
+      "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "setp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 
-__device__ __forceinline__ void umma_commit(uint64_t* bar, uint32_t leader) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\t"
-      "setp.ne.b32 q, %1, 0;\n\t"
-      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar)),
-      "r"(leader)
-      : "memory");
+__device__ __forceinline__ void umma_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+               : "memory");
 }
 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -304,6 +313,14 @@ __device__ __forceinline__ void tmem_get(uint32_t t, float (&v)[16]) {
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(t)
       : "memory");
+}
+__device__ __forceinline__ void tmem_get(uint32_t t, float (&v)[4]) {
+  __syncwarp();
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(t)
+               : "memory");
 }
 __device__ __forceinline__ void tmem_get(uint32_t t, float (&v)[8]) {
   __syncwarp();
@@ -537,8 +554,9 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
   __shared__ uint64_t node_sees[kNQ][SS_TREE_MAX_NODES];
   __shared__ uint32_t info[kInfo];
   __shared__ uint32_t k_pair[kPacked ? kPairs : 1][kPacked ? kTile : 1], v_pair[kPacked ? kPairs : 1][kPacked ? kTile : 1];
-  __shared__ __align__(16) float nref[kN], corr[kN], shift[kN], sums[kN], csums[kN];
-  __shared__ float part[4][kN];
+  constexpr int kRows = F::kStreams * kN;  // of the softmax's state
+  __shared__ __align__(16) float nref[kRows], corr[kRows], shift[kRows], sums[kRows], csums[kRows];
+  __shared__ float part[4][kRows];
   __shared__ uint32_t tmem_slot;
   __shared__ int32_t s_dead, s_last, s_r0, s_r1, s_before, s_tiles0, s_scan[32];
 
@@ -561,8 +579,8 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(sfull + i, 1);
-      mbar_init(sempty + i, F::kSoft);
-      mbar_init(pfull + i, F::kSoft);
+      mbar_init(sempty + i, F::kPerTile);
+      mbar_init(pfull + i, F::kPerTile);
       mbar_init(pdone + i, 1);
       mbar_init(oempty + i, F::kSoft);
     }
@@ -673,7 +691,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
     // ---------------------------------------------------- tensor copies --
     const int32_t unit_shift = min(a.c.page_shift, 7), units = kTile >> unit_shift;
     const int32_t tiles_all = __shfl_sync(0xffffffffu, my_tiles, 0);
-    const uint32_t ring_a = __shfl_sync(0xffffffffu, smem_addr(ring), 0);
+    const uint32_t ring_a = smem_addr(ring);
     const uint32_t vring_a = ring_a + (kPacked ? 0 : kKs) * F::kStage;
     const uint32_t raw_a = ring_a + kRing * F::kStage + F::kPBufs * F::kP + F::kQBufs * F::kQ;
     int32_t at = 0, k = 0;  // tile, item
@@ -789,10 +807,9 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
     // its warp waits that long to issue the next; the second product has a warp
     // of its own, so that one's waits pass under the other's MMAs.
     constexpr uint32_t kHi = desc_hi(1024, 2);
-    const uint32_t leader = lane == 0;
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     const int32_t tiles_all = __shfl_sync(0xffffffffu, my_tiles, 0);
-    const uint32_t ring_a = __shfl_sync(0xffffffffu, smem_addr(ring), 0);
+    const uint32_t ring_a = smem_addr(ring);
     const uint32_t q_a = ring_a + kRing * F::kStage + F::kPBufs * F::kP;
     const int k_steps = kPacked ? (a.c.dim + 31) / 32 : (a.c.dim + 15) / 16;
     bool ok = true;
@@ -815,36 +832,38 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
         wait(sempty + b, (at >> 1) + 1);
         if (!ok) break;
         tc_fence_after();
-        if constexpr (kPacked) {
+        if (elect_one()) {
+          if constexpr (kPacked) {
 #pragma unroll
-          for (int kk = 0; kk < 2 * kHalves; ++kk)
-            if (kk < k_steps)
-              umma_ts(tm + b * kNS, tm + F::kKCol + s * F::kKCols + kk * 8, desc(qa + kk * 2, kHi), instr_desc_e4m3<kNS>(),
-                      kk > 0 ? 1u : 0u, leader);
-        } else {
-          const uint32_t ka = desc_lo(ring_a + s * F::kStage, 16);
+            for (int kk = 0; kk < 2 * kHalves; ++kk)
+              if (kk < k_steps)
+                umma_ts(tm + b * kNS, tm + F::kKCol + s * F::kKCols + kk * 8, desc(qa + kk * 2, kHi), instr_desc_e4m3<kNS>(),
+                        kk > 0 ? 1u : 0u);
+          } else {
+            const uint32_t ka = desc_lo(ring_a + s * F::kStage, 16);
 #pragma unroll
-          for (int kk = 0; kk < 4 * kHalves; ++kk)
-            if (kk < k_steps)
-              umma(tm + b * kNS, desc(ka + (kk >> 2) * (16384 >> 4) + (kk & 3) * 2, kHi),
-                   desc(qa + (kk >> 2) * (kN * 128 >> 4) + (kk & 3) * 2, kHi), instr_desc<kN>(false), kk > 0 ? 1u : 0u, leader);
+            for (int kk = 0; kk < 4 * kHalves; ++kk)
+              if (kk < k_steps)
+                umma(tm + b * kNS, desc(ka + (kk >> 2) * (16384 >> 4) + (kk & 3) * 2, kHi),
+                     desc(qa + (kk >> 2) * (kN * 128 >> 4) + (kk & 3) * 2, kHi), instr_desc<kN>(false), kk > 0 ? 1u : 0u);
+          }
+          umma_commit(kempty + s);
+          umma_commit(sfull + b);
+          if (t == tiles - 1) umma_commit(qfree + k % F::kQBufs);  // the queries are read
         }
-        umma_commit(kempty + s, leader);
-        umma_commit(sfull + b, leader);
+        __syncwarp();
       }
-      umma_commit(qfree + k % F::kQBufs, leader);  // the queries are read
     }
     if (!ok && lane == 0) {  // given up: the MMAs in flight end before tensor memory is freed
-      umma_commit(&drain[0], 1);
+      umma_commit(&drain[0]);
       mbar_wait_bounded(&drain[0], 0, 1u << 16);
     }
   } else if (warp == 2) {
     // ---------------------------------------- second product, O^T += V^T P^T --
     constexpr uint32_t kHiV = desc_hi(1024, 2), kHiP = desc_hi(8 * F::kPitch, kN >= 64 ? 2u : kN == 32 ? 4u : 6u);
-    const uint32_t leader = lane == 0;
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     const int32_t tiles_all = __shfl_sync(0xffffffffu, my_tiles, 0);
-    const uint32_t ring_a = __shfl_sync(0xffffffffu, smem_addr(ring), 0);
+    const uint32_t ring_a = smem_addr(ring);
     const uint32_t p_a = ring_a + kRing * F::kStage, v_a = ring_a + (kPacked ? 0 : kKs) * F::kStage;
     bool ok = true;
     const auto wait = [&](uint64_t* bar, int32_t use) {
@@ -858,7 +877,6 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
       if (!ok) break;
       const int32_t tiles = __shfl_sync(0xffffffffu, items[qb].tiles, 0);
       wait(oempty + (k & 1), (k >> 1) + 1);
-      const uint32_t d = tm + F::kOCol + (k & 1) * kN;
 #pragma unroll 1
       for (int32_t t = 0; t < tiles; ++t, ++at) {
         const int b = at & 1;
@@ -867,18 +885,22 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
         wait(pfull + b, at >> 1);
         if (!ok) break;
         tc_fence_after();
+        const uint32_t d = tm + F::kOCol + ((k & 1) * F::kStreams + (F::kStreams == 2 ? b : 0)) * kN;
         const uint32_t va = desc_lo(v_a + s * F::kStage, kHalves == 2 ? 16384 : 0);
         const uint32_t pa = desc_lo(p_a + b % F::kPBufs * F::kP, kTile * 128);
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < kTile / 16; ++kk)
-          umma(d, desc(va + kk * (16 * 128 >> 4), kHiV), desc(pa + kk * (16 * F::kPitch >> 4), kHiP), instr_desc<kN>(true),
-               (t > 0 || kk > 0) ? 1u : 0u, leader);
-        umma_commit(vempty + s, leader);
-        umma_commit(pdone + b, leader);
+          for (int kk = 0; kk < kTile / 16; ++kk)
+            umma(d, desc(va + kk * (16 * 128 >> 4), kHiV), desc(pa + kk * (16 * F::kPitch >> 4), kHiP), instr_desc<kN>(true),
+                 (t >= F::kStreams || kk > 0) ? 1u : 0u);
+          umma_commit(vempty + s);
+          umma_commit(pdone + b);
+        }
+        __syncwarp();
       }
     }
     if (!ok && lane == 0) {
-      umma_commit(&drain[1], 1);
+      umma_commit(&drain[1]);
       mbar_wait_bounded(&drain[1], 0, 1u << 16);
     }
   } else if (warp == 3) {
@@ -1103,7 +1125,9 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
     if constexpr (F::kSplit) regs_more<F::kRegsSoft>();
     // ---------------------------------------------------------- softmax --
     const int st = tid - 128, wg = st >> 7, lt = st & 127, wq = warp & 3;
-    const int c0 = wg * kCols;                                    // this warpgroup's rows
+    const int stream = F::kStreams == 2 ? wg : 0;
+    const int c0 = F::kStreams == 2 ? 0 : wg * kCols;             // this warpgroup's rows
+    const int h0 = stream * kN + c0;                              // their state
     const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;  // this warp's tensor-memory lanes
     const int bar = 1 + wg;                                       // its barrier
     const int32_t unit_shift = min(a.c.page_shift, 7);
@@ -1112,9 +1136,9 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
     // two channels per store where the rows of out allow it
     const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 3) == 0 && ((a.out_token | a.out_head) & 1) == 0;
     constexpr uint32_t kSwz = kN >= 64 ? 0x70u : kN == 32 ? 0x30u : 0x10u;  // P's swizzle
-    int32_t at = 0;
+    int32_t done = 0;  // tiles of the items before
     uint32_t uses[2] = {0, 0};  // of written
-    for (int32_t k = 0; at < my_tiles; ++k) {
+    for (int32_t k = 0; done < my_tiles; ++k) {
       const int b = k % kNQ;
       const bool in = wait_or_dead(qfull + b, (k / kNQ) & 1, dead);
       if (bar_any(5, F::kSoft, !in)) break;  // the same decision for every softmax thread
@@ -1125,14 +1149,15 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
       if (kPacked)
 #pragma unroll
         for (int n = 0; n < kCols; ++n) cs[n] = 0.0f;
-      if (lt < kCols) nref[c0 + lt] = 0.0f;
+      if (lt < kCols) nref[h0 + lt] = 0.0f;
       bool unset = true;  // thread i of the warpgroup: row i has seen no key yet
       bool fresh = true;  // some row has not
-      const uint32_t o_base = tmem + F::kOCol + (k & 1) * kN + c0 + lanes;
+      const uint32_t o_item = tmem + F::kOCol + (k & 1) * F::kStreams * kN + lanes, o_base = o_item + h0;
       const int32_t first_pos = it.base + (tree ? 0 : token_of(a, it.row0));
       const int32_t last_pos = it.base + token_of(a, it.row0 + it.rows - 1);  // of a tree: at most
 #pragma unroll 1
-      for (int32_t t = 0; t < it.tiles; ++t, ++at) {
+      for (int32_t t = F::kStreams == 2 ? (done ^ stream) & 1 : 0; t < it.tiles; t += F::kStreams) {
+        const int32_t at = done + t;
         const int sb = at & 1;
         const int32_t n = it.tile0 + t;
         const bool sink = n < it.nsink;
@@ -1233,7 +1258,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
         mbar_arrive(sempty + sb);
 #pragma unroll
         for (int i = 0; i < kCols; i += 4) {
-          const float4 r4 = *reinterpret_cast<const float4*>(nref + c0 + i);
+          const float4 r4 = *reinterpret_cast<const float4*>(nref + h0 + i);
           float y[4] = {r4.x, r4.y, r4.z, r4.w};
           if (kPacked) {
             const float4 q4 = *reinterpret_cast<const float4*>(&row_qsum[b][c0 + i]);
@@ -1267,11 +1292,11 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
 #pragma unroll
           for (int i = 0; i < kCols; ++i) {
             const float m = warp_max(x[i]);  // a NaN counts as nothing
-            if (lane == i) part[wq][c0 + i] = m;
+            if (lane == i) part[wq][h0 + i] = m;
           }
           bar_sync(bar, 128);
           if (lt < kCols) {
-            const int c = c0 + lt;
+            const int c = h0 + lt;
             const float m = fmaxf(fmaxf(part[0][c], part[1][c]), fmaxf(part[2][c], part[3][c]));
             const bool move = m > (unset ? -INFINITY : kSlack);
             corr[c] = !move ? 1.0f : unset ? 0.0f : ex2(-m);  // 2^(old reference - new)
@@ -1284,21 +1309,22 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
           bool change = false;
 #pragma unroll
           for (int i = 0; i < kCols; ++i) {
-            const float g = corr[c0 + i];
+            const float g = corr[h0 + i];
             change |= g != 1.0f;
             l[i] *= g;
             if (kPacked) cs[i] *= g;
-            x[i] -= shift[c0 + i];
+            x[i] -= shift[h0 + i];
           }
-          if (change && t > 0) {
-            wait_or_dead(pdone + ((at - 1) & 1), ((at - 1) >> 1) & 1, dead);
+          if (change && t >= F::kStreams) {
+            // the accumulator's last tile (of two streams: waited for above)
+            if (F::kStreams == 1) wait_or_dead(pdone + ((at - 1) & 1), ((at - 1) >> 1) & 1, dead);
             tc_fence_after();
 #pragma unroll 1
             for (int i0 = 0; i0 < kCols; i0 += 8) {
               float o[8];
               tmem_ld(o_base + i0, o);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) o[i] *= corr[c0 + i0 + i];
+              for (int i = 0; i < 8; ++i) o[i] *= corr[h0 + i0 + i];
               tmem_st(o_base + i0, o);
             }
           }
@@ -1348,55 +1374,94 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
         mbar_arrive(pfull + sb);
       }
       // ---- the item's end: sums over the keys, then the rows
-      wait_or_dead(pdone + ((at - 1) & 1), ((at - 1) >> 1) & 1, dead);
+      done += it.tiles;
+      const int32_t mine = F::kStreams == 2 ? done - 1 - ((done - 1 - stream) & 1) : done - 1;  // this stream's last tile
+      const bool any = mine >= done - it.tiles;
+      if (any) wait_or_dead(pdone + (mine & 1), (mine >> 1) & 1, dead);
       tc_fence_after();
-      {
-        const float s = warp_sums<kCols>(l);
-        if (lane < kCols) part[wq][c0 + lane] = s;
-      }
-      bar_sync(bar, 128);
-      float sum = 0.0f;  // thread i: row i's
-      if (lt < kCols) {
-        sum = (part[0][c0 + lt] + part[1][c0 + lt]) + (part[2][c0 + lt] + part[3][c0 + lt]);
-        sums[c0 + lt] = sum == 0.0f ? 0.0f : __fdividef(1.0f, sum);
-      }
+      const auto over_keys = [&](auto& v) {  // thread i: the sum of row i over the warpgroup's keys
+        const float w = warp_sums<kCols>(v);
+        if (lane < kCols) part[wq][h0 + lane] = w;
+        bar_sync(bar, 128);
+        return lt < kCols ? (part[0][h0 + lt] + part[1][h0 + lt]) + (part[2][h0 + lt] + part[3][h0 + lt]) : 0.0f;
+      };
+      float sum = over_keys(l), csum = 0.0f;
       if constexpr (kPacked) {
         bar_sync(bar, 128);
-        const float s = warp_sums<kCols>(cs);
-        if (lane < kCols) part[wq][c0 + lane] = s;
-        bar_sync(bar, 128);
-        if (lt < kCols) csums[c0 + lt] = (part[0][c0 + lt] + part[1][c0 + lt]) + (part[2][c0 + lt] + part[3][c0 + lt]);
+        csum = over_keys(cs);
       }
-      bar_sync(bar, 128);
       const int32_t rows = it.rows;            // live rows
       const int ch = wq * 32 + lane;           // this lane's channel
       const bool whole = it.tiles == it.all;
       float* piece = a.pieces + (static_cast<int64_t>(blockIdx.x) * 2 + it.piece) * kSlotFloats;
-      if (wq * 32 < kHalves * 64 && c0 < rows) {
-        float o[kCols];
-        tmem_ld(o_base, o);
+      if constexpr (F::kStreams == 1) {
+        if (lt < kCols) {
+          sums[c0 + lt] = !whole ? 1.0f : sum == 0.0f ? 0.0f : __fdividef(1.0f, sum);
+          csums[c0 + lt] = csum * sums[c0 + lt];
+        }
+        bar_sync(bar, 128);
+      } else {
+        // both streams' sums at the larger reference; a stream that saw nothing
+        // of a row has sum 0 there (or NaN from a NaN score, which stays)
+        if (lt < kCols) {
+          part[0][h0 + lt] = unset ? kUnset : nref[h0 + lt];
+          part[1][h0 + lt] = sum;
+          part[2][h0 + lt] = csum;
+        }
+        tc_fence_before();  // each warpgroup reads both accumulators
+        bar_sync(5, F::kSoft);
+        tc_fence_after();
+        if (st < kCols) {
+          const float n0 = part[0][st], n1 = part[0][kN + st], s0 = part[1][st], s1 = part[1][kN + st];
+          const float top = fminf(n0, n1);
+          const float g0 = n0 == kUnset ? (s0 == 0.0f ? 0.0f : 1.0f) : ex2(top - n0);
+          const float g1 = n1 == kUnset ? (s1 == 0.0f ? 0.0f : 1.0f) : ex2(top - n1);
+          sum = __fmaf_rn(g0, s0, g1 * s1);
+          const float inv = !whole ? 1.0f : sum == 0.0f ? 0.0f : __fdividef(1.0f, sum);
+          nref[st] = top;
+          sums[st] = g0 * inv;
+          sums[kN + st] = g1 * inv;
+          csums[st] = __fmaf_rn(g0, part[2][st], g1 * part[2][kN + st]) * inv;
+          unset = top == kUnset;
+        }
+        bar_sync(5, F::kSoft);
+      }
+      // this warpgroup's rows of the result, scaled
+      constexpr int kOut = kCols / F::kStreams;
+      const int r0 = F::kStreams == 2 ? wg * kOut : c0;
+      if (wq * 32 < kHalves * 64 && r0 < rows) {
+        float o[kOut];
+        tmem_ld(o_item + r0, o);
+#pragma unroll
+        for (int i = 0; i < kOut; ++i) o[i] = F::kStreams == 2 && sums[r0 + i] == 0.0f ? 0.0f : o[i] * sums[r0 + i];
+        if constexpr (F::kStreams == 2) {
+          float o1[kOut];
+          tmem_ld(o_item + kN + r0, o1);
+#pragma unroll
+          for (int i = 0; i < kOut; ++i)
+            if (sums[kN + r0 + i] != 0.0f) o[i] = __fmaf_rn(o1[i], sums[kN + r0 + i], o[i]);
+        }
+        if (kPacked)
+#pragma unroll
+          for (int i = 0; i < kOut; ++i) o[i] += csums[r0 + i];
         if (whole) {
           // even lanes take two channels of the even row, odd lanes of the odd one
           const bool odd = lane & 1;
           const bool in = (ch & ~1) < a.c.dim;
 #pragma unroll
-          for (int i = 0; i < kCols; i += 2) {
-            const int c = c0 + i + odd;
-            float2 y = make_float2(o[i], o[i + 1]);
-            if (kPacked) y = make_float2(y.x + csums[c0 + i], y.y + csums[c0 + i + 1]);
-            y.x *= sums[c0 + i];
-            y.y *= sums[c0 + i + 1];
-            const float other = __shfl_xor_sync(0xffffffffu, odd ? y.x : y.y, 1);
-            const uint32_t pair = odd ? bf16_pair(other, y.y) : bf16_pair(y.x, other);
+          for (int i = 0; i < kOut; i += 2) {
+            const int c = r0 + i + odd;
+            const float other = __shfl_xor_sync(0xffffffffu, odd ? o[i] : o[i + 1], 1);
+            const uint32_t pair = odd ? bf16_pair(other, o[i + 1]) : bf16_pair(o[i], other);
             if (c < rows && in) store_pair(a.out + row_out[b][c] + (ch & ~1), pair, wide);
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < kCols; ++i)
-            if (c0 + i < rows) __stcg(piece + (c0 + i) * 128 + ch, kPacked ? o[i] + csums[c0 + i] : o[i]);
+          for (int i = 0; i < kOut; ++i)
+            if (r0 + i < rows) __stcg(piece + (r0 + i) * 128 + ch, o[i]);
         }
       }
-      if (lt < kCols && c0 + lt < rows) {
+      if (stream == 0 && lt < kCols && c0 + lt < rows) {
         const int c = c0 + lt;
         if (!whole) {
           __stcg(piece + 128 * 128 + 2 * c, unset ? kUnset : nref[c]);
