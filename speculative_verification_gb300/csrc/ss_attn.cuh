@@ -48,6 +48,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "ss.h"
 #include "ss_cache.h"
 #include "ss_ptx.cuh"
@@ -57,6 +59,7 @@ using namespace ss;
 
 constexpr int kTile = 128;                // keys per tile
 constexpr int kMaxCtas = 256;             // the workspace's limit on the grid
+constexpr int kMaxDevices = 64;
 constexpr uint32_t kPolls = 1u << 14;     // bounded waits: polls that each sleep up to kSleepNs
 constexpr uint32_t kSleepNs = 50000;
 constexpr int kInfo = 16;                 // tiles whose page masks are kept
@@ -1634,21 +1637,24 @@ ss_status launch(const AttnArgs& a, cudaStream_t s) {
   const int unit = 1 << (a.c.page_shift < 7 ? a.c.page_shift : 7);
   if (!make_cache_map(&mk, a.c.k, a.c, unit) || !make_cache_map(&mv, a.c.v, a.c, unit)) return SS_ERR_UNSUPPORTED;
   if (!kPacked && !make_query_map(&mq, a, kLive)) return SS_ERR_UNSUPPORTED;
-  int dev = 0, sms = 0;
+  // what does not change from call to call, once per device
+  int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, F::kSmem);
-  if (e == cudaSuccess) {
-    if constexpr (F::kSplit) {  // the shares are of what the launch brings
-      static const int regs = [&] {
-        cudaFuncAttributes at{};
-        return cudaFuncGetAttributes(&at, fn) == cudaSuccess ? at.numRegs : 0;
-      }();
-      if (regs != F::kRegs) return SS_ERR_UNSUPPORTED;
-    }
-    const int grid = sms < kMaxCtas ? sms : kMaxCtas;
-    attn_kernel<kLive, kPacked, kHalves><<<grid, F::kThreads, F::kSmem, s>>>(mk, mv, mq, a);
+  static std::atomic<int> grids[kMaxDevices];
+  int grid = (e == cudaSuccess && dev < kMaxDevices) ? grids[dev].load(std::memory_order_relaxed) : 0;
+  if (e == cudaSuccess && grid == 0) {
+    cudaFuncAttributes at{};
+    int sms = 0;
+    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, F::kSmem);
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, fn);
+    if (e != cudaSuccess) return finish(e);
+    // the warpgroups' shares of registers are of what the launch brings
+    if (F::kSplit && at.numRegs != F::kRegs) return SS_ERR_UNSUPPORTED;
+    grid = sms < kMaxCtas ? sms : kMaxCtas;
+    if (dev < kMaxDevices) grids[dev].store(grid, std::memory_order_relaxed);
   }
+  if (e == cudaSuccess) attn_kernel<kLive, kPacked, kHalves><<<grid, F::kThreads, F::kSmem, s>>>(mk, mv, mq, a);
   return finish(e);
 }
 

@@ -7,6 +7,7 @@ present, the calls raise.
 """
 import ctypes as C
 import os
+import struct
 
 import numpy as np
 
@@ -551,10 +552,45 @@ def ss_tree_verify(target_logits, node_offsets, parents, node_tokens, draft_prob
 def _want(t, name, dtype, shape=None):
     """A device tensor's pointer, after the checks that the C entry cannot
     make: its type, its shape and that it is contiguous."""
-    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or (shape is not None and tuple(t.shape) != shape):
+    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous() or (shape is not None and t.shape != shape):
         raise SSError("%s: want a contiguous %s device tensor%s, got %s %s on %s" %
                       (name, dtype, "" if shape is None else " of shape %s" % (shape,), t.dtype, tuple(t.shape), t.device))
     return t.data_ptr()
+
+
+def _raw_stream(stream):
+    """The CUDA stream handle as an integer."""
+    import torch
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+
+
+def _packer(cls):
+    """struct.Struct with a ctypes structure's layout: packing one is several
+    times quicker than filling the ctypes fields, and these calls are short."""
+    code = {C.c_int32: "i", C.c_int64: "q", C.c_float: "f", C.c_void_p: "Q"}
+    fmt, at = "", 0
+    for name, typ in cls._fields_:
+        gap = getattr(cls, name).offset - at
+        fmt += "%dx" % gap if gap else ""
+        fmt += code.get(typ, "Q")
+        at = getattr(cls, name).offset + C.sizeof(typ)
+    return struct.Struct("=%s%s" % (fmt, "%dx" % (C.sizeof(cls) - at) if C.sizeof(cls) > at else ""))
+
+
+_POOL, _APPEND, _ATTENTION = _packer(ss_page_pool), _packer(ss_append_args), _packer(ss_attention_args)
+_quick = {}
+
+
+def _quick_call(name, argtypes):
+    """The C function with `argtypes` in place of its structure pointers."""
+    fn = _quick.get(name)
+    if fn is None:
+        fn = load()[name]  # a function object of its own
+        fn.argtypes, fn.restype = argtypes, C.c_int
+        _quick[name] = fn
+    return fn
 
 
 class KVCache:
@@ -591,6 +627,7 @@ class KVCache:
             c.scale_layer_stride, c.scale_page_stride, c.scale_head_stride = (_span(k_scale, i) * 2 for i in range(3))
         self.struct = c
         self.ref = C.pointer(c)
+        self.address = C.addressof(c)
 
 
 def _span(t, i):
@@ -631,6 +668,7 @@ class PagePool:
                                    _want(free_pages, "free_pages", torch.int32, (pages,)),
                                    _want(free_count, "free_count", torch.int32, (1,)))
         self.ref = C.pointer(self.struct)
+        self.address = C.addressof(self.struct)
 
 
 def alloc_pool(rows, entries, pages, page_size, device="cuda"):
@@ -641,32 +679,37 @@ def alloc_pool(rows, entries, pages, page_size, device="cuda"):
                     torch.arange(pages - 1, -1, -1, **i32), torch.full((1,), pages, **i32), page_size)
 
 
-def _table(page_table, cache):
-    """ss_page_pool of a bare page table (the calls that only read the table)."""
-    import torch
+def _with_table(packer, page_table, cache):
+    """A buffer for a call's arguments, with the ss_page_pool of a bare page
+    table behind them, and the address of the page table's structure."""
     if isinstance(page_table, PagePool):
-        return page_table.ref
-    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.stride(1) != 1 or not page_table.is_cuda:
+        return C.create_string_buffer(packer.size), page_table.address
+    import torch
+    if page_table.dtype is not torch.int32 or page_table.dim() != 2 or page_table.stride(1) != 1 or not page_table.is_cuda:
         raise SSError("page_table: want a PagePool or a [rows, entries] int32 device tensor with contiguous rows")
     rows, entries = page_table.shape
-    return C.pointer(ss_page_pool(rows, entries, page_table.stride(0) if rows > 1 else entries, page_table.data_ptr(),
-                                  cache.num_pages, cache.page_size))
+    buf = C.create_string_buffer(packer.size + _POOL.size)
+    _POOL.pack_into(buf, packer.size, rows, entries, page_table.stride(0) if rows > 1 else entries,
+                    page_table.data_ptr(), cache.num_pages, cache.page_size, 0, 0, 0)
+    return buf, C.addressof(buf) + packer.size
 
 
-def _rows_args(cache, layer, k, v, page_table, kv_len, status, token_offsets, max_tokens, table_rows):
+def _rows_call(name, cache, layer, k, v, page_table, kv_len, status, token_offsets, max_tokens, table_rows, stream):
     import torch
-    n = kv_len.numel()
-    for t in (k, v):
-        if t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() != 3 or t.shape != k.shape or \
-                t.stride() != k.stride() or t.stride(2) != 1 or tuple(t.shape[1:]) != (cache.num_kv_heads, cache.head_dim):
-            raise SSError("want k and v as [tokens, %d, %d] bf16 device tensors of the same strides with contiguous rows"
-                          % (cache.num_kv_heads, cache.head_dim))
-    i32 = torch.int32
-    return ss_append_args(cache.ref, _table(page_table, cache), layer, n, 1 if max_tokens is None else max_tokens,
-                          k.shape[0], None if token_offsets is None else _want(token_offsets, "token_offsets", i32, (n + 1,)),
-                          None if table_rows is None else _want(table_rows, "table_rows", i32, (n,)),
-                          _want(kv_len, "kv_len", i32), k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1),
-                          _want(status, "status", i32, (n,)))
+    n, i32, shape = kv_len.numel(), torch.int32, k.shape
+    stride = k.stride()
+    if k.dtype is not torch.bfloat16 or v.dtype is not torch.bfloat16 or not k.is_cuda or not v.is_cuda or \
+            len(shape) != 3 or v.shape != shape or v.stride() != stride or stride[2] != 1 or \
+            shape[1] != cache.num_kv_heads or shape[2] != cache.head_dim:
+        raise SSError("want k and v as [tokens, %d, %d] bf16 device tensors of the same strides with contiguous rows"
+                      % (cache.num_kv_heads, cache.head_dim))
+    buf, table = _with_table(_APPEND, page_table, cache)
+    _APPEND.pack_into(buf, 0, cache.address, table, layer, n, 1 if max_tokens is None else max_tokens, shape[0],
+                      0 if token_offsets is None else _want(token_offsets, "token_offsets", i32, (n + 1,)),
+                      0 if table_rows is None else _want(table_rows, "table_rows", i32, (n,)),
+                      _want(kv_len, "kv_len", i32), k.data_ptr(), v.data_ptr(), stride[0], stride[1],
+                      _want(status, "status", i32, (n,)))
+    _check(_quick_call(name, [C.c_char_p, C.c_void_p])(buf, _raw_stream(stream)))
 
 
 def ss_cache_append(cache, layer, k, v, page_table, kv_len, status, *, token_offsets=None, max_tokens=None,
@@ -675,15 +718,15 @@ def ss_cache_append(cache, layer, k, v, page_table, kv_len, status, *, token_off
     one layer into the cache at the slots from kv_len (see include/ss.h).
     page_table: a PagePool or the table alone; token_offsets None: one token
     per request."""
-    a = _rows_args(cache, layer, k, v, page_table, kv_len, status, token_offsets, max_tokens, table_rows)
-    _check(load().ss_cache_append(a, _stream_handle(stream)))
+    _rows_call("ss_cache_append", cache, layer, k, v, page_table, kv_len, status, token_offsets, max_tokens, table_rows,
+               stream)
 
 
 def ss_cache_read(cache, layer, k, v, page_table, kv_len, status, *, token_offsets=None, max_tokens=None,
                   table_rows=None, stream=None):
     """The inverse of ss_cache_append: k and v are written."""
-    a = _rows_args(cache, layer, k, v, page_table, kv_len, status, token_offsets, max_tokens, table_rows)
-    _check(load().ss_cache_read(a, _stream_handle(stream)))
+    _rows_call("ss_cache_read", cache, layer, k, v, page_table, kv_len, status, token_offsets, max_tokens, table_rows,
+               stream)
 
 
 def ss_attention_workspace_size():
@@ -704,24 +747,24 @@ def ss_cache_attention(cache, layer, q, out, page_table, kv_len, workspace, stat
     query_offsets None: one query per request; parents: a draft tree per
     request, as ss_tree_verify takes it; scale None: 1 / sqrt(head dim)."""
     import torch
-    i32 = torch.int32
-    n, total, heads = kv_len.numel(), q.shape[0], q.shape[1]
-    for t in (q, out):
-        if t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() != 3 or t.shape != q.shape or t.stride(2) != 1 or \
-                t.shape[2] != cache.head_dim:
-            raise SSError("want q and out as [tokens, heads, %d] bf16 device tensors with contiguous rows" % cache.head_dim)
-    a = ss_attention_args(cache.ref, _table(page_table, cache), layer, n, heads,
-                          1 if max_queries is None else max_queries, total,
-                          None if query_offsets is None else _want(query_offsets, "query_offsets", i32, (n + 1,)),
-                          None if table_rows is None else _want(table_rows, "table_rows", i32, (n,)),
-                          _want(kv_len, "kv_len", i32),
-                          None if parents is None else _want(parents, "parents", i32, (total,)),
-                          q.data_ptr(), q.stride(0), q.stride(1), out.data_ptr(), out.stride(0), out.stride(1),
-                          None if lse is None else _want(lse, "lse", torch.float32, (total, heads)),
-                          cache.head_dim ** -0.5 if scale is None else scale, window, sinks,
-                          _want(status, "status", i32, (n,)))
-    _check(load().ss_cache_attention(a, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                     _stream_handle(stream)))
+    i32, n, shape = torch.int32, kv_len.numel(), q.shape
+    qs, os_ = q.stride(), out.stride()
+    if q.dtype is not torch.bfloat16 or out.dtype is not torch.bfloat16 or not q.is_cuda or not out.is_cuda or \
+            len(shape) != 3 or out.shape != shape or qs[2] != 1 or os_[2] != 1 or shape[2] != cache.head_dim:
+        raise SSError("want q and out as [tokens, heads, %d] bf16 device tensors with contiguous rows" % cache.head_dim)
+    total, heads = shape[0], shape[1]
+    buf, table = _with_table(_ATTENTION, page_table, cache)
+    _ATTENTION.pack_into(buf, 0, cache.address, table, layer, n, heads, 1 if max_queries is None else max_queries, total,
+                         0 if query_offsets is None else _want(query_offsets, "query_offsets", i32, (n + 1,)),
+                         0 if table_rows is None else _want(table_rows, "table_rows", i32, (n,)),
+                         _want(kv_len, "kv_len", i32),
+                         0 if parents is None else _want(parents, "parents", i32, (total,)),
+                         q.data_ptr(), qs[0], qs[1], out.data_ptr(), os_[0], os_[1],
+                         0 if lse is None else _want(lse, "lse", torch.float32, (total, heads)),
+                         cache.head_dim ** -0.5 if scale is None else scale, window, sinks,
+                         _want(status, "status", i32, (n,)))
+    fn = _quick_call("ss_cache_attention", [C.c_char_p, C.c_void_p, C.c_size_t, C.c_void_p])
+    _check(fn(buf, workspace.data_ptr(), workspace.numel() * workspace.element_size(), _raw_stream(stream)))
 
 
 def ss_pages_reserve(pool, from_len, to_len, status, *, table_rows=None, stream=None):
@@ -730,7 +773,7 @@ def ss_pages_reserve(pool, from_len, to_len, status, *, table_rows=None, stream=
     i32, n = torch.int32, from_len.numel()
     _check(load().ss_pages_reserve(pool.ref, n, None if table_rows is None else _want(table_rows, "table_rows", i32, (n,)),
                                    _want(from_len, "from_len", i32), _want(to_len, "to_len", i32, (n,)),
-                                   _want(status, "status", i32, (n,)), _stream_handle(stream)))
+                                   _want(status, "status", i32, (n,)), _raw_stream(stream)))
 
 
 def ss_pages_fork(pool, cache, parent, child, length, status, *, stream=None):
@@ -740,7 +783,7 @@ def ss_pages_fork(pool, cache, parent, child, length, status, *, stream=None):
     i32, n = torch.int32, parent.numel()
     _check(load().ss_pages_fork(pool.ref, cache.ref, n, _want(parent, "parent", i32), _want(child, "child", i32, (n,)),
                                 _want(length, "length", i32, (n,)), _want(status, "status", i32, (n,)),
-                                _stream_handle(stream)))
+                                _raw_stream(stream)))
 
 
 def ss_pages_compact(pool, cache, kv_len, path, num_accepted, verify_status, new_len, status, *, table_rows=None,
@@ -757,7 +800,7 @@ def ss_pages_compact(pool, cache, kv_len, path, num_accepted, verify_status, new
                                    _want(num_accepted, "num_accepted", i32, (n,)),
                                    None if verify_status is None else _want(verify_status, "verify_status", i32, (n,)),
                                    _want(new_len, "new_len", i32, (n,)), _want(status, "status", i32, (n,)),
-                                   _stream_handle(stream)))
+                                   _raw_stream(stream)))
 
 
 def ss_pages_trim(pool, length, status, *, window=0, sinks=0, table_rows=None, stream=None):
@@ -767,7 +810,7 @@ def ss_pages_trim(pool, length, status, *, window=0, sinks=0, table_rows=None, s
     i32, n = torch.int32, length.numel()
     _check(load().ss_pages_trim(pool.ref, n, None if table_rows is None else _want(table_rows, "table_rows", i32, (n,)),
                                 _want(length, "length", i32), window, sinks, _want(status, "status", i32, (n,)),
-                                _stream_handle(stream)))
+                                _raw_stream(stream)))
 
 
 # ------------------------------------------------------------ workloads --
