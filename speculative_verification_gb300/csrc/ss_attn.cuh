@@ -181,31 +181,40 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
-// A wait that gives up: after kPolls polls, or at once when another wait of
-// the CTA has given up before.  The caller goes on (single-role warps stop);
-// nothing it computes then is used.
-__device__ __forceinline__ bool wait_or_dead(uint64_t* bar, uint32_t parity, volatile int32_t* dead) {
-  if (mbar_try_wait(bar, parity)) return true;  // 41 clocks when complete; with a time limit 116
-#pragma unroll 1
-  for (uint32_t i = 0; i < kPolls; ++i) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(smem_addr(bar)), "r"(parity), "r"(kSleepNs)
-        : "memory");
-    if (done) return true;
-    if (*dead) return false;
-  }
-  *dead = 1;
-  return false;
+// The waits give up after kPolls polls, or at once when another wait of the CTA
+// has given up before (*dead).  The caller goes on (single-role warps stop);
+// nothing it computes then is used.  One block of PTX, small where it is not
+// taken: the code around it is bound by instruction fetch.
+__device__ __forceinline__ bool wait_more(uint32_t bar, uint32_t parity, int32_t* dead) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 n, d;\n\t"
+      "mov.u32 n, %4;\n\t"
+      "poll:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %5;\n\t"
+      "@p bra over;\n\t"
+      "ld.volatile.shared.u32 d, [%3];\n\t"
+      "setp.ne.u32 q, d, 0;\n\t"
+      "@q bra over;\n\t"
+      "sub.u32 n, n, 1;\n\t"
+      "setp.ne.u32 q, n, 0;\n\t"
+      "@q bra poll;\n\t"
+      "st.volatile.shared.u32 [%3], 1;\n\t"
+      "over:\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity), "r"(smem_addr(dead)), "n"(kPolls), "n"(kSleepNs)
+      : "memory");
+  return done != 0;
+}
+__device__ __forceinline__ bool wait_or_dead(uint64_t* bar, uint32_t parity, int32_t* dead) {
+  if (__builtin_expect(mbar_try_wait(bar, parity), 1)) return true;
+  return wait_more(smem_addr(bar), parity, dead);
 }
 
 // Two barriers at once: the polls' latencies overlap.
 __device__ __forceinline__ void wait_both(uint64_t* bar0, uint32_t parity0, uint64_t* bar1, uint32_t parity1,
-                                          volatile int32_t* dead) {
+                                          int32_t* dead) {
   const bool d0 = mbar_try_wait(bar0, parity0), d1 = mbar_try_wait(bar1, parity1);
   if (!d0) wait_or_dead(bar0, parity0, dead);
   if (!d1) wait_or_dead(bar1, parity1, dead);
@@ -569,7 +578,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
   uint8_t* vring = ring + (kPacked ? 0 : kKs) * F::kStage;  // after K's slots
   uint8_t* raw = qbuf + F::kQBufs * F::kQ;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  volatile int32_t* dead = &s_dead;
+  int32_t* dead = &s_dead;
 
   if (tid == 0) {
     for (int i = 0; i < kKs; ++i) {
@@ -1283,10 +1292,10 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
           for (int i = 0; i < kCols; ++i) x[i] = ((vis >> i) & 1u) ? x[i] : -INFINITY;
         bool pass = fresh;
         if (!pass) {
-          float most = x[0];
+          float most[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-          for (int i = 1; i < kCols; ++i) most = fmaxf(most, x[i]);
-          pass = bar_any(bar, 128, most > kSlack);
+          for (int i = 4; i < kCols; ++i) most[i & 3] = fmaxf(most[i & 3], x[i]);
+          pass = bar_any(bar, 128, fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])) > kSlack);
         }
         if (pass) {
           // some row's score passes its reference by too much (or the row
