@@ -30,47 +30,97 @@ struct AppendArgs {
   int32_t* status;
 };
 
+// Row number to token and head (division by multiplication: the multiplier is
+// floor(2^(31+l) / d) + 1, l = ceil(log2 d), after Granlund and Montgomery).
+struct FastDiv {
+  uint32_t d, mul, shift;
+};
+static FastDiv fast_div(uint32_t d) {
+  uint32_t l = 0;
+  while ((1u << l) < d) ++l;
+  return {d, static_cast<uint32_t>((1ull << (31 + l)) / d + 1), l ? l - 1 : 0};
+}
+__device__ __forceinline__ uint32_t divide(uint32_t n, const FastDiv& f) {
+  return f.d == 1 ? n : __umulhi(n, f.mul) >> f.shift;
+}
+
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {  // bf16 pairs; a NaN stays
+  uint32_t r;
+  asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t two(float a, float b) {
+  return static_cast<uint64_t>(__float_as_uint(b)) << 32 | __float_as_uint(a);
+}
+__device__ __forceinline__ uint64_t add_2(uint64_t a, uint64_t b) {
+  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(a) : "l"(b));
+  return a;
+}
+__device__ __forceinline__ uint64_t mul_2(uint64_t a, uint64_t b) {
+  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(a) : "l"(b));
+  return a;
+}
+__device__ __forceinline__ uint64_t fma_2(uint64_t a, uint64_t b, uint64_t c) {
+  asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(a) : "l"(b), "l"(c));
+  return a;
+}
+
 // Eight channels of a row, quantised: the row's low value and step come from
-// the 16 lanes of the row.
+// the 16 lanes of the row, as the pair (min x, min -x), so that one shuffle and
+// one instruction join two lanes.
+//
+// round((x - m) / s) without a division per channel: with y = x - m and
+// q = y * (1 / s), the remainder y - q s is exact in fp32 (q is off by a few
+// units at most and s has 8 bits), and q + (y - q s) / s is the quotient to
+// within 2^-20 of its last place before the one rounding.  A quotient that is
+// no half differs from every half by more than 1.003 times half a unit (y has
+// 24 bits, s has 8), so it is not rounded onto one: adding 1.5 * 2^23 then
+// leaves the integer, ties to even, in the low bits.
 __device__ __forceinline__ uint32_t quantise8(const uint4 x, bool live, uint32_t lanes, uint32_t& pair) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  float f[8];
-  float lo = __int_as_float(0x7f800000), hi = -lo;
-  bool bad = false;
+  uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  const uint32_t mn = min2(min2(w[0], w[1]), min2(w[2], w[3]));
+  const uint32_t mx = max2(max2(w[0], w[1]), max2(w[2], w[3])) ^ 0x80008000u;
+  uint32_t both = min2(__byte_perm(mn, mx, 0x5410), __byte_perm(mn, mx, 0x7632));
+  if (!live) both = 0x7f807f80u;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = bf16_lo(w[i]);
-    f[2 * i + 1] = bf16_hi(w[i]);
-  }
-  if (live) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      lo = fminf(lo, f[i]);
-      hi = fmaxf(hi, f[i]);
-      bad |= !(fabsf(f[i]) <= 3.4e38f);
-    }
-  }
-#pragma unroll
-  for (int o = kRowLanes / 2; o > 0; o >>= 1) {
-    lo = fminf(lo, __shfl_xor_sync(lanes, lo, o, kRowLanes));
-    hi = fmaxf(hi, __shfl_xor_sync(lanes, hi, o, kRowLanes));
-    bad |= __shfl_xor_sync(lanes, static_cast<int>(bad), o, kRowLanes) != 0;
-  }
-  const float range = __fsub_rn(hi, lo);
-  if (bad || !(range <= 3.4e38f)) {
+  for (int o = kRowLanes / 2; o > 0; o >>= 1) both = min2(both, __shfl_xor_sync(lanes, both, o, kRowLanes));
+  float lo = bf16_lo(both);
+  const float range = __fsub_rn(-bf16_hi(both), lo);
+  if (!(range < __int_as_float(0x7f800000))) {  // a NaN, an infinity or too wide
     pair = kNaN2;
     return 0;
   }
   // the smallest bf16 that is not below range / 15: then 15 steps reach the
-  // highest channel
-  const float step = __uint_as_float((__float_as_uint(__fdiv_rn(range, 15.0f)) + 0xffffu) & 0xffff0000u);
-  pair = (__float_as_uint(step) >> 16) | (__float_as_uint(lo) & 0xffff0000u);  // lo is one of the row's bf16
+  // highest channel (the division as above)
+  constexpr float kTiny = 1.0e-28f, kUp = 18446744073709551616.0f;
+  float step = range * (1.0f / 15.0f);
+  step = __fmaf_rn(__fmaf_rn(-step, 15.0f, range), 1.0f / 15.0f, step);
+  if (range < kTiny) step = __fdiv_rn(range, 15.0f);
+  step = __uint_as_float((__float_as_uint(step) + 0xffffu) & 0xffff0000u);
+  pair = (__float_as_uint(step) >> 16) | __float_as_uint(lo);  // lo is one of the row's bf16
   if (step == 0.0f) return 0;
-  uint32_t out = 0;
+  if (range < kTiny) {  // keep 1 / step and the remainders in the normal range: all of it times 2^64
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float q = fminf(rintf(__fdiv_rn(__fsub_rn(f[i], lo), step)), 15.0f);
-    out |= static_cast<uint32_t>(q) << ((i & 1) * 16 + (i >> 1) * 4);
+    for (int i = 0; i < 4; ++i) asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(w[i]) : "r"(0x5f805f80u));
+    lo *= kUp;
+    step *= kUp;
+  }
+  const float inv = __fdividef(1.0f, step);
+  const uint64_t low2 = two(-lo, -lo), inv2 = two(inv, inv), step2 = two(-step, -step);
+  constexpr uint32_t kRound = 0x4b400000u;  // 1.5 * 2^23
+  uint32_t out = 0u - 0x11111111u * kRound;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint64_t y = add_2(two(bf16_lo(w[i]), bf16_hi(w[i])), low2), q = mul_2(y, inv2);
+    const uint64_t t = add_2(fma_2(fma_2(q, step2, y), inv2, q), two(__uint_as_float(kRound), __uint_as_float(kRound)));
+    out += (static_cast<uint32_t>(t) << (4 * i)) + (static_cast<uint32_t>(t >> 32) << (16 + 4 * i));
   }
   return out;
 }
@@ -79,16 +129,20 @@ __device__ __forceinline__ uint4 dequantise8(uint32_t w, uint32_t pair) {
   const float s = bf16_lo(pair), m = bf16_hi(pair);
   uint32_t o[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    o[i] = bf16_pair(__fmaf_rn(static_cast<float>((w >> (4 * i)) & 15u), s, m),
-                     __fmaf_rn(static_cast<float>((w >> (16 + 4 * i)) & 15u), s, m));
+  for (int i = 0; i < 4; ++i)  // 2^23 + n, minus 2^23: no conversion
+    o[i] = bf16_pair(__fmaf_rn(__uint_as_float(((w >> (4 * i)) & 15u) | 0x4b000000u) - 8388608.0f, s, m),
+                     __fmaf_rn(__uint_as_float(((w >> (16 + 4 * i)) & 15u) | 0x4b000000u) - 8388608.0f, s, m));
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// CTA (x, r): rows x * kGroups + group, then a grid's width further, of
-// request r; a row is (K or V, token, head), 16 lanes of 16 bytes (bf16 side).
+constexpr int kRowsEach = 4;  // rows that 16 lanes have in flight
+
+// A row is (token, K or V, head): 16 lanes of 16 bytes on the bf16 side.  16
+// lanes take kRowsEach consecutive rows, most often of one token, whose
+// addresses follow from one another; CTA (x, r) takes kGroups * kRowsEach rows
+// of request r, then a grid's width further.
 template <bool kPacked, bool kRead>
-__global__ void __launch_bounds__(kThreads) rows_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kThreads) rows_kernel(const AppendArgs a, const FastDiv by_token, const FastDiv by_head) {
   const int r = blockIdx.y;
   const int32_t begin = a.offsets ? a.offsets[r] : r;
   const int32_t end = a.offsets ? a.offsets[r + 1] : r + 1;
@@ -100,6 +154,79 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const AppendArgs a) {
     if (blockIdx.x == 0 && threadIdx.x == 0) a.status[r] = SS_ROW_BAD_PARAM;
     return;
   }
+  const int lane = threadIdx.x % kRowLanes, group = threadIdx.x / kRowLanes;
+  const bool live = lane * 8 < a.c.dim;
+  const uint32_t lanes = 0xffffu << (threadIdx.x & 16);
+  const uint32_t total = 2u * static_cast<uint32_t>(n) * static_cast<uint32_t>(a.c.heads);
+  for (uint32_t i0 = (blockIdx.x * kGroups + group) * kRowsEach; i0 < total; i0 += gridDim.x * (kGroups * kRowsEach)) {
+    uint32_t token = divide(i0, by_token), head = i0 - token * by_token.d;
+    bool is_v = head >= by_head.d;
+    if (is_v) head -= by_head.d;
+    int64_t in_flat, in_cell, in_scale;
+    int32_t at;
+    const auto locate = [&] {  // the row of head 0 of this token
+      const int64_t slot = static_cast<int64_t>(base) + token;
+      const int32_t in_page = static_cast<int32_t>(slot) & ((1 << a.c.page_shift) - 1);
+      at = page_of(a.t, a.c, row, slot);
+      in_flat = (begin + static_cast<int64_t>(token)) * a.token_stride + lane * 16;
+      in_cell = max(at, 0) * a.c.page_stride + in_page * a.c.slot_stride + lane * (kPacked ? 4 : 16);
+      if (kPacked) in_scale = max(at, 0) * a.c.s_page_stride + in_page * 4;
+    };
+    locate();
+    uint8_t* flat[kRowsEach];
+    uint8_t* cell[kRowsEach];
+    uint8_t* scale[kRowsEach];
+    int32_t page[kRowsEach];
+    uint4 x[kRowsEach];
+    uint32_t word[kRowsEach], pair[kRowsEach];
+#pragma unroll
+    for (int u = 0; u < kRowsEach; ++u) {
+      flat[u] = (is_v ? a.v : a.k) + in_flat + head * a.head_stride;
+      cell[u] = (is_v ? a.c.v : a.c.k) + in_cell + head * a.c.head_stride;
+      if (kPacked) scale[u] = (is_v ? a.c.vs : a.c.ks) + in_scale + head * a.c.s_head_stride;
+      page[u] = at;
+      if (i0 + u >= total) {
+        flat[u] = nullptr;
+        page[u] = -1;
+      } else if (u + 1 < kRowsEach && ++head == by_head.d) {
+        head = 0;
+        is_v = !is_v;
+        if (!is_v && i0 + u + 1 < total) {
+          ++token;
+          locate();
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kRowsEach; ++u) {
+      x[u] = make_uint4(0u, 0u, 0u, 0u);
+      word[u] = pair[u] = 0;
+      if (!live || page[u] < 0) continue;
+      if (!kRead) {
+        x[u] = *reinterpret_cast<const uint4*>(flat[u]);
+      } else if (kPacked) {
+        word[u] = *reinterpret_cast<const uint32_t*>(cell[u]);
+        pair[u] = *reinterpret_cast<const uint32_t*>(scale[u]);
+      } else {
+        x[u] = *reinterpret_cast<const uint4*>(cell[u]);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kRowsEach; ++u) {
+      if (kRead) {
+        if (live && flat[u])
+          *reinterpret_cast<uint4*>(flat[u]) = kPacked && page[u] >= 0 ? dequantise8(word[u], pair[u]) : x[u];
+      } else if (page[u] >= 0) {  // the same for the row's 16 lanes
+        if (kPacked) {
+          const uint32_t w = quantise8(x[u], live, lanes, pair[u]);
+          if (live) *reinterpret_cast<uint32_t*>(cell[u]) = w;
+          if (lane == 0) *reinterpret_cast<uint32_t*>(scale[u]) = pair[u];
+        } else if (live) {
+          *reinterpret_cast<uint4*>(cell[u]) = x[u];
+        }
+      }
+    }
+  }
   if (blockIdx.x == 0) {  // the status: does every slot have a page?
     int missing = 0;
     const int64_t last = (static_cast<int64_t>(base) + n - 1) >> a.c.page_shift;
@@ -108,46 +235,6 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const AppendArgs a) {
         missing |= e >= a.t.max_pages || row[e] < 0 || row[e] >= a.c.num_pages;
     missing = __syncthreads_or(missing);
     if (threadIdx.x == 0) a.status[r] = missing ? SS_ROW_BAD_INDEX : SS_ROW_OK;
-  }
-  const int lane = threadIdx.x % kRowLanes;
-  const bool live = lane * 8 < a.c.dim;
-  const uint32_t lanes = 0xffffu << (threadIdx.x & 16);
-  const uint32_t per = static_cast<uint32_t>(n) * a.c.heads;  // rows of K, then as many of V
-  const int64_t total = 2 * static_cast<int64_t>(n) * a.c.heads;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kGroups + threadIdx.x / kRowLanes; i < total;
-       i += static_cast<int64_t>(gridDim.x) * kGroups) {
-    const bool is_v = i >= per;
-    const uint32_t j = static_cast<uint32_t>(is_v ? i - per : i);
-    const uint32_t token = j / a.c.heads, head = j - token * a.c.heads;
-    const int64_t slot = static_cast<int64_t>(base) + token;
-    const int32_t page = page_of(a.t, a.c, row, slot);
-    const int32_t in_page = static_cast<int32_t>(slot) & ((1 << a.c.page_shift) - 1);
-    uint8_t* flat = (is_v ? a.v : a.k) + (begin + static_cast<int64_t>(token)) * a.token_stride +
-                    head * a.head_stride + lane * 16;
-    uint8_t* cell = (is_v ? a.c.v : a.c.k) + page * a.c.page_stride + head * a.c.head_stride +
-                    in_page * a.c.slot_stride;
-    uint32_t* scale = kPacked ? reinterpret_cast<uint32_t*>((is_v ? a.c.vs : a.c.ks) + page * a.c.s_page_stride +
-                                                            head * a.c.s_head_stride) + in_page
-                              : nullptr;
-    if (kRead) {
-      uint4 x = make_uint4(0u, 0u, 0u, 0u);
-      if (page >= 0 && live)
-        x = kPacked ? dequantise8(reinterpret_cast<const uint32_t*>(cell)[lane], *scale)
-                    : reinterpret_cast<const uint4*>(cell)[lane];
-      if (live) *reinterpret_cast<uint4*>(flat) = x;
-    } else {
-      if (page < 0) continue;  // the same for the row's 16 lanes
-      uint4 x = make_uint4(0u, 0u, 0u, 0u);
-      if (live) x = *reinterpret_cast<const uint4*>(flat);
-      if (kPacked) {
-        uint32_t pair;
-        const uint32_t w = quantise8(x, live, lanes, pair);
-        if (live) reinterpret_cast<uint32_t*>(cell)[lane] = w;
-        if (lane == 0) *scale = pair;
-      } else if (live) {
-        reinterpret_cast<uint4*>(cell)[lane] = x;
-      }
-    }
   }
 }
 
@@ -175,13 +262,15 @@ static ss_status rows_call(const ss_append_args* args, bool read, cudaStream_t s
   a.head_stride = A.head_stride * 2;
   a.status = A.out_status;
   const int64_t rows = 2ll * a.max_tokens * a.c.heads;
-  const int64_t want = (rows + kGroups - 1) / kGroups;
+  if (rows >= (1ll << 31)) return SS_ERR_UNSUPPORTED;
+  const int64_t each = kGroups * kRowsEach, want = (rows + each - 1) / each;
   const dim3 grid(static_cast<unsigned>(want < 1 ? 1 : want > 4096 ? 4096 : want), A.num_requests);
+  const FastDiv by_token = fast_div(2u * a.c.heads), by_head = fast_div(a.c.heads);
   const bool packed = a.c.format == SS_CACHE_INT4;
-  if (packed && read) rows_kernel<true, true><<<grid, kThreads, 0, s>>>(a);
-  else if (packed) rows_kernel<true, false><<<grid, kThreads, 0, s>>>(a);
-  else if (read) rows_kernel<false, true><<<grid, kThreads, 0, s>>>(a);
-  else rows_kernel<false, false><<<grid, kThreads, 0, s>>>(a);
+  if (packed && read) rows_kernel<true, true><<<grid, kThreads, 0, s>>>(a, by_token, by_head);
+  else if (packed) rows_kernel<true, false><<<grid, kThreads, 0, s>>>(a, by_token, by_head);
+  else if (read) rows_kernel<false, true><<<grid, kThreads, 0, s>>>(a, by_token, by_head);
+  else rows_kernel<false, false><<<grid, kThreads, 0, s>>>(a, by_token, by_head);
   return finish(cudaSuccess);
 }
 
@@ -253,7 +342,7 @@ __global__ void __launch_bounds__(kBook) reserve_kernel(const PoolView p, int32_
       int32_t need = -1;  // invalid
       if (row >= 0 && row < p.num_rows && a >= 0 && a <= b && b <= most) {
         need = 0;
-        const int32_t last = (b + (1 << p.page_shift) - 1) >> p.page_shift;
+        const int32_t last = b > 0 ? ((b - 1) >> p.page_shift) + 1 : 0;
         for (int32_t e = (a >> p.page_shift) + lane; e < last; e += 32) need += is_hole(p, p.table[row * p.stride + e]);
         need = (a < b) ? __reduce_add_sync(0xffffffffu, need) : 0;
       }
@@ -280,7 +369,7 @@ __global__ void __launch_bounds__(kBook) reserve_kernel(const PoolView p, int32_
       int32_t at = s_place[i];
       if (at < 0) continue;
       const int32_t row = rows ? rows[c + i] : c + i, a = from[c + i], b = to[c + i];
-      const int32_t last = (b + (1 << p.page_shift) - 1) >> p.page_shift;
+      const int32_t last = b > 0 ? ((b - 1) >> p.page_shift) + 1 : 0;
       for (int32_t e0 = a >> p.page_shift; e0 < last; e0 += 32) {
         int32_t* cell = p.table + row * p.stride + e0 + lane;
         const bool hole = e0 + lane < last && is_hole(p, *cell);
@@ -378,10 +467,20 @@ __global__ void __launch_bounds__(kThreads) fork_copy_kernel(const PoolView p, c
   const uint8_t* from = (is_v ? c.v : c.k) + layer * c.layer_stride + src * c.page_stride;
   uint8_t* to = (is_v ? c.v : c.k) + layer * c.layer_stride + dst * c.page_stride;
   const int32_t per_head = slots * chunks, total = per_head * c.heads;
-  for (int32_t x = threadIdx.x; x < total; x += kThreads) {
-    const int32_t head = x / per_head, y = x - head * per_head, slot = y / chunks, chunk = y - slot * chunks;
-    const int64_t at = head * c.head_stride + slot * c.slot_stride + chunk * 16;
-    *reinterpret_cast<uint4*>(to + at) = *reinterpret_cast<const uint4*>(from + at);
+  for (int32_t x0 = threadIdx.x; x0 < total; x0 += 4 * kThreads) {
+    int64_t at[4];
+    uint4 v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int32_t x = x0 + u * kThreads;
+      if (x >= total) continue;
+      const int32_t head = x / per_head, y = x - head * per_head, slot = y / chunks, chunk = y - slot * chunks;
+      at[u] = head * c.head_stride + slot * c.slot_stride + chunk * 16;
+      v[u] = *reinterpret_cast<const uint4*>(from + at[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (x0 + u * kThreads < total) *reinterpret_cast<uint4*>(to + at[u]) = v[u];
   }
   if (c.format == SS_CACHE_INT4) {
     const uint8_t* sf = (is_v ? c.vs : c.ks) + layer * c.s_layer_stride + src * c.s_page_stride;
@@ -452,8 +551,15 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactArgs a) 
     for (int32_t x = threadIdx.x; x < 2 * per; x += kThreads) {
       const int32_t y = x < per ? x : x - per, head = y / chunks, chunk = y - head * chunks;
       uint8_t* at = (x < per ? c.k : c.v) + layer * c.layer_stride + head * c.head_stride + chunk * 16;
-      for (int32_t j = 0; j < m; ++j)
-        if (s_from[j] >= 0) *reinterpret_cast<uint4*>(at + s_to[j]) = *reinterpret_cast<const uint4*>(at + s_from[j]);
+      for (int32_t j8 = 0; j8 < m; j8 += 8) {  // read, then written: no later source lies before these places
+        uint4 v[8];
+#pragma unroll
+        for (int32_t u = 0; u < 8; ++u)
+          if (j8 + u < m && s_from[j8 + u] >= 0) v[u] = *reinterpret_cast<const uint4*>(at + s_from[j8 + u]);
+#pragma unroll
+        for (int32_t u = 0; u < 8; ++u)
+          if (j8 + u < m && s_from[j8 + u] >= 0) *reinterpret_cast<uint4*>(at + s_to[j8 + u]) = v[u];
+      }
     }
     if (c.format == SS_CACHE_INT4)
       for (int32_t x = threadIdx.x; x < 2 * c.heads; x += kThreads) {
@@ -464,6 +570,76 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactArgs a) 
             *reinterpret_cast<uint32_t*>(at + s_sto[j]) = *reinterpret_cast<const uint32_t*>(at + s_sfrom[j]);
       }
   }
+}
+
+// The usual sizes, up to kBook * kFew entries in all: the four passes of
+// trim_kernel with the entries in registers, thread t holding consecutive ones
+// from the last entry of the last request on.  64 rows of 96 entries take
+// 10.3 us instead of 12.7, 80 rows of 33 take 7.1 instead of 12.
+constexpr int kFew = 8;
+__device__ void trim_few(const PoolView& p, int32_t n, const int32_t* rows, const int32_t* length, int32_t window,
+                         int32_t sinks, int32_t* status) {
+  __shared__ int32_t ws[kBook / 32];
+  const int32_t t = threadIdx.x, have = free_now(p), total = n * p.max_pages;
+  const int32_t per = (total + kBook - 1) / kBook, size = 1 << p.page_shift;
+  for (int32_t i = t; i < n; i += kBook) {
+    const int32_t row = rows ? rows[i] : i;
+    status[i] = row < 0 || row >= p.num_rows || length[i] < 0 ? SS_ROW_BAD_PARAM : SS_ROW_OK;
+  }
+  int32_t page[kFew];
+  int32_t* cell[kFew];
+#pragma unroll
+  for (int u = 0; u < kFew; ++u) {
+    page[u] = -1;
+    const int32_t lin = total - 1 - (t * per + u);
+    if (u >= per || lin < 0) continue;
+    const int32_t i = lin / p.max_pages, e = lin - i * p.max_pages;
+    const int32_t row = rows ? rows[i] : i;
+    const int64_t len = length[i], first = static_cast<int64_t>(e) << p.page_shift;
+    if (row < 0 || row >= p.num_rows || len < 0) continue;
+    if (first < len && (first < sinks || window == 0 || first + size > len - window)) continue;  // kept
+    cell[u] = p.table + row * p.stride + e;
+    page[u] = *cell[u];
+  }
+  __syncthreads();  // the statuses are there
+#pragma unroll
+  for (int u = 0; u < kFew; ++u) {
+    if (u >= per || page[u] < 0) continue;
+    *cell[u] = -1;
+    bool bad = page[u] >= p.num_pages;
+    if (!bad && atomicSub(p.refs + page[u], 1) <= 0) {
+      atomicAdd(p.refs + page[u], 1);
+      bad = true;
+    }
+    if (bad) {
+      status[(total - 1 - (t * per + u)) / p.max_pages] = SS_ROW_BAD_INDEX;
+      page[u] = -1;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < kFew; ++u)
+    if (u < per && page[u] >= 0 && *reinterpret_cast<volatile int32_t*>(p.refs + page[u]) <= 0)
+      atomicMin(p.refs + page[u], -1 - (total - 1 - (t * per + u)));
+  __syncthreads();
+  int32_t wins = 0;
+#pragma unroll
+  for (int u = 0; u < kFew; ++u) {
+    const bool win = u < per && page[u] >= 0 &&
+                     *reinterpret_cast<volatile int32_t*>(p.refs + page[u]) == -1 - (total - 1 - (t * per + u));
+    if (!win) page[u] = -1;
+    wins += win;
+  }
+  const int32_t upto = block_scan(wins, ws);
+  int32_t place = have + upto - wins;
+#pragma unroll
+  for (int u = 0; u < kFew; ++u)
+    if (u < per && page[u] >= 0) {
+      if (place < p.num_pages) p.free_pages[place] = page[u];
+      p.refs[page[u]] = 0;
+      ++place;
+    }
+  if (t == kBook - 1) *p.free_count = min(have + upto, p.num_pages);
 }
 
 // One CTA, a warp per table row, passes over the rows:
@@ -477,6 +653,10 @@ __global__ void __launch_bounds__(kBook) trim_kernel(const PoolView p, int32_t n
                                                      const int32_t* length, int32_t window, int32_t sinks,
                                                      int32_t* status) {
   __shared__ int32_t s_count[kBook], s_place[kBook], ws[kBook / 32], s_total;
+  if (static_cast<int64_t>(n) * p.max_pages <= kBook * kFew) {
+    trim_few(p, n, rows, length, window, sinks, status);
+    return;
+  }
   const int wid = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int32_t have = free_now(p);
   const int32_t size = 1 << p.page_shift;

@@ -483,6 +483,28 @@ def test_append_rows_that_are_not_finite(ss):
     assert torch.isnan(y[:4]).all() and torch.isfinite(y[4]).all() and torch.isnan(z[:4]).all()
 
 
+def test_append_rounds_as_defined_at_every_scale(ss):
+    # rows over the whole range of bf16, many of them with channels next to or on a half
+    rng = np.random.default_rng(3)
+    rows, dim = 6000, 64
+    x = rng.standard_normal((rows, 1, dim)) * 2.0 ** rng.integers(-133, 120, (rows, 1, 1))
+    on = rng.integers(0, 31, (rows // 2, 1, dim)) * 0.5 * 2.0 ** rng.integers(-125, 110, (rows // 2, 1, 1))
+    x[::2] = on + rng.integers(-3, 4, (rows // 2, 1, 1)) * on.max(-1, keepdims=True)
+    x[1, 0, :2] = 3.3895313892515355e38, -1.2e36  # their difference is finite, just
+    x = torch.from_numpy(x).to(torch.bfloat16).cuda()
+    cache = ss.alloc_cache(1, 6, 1, 1024, dim, "int4")
+    st = ints([-1])
+    ss.ss_cache_append(cache, 0, x, x, ints([list(range(6))]), ints([0]), st, token_offsets=ints([0, rows]),
+                       max_tokens=rows)
+    torch.cuda.synchronize()
+    n, step, low = R.quantise(np32(x)[:, 0])
+    assert st.tolist() == [0] and np.isfinite(step).all()
+    cells = cache.k[0].cpu().numpy().reshape(-1, dim // 2)[:rows]
+    assert (cells == R.pack(n)).all()
+    pairs = cache.k_scale[0].float().cpu().numpy().reshape(-1, 2)[:rows]
+    assert (pairs[:, 0] == step).all() and (pairs[:, 1] == low).all()
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 def test_append_reports_holes_and_bad_requests(ss, fmt):
     cache = ss.alloc_cache(1, 6, 2, 16, 64, fmt)
@@ -586,6 +608,37 @@ def test_pages_many_requests(ss):
     ss.ss_pages_trim(pool, ints(keep), st)
     assert ref.trim(range(n), keep, 0, 0) == st.tolist()
     same(pool, ref)
+
+
+@pytest.mark.parametrize("n,width", [(8, 1024), (9, 1024), (3, 5000), (700, 30)])
+def test_pages_wide_tables(ss, n, width):
+    # on both sides of the sizes that the bookkeeping holds in registers
+    rng = random.Random(n * width)
+    page, rows = 8, 2 * n
+    pages = n * width + n // 2
+    order = list(range(pages))
+    rng.shuffle(order)
+    pool = pool_of(ss, [[-1] * width for _ in range(rows)], [0] * pages, order, page, pages)
+    ref = R.Pages([[-1] * width for _ in range(rows)], [0] * pages, order, page)
+    cache = ss.alloc_cache(1, pages, 1, page, 8, "bf16")
+    st = ints([-1] * n)
+    full = [rng.randint(0, width * page) for _ in range(n)]
+    full[0] = width * page
+    for part in (0.3, 1.0):  # the second time the first entries are held
+        stop = [int(part * x) for x in full]
+        ss.ss_pages_reserve(pool, ints([0] * n), ints(stop), st)
+        assert ref.reserve(range(n), [0] * n, stop) == st.tolist()
+        same(pool, ref)
+    child = [n + i for i in range(n)]
+    ss.ss_pages_fork(pool, cache, ints(list(range(n))), ints(child), ints(full), st)
+    want, _ = ref.fork(list(range(n)), child, full)
+    assert st.tolist() == want
+    same(pool, ref)
+    for rows_, window, sinks in ((list(range(n)), 100, 9), (child, 0, 0), (list(range(n)), 0, 0)):
+        keep = full if window else [rng.randint(0, 50) for _ in rows_]
+        ss.ss_pages_trim(pool, ints(keep), st, window=window, sinks=sinks, table_rows=ints(rows_))
+        assert ref.trim(rows_, keep, window, sinks) == st.tolist()
+        same(pool, ref)
 
 
 def test_pages_bad_arguments_per_row(ss):
