@@ -16,6 +16,7 @@ using namespace ss;
 constexpr int kThreads = 256;
 constexpr int kRowLanes = 16;                     // a row is at most 16 lanes of 8 channels
 constexpr int kGroups = kThreads / kRowLanes;     // rows in flight per CTA
+constexpr int kMostCtas = 4 * 152;                // per request
 constexpr uint32_t kNaN2 = 0x7fc07fc0u;           // a bf16 pair of NaNs
 
 struct AppendArgs {
@@ -127,22 +128,25 @@ __device__ __forceinline__ uint32_t quantise8(const uint4 x, bool live, uint32_t
 
 __device__ __forceinline__ uint4 dequantise8(uint32_t w, uint32_t pair) {
   const float s = bf16_lo(pair), m = bf16_hi(pair);
+  const uint64_t s2 = two(s, s), m2 = two(m, m), off = two(-8388608.0f, -8388608.0f);
   uint32_t o[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)  // 2^23 + n, minus 2^23: no conversion
-    o[i] = bf16_pair(__fmaf_rn(__uint_as_float(((w >> (4 * i)) & 15u) | 0x4b000000u) - 8388608.0f, s, m),
-                     __fmaf_rn(__uint_as_float(((w >> (16 + 4 * i)) & 15u) | 0x4b000000u) - 8388608.0f, s, m));
+  for (int i = 0; i < 4; ++i) {  // 2^23 + n, minus 2^23: no conversion
+    const uint64_t n = add_2(two(__uint_as_float(((w >> (4 * i)) & 15u) | 0x4b000000u),
+                                 __uint_as_float(((w >> (16 + 4 * i)) & 15u) | 0x4b000000u)), off);
+    const uint64_t v = fma_2(n, s2, m2);
+    o[i] = bf16_pair(__uint_as_float(static_cast<uint32_t>(v)), __uint_as_float(static_cast<uint32_t>(v >> 32)));
+  }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-constexpr int kRowsEach = 4;  // rows that 16 lanes have in flight
-
 // A row is (token, K or V, head): 16 lanes of 16 bytes on the bf16 side.  16
-// lanes take kRowsEach consecutive rows, most often of one token, whose
-// addresses follow from one another; CTA (x, r) takes kGroups * kRowsEach rows
-// of request r, then a grid's width further.
-template <bool kPacked, bool kRead>
-__global__ void __launch_bounds__(kThreads) rows_kernel(const AppendArgs a, const FastDiv by_token, const FastDiv by_head) {
+// lanes take kEach consecutive rows of one token (four where the heads are
+// even), so a token's page is looked up once for them and their loads are in
+// flight together; CTA (x, r) takes kGroups * kEach rows of request r, then a
+// grid's width further.
+template <bool kPacked, bool kRead, int kEach>
+__global__ void __launch_bounds__(kThreads, 4) rows_kernel(const AppendArgs a, const FastDiv by_token) {
   const int r = blockIdx.y;
   const int32_t begin = a.offsets ? a.offsets[r] : r;
   const int32_t end = a.offsets ? a.offsets[r + 1] : r + 1;
@@ -158,72 +162,55 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const AppendArgs a, cons
   const bool live = lane * 8 < a.c.dim;
   const uint32_t lanes = 0xffffu << (threadIdx.x & 16);
   const uint32_t total = 2u * static_cast<uint32_t>(n) * static_cast<uint32_t>(a.c.heads);
-  for (uint32_t i0 = (blockIdx.x * kGroups + group) * kRowsEach; i0 < total; i0 += gridDim.x * (kGroups * kRowsEach)) {
-    uint32_t token = divide(i0, by_token), head = i0 - token * by_token.d;
-    bool is_v = head >= by_head.d;
-    if (is_v) head -= by_head.d;
-    int64_t in_flat, in_cell, in_scale;
-    int32_t at;
-    const auto locate = [&] {  // the row of head 0 of this token
-      const int64_t slot = static_cast<int64_t>(base) + token;
-      const int32_t in_page = static_cast<int32_t>(slot) & ((1 << a.c.page_shift) - 1);
-      at = page_of(a.t, a.c, row, slot);
-      in_flat = (begin + static_cast<int64_t>(token)) * a.token_stride + lane * 16;
-      in_cell = max(at, 0) * a.c.page_stride + in_page * a.c.slot_stride + lane * (kPacked ? 4 : 16);
-      if (kPacked) in_scale = max(at, 0) * a.c.s_page_stride + in_page * 4;
+  for (uint32_t i = (blockIdx.x * kGroups + group) * kEach; i < total; i += gridDim.x * (kGroups * kEach)) {
+    const uint32_t token = divide(i, by_token), first = i - token * by_token.d;
+    const int64_t slot = static_cast<int64_t>(base) + token;
+    const int32_t in_page = static_cast<int32_t>(slot) & ((1 << a.c.page_shift) - 1);
+    const int32_t page = page_of(a.t, a.c, row, slot);
+    const int64_t in_flat = (begin + static_cast<int64_t>(token)) * a.token_stride + lane * 16;
+    const int64_t in_cell = max(page, 0) * a.c.page_stride + in_page * a.c.slot_stride + lane * (kPacked ? 4 : 16);
+    const int64_t in_scale = max(page, 0) * a.c.s_page_stride + in_page * 4;
+    const auto flat = [&](int u) {
+      const int32_t head = first + u;
+      return head < a.c.heads ? a.k + in_flat + head * a.head_stride : a.v + in_flat + (head - a.c.heads) * a.head_stride;
     };
-    locate();
-    uint8_t* flat[kRowsEach];
-    uint8_t* cell[kRowsEach];
-    uint8_t* scale[kRowsEach];
-    int32_t page[kRowsEach];
-    uint4 x[kRowsEach];
-    uint32_t word[kRowsEach], pair[kRowsEach];
+    const auto cell = [&](int u) {
+      const int32_t head = first + u;
+      return head < a.c.heads ? a.c.k + in_cell + head * a.c.head_stride
+                              : a.c.v + in_cell + (head - a.c.heads) * a.c.head_stride;
+    };
+    const auto scale = [&](int u) {
+      const int32_t head = first + u;
+      return reinterpret_cast<uint32_t*>(head < a.c.heads ? a.c.ks + in_scale + head * a.c.s_head_stride
+                                                          : a.c.vs + in_scale + (head - a.c.heads) * a.c.s_head_stride);
+    };
+    uint4 x[kEach];
+    uint32_t word[kEach], pair[kEach];
 #pragma unroll
-    for (int u = 0; u < kRowsEach; ++u) {
-      flat[u] = (is_v ? a.v : a.k) + in_flat + head * a.head_stride;
-      cell[u] = (is_v ? a.c.v : a.c.k) + in_cell + head * a.c.head_stride;
-      if (kPacked) scale[u] = (is_v ? a.c.vs : a.c.ks) + in_scale + head * a.c.s_head_stride;
-      page[u] = at;
-      if (i0 + u >= total) {
-        flat[u] = nullptr;
-        page[u] = -1;
-      } else if (u + 1 < kRowsEach && ++head == by_head.d) {
-        head = 0;
-        is_v = !is_v;
-        if (!is_v && i0 + u + 1 < total) {
-          ++token;
-          locate();
-        }
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kRowsEach; ++u) {
+    for (int u = 0; u < kEach; ++u) {
       x[u] = make_uint4(0u, 0u, 0u, 0u);
       word[u] = pair[u] = 0;
-      if (!live || page[u] < 0) continue;
+      if (!live || page < 0) continue;
       if (!kRead) {
-        x[u] = *reinterpret_cast<const uint4*>(flat[u]);
+        x[u] = *reinterpret_cast<const uint4*>(flat(u));
       } else if (kPacked) {
-        word[u] = *reinterpret_cast<const uint32_t*>(cell[u]);
-        pair[u] = *reinterpret_cast<const uint32_t*>(scale[u]);
+        word[u] = *reinterpret_cast<const uint32_t*>(cell(u));
+        pair[u] = *scale(u);
       } else {
-        x[u] = *reinterpret_cast<const uint4*>(cell[u]);
+        x[u] = *reinterpret_cast<const uint4*>(cell(u));
       }
     }
+    if (!kRead && page < 0) continue;  // the same for the row's 16 lanes
 #pragma unroll
-    for (int u = 0; u < kRowsEach; ++u) {
-      if (kRead) {
-        if (live && flat[u])
-          *reinterpret_cast<uint4*>(flat[u]) = kPacked && page[u] >= 0 ? dequantise8(word[u], pair[u]) : x[u];
-      } else if (page[u] >= 0) {  // the same for the row's 16 lanes
-        if (kPacked) {
-          const uint32_t w = quantise8(x[u], live, lanes, pair[u]);
-          if (live) *reinterpret_cast<uint32_t*>(cell[u]) = w;
-          if (lane == 0) *reinterpret_cast<uint32_t*>(scale[u]) = pair[u];
-        } else if (live) {
-          *reinterpret_cast<uint4*>(cell[u]) = x[u];
-        }
+    for (int u = 0; u < kEach; ++u) {
+      if (kRead) {  // (a step and a low value of 0 give the zeros of a hole)
+        if (live) *reinterpret_cast<uint4*>(flat(u)) = kPacked ? dequantise8(word[u], pair[u]) : x[u];
+      } else if (kPacked) {
+        const uint32_t w = quantise8(x[u], live, lanes, pair[u]);
+        if (live) *reinterpret_cast<uint32_t*>(cell(u)) = w;
+        if (lane == 0) *scale(u) = pair[u];
+      } else if (live) {
+        *reinterpret_cast<uint4*>(cell(u)) = x[u];
       }
     }
   }
@@ -263,14 +250,18 @@ static ss_status rows_call(const ss_append_args* args, bool read, cudaStream_t s
   a.status = A.out_status;
   const int64_t rows = 2ll * a.max_tokens * a.c.heads;
   if (rows >= (1ll << 31)) return SS_ERR_UNSUPPORTED;
-  const int64_t each = kGroups * kRowsEach, want = (rows + each - 1) / each;
-  const dim3 grid(static_cast<unsigned>(want < 1 ? 1 : want > 4096 ? 4096 : want), A.num_requests);
-  const FastDiv by_token = fast_div(2u * a.c.heads), by_head = fast_div(a.c.heads);
+  // No more CTAs per request than fill the GPU; they loop over the rest of its
+  // rows (4 bits, 4 x 2-6k tokens: 32 us, 35 with a CTA for every 64 rows).
+  const bool even = (a.c.heads & 1) == 0;
+  const int64_t each = kGroups * (even ? 4 : 2), want = (rows + each - 1) / each;
+  const dim3 grid(static_cast<unsigned>(want < 1 ? 1 : want > kMostCtas ? kMostCtas : want), A.num_requests);
+  const FastDiv by_token = fast_div(2u * a.c.heads);
   const bool packed = a.c.format == SS_CACHE_INT4;
-  if (packed && read) rows_kernel<true, true><<<grid, kThreads, 0, s>>>(a, by_token, by_head);
-  else if (packed) rows_kernel<true, false><<<grid, kThreads, 0, s>>>(a, by_token, by_head);
-  else if (read) rows_kernel<false, true><<<grid, kThreads, 0, s>>>(a, by_token, by_head);
-  else rows_kernel<false, false><<<grid, kThreads, 0, s>>>(a, by_token, by_head);
+  const auto launch = [&](auto kernel) { kernel<<<grid, kThreads, 0, s>>>(a, by_token); };
+  if (even) launch(packed ? (read ? rows_kernel<true, true, 4> : rows_kernel<true, false, 4>)
+                          : (read ? rows_kernel<false, true, 4> : rows_kernel<false, false, 4>));
+  else launch(packed ? (read ? rows_kernel<true, true, 2> : rows_kernel<true, false, 2>)
+                     : (read ? rows_kernel<false, true, 2> : rows_kernel<false, false, 2>));
   return finish(cudaSuccess);
 }
 
