@@ -153,6 +153,11 @@ struct Cfg {
   static constexpr int kRawRow = 32 * kHalves;               // packed bytes per key
   static constexpr int kRaw = kPacked ? 2 * kTile * kRawRow + 2 * kTile * 4 : 0;
   static constexpr int kRawStages = kPacked ? 4 : 1;
+  // V's unpacking in a loop where the other warps' code is long: together they
+  // are bound by instruction fetch (48 x 1-8 drafts of 64 rows: 353 us, 414
+  // unrolled); unrolled with its loads ahead of the wait where it is latency
+  // that counts.
+  static constexpr int kUnrollV = kLive >= 64 ? 1 : 2 * kHalves;
   // the static arrays, rounded up
   static constexpr int kMeta = kNQ * (static_cast<int>(sizeof(Item)) + kN * 32 + 64 + 512) + kStreams * kN * 36 + 1536 +
                                (kPacked ? 2 * kPairs * kTile * 4 : 0);
@@ -1263,7 +1268,8 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
             if (i0 > 0) tmem_get(tmem + sb * kNS + kLive + c0 + i0 + lanes, low);
             tmem_wait(low);
 #pragma unroll
-            for (int i = 0; i < kPart; ++i) x[i0 + i] = __fmaf_rn(low[i], 0.03125f, x[i0 + i]);
+            for (int i = 0; i < kPart; i += 2)
+              split(fma_2(two(low[i], low[i + 1]), two(0.03125f, 0.03125f), two(x[i0 + i], x[i0 + i + 1])), x[i0 + i], x[i0 + i + 1]);
           }
         }
         tc_fence_before();
@@ -1271,21 +1277,17 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
 #pragma unroll
         for (int i = 0; i < kCols; i += 4) {
           const float4 r4 = *reinterpret_cast<const float4*>(nref + h0 + i);
-          float y[4] = {r4.x, r4.y, r4.z, r4.w};
+          uint64_t y[2] = {two(r4.x, r4.y), two(r4.z, r4.w)}, z[2] = {two(x[i], x[i + 1]), two(x[i + 2], x[i + 3])};
           if (kPacked) {
             const float4 q4 = *reinterpret_cast<const float4*>(&row_qsum[b][c0 + i]);
             const float4 u4 = *reinterpret_cast<const float4*>(&row_unit[b][c0 + i]);
-            y[0] = __fmaf_rn(kb, q4.x, y[0]);
-            y[1] = __fmaf_rn(kb, q4.y, y[1]);
-            y[2] = __fmaf_rn(kb, q4.z, y[2]);
-            y[3] = __fmaf_rn(kb, q4.w, y[3]);
-            x[i] *= u4.x;
-            x[i + 1] *= u4.y;
-            x[i + 2] *= u4.z;
-            x[i + 3] *= u4.w;
+            y[0] = fma_2(two(kb, kb), two(q4.x, q4.y), y[0]);
+            y[1] = fma_2(two(kb, kb), two(q4.z, q4.w), y[1]);
+            z[0] = mul_2(z[0], two(u4.x, u4.y));
+            z[1] = mul_2(z[1], two(u4.z, u4.w));
           }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[i + e] = __fmaf_rn(x[i + e], ka, y[e]);
+          for (int e = 0; e < 2; ++e) split(fma_2(z[e], two(ka, ka), y[e]), x[i + 2 * e], x[i + 2 * e + 1]);
         }
         if (masked)
 #pragma unroll
@@ -1349,16 +1351,13 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
           uint32_t o4[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            float p[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int i = i8 * 8 + e * 2 + h;
-              p[h] = ex2(x[i]);
-              l[i] += p[h];
-              if (kPacked) {
-                cs[i] = __fmaf_rn(p[h], wv, cs[i]);
-                p[h] *= sv;
-              }
+            const int i = i8 * 8 + e * 2;
+            float p[2] = {ex2(x[i]), ex2(x[i + 1])};
+            const uint64_t p2 = two(p[0], p[1]);
+            split(add_2(two(l[i], l[i + 1]), p2), l[i], l[i + 1]);
+            if constexpr (kPacked) {
+              split(fma_2(p2, two(wv, wv), two(cs[i], cs[i + 1])), cs[i], cs[i + 1]);
+              split(mul_2(p2, two(sv, sv)), p[0], p[1]);
             }
             o4[e] = bf16_pair(p[0], p[1]);
           }
@@ -1572,19 +1571,23 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
       if (!wait_or_dead(rfull + rs, (at / F::kRawStages) & 1, dead)) break;
       const uint8_t* src = raw + rs * F::kRaw + (is_v ? kTile * F::kRawRow : 0);
       const uint32_t* pairs = reinterpret_cast<const uint32_t*>(raw + rs * F::kRaw + 2 * kTile * F::kRawRow) + key;
-      uint4 w4[2 * kHalves];  // 16 packed bytes: 32 channels
-#pragma unroll
-      for (int c = 0; c < 2 * kHalves; ++c) {
+      const auto packed = [&](int c) {  // 16 bytes: 32 channels
         const uint32_t off = key * F::kRawRow + c * 16;
-        w4[c] = *reinterpret_cast<const uint4*>(src + (off ^ ((off >> 3) & (kHalves == 2 ? 0x30u : 0x10u))));
-      }
+        return *reinterpret_cast<const uint4*>(src + (off ^ ((off >> 3) & (kHalves == 2 ? 0x30u : 0x10u))));
+      };
+      constexpr bool kAhead = F::kUnrollV > 1;  // the loads before the wait
+      uint4 w4[2 * kHalves];
+      if constexpr (kAhead)
+#pragma unroll
+        for (int c = 0; c < 2 * kHalves; ++c) w4[c] = packed(c);
       if (is_v) {
         const int32_t s = at % kVs;
         if (!wait_or_dead(vempty + s, ((at / kVs) & 1) ^ 1u, dead)) break;
         uint8_t* dst = vring + s * F::kStage + key * 128;
-#pragma unroll
+#pragma unroll F::kUnrollV
         for (int c = 0; c < 2 * kHalves; ++c) {
-          const uint32_t w[4] = {w4[c].x, w4[c].y, w4[c].z, w4[c].w};
+          const uint4 x4 = kAhead ? w4[c] : packed(c);
+          const uint32_t w[4] = {x4.x, x4.y, x4.z, x4.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             uint32_t o[4];
@@ -1610,8 +1613,8 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
         const uint32_t dst = tmem + F::kKCol + (at & 1) * F::kKCols + (static_cast<uint32_t>((warp & 3) * 32) << 16);
 #pragma unroll
         for (int c = 0; c < kHalves; ++c) {
-          const uint32_t w[8] = {w4[2 * c].x,     w4[2 * c].y,     w4[2 * c].z,     w4[2 * c].w,
-                                 w4[2 * c + 1].x, w4[2 * c + 1].y, w4[2 * c + 1].z, w4[2 * c + 1].w};
+          const uint4 w0 = kAhead ? w4[2 * c] : packed(2 * c), w1 = kAhead ? w4[2 * c + 1] : packed(2 * c + 1);
+          const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
           float o[16];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {

@@ -56,23 +56,6 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ uint64_t two(float a, float b) {
-  return static_cast<uint64_t>(__float_as_uint(b)) << 32 | __float_as_uint(a);
-}
-__device__ __forceinline__ uint64_t add_2(uint64_t a, uint64_t b) {
-  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(a) : "l"(b));
-  return a;
-}
-__device__ __forceinline__ uint64_t mul_2(uint64_t a, uint64_t b) {
-  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(a) : "l"(b));
-  return a;
-}
-__device__ __forceinline__ uint64_t fma_2(uint64_t a, uint64_t b, uint64_t c) {
-  asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(a) : "l"(b), "l"(c));
-  return a;
-}
-
 // Eight channels of a row, quantised: the row's low value and step come from
 // the 16 lanes of the row, as the pair (min x, min -x), so that one shuffle and
 // one instruction join two lanes.
@@ -135,7 +118,9 @@ __device__ __forceinline__ uint4 dequantise8(uint32_t w, uint32_t pair) {
     const uint64_t n = add_2(two(__uint_as_float(((w >> (4 * i)) & 15u) | 0x4b000000u),
                                  __uint_as_float(((w >> (16 + 4 * i)) & 15u) | 0x4b000000u)), off);
     const uint64_t v = fma_2(n, s2, m2);
-    o[i] = bf16_pair(__uint_as_float(static_cast<uint32_t>(v)), __uint_as_float(static_cast<uint32_t>(v >> 32)));
+    float a, b;
+    split(v, a, b);
+    o[i] = bf16_pair(a, b);
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
