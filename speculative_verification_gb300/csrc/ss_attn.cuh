@@ -66,6 +66,7 @@ constexpr int kInfo = 16;                 // tiles whose page masks are kept
 constexpr int kPairs = 8;                 // tiles whose (s, m) pairs are kept
 constexpr float kUnset = 3.0e38f;         // in a piece: minus the reference of a row that has seen nothing
 constexpr float kSlack = 32.0f;           // how far a score (log2) may pass its row's reference
+constexpr float kDeep = 64.0f;            // how far the first ones may lie below the reference 0
 constexpr int kSlotFloats = 128 * 130;    // one piece: up to 128 rows of 128 channels, r and l
 
 struct AttnArgs {
@@ -575,6 +576,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
   __shared__ __align__(16) float nref[kRows], corr[kRows], shift[kRows], sums[kRows], csums[kRows];
   __shared__ float part[4][kRows];
   __shared__ uint32_t tmem_slot;
+  __shared__ uint8_t v_bad[2][F::kGroups > 1 && !kPacked ? kTile : 1];  // keys whose values are not finite
   __shared__ int32_t s_dead, s_last, s_r0, s_r1, s_before, s_tiles0, s_scan[32];
 
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -618,6 +620,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
     s_r0 = s_r1 = 0;
     fence_barrier_init();
   }
+  if (F::kGroups > 1 && !kPacked && tid < kTile) v_bad[0][tid] = v_bad[1][tid] = 0;
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_slot)),
                  "r"(F::kTmem)
@@ -1172,6 +1175,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
       const uint32_t o_item = tmem + F::kOCol + (k & 1) * F::kStreams * kN + lanes, o_base = o_item + h0;
       const int32_t first_pos = it.base + (tree ? 0 : token_of(a, it.row0));
       const int32_t last_pos = it.base + token_of(a, it.row0 + it.rows - 1);  // of a tree: at most
+      const int32_t first_off = it.row0 - token_of(a, it.row0) * a.group;     // rows of the first token in blocks before
 #pragma unroll 1
       for (int32_t t = F::kStreams == 2 ? (done ^ stream) & 1 : 0; t < it.tiles; t += F::kStreams) {
         const int32_t at = done + t;
@@ -1220,6 +1224,16 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
           from = here ? place : 0x7fffffff;
           if (draft) node = j - it.base;
           vis = 0;
+          if (!tree) {
+            // the rows are in the order of their positions: a range sees the key
+            const int32_t e = place - first_pos;  // in tokens from the block's first
+            const int32_t f = always ? kLive : static_cast<int32_t>(min(static_cast<int64_t>(e) + a.window,
+                                                                       static_cast<int64_t>(kLive)));
+            const int32_t lo_row = min(max(e, 0), kLive) * a.group - first_off - c0;
+            const int32_t hi_row = max(f, 0) * a.group - first_off - c0;
+            const auto below = [](int32_t n) { return n >= 32 ? 0xffffffffu : (1u << max(n, 0)) - 1u; };
+            if (here) vis = below(hi_row) & ~below(lo_row);
+          } else {
 #pragma unroll
           for (int i = 0; i < kCols; i += 4) {
             const int4 p4 = *reinterpret_cast<const int4*>(&row_pos[b][c0 + i]);
@@ -1235,10 +1249,13 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
             for (int i = 0; i < kCols; ++i) on |= ((word[2 * i] >> ((j - it.base) & 31)) & 1u) << i;
             vis &= on;
           }
-          if (!kPacked && wg == 0) {
+          }
+          if (!kPacked) {
             // A value that is not finite must not meet a weight of 0: the row
             // of such a key, where not every query sees it, becomes 0 in
             // shared memory, and the queries that do see it get a weight of NaN.
+            // Each warpgroup looks at its part of the channels.
+            constexpr int kScan = 8 * kHalves / F::kGroups;
             const int32_t s = at % kVs;
             wait_or_dead(vfull + s, (at / kVs) & 1, dead);
             const bool all = here && !draft && j <= first_pos && (always || j > last_pos - a.window);
@@ -1246,17 +1263,14 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
               uint4* v = reinterpret_cast<uint4*>(vring + s * F::kStage + lt * 128);
               uint32_t acc = 0;  // 0 times each channel, added up: NaN as soon as one is not finite
 #pragma unroll 4
-              for (int c = 0; c < 8 * kHalves; ++c) {
+              for (int c = wg * kScan; c < (wg + 1) * kScan; ++c) {
                 const uint4 x = v[(c >> 3) * 1024 + ((c & 7) ^ (lt & 7))];
                 const uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(y[e]), "r"(0u));
               }
               poison = (acc & 0x7fff7fffu) != 0;
-              if (poison) {
-#pragma unroll 1
-                for (int c = 0; c < 8 * kHalves; ++c) v[(c >> 3) * 1024 + (c & 7)] = make_uint4(0u, 0u, 0u, 0u);
-              }
+              if (F::kGroups > 1 && poison) v_bad[sb][lt] = 1;
             }
           }
         }
@@ -1289,20 +1303,34 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 2; ++e) split(fma_2(z[e], two(ka, ka), y[e]), x[i + 2 * e], x[i + 2 * e + 1]);
         }
+        float least = 0.0f;
+        if (fresh)
+#pragma unroll
+          for (int i = 0; i < kCols; ++i) least = fminf(least, ((vis >> i) & 1u) ? x[i] : 0.0f);
         if (masked)
 #pragma unroll
           for (int i = 0; i < kCols; ++i) x[i] = ((vis >> i) & 1u) ? x[i] : -INFINITY;
-        bool pass = fresh;
-        if (!pass) {
-          float most[4] = {x[0], x[1], x[2], x[3]};
+        float most[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-          for (int i = 4; i < kCols; ++i) most[i & 3] = fmaxf(most[i & 3], x[i]);
-          pass = bar_any(bar, 128, fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])) > kSlack);
+        for (int i = 4; i < kCols; ++i) most[i & 3] = fmaxf(most[i & 3], x[i]);
+        const bool pass = bar_any(bar, 128, fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])) > kSlack || least < -kDeep);
+        if (fresh && !pass) {
+          // the rows that see a key here may keep the reference 0
+          uint32_t seen = 0xffffffffu;
+          if (masked) {
+            const uint32_t any = __reduce_or_sync(0xffffffffu, vis);
+            if (lane == 0) part[wq][h0] = __uint_as_float(any);
+            bar_sync(bar, 128);
+            seen = (__float_as_uint(part[0][h0]) | __float_as_uint(part[1][h0])) |
+                   (__float_as_uint(part[2][h0]) | __float_as_uint(part[3][h0]));
+          }
+          unset = unset && ((seen >> (lt & 31)) & 1u) == 0;
+          fresh = masked && bar_any(bar, 128, lt < kCols && c0 + lt < it.rows && unset);
         }
         if (pass) {
-          // some row's score passes its reference by too much (or the row
-          // has none yet): the new reference is the row's largest score of the
-          // tile
+          // some row's score passes its reference by too much (or is far below
+          // 0 and the row has no reference yet): the new reference is the row's
+          // largest score of the tile
 #pragma unroll
           for (int i = 0; i < kCols; ++i) {
             const float m = warp_max(x[i]);  // a NaN counts as nothing
@@ -1312,11 +1340,12 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
           if (lt < kCols) {
             const int c = h0 + lt;
             const float m = fmaxf(fmaxf(part[0][c], part[1][c]), fmaxf(part[2][c], part[3][c]));
-            const bool move = m > (unset ? -INFINITY : kSlack);
+            // by the row's own scores alone, so that what other rows see changes no bit of it
+            const bool move = m > kSlack || (unset && m < -kDeep && m > -INFINITY);
             corr[c] = !move ? 1.0f : unset ? 0.0f : ex2(-m);  // 2^(old reference - new)
             shift[c] = move ? m : 0.0f;
             if (move) nref[c] -= m;
-            unset = unset && !move;
+            unset = unset && !(m > -INFINITY);
           }
           // is there a row left that has seen nothing?
           fresh = bar_any(bar, 128, lt < kCols && c0 + lt < it.rows && unset);
@@ -1365,12 +1394,24 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
           *reinterpret_cast<uint4*>(pb + (off ^ ((off >> 3) & kSwz))) = make_uint4(o4[0], o4[1], o4[2], o4[3]);
         }
         if (!kPacked && F::kGroups > 1 && masked) {
-          // warpgroup 0 writes into the others' weights (below) once they are there
-          if (wg != 0) mbar_arrive(&written[sb]);
-          else if (poison) wait_or_dead(&written[sb], uses[sb] & 1, dead);
+          // warpgroup 0 hears what the others found, and writes into their
+          // weights once they are there
+          poison = false;
+          if (wg != 0) {
+            mbar_arrive(&written[sb]);
+          } else {
+            wait_or_dead(&written[sb], uses[sb] & 1, dead);
+            poison = v_bad[sb][lt] != 0;
+          }
           uses[sb] += 1;
         }
         if (poison) {
+          if (!kPacked) {
+            if (F::kGroups > 1) v_bad[sb][lt] = 0;
+            uint4* v = reinterpret_cast<uint4*>(vring + at % kVs * F::kStage + lt * 128);
+#pragma unroll 1
+            for (int c = 0; c < 8 * kHalves; ++c) v[(c >> 3) * 1024 + (c & 7)] = make_uint4(0u, 0u, 0u, 0u);
+          }
           const int from = kPacked ? c0 : 0, upto = kPacked ? c0 + kCols : kLive;
 #pragma unroll 1
           for (int c = from; c < upto; ++c) {
