@@ -159,6 +159,7 @@ struct Cfg {
   // unrolled); unrolled with its loads ahead of the wait where it is latency
   // that counts.
   static constexpr int kUnrollV = kLive >= 64 ? 1 : 2 * kHalves;
+  static constexpr int kUnrollPV = kPacked && kLive >= 64 ? 1 : 8;
   // the static arrays, rounded up
   static constexpr int kMeta = kNQ * (static_cast<int>(sizeof(Item)) + kN * 32 + 64 + 512) + kStreams * kN * 36 + 1536 +
                                (kPacked ? 2 * kPairs * kTile * 4 : 0);
@@ -553,6 +554,75 @@ __device__ __forceinline__ int32_t request_tiles(const AttnArgs& a, const Reques
   return sum;
 }
 
+// The queries of an item over a 4-bit cache: row n as unit (hi + lo / 32), both
+// e4m3, unit a power of two by the row's largest channel: q's 8 bits are 4 + 4,
+// so this is exact but for channels below 2^-15 of the largest.  16 lanes per
+// row, 8 channels each; a warp has 2 kEach rows in flight.
+template <int kLive, int kEach>
+__device__ __forceinline__ void convert_queries(const AttnArgs& a, const Item& it, uint8_t* q, float* qsum, float* unit,
+                                                int warp, int warps) {
+  const int lane = threadIdx.x & 31, ch = lane & 15;
+  const int32_t row0 = it.row0, rows = it.rows, head = it.head, qbegin = it.qbegin;
+#pragma unroll 1
+  for (int n0 = warp * (2 * kEach) + (lane >> 4); n0 < kLive; n0 += warps * (2 * kEach)) {
+    uint4 x[kEach];
+#pragma unroll
+    for (int u = 0; u < kEach; ++u) {
+      const int n = n0 + 2 * u, token = token_of(a, row0 + n);
+      x[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (n < rows && ch * 8 < a.c.dim)
+        x[u] = *reinterpret_cast<const uint4*>(
+            a.q + (static_cast<int64_t>(qbegin) + token) * a.q_token +
+            (static_cast<int64_t>(head) * a.group + (row0 + n - token * a.group)) * a.q_head + ch * 16);
+    }
+#pragma unroll
+    for (int u = 0; u < kEach; ++u) {
+      const int n = n0 + 2 * u;
+      const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+      float v[8], sum = 0.0f, top = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = bf16_lo(w[i]);
+        v[2 * i + 1] = bf16_hi(w[i]);
+        sum += v[2 * i] + v[2 * i + 1];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const bool finite = fabsf(v[i]) <= 3.4e38f;
+        if (finite) top = fmaxf(top, fabsf(v[i]));
+        else v[i] = __int_as_float(0x7fffffff);
+      }
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, o, 16);
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o, 16));
+      }
+      // top * scale is in [128, 256)
+      const int e = max((__float_as_int(top) >> 23) & 0xff, 16);
+      const float scale = __int_as_float((261 - e) << 23);
+      uint32_t hi[2] = {0u, 0u}, lo[2] = {0u, 0u};
+      // the unpacked keys' order of eight channels: 0 4 1 5, 2 6 3 7
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = (i & 1) + (i >> 1) * 2;  // pairs (0, 4), (1, 5), (2, 6), (3, 7)
+        const float p0 = v[c] * scale, p1 = v[c + 4] * scale;
+        const uint32_t h = e4m3_pair(p0, p1);
+        const float2 back = e4m3_floats(h);
+        const uint32_t r = e4m3_pair((p0 - back.x) * 32.0f, (p1 - back.y) * 32.0f);
+        hi[i >> 1] |= h << (16 * (i & 1));
+        lo[i >> 1] |= r << (16 * (i & 1));
+      }
+      uint8_t* at = q + (((ch >> 1) ^ (n & 7)) << 4) + (ch & 1) * 8;  // kLive is a multiple of 8
+      *reinterpret_cast<uint2*>(at + n * 128) = make_uint2(hi[0], hi[1]);
+      *reinterpret_cast<uint2*>(at + (kLive + n) * 128) = make_uint2(lo[0], lo[1]);
+      if (ch == 0) {
+        qsum[n] = sum;
+        unit[n] = __int_as_float((e - 7) << 23);
+      }
+    }
+  }
+}
+
 template <int kLive, bool kPacked, int kHalves>
 __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
     attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -561,7 +631,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
   constexpr int kRing = F::kRing, kKs = F::kKs, kVs = F::kVs, kNQ = F::kNQ, kCols = F::kCols, kN = F::kN, kNS = F::kNS;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t kfull[kKs], kempty[kKs], vfull[kVs], vempty[kVs], sfull[2], sempty[2], pfull[2], pdone[2], oempty[2],
-      qfull[kNQ], qempty[kNQ], qfree[F::kQBufs], rfull[F::kRawStages], rempty[F::kRawStages], written[2], drain[2];
+      mfull[kNQ], qfull[kNQ], qempty[kNQ], qfree[F::kQBufs], rfull[F::kRawStages], rempty[F::kRawStages], written[2], drain[2];
   __shared__ Item items[kNQ];
   __shared__ __align__(16) int32_t row_pos[kNQ][kN];
   __shared__ __align__(16) uint64_t row_path[kNQ][kN];
@@ -604,6 +674,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
       mbar_init(oempty + i, F::kSoft);
     }
     for (int i = 0; i < kNQ; ++i) {
+      mbar_init(mfull + i, 32);
       mbar_init(qfull + i, 32);
       mbar_init(qempty + i, 1 + F::kSoft / 32);
     }
@@ -723,7 +794,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
 #pragma unroll 1
     while (at < tiles_all && ok) {
       const int b = k % kNQ;
-      wait(qfull + b, k / kNQ);
+      wait(mfull + b, k / kNQ);
       if (!ok) break;
       const Item& it = items[b];
       const auto same = [](int32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
@@ -893,7 +964,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
 #pragma unroll 1
     for (int32_t k = 0; at < tiles_all && ok; ++k) {
       const int qb = k % kNQ;
-      wait(qfull + qb, k / kNQ);
+      wait(mfull + qb, k / kNQ);
       if (!ok) break;
       const int32_t tiles = __shfl_sync(0xffffffffu, items[qb].tiles, 0);
       wait(oempty + (k & 1), (k >> 1) + 1);
@@ -909,7 +980,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
         const uint32_t va = desc_lo(v_a + s * F::kStage, kHalves == 2 ? 16384 : 0);
         const uint32_t pa = desc_lo(p_a + b % F::kPBufs * F::kP, kTile * 128);
         if (elect_one()) {
-#pragma unroll
+#pragma unroll F::kUnrollPV
           for (int kk = 0; kk < kTile / 16; ++kk)
             umma(d, desc(va + kk * (16 * 128 >> 4), kHiV), desc(pa + kk * (16 * F::kPitch >> 4), kHiP), instr_desc<kN>(true),
                  (t >= F::kStreams || kk > 0) ? 1u : 0u);
@@ -1031,6 +1102,8 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
         row_out[b][n] = t * a.out_token + h * a.out_head;
         row_lse[b][n] = static_cast<int32_t>(t * a.num_heads + h);
       }
+      mbar_arrive(mfull + b);
+      __syncwarp();
       const int qb = k % F::kQBufs;
       if (!__all_sync(0xffffffffu, wait_or_dead(qfree + qb, ((k / F::kQBufs) & 1) ^ 1u, dead))) break;
       if constexpr (!kPacked) {
@@ -1053,74 +1126,12 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
           }
         }
       } else {
-      // 16 lanes per row, 8 channels each; 8 rows in flight
-      const int ch = lane & 15;
-#pragma unroll 1
-      for (int n0 = lane >> 4; n0 < kN; n0 += 8) {
-        uint4 x[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int n = n0 + 2 * u, token = token_of(a, row0 + n);
-          x[u] = make_uint4(0u, 0u, 0u, 0u);
-          if (n < rows && ch * 8 < a.c.dim)
-            x[u] = *reinterpret_cast<const uint4*>(
-                a.q + (static_cast<int64_t>(q.qbegin) + token) * a.q_token +
-                (static_cast<int64_t>(head) * a.group + (row0 + n - token * a.group)) * a.q_head + ch * 16);
+        if (k > 0) {
+          convert_queries<kLive, 4>(a, items[b], qbuf + qb * F::kQ, row_qsum[b], row_unit[b], 0, 1);
+          proxy_fence();
+        } else {
+          bar_sync(6, F::kSoft + 32);  // the softmax warps have done it
         }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int n = n0 + 2 * u;
-          {
-            // q as unit (hi + lo / 32), both e4m3, unit a power of two by the
-            // row's largest channel: q's 8 bits are 4 + 4, so this is exact but
-            // for channels below 2^-15 of the largest
-            const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-            float v[8], sum = 0.0f, top = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              v[2 * i] = bf16_lo(w[i]);
-              v[2 * i + 1] = bf16_hi(w[i]);
-              sum += v[2 * i] + v[2 * i + 1];
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const bool finite = fabsf(v[i]) <= 3.4e38f;
-              if (finite) top = fmaxf(top, fabsf(v[i]));
-              else v[i] = __int_as_float(0x7fffffff);
-            }
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1) {
-              sum += __shfl_xor_sync(0xffffffffu, sum, o, 16);
-              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o, 16));
-            }
-            // top * scale is in [128, 256)
-            const int e = max((__float_as_int(top) >> 23) & 0xff, 16);
-            const float scale = __int_as_float((261 - e) << 23);
-            uint32_t hi[2] = {0u, 0u}, lo[2] = {0u, 0u};
-            // the unpacked keys' order of eight channels: 0 4 1 5, 2 6 3 7
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int c = (i & 1) + (i >> 1) * 2;  // pairs (0, 4), (1, 5), (2, 6), (3, 7)
-              const float p0 = v[c] * scale, p1 = v[c + 4] * scale;
-              const uint32_t h = e4m3_pair(p0, p1);
-              const float2 back = e4m3_floats(h);
-              const uint32_t r = e4m3_pair((p0 - back.x) * 32.0f, (p1 - back.y) * 32.0f);
-              hi[i >> 1] |= h << (16 * (i & 1));
-              lo[i >> 1] |= r << (16 * (i & 1));
-            }
-            uint8_t* at = qbuf + qb * F::kQ + (((ch >> 1) ^ (n & 7)) << 4) + (ch & 1) * 8;  // kLive is a multiple of 8
-            if (n < kLive) {
-              *reinterpret_cast<uint2*>(at + n * 128) = make_uint2(hi[0], hi[1]);
-              *reinterpret_cast<uint2*>(at + (kLive + n) * 128) = make_uint2(lo[0], lo[1]);
-            }
-            if (ch == 0) {
-              row_qsum[b][n] = sum;
-              row_unit[b][n] = __int_as_float((e - 7) << 23);
-            }
-          }
-        }
-      }
-        proxy_fence();
       }
       mbar_arrive(qfull + b);
       // the next item
@@ -1160,7 +1171,16 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
     uint32_t uses[2] = {0, 0};  // of written
     for (int32_t k = 0; done < my_tiles; ++k) {
       const int b = k % kNQ;
-      const bool in = wait_or_dead(qfull + b, (k / kNQ) & 1, dead);
+      if constexpr (kPacked)
+        if (k == 0) {  // the first item's queries, for which everyone waits, by all of these warps
+          constexpr int kWarps = F::kSoft / 32, kEach = kLive >= 8 * kWarps ? 4 : kLive >= 4 * kWarps ? 2 : 1;
+          wait_or_dead(mfull, 0, dead);
+          convert_queries<kLive, kEach>(a, items[0], qbuf, row_qsum[0], row_unit[0], st >> 5, kWarps);
+          proxy_fence();
+          bar_sync(6, F::kSoft + 32);
+        }
+      // (4 bits: the rows' sums and units come with the queries)
+      const bool in = wait_or_dead((kPacked ? qfull : mfull) + b, (k / kNQ) & 1, dead);
       if (bar_any(5, F::kSoft, !in)) break;  // the same decision for every softmax thread
       const Item it = items[b];
       float l[kCols], cs[kPacked ? kCols : 1];
@@ -1234,7 +1254,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
             const auto below = [](int32_t n) { return n >= 32 ? 0xffffffffu : (1u << max(n, 0)) - 1u; };
             if (here) vis = below(hi_row) & ~below(lo_row);
           } else {
-#pragma unroll
+#pragma unroll 1
           for (int i = 0; i < kCols; i += 4) {
             const int4 p4 = *reinterpret_cast<const int4*>(&row_pos[b][c0 + i]);
             vis |= (static_cast<uint32_t>(static_cast<uint32_t>(p4.x - from) <= span) << i) |
@@ -1245,7 +1265,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
           if (draft) {
             const uint32_t* word = reinterpret_cast<const uint32_t*>(&row_path[b][c0]) + ((j - it.base) >> 5);
             uint32_t on = 0;
-#pragma unroll
+#pragma unroll 4
             for (int i = 0; i < kCols; ++i) on |= ((word[2 * i] >> ((j - it.base) & 31)) & 1u) << i;
             vis &= on;
           }
@@ -1545,50 +1565,79 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
           const auto piece_at = [&](int32_t p) {
             return base + (static_cast<int64_t>(p) * 2 + (p == 0 ? first_piece : 0)) * kSlotFloats;
           };
+          // a warp takes kJoin rows at once: what one row costs is the latency
+          // of its loads
+          constexpr int kWarps = F::kSoft / 32, kJoin = kLive >= 4 * kWarps ? 4 : kLive > kWarps ? 2 : 1;
 #pragma unroll 1
-          for (int c = st >> 5; c < rows; c += F::kSoft / 32) {
-            float top = -INFINITY;  // the largest reference
-#pragma unroll 1
-            for (int32_t p = lane; p < parts; p += 32) {
-              const float nr = __ldcg(piece_at(p) + 128 * 128 + 2 * c);
-              top = fmaxf(top, nr == kUnset ? -INFINITY : -nr);
-            }
+          for (int cj = (st >> 5) * kJoin; cj < rows; cj += kWarps * kJoin) {
+            float top[kJoin], total_sum[kJoin];
+            float4 acc[kJoin];
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            float sum = 0.0f;
+            for (int u = 0; u < kJoin; ++u) {
+              top[u] = -INFINITY;  // the largest reference
+              total_sum[u] = 0.0f;
+              acc[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
 #pragma unroll 1
             for (int32_t p0 = 0; p0 < parts; p0 += 32) {
-              float g = 0.0f, ls = 0.0f;
-              if (p0 + lane < parts) {
-                const float* pc = piece_at(p0 + lane);
-                const float nr = __ldcg(pc + 128 * 128 + 2 * c);
-                ls = __ldcg(pc + 128 * 128 + 2 * c + 1);
+              float2 rl[kJoin];  // lane i: piece p0 + i's reference and sum
+              float g[kJoin];
+              const float* pc = piece_at(min(p0 + lane, parts - 1)) + 128 * 128;
+#pragma unroll
+              for (int u = 0; u < kJoin; ++u)
+                rl[u] = __ldcg(reinterpret_cast<const float2*>(pc + 2 * min(cj + u, rows - 1)));
+#pragma unroll
+              for (int u = 0; u < kJoin; ++u) {
+                const bool set = p0 + lane < parts && rl[u].x != kUnset;
+                float m = set ? -rl[u].x : -INFINITY;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                m = fmaxf(m, top[u]);
+                if (p0 > 0) {
+                  const float f = top[u] == -INFINITY ? 1.0f : ex2(top[u] - m);
+                  total_sum[u] *= f;
+                  acc[u].x *= f;
+                  acc[u].y *= f;
+                  acc[u].z *= f;
+                  acc[u].w *= f;
+                }
+                top[u] = m;
                 // a piece in which the row saw nothing has sum 0 (or NaN from a NaN score, which stays)
-                g = nr == kUnset ? (ls == 0.0f ? 0.0f : 1.0f) : ex2(-nr - top);
+                g[u] = set ? ex2(-rl[u].x - m) : rl[u].y == 0.0f ? 0.0f : 1.0f;
               }
               const int32_t m = min(32, parts - p0);
-#pragma unroll 4
+#pragma unroll 2
               for (int32_t i = 0; i < m; ++i) {
-                const float gi = __shfl_sync(0xffffffffu, g, i), li = __shfl_sync(0xffffffffu, ls, i);
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(piece_at(p0 + i) + c * 128 + lane * 4));
-                sum = __fmaf_rn(gi, li, sum);
-                if (gi != 0.0f) {
-                  acc.x = __fmaf_rn(gi, v.x, acc.x);
-                  acc.y = __fmaf_rn(gi, v.y, acc.y);
-                  acc.z = __fmaf_rn(gi, v.z, acc.z);
-                  acc.w = __fmaf_rn(gi, v.w, acc.w);
+                const float* po = piece_at(p0 + i) + lane * 4;
+                float4 v[kJoin];
+#pragma unroll
+                for (int u = 0; u < kJoin; ++u) v[u] = __ldcg(reinterpret_cast<const float4*>(po + min(cj + u, rows - 1) * 128));
+#pragma unroll
+                for (int u = 0; u < kJoin; ++u) {
+                  const float gi = __shfl_sync(0xffffffffu, g[u], i), li = __shfl_sync(0xffffffffu, rl[u].y, i);
+                  total_sum[u] = __fmaf_rn(gi, li, total_sum[u]);
+                  if (gi != 0.0f) {
+                    acc[u].x = __fmaf_rn(gi, v[u].x, acc[u].x);
+                    acc[u].y = __fmaf_rn(gi, v[u].y, acc[u].y);
+                    acc[u].z = __fmaf_rn(gi, v[u].z, acc[u].z);
+                    acc[u].w = __fmaf_rn(gi, v[u].w, acc[u].w);
+                  }
                 }
               }
             }
-            const float inv = sum == 0.0f ? 0.0f : __fdividef(1.0f, sum);
-            if (lane * 4 < a.c.dim) {
-              uint16_t* o = a.out + row_out[b][c] + lane * 4;
-              store_pair(o, bf16_pair(acc.x * inv, acc.y * inv), wide);
-              store_pair(o + 2, bf16_pair(acc.z * inv, acc.w * inv), wide);
+#pragma unroll
+            for (int u = 0; u < kJoin; ++u) {
+              const int c = cj + u;
+              if (c >= rows) break;
+              const float inv = total_sum[u] == 0.0f ? 0.0f : __fdividef(1.0f, total_sum[u]);
+              if (lane * 4 < a.c.dim) {
+                uint16_t* o = a.out + row_out[b][c] + lane * 4;
+                store_pair(o, bf16_pair(acc[u].x * inv, acc[u].y * inv), wide);
+                store_pair(o + 2, bf16_pair(acc[u].z * inv, acc[u].w * inv), wide);
+              }
+              if (lane == 0 && a.lse)
+                a.lse[row_lse[b][c]] = total_sum[u] == 0.0f ? -INFINITY : 0.69314718055994531f * (log2f(total_sum[u]) + top[u]);
             }
-            if (lane == 0 && a.lse)
-              a.lse[row_lse[b][c]] = sum == 0.0f ? -INFINITY : 0.69314718055994531f * (log2f(sum) + top);
           }
         }
       }
