@@ -1502,35 +1502,40 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
       constexpr int kOut = kCols / F::kStreams;
       const int r0 = F::kStreams == 2 ? wg * kOut : c0;
       if (wq * 32 < kHalves * 64 && r0 < rows) {
-        float o[kOut];
-        tmem_ld(o_item + r0, o);
+        // eight rows at a time, in a loop: the code is fetched once per item
+        constexpr int kStep = kOut < 8 ? kOut : 8;
+#pragma unroll 1
+        for (int i0 = r0; i0 < min(r0 + kOut, rows); i0 += kStep) {
+          float o[kStep];
+          tmem_ld(o_item + i0, o);
 #pragma unroll
-        for (int i = 0; i < kOut; ++i) o[i] = F::kStreams == 2 && sums[r0 + i] == 0.0f ? 0.0f : o[i] * sums[r0 + i];
-        if constexpr (F::kStreams == 2) {
-          float o1[kOut];
-          tmem_ld(o_item + kN + r0, o1);
+          for (int i = 0; i < kStep; ++i) o[i] = F::kStreams == 2 && sums[i0 + i] == 0.0f ? 0.0f : o[i] * sums[i0 + i];
+          if constexpr (F::kStreams == 2) {
+            float o1[kStep];
+            tmem_ld(o_item + kN + i0, o1);
 #pragma unroll
-          for (int i = 0; i < kOut; ++i)
-            if (sums[kN + r0 + i] != 0.0f) o[i] = __fmaf_rn(o1[i], sums[kN + r0 + i], o[i]);
-        }
-        if (kPacked)
-#pragma unroll
-          for (int i = 0; i < kOut; ++i) o[i] += csums[r0 + i];
-        if (whole) {
-          // even lanes take two channels of the even row, odd lanes of the odd one
-          const bool odd = lane & 1;
-          const bool in = (ch & ~1) < a.c.dim;
-#pragma unroll
-          for (int i = 0; i < kOut; i += 2) {
-            const int c = r0 + i + odd;
-            const float other = __shfl_xor_sync(0xffffffffu, odd ? o[i] : o[i + 1], 1);
-            const uint32_t pair = odd ? bf16_pair(other, o[i + 1]) : bf16_pair(o[i], other);
-            if (c < rows && in) store_pair(a.out + row_out[b][c] + (ch & ~1), pair, wide);
+            for (int i = 0; i < kStep; ++i)
+              if (sums[kN + i0 + i] != 0.0f) o[i] = __fmaf_rn(o1[i], sums[kN + i0 + i], o[i]);
           }
-        } else {
+          if (kPacked)
 #pragma unroll
-          for (int i = 0; i < kOut; ++i)
-            if (r0 + i < rows) __stcg(piece + (r0 + i) * 128 + ch, o[i]);
+            for (int i = 0; i < kStep; ++i) o[i] += csums[i0 + i];
+          if (whole) {
+            // even lanes take two channels of the even row, odd lanes of the odd one
+            const bool odd = lane & 1;
+            const bool in = (ch & ~1) < a.c.dim;
+#pragma unroll
+            for (int i = 0; i < kStep; i += 2) {
+              const int c = i0 + i + odd;
+              const float other = __shfl_xor_sync(0xffffffffu, odd ? o[i] : o[i + 1], 1);
+              const uint32_t pair = odd ? bf16_pair(other, o[i + 1]) : bf16_pair(o[i], other);
+              if (c < rows && in) store_pair(a.out + row_out[b][c] + (ch & ~1), pair, wide);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < kStep; ++i)
+              if (i0 + i < rows) __stcg(piece + (i0 + i) * 128 + ch, o[i]);
+          }
         }
       }
       if (stream == 0 && lt < kCols && c0 + lt < rows) {
