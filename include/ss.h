@@ -589,8 +589,9 @@ typedef struct {
   const ss_kv_cache* cache;
   const ss_page_pool* pool;     /* only the page table's four fields are used      */
   int32_t layer;
-  int32_t num_requests;
-  int32_t max_tokens;           /* >= every request's number of new tokens         */
+  int32_t num_requests;         /* at most 65535                                   */
+  int32_t max_tokens;           /* >= every request's number of new tokens; times
+                                   2 num_kv_heads below 2^31                       */
   int32_t total_tokens;         /* rows of k and v                                 */
   const int32_t* token_offsets; /* [num_requests + 1], or NULL: one token each     */
   const int32_t* table_rows;    /* [num_requests] each request's row of the page
@@ -620,7 +621,8 @@ ss_status ss_cache_read(const ss_append_args* args, ss_stream_t stream);
  * node's position).  A query that sees nothing (holes) gets out = 0 and
  * lse = -infinity.  Keys and values that a query does not see never reach its
  * result, whatever they hold.  A query that sees a NaN or an infinity gets
- * results that are not finite or, for an infinite key, weights of 0 and 1.
+ * results that are not finite or, for an infinite key, weights of 0 and 1
+ * (lse stays finite where only a value is not).
  *
  * Sums and softmax statistics are held in fp32; the weights are rounded to
  * bf16 before they meet the values.  The result does not depend on timing: the
@@ -628,10 +630,11 @@ ss_status ss_cache_read(const ss_append_args* args, ss_stream_t stream);
  *
  * out_status: SS_ROW_BAD_PARAM (a count outside [0, max_queries], with parents
  * above SS_TREE_MAX_NODES, query rows outside [0, total_queries), a negative
- * kv_len, a table row outside the table: the request's rows are not written;
- * or a parent outside [0, i): the node is taken as a child of the root),
- * SS_ROW_BAD_INDEX (slots beyond the table: they are holes), SS_ROW_TIMEOUT (a
- * bounded wait gave up: the request's rows are undefined).
+ * kv_len, kv_len plus the count above 2^31 - 256, a table row outside the
+ * table: the request's rows are not written; or a parent outside [0, i): the
+ * node is taken as a child of the root), SS_ROW_BAD_INDEX (slots beyond the
+ * table: they are holes), SS_ROW_TIMEOUT (a bounded wait gave up: the
+ * request's rows are undefined, and the workspace must be zeroed again).
  *
  * The workspace (ss_attention_workspace_size() bytes, 256-byte aligned) must
  * have been zeroed once (ss_workspace_init); calls that share one must not
@@ -640,9 +643,10 @@ typedef struct {
   const ss_kv_cache* cache;
   const ss_page_pool* pool;     /* only the page table's four fields are used      */
   int32_t layer;
-  int32_t num_requests;
+  int32_t num_requests;         /* at most 16384                                   */
   int32_t num_heads;            /* num_kv_heads times 1 .. 128                     */
-  int32_t max_queries;          /* >= every request's number of queries            */
+  int32_t max_queries;          /* >= every request's number of queries; times
+                                   num_heads below 2^31                           */
   int32_t total_queries;        /* rows of q and out                               */
   const int32_t* query_offsets; /* [num_requests + 1], or NULL: one query each     */
   const int32_t* table_rows;    /* as ss_append_args                               */

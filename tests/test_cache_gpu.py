@@ -282,6 +282,29 @@ def test_rows_that_see_nothing(ss, workspace, fmt):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+def test_lengths_far_beyond_the_table(ss, workspace, fmt):
+    # 200 requests whose lengths say 2^31 slots, of a table of four pages
+    n, page, heads, dim, far = 200, 16, 4, 64, 2 ** 31 - 300
+    rng = np.random.default_rng(8)
+    cache = make_cache(ss, rng, fmt, 8, 2, page, dim)
+    q = torch.randn(n, heads, dim, device="cuda").to(torch.bfloat16)
+    table = ints(rng.integers(0, 8, (n, 4)).tolist())
+    out, lse, st = torch.full_like(q, 7), torch.full((n, heads), 7.0, device="cuda"), ints([-1] * n)
+    ss.ss_cache_attention(cache, 0, q, out, table, ints([far] * n), workspace, st, lse=lse)
+    torch.cuda.synchronize()
+    assert st.tolist() == [3] * n
+    want, want_lse, st2 = torch.empty_like(q), torch.empty_like(lse), ints([-1] * n)
+    # all four pages are seen: the same as at the table's last slot
+    ss.ss_cache_attention(cache, 0, q, want, table, ints([4 * page - 1] * n), workspace, st2, lse=want_lse)
+    torch.cuda.synchronize()
+    assert st2.tolist() == [0] * n and torch.equal(out, want) and torch.equal(lse, want_lse)
+    # a window that lies beyond the table shows nothing, but for the sinks
+    ss.ss_cache_attention(cache, 0, q, out, table, ints([far] * n), workspace, st, lse=lse, window=500)
+    torch.cuda.synchronize()
+    assert not out.any() and bool((lse == -float("inf")).all()) and st.tolist() == [3] * n
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 def test_a_draft_that_is_not_finite_stays_on_its_branch(ss, workspace, fmt):
     p = Problem(ss, 27, fmt, [150], [40], 8, 2, 64, 16, tree=True)
     clean, clean_lse, _ = p.call(ss, workspace)
