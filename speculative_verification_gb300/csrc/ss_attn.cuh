@@ -27,10 +27,12 @@
 //   q.k = s_k (q.n) + m_k sum(q)
 //   sum_j p v = sum_j (p s_v) (n - 8) + sum_j p (m_v + 8 s_v),
 // the first in fp32 on the thread that owns the key, the second by rounding
-// p s_v to bf16 instead of p, plus one fp32 sum per row.
+// p s_v to f16, plus one fp32 sum per row.  f16 has the range for it because
+// the references then also count the keys' magnitudes (kSlack).
 //
-// Roundings: P (or p s_v) to bf16, the result to bf16; everything else is
-// fp32 (sums of p on the unrounded values).
+// Roundings: P to bf16 (4 bits: p s_v to f16, whose 11 bits leave only the
+// result's own rounding to see), the result to bf16; everything else is fp32
+// (sums of p on the unrounded values).
 //
 // The split.  The tiles of all (request, kv head, block of rows) items are put
 // in one line and cut into as many equal parts as there are CTAs (one per SM);
@@ -65,8 +67,11 @@ constexpr uint32_t kSleepNs = 50000;
 constexpr int kInfo = 16;                 // tiles whose page masks are kept
 constexpr int kPairs = 8;                 // tiles whose (s, m) pairs are kept
 constexpr float kUnset = 3.0e38f;         // in a piece: minus the reference of a row that has seen nothing
-constexpr float kSlack = 32.0f;           // how far a score (log2) may pass its row's reference
-constexpr float kDeep = 64.0f;            // how far the first ones may lie below the reference 0
+// How far a score (log2) may pass its row's reference, and how far the first
+// ones may lie below the reference 0.  4 bits: of the score plus its key's
+// magnitude, so that f16 holds the weights (65504 at most, 2^-24 their unit).
+template <bool kPacked> constexpr float kSlack = kPacked ? 14.0f : 32.0f;
+template <bool kPacked> constexpr float kDeep = kPacked ? 10.0f : 64.0f;
 constexpr int kSlotFloats = 128 * 130;    // one piece: up to 128 rows of 128 channels, r and l
 
 struct AttnArgs {
@@ -266,11 +271,12 @@ __device__ __forceinline__ uint64_t desc(uint32_t lo, uint32_t hi) {
   return static_cast<uint64_t>(lo) | (static_cast<uint64_t>(hi) << 32);
 }
 
-// Instruction descriptors: fp32 accumulator, M = 128.  kind::f16 with bf16 A
-// and B, `mn`: both M-/N-major instead of K-major; kind::f8f6f4 with e4m3.
-template <int kN>
+// Instruction descriptors: fp32 accumulator, M = 128.  kind::f16 with A and B
+// both bf16 or both f16, `mn`: both M-/N-major instead of K-major; kind::f8f6f4
+// with e4m3.
+template <int kN, bool kF16 = false>
 __device__ __forceinline__ constexpr uint32_t instr_desc(bool mn) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | (mn ? (3u << 15) : 0u) | (static_cast<uint32_t>(kN >> 3) << 17) |
+  return (1u << 4) | (kF16 ? 0u : (1u << 7) | (1u << 10)) | (mn ? (3u << 15) : 0u) | (static_cast<uint32_t>(kN >> 3) << 17) |
          (static_cast<uint32_t>(128 >> 4) << 24);
 }
 
@@ -423,6 +429,13 @@ __device__ __forceinline__ void tmem_ld(uint32_t t, float (&v)[kCount]) {
 __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// Two fp32 values as an f16 pair (a in the low half).
+__device__ __forceinline__ uint32_t f16_pair(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
   return r;
 }
 
@@ -985,7 +998,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
         if (elect_one()) {
 #pragma unroll F::kUnrollPV
           for (int kk = 0; kk < kTile / 16; ++kk)
-            umma(d, desc(va + kk * (16 * 128 >> 4), kHiV), desc(pa + kk * (16 * F::kPitch >> 4), kHiP), instr_desc<kN>(true),
+            umma(d, desc(va + kk * (16 * 128 >> 4), kHiV), desc(pa + kk * (16 * F::kPitch >> 4), kHiP), instr_desc<kN, kPacked>(true),
                  (t >= F::kStreams || kk > 0) ? 1u : 0u);
           umma_commit(vempty + s);
           umma_commit(pdone + b);
@@ -1220,6 +1233,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
         const bool masked = sink || there != every || j0 + kTile - 1 > (tree ? it.base - 1 : first_pos) ||
                             (a.window > 0 && j0 <= last_pos - a.window);
         float ka = a.scale_log2, kb = 0.0f, sv = 0.0f, wv = 0.0f;
+        float big = 0.0f;  // log2 of the key's values, rounded up: 0 where it does not matter
         bool poison = false;
         if (kPacked) {  // the tensor cores multiplied n / 512 and n - 8
           const uint32_t kp = k_pair[at % kPairs][lt], vp = v_pair[at % kPairs][lt];
@@ -1229,6 +1243,9 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
           wv = __fmaf_rn(8.0f, sv, bf16_hi(vp));
           poison = !(fabsf(wv) <= 3.0e38f);  // as below; a step that is not finite makes wv so
           if (poison) sv = wv = 0.0f;
+          // at most 2^big are s and |m + 8 s| / 16; 2^-80 stands for a row of zeros
+          const float top = fmaxf(sv, fabsf(wv) * 0.0625f);
+          big = static_cast<float>(max((__float_as_int(top) >> 23) - 126, -80));
         }
         uint32_t vis = 0xffffffffu;  // the rows that see this thread's key
         int32_t from = 0, node = -1;
@@ -1326,17 +1343,18 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 2; ++e) split(fma_2(z[e], two(ka, ka), y[e]), x[i + 2 * e], x[i + 2 * e + 1]);
         }
-        float least = 0.0f;
+        float least = INFINITY;
         if (fresh)
 #pragma unroll
-          for (int i = 0; i < kCols; ++i) least = fminf(least, ((vis >> i) & 1u) ? x[i] : 0.0f);
+          for (int i = 0; i < kCols; ++i) least = fminf(least, ((vis >> i) & 1u) ? x[i] : INFINITY);
         if (masked)
 #pragma unroll
           for (int i = 0; i < kCols; ++i) x[i] = ((vis >> i) & 1u) ? x[i] : -INFINITY;
         float most[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
         for (int i = 4; i < kCols; ++i) most[i & 3] = fmaxf(most[i & 3], x[i]);
-        const bool pass = bar_any(bar, 128, fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])) > kSlack || least < -kDeep);
+        const bool pass = bar_any(bar, 128, fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])) + big > kSlack<kPacked> ||
+                                            (fresh && least + big < -kDeep<kPacked>));
         if (fresh && !pass) {
           // the rows that see a key here may keep the reference 0
           uint32_t seen = 0xffffffffu;
@@ -1356,7 +1374,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
           // largest score of the tile
 #pragma unroll
           for (int i = 0; i < kCols; ++i) {
-            const float m = warp_max(x[i]);  // a NaN counts as nothing
+            const float m = warp_max(x[i] + big);  // a NaN counts as nothing
             if (lane == i) part[wq][h0 + i] = m;
           }
           bar_sync(bar, 128);
@@ -1364,7 +1382,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
             const int c = h0 + lt;
             const float m = fmaxf(fmaxf(part[0][c], part[1][c]), fmaxf(part[2][c], part[3][c]));
             // by the row's own scores alone, so that what other rows see changes no bit of it
-            const bool move = m > kSlack || (unset && m < -kDeep && m > -INFINITY);
+            const bool move = m > kSlack<kPacked> || (unset && m < -kDeep<kPacked> && m > -INFINITY);
             corr[c] = !move ? 1.0f : unset ? 0.0f : ex2(-m);  // 2^(old reference - new)
             shift[c] = move ? m : 0.0f;
             if (move) nref[c] -= m;
@@ -1411,7 +1429,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
               split(fma_2(p2, two(wv, wv), two(cs[i], cs[i + 1])), cs[i], cs[i + 1]);
               split(mul_2(p2, two(sv, sv)), p[0], p[1]);
             }
-            o4[e] = bf16_pair(p[0], p[1]);
+            o4[e] = kPacked ? f16_pair(p[0], p[1]) : bf16_pair(p[0], p[1]);
           }
           const uint32_t off = lt * F::kPitch + ((c0 & 63) + i8 * 8) * 2;
           *reinterpret_cast<uint4*>(pb + (off ^ ((off >> 3) & kSwz))) = make_uint4(o4[0], o4[1], o4[2], o4[3]);
@@ -1659,8 +1677,9 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
     // A byte n = 0..15 is the e4m3 number n / 512 (0..7 its subnormals, 8..15
     // the first binade), so K only takes its bits apart; it goes to tensor
     // memory (a key's lane is the thread's), which spares shared memory a write
-    // and the MMAs a read of the tile.  V becomes n - 8 in bf16: its weights
-    // need bf16's range, and as an M-major operand it is in shared memory.
+    // and the MMAs a read of the tile.  V becomes n - 8 in f16, whose 11
+    // bits for the weights halve the error (references: kSlack), and as an
+    // M-major operand it is in shared memory.
     const int key = (tid - 128 - F::kSoft) & 127, turn = ((tid - 128 - F::kSoft) >> 7) - 1;
     const bool is_v = turn >= 0;
 #pragma unroll 1
@@ -1691,10 +1710,10 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
             uint32_t o[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              // 128 + n in bf16 is 0x4300 | n; minus 136 leaves n - 8 exactly
-              uint32_t y;  // (w >> 4 i) & 0x000f000f | 0x43004300 in one instruction after the shift
-              asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(y) : "r"(w[e] >> (4 * i)), "r"(0x000f000fu), "r"(0x43004300u));
-              asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(o[i]) : "r"(y), "r"(0x43084308u));
+              // 1024 + n in f16 is 0x6400 | n; minus 1032 leaves n - 8 exactly
+              uint32_t y;  // (w >> 4 i) & 0x000f000f | 0x64006400 in one instruction after the shift
+              asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(y) : "r"(w[e] >> (4 * i)), "r"(0x000f000fu), "r"(0x64006400u));
+              asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(o[i]) : "r"(y), "r"(0x64086408u));
             }
             const int x = c * 4 + e;  // 8 channels
             *reinterpret_cast<uint4*>(dst + (x >> 3) * 16384 + (((x & 7) ^ (key & 7)) << 4)) =
