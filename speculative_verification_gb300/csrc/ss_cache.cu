@@ -129,7 +129,10 @@ __device__ __forceinline__ uint4 dequantise8(uint32_t w, uint32_t pair) {
 // lanes take kEach consecutive rows of one token (four where the heads are
 // even), so a token's page is looked up once for them and their loads are in
 // flight together; CTA (x, r) takes kGroups * kEach rows of request r, then a
-// grid's width further.
+// grid's width further.  4 x 2-6k tokens, 8 heads of 128 channels: 4 bits in
+// 32.6 us (bound by the rounding's instructions; 67 with a division per
+// channel), out in 21.6 (4.4 TB/s, bound by the loads' latency); bf16, 32 x 1-8
+// tokens: 4.4 us, the latency of lengths, table and rows one after the other.
 template <bool kPacked, bool kRead, int kEach>
 __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const AppendArgs a, const FastDiv by_token) {
   const int r = blockIdx.y;
@@ -428,6 +431,8 @@ __global__ void __launch_bounds__(kBook) fork_kernel(const PoolView p, int32_t n
   if (threadIdx.x == 0) *p.free_count = have - taken;
 }
 
+// Bound by HBM: 64 children, 32 layers, half-filled pages of 64 slots, 57 us
+// (66 with one load in flight per thread).
 // CTA (i, 2 * layer + K or V): the used slots of the last page of child i.
 __global__ void __launch_bounds__(kThreads) fork_copy_kernel(const PoolView p, const CacheView c, const int32_t* parent,
                                                              const int32_t* child, const int32_t* length,
@@ -485,7 +490,8 @@ constexpr int kPath = 64;  // accepted nodes whose places are held in shared mem
 // CTA (i, layer): thread t moves the same 16 bytes of every accepted row, in
 // the path's order: node j's place kv_len + 1 + j is at or before its source
 // kv_len + path[j] (the path is increasing and starts at 1 or more) and before
-// every later source, so no row is overwritten before it is read.
+// every later source, so no row is overwritten before it is read.  64 requests, 32
+// layers, up to 7 accepted rows: 13 us, the latency of path, table and rows.
 __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactArgs a) {
   __shared__ int64_t s_from[kPath], s_to[kPath], s_sfrom[kPath], s_sto[kPath];
   const int i = blockIdx.x, layer = blockIdx.y;
