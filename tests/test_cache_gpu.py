@@ -268,6 +268,22 @@ def test_scores_far_apart(ss, workspace, fmt):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("low,high,zeros", [(-60, -60, False), (60, 60, False), (100, 100, False), (-40, 40, False),
+                                            (-20, 0, True)])
+def test_values_of_every_size(ss, workspace, fmt, low, high, zeros):
+    # values far from 1, keys whose values differ by many powers of two, rows of zeros
+    rng = np.random.default_rng(abs(high) + 7)
+    for news, heads in (([3, 1], 4), ([8, 5], 16)):
+        p = Problem(ss, 31, fmt, [700, 40], news, heads, 2, 64, 16)
+        f = torch.from_numpy(2.0 ** rng.integers(low, high + 1, p.cache.v.shape[:4])).to(torch.bfloat16).cuda()
+        if zeros:
+            f[torch.from_numpy(rng.random(f.shape) < 0.3).cuda()] = 0
+        t = p.cache.v if fmt == "bf16" else p.cache.v_scale
+        t.mul_(f[..., None])
+        p.check(ss, workspace)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 def test_rows_that_see_nothing(ss, workspace, fmt):
     # the pages of some requests are holes: out = 0, lse = -inf
     p = Problem(ss, 25, fmt, [40, 200, 10], [2, 3, 1], 4, 2, 64, 16)
