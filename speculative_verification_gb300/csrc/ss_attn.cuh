@@ -1207,6 +1207,9 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
           proxy_fence();
           bar_sync(6, F::kSoft + 32);
         }
+      // The rows' references start at 0: before the barrier, behind which every
+      // warp reads them (the last item's readers have passed barriers since).
+      if (lt < kCols) nref[h0 + lt] = 0.0f;
       // (4 bits: the rows' sums and units come with the queries)
       const bool in = wait_or_dead((kPacked ? qfull : mfull) + b, (k / kNQ) & 1, dead);
       if (bar_any(5, F::kSoft, !in)) break;  // the same decision for every softmax thread
@@ -1217,7 +1220,6 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
       if (kPacked)
 #pragma unroll
         for (int n = 0; n < kCols; ++n) cs[n] = 0.0f;
-      if (lt < kCols) nref[h0 + lt] = 0.0f;
       bool unset = true;  // thread i of the warpgroup: row i has seen no key yet
       bool fresh = true;  // some row has not
       const uint32_t o_item = tmem + F::kOCol + (k & 1) * F::kStreams * kN + lanes, o_base = o_item + h0;
