@@ -6,12 +6,14 @@
 //   p_nj = 2^(x_nj - r_n),  out_n = sum_j p_nj v_j / sum_j p_nj,
 //   lse_n = ln 2 (r_n + log2 sum_j p_nj).
 // Any r_n gives the same result; it only has to keep the powers in range.  The
-// running maximum is the usual choice; here r_n starts at 0 and moves only when
+// running maximum is the usual choice; here (bf16) r_n starts at 0 and moves only when
 // some x_nj passes it by more than 32 (or the first ones lie below -64), so the
 // accumulated sums are rarely rescaled and a tile needs no maximum over its
 // keys at all (2 x 4096-token prompt chunks: 390 us when every item's first
 // tile took its maximum and masks were tested per row, 341 since).  p up to 2^32 and what lies 2^-126 below rounds no worse: bf16
-// and fp32 are relative and have the same range.
+// and fp32 are relative and have the same range.  Over 4 bits the weights are
+// f16, whose range is short: there r_n is set at the first keys, and moves
+// when a later one passes them by much (kSlack, kTop below).
 //
 // The transposed product.  A tile is 128 keys of one kv head; the rows are the
 // new tokens of one request times the query heads that share the kv head,
@@ -29,11 +31,13 @@
 //   sum_j p v = sum_j (p s_v) (n - 8) + sum_j p (m_v + 8 s_v),
 // the first in fp32 on the thread that owns the key, the second by rounding
 // p s_v to f16, plus one fp32 sum per row.  f16 has the range for it because
-// the references then also count the keys' magnitudes (kSlack).
+// the references then also count the keys' magnitudes and keep the largest
+// weight near f16's upper end (kSlack, kTop).
 //
 // Roundings: P to bf16 (4 bits: p s_v to f16, whose 11 bits leave only the
-// result's own rounding to see), the result to bf16; everything else is fp32
-// (sums of p on the unrounded values).
+// result's own rounding to see; weights 2^22 below a row's largest and smaller
+// lose bits, 2^33 below it they are 0), the result to bf16; everything else is
+// fp32 (sums of p on the unrounded values).
 //
 // The split.  The tiles of all (request, kv head, block of rows) items are put
 // in one line and cut into as many equal parts as there are CTAs (one per SM);
@@ -77,11 +81,17 @@ constexpr uint32_t kSleepNs = 50000;
 constexpr int kInfo = 16;                 // tiles whose page masks are kept
 constexpr int kPairs = 8;                 // tiles whose (s, m) pairs are kept
 constexpr float kUnset = 3.0e38f;         // in a piece: minus the reference of a row that has seen nothing
-// How far a score (log2) may pass its row's reference, and how far the first
-// ones may lie below the reference 0.  4 bits: of the score plus its key's
-// magnitude, so that f16 holds the weights (65504 at most, 2^-24 their unit).
-template <bool kPacked> constexpr float kSlack = kPacked ? 14.0f : 32.0f;
-template <bool kPacked> constexpr float kDeep = kPacked ? 10.0f : 64.0f;
+// How far a score (log2) may pass its row's reference, and for bf16 how far the
+// first ones may lie below the reference 0.  4 bits: of the score plus its key's
+// magnitude, so that f16 holds the weights (65504 at most, 2^-24 their unit), and
+// a reference that is set or moved puts the largest of them at 2^kTop: from its
+// first key on a row's largest weight is in [2^8, 2^15].  Beside one sink 2^20
+// other keys that count as much together then stand at 2^-12 or above, where f16
+// still has all its bits (down to 2^-14); and 7 binades, 4.9 of a score, are left
+// before the next move.
+template <bool kPacked> constexpr float kSlack = kPacked ? 15.0f : 32.0f;
+constexpr float kDeep = 64.0f;
+constexpr float kTop = 8.0f;
 constexpr int kSlotFloats = 128 * 130;    // one piece: up to 128 rows of 128 channels, r and l
 
 struct AttnArgs {
@@ -1358,7 +1368,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
           for (int e = 0; e < 2; ++e) split(fma_2(z[e], two(ka, ka), y[e]), x[i + 2 * e], x[i + 2 * e + 1]);
         }
         float least = INFINITY;
-        if (fresh)
+        if (!kPacked && fresh)
 #pragma unroll
           for (int i = 0; i < kCols; ++i) least = fminf(least, ((vis >> i) & 1u) ? x[i] : INFINITY);
         if (masked)
@@ -1367,9 +1377,10 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
         float most[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
         for (int i = 4; i < kCols; ++i) most[i & 3] = fmaxf(most[i & 3], x[i]);
-        const bool pass = bar_any(bar, 128, fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])) + big > kSlack<kPacked> ||
-                                            (fresh && least + big < -kDeep<kPacked>));
-        if (fresh && !pass) {
+        bool pass = bar_any(bar, 128, fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])) + big > kSlack<kPacked> ||
+                                      (!kPacked && fresh && least < -kDeep));
+        if (kPacked) pass |= fresh;  // a row's first keys set its reference
+        if (!kPacked && fresh && !pass) {
           // the rows that see a key here may keep the reference 0
           uint32_t seen = 0xffffffffu;
           if (masked) {
@@ -1383,9 +1394,9 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
           fresh = masked && bar_any(bar, 128, lt < kCols && c0 + lt < it.rows && unset);
         }
         if (pass) {
-          // some row's score passes its reference by too much (or is far below
-          // 0 and the row has no reference yet): the new reference is the row's
-          // largest score of the tile
+          // some row's score passes its reference by too much (or the row has
+          // no reference yet; bf16: and its scores are far below 0): the new
+          // reference is the row's largest score of the tile (4 bits: kTop below)
 #pragma unroll
           for (int i = 0; i < kCols; ++i) {
             const float m = warp_max(x[i] + big);  // a NaN counts as nothing
@@ -1396,10 +1407,11 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
             const int c = h0 + lt;
             const float m = fmaxf(fmaxf(part[0][c], part[1][c]), fmaxf(part[2][c], part[3][c]));
             // by the row's own scores alone, so that what other rows see changes no bit of it
-            const bool move = m > kSlack<kPacked> || (unset && m < -kDeep<kPacked> && m > -INFINITY);
-            corr[c] = !move ? 1.0f : unset ? 0.0f : ex2(-m);  // 2^(old reference - new)
-            shift[c] = move ? m : 0.0f;
-            if (move) nref[c] -= m;
+            const bool move = m > kSlack<kPacked> || (unset && m > -INFINITY && (kPacked || m < -kDeep));
+            const float by = kPacked ? m - kTop : m;
+            corr[c] = !move ? 1.0f : unset ? 0.0f : ex2(-by);  // 2^(old reference - new)
+            shift[c] = move ? by : 0.0f;
+            if (move) nref[c] -= by;
             unset = unset && !(m > -INFINITY);
           }
           // is there a row left that has seen nothing?

@@ -62,3 +62,63 @@ def test_an_item_starts_from_references_of_its_own(ss, workspace, fmt, heads):
                 # scores of up to 90 + 64 products, each to 2^-24 of it
                 assert (np.abs(lse[i::3].cpu().numpy() - l) <= 2.0 ** -17 * (90 + 64)).all(), far[i]
         assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+
+
+@pytest.mark.parametrize("spread", [1.0, 0.02])
+@pytest.mark.parametrize("heads", [4, 16, 32, 64])
+def test_a_sink_over_a_long_4_bit_context(ss, workspace, heads, spread):
+    """One key takes about half of the mass of 64k keys, and all scores have a
+    constant added to them, -24 to 12: each of the others weighs 2^-16 of the
+    first, and together they count as much.
+
+    Tolerance: the result's rounding to bf16 (2^-8 of it); each weight's to f16, 11 significant bits, so 2^-11 of
+    sum p (s |n - 8| + |m + 8 s|) / sum p; and half as much for the fp32 scores, exponentials and sums.  A weight that
+    loses bits because f16's range ends is not in it."""
+    dim, page, keys = 128, 1024, 1 << 16
+    gen = torch.Generator(device="cuda").manual_seed(heads)
+    n = torch.full((1, keys // page, 1, page, dim), 8, dtype=torch.uint8, device="cuda")
+    n[..., 2:] = torch.randint(6, 11, n[..., 2:].shape, generator=gen, device="cuda", dtype=torch.uint8)
+    n[..., 1] = 15
+    n[0, 0, 0, 0, 0] = 15  # the sink is the first key: 7/8 in channel 0, the others 0
+    v = torch.randint(0, 16, n.shape, generator=gen, device="cuda", dtype=torch.uint8)
+
+    def packed(x):
+        x = x.unflatten(-1, (-1, 8))[..., [0, 2, 4, 6, 1, 3, 5, 7]].flatten(-2)
+        return x[..., 0::2] | (x[..., 1::2] << 4)
+
+    pairs = []
+    for step, low in ((0.125, -1.0), (0.25 * spread, -7.5 * 0.25 * spread)):
+        pair = torch.empty(1, keys // page, 1, page, 2, device="cuda")
+        pair[..., 0], pair[..., 1] = step, low
+        pairs.append(pair.to(torch.bfloat16))
+    cache = ss.KVCache(packed(n), packed(v), *pairs)
+    # enough requests for an item per SM; they take turns at the constants and share the pages
+    count = torch.cuda.get_device_properties(0).multi_processor_count
+    consts = [x * 0.5 for x in range(-48, 25)]
+    q = torch.randn(len(consts), heads, dim, generator=gen, device="cuda") * 0.05
+    q[..., 0] = 12.0 / 0.875
+    q[..., 1] = torch.tensor(consts, device="cuda")[:, None] / 0.875
+    q = q.to(torch.bfloat16)
+    kind = torch.arange(count, device="cuda") % len(consts)
+    batch = q[kind].contiguous()
+    out, lse, st = torch.full_like(batch, 7), torch.full((count, heads), 7.0, device="cuda"), ints([-1] * count)
+    ss.ss_cache_attention(cache, 0, batch, out, ints([list(range(keys // page))] * count), ints([keys - 1] * count), workspace,
+                          st, scale=1.0, lse=lse)
+    torch.cuda.synchronize()
+    assert not st.any()
+    k64 = (n[0, :, 0].flatten(0, 1).double() * 0.125 - 1.0)
+    s, m = (pairs[1][0, 0, 0, 0, i].double() for i in (0, 1))
+    v64 = v[0, :, 0].flatten(0, 1).double()
+    x = q.double().flatten(0, 1) @ k64.T
+    p = torch.softmax(x, -1)
+    want = (p @ (s * v64 + m)).view(len(consts), heads, dim)
+    mag = (p @ (s * (v64 - 8).abs() + (m + 8 * s).abs())).view(len(consts), heads, dim)
+    share = p[:, 0]
+    assert 0.3 < float(share.min()) and float(share.max()) < 0.95
+    err = (out.double() - want[kind]).abs()
+    tol = (2.0 ** -8 + 2.0 ** -12) * want.abs() + (2.0 ** -11 + 2.0 ** -12) * mag
+    worst = (err / tol[kind]).amax((1, 2))
+    assert float(worst.max()) <= 1, [(consts[i], round(float(worst[i]), 1)) for i in range(len(consts)) if worst[i] > 1]
+    reach = (q.double().abs().flatten(0, 1) @ k64.abs().T).amax(-1).view(len(consts), heads)
+    want_lse = torch.logsumexp(x, -1).view(len(consts), heads)
+    assert ((lse.double() - want_lse[kind]).abs() <= 2.0 ** -17 * (reach + 1)[kind]).all()
