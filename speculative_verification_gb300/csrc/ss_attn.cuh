@@ -7,11 +7,13 @@
 //   lse_n = ln 2 (r_n + log2 sum_j p_nj).
 // Any r_n gives the same result; it only has to keep the powers in range.  The
 // running maximum is the usual choice; here (bf16) r_n starts at 0 and moves only when
-// some x_nj passes it by more than 32 (or the first ones lie below -64), so the
+// some x_nj passes it by more than 16 (or the first ones lie below -32), so the
 // accumulated sums are rarely rescaled and a tile needs no maximum over its
 // keys at all (2 x 4096-token prompt chunks: 390 us when every item's first
-// tile took its maximum and masks were tested per row, 341 since).  p up to 2^32 and what lies 2^-126 below rounds no worse: bf16
-// and fp32 are relative and have the same range.  Over 4 bits the weights are
+// tile took its maximum and masks were tested per row, 341 since).  Weights in
+// [2^-32, 2^16] round no worse than those around 1, as bf16 is relative; but
+// they meet the values in fp32, which therefore have 2^-16 of its range at the
+// upper end and 2^32 at the lower one.  Over 4 bits the weights are
 // f16, whose range is short: there r_n is set at the first keys, and moves
 // when a later one passes them by much (kSlack, kTop below).
 //
@@ -82,15 +84,16 @@ constexpr int kInfo = 16;                 // tiles whose page masks are kept
 constexpr int kPairs = 8;                 // tiles whose (s, m) pairs are kept
 constexpr float kUnset = 3.0e38f;         // in a piece: minus the reference of a row that has seen nothing
 // How far a score (log2) may pass its row's reference, and for bf16 how far the
-// first ones may lie below the reference 0.  4 bits: of the score plus its key's
+// first ones may lie below the reference 0: as far as costs nothing (8 and 16:
+// prompt 311 -> 324 us, trees 85 -> 92; 32 and 64 no faster).  4 bits: of the score plus its key's
 // magnitude, so that f16 holds the weights (65504 at most, 2^-24 their unit), and
 // a reference that is set or moved puts the largest of them at 2^kTop: from its
 // first key on a row's largest weight is in [2^8, 2^15].  Beside one sink 2^20
 // other keys that count as much together then stand at 2^-12 or above, where f16
 // still has all its bits (down to 2^-14); and 7 binades, 4.9 of a score, are left
 // before the next move.
-template <bool kPacked> constexpr float kSlack = kPacked ? 15.0f : 32.0f;
-constexpr float kDeep = 64.0f;
+template <bool kPacked> constexpr float kSlack = kPacked ? 15.0f : 16.0f;
+constexpr float kDeep = 32.0f;
 constexpr float kTop = 8.0f;
 constexpr int kSlotFloats = 128 * 130;    // one piece: up to 128 rows of 128 channels, r and l
 

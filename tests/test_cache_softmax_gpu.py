@@ -122,3 +122,38 @@ def test_a_sink_over_a_long_4_bit_context(ss, workspace, heads, spread):
     reach = (q.double().abs().flatten(0, 1) @ k64.abs().T).amax(-1).view(len(consts), heads)
     want_lse = torch.logsumexp(x, -1).view(len(consts), heads)
     assert ((lse.double() - want_lse[kind]).abs() <= 2.0 ** -17 * (reach + 1)[kind]).all()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("heads", [2, 32, 128])
+@pytest.mark.parametrize("power", [92, -80])
+def test_large_and_small_values_with_large_and_small_scores(ss, workspace, fmt, heads, power):
+    # Scores around -44 to 42 (64 powers of two both ways) with values around 2^92 and 2^-80, 700 keys: the products of
+    # weights and values stay in fp32's range.  The file's own tolerance: nothing is lost at either end.
+    rng = np.random.default_rng(power + 100)
+    dim, page, keys = 64, 16, 700
+    entries = -(-keys // page)
+    cache = make_cache(ss, rng, fmt, entries, 1, page, dim)
+    if fmt == "bf16":
+        cache.k[..., 0] = 1.0
+        cache.v.mul_(2.0 ** power)
+    else:
+        cache.k[..., 0] |= 15
+        cache.k_scale[..., 0], cache.k_scale[..., 1] = 0.125, 1 - 15 * 0.125
+        cache.v_scale.mul_(2.0 ** power)
+    consts = list(range(-44, 43, 2))
+    q = rng.standard_normal((len(consts), heads, dim)) * 0.1
+    q[:, :, 0] = np.array(consts)[:, None]
+    q = torch.from_numpy(R.bf16(q)).to(torch.bfloat16).cuda()
+    out, st = torch.full_like(q, 7), ints([-1] * len(consts))
+    ss.ss_cache_attention(cache, 0, q, out, ints([list(range(entries))] * len(consts)), ints([keys - 1] * len(consts)),
+                          workspace, st, scale=1.0)
+    torch.cuda.synchronize()
+    assert not st.any()
+    k, v, mv = (x[:, 0].reshape(-1, dim)[:keys] for x in dense(cache))
+    x = np32(q).astype(np.float64) @ k.T
+    p = np.exp(x - x.max(-1, keepdims=True))
+    p /= p.sum(-1, keepdims=True)
+    o, m = p @ v, p @ mv
+    bad = ~(np.abs(np32(out) - o) <= 2.0 ** -8 * (np.abs(o) + m) * (1 + 1 / 16))
+    assert not bad.any(), [consts[i] for i in range(len(consts)) if bad[i].any()]
