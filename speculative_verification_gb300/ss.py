@@ -549,21 +549,24 @@ def ss_tree_verify(target_logits, node_offsets, parents, node_tokens, draft_prob
 # ---------------------------------------------------------- paged cache --
 
 
-def _want(t, name, dtype, shape=None):
-    """A device tensor's pointer, after the checks that the C entry cannot
-    make: its type, its shape and that it is contiguous."""
-    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous() or (shape is not None and t.shape != shape):
-        raise SSError("%s: want a contiguous %s device tensor%s, got %s %s on %s" %
-                      (name, dtype, "" if shape is None else " of shape %s" % (shape,), t.dtype, tuple(t.shape), t.device))
+def _want(t, device, name, dtype, shape=None):
+    """A tensor's pointer, after the checks that the C entry cannot make: the
+    GPU it is on, its type, its shape and that it is contiguous."""
+    if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous() or (shape is not None and t.shape != shape):
+        raise SSError("%s: want a contiguous %s tensor%s on cuda:%d, got %s %s on %s" %
+                      (name, dtype, "" if shape is None else " of shape %s" % (shape,), device, t.dtype, tuple(t.shape),
+                       t.device))
     return t.data_ptr()
 
 
-def _raw_stream(stream):
-    """The CUDA stream handle as an integer."""
+def _raw_stream(stream, device):
+    """The CUDA stream handle as an integer, for a call on `device`'s memory."""
     import torch
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    if device < 0:
+        raise SSError("want the cache or the pool on a GPU, it is on the host")
+    if device != torch.cuda.current_device() or (stream is not None and stream.device_index != device):
+        raise SSError("want cuda:%d, where the cache or the pool is, as the current device and the stream's" % device)
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
 
 def _packer(cls):
@@ -605,11 +608,13 @@ class KVCache:
     def __init__(self, k, v, k_scale=None, v_scale=None):
         import torch
         packed = k_scale is not None
+        self.device = k.get_device()  # -1: the host; the calls refuse it
         want = torch.uint8 if packed else torch.bfloat16
         for t in (k, v):
-            if t.dim() != 5 or t.dtype != want or t.shape != k.shape or t.stride() != k.stride() or t.stride(4) != 1:
+            if t.dim() != 5 or t.dtype != want or t.shape != k.shape or t.stride() != k.stride() or t.stride(4) != 1 or \
+                    t.get_device() != self.device:
                 raise SSError("KVCache: want k and v as [layers, pages, kv heads, page size, row] %s tensors of the same "
-                              "shape and strides with contiguous rows" % want)
+                              "shape and strides with contiguous rows, on one device" % want)
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.format = "int4" if packed else "bf16"
         layers, self.num_pages, self.num_kv_heads, self.page_size, row = k.shape
@@ -620,9 +625,9 @@ class KVCache:
         if packed:
             for t in (k_scale, v_scale):
                 if t is None or t.dtype != torch.bfloat16 or t.shape != (*k.shape[:4], 2) or \
-                        t.stride() != k_scale.stride() or t.stride()[3:] != (2, 1):
+                        t.stride() != k_scale.stride() or t.stride()[3:] != (2, 1) or t.get_device() != self.device:
                     raise SSError("KVCache: want k_scale and v_scale as [layers, pages, kv heads, page size, 2] bf16 "
-                                  "tensors of the same strides, a page's pairs next to each other")
+                                  "tensors of the same strides, a page's pairs next to each other, on k's device")
             c.k_scale, c.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
             c.scale_layer_stride, c.scale_page_stride, c.scale_head_stride = (_span(k_scale, i) * 2 for i in range(3))
         self.struct = c
@@ -657,16 +662,17 @@ class PagePool:
 
     def __init__(self, page_table, ref_count, free_pages, free_count, page_size):
         import torch
-        pages = ref_count.numel()
-        if page_table.dim() != 2 or page_table.dtype != torch.int32 or page_table.stride(1) != 1:
-            raise SSError("PagePool: want page_table as [rows, entries] int32 with contiguous rows")
+        pages, device = ref_count.numel(), page_table.get_device()
+        if page_table.dim() != 2 or page_table.dtype != torch.int32 or page_table.stride(1) != 1 or device < 0:
+            raise SSError("PagePool: want page_table as [rows, entries] int32 device tensor with contiguous rows")
+        self.device = device
         self.page_table, self.ref_count, self.free_pages, self.free_count = page_table, ref_count, free_pages, free_count
         self.page_size = page_size
         rows, entries = page_table.shape
         self.struct = ss_page_pool(rows, entries, page_table.stride(0) if rows > 1 else entries, page_table.data_ptr(),
-                                   pages, page_size, _want(ref_count, "ref_count", torch.int32, (pages,)),
-                                   _want(free_pages, "free_pages", torch.int32, (pages,)),
-                                   _want(free_count, "free_count", torch.int32, (1,)))
+                                   pages, page_size, _want(ref_count, device, "ref_count", torch.int32, (pages,)),
+                                   _want(free_pages, device, "free_pages", torch.int32, (pages,)),
+                                   _want(free_count, device, "free_count", torch.int32, (1,)))
         self.ref = C.pointer(self.struct)
         self.address = C.addressof(self.struct)
 
@@ -683,10 +689,14 @@ def _with_table(packer, page_table, cache):
     """A buffer for a call's arguments, with the ss_page_pool of a bare page
     table behind them, and the address of the page table's structure."""
     if isinstance(page_table, PagePool):
+        if page_table.device != cache.device:
+            raise SSError("page_table: want the pool on the cache's device")
         return C.create_string_buffer(packer.size), page_table.address
     import torch
-    if page_table.dtype is not torch.int32 or page_table.dim() != 2 or page_table.stride(1) != 1 or not page_table.is_cuda:
-        raise SSError("page_table: want a PagePool or a [rows, entries] int32 device tensor with contiguous rows")
+    if page_table.dtype is not torch.int32 or page_table.dim() != 2 or page_table.stride(1) != 1 or \
+            page_table.get_device() != cache.device:
+        raise SSError("page_table: want a PagePool or a [rows, entries] int32 tensor with contiguous rows on the cache's "
+                      "device")
     rows, entries = page_table.shape
     buf = C.create_string_buffer(packer.size + _POOL.size)
     _POOL.pack_into(buf, packer.size, rows, entries, page_table.stride(0) if rows > 1 else entries,
@@ -696,20 +706,20 @@ def _with_table(packer, page_table, cache):
 
 def _rows_call(name, cache, layer, k, v, page_table, kv_len, status, token_offsets, max_tokens, table_rows, stream):
     import torch
-    n, i32, shape = kv_len.numel(), torch.int32, k.shape
-    stride = k.stride()
-    if k.dtype is not torch.bfloat16 or v.dtype is not torch.bfloat16 or not k.is_cuda or not v.is_cuda or \
+    n, i32, shape, dev = kv_len.numel(), torch.int32, k.shape, cache.device
+    stride, handle = k.stride(), _raw_stream(stream, dev)
+    if k.dtype is not torch.bfloat16 or v.dtype is not torch.bfloat16 or k.get_device() != dev or v.get_device() != dev or \
             len(shape) != 3 or v.shape != shape or v.stride() != stride or stride[2] != 1 or \
             shape[1] != cache.num_kv_heads or shape[2] != cache.head_dim:
-        raise SSError("want k and v as [tokens, %d, %d] bf16 device tensors of the same strides with contiguous rows"
-                      % (cache.num_kv_heads, cache.head_dim))
+        raise SSError("want k and v as [tokens, %d, %d] bf16 tensors of the same strides with contiguous rows on cuda:%d"
+                      % (cache.num_kv_heads, cache.head_dim, dev))
     buf, table = _with_table(_APPEND, page_table, cache)
     _APPEND.pack_into(buf, 0, cache.address, table, layer, n, 1 if max_tokens is None else max_tokens, shape[0],
-                      0 if token_offsets is None else _want(token_offsets, "token_offsets", i32, (n + 1,)),
-                      0 if table_rows is None else _want(table_rows, "table_rows", i32, (n,)),
-                      _want(kv_len, "kv_len", i32), k.data_ptr(), v.data_ptr(), stride[0], stride[1],
-                      _want(status, "status", i32, (n,)))
-    _check(_quick_call(name, [C.c_char_p, C.c_void_p])(buf, _raw_stream(stream)))
+                      0 if token_offsets is None else _want(token_offsets, dev, "token_offsets", i32, (n + 1,)),
+                      0 if table_rows is None else _want(table_rows, dev, "table_rows", i32, (n,)),
+                      _want(kv_len, dev, "kv_len", i32), k.data_ptr(), v.data_ptr(), stride[0], stride[1],
+                      _want(status, dev, "status", i32, (n,)))
+    _check(_quick_call(name, [C.c_char_p, C.c_void_p])(buf, handle))
 
 
 def ss_cache_append(cache, layer, k, v, page_table, kv_len, status, *, token_offsets=None, max_tokens=None,
@@ -747,43 +757,51 @@ def ss_cache_attention(cache, layer, q, out, page_table, kv_len, workspace, stat
     query_offsets None: one query per request; parents: a draft tree per
     request, as ss_tree_verify takes it; scale None: 1 / sqrt(head dim)."""
     import torch
-    i32, n, shape = torch.int32, kv_len.numel(), q.shape
-    qs, os_ = q.stride(), out.stride()
-    if q.dtype is not torch.bfloat16 or out.dtype is not torch.bfloat16 or not q.is_cuda or not out.is_cuda or \
-            len(shape) != 3 or out.shape != shape or qs[2] != 1 or os_[2] != 1 or shape[2] != cache.head_dim:
-        raise SSError("want q and out as [tokens, heads, %d] bf16 device tensors with contiguous rows" % cache.head_dim)
+    i32, n, shape, dev = torch.int32, kv_len.numel(), q.shape, cache.device
+    qs, os_, handle = q.stride(), out.stride(), _raw_stream(stream, dev)
+    if q.dtype is not torch.bfloat16 or out.dtype is not torch.bfloat16 or q.get_device() != dev or \
+            out.get_device() != dev or len(shape) != 3 or out.shape != shape or qs[2] != 1 or os_[2] != 1 or \
+            shape[2] != cache.head_dim:
+        raise SSError("want q and out as [tokens, heads, %d] bf16 tensors with contiguous rows on cuda:%d"
+                      % (cache.head_dim, dev))
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise SSError("workspace: want a contiguous tensor on cuda:%d, got one on %s" % (dev, workspace.device))
     total, heads = shape[0], shape[1]
     buf, table = _with_table(_ATTENTION, page_table, cache)
     _ATTENTION.pack_into(buf, 0, cache.address, table, layer, n, heads, 1 if max_queries is None else max_queries, total,
-                         0 if query_offsets is None else _want(query_offsets, "query_offsets", i32, (n + 1,)),
-                         0 if table_rows is None else _want(table_rows, "table_rows", i32, (n,)),
-                         _want(kv_len, "kv_len", i32),
-                         0 if parents is None else _want(parents, "parents", i32, (total,)),
+                         0 if query_offsets is None else _want(query_offsets, dev, "query_offsets", i32, (n + 1,)),
+                         0 if table_rows is None else _want(table_rows, dev, "table_rows", i32, (n,)),
+                         _want(kv_len, dev, "kv_len", i32),
+                         0 if parents is None else _want(parents, dev, "parents", i32, (total,)),
                          q.data_ptr(), qs[0], qs[1], out.data_ptr(), os_[0], os_[1],
-                         0 if lse is None else _want(lse, "lse", torch.float32, (total, heads)),
+                         0 if lse is None else _want(lse, dev, "lse", torch.float32, (total, heads)),
                          cache.head_dim ** -0.5 if scale is None else scale, window, sinks,
-                         _want(status, "status", i32, (n,)))
+                         _want(status, dev, "status", i32, (n,)))
     fn = _quick_call("ss_cache_attention", [C.c_char_p, C.c_void_p, C.c_size_t, C.c_void_p])
-    _check(fn(buf, workspace.data_ptr(), workspace.numel() * workspace.element_size(), _raw_stream(stream)))
+    _check(fn(buf, workspace.data_ptr(), workspace.numel() * workspace.element_size(), handle))
 
 
 def ss_pages_reserve(pool, from_len, to_len, status, *, table_rows=None, stream=None):
     """Pages from the pool for the slots [from_len, to_len) of each row."""
     import torch
-    i32, n = torch.int32, from_len.numel()
-    _check(load().ss_pages_reserve(pool.ref, n, None if table_rows is None else _want(table_rows, "table_rows", i32, (n,)),
-                                   _want(from_len, "from_len", i32), _want(to_len, "to_len", i32, (n,)),
-                                   _want(status, "status", i32, (n,)), _raw_stream(stream)))
+    dev, i32, n = pool.device, torch.int32, from_len.numel()
+    _check(load().ss_pages_reserve(pool.ref, n,
+                                   None if table_rows is None else _want(table_rows, dev, "table_rows", i32, (n,)),
+                                   _want(from_len, dev, "from_len", i32), _want(to_len, dev, "to_len", i32, (n,)),
+                                   _want(status, dev, "status", i32, (n,)), _raw_stream(stream, dev)))
 
 
 def ss_pages_fork(pool, cache, parent, child, length, status, *, stream=None):
     """Table rows `child` become copies of rows `parent`: full pages shared,
     the partly filled last one copied in every layer."""
     import torch
-    i32, n = torch.int32, parent.numel()
-    _check(load().ss_pages_fork(pool.ref, cache.ref, n, _want(parent, "parent", i32), _want(child, "child", i32, (n,)),
-                                _want(length, "length", i32, (n,)), _want(status, "status", i32, (n,)),
-                                _raw_stream(stream)))
+    dev, i32, n = pool.device, torch.int32, parent.numel()
+    if cache.device != dev:
+        raise SSError("want the cache on the pool's device")
+    _check(load().ss_pages_fork(pool.ref, cache.ref, n, _want(parent, dev, "parent", i32),
+                                _want(child, dev, "child", i32, (n,)),
+                                _want(length, dev, "length", i32, (n,)), _want(status, dev, "status", i32, (n,)),
+                                _raw_stream(stream, dev)))
 
 
 def ss_pages_compact(pool, cache, kv_len, path, num_accepted, verify_status, new_len, status, *, table_rows=None,
@@ -791,26 +809,29 @@ def ss_pages_compact(pool, cache, kv_len, path, num_accepted, verify_status, new
     """After ss_tree_verify: the accepted nodes' rows to consecutive slots, in
     every layer; new_len = kv_len + 1 + num_accepted.  path: out_path."""
     import torch
-    i32, n = torch.int32, kv_len.numel()
+    dev, i32, n = pool.device, torch.int32, kv_len.numel()
     if path.dim() != 2 or path.shape[0] != n:
         raise SSError("path: want ss_tree_verify's out_path, [%d, nodes]" % n)
+    if cache.device != dev:
+        raise SSError("want the cache on the pool's device")
     _check(load().ss_pages_compact(pool.ref, cache.ref, n,
-                                   None if table_rows is None else _want(table_rows, "table_rows", i32, (n,)),
-                                   _want(kv_len, "kv_len", i32), _want(path, "path", i32), path.shape[1],
-                                   _want(num_accepted, "num_accepted", i32, (n,)),
-                                   None if verify_status is None else _want(verify_status, "verify_status", i32, (n,)),
-                                   _want(new_len, "new_len", i32, (n,)), _want(status, "status", i32, (n,)),
-                                   _raw_stream(stream)))
+                                   None if table_rows is None else _want(table_rows, dev, "table_rows", i32, (n,)),
+                                   _want(kv_len, dev, "kv_len", i32), _want(path, dev, "path", i32), path.shape[1],
+                                   _want(num_accepted, dev, "num_accepted", i32, (n,)),
+                                   None if verify_status is None else _want(verify_status, dev, "verify_status", i32, (n,)),
+                                   _want(new_len, dev, "new_len", i32, (n,)), _want(status, dev, "status", i32, (n,)),
+                                   _raw_stream(stream, dev)))
 
 
 def ss_pages_trim(pool, length, status, *, window=0, sinks=0, table_rows=None, stream=None):
     """Give back the rows' pages past `length`, and with a window those that
     no later token sees; length 0 frees a row."""
     import torch
-    i32, n = torch.int32, length.numel()
-    _check(load().ss_pages_trim(pool.ref, n, None if table_rows is None else _want(table_rows, "table_rows", i32, (n,)),
-                                _want(length, "length", i32), window, sinks, _want(status, "status", i32, (n,)),
-                                _raw_stream(stream)))
+    dev, i32, n = pool.device, torch.int32, length.numel()
+    _check(load().ss_pages_trim(pool.ref, n,
+                                None if table_rows is None else _want(table_rows, dev, "table_rows", i32, (n,)),
+                                _want(length, dev, "length", i32), window, sinks, _want(status, dev, "status", i32, (n,)),
+                                _raw_stream(stream, dev)))
 
 
 # ------------------------------------------------------------ workloads --
