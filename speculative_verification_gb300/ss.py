@@ -689,8 +689,8 @@ def _with_table(packer, page_table, cache):
     """A buffer for a call's arguments, with the ss_page_pool of a bare page
     table behind them, and the address of the page table's structure."""
     if isinstance(page_table, PagePool):
-        if page_table.device != cache.device:
-            raise SSError("page_table: want the pool on the cache's device")
+        if page_table.device != cache.device or page_table.page_size != cache.page_size:
+            raise SSError("page_table: want a pool of the cache's page size on its device")
         return C.create_string_buffer(packer.size), page_table.address
     import torch
     if page_table.dtype is not torch.int32 or page_table.dim() != 2 or page_table.stride(1) != 1 or \

@@ -184,3 +184,15 @@ def test_the_current_device_and_the_stream_are_the_memorys(calls, monkeypatch):
     with pytest.raises(ss.SSError):
         call(cache, None, {})
     assert calls == ["ss_cache_attention"]
+
+
+def test_a_pool_of_another_page_size(calls):
+    # slots would be looked up in the wrong pages
+    cache, pool = ss.KVCache(**caches("bf16")), ss.PagePool(page_size=32, **pools())
+    for x in ("ss_cache_append", "ss_cache_read", "ss_cache_attention"):
+        with pytest.raises(ss.SSError):
+            CALLS[x][0](cache, pool, {"page_table": pool})
+    assert not calls
+    pool = ss.PagePool(page_size=16, **pools())
+    CALLS["ss_cache_append"][0](cache, pool, {"page_table": pool})
+    assert calls == ["ss_cache_append"]
