@@ -671,6 +671,24 @@ size_t ss_attention_workspace_size(void);
 ss_status ss_cache_attention(const ss_attention_args* args, void* workspace, size_t workspace_bytes,
                              ss_stream_t stream);
 
+/* Self-test of the attention kernel's bounded waits: ss_cache_attention with
+ * one kind of its barriers expecting an arrival that never comes, so that the
+ * waits on it give up (within a second).  Every request with
+ * queries then reports SS_ROW_TIMEOUT and its rows are undefined; the context
+ * stays usable, the workspace must be zeroed again. */
+typedef enum {
+  SS_STALL_ITEMS = 1,  /* the work items (their rows' positions and masks)        */
+  SS_STALL_QUERIES,
+  SS_STALL_KEYS,       /* a tile of K, copied or unpacked                         */
+  SS_STALL_VALUES,     /* a tile of V                                             */
+  SS_STALL_SCORES,     /* the first product                                       */
+  SS_STALL_WEIGHTS,    /* the softmax's weights                                   */
+  SS_STALL_PACKED      /* a tile's packed bytes (4 bits only, else
+                          SS_ERR_UNSUPPORTED)                                     */
+} ss_stall;
+ss_status ss_selftest_attention_timeout(const ss_attention_args* args, int32_t stall, void* workspace,
+                                        size_t workspace_bytes, ss_stream_t stream);
+
 /* ss_pages_reserve: for each i, table row r = table_rows[i] (NULL: i) gets a
  * page from the pool in every hole among the entries that hold the slots
  * [from_len[i], to_len[i]).  Pages are taken in the order of i and of the

@@ -71,9 +71,8 @@ size_t ss_attention_workspace_size(void) {
   return ssa::kMaxCtas * sizeof(int32_t) + static_cast<size_t>(ssa::kMaxCtas) * 2 * ssa::kSlotFloats * sizeof(float);
 }
 
-ss_status ss_cache_attention(const ss_attention_args* args, void* workspace, size_t workspace_bytes,
-                             ss_stream_t stream) {
-  SS_NVTX_RANGE("ss_cache_attention");
+static ss_status attention(const ss_attention_args* args, int32_t stall, void* workspace, size_t workspace_bytes,
+                           ss_stream_t stream) {
   using namespace ssa;
   if (!args || !check_cache(args->cache) || !check_table(args->pool)) return SS_ERR_INVALID_ARG;
   const ss_attention_args& A = *args;
@@ -115,6 +114,7 @@ ss_status ss_cache_attention(const ss_attention_args* args, void* workspace, siz
   a.scale_log2 = static_cast<float>(static_cast<double>(A.scale) * 1.4426950408889634);
   a.window = A.window;
   a.sinks = A.sinks;
+  a.stall = stall;
   a.status = A.out_status;
   // Rows per item: the rows that a request can have, up to what the kernel
   // holds.  More rows per item read the cache fewer times; unused rows cost
@@ -128,6 +128,20 @@ ss_status ss_cache_attention(const ss_attention_args* args, void* workspace, siz
   a.pieces = reinterpret_cast<float*>(a.counters + kMaxCtas);
   return a.c.format == SS_CACHE_INT4 ? launch_int4(a, reinterpret_cast<cudaStream_t>(stream))
                                      : launch_bf16(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+ss_status ss_cache_attention(const ss_attention_args* args, void* workspace, size_t workspace_bytes,
+                             ss_stream_t stream) {
+  SS_NVTX_RANGE("ss_cache_attention");
+  return attention(args, 0, workspace, workspace_bytes, stream);
+}
+
+ss_status ss_selftest_attention_timeout(const ss_attention_args* args, int32_t stall, void* workspace,
+                                        size_t workspace_bytes, ss_stream_t stream) {
+  SS_NVTX_RANGE("ss_selftest_attention_timeout");
+  if (stall < SS_STALL_ITEMS || stall > SS_STALL_PACKED) return SS_ERR_INVALID_ARG;
+  if (stall == SS_STALL_PACKED && args && args->cache && args->cache->format != SS_CACHE_INT4) return SS_ERR_UNSUPPORTED;
+  return attention(args, stall, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

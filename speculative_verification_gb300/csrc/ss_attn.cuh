@@ -113,6 +113,7 @@ struct AttnArgs {
   float* lse;
   float scale_log2;
   int32_t window, sinks;
+  int32_t stall;  // 0, or the barriers that the self-test stalls (SS_STALL_*)
   int32_t* status;
   int32_t* counters;  // [kMaxCtas], zero between calls
   float* pieces;      // [kMaxCtas][2][kSlotFloats]
@@ -219,8 +220,9 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 }
 
 // The waits give up after kPolls polls, or at once when another wait of the CTA
-// has given up before (*dead).  The caller goes on (single-role warps stop);
-// nothing it computes then is used.  One block of PTX, small where it is not
+// has given up before (*dead).  The caller goes on (single-role warps stop, the
+// softmax at its next item); nothing it computes then is used.  What follows
+// from a wait's outcome is decided for whole warps, and no barrier depends on it.  One block of PTX, small where it is not
 // taken: the code around it is bound by instruction fetch.
 __device__ __forceinline__ bool wait_more(uint32_t bar, uint32_t parity, int32_t* dead) {
   uint32_t done;
@@ -247,6 +249,23 @@ __device__ __forceinline__ bool wait_more(uint32_t bar, uint32_t parity, int32_t
 __device__ __forceinline__ bool wait_or_dead(uint64_t* bar, uint32_t parity, int32_t* dead) {
   if (__builtin_expect(mbar_try_wait(bar, parity), 1)) return true;
   return wait_more(smem_addr(bar), parity, dead);
+}
+
+// A bounded wait for what the waiter itself has in flight, whether the CTA has
+// given up or not: nothing may write into the CTA's memory after its end.
+__device__ __forceinline__ bool wait_drained(uint64_t* bar, uint32_t parity) {
+  for (uint32_t i = 0; i < kPolls; ++i) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity), "n"(kSleepNs)
+        : "memory");
+    if (done) return true;
+  }
+  return false;
 }
 
 // Two barriers at once: the polls' latencies overlap.
@@ -699,30 +718,32 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
   int32_t* dead = &s_dead;
 
   if (tid == 0) {
+    // the self-test of the waits: one kind of barrier expects an arrival more
+    const auto more = [&](int kind) { return a.stall == kind ? 1u : 0u; };
     for (int i = 0; i < kKs; ++i) {
-      mbar_init(kfull + i, kPacked ? 128 : 1);
+      mbar_init(kfull + i, (kPacked ? 128 : 1) + more(SS_STALL_KEYS));
       mbar_init(kempty + i, 1);
     }
     for (int i = 0; i < kVs; ++i) {
-      mbar_init(vfull + i, kPacked ? 128 : 1);
+      mbar_init(vfull + i, (kPacked ? 128 : 1) + more(SS_STALL_VALUES));
       mbar_init(vempty + i, 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(sfull + i, 1);
+      mbar_init(sfull + i, 1 + more(SS_STALL_SCORES));
       mbar_init(sempty + i, F::kPerTile);
-      mbar_init(pfull + i, F::kPerTile);
+      mbar_init(pfull + i, F::kPerTile + more(SS_STALL_WEIGHTS));
       mbar_init(pdone + i, 1);
       mbar_init(oempty + i, F::kSoft);
     }
     for (int i = 0; i < kNQ; ++i) {
-      mbar_init(mfull + i, 32);
-      mbar_init(qfull + i, 32);
+      mbar_init(mfull + i, 32 + more(SS_STALL_ITEMS));
+      mbar_init(qfull + i, 32 + more(SS_STALL_QUERIES));
       mbar_init(qempty + i, 1 + F::kSoft / 32);
     }
     for (int i = 0; i < F::kQBufs; ++i) mbar_init(qfree + i, 1);
     if (kPacked)
       for (int i = 0; i < F::kRawStages; ++i) {
-        mbar_init(rfull + i, 33);  // the copies' bytes, and the lanes' own copies
+        mbar_init(rfull + i, 33 + more(SS_STALL_PACKED));  // the copies' bytes, and the lanes' own copies
         mbar_init(rempty + i, 256);
       }
     for (int i = 0; i < 2; ++i) mbar_init(written + i, F::kGroups > 1 ? F::kSoft - 128 : 1);
@@ -919,17 +940,18 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
       if (lane == 0) mbar_arrive(qempty + b);
       ++k;
     }
-    if (!ok) {
-      // given up: wait (bounded) for the copies in flight before leaving
-      if (kPacked) {
-        for (int32_t i = max(0, at - F::kRawStages); i < at; ++i)
-          mbar_wait_bounded(rfull + i % F::kRawStages, (i / F::kRawStages) & 1, 1u << 16);
-      } else {
-        for (int32_t i = max(0, k_tiles - kKs); i < k_tiles; ++i)
-          mbar_wait_bounded(kfull + i % kKs, (i / kKs) & 1, 1u << 16);
-        for (int32_t i = max(0, v_tiles - kVs); i < v_tiles; ++i)
-          mbar_wait_bounded(vfull + i % kVs, (i / kVs) & 1, 1u << 16);
-      }
+    // The copies in flight end before this warp does, also where other warps
+    // have given up on them (else their users wait for them anyway).
+    bool landed = true;
+    if (kPacked) {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      for (int32_t i = max(0, at - F::kRawStages); i < at && landed; ++i)
+        landed = wait_drained(rfull + i % F::kRawStages, (i / F::kRawStages) & 1);
+    } else {
+      for (int32_t i = max(0, k_tiles - kKs); i < k_tiles && landed; ++i)
+        landed = wait_drained(kfull + i % kKs, (i / kKs) & 1);
+      for (int32_t i = max(0, v_tiles - kVs); i < v_tiles && landed; ++i)
+        landed = wait_drained(vfull + i % kVs, (i / kVs) & 1);
     }
   } else if (warp == 1) {
     // -------------------------------------------- first product, S^T = K Q^T --
@@ -986,10 +1008,13 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
         __syncwarp();
       }
     }
-    if (!ok && lane == 0) {  // given up: the MMAs in flight end before tensor memory is freed
+    // The MMAs in flight end before tensor memory is freed, also where the
+    // softmax has given up (the lane that issued them commits).
+    if (elect_one()) {
       umma_commit(&drain[0]);
-      mbar_wait_bounded(&drain[0], 0, 1u << 16);
+      wait_drained(&drain[0], 0);
     }
+    __syncwarp();
   } else if (warp == 2) {
     // ---------------------------------------- second product, O^T += V^T P^T --
     constexpr uint32_t kHiV = desc_hi(1024, 2), kHiP = desc_hi(8 * F::kPitch, kN >= 64 ? 2u : kN == 32 ? 4u : 6u);
@@ -1031,10 +1056,11 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
         __syncwarp();
       }
     }
-    if (!ok && lane == 0) {
+    if (elect_one()) {
       umma_commit(&drain[1]);
-      mbar_wait_bounded(&drain[1], 0, 1u << 16);
+      wait_drained(&drain[1], 0);
     }
+    __syncwarp();
   } else if (warp == 3) {
     // --------------------------------------------- the items' queries --
     int32_t r = s_r0, left = my_tiles;
@@ -1066,6 +1092,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
       }
     }
     Span s = span_of(a, q, row0);
+    int32_t q_items = 0;  // whose queries are issued
     int32_t tree_of = -1, node_deep[2];
     uint64_t node_path[2];
 #pragma unroll 1
@@ -1175,6 +1202,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
         }
       }
       mbar_arrive(qfull + b);
+      q_items = k + 1;
       // the next item
       left -= take;
       if (left == 0) break;
@@ -1191,6 +1219,10 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
         }
       }
       s = span_of(a, q, row0);
+    }
+    if constexpr (!kPacked) {  // their copies end before this warp does
+      bool landed = true;
+      for (int32_t i = max(0, q_items - kNQ); i < q_items && landed; ++i) landed = wait_drained(qfull + i % kNQ, (i / kNQ) & 1);
     }
   }
   } else if (!kPacked || warp < 4 + F::kSoft / 32) {
@@ -1215,8 +1247,9 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
       if constexpr (kPacked)
         if (k == 0) {  // the first item's queries, for which everyone waits, by all of these warps
           constexpr int kWarps = F::kSoft / 32, kEach = kLive >= 8 * kWarps ? 4 : kLive >= 4 * kWarps ? 2 : 1;
-          wait_or_dead(mfull, 0, dead);
-          convert_queries<kLive, kEach>(a, items[0], qbuf, row_qsum[0], row_unit[0], st >> 5, kWarps);
+          // (given up: there is no item to read; the barrier all the same)
+          if (__all_sync(0xffffffffu, wait_or_dead(mfull, 0, dead)))
+            convert_queries<kLive, kEach>(a, items[0], qbuf, row_qsum[0], row_unit[0], st >> 5, kWarps);
           proxy_fence();
           bar_sync(6, F::kSoft + 32);
         }
@@ -1255,7 +1288,8 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
         float x[kCols], low[kPart];
         tmem_get(tmem + sb * kNS + c0 + lanes, x);
         if constexpr (kPacked) tmem_get(tmem + sb * kNS + kLive + c0 + lanes, low);
-        const uint32_t there = *reinterpret_cast<volatile uint32_t*>(info + at % kInfo);
+        // (the same for the warp even if the wait has given up and the copies' warp writes it now)
+        const uint32_t there = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(info + at % kInfo), 0);
         // does some row miss some key of the tile?
         const bool masked = sink || there != every || j0 + kTile - 1 > (tree ? it.base - 1 : first_pos) ||
                             (a.window > 0 && j0 <= last_pos - a.window);
@@ -1384,17 +1418,16 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
                                       (!kPacked && fresh && least < -kDeep));
         if (kPacked) pass |= fresh;  // a row's first keys set its reference
         if (!kPacked && fresh && !pass) {
-          // the rows that see a key here may keep the reference 0
-          uint32_t seen = 0xffffffffu;
-          if (masked) {
-            const uint32_t any = __reduce_or_sync(0xffffffffu, vis);
-            if (lane == 0) part[wq][h0] = __uint_as_float(any);
-            bar_sync(bar, 128);
-            seen = (__float_as_uint(part[0][h0]) | __float_as_uint(part[1][h0])) |
-                   (__float_as_uint(part[2][h0]) | __float_as_uint(part[3][h0]));
-          }
+          // the rows that see a key here may keep the reference 0 (whatever
+          // the tile's mask, the barriers are the same: after a wait that gave
+          // up the warps need not agree on it)
+          const uint32_t any = __reduce_or_sync(0xffffffffu, vis);
+          if (lane == 0) part[wq][h0] = __uint_as_float(any);
+          bar_sync(bar, 128);
+          const uint32_t seen = (__float_as_uint(part[0][h0]) | __float_as_uint(part[1][h0])) |
+                                (__float_as_uint(part[2][h0]) | __float_as_uint(part[3][h0]));
           unset = unset && ((seen >> (lt & 31)) & 1u) == 0;
-          fresh = masked && bar_any(bar, 128, lt < kCols && c0 + lt < it.rows && unset);
+          fresh = bar_any(bar, 128, lt < kCols && c0 + lt < it.rows && unset);
         }
         if (pass) {
           // some row's score passes its reference by too much (or the row has
@@ -1714,7 +1747,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
 #pragma unroll 1
     for (int32_t at = is_v ? turn : 0; at < my_tiles; at += is_v ? F::kVGroups : 1) {
       const int32_t rs = at % F::kRawStages;
-      if (!wait_or_dead(rfull + rs, (at / F::kRawStages) & 1, dead)) break;
+      if (!__all_sync(0xffffffffu, wait_or_dead(rfull + rs, (at / F::kRawStages) & 1, dead))) break;
       const uint8_t* src = raw + rs * F::kRaw + (is_v ? kTile * F::kRawRow : 0);
       const uint32_t* pairs = reinterpret_cast<const uint32_t*>(raw + rs * F::kRaw + 2 * kTile * F::kRawRow) + key;
       const auto packed = [&](int c) {  // 16 bytes: 32 channels
@@ -1728,7 +1761,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
         for (int c = 0; c < 2 * kHalves; ++c) w4[c] = packed(c);
       if (is_v) {
         const int32_t s = at % kVs;
-        if (!wait_or_dead(vempty + s, ((at / kVs) & 1) ^ 1u, dead)) break;
+        if (!__all_sync(0xffffffffu, wait_or_dead(vempty + s, ((at / kVs) & 1) ^ 1u, dead))) break;
         uint8_t* dst = vring + s * F::kStage + key * 128;
 #pragma unroll F::kUnrollV
         for (int c = 0; c < 2 * kHalves; ++c) {

@@ -247,6 +247,8 @@ SIGNATURES = {
     "ss_cache_read": ([C.POINTER(ss_append_args), C.c_void_p], C.c_int),
     "ss_attention_workspace_size": ([], C.c_size_t),
     "ss_cache_attention": ([C.POINTER(ss_attention_args), C.c_void_p, C.c_size_t, C.c_void_p], C.c_int),
+    "ss_selftest_attention_timeout": ([C.POINTER(ss_attention_args), C.c_int32, C.c_void_p, C.c_size_t, C.c_void_p],
+                                      C.c_int),
     "ss_pages_reserve": ([C.POINTER(ss_page_pool), C.c_int32] + [C.c_void_p] * 5, C.c_int),
     "ss_pages_fork": ([C.POINTER(ss_page_pool), C.POINTER(ss_kv_cache), C.c_int32] + [C.c_void_p] * 5, C.c_int),
     "ss_pages_compact": ([C.POINTER(ss_page_pool), C.POINTER(ss_kv_cache), C.c_int32] + [C.c_void_p] * 3 +
@@ -756,6 +758,26 @@ def ss_cache_attention(cache, layer, q, out, page_table, kv_len, workspace, stat
     layer of the cache, their own keys included (see include/ss.h).
     query_offsets None: one query per request; parents: a draft tree per
     request, as ss_tree_verify takes it; scale None: 1 / sqrt(head dim)."""
+    _attention(None, cache, layer, q, out, page_table, kv_len, workspace, status, query_offsets, max_queries, parents, scale,
+               window, sinks, lse, table_rows, stream)
+
+
+#: The barriers that ss_selftest_attention_timeout stalls.
+SS_STALL = {"items": 1, "queries": 2, "keys": 3, "values": 4, "scores": 5, "weights": 6, "packed": 7}
+
+
+def ss_selftest_attention_timeout(cache, layer, q, out, page_table, kv_len, workspace, status, *, stall, query_offsets=None,
+                                  max_queries=None, parents=None, scale=None, window=0, sinks=0, lse=None, table_rows=None,
+                                  stream=None):
+    """ss_cache_attention with waits that nothing ends (the timeout self-test):
+    every request with queries reports SS_ROW_TIMEOUT, and the workspace must
+    be zeroed again.  stall: a name of SS_STALL."""
+    _attention(SS_STALL[stall], cache, layer, q, out, page_table, kv_len, workspace, status, query_offsets, max_queries,
+               parents, scale, window, sinks, lse, table_rows, stream)
+
+
+def _attention(stall, cache, layer, q, out, page_table, kv_len, workspace, status, query_offsets, max_queries, parents, scale,
+               window, sinks, lse, table_rows, stream):
     import torch
     i32, n, shape, dev = torch.int32, kv_len.numel(), q.shape, cache.device
     qs, os_, handle = q.stride(), out.stride(), _raw_stream(stream, dev)
@@ -777,8 +799,13 @@ def ss_cache_attention(cache, layer, q, out, page_table, kv_len, workspace, stat
                          0 if lse is None else _want(lse, dev, "lse", torch.float32, (total, heads)),
                          cache.head_dim ** -0.5 if scale is None else scale, window, sinks,
                          _want(status, dev, "status", i32, (n,)))
-    fn = _quick_call("ss_cache_attention", [C.c_char_p, C.c_void_p, C.c_size_t, C.c_void_p])
-    _check(fn(buf, workspace.data_ptr(), workspace.numel() * workspace.element_size(), handle))
+    memory = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if stall is None:
+        fn = _quick_call("ss_cache_attention", [C.c_char_p, C.c_void_p, C.c_size_t, C.c_void_p])
+        _check(fn(buf, *memory, handle))
+    else:
+        fn = _quick_call("ss_selftest_attention_timeout", [C.c_char_p, C.c_int32, C.c_void_p, C.c_size_t, C.c_void_p])
+        _check(fn(buf, stall, *memory, handle))
 
 
 def ss_pages_reserve(pool, from_len, to_len, status, *, table_rows=None, stream=None):

@@ -1,0 +1,53 @@
+"""The bounded waits of the attention kernel: a wait that nothing ends gives
+up, the requests' statuses say so, and the next call is right.  Each kind of
+barrier by itself, in the kernel's different shapes."""
+import time
+
+import pytest
+
+from tests.test_cache_gpu import Problem, ints, ss, workspace  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+STALLS = ["items", "queries", "keys", "values", "scores", "weights", "packed"]
+
+
+def stalled(ss, p, workspace, stall, lens=None, offsets=None):
+    out, lse = torch.full_like(p.q, 7.0), torch.full(p.q.shape[:2], 7.0, device="cuda")
+    st = ints([-1] * len(p.lens))
+    par = ints([x for row in p.parents for x in row]) if p.parents is not None else None
+    ss.ss_selftest_attention_timeout(p.cache, 0, p.q, out, ints(p.table), ints(lens or p.lens), workspace, st, stall=stall,
+                                     query_offsets=ints(offsets or p.offsets), max_queries=max(p.news), parents=par,
+                                     scale=p.scale, window=p.window, sinks=p.sinks, lse=lse)
+    torch.cuda.synchronize()
+    return st.tolist()
+
+
+# rows of an item: 8, 16, 32, 64 (two warpgroups or four), 128
+@pytest.mark.parametrize("fmt,heads,tree", [("bf16", 2, False), ("bf16", 16, False), ("bf16", 64, True), ("bf16", 128, False),
+                                            ("int4", 4, False), ("int4", 16, True), ("int4", 32, False), ("int4", 64, True)])
+@pytest.mark.parametrize("stall", STALLS)
+def test_a_wait_that_nothing_ends_gives_up(ss, workspace, fmt, heads, tree, stall):
+    p = Problem(ss, 50, fmt, [300, 700, 40, 0], [2, 5, 1, 3], heads, 1, 128, 16, window=200, sinks=4, tree=tree)
+    if stall == "packed" and fmt == "bf16":
+        with pytest.raises(ss.SSError):
+            stalled(ss, p, workspace, stall)
+        return
+    t0 = time.monotonic()
+    assert stalled(ss, p, workspace, stall) == [ss.SS_ROW_TIMEOUT] * 4
+    assert time.monotonic() - t0 < 20
+    workspace.zero_()
+    p.check(ss, workspace)
+
+
+def test_the_self_test_checks_its_arguments(ss, workspace):
+    p = Problem(ss, 51, "bf16", [30], [1], 2, 1, 64, 16)
+    lib = ss.load()
+    assert lib.ss_selftest_attention_timeout(None, 0, None, 0, None) == 1
+    assert lib.ss_selftest_attention_timeout(None, 8, None, 0, None) == 1
+    assert lib.ss_selftest_attention_timeout(None, 1, None, 0, None) == 1
+    with pytest.raises(ss.SSError):
+        stalled(ss, p, workspace.cpu(), "keys")
+    p.check(ss, workspace)
