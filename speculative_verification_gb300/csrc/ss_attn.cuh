@@ -222,8 +222,9 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 // The waits give up after kPolls polls, or at once when another wait of the CTA
 // has given up before (*dead).  The caller goes on (single-role warps stop, the
 // softmax at its next item); nothing it computes then is used.  What follows
-// from a wait's outcome is decided for whole warps, and no barrier depends on it.  One block of PTX, small where it is not
-// taken: the code around it is bound by instruction fetch.
+// from a wait's outcome is decided for whole warps, and no barrier depends on
+// it.  One block of PTX, small where it is not taken: the code around it is
+// bound by instruction fetch.
 __device__ __forceinline__ bool wait_more(uint32_t bar, uint32_t parity, int32_t* dead) {
   uint32_t done;
   asm volatile(
@@ -832,7 +833,11 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
       s_tiles0 = weights[r];
     }
     before = upto - mine;
-    if (hi - 1 >= before * heads && hi - 1 < upto * heads) s_r1 = r_to - 1;  // at or past the last request
+    if (hi - 1 >= before * heads && hi - 1 < upto * heads) {
+      int32_t r = r_from;
+      while (hi - 1 >= (before + weights[r]) * heads) before += weights[r++];
+      s_r1 = r;
+    }
   }
   proxy_fence();  // the weights' reads before the ring's copies
   __syncthreads();
@@ -1810,8 +1815,9 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
     }
   }
   __syncthreads();
-  if (s_dead && my_tiles > 0) {
-    for (int32_t r = s_r0 + tid; r <= s_r1; r += F::kThreads) a.status[r] = SS_ROW_TIMEOUT;
+  if (s_dead && my_tiles > 0) {  // the requests with tiles from this CTA's first to its last
+    for (int32_t r = s_r0 + tid; r <= s_r1; r += F::kThreads)
+      if (request_of(a, r).n > 0) a.status[r] = SS_ROW_TIMEOUT;
   }
   if (warp == 1) {
     __syncwarp();

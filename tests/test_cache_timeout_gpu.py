@@ -42,6 +42,21 @@ def test_a_wait_that_nothing_ends_gives_up(ss, workspace, fmt, heads, tree, stal
     p.check(ss, workspace)
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "int4"])
+def test_only_requests_with_queries_time_out(ss, workspace, fmt):
+    # bad requests and those without queries, at the ends and between others, keep their statuses
+    lens, news = [50, 60, -1, 70, 80, 90, 10], [0, 2, 1, 0, 3, 1, 0]
+    p = Problem(ss, 52, fmt, [max(x, 0) for x in lens], news, 4, 1, 64, 16)
+    assert stalled(ss, p, workspace, "scores", lens=lens) == [0, 5, 4, 0, 5, 5, 0]
+    # more requests than threads, most of them without queries
+    n = 3000
+    p = Problem(ss, 53, fmt, [20] * n, [int(i % 100 == 7) for i in range(n)], 4, 1, 64, 16)
+    workspace.zero_()
+    assert stalled(ss, p, workspace, "keys") == [5 * x for x in p.news]
+    workspace.zero_()
+    p.check(ss, workspace)
+
+
 def test_the_self_test_checks_its_arguments(ss, workspace):
     p = Problem(ss, 51, "bf16", [30], [1], 2, 1, 64, 16)
     lib = ss.load()
