@@ -636,7 +636,8 @@ ss_status ss_cache_read(const ss_append_args* args, ss_stream_t stream);
  * table: the request's rows are not written; or a parent outside [0, i): the
  * node is taken as a child of the root), SS_ROW_BAD_INDEX (slots beyond the
  * table: they are holes), SS_ROW_TIMEOUT (a bounded wait gave up: the
- * request's rows are undefined, and the workspace must be zeroed again).
+ * request's rows are undefined, and the workspace must be zeroed again; until
+ * then every call with it reports this for its requests).
  *
  * The workspace (ss_attention_workspace_size() bytes, 256-byte aligned) must
  * have been zeroed once (ss_workspace_init); calls that share one must not

@@ -68,7 +68,7 @@ bool make_query_map(CUtensorMap* m, const AttnArgs& a, int rows) {
 extern "C" {
 
 size_t ss_attention_workspace_size(void) {
-  return ssa::kMaxCtas * sizeof(int32_t) + static_cast<size_t>(ssa::kMaxCtas) * 2 * ssa::kSlotFloats * sizeof(float);
+  return ssa::kMaxCtas * sizeof(int32_t) + static_cast<size_t>(ssa::kMaxCtas) * 2 * ssa::kSlotFloats * sizeof(float) + 256;
 }
 
 static ss_status attention(const ss_attention_args* args, int32_t stall, void* workspace, size_t workspace_bytes,
@@ -126,6 +126,7 @@ static ss_status attention(const ss_attention_args* args, int32_t stall, void* w
   while (a.block_rows < rows && a.block_rows < most) a.block_rows *= 2;
   a.counters = static_cast<int32_t*>(workspace);
   a.pieces = reinterpret_cast<float*>(a.counters + kMaxCtas);
+  a.gave_up = reinterpret_cast<int32_t*>(a.pieces + static_cast<size_t>(kMaxCtas) * 2 * kSlotFloats);
   return a.c.format == SS_CACHE_INT4 ? launch_int4(a, reinterpret_cast<cudaStream_t>(stream))
                                      : launch_bf16(a, reinterpret_cast<cudaStream_t>(stream));
 }

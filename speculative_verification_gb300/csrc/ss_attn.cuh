@@ -116,6 +116,7 @@ struct AttnArgs {
   int32_t stall;  // 0, or the barriers that the self-test stalls (SS_STALL_*)
   int32_t* status;
   int32_t* counters;  // [kMaxCtas], zero between calls
+  int32_t* gave_up;   // 0 until a CTA gives up on a wait
   float* pieces;      // [kMaxCtas][2][kSlotFloats]
 };
 
@@ -583,6 +584,40 @@ __device__ __forceinline__ Request request_of(const AttnArgs& a, int32_t r) {
   return q;
 }
 
+// The statuses of this CTA's share of the requests: a thread per request, or
+// with parents, which are looked at, a warp; from warp 3 on, as the first ones
+// have the requests' tiles to count.
+//
+// A time-out wins over them, whatever the order of the CTAs: a CTA that gives
+// up sets the workspace's word, and then exchanges the statuses for the
+// time-out.  Either that comes after the exchange here, or what comes back here
+// is the time-out, and the word is there to be seen.  (It stays until the
+// workspace is zeroed: the joining's counts may be off.)
+template <int kThreads>
+__device__ __forceinline__ void write_statuses(const AttnArgs& a) {
+  const int t = (threadIdx.x + kThreads - 96) % kThreads, lane = t & 31;
+  const int64_t first = a.parents ? t >> 5 : t, width = a.parents ? kThreads / 32 : kThreads;
+#pragma unroll 1
+  for (int64_t r = blockIdx.x + first * gridDim.x; r < a.num_requests; r += width * gridDim.x) {
+    const Request q = request_of(a, static_cast<int32_t>(r));
+    bool bad = !q.ok;
+    if (a.parents) {
+#pragma unroll 1
+      for (int32_t n = 1 + lane; n < q.n; n += 32) {
+        const int32_t pa = a.parents[q.qbegin + n];
+        bad |= pa < 0 || pa >= n;
+      }
+      bad = __any_sync(0xffffffffu, bad);
+      if (lane != 0) continue;
+    }
+    const bool beyond = q.n > 0 && ((q.base + q.n - 1) >> a.c.page_shift) >= a.t.max_pages;
+    const int32_t before = atomicExch(a.status + r, bad ? SS_ROW_BAD_PARAM : beyond ? SS_ROW_BAD_INDEX : SS_ROW_OK);
+    if (before == SS_ROW_TIMEOUT) __threadfence();
+    if (*reinterpret_cast<volatile int32_t*>(a.gave_up) != 0 && q.n > 0) atomicExch(a.status + r, SS_ROW_TIMEOUT);
+  }
+  __syncwarp();
+}
+
 // The keys of the block of rows that starts at row0: tiles over the first
 // tokens (sinks) and tiles from the window's start on, in units of a page (or
 // 128 slots of a larger one).
@@ -708,7 +743,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
   __shared__ float part[4][kRows];
   __shared__ uint32_t tmem_slot;
   __shared__ uint8_t v_bad[2][F::kGroups > 1 && !kPacked ? kTile : 1];  // keys whose values are not finite
-  __shared__ int32_t s_dead, s_last, s_r0, s_r1, s_before, s_tiles0, s_scan[32];
+  __shared__ int32_t s_dead, s_last, s_r0, s_before, s_tiles0, s_scan[32];
 
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* pbuf = ring + kRing * F::kStage;
@@ -751,7 +786,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
     mbar_init(&drain[0], 1);
     mbar_init(&drain[1], 1);
     s_dead = 0;
-    s_r0 = s_r1 = 0;
+    s_r0 = s_before = 0;
     fence_barrier_init();
   }
   if (F::kGroups > 1 && !kPacked && tid < kTile) v_bad[0][tid] = v_bad[1][tid] = 0;
@@ -780,22 +815,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
       if (lane == 0) weights[r] = w;
     }
   }
-  // The statuses: each by one warp of one CTA.
-#pragma unroll 1
-  for (int64_t r = blockIdx.x + static_cast<int64_t>(gridDim.x) * warp; r < a.num_requests;
-       r += static_cast<int64_t>(gridDim.x) * (F::kThreads / 32)) {
-    const Request q = request_of(a, static_cast<int32_t>(r));
-    bool bad = !q.ok;
-    if (q.ok && a.parents)
-#pragma unroll 1
-      for (int32_t n = 1 + lane; n < q.n; n += 32) {
-        const int32_t pa = a.parents[q.qbegin + n];
-        bad |= pa < 0 || pa >= n;
-      }
-    bad = __any_sync(0xffffffffu, bad);
-    const bool beyond = q.n > 0 && ((q.base + q.n - 1) >> a.c.page_shift) >= a.t.max_pages;
-    if (lane == 0) a.status[r] = bad ? SS_ROW_BAD_PARAM : beyond ? SS_ROW_BAD_INDEX : SS_ROW_OK;
-  }
+  write_statuses<F::kThreads>(a);
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
@@ -831,12 +851,6 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
       s_r0 = r;
       s_before = before;
       s_tiles0 = weights[r];
-    }
-    before = upto - mine;
-    if (hi - 1 >= before * heads && hi - 1 < upto * heads) {
-      int32_t r = r_from;
-      while (hi - 1 >= (before + weights[r]) * heads) before += weights[r++];
-      s_r1 = r;
     }
   }
   proxy_fence();  // the weights' reads before the ring's copies
@@ -1815,9 +1829,18 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
     }
   }
   __syncthreads();
-  if (s_dead && my_tiles > 0) {  // the requests with tiles from this CTA's first to its last
-    for (int32_t r = s_r0 + tid; r <= s_r1; r += F::kThreads)
-      if (request_of(a, r).n > 0) a.status[r] = SS_ROW_TIMEOUT;
+  // Given up: every request with tiles of this CTA (by a thread of the softmax,
+  // whose warps have registers for it).
+  if (s_dead && my_tiles > 0 && tid == 128) {
+    *reinterpret_cast<volatile int32_t*>(a.gave_up) = 1;
+    __threadfence();
+    int64_t upto = s_before;  // tiles of one head before and in the requests
+#pragma unroll 1
+    for (int32_t r = s_r0; r < a.num_requests && upto * a.c.heads < hi; ++r) {
+      const Request q = request_of(a, r);
+      upto += request_tiles(a, q, 0, 1);
+      if (q.n > 0) atomicExch(a.status + r, SS_ROW_TIMEOUT);
+    }
   }
   if (warp == 1) {
     __syncwarp();

@@ -57,6 +57,17 @@ def test_only_requests_with_queries_time_out(ss, workspace, fmt):
     p.check(ss, workspace)
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "int4"])
+def test_a_workspace_that_was_not_zeroed_again_says_so(ss, workspace, fmt):
+    # the counts of the pieces' joining may be off from then on: no call may pass that over
+    p = Problem(ss, 54, fmt, [5000, 30], [2, 0], 4, 1, 64, 16)
+    assert stalled(ss, p, workspace, "values") == [5, 0]
+    for _ in range(2):
+        assert p.call(ss, workspace)[2].tolist() == [5, 0]
+    workspace.zero_()
+    p.check(ss, workspace)
+
+
 def test_the_self_test_checks_its_arguments(ss, workspace):
     p = Problem(ss, 51, "bf16", [30], [1], 2, 1, 64, 16)
     lib = ss.load()
