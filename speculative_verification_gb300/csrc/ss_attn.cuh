@@ -635,7 +635,7 @@ __device__ __forceinline__ Span span_of(const AttnArgs& a, const Request& q, int
   // slots beyond the table are holes: no tiles for them, but one if nothing else is left
   const int64_t table_end = static_cast<int64_t>(a.t.max_pages) << a.c.page_shift;
   if (s.end > table_end) s.end = max(static_cast<int32_t>(table_end), s.origin + 1);
-  s.sink_end = min(a.sinks, s.origin);
+  s.sink_end = static_cast<int32_t>(min(static_cast<int64_t>(min(a.sinks, s.origin)), table_end));
   s.nsink = (s.sink_end + kTile - 1) / kTile;
   s.tiles = s.nsink + (s.end - s.origin + kTile - 1) / kTile;
   return s;
