@@ -92,6 +92,8 @@ static ss_status attention(const ss_attention_args* args, int32_t stall, void* w
   AttnArgs a{};
   a.c = view_of(A.cache, A.layer);
   a.t = table_of(A.pool, A.table_rows);
+  const int64_t slots = static_cast<int64_t>(A.pool->max_pages) << a.c.page_shift;
+  a.table_end = static_cast<int32_t>(slots < 0x7fffffff ? slots : 0x7fffffff);
   a.num_requests = A.num_requests;
   a.num_heads = A.num_heads;
   a.group = A.num_heads / kv_heads;
@@ -124,6 +126,9 @@ static ss_status attention(const ss_attention_args* args, int32_t stall, void* w
   const int32_t most = a.c.format == SS_CACHE_INT4 ? 64 : 128;
   a.block_rows = 8;
   while (a.block_rows < rows && a.block_rows < most) a.block_rows *= 2;
+  // The most tiles that the table and the numbers of queries allow.
+  const int64_t blocks = rows > 0 ? (rows - 1) / a.block_rows + 1 : 0;
+  a.few_tiles = blocks * (2ll * a.table_end / kTile + 3) < (1ll << 31) / a.num_requests;
   a.counters = static_cast<int32_t*>(workspace);
   a.pieces = reinterpret_cast<float*>(a.counters + kMaxCtas);
   a.gave_up = reinterpret_cast<int32_t*>(a.pieces + static_cast<size_t>(kMaxCtas) * 2 * kSlotFloats);

@@ -22,14 +22,59 @@ def test_sinks_and_lengths_far_beyond_the_table(ss, workspace, fmt, sinks):
     n, page, heads, dim = 200, 16, 4, 64
     rng = np.random.default_rng(9)
     cache = make_cache(ss, rng, fmt, 8, 2, page, dim)
-    q = torch.randn(n, heads, dim, device="cuda").to(torch.bfloat16)
+    q = torch.from_numpy(R.bf16(rng.standard_normal((n, heads, dim)))).to(torch.bfloat16).cuda()
     rows = rng.integers(0, 8, (n, 4)).tolist()
     out, lse, st = torch.full_like(q, 7), torch.full((n, heads), 7.0, device="cuda"), ints([-1] * n)
     ss.ss_cache_attention(cache, 0, q, out, ints(rows), ints([FAR] * n), workspace, st, lse=lse, window=500, sinks=sinks)
     torch.cuda.synchronize()
     assert st.tolist() == [3] * n
-    # the same keys as those of a query at the table's last slot, or at the last sink
-    want, want_lse, st2 = torch.empty_like(q), torch.empty_like(lse), ints([-1] * n)
-    ss.ss_cache_attention(cache, 0, q, want, ints(rows), ints([min(sinks, 4 * page) - 1] * n), workspace, st2, lse=want_lse)
+    # the keys of a query at the table's last slot, or at the last sink.  Held to the 64-bit results by the attention
+    # tests' bound, not to such a call's bits: other lengths are cut over the SMs in other places.
+    k, v, mv = dense(cache)
+    for r in range(n):
+        o, l, m, reach = R.attend(np32(q[r:r + 1]).astype(np.float64), lambda p, s: (k[p, :, s], v[p, :, s], mv[p, :, s]),
+                                  rows[r], page, min(sinks, 4 * page) - 1, dim ** -0.5, 0, 0, None, 8)
+        assert (np.abs(np32(out[r:r + 1]) - o) <= 2.0 ** -8 * (np.abs(o) + m) * (1 + 1 / 16)).all(), r
+        assert (np.abs(lse[r].cpu().numpy() - l[0]) <= 2.0 ** -17 * reach[0] + 2.0 ** -21 * (1 + np.abs(l[0]))).all(), r
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_more_tiles_than_can_be_walked(ss, workspace, fmt):
+    # 2^14 requests of 2^24 tiles each: reported, nothing written, at once
+    n, page, dim = 1 << 14, 1024, 64
+    cache = make_cache(ss, np.random.default_rng(1), fmt, 2, 1, page, dim)
+    q = torch.randn(n, 2, dim, device="cuda").to(torch.bfloat16)
+    table = torch.zeros(1, 1 << 21, dtype=torch.int32, device="cuda")
+    rows = torch.zeros(n, dtype=torch.int32, device="cuda")
+    lens = torch.full((n,), FAR, dtype=torch.int32, device="cuda")
+    lens[5] = -1
+    out, lse, st = torch.full_like(q, 7), torch.full((n, 2), 7.0, device="cuda"), torch.full_like(lens, -1)
+    ss.ss_cache_attention(cache, 0, q, out, table, lens, workspace, st, lse=lse, table_rows=rows)
     torch.cuda.synchronize()
-    assert st2.tolist() == [0] * n and torch.equal(out, want) and torch.equal(lse, want_lse)
+    want = torch.full_like(st, 6)
+    want[5] = 4
+    assert torch.equal(st, want) and bool((out == 7).all()) and bool((lse == 7).all())
+    # a window makes the same requests short
+    ss.ss_cache_attention(cache, 0, q, out, table, lens, workspace, st, lse=lse, table_rows=rows, window=100, sinks=3)
+    torch.cuda.synchronize()
+    want.zero_()
+    want[5] = 4
+    assert torch.equal(st, want) and bool((lse[6:] != 7).all()) and bool((out[5] == 7).all())
+
+
+def test_a_request_of_more_tiles_than_31_bits_count(ss, workspace):
+    # 2^22 queries of 64 heads over 2^30 keys: refused for itself, the request beside it is done
+    heads, dim, page, many = 64, 32, 1024, 1 << 22
+    cache = make_cache(ss, np.random.default_rng(2), "int4", 2, 1, page, dim)
+    q = torch.randn(1, heads, dim, device="cuda").to(torch.bfloat16)
+    out = torch.full_like(q, 7)
+    table = torch.zeros(1, 1 << 21, dtype=torch.int32, device="cuda")
+    st = ints([-1, -1])
+    ss.ss_cache_attention(cache, 0, q.expand(many + 1, -1, -1), out.expand(many + 1, -1, -1), table, ints([200, 1 << 30]),
+                          workspace, st, query_offsets=ints([0, 1, many + 1]), max_queries=many, table_rows=ints([0, 0]))
+    torch.cuda.synchronize()
+    assert st.tolist() == [0, 4]
+    k, v, mv = dense(cache)
+    o, _, m, _ = R.attend(np32(q).astype(np.float64), lambda p, s: (k[p, :, s], v[p, :, s], mv[p, :, s]), [0], page, 200,
+                          dim ** -0.5, 0, 0, None, 2)
+    assert (np.abs(np32(out) - o) <= 2.0 ** -8 * (np.abs(o) + m) * (1 + 1 / 16)).all()
