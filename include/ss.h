@@ -636,8 +636,8 @@ ss_status ss_cache_read(const ss_append_args* args, ss_stream_t stream);
  * table, about 2^31 or more tiles of 128 keys by up to 128 rows in one kv head:
  * the request's rows are not written; or a parent outside [0, i): the
  * node is taken as a child of the root), SS_ROW_BAD_INDEX (slots beyond the
- * table: they are holes), SS_ROW_LIMIT (more than 2^30 such tiles per SM in the
- * call: no rows are written), SS_ROW_TIMEOUT (a bounded wait gave up: the
+ * table: they are holes), SS_ROW_LIMIT (about 2^31 or more such tiles in all
+ * requests, fewer with more than 64 kv heads: no rows are written), SS_ROW_TIMEOUT (a bounded wait gave up: the
  * request's rows are undefined, and the workspace must be zeroed again; until
  * then every call with it reports this for its requests).
  *

@@ -129,6 +129,8 @@ static ss_status attention(const ss_attention_args* args, int32_t stall, void* w
   // The most tiles that the table and the numbers of queries allow.
   const int64_t blocks = rows > 0 ? (rows - 1) / a.block_rows + 1 : 0;
   a.few_tiles = blocks * (2ll * a.table_end / kTile + 3) < (1ll << 31) / a.num_requests;
+  // (a CTA's share of the tiles of all heads fits 31 bits with 64 SMs or more)
+  a.most_tiles = static_cast<int32_t>(kv_heads <= 64 ? 0x7ffffffell : (64ll << 31) / kv_heads);
   a.counters = static_cast<int32_t*>(workspace);
   a.pieces = reinterpret_cast<float*>(a.counters + kMaxCtas);
   a.gave_up = reinterpret_cast<int32_t*>(a.pieces + static_cast<size_t>(kMaxCtas) * 2 * kSlotFloats);

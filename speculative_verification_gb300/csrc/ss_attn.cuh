@@ -105,6 +105,7 @@ struct AttnArgs {
   int32_t block_rows;  // rows of an item (the kernel's kLive)
   int32_t table_end;   // slots of a table row, at most 2^31 - 1
   int32_t few_tiles;   // the requests' tiles for one head stay below 2^31, whatever the lengths
+  int32_t most_tiles;  // that a call may have for one head
   const int32_t* offsets;
   const int32_t* kv_len;
   const int32_t* parents;
@@ -649,6 +650,11 @@ __device__ __forceinline__ Span span_of(const AttnArgs& a, const Request& q, int
   return s;
 }
 
+// Sums of tiles end at 2^31 - 1.
+__device__ __forceinline__ int32_t add_tiles(int32_t x, int32_t y) {
+  return static_cast<int32_t>(min(static_cast<uint32_t>(x) + static_cast<uint32_t>(y), 0x7fffffffu));
+}
+
 // Tiles of one kv head of a request; the lanes of a warp share its blocks.
 __device__ __forceinline__ int32_t request_tiles(const AttnArgs& a, const Request& q, int32_t block0, int32_t step) {
   int32_t sum = 0;
@@ -751,8 +757,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
   __shared__ float part[4][kRows];
   __shared__ uint32_t tmem_slot;
   __shared__ uint8_t v_bad[2][F::kGroups > 1 && !kPacked ? kTile : 1];  // keys whose values are not finite
-  __shared__ int32_t s_dead, s_last, s_r0, s_tiles0;
-  __shared__ __align__(16) int64_t s_before, s_scan[32];
+  __shared__ int32_t s_dead, s_last, s_r0, s_before, s_tiles0, s_scan[32];
 
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* pbuf = ring + kRing * F::kStage;
@@ -830,44 +835,32 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
   const uint32_t tmem = tmem_slot;
   const int32_t chunk = (a.num_requests + F::kThreads - 1) / F::kThreads;  // consecutive requests per thread
   const int32_t r_from = min(a.num_requests, tid * chunk), r_to = min(a.num_requests, r_from + chunk);
-  const auto scan = [&](auto* sums, auto& mine, auto& upto, auto& all) {  // of the requests' tiles for one head
+  int32_t mine = 0;  // the requests' tiles for one head; sums end at 2^31 - 1
 #pragma unroll 1
-    for (int32_t r = r_from; r < r_to; ++r) mine += weights[r];
-    upto = mine;
+  for (int32_t r = r_from; r < r_to; ++r) mine = add_tiles(mine, weights[r]);
+  int32_t upto = mine;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const auto y = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += y;
-    }
-    if (lane == 31) sums[warp] = upto;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < F::kThreads / 32; ++w) {
-      if (w == warp) upto += all;
-      all += sums[w];
-    }
-  };
-  int64_t mine = 0, upto = 0, all_tiles = 0;
-  if (__builtin_expect(a.few_tiles, 1)) {  // in 32 bits: 0.3 us less
-    int32_t mine32 = 0, upto32 = 0, all32 = 0;
-    scan(reinterpret_cast<int32_t*>(s_scan), mine32, upto32, all32);
-    mine = mine32;
-    upto = upto32;
-    all_tiles = all32;
-  } else {
-    scan(s_scan, mine, upto, all_tiles);
+  for (int o = 1; o < 32; o <<= 1) {
+    const int32_t y = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto = add_tiles(upto, y);
   }
-  // (at most 2^14 requests of 2^31 tiles and 2^16 heads; below 2^38, a matter of
-  // an hour, the products below fit as well)
-  const int64_t sum = all_tiles * a.c.heads;
-  const bool too_many = __builtin_expect(!a.few_tiles, 0) && sum > static_cast<int64_t>(gridDim.x) << 30;
-  const int64_t total = too_many ? 0 : sum;
+  if (lane == 31) s_scan[warp] = upto;
+  __syncthreads();
+  int32_t all_tiles = 0;
+#pragma unroll
+  for (int w = 0; w < F::kThreads / 32; ++w) {
+    if (w == warp) upto = add_tiles(upto, all_tiles);
+    all_tiles = add_tiles(all_tiles, s_scan[w]);
+  }
+  const bool too_many = all_tiles > a.most_tiles;
+  if (too_many) all_tiles = 0;
+  const int64_t total = static_cast<int64_t>(all_tiles) * a.c.heads;
   const int32_t ctas = static_cast<int32_t>(min(total, static_cast<int64_t>(gridDim.x)));  // each has a tile or more
   const int64_t lo = ctas ? total * blockIdx.x / ctas : 0, hi = ctas ? total * (blockIdx.x + 1) / ctas : 0;
   const int32_t my_tiles = static_cast<int32_t>(blockIdx.x) < ctas ? static_cast<int32_t>(hi - lo) : 0;
   if (my_tiles > 0 && mine > 0) {
     const int64_t heads = a.c.heads;
-    int64_t before = upto - mine;
+    int32_t before = upto - mine;
     if (lo >= before * heads && lo < upto * heads) {
       int32_t r = r_from;
       while (lo >= (before + weights[r]) * heads) before += weights[r++];
@@ -1110,7 +1103,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
     // --------------------------------------------- the items' queries --
     int32_t r = s_r0, left = my_tiles;
     Request q = request_of(a, r);
-    const int64_t before = s_before * a.c.heads;  // tiles before request r
+    const int64_t before = static_cast<int64_t>(s_before) * a.c.heads;  // tiles before request r
     const int32_t w = s_tiles0;
     int32_t head = static_cast<int32_t>((lo - before) / w);
     int32_t skip = static_cast<int32_t>((lo - before) - static_cast<int64_t>(head) * w);  // tiles of the head passed
