@@ -196,7 +196,7 @@ struct Cfg {
   static constexpr int kUnrollV = kLive >= 64 ? 1 : 2 * kHalves;
   static constexpr int kUnrollPV = kLive >= 64 ? 1 : 8;  // likewise (2 x 4096 prompt: 311 us, 318 unrolled)
   // the static arrays, rounded up
-  static constexpr int kMeta = kNQ * (static_cast<int>(sizeof(Item)) + kN * 32 + 64 + 512) + kStreams * kN * 36 + 1536 +
+  static constexpr int kMeta = kNQ * (static_cast<int>(sizeof(Item)) + kN * 36 + 64 + 512) + kStreams * kN * 36 + 1536 +
                                (kPacked ? 2 * kPairs * kTile * 4 : 0);
   static constexpr int kBudget = 232448 - 1024 - kQBufs * kQ - kPBufs * kP - kRawStages * kRaw - kMeta;
   // K and V have a ring each, so that whoever waits for a slot has used the
@@ -746,7 +746,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
   __shared__ __align__(16) int32_t row_pos[kNQ][kN];
   __shared__ __align__(16) uint64_t row_path[kNQ][kN];
   __shared__ int64_t row_out[kNQ][kN];
-  __shared__ int32_t row_lse[kNQ][kN];
+  __shared__ int64_t row_lse[kNQ][kN];
   __shared__ __align__(16) float row_qsum[kPacked ? kNQ : 1][kPacked ? kN : 4], row_unit[kPacked ? kNQ : 1][kPacked ? kN : 4];
   __shared__ uint8_t node_depth[kNQ][SS_TREE_MAX_NODES];
   __shared__ uint64_t node_sees[kNQ][SS_TREE_MAX_NODES];
@@ -1206,7 +1206,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
         if (a.parents) row_path[b][n] = live ? node_sees[b][token] : ~0ull;
         const int64_t t = static_cast<int64_t>(q.qbegin) + token;
         row_out[b][n] = t * a.out_token + h * a.out_head;
-        row_lse[b][n] = static_cast<int32_t>(t * a.num_heads + h);
+        row_lse[b][n] = t * a.num_heads + h;
       }
       mbar_arrive(mfull + b);
       __syncwarp();

@@ -78,3 +78,25 @@ def test_a_request_of_more_tiles_than_31_bits_count(ss, workspace):
     o, _, m, _ = R.attend(np32(q).astype(np.float64), lambda p, s: (k[p, :, s], v[p, :, s], mv[p, :, s]), [0], page, 200,
                           dim ** -0.5, 0, 0, None, 2)
     assert (np.abs(np32(out) - o) <= 2.0 ** -8 * (np.abs(o) + m) * (1 + 1 / 16)).all()
+
+
+def test_rows_of_lse_past_31_bits(ss, workspace):
+    # one query whose row of lse is number 2^24 of 128 heads
+    heads, dim, page, first = 128, 32, 16, 1 << 24
+    if torch.cuda.mem_get_info()[0] < 20 << 30:
+        pytest.skip("needs 9 GB of device memory")
+    cache = make_cache(ss, np.random.default_rng(3), "int4", 4, 1, page, dim)
+    q = torch.from_numpy(R.bf16(np.random.default_rng(4).standard_normal((1, heads, dim)))).to(torch.bfloat16).cuda()
+    out, st = torch.full_like(q, 7), ints([-1])
+    lse = torch.full((first + 3, heads), 7.0, device="cuda")
+    ss.ss_cache_attention(cache, 0, q.expand(first + 3, -1, -1), out.expand(first + 3, -1, -1), ints([[0, 1, 2, 3]]), ints([50]),
+                          workspace, st, query_offsets=ints([first + 1, first + 2]), max_queries=1, lse=lse)
+    torch.cuda.synchronize()
+    assert st.tolist() == [0]
+    k, v, mv = dense(cache)
+    o, l, m, reach = R.attend(np32(q).astype(np.float64), lambda p, s: (k[p, :, s], v[p, :, s], mv[p, :, s]), [0, 1, 2, 3], page,
+                              50, dim ** -0.5, 0, 0, None, 4)
+    assert (np.abs(np32(out) - o) <= 2.0 ** -8 * (np.abs(o) + m) * (1 + 1 / 16)).all()
+    got = lse[first + 1].cpu().numpy()
+    assert (np.abs(got - l[0]) <= 2.0 ** -17 * reach[0] + 2.0 ** -21 * (1 + np.abs(l[0]))).all()
+    assert bool((lse[first] == 7).all()) and bool((lse[first + 2] == 7).all()) and bool((lse[:100] == 7).all())
