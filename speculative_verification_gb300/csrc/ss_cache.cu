@@ -268,21 +268,22 @@ struct PoolView {
 };
 
 // Inclusive sum over the CTA's kBook threads; `ws` has kBook / 32 words.
-__device__ __forceinline__ int32_t block_scan(int32_t x, int32_t* ws) {
+template <typename T>
+__device__ __forceinline__ T block_scan(T x, T* ws) {
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int32_t y = __shfl_up_sync(0xffffffffu, x, o);
+    const T y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
   __syncthreads();
   if (lane == 31) ws[wid] = x;
   __syncthreads();
   if (wid == 0) {
-    int32_t y = ws[lane];
+    T y = ws[lane];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int32_t z = __shfl_up_sync(0xffffffffu, y, o);
+      const T z = __shfl_up_sync(0xffffffffu, y, o);
       if (lane >= o) y += z;
     }
     ws[lane] = y;
@@ -306,14 +307,17 @@ __device__ __forceinline__ int32_t take(const PoolView& p, int32_t have, int32_t
 }
 
 // A warp per request counts its holes, one scan over the requests gives each
-// its place in the stack, the warps fill the holes.
+// its place in the stack, the warps fill the holes.  What the requests want in
+// all passes 2^31 where the table does: summed in 64 bits.
 __global__ void __launch_bounds__(kBook) reserve_kernel(const PoolView p, int32_t n, const int32_t* rows,
                                                         const int32_t* from, const int32_t* to, int32_t* status) {
-  __shared__ int32_t s_need[kBook], s_place[kBook], ws[kBook / 32], s_used, s_given;
+  __shared__ int32_t s_need[kBook], s_place[kBook], ws[kBook / 32], s_given;
+  __shared__ int64_t ws64[kBook / 32], s_used;
   const int wid = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int32_t have = free_now(p);
   const int64_t most = static_cast<int64_t>(p.max_pages) << p.page_shift;
-  int32_t used = 0, taken = 0;  // pages wanted and given by the chunks before
+  int64_t used = 0;   // pages wanted by the chunks before
+  int32_t taken = 0;  // and given
   for (int32_t c = 0; c < n; c += kBook) {
     const int32_t m = min(kBook, n - c);
     for (int32_t i = wid; i < m; i += kBook / 32) {
@@ -329,9 +333,9 @@ __global__ void __launch_bounds__(kBook) reserve_kernel(const PoolView p, int32_
     }
     __syncthreads();
     const int32_t need = (threadIdx.x < m) ? max(0, s_need[threadIdx.x]) : 0;
-    const int32_t upto = used + block_scan(need, ws);
+    const int64_t upto = used + block_scan(static_cast<int64_t>(need), ws64);
     const bool fits = upto <= have;
-    if (threadIdx.x < m) s_place[threadIdx.x] = (need > 0 && fits) ? upto - need : -1;
+    if (threadIdx.x < m) s_place[threadIdx.x] = (need > 0 && fits) ? static_cast<int32_t>(upto) - need : -1;
     if (threadIdx.x < m)
       status[c + threadIdx.x] = s_need[threadIdx.x] < 0 ? SS_ROW_BAD_PARAM
                                 : need == 0 || fits     ? SS_ROW_OK

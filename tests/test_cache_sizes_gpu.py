@@ -100,3 +100,22 @@ def test_rows_of_lse_past_31_bits(ss, workspace):
     got = lse[first + 1].cpu().numpy()
     assert (np.abs(got - l[0]) <= 2.0 ** -17 * reach[0] + 2.0 ** -21 * (1 + np.abs(l[0]))).all()
     assert bool((lse[first] == 7).all()) and bool((lse[first + 2] == 7).all()) and bool((lse[:100] == 7).all())
+
+
+def test_reserving_more_pages_than_31_bits_count(ss):
+    # nine rows of 2^28 holes want 2^31 + 2^28 pages of a pool of 16: none fits, none is taken
+    rows, entries, page = 9, 1 << 28, 8
+    if torch.cuda.mem_get_info()[0] < 20 << 30:
+        pytest.skip("needs 10 GB of device memory")
+    pool = ss.alloc_pool(rows, entries, 16, page)
+    st = ints([-1] * rows)
+    ss.ss_pages_reserve(pool, ints([0] * rows), ints([2 ** 31 - 1] * rows), st)
+    torch.cuda.synchronize()
+    assert st.tolist() == [6] * rows
+    assert int(pool.free_count) == 16 and not bool(pool.ref_count.any())
+    assert pool.free_pages.tolist() == list(range(15, -1, -1))
+    assert all(bool((pool.page_table[r] == -1).all()) for r in range(rows))
+    # rows that want little get it
+    ss.ss_pages_reserve(pool, ints([0] * rows), ints([8] * 4 + [0] * 4 + [2 ** 31 - 1]), st)
+    torch.cuda.synchronize()
+    assert st.tolist() == [0] * 8 + [6] and pool.page_table[:, 0].tolist() == [0, 1, 2, 3] + [-1] * 5
