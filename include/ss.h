@@ -651,7 +651,7 @@ typedef struct {
   int32_t num_requests;         /* at most 16384                                   */
   int32_t num_heads;            /* num_kv_heads times 1 .. 128                     */
   int32_t max_queries;          /* >= every request's number of queries; times
-                                   num_heads below 2^31                           */
+                                   num_heads at most 2^31 - 8192                  */
   int32_t total_queries;        /* rows of q and out                               */
   const int32_t* query_offsets; /* [num_requests + 1], or NULL: one query each     */
   const int32_t* table_rows;    /* as ss_append_args                               */

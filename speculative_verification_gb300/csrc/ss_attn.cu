@@ -79,8 +79,10 @@ static ss_status attention(const ss_attention_args* args, int32_t stall, void* w
   const int32_t kv_heads = A.cache->num_kv_heads;
   if (A.layer < 0 || A.layer >= A.cache->num_layers || A.num_requests < 0 || A.num_requests > 16384 ||
       A.max_queries < 0 || A.total_queries < 0 || A.num_heads < 1 || A.num_heads % kv_heads != 0 ||
-      A.num_heads / kv_heads > 128 || static_cast<int64_t>(A.max_queries) * A.num_heads >= (1ll << 31) || A.window < 0 || A.sinks < 0 || !isfinite(A.scale))
+      A.num_heads / kv_heads > 128 || A.window < 0 || A.sinks < 0 || !isfinite(A.scale))
     return SS_ERR_INVALID_ARG;
+  // a request's rows, and where the loops over 32 blocks of 128 of them end, are counted in 31 bits
+  if (static_cast<int64_t>(A.max_queries) * A.num_heads > (1ll << 31) - 8192) return SS_ERR_INVALID_ARG;
   if (!A.query_offsets && A.total_queries < A.num_requests) return SS_ERR_INVALID_ARG;
   if (A.num_requests == 0) return SS_OK;
   if (!A.kv_len || !A.out_status || !A.q || !A.out || !aligned16(A.q) || (A.q_token_stride & 7) != 0 ||

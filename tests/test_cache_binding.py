@@ -196,3 +196,16 @@ def test_a_pool_of_another_page_size(calls):
     pool = ss.PagePool(page_size=16, **pools())
     CALLS["ss_cache_append"][0](cache, pool, {"page_table": pool})
     assert calls == ["ss_cache_append"]
+
+
+def test_rows_of_a_request_end_before_31_bits_do():
+    # the library itself, which refuses before anything is launched
+    from speculative_verification_gb300 import build as ss_build
+    from tests.test_cache_abi import attention, attention_args
+    ss_build.build()
+    lib = ss.load()
+    for heads, most, want in ((4, 2 ** 29 - 2048, 4), (4, 2 ** 29 - 2047, 1), (4, 2 ** 29 - 1, 1), (128, 2 ** 24 - 64, 4),
+                              (128, 2 ** 24 - 63, 1), (512, 2 ** 31 - 1, 1)):
+        a = attention_args(num_heads=heads, max_queries=most)
+        # accepted counts go on to the next check, a workspace that is too small
+        assert attention(lib, a, size=0) == want, (heads, most)
