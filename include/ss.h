@@ -592,7 +592,7 @@ typedef struct {
   int32_t num_requests;         /* at most 65535                                   */
   int32_t max_tokens;           /* >= every request's number of new tokens; times
                                    2 num_kv_heads below 2^31                       */
-  int32_t total_tokens;         /* rows of k and v                                 */
+  int32_t total_tokens;         /* rows of k and v (0: they may be NULL)           */
   const int32_t* token_offsets; /* [num_requests + 1], or NULL: one token each     */
   const int32_t* table_rows;    /* [num_requests] each request's row of the page
                                    table, or NULL: the request's index            */
@@ -652,7 +652,7 @@ typedef struct {
   int32_t num_heads;            /* num_kv_heads times 1 .. 128                     */
   int32_t max_queries;          /* >= every request's number of queries; times
                                    num_heads at most 2^31 - 8192                  */
-  int32_t total_queries;        /* rows of q and out                               */
+  int32_t total_queries;        /* rows of q and out (0: they may be NULL)         */
   const int32_t* query_offsets; /* [num_requests + 1], or NULL: one query each     */
   const int32_t* table_rows;    /* as ss_append_args                               */
   const int32_t* kv_len;        /* [num_requests]                                  */

@@ -52,13 +52,15 @@ bool make_query_map(CUtensorMap* m, const AttnArgs& a, int rows) {
   const bool boxes = rows % a.group == 0;
   // the stride of a dimension of one entry is never used
   const int64_t head = a.num_heads > 1 ? a.q_head : 256, token = a.total_queries > 1 ? a.q_token : 256;
+  // (no queries at all: a map that nothing is copied with, of an address that is there)
+  void* base = a.total_queries > 0 ? const_cast<uint8_t*>(a.q) : a.c.k;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(a.c.dim), static_cast<cuuint64_t>(a.num_heads),
-                              static_cast<cuuint64_t>(a.total_queries)};
+                              static_cast<cuuint64_t>(a.total_queries > 0 ? a.total_queries : 1)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(head), static_cast<cuuint64_t>(token)};
   const cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(boxes ? a.group : 1),
                              static_cast<cuuint32_t>(boxes ? rows / a.group : 1)};
   const cuuint32_t estr[3] = {1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint8_t*>(a.q), dims, strides, box, estr,
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -85,7 +87,7 @@ static ss_status attention(const ss_attention_args* args, int32_t stall, void* w
   if (static_cast<int64_t>(A.max_queries) * A.num_heads > (1ll << 31) - 8192) return SS_ERR_INVALID_ARG;
   if (!A.query_offsets && A.total_queries < A.num_requests) return SS_ERR_INVALID_ARG;
   if (A.num_requests == 0) return SS_OK;
-  if (!A.kv_len || !A.out_status || !A.q || !A.out || !aligned16(A.q) || (A.q_token_stride & 7) != 0 ||
+  if (!A.kv_len || !A.out_status || (A.total_queries > 0 && (!A.q || !A.out)) || !aligned16(A.q) || (A.q_token_stride & 7) != 0 ||
       (A.q_head_stride & 7) != 0 || (reinterpret_cast<uintptr_t>(A.out) & 1) != 0)
     return SS_ERR_INVALID_ARG;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||

@@ -221,7 +221,7 @@ static ss_status rows_call(const ss_append_args* args, bool read, cudaStream_t s
     return SS_ERR_INVALID_ARG;
   if (!A.token_offsets && A.total_tokens < A.num_requests) return SS_ERR_INVALID_ARG;
   if (A.num_requests == 0) return SS_OK;
-  if (!A.kv_len || !A.out_status || !A.k || !A.v || !aligned16(A.k) || !aligned16(A.v) || (A.token_stride & 7) != 0 ||
+  if (!A.kv_len || !A.out_status || (A.total_tokens > 0 && (!A.k || !A.v)) || !aligned16(A.k) || !aligned16(A.v) || (A.token_stride & 7) != 0 ||
       (A.head_stride & 7) != 0)
     return SS_ERR_INVALID_ARG;
   AppendArgs a{};

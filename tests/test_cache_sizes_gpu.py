@@ -119,3 +119,33 @@ def test_reserving_more_pages_than_31_bits_count(ss):
     ss.ss_pages_reserve(pool, ints([0] * rows), ints([8] * 4 + [0] * 4 + [2 ** 31 - 1]), st)
     torch.cuda.synchronize()
     assert st.tolist() == [0] * 8 + [6] and pool.page_table[:, 0].tolist() == [0, 1, 2, 3] + [-1] * 5
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_a_step_in_which_no_request_has_tokens(ss, workspace, fmt):
+    cache = make_cache(ss, np.random.default_rng(5), fmt, 4, 2, 16, 64)
+    before = [t.clone() for t in (cache.k, cache.v, cache.k_scale, cache.v_scale) if t is not None]
+    table, offsets = ints([[0], [1], [2]]), ints([0] * 4)
+    k = torch.empty(0, 2, 64, dtype=torch.bfloat16, device="cuda")
+    q = torch.empty(0, 4, 64, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(0, 4, device="cuda")
+    for lens, want in (([3, 0, 15], [0, 0, 0]), ([3, -1, 40], [0, 4, 0])):
+        for most in (0, 1, 8):
+            st = ints([-1] * 3)
+            ss.ss_cache_append(cache, 0, k, k, table, ints(lens), st, token_offsets=offsets, max_tokens=most)
+            assert st.tolist() == want
+            st = ints([-1] * 3)
+            ss.ss_cache_read(cache, 0, k, k, table, ints(lens), st, token_offsets=offsets, max_tokens=most)
+            assert st.tolist() == want
+            for parents in (None, torch.empty(0, dtype=torch.int32, device="cuda")):
+                st = ints([-1] * 3)
+                ss.ss_cache_attention(cache, 0, q, q, table, ints(lens), workspace, st, query_offsets=offsets,
+                                      max_queries=most, lse=lse, parents=parents)
+                assert st.tolist() == want
+    after = [t for t in (cache.k, cache.v, cache.k_scale, cache.v_scale) if t is not None]
+    assert all(torch.equal(a, b) for a, b in zip(after, before))
+    # and none at all
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    ss.ss_cache_append(cache, 0, k, k, table, none, none, max_tokens=1)
+    ss.ss_cache_attention(cache, 0, q, q, table, none, workspace, none)
+    torch.cuda.synchronize()
