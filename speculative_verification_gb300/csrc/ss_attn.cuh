@@ -733,7 +733,10 @@ __device__ __forceinline__ void convert_queries(const AttnArgs& a, const Item& i
   }
 }
 
-template <int kLive, bool kPacked, int kHalves>
+// kAtLaunch: the registers per thread that the warpgroups share out again, or 0
+// where they do not.  As a part of the kernel's name it lets the build hold what
+// the compiler used against it.
+template <int kLive, bool kPacked, int kHalves, int kAtLaunch>
 __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
     attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                 const __grid_constant__ CUtensorMap tm_q, const AttnArgs a) {
@@ -1871,7 +1874,8 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
 template <int kLive, bool kPacked, int kHalves>
 ss_status launch(const AttnArgs& a, cudaStream_t s) {
   using F = Cfg<kLive, kPacked, kHalves>;
-  const void* fn = reinterpret_cast<const void*>(&attn_kernel<kLive, kPacked, kHalves>);
+  const auto kernel = attn_kernel<kLive, kPacked, kHalves, F::kSplit ? F::kRegs : 0>;
+  const void* fn = reinterpret_cast<const void*>(kernel);
   CUtensorMap mk, mv, mq{};
   const int unit = 1 << (a.c.page_shift < 7 ? a.c.page_shift : 7);
   if (!make_cache_map(&mk, a.c.k, a.c, unit) || !make_cache_map(&mv, a.c.v, a.c, unit)) return SS_ERR_UNSUPPORTED;
@@ -1888,12 +1892,13 @@ ss_status launch(const AttnArgs& a, cudaStream_t s) {
     if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, F::kSmem);
     if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, fn);
     if (e != cudaSuccess) return finish(e);
-    // the warpgroups' shares of registers are of what the launch brings
+    // the warpgroups' shares of registers are of what the launch brings (a
+    // build in which they are not fails: build.py)
     if (F::kSplit && at.numRegs != F::kRegs) return SS_ERR_UNSUPPORTED;
     grid = sms < kMaxCtas ? sms : kMaxCtas;
     if (dev < kMaxDevices) grids[dev].store(grid, std::memory_order_relaxed);
   }
-  if (e == cudaSuccess) attn_kernel<kLive, kPacked, kHalves><<<grid, F::kThreads, F::kSmem, s>>>(mk, mv, mq, a);
+  if (e == cudaSuccess) kernel<<<grid, F::kThreads, F::kSmem, s>>>(mk, mv, mq, a);
   return finish(e);
 }
 
