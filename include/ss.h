@@ -717,7 +717,8 @@ ss_status ss_selftest_attention_timeout(const ss_attention_args* args, int32_t s
  * SS_ROW_OK keeps new_len = kv_len and that status.  SS_ROW_BAD_INDEX (nothing
  * is moved and new_len = kv_len): a path that is not increasing, a slot beyond
  * the table or in a hole.  SS_ROW_BAD_PARAM (the same): num_accepted outside
- * [0, path_stride], a negative kv_len, a table row outside the table.  new_len
+ * [0, path_stride], a negative kv_len or a new_len past 2^31 - 1, a table row
+ * outside the table.  new_len
  * must not be the array kv_len.
  *
  * ss_pages_trim: table row i keeps the pages that hold a slot < length[i] that

@@ -505,7 +505,7 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactArgs a) 
   const int32_t* path = a.path + static_cast<int64_t>(i) * a.path_stride;
   int32_t st = SS_ROW_OK;
   if (verified != SS_ROW_OK) st = verified;
-  else if (!row || base < 0 || count < 0 || count > a.path_stride) st = SS_ROW_BAD_PARAM;
+  else if (!row || base < 0 || count < 0 || count > a.path_stride || base > 0x7ffffffe - count) st = SS_ROW_BAD_PARAM;
   int bad = 0;
   if (st == SS_ROW_OK)
     for (int32_t j = threadIdx.x; j < count; j += kThreads) {

@@ -149,3 +149,14 @@ def test_a_step_in_which_no_request_has_tokens(ss, workspace, fmt):
     ss.ss_cache_append(cache, 0, k, k, table, none, none, max_tokens=1)
     ss.ss_cache_attention(cache, 0, q, q, table, none, workspace, none)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_compact_at_the_last_length(ss, fmt):
+    # new_len = kv_len + 1 + accepted would pass 2^31 - 1
+    cache, pool = ss.alloc_cache(1, 4, 1, 16, 64, fmt), ss.alloc_pool(3, 4, 4, 16)
+    lens, new, st = [2 ** 31 - 1, 2 ** 31 - 2, 2 ** 31 - 2], ints([-1] * 3), ints([-1] * 3)
+    path = ints([[1, 2]] * 3)
+    ss.ss_pages_compact(pool, cache, ints(lens), path, ints([0, 0, 1]), None, new, st)
+    torch.cuda.synchronize()
+    assert st.tolist() == [4, 0, 4] and new.tolist() == [2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 2]
