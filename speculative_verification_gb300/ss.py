@@ -561,9 +561,8 @@ def _want(t, device, name, dtype, shape=None):
     return t.data_ptr()
 
 
-def _raw_stream(stream, device):
+def _raw_stream(torch, stream, device):
     """The CUDA stream handle as an integer, for a call on `device`'s memory."""
-    import torch
     if device < 0:
         raise SSError("want the cache or the pool on a GPU, it is on the host")
     if device != torch.cuda.current_device() or (stream is not None and stream.device_index != device):
@@ -687,15 +686,14 @@ def alloc_pool(rows, entries, pages, page_size, device="cuda"):
                     torch.arange(pages - 1, -1, -1, **i32), torch.full((1,), pages, **i32), page_size)
 
 
-def _with_table(packer, page_table, cache):
+def _with_table(packer, page_table, cache, int32):
     """A buffer for a call's arguments, with the ss_page_pool of a bare page
     table behind them, and the address of the page table's structure."""
     if isinstance(page_table, PagePool):
         if page_table.device != cache.device or page_table.page_size != cache.page_size:
             raise SSError("page_table: want a pool of the cache's page size on its device")
         return C.create_string_buffer(packer.size), page_table.address
-    import torch
-    if page_table.dtype is not torch.int32 or page_table.dim() != 2 or page_table.stride(1) != 1 or \
+    if page_table.dtype is not int32 or page_table.dim() != 2 or page_table.stride(1) != 1 or \
             page_table.get_device() != cache.device:
         raise SSError("page_table: want a PagePool or a [rows, entries] int32 tensor with contiguous rows on the cache's "
                       "device")
@@ -709,13 +707,13 @@ def _with_table(packer, page_table, cache):
 def _rows_call(name, cache, layer, k, v, page_table, kv_len, status, token_offsets, max_tokens, table_rows, stream):
     import torch
     n, i32, shape, dev = kv_len.numel(), torch.int32, k.shape, cache.device
-    stride, handle = k.stride(), _raw_stream(stream, dev)
+    stride, handle = k.stride(), _raw_stream(torch, stream, dev)
     if k.dtype is not torch.bfloat16 or v.dtype is not torch.bfloat16 or k.get_device() != dev or v.get_device() != dev or \
             len(shape) != 3 or v.shape != shape or v.stride() != stride or stride[2] != 1 or \
             shape[1] != cache.num_kv_heads or shape[2] != cache.head_dim:
         raise SSError("want k and v as [tokens, %d, %d] bf16 tensors of the same strides with contiguous rows on cuda:%d"
                       % (cache.num_kv_heads, cache.head_dim, dev))
-    buf, table = _with_table(_APPEND, page_table, cache)
+    buf, table = _with_table(_APPEND, page_table, cache, i32)
     _APPEND.pack_into(buf, 0, cache.address, table, layer, n, 1 if max_tokens is None else max_tokens, shape[0],
                       0 if token_offsets is None else _want(token_offsets, dev, "token_offsets", i32, (n + 1,)),
                       0 if table_rows is None else _want(table_rows, dev, "table_rows", i32, (n,)),
@@ -729,7 +727,7 @@ def ss_cache_append(cache, layer, k, v, page_table, kv_len, status, *, token_off
     """Write the new tokens' keys and values [tokens, kv heads, head dim] of
     one layer into the cache at the slots from kv_len (see include/ss.h).
     page_table: a PagePool or the table alone; token_offsets None: one token
-    per request."""
+    per request, else max_tokens is no less than any request's number."""
     _rows_call("ss_cache_append", cache, layer, k, v, page_table, kv_len, status, token_offsets, max_tokens, table_rows,
                stream)
 
@@ -753,34 +751,16 @@ def alloc_attention_workspace(device="cuda"):
 
 def ss_cache_attention(cache, layer, q, out, page_table, kv_len, workspace, status, *, query_offsets=None,
                        max_queries=None, parents=None, scale=None, window=0, sinks=0, lse=None, table_rows=None,
-                       stream=None):
+                       stream=None, _stall=None):
     """Attention of the new tokens' queries [tokens, heads, head dim] over one
     layer of the cache, their own keys included (see include/ss.h).
-    query_offsets None: one query per request; parents: a draft tree per
-    request, as ss_tree_verify takes it; scale None: 1 / sqrt(head dim)."""
-    _attention(None, cache, layer, q, out, page_table, kv_len, workspace, status, query_offsets, max_queries, parents, scale,
-               window, sinks, lse, table_rows, stream)
-
-
-#: The barriers that ss_selftest_attention_timeout stalls.
-SS_STALL = {"items": 1, "queries": 2, "keys": 3, "values": 4, "scores": 5, "weights": 6, "packed": 7}
-
-
-def ss_selftest_attention_timeout(cache, layer, q, out, page_table, kv_len, workspace, status, *, stall, query_offsets=None,
-                                  max_queries=None, parents=None, scale=None, window=0, sinks=0, lse=None, table_rows=None,
-                                  stream=None):
-    """ss_cache_attention with waits that nothing ends (the timeout self-test):
-    every request with queries reports SS_ROW_TIMEOUT, and the workspace must
-    be zeroed again.  stall: a name of SS_STALL."""
-    _attention(SS_STALL[stall], cache, layer, q, out, page_table, kv_len, workspace, status, query_offsets, max_queries,
-               parents, scale, window, sinks, lse, table_rows, stream)
-
-
-def _attention(stall, cache, layer, q, out, page_table, kv_len, workspace, status, query_offsets, max_queries, parents, scale,
-               window, sinks, lse, table_rows, stream):
+    query_offsets None: one query per request, else max_queries is no less
+    than any request's number; parents: a draft tree per request, as
+    ss_tree_verify takes it; scale None: 1 / sqrt(head dim).  (_stall: for the
+    self-test below.)"""
     import torch
     i32, n, shape, dev = torch.int32, kv_len.numel(), q.shape, cache.device
-    qs, os_, handle = q.stride(), out.stride(), _raw_stream(stream, dev)
+    qs, os_, handle = q.stride(), out.stride(), _raw_stream(torch, stream, dev)
     if q.dtype is not torch.bfloat16 or out.dtype is not torch.bfloat16 or q.get_device() != dev or \
             out.get_device() != dev or len(shape) != 3 or out.shape != shape or qs[2] != 1 or os_[2] != 1 or \
             shape[2] != cache.head_dim:
@@ -789,7 +769,7 @@ def _attention(stall, cache, layer, q, out, page_table, kv_len, workspace, statu
     if workspace.get_device() != dev or not workspace.is_contiguous():
         raise SSError("workspace: want a contiguous tensor on cuda:%d, got one on %s" % (dev, workspace.device))
     total, heads = shape[0], shape[1]
-    buf, table = _with_table(_ATTENTION, page_table, cache)
+    buf, table = _with_table(_ATTENTION, page_table, cache, i32)
     _ATTENTION.pack_into(buf, 0, cache.address, table, layer, n, heads, 1 if max_queries is None else max_queries, total,
                          0 if query_offsets is None else _want(query_offsets, dev, "query_offsets", i32, (n + 1,)),
                          0 if table_rows is None else _want(table_rows, dev, "table_rows", i32, (n,)),
@@ -799,13 +779,23 @@ def _attention(stall, cache, layer, q, out, page_table, kv_len, workspace, statu
                          0 if lse is None else _want(lse, dev, "lse", torch.float32, (total, heads)),
                          cache.head_dim ** -0.5 if scale is None else scale, window, sinks,
                          _want(status, dev, "status", i32, (n,)))
-    memory = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    if stall is None:
+    if _stall is None:
         fn = _quick_call("ss_cache_attention", [C.c_char_p, C.c_void_p, C.c_size_t, C.c_void_p])
-        _check(fn(buf, *memory, handle))
+        _check(fn(buf, workspace.data_ptr(), workspace.nbytes, handle))
     else:
         fn = _quick_call("ss_selftest_attention_timeout", [C.c_char_p, C.c_int32, C.c_void_p, C.c_size_t, C.c_void_p])
-        _check(fn(buf, stall, *memory, handle))
+        _check(fn(buf, _stall, workspace.data_ptr(), workspace.nbytes, handle))
+
+
+#: The barriers that ss_selftest_attention_timeout stalls.
+SS_STALL = {"items": 1, "queries": 2, "keys": 3, "values": 4, "scores": 5, "weights": 6, "packed": 7}
+
+
+def ss_selftest_attention_timeout(*args, stall, **kw):
+    """ss_cache_attention with waits that nothing ends (the timeout self-test):
+    every request with queries reports SS_ROW_TIMEOUT, and the workspace must
+    be zeroed again.  stall: a name of SS_STALL."""
+    ss_cache_attention(*args, _stall=SS_STALL[stall], **kw)
 
 
 def ss_pages_reserve(pool, from_len, to_len, status, *, table_rows=None, stream=None):
@@ -815,7 +805,7 @@ def ss_pages_reserve(pool, from_len, to_len, status, *, table_rows=None, stream=
     _check(load().ss_pages_reserve(pool.ref, n,
                                    None if table_rows is None else _want(table_rows, dev, "table_rows", i32, (n,)),
                                    _want(from_len, dev, "from_len", i32), _want(to_len, dev, "to_len", i32, (n,)),
-                                   _want(status, dev, "status", i32, (n,)), _raw_stream(stream, dev)))
+                                   _want(status, dev, "status", i32, (n,)), _raw_stream(torch, stream, dev)))
 
 
 def ss_pages_fork(pool, cache, parent, child, length, status, *, stream=None):
@@ -828,7 +818,7 @@ def ss_pages_fork(pool, cache, parent, child, length, status, *, stream=None):
     _check(load().ss_pages_fork(pool.ref, cache.ref, n, _want(parent, dev, "parent", i32),
                                 _want(child, dev, "child", i32, (n,)),
                                 _want(length, dev, "length", i32, (n,)), _want(status, dev, "status", i32, (n,)),
-                                _raw_stream(stream, dev)))
+                                _raw_stream(torch, stream, dev)))
 
 
 def ss_pages_compact(pool, cache, kv_len, path, num_accepted, verify_status, new_len, status, *, table_rows=None,
@@ -847,7 +837,7 @@ def ss_pages_compact(pool, cache, kv_len, path, num_accepted, verify_status, new
                                    _want(num_accepted, dev, "num_accepted", i32, (n,)),
                                    None if verify_status is None else _want(verify_status, dev, "verify_status", i32, (n,)),
                                    _want(new_len, dev, "new_len", i32, (n,)), _want(status, dev, "status", i32, (n,)),
-                                   _raw_stream(stream, dev)))
+                                   _raw_stream(torch, stream, dev)))
 
 
 def ss_pages_trim(pool, length, status, *, window=0, sinks=0, table_rows=None, stream=None):
@@ -858,7 +848,7 @@ def ss_pages_trim(pool, length, status, *, window=0, sinks=0, table_rows=None, s
     _check(load().ss_pages_trim(pool.ref, n,
                                 None if table_rows is None else _want(table_rows, dev, "table_rows", i32, (n,)),
                                 _want(length, dev, "length", i32), window, sinks, _want(status, dev, "status", i32, (n,)),
-                                _raw_stream(stream, dev)))
+                                _raw_stream(torch, stream, dev)))
 
 
 # ------------------------------------------------------------ workloads --
