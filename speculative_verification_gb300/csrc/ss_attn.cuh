@@ -607,8 +607,10 @@ template <int kThreads>
 __device__ __forceinline__ void write_statuses(const AttnArgs& a) {
   const int t = (threadIdx.x + kThreads - 96) % kThreads, lane = t & 31;
   const int64_t first = a.parents ? t >> 5 : t, width = a.parents ? kThreads / 32 : kThreads;
+  const volatile int32_t* word = a.gave_up;
 #pragma unroll 1
   for (int64_t r = blockIdx.x + first * gridDim.x; r < a.num_requests; r += width * gridDim.x) {
+    const int32_t early = *word;  // on its way with the request's numbers
     const Request q = request_of(a, static_cast<int32_t>(r));
     bool bad = !q.ok;
     if (a.parents) {
@@ -622,8 +624,12 @@ __device__ __forceinline__ void write_statuses(const AttnArgs& a) {
     }
     const bool beyond = q.n > 0 && ((q.base + q.n - 1) >> a.c.page_shift) >= a.t.max_pages;
     const int32_t before = atomicExch(a.status + r, bad ? SS_ROW_BAD_PARAM : beyond ? SS_ROW_BAD_INDEX : SS_ROW_OK);
-    if (before == SS_ROW_TIMEOUT) __threadfence();
-    if (*reinterpret_cast<volatile int32_t*>(a.gave_up) != 0 && q.n > 0) atomicExch(a.status + r, SS_ROW_TIMEOUT);
+    bool gave_up = early != 0;
+    if (before == SS_ROW_TIMEOUT) {
+      __threadfence();
+      gave_up = *word != 0;
+    }
+    if (gave_up && q.n > 0) atomicExch(a.status + r, SS_ROW_TIMEOUT);
   }
   __syncwarp();
 }
@@ -1329,8 +1335,10 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
         float x[kCols], low[kPart];
         tmem_get(tmem + sb * kNS + c0 + lanes, x);
         if constexpr (kPacked) tmem_get(tmem + sb * kNS + kLive + c0 + lanes, low);
-        // (the same for the warp even if the wait has given up and the copies' warp writes it now)
-        const uint32_t there = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(info + at % kInfo), 0);
+        // (Where the wait has given up the copies' warp may write it now: the
+        // threads need not agree on it, and nothing that they do together
+        // depends on it.)
+        const uint32_t there = *reinterpret_cast<volatile uint32_t*>(info + at % kInfo);
         // does some row miss some key of the tile?
         const bool masked = sink || there != every || j0 + kTile - 1 > (tree ? it.base - 1 : first_pos) ||
                             (a.window > 0 && j0 <= last_pos - a.window);
