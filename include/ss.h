@@ -625,10 +625,11 @@ ss_status ss_cache_read(const ss_append_args* args, ss_stream_t stream);
  * (lse stays finite where only a value is not).
  *
  * Sums and softmax statistics are held in fp32; the weights are rounded to
- * bf16 (4 bits: to f16) before they meet the values.  Results are right for values up to
- * 2^110 over the query's number of keys (4 bits: 2^100) in magnitude; values
- * below 2^-80 may count as 0.  The result does not depend on timing: the
- * work is split over the SMs by the lengths alone and joined in a fixed order.
+ * bf16 (4 bits: to f16) before they meet the values.  Results are right for
+ * values up to 2^110 over the query's number of keys (4 bits: 2^100) in
+ * magnitude; values below 2^-80 may count as 0.  The result does not depend on
+ * timing: the work is split over the SMs by the lengths alone and joined in a
+ * fixed order.
  *
  * out_status: SS_ROW_BAD_PARAM (a count outside [0, max_queries], with parents
  * above SS_TREE_MAX_NODES, query rows outside [0, total_queries), a negative
@@ -637,9 +638,10 @@ ss_status ss_cache_read(const ss_append_args* args, ss_stream_t stream);
  * the request's rows are not written; or a parent outside [0, i): the
  * node is taken as a child of the root), SS_ROW_BAD_INDEX (slots beyond the
  * table: they are holes), SS_ROW_LIMIT (about 2^31 or more such tiles in all
- * requests, fewer with more than 64 kv heads: no rows are written), SS_ROW_TIMEOUT (a bounded wait gave up: the
- * request's rows are undefined, and the workspace must be zeroed again; until
- * then every call with it reports this for its requests).
+ * requests, fewer with more than 64 kv heads: no rows are written),
+ * SS_ROW_TIMEOUT (a bounded wait gave up: the request's rows are undefined, and
+ * the workspace must be zeroed again; until then every call with it reports
+ * this for its requests).
  *
  * The workspace (ss_attention_workspace_size() bytes, 256-byte aligned) must
  * have been zeroed once (ss_workspace_init); calls that share one must not
@@ -702,7 +704,8 @@ ss_status ss_selftest_attention_timeout(const ss_attention_args* args, int32_t s
  * ss_pages_fork: table row child[i] becomes a copy of row parent[i]'s first
  * length[i] slots: full pages are shared (their reference counts grow), the
  * last one, when it is partly filled, is copied to a page from the pool, in
- * every layer, so that both rows can go on writing.  Holes stay holes.
+ * every layer, so that both rows can go on writing (from slot length[i] on:
+ * nothing copies a shared page when a slot before is written).  Holes stay holes.
  * SS_ROW_LIMIT as above; SS_ROW_BAD_PARAM: rows outside the table, a length
  * outside [0, max_pages * page_size], or a child row that holds pages.  A row
  * without a page of its own is left as it was.  The children must be distinct
@@ -718,8 +721,7 @@ ss_status ss_selftest_attention_timeout(const ss_attention_args* args, int32_t s
  * is moved and new_len = kv_len): a path that is not increasing, a slot beyond
  * the table or in a hole.  SS_ROW_BAD_PARAM (the same): num_accepted outside
  * [0, path_stride], a negative kv_len or a new_len past 2^31 - 1, a table row
- * outside the table.  new_len
- * must not be the array kv_len.
+ * outside the table.  new_len must not be the array kv_len.
  *
  * ss_pages_trim: table row i keeps the pages that hold a slot < length[i] that
  * is < sinks or, with window > 0, >= length[i] - window; every other entry

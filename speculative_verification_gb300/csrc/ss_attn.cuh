@@ -6,16 +6,16 @@
 //   p_nj = 2^(x_nj - r_n),  out_n = sum_j p_nj v_j / sum_j p_nj,
 //   lse_n = ln 2 (r_n + log2 sum_j p_nj).
 // Any r_n gives the same result; it only has to keep the powers in range.  The
-// running maximum is the usual choice; here (bf16) r_n starts at 0 and moves only when
-// some x_nj passes it by more than 16 (or the first ones lie below -32), so the
-// accumulated sums are rarely rescaled and a tile needs no maximum over its
-// keys at all (2 x 4096-token prompt chunks: 390 us when every item's first
-// tile took its maximum and masks were tested per row, 341 since).  Weights in
-// [2^-32, 2^16] round no worse than those around 1, as bf16 is relative; but
-// they meet the values in fp32, which therefore have 2^-16 of its range at the
-// upper end and 2^32 at the lower one.  Over 4 bits the weights are
-// f16, whose range is short: there r_n is set at the first keys, and moves
-// when a later one passes them by much (kSlack, kTop below).
+// running maximum is the usual choice; here (bf16) r_n starts at 0 and moves
+// only when some x_nj passes it by more than 16 (or the first ones lie below
+// -32), so the accumulated sums are rarely rescaled and a tile needs no maximum
+// over its keys at all (2 x 4096-token prompt chunks: 390 us when every item's
+// first tile took its maximum and masks were tested per row, 341 since).
+// Largest weights in [2^-32, 2^16] round no worse than those around 1, as bf16
+// is relative; but they meet the values in fp32, whose range is that much
+// narrower for the values.  Over 4 bits the weights are f16, whose range is
+// short: there r_n is set at the first keys, and moves when a later one passes
+// them by much (kSlack, kTop below).
 //
 // The transposed product.  A tile is 128 keys of one kv head; the rows are the
 // new tokens of one request times the query heads that share the kv head,
@@ -54,13 +54,15 @@
 // rows) and for 4 bits those that unpack.
 //
 // Measured on one GB300, and what bounds it: bf16, 32 requests of 1-8 drafts
-// over 1-32k tokens (32 heads on 8, dim 128): 246 us, 6.65 TB/s, the cache's
-// bytes.  2 x 4096-token prompt chunks in a window of 1024: 310 us, 417
-// TFLOP/s; 16 trees over 2-12k tokens, dim 64: 84 us; both by the chain of one
+// over 1-32k tokens (32 heads on 8, dim 128): 244 us, 6.68 TB/s, the cache's
+// bytes.  2 x 4096-token prompt chunks in a window of 1024: 313 us, 412
+// TFLOP/s; 16 trees over 2-12k tokens, dim 64: 85 us; both by the chain of one
 // tile's softmax, 2900 clocks for 128 x 128 weights (the powers alone take
-// 1024).  4 bits, 32 x 1 token over 8-64k: 363 us, 3.45 TB/s, 1390 clocks a
-// tile, the unpacking's and the waits' latency; 48 x 1-8 drafts, 64 rows: 338
-// us, instruction issue.  One token of one request: 12 us, all latency.
+// 1024), in which all softmax warps are in one phase.  4 bits, 32 x 1 token over
+// 8-64k: 365 us, 3.43 TB/s, 1390 clocks a tile, the unpacking's and the waits'
+// latency; 48 x 1-8 drafts, 64 rows, of which 44 % are without a query: 325 us,
+// instruction issue (54 % of the slots).  One token of one request: 12 us, all
+// latency.
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -84,10 +86,12 @@ constexpr int kInfo = 16;                 // tiles whose page masks are kept
 constexpr int kPairs = 8;                 // tiles whose (s, m) pairs are kept
 constexpr float kUnset = 3.0e38f;         // in a piece: minus the reference of a row that has seen nothing
 // How far a score (log2) may pass its row's reference, and for bf16 how far the
-// first ones may lie below the reference 0: as far as costs nothing (8 and 16:
-// prompt 311 -> 324 us, trees 85 -> 92; 32 and 64 no faster).  4 bits: of the score plus its key's
-// magnitude, so that f16 holds the weights (65504 at most, 2^-24 their unit), and
-// a reference that is set or moved puts the largest of them at 2^kTop: from its
+// first ones may lie below the reference 0: as little as costs nothing (8 and 16:
+// prompt 311 -> 324 us, trees 85 -> 92; 32 and 64 no faster).  4 bits: of the
+// score plus its key's magnitude, so that f16 holds the weights (65504 at most,
+// 2^-24 their unit); there a reference that is set or moved puts the largest
+// weight at 2^kTop (48 x 1-8 drafts 338 -> 322 us against references that
+// start at 0, which also lost small weights beside a large one): from its
 // first key on a row's largest weight is in [2^8, 2^15].  Beside one sink 2^20
 // other keys that count as much together then stand at 2^-12 or above, where f16
 // still has all its bits (down to 2^-14); and 7 binades, 4.9 of a score, are left

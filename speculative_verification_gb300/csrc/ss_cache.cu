@@ -130,9 +130,10 @@ __device__ __forceinline__ uint4 dequantise8(uint32_t w, uint32_t pair) {
 // even), so a token's page is looked up once for them and their loads are in
 // flight together; CTA (x, r) takes kGroups * kEach rows of request r, then a
 // grid's width further.  4 x 2-6k tokens, 8 heads of 128 channels: 4 bits in
-// 32.6 us (bound by the rounding's instructions; 67 with a division per
-// channel), out in 21.6 (4.4 TB/s, bound by the loads' latency); bf16, 32 x 1-8
-// tokens: 4.4 us, the latency of lengths, table and rows one after the other.
+// 32.6 us (67 with a division per channel), out in 21.6 (4.4 TB/s), both bound
+// by instructions first (72 % of the issue slots: rounding or unpacking, and
+// the addresses), out also by the loads' latency; bf16, 32 x 1-8 tokens: 4.4
+// us, the latency of lengths, table and rows one after the other.
 template <bool kPacked, bool kRead, int kEach>
 __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const AppendArgs a, const FastDiv by_token) {
   const int r = blockIdx.y;
