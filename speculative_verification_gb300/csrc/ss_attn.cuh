@@ -80,7 +80,7 @@ using namespace ss;
 constexpr int kTile = 128;                // keys per tile
 constexpr int kMaxCtas = 256;             // the workspace's limit on the grid
 constexpr int kMaxDevices = 64;
-constexpr uint32_t kPolls = 1u << 14;     // bounded waits: polls that each sleep up to kSleepNs
+constexpr uint32_t kPolls = 1u << 14;     // bounded waits: polls that each sleep up to kSleepNs, 60 ms in all
 constexpr uint32_t kSleepNs = 50000;
 constexpr int kInfo = 16;                 // tiles whose page masks are kept
 constexpr int kPairs = 8;                 // tiles whose (s, m) pairs are kept
@@ -258,6 +258,27 @@ __device__ __forceinline__ bool wait_more(uint32_t bar, uint32_t parity, int32_t
 __device__ __forceinline__ bool wait_or_dead(uint64_t* bar, uint32_t parity, int32_t* dead) {
   if (__builtin_expect(mbar_try_wait(bar, parity), 1)) return true;
   return wait_more(smem_addr(bar), parity, dead);
+}
+
+// A wait for the end of an item, which may be long: given up when another wait
+// of the CTA has (each of those is for a tile or less, about 60 ms), or after a
+// minute.
+__device__ __forceinline__ bool wait_item(uint64_t* bar, uint32_t parity, int32_t* dead) {
+#pragma unroll 1
+  for (uint32_t i = 0; i < 1024 * kPolls; ++i) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity), "n"(kSleepNs)
+        : "memory");
+    if (done) return true;
+    if (*reinterpret_cast<volatile int32_t*>(dead) != 0) return false;
+  }
+  *reinterpret_cast<volatile int32_t*>(dead) = 1;
+  return false;
 }
 
 // A bounded wait for what the waiter itself has in flight, whether the CTA has
@@ -1149,7 +1170,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
 #pragma unroll 1
     for (int32_t k = 0; left > 0; ++k) {
       const int b = k % kNQ;
-      if (!__all_sync(0xffffffffu, wait_or_dead(qempty + b, ((k / kNQ) & 1) ^ 1u, dead))) break;
+      if (!__all_sync(0xffffffffu, wait_item(qempty + b, ((k / kNQ) & 1) ^ 1u, dead))) break;
       const int32_t rows = min(kLive, q.n * a.group - row0), take = min(left, s.tiles - skip);
       if (lane == 0) {
         Item it;
@@ -1224,7 +1245,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
       mbar_arrive(mfull + b);
       __syncwarp();
       const int qb = k % F::kQBufs;
-      if (!__all_sync(0xffffffffu, wait_or_dead(qfree + qb, ((k / F::kQBufs) & 1) ^ 1u, dead))) break;
+      if (!__all_sync(0xffffffffu, wait_item(qfree + qb, ((k / F::kQBufs) & 1) ^ 1u, dead))) break;
       if constexpr (!kPacked) {
         // by tensor copies: the block's tokens times the group's heads in one
         // box where blocks start at tokens, else row by row

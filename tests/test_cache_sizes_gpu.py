@@ -160,3 +160,32 @@ def test_compact_at_the_last_length(ss, fmt):
     ss.ss_pages_compact(pool, cache, ints(lens), path, ints([0, 0, 1]), None, new, st)
     torch.cuda.synchronize()
     assert st.tolist() == [4, 0, 4] and new.tolist() == [2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 2]
+
+
+@pytest.mark.parametrize("fmt,heads", [("bf16", 4), ("bf16", 128), ("int4", 4), ("int4", 64)])
+def test_items_that_take_a_tenth_of_a_second(ss, workspace, fmt, heads):
+    # Several items per SM of 2^24 keys each (one page, 2^14 times): a warp that waits for the end of an item does not
+    # give up as one that waits for a tile does.  Each thread adds up 2^17 weights in fp32, so a sum is off by at most
+    # 2^17 units of 2^-24 of it, 2^-7, and the quotient of two by twice that, beside the attention tests' bound.
+    times, page, dim = 1 << 14, 1024, 64
+    n = 3 * torch.cuda.get_device_properties(0).multi_processor_count + 5
+    rng = np.random.default_rng(heads)
+    cache = make_cache(ss, rng, fmt, 1, 1, page, dim)
+    q = torch.from_numpy(R.bf16(rng.standard_normal((3, heads, dim)))).to(torch.bfloat16).cuda()
+    batch = q[torch.arange(n, device="cuda") % 3].contiguous()
+    out, lse, st = torch.full_like(batch, 7), torch.full((n, heads), 7.0, device="cuda"), ints([-1] * n)
+    table, rows = torch.zeros(1, times, dtype=torch.int32, device="cuda"), torch.zeros(n, dtype=torch.int32, device="cuda")
+    lens = torch.full((n,), times * page - 1, dtype=torch.int32, device="cuda")
+    ss.ss_cache_attention(cache, 0, batch, out, table, lens, workspace, st, table_rows=rows, lse=lse)
+    torch.cuda.synchronize()
+    late = bool((st == ss.SS_ROW_TIMEOUT).any())
+    if late:
+        workspace.zero_()
+    assert not late and not st.any()
+    k, v, mv = dense(cache)
+    for i in range(3):
+        o, l, m, _ = R.attend(np32(q[i:i + 1]).astype(np.float64), lambda p, s: (k[p, :, s], v[p, :, s], mv[p, :, s]), [0], page,
+                              page - 1, dim ** -0.5, 0, 0, None, 1)
+        err = np.abs(np32(out[i::3]).astype(np.float64) - o)
+        assert (err <= 2.0 ** -8 * (np.abs(o) + m) * (1 + 1 / 16) + 2.0 ** -6 * m).all()
+        assert (np.abs(lse[i::3].cpu().numpy() - (l + np.log(times))) <= 2.0 ** -7 + 2.0 ** -12).all()
