@@ -625,11 +625,12 @@ ss_status ss_cache_read(const ss_append_args* args, ss_stream_t stream);
  * (lse stays finite where only a value is not).
  *
  * Sums and softmax statistics are held in fp32; the weights are rounded to
- * bf16 (4 bits: to f16) before they meet the values.  Results are right for
- * values up to 2^110 over the query's number of keys (4 bits: 2^100) in
- * magnitude; values below 2^-80 may count as 0.  The result does not depend on
- * timing: the work is split over the SMs by the lengths alone and joined in a
- * fixed order.
+ * bf16 (4 bits: to f16, in which those 2^22 and more below the query's largest
+ * lose bits and those 2^33 below it are 0) before they meet the values.
+ * Results are right for values up to 2^110 over the query's number of keys
+ * (4 bits: 2^100) in magnitude; values below 2^-80 may count as 0.  The result
+ * does not depend on timing: the work is split over the SMs by the lengths
+ * alone and joined in a fixed order.
  *
  * out_status: SS_ROW_BAD_PARAM (a count outside [0, max_queries], with parents
  * above SS_TREE_MAX_NODES, query rows outside [0, total_queries), a negative
