@@ -514,7 +514,8 @@ ss_status ss_fused_lmhead_sample(const ss_fused_args* args, ss_stream_t stream);
  * pages: token number t of request r lies in page page_table[r][t / page_size],
  * slot t % page_size.  A verification step with this library is
  *   ss_pages_reserve     pages for the step's new tokens
- *   per layer            ss_cache_append, ss_cache_attention
+ *   per layer            ss_rope_append (or ss_rope, ss_cache_append),
+ *                        ss_cache_attention
  *   ss_spec_verify or ss_tree_verify on the target's logits
  *   ss_commit_accepted, ss_pages_compact (trees), ss_pages_trim
  * The step's new tokens of a request are those its target rows belong to: the
@@ -529,14 +530,27 @@ ss_status ss_fused_lmhead_sample(const ss_fused_args* args, ss_stream_t stream);
  * tokens are invisible to attention. */
 typedef enum {
   SS_CACHE_BF16 = 0,
-  SS_CACHE_INT4 = 1 /* per (token, kv head) row x[0 .. head_dim) of K and of V: a low value m = min x
+  SS_CACHE_INT4 = 1,/* per (token, kv head) row x[0 .. head_dim) of K and of V: a low value m = min x
                        and a step s = the smallest bf16 >= (max x - m) / 15 (in fp32), both bf16, and
                        per channel n = min(15, round-half-even((x - m) / s)), 0 when s = 0; the row
                        stands for s * n + m.  A row with a NaN, an infinity or max x - m beyond fp32
                        has s = m = NaN.  Packed little-endian, eight channels per 32-bit word: channel
                        2i of the eight in bits 4i.. , channel 2i + 1 in bits 16 + 4i.. (i = 0..3).
                        The scale arrays hold the pair (s, m) per row. */
+  SS_CACHE_FP8 = 2  /* a channel is an e4m3 byte n and stands for s * n, s an fp32 scale that the rows of one
+                       block share: SS_FP8_BLOCK consecutive slots (all 8 of a page of 8) of one kv head, of K
+                       and of V separately.  The calls that write set s to the smallest power of two >= 2^-100
+                       with 448 s >= |x| for every finite value x of the block's rows, and n = x / s rounded to
+                       nearest even (a power of two: the scale costs no bit of x); a value that is not finite
+                       becomes the NaN of e4m3 and counts for no scale.  The rows of a block are those up to the
+                       request's last token: rows that were there before are read with the old scale and
+                       written again with the new one, rows past them are left.  So a row's small values are
+                       held to 2^-10 s, half of e4m3's smallest step, s by the largest value beside it.
+                       Attention and the reading calls take any scales.  The scale arrays hold s per block. */
 } ss_cache_format;
+
+/* Slots of a page that share a scale in an SS_CACHE_FP8 cache. */
+#define SS_FP8_BLOCK 16
 
 /* One cache: [num_layers][num_pages][num_kv_heads][page_size] rows of K and of
  * V in any order of those four (strides in bytes, the same for K and V). */
@@ -547,16 +561,19 @@ typedef struct {
   int32_t num_kv_heads;
   int32_t page_size;            /* power of two in [8, 1024]                       */
   int32_t head_dim;             /* bf16: multiple of 8 in [8, 128]; 4 bits:
-                                   multiple of 32 in [32, 128]                    */
+                                   multiple of 32 in [32, 128]; 8 bits: multiple
+                                   of 16 in [16, 128]                             */
   void* k;                      /* 16-byte aligned                                 */
   void* v;
   int64_t layer_stride;         /* bytes, multiples of 16                          */
   int64_t page_stride;
   int64_t head_stride;
-  int64_t slot_stride;          /* >= the row's bytes: 2 head_dim, or head_dim / 2 */
-  void* k_scale;                /* 4 bits only: pairs, 16-byte aligned; the pairs  */
-  void* v_scale;                /* of a page's slots lie next to each other        */
-  int64_t scale_layer_stride;   /* bytes, multiples of 16                          */
+  int64_t slot_stride;          /* >= the row's bytes: 2 head_dim, head_dim / 2 or
+                                   head_dim                                       */
+  void* k_scale;                /* 4 bits: pairs, 16-byte aligned; 8 bits: fp32,   */
+  void* v_scale;                /* 4-byte aligned; those of a page lie next to each
+                                   other                                          */
+  int64_t scale_layer_stride;   /* bytes, multiples of 16 (8 bits: of 4)           */
   int64_t scale_page_stride;
   int64_t scale_head_stride;
 } ss_kv_cache;
@@ -578,13 +595,15 @@ typedef struct {
 
 /* ss_cache_append writes the new tokens' keys and values of one layer (k and
  * v are read); ss_cache_read reads the same rows back as bf16 (k and v are
- * written; 4-bit values s * n + m rounded once).  Request r has the rows
+ * written; 4-bit values s * n + m and 8-bit values s * n rounded once).
+ * Request r has the rows
  * token_offsets[r] .. token_offsets[r + 1] - 1 of k and v, at the slots from
  * kv_len[r].  out_status: SS_ROW_BAD_PARAM (a count outside [0, max_tokens],
  * rows outside [0, total_tokens), a negative kv_len or a table row outside the
  * table: nothing of the request is touched), SS_ROW_BAD_INDEX (a slot beyond
  * the table or in a hole: those tokens are left out, the others done; rows
- * read from there are zero). */
+ * read from there are zero).  8 bits: no two requests of a call may write into
+ * one block, and a block's rows before kv_len are read and may be written. */
 typedef struct {
   const ss_kv_cache* cache;
   const ss_page_pool* pool;     /* only the page table's four fields are used      */
@@ -620,15 +639,17 @@ ss_status ss_cache_read(const ss_append_args* args, ss_stream_t stream);
  * keys at positions > p - window or < sinks (a draft key of a tree is at its
  * node's position).  A query that sees nothing (holes) gets out = 0 and
  * lse = -infinity.  Keys and values that a query does not see never reach its
- * result, whatever they hold.  A query that sees a NaN or an infinity gets
+ * result, whatever they hold (8 bits: nor does a NaN or an infinity in a scale
+ * that only they have).  A query that sees a NaN or an infinity gets
  * results that are not finite or, for an infinite key, weights of 0 and 1
  * (lse stays finite where only a value is not).
  *
  * Sums and softmax statistics are held in fp32; the weights are rounded to
- * bf16 (4 bits: to f16, in which those 2^22 and more below the query's largest
- * lose bits and those 2^33 below it are 0) before they meet the values.
+ * bf16 (4 and 8 bits: to f16, in which those 2^22 and more below the query's
+ * largest lose bits and those 2^33 below it are 0) before they meet the values.
+ * (4 and 8 bits: queries' channels below 2^-15 of the row's largest lose bits.)
  * Results are right for values up to 2^110 over the query's number of keys
- * (4 bits: 2^100) in magnitude; values below 2^-80 may count as 0.  The result
+ * (4 and 8 bits: 2^100) in magnitude; values below 2^-80 may count as 0.  The result
  * does not depend on timing: the work is split over the SMs by the lengths
  * alone and joined in a fixed order.
  *
@@ -689,7 +710,7 @@ typedef enum {
   SS_STALL_VALUES,     /* a tile of V                                             */
   SS_STALL_SCORES,     /* the first product                                       */
   SS_STALL_WEIGHTS,    /* the softmax's weights                                   */
-  SS_STALL_PACKED      /* a tile's packed bytes (4 bits only, else
+  SS_STALL_PACKED      /* a tile's packed bytes (4 and 8 bits, else
                           SS_ERR_UNSUPPORTED)                                     */
 } ss_stall;
 ss_status ss_selftest_attention_timeout(const ss_attention_args* args, int32_t stall, void* workspace,
@@ -713,7 +734,8 @@ ss_status ss_selftest_attention_timeout(const ss_attention_args* args, int32_t s
  * and none of them a parent of the same call.
  *
  * ss_pages_compact: after ss_tree_verify, moves the accepted nodes' rows (K, V
- * and scales, in every layer) from slot kv_len[i] + path[i][j] to slot
+ * and scales, in every layer; 8 bits: a block into which rows move gets the
+ * scale of its rows up to new_len, and these are encoded anew) from slot kv_len[i] + path[i][j] to slot
  * kv_len[i] + 1 + j, j < num_accepted[i], and writes new_len[i] =
  * kv_len[i] + 1 + num_accepted[i] (the root, already in place, and the
  * accepted nodes).  path is ss_tree_verify's out_path ([n, path_stride], each
@@ -746,6 +768,103 @@ ss_status ss_pages_compact(const ss_page_pool* pool, const ss_kv_cache* cache, i
                            int32_t* out_status, ss_stream_t stream);
 ss_status ss_pages_trim(const ss_page_pool* pool, int32_t n, const int32_t* table_rows, const int32_t* length,
                         int32_t window, int32_t sinks, int32_t* out_status, ss_stream_t stream);
+
+/* ------------------------------------------------------ rotary positions --
+ * Queries and keys turned by their positions: the first rot_dim channels of a
+ * head are rot_dim / 2 pairs, (x_i, x_{i + rot_dim/2}) (halves) or
+ * (x_2i, x_{2i+1}) (interleaved), i = 0 .. rot_dim/2 - 1, and at position p
+ * pair (x, y) becomes
+ *   (magnitude (x cos a - y sin a), magnitude (y cos a + x sin a)),
+ *   a = 2 pi p turns[i];
+ * the other channels stay.  turns are fractions of a full turn per position in
+ * units of 2^-64 (0.64 fixed point): p turns[i] modulo 2^64 is exact in integer
+ * arithmetic, so far positions lose nothing.  Angles are rounded to 2^-24 of
+ * half a turn, the products and sums held in fp32, the result rounded to bf16.
+ *
+ * ss_rope_turns fills turns (HOST memory, rot_dim / 2 entries; to be copied to
+ * the device once) for the frequencies f_i = base^(-2i / rot_dim), scaled:
+ *   SS_ROPE_PLAIN     f_i
+ *   SS_ROPE_LINEAR    f_i / factor: positions squeezed into the trained length
+ *   SS_ROPE_BY_PARTS  f_i (g + (1 - g) / factor), g = (r - low) / (high - low)
+ *                     clamped to [0, 1], r = length f_i / (2 pi): pairs that
+ *                     turn less than `low` times within the trained length are
+ *                     squeezed, those that turn more than `high` times stay
+ * It needs 2 <= rot_dim <= 128 and even, a finite base > 0 and frequencies of
+ * at most pi; factor > 0, length > 0 and high > low >= 0 finite where they are
+ * used; else SS_ERR_INVALID_ARG. */
+typedef enum { SS_ROPE_PLAIN = 0, SS_ROPE_LINEAR = 1, SS_ROPE_BY_PARTS = 2 } ss_rope_scaling;
+typedef enum { SS_ROPE_HALVES = 0, SS_ROPE_INTERLEAVED = 1 } ss_rope_layout;
+
+ss_status ss_rope_turns(int32_t rot_dim, double base, int32_t scaling, double factor, double length, double low,
+                        double high, uint64_t* turns);
+
+typedef struct {
+  const uint64_t* turns;        /* DEVICE memory, [rot_dim / 2], 8-byte aligned    */
+  int32_t rot_dim;              /* even, in [2, head_dim]                          */
+  int32_t layout;               /* ss_rope_layout                                  */
+  float magnitude;              /* finite                                          */
+} ss_rope_table;
+
+/* ss_rope: the new tokens' queries and keys turned.  Token i of request r
+ * stands at position kv_len[r] + i; with parents (a draft tree per request, as
+ * ss_tree_verify takes it) at kv_len[r] + depth(i); with positions at
+ * positions[its row], any int32.  k may be NULL (queries alone), and q.  An
+ * output may be its input (the same pointer and strides); it must not overlap
+ * an input otherwise.  Rows of no request are left as they were.
+ * out_status: SS_ROW_BAD_PARAM (a count outside [0, max_tokens], with parents
+ * above SS_TREE_MAX_NODES, rows outside [0, total_tokens), a negative kv_len:
+ * the request's rows are not written; or a parent outside [0, i): the node is
+ * taken as a child of the root). */
+typedef struct {
+  const ss_rope_table* rope;
+  int32_t num_requests;         /* at most 65535                                   */
+  int32_t max_tokens;           /* >= every request's number of new tokens         */
+  int32_t total_tokens;         /* rows of q and k (0: they may be NULL)           */
+  int32_t head_dim;             /* multiple of 8 in [8, 128]                       */
+  const int32_t* token_offsets; /* [num_requests + 1], or NULL: one token each     */
+  const int32_t* kv_len;        /* [num_requests]; with positions not read: NULL   */
+  const int32_t* parents;       /* [total_tokens] local parent node, or NULL       */
+  const int32_t* positions;     /* [total_tokens], or NULL (one of the two at most) */
+  int32_t num_heads;            /* of q, [0, 65535]                                */
+  int32_t num_kv_heads;         /* of k, [0, 65535]                                */
+  const void* q;                /* [total_tokens, num_heads, head_dim] bf16,       */
+  void* q_out;                  /* 16-byte aligned; strides in elements, multiples */
+  int64_t q_token_stride;       /* of 8                                            */
+  int64_t q_head_stride;
+  int64_t q_out_token_stride;
+  int64_t q_out_head_stride;
+  const void* k;                /* the same with num_kv_heads                      */
+  void* k_out;
+  int64_t k_token_stride;
+  int64_t k_head_stride;
+  int64_t k_out_token_stride;
+  int64_t k_out_head_stride;
+  int32_t* out_status;          /* [num_requests]                                  */
+} ss_rope_args;
+
+ss_status ss_rope(const ss_rope_args* args, ss_stream_t stream);
+
+/* ss_rope_append: ss_rope on the queries and keys, and ss_cache_append of the
+ * turned keys (as bf16 has them) and of the values, in one launch: the cache
+ * holds what the two calls would leave there, the turned keys go nowhere else.
+ * `append` describes the requests, k and v; k is not written.  out_status
+ * (append's): the larger of both calls' codes; SS_ROW_BAD_PARAM for a request
+ * that either refuses: nothing of it is touched. */
+typedef struct {
+  const ss_rope_table* rope;
+  const ss_append_args* append;
+  const int32_t* parents;       /* as ss_rope_args                                 */
+  const int32_t* positions;     /* (the slots are those from kv_len all the same)  */
+  int32_t num_heads;            /* of q, [0, 65535]; 0: q and q_out may be NULL    */
+  const void* q;
+  void* q_out;
+  int64_t q_token_stride;
+  int64_t q_head_stride;
+  int64_t q_out_token_stride;
+  int64_t q_out_head_stride;
+} ss_rope_append_args;
+
+ss_status ss_rope_append(const ss_rope_append_args* args, ss_stream_t stream);
 
 /* Cluster size (CTAs per vocabulary row) the kernels use for this vocabulary
  * and dtype, or 0 if unsupported.  A row is split over at most 8 CTAs of at

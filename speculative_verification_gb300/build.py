@@ -14,10 +14,11 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libss.so")
-SOURCES = ["ss_kernel.cu", "ss_hist.cu", "ss_shard.cu", "ss_fused.cu", "ss_cache.cu", "ss_attn.cu",
-           "ss_attn_bf16.cu", "ss_attn_int4.cu"]
-SHARED_REGISTERS = ["ss_attn_bf16.cu", "ss_attn_int4.cu"]  # whose kernels' warpgroups share registers out again
-DEPS = SOURCES + ["ss_hist.h", "ss_cache.h", "ss_attn.cuh", "ss_philox.cuh", "ss_ptx.cuh", "ss_nvtx.h"]
+SOURCES = ["ss_kernel.cu", "ss_hist.cu", "ss_shard.cu", "ss_fused.cu", "ss_cache.cu", "ss_rope.cu", "ss_attn.cu",
+           "ss_attn_bf16.cu", "ss_attn_int4.cu", "ss_attn_fp8.cu"]
+# whose kernels' warpgroups share registers out again: bf16, and those that unpack
+SHARED_REGISTERS = [["ss_attn_bf16.cu"], ["ss_attn_int4.cu", "ss_attn_fp8.cu"]]
+DEPS = SOURCES + ["ss_hist.h", "ss_cache.h", "ss_rows.cuh", "ss_attn.cuh", "ss_philox.cuh", "ss_ptx.cuh", "ss_nvtx.h"]
 
 NVCC_FLAGS = [
     "-std=c++17", "-O3", "-lineinfo",
@@ -45,7 +46,7 @@ def check_registers(log):
         if int(want) and want != used:
             raise RuntimeError("attention kernel for %s rows, %s, %s x 64 channels: the compiler used %s registers per "
                                "thread, its warpgroups share out %s" %
-                               (rows, "4 bits" if packed == "1" else "bf16", halves, used, want))
+                               (rows, "4 or 8 bits" if packed == "1" else "bf16", halves, used, want))
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -58,7 +59,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     for src in SOURCES:
         obj = os.path.join(OUT_DIR, src.replace(".cu", ".o"))
         cmd = [nvcc()] + NVCC_FLAGS + ["-I" + INCLUDE, "-c", "-o", obj, os.path.join(CSRC, src)]
-        checked = src in SHARED_REGISTERS
+        checked = any(src in family for family in SHARED_REGISTERS)
         if verbose or checked:
             cmd.insert(1, "-Xptxas=-v")
         procs.append((src, subprocess.Popen(cmd, stderr=subprocess.PIPE if checked else None, text=True)))
@@ -70,8 +71,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
             sys.stderr.write(log)
     if failed:
         raise subprocess.CalledProcessError(1, "nvcc " + " ".join(failed))
-    for src in SHARED_REGISTERS:
-        check_registers(logs[src])
+    for family in SHARED_REGISTERS:
+        check_registers("".join(logs[src] for src in family))
     tmp = LIB + ".tmp%d" % os.getpid()
     subprocess.check_call([nvcc()] + LINK_FLAGS + ["-o", tmp] + objs)
     os.replace(tmp, LIB)

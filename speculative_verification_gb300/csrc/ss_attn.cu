@@ -27,22 +27,24 @@ static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 
 // bf16: boxes of 64 channels, the 128-byte swizzle, as the tensor cores read
 // them.  4 bits: whole rows (32 or 64 bytes), the swizzle of that width, which
-// spreads the rows that a warp unpacks over the shared-memory banks.  Channels
-// and pages out of range read as zero.
+// spreads the rows that a warp unpacks over the shared-memory banks.  8 bits:
+// whole rows (64 or 128 bytes), likewise, and K's are what the tensor cores read.
+// Channels and pages out of range read as zero.
 bool make_cache_map(CUtensorMap* m, void* base, const CacheView& c, int box_slots) {
   auto fn = encode_fn();
   if (!fn) return false;
-  const bool packed = c.format == SS_CACHE_INT4;
+  const bool packed = c.format == SS_CACHE_INT4, bytes = c.format == SS_CACHE_FP8;
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(packed ? c.dim / 2 : c.dim), 1ull << c.page_shift,
                               static_cast<cuuint64_t>(c.heads), static_cast<cuuint64_t>(c.num_pages)};
   const cuuint64_t strides[3] = {static_cast<cuuint64_t>(c.slot_stride), static_cast<cuuint64_t>(c.head_stride),
                                  static_cast<cuuint64_t>(c.page_stride)};
   const bool wide = c.dim > 64;
-  const cuuint32_t box[4] = {packed ? (wide ? 64u : 32u) : 64u, static_cast<cuuint32_t>(box_slots), 1u, 1u};
+  const cuuint32_t box[4] = {packed ? (wide ? 64u : 32u) : bytes && wide ? 128u : 64u, static_cast<cuuint32_t>(box_slots), 1u, 1u};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
-  return fn(m, packed ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, box,
+  return fn(m, packed || bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, box,
             estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            !packed ? CU_TENSOR_MAP_SWIZZLE_128B : wide ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
+            packed ? (wide ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B)
+            : bytes && !wide ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -127,7 +129,7 @@ static ss_status attention(const ss_attention_args* args, int32_t stall, void* w
   // tensor-core and softmax time (clocks a tile, bf16: 2550 for 8 rows, where the
   // copy bounds it, 2900 for 128; 4 bits: 1390 for 8, 2700 for 64).
   const int64_t rows = static_cast<int64_t>(a.max_queries) * a.group;
-  const int32_t most = a.c.format == SS_CACHE_INT4 ? 64 : 128;
+  const int32_t most = a.c.format == SS_CACHE_BF16 ? 128 : 64;
   a.block_rows = 8;
   while (a.block_rows < rows && a.block_rows < most) a.block_rows *= 2;
   // The most tiles that the table and the numbers of queries allow.
@@ -138,8 +140,8 @@ static ss_status attention(const ss_attention_args* args, int32_t stall, void* w
   a.counters = static_cast<int32_t*>(workspace);
   a.pieces = reinterpret_cast<float*>(a.counters + kMaxCtas);
   a.gave_up = reinterpret_cast<int32_t*>(a.pieces + static_cast<size_t>(kMaxCtas) * 2 * kSlotFloats);
-  return a.c.format == SS_CACHE_INT4 ? launch_int4(a, reinterpret_cast<cudaStream_t>(stream))
-                                     : launch_bf16(a, reinterpret_cast<cudaStream_t>(stream));
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return a.c.format == SS_CACHE_FP8 ? launch_fp8(a, s) : a.c.format == SS_CACHE_INT4 ? launch_int4(a, s) : launch_bf16(a, s);
 }
 
 ss_status ss_cache_attention(const ss_attention_args* args, void* workspace, size_t workspace_bytes,
@@ -152,7 +154,7 @@ ss_status ss_selftest_attention_timeout(const ss_attention_args* args, int32_t s
                                         size_t workspace_bytes, ss_stream_t stream) {
   SS_NVTX_RANGE("ss_selftest_attention_timeout");
   if (stall < SS_STALL_ITEMS || stall > SS_STALL_PACKED) return SS_ERR_INVALID_ARG;
-  if (stall == SS_STALL_PACKED && args && args->cache && args->cache->format != SS_CACHE_INT4) return SS_ERR_UNSUPPORTED;
+  if (stall == SS_STALL_PACKED && args && args->cache && args->cache->format == SS_CACHE_BF16) return SS_ERR_UNSUPPORTED;
   return attention(args, stall, workspace, workspace_bytes, stream);
 }
 

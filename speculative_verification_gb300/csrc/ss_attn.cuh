@@ -1,5 +1,5 @@
 // ss_attn.cuh -- attention of a step's new tokens over the paged cache, on the
-// tensor cores (ss_attn_bf16.cu and ss_attn_int4.cu instantiate it).
+// tensor cores (ss_attn_bf16.cu, ss_attn_int4.cu and ss_attn_fp8.cu instantiate it).
 //
 // The mathematics.  For a row n (one query of one head) and the keys j it
 // sees, x_nj = scale log2(e) q_n.k_j, with a reference r_n (below):
@@ -129,6 +129,7 @@ struct AttnArgs {
 
 ss_status launch_bf16(const AttnArgs& a, cudaStream_t s);
 ss_status launch_int4(const AttnArgs& a, cudaStream_t s);
+ss_status launch_fp8(const AttnArgs& a, cudaStream_t s);
 
 // Rank-4 tensor map (channel bytes, slot, head, page) of K or V.
 bool make_cache_map(CUtensorMap* m, void* base, const CacheView& c, int box_slots);
@@ -154,9 +155,11 @@ struct Item {
 };
 
 // kLive: rows of an item; kN: rows of the second product's MMAs (16 at least);
-// kNS: columns of the first product (4 bits: two per row).
-template <int kLive, bool kPacked, int kHalves>
+// kNS: columns of the first product (4 and 8 bits: two per row).  kPacked: 4 or
+// 8 bits, kBytes: 8.
+template <int kLive, bool kPacked, int kHalves, bool kBytes>
 struct Cfg {
+  static constexpr bool kNibbles = kPacked && !kBytes;
   static constexpr int kN = kLive < 16 ? 16 : kLive;
   static constexpr int kNS = kPacked ? 2 * kLive : kN;
   static constexpr int kGroups = kLive <= 16 ? 1 : kLive == 32 ? 2 : kPacked ? 2 : 4;  // softmax warpgroups
@@ -168,17 +171,17 @@ struct Cfg {
   static constexpr int kSoft = 128 * kGroups * kStreams;
   static constexpr int kPerTile = kSoft / kStreams;          // softmax threads of one tile
   // 4 bits: one warpgroup unpacks K; V, twice the work, has two that take turns
-  // where the softmax leaves the registers
+  // where the softmax leaves the registers.  8 bits: K is used as it is.
   static constexpr int kVGroups = kLive <= 16 ? 2 : 1;
-  static constexpr int kUnpack = kPacked ? 128 * (1 + kVGroups) : 0;
+  static constexpr int kUnpack = kPacked ? 128 * (kNibbles + kVGroups) : 0;
   static constexpr int kThreads = 128 + kSoft + kUnpack;
   // Registers per thread by warpgroup where one size does not fit all: the
   // launch's kThreads x kRegs are shared out again (all or none of them).
   static constexpr int kRegs = kThreads > 640 ? 80 : kThreads > 512 ? 96 : kThreads > 384 ? 128 : 168;
   static constexpr bool kSplit = kPacked || kLive == 128;
   static constexpr int kRegs0 = kStreams == 2 ? 56 : 64;                                   // copies, MMAs, queries
-  static constexpr int kRegsSoft = !kPacked || kStreams == 2 ? 104 : kLive >= 64 ? 152 : 136;
-  static constexpr int kRegsUnpack = kLive >= 64 ? 56 : 72;
+  static constexpr int kRegsSoft = kBytes ? (kStreams == 2 ? 128 : 184) : !kPacked || kStreams == 2 ? 104 : kLive >= 64 ? 152 : 136;
+  static constexpr int kRegsUnpack = kBytes ? 80 : kLive >= 64 ? 56 : 72;
   static_assert(!kSplit || kRegs0 + kSoft / 128 * kRegsSoft + kUnpack / 128 * kRegsUnpack <= kThreads / 128 * kRegs,
                 "a warpgroup would wait for registers for ever");
   static constexpr int kStage = kHalves * 16384;             // 128 keys x 64 channels x 2 bytes per half
@@ -190,9 +193,8 @@ struct Cfg {
   // a second buffer of P where it costs K and V no slot of their ring (128 rows:
   // 16 trees 95 us with one, 108 with two and a ring of three)
   static constexpr int kPBufs = kLive >= 128 ? 1 : 2;
-  static constexpr int kRawRow = 32 * kHalves;               // packed bytes per key
-  static constexpr int kRaw = kPacked ? 2 * kTile * kRawRow + 2 * kTile * 4 : 0;
-  static constexpr int kRawStages = kPacked ? 4 : 1;
+  static constexpr int kRawRow = (kBytes ? 64 : 32) * kHalves;  // packed bytes per key
+  static constexpr int kRaw = kNibbles ? 2 * kTile * kRawRow + 2 * kTile * 4 : kBytes ? kTile * kRawRow : 0;  // 8 bits: V's
   // V's unpacking in a loop where the other warps' code is long: together they
   // are bound by instruction fetch (48 x 1-8 drafts of 64 rows: 353 us, 414
   // unrolled); unrolled with its loads ahead of the wait where it is latency
@@ -201,18 +203,25 @@ struct Cfg {
   static constexpr int kUnrollPV = kLive >= 64 ? 1 : 8;  // likewise (2 x 4096 prompt: 311 us, 318 unrolled)
   // the static arrays, rounded up
   static constexpr int kMeta = kNQ * (static_cast<int>(sizeof(Item)) + kN * 36 + 64 + 512) + kStreams * kN * 36 + 1536 +
-                               (kPacked ? 2 * kPairs * kTile * 4 : 0);
-  static constexpr int kBudget = 232448 - 1024 - kQBufs * kQ - kPBufs * kP - kRawStages * kRaw - kMeta;
+                               (kNibbles ? 2 * kPairs * kTile * 4 : kBytes ? kInfo * 32 * 4 : 0);
+  static constexpr int kRoom = 232448 - 1024 - kQBufs * kQ - kPBufs * kP - kMeta;
+  // 8 bits: two tiles of V unpacked (four small ones), the rest for tiles as they
+  // come, K's and V's
+  static constexpr int kBytesVs = kHalves == 2 ? 2 : 4;
+  static constexpr int kTiles8 = kBytes ? (kRoom - kBytesVs * kStage) / kRaw : 0;
+  static constexpr int kRawStages = kNibbles ? 4 : !kBytes ? 1 : kTiles8 / 2 >= 4 ? 4 : 2;
+  static constexpr int kKs8 = kTiles8 - kRawStages < 8 ? kTiles8 - kRawStages : 8;
+  static constexpr int kBudget = kRoom - kRawStages * kRaw;
   // K and V have a ring each, so that whoever waits for a slot has used the
   // slot's previous contents itself: a parity wait tells two phases apart, no
   // more.  4 bits: only V's is in shared memory, K's two slots are columns.
   static constexpr int kMost = kPacked ? 4 : 8;
-  static constexpr int kRing = kBudget / kStage < kMost ? kBudget / kStage : kMost;
-  static constexpr int kKs = kPacked ? 2 : kRing / 2, kVs = kPacked ? kRing : kRing - kKs;
-  static constexpr int kSmem = 1024 + kRing * kStage + kQBufs * kQ + kPBufs * kP + kRawStages * kRaw;
+  static constexpr int kRing = kBytes ? kBytesVs : kBudget / kStage < kMost ? kBudget / kStage : kMost;
+  static constexpr int kKs = kBytes ? kKs8 : kPacked ? 2 : kRing / 2, kVs = kPacked ? kRing : kRing - kKs;
+  static constexpr int kSmem = 1024 + kRing * kStage + kQBufs * kQ + kPBufs * kP + kRawStages * kRaw + (kBytes ? kKs * kRaw : 0);
   // tensor-memory columns: S x 2, O x 2, and for 4 bits K x 2 (four channels per column)
   static constexpr uint32_t kOCol = 2 * kNS, kKCol = kOCol + 2 * kStreams * kN;
-  static constexpr uint32_t kKCols = kPacked ? 16 * kHalves : 0;
+  static constexpr uint32_t kKCols = kNibbles ? 16 * kHalves : 0;
   static constexpr uint32_t kUsed = kKCol + 2 * kKCols;
   static constexpr uint32_t kTmem = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
   static_assert(kKs >= 1 && kVs >= 2, "a tile in use and one on its way");
@@ -323,10 +332,13 @@ __device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, int
       : "memory");
 }
 
-// 16 bytes by the thread's own asynchronous copy (zeros where `there` is
+// 16 or 4 bytes by the thread's own asynchronous copy (zeros where `there` is
 // false), and an arrival on `bar` once the thread's copies so far are done.
 __device__ __forceinline__ void async_load16(uint32_t dst, const void* src, bool there) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16u : 0u) : "memory");
+}
+__device__ __forceinline__ void async_load4(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4u : 0u) : "memory");
 }
 __device__ __forceinline__ void async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
@@ -388,6 +400,16 @@ __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// e4m3, both operands in shared memory.
+__device__ __forceinline__ void umma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 
@@ -519,9 +541,13 @@ __device__ __forceinline__ uint32_t e4m3_pair(float a, float b) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
   return r;
 }
-__device__ __forceinline__ float2 e4m3_floats(uint32_t pair) {
+__device__ __forceinline__ uint32_t f16_of_e4m3(uint32_t pair) {
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(pair)));
+  return h;
+}
+__device__ __forceinline__ float2 e4m3_floats(uint32_t pair) {
+  const uint32_t h = f16_of_e4m3(pair);
   float2 f;
   asm("{\n\t.reg .f16 l, u;\n\tmov.b32 {l, u}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, u;\n\t}"
       : "=f"(f.x), "=f"(f.y)
@@ -695,11 +721,11 @@ __device__ __forceinline__ int32_t request_tiles(const AttnArgs& a, const Reques
   return sum;
 }
 
-// The queries of an item over a 4-bit cache: row n as unit (hi + lo / 32), both
+// The queries of an item over a cache of 4 or 8 bits: row n as unit (hi + lo / 32), both
 // e4m3, unit a power of two by the row's largest channel: q's 8 bits are 4 + 4,
 // so this is exact but for channels below 2^-15 of the largest.  16 lanes per
 // row, 8 channels each; a warp has 2 kEach rows in flight.
-template <int kLive, int kEach>
+template <int kLive, int kEach, bool kBytes>
 __device__ __forceinline__ void convert_queries(const AttnArgs& a, const Item& it, uint8_t* q, float* qsum, float* unit,
                                                 int warp, int warps) {
   const int lane = threadIdx.x & 31, ch = lane & 15;
@@ -742,11 +768,12 @@ __device__ __forceinline__ void convert_queries(const AttnArgs& a, const Item& i
       const int e = max((__float_as_int(top) >> 23) & 0xff, 16);
       const float scale = __int_as_float((261 - e) << 23);
       uint32_t hi[2] = {0u, 0u}, lo[2] = {0u, 0u};
-      // the unpacked keys' order of eight channels: 0 4 1 5, 2 6 3 7
+      // the keys' order of eight channels; 4 bits, unpacked: 0 4 1 5, 2 6 3 7
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int c = (i & 1) + (i >> 1) * 2;  // pairs (0, 4), (1, 5), (2, 6), (3, 7)
-        const float p0 = v[c] * scale, p1 = v[c + 4] * scale;
+        // 4 bits: pairs (0, 4), (1, 5), (2, 6), (3, 7)
+        const int c = kBytes ? 2 * i : (i & 1) + (i >> 1) * 2, d = kBytes ? c + 1 : c + 4;
+        const float p0 = v[c] * scale, p1 = v[d] * scale;
         const uint32_t h = e4m3_pair(p0, p1);
         const float2 back = e4m3_floats(h);
         const uint32_t r = e4m3_pair((p0 - back.x) * 32.0f, (p1 - back.y) * 32.0f);
@@ -757,7 +784,7 @@ __device__ __forceinline__ void convert_queries(const AttnArgs& a, const Item& i
       *reinterpret_cast<uint2*>(at + n * 128) = make_uint2(hi[0], hi[1]);
       *reinterpret_cast<uint2*>(at + (kLive + n) * 128) = make_uint2(lo[0], lo[1]);
       if (ch == 0) {
-        qsum[n] = sum;
+        if (!kBytes) qsum[n] = sum;
         unit[n] = __int_as_float((e - 7) << 23);
       }
     }
@@ -767,11 +794,12 @@ __device__ __forceinline__ void convert_queries(const AttnArgs& a, const Item& i
 // kAtLaunch: the registers per thread that the warpgroups share out again, or 0
 // where they do not.  As a part of the kernel's name it lets the build hold what
 // the compiler used against it.
-template <int kLive, bool kPacked, int kHalves, int kAtLaunch>
-__global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
+template <int kLive, bool kPacked, int kHalves, int kAtLaunch, bool kBytes>
+__global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves, kBytes>::kThreads, 1)
     attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                 const __grid_constant__ CUtensorMap tm_q, const AttnArgs a) {
-  using F = Cfg<kLive, kPacked, kHalves>;
+  using F = Cfg<kLive, kPacked, kHalves, kBytes>;
+  constexpr bool kNibbles = F::kNibbles;
   constexpr int kRing = F::kRing, kKs = F::kKs, kVs = F::kVs, kNQ = F::kNQ, kCols = F::kCols, kN = F::kN, kNS = F::kNS;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t kfull[kKs], kempty[kKs], vfull[kVs], vempty[kVs], sfull[2], sempty[2], pfull[2], pdone[2], oempty[2],
@@ -781,23 +809,24 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
   __shared__ __align__(16) uint64_t row_path[kNQ][kN];
   __shared__ int64_t row_out[kNQ][kN];
   __shared__ int64_t row_lse[kNQ][kN];
-  __shared__ __align__(16) float row_qsum[kPacked ? kNQ : 1][kPacked ? kN : 4], row_unit[kPacked ? kNQ : 1][kPacked ? kN : 4];
+  __shared__ __align__(16) float row_qsum[kNibbles ? kNQ : 1][kNibbles ? kN : 4], row_unit[kPacked ? kNQ : 1][kPacked ? kN : 4];
   __shared__ uint8_t node_depth[kNQ][SS_TREE_MAX_NODES];
   __shared__ uint64_t node_sees[kNQ][SS_TREE_MAX_NODES];
   __shared__ uint32_t info[kInfo];
-  __shared__ uint32_t k_pair[kPacked ? kPairs : 1][kPacked ? kTile : 1], v_pair[kPacked ? kPairs : 1][kPacked ? kTile : 1];
+  __shared__ uint32_t k_pair[kNibbles ? kPairs : 1][kNibbles ? kTile : 1], v_pair[kNibbles ? kPairs : 1][kNibbles ? kTile : 1];
+  __shared__ float scales[kBytes ? kInfo : 1][kBytes ? 32 : 1];  // 8 bits, of 8 keys each: K's, V's
   constexpr int kRows = F::kStreams * kN;  // of the softmax's state
   __shared__ __align__(16) float nref[kRows], corr[kRows], shift[kRows], sums[kRows], csums[kRows];
   __shared__ float part[4][kRows];
   __shared__ uint32_t tmem_slot;
-  __shared__ uint8_t v_bad[2][F::kGroups > 1 && !kPacked ? kTile : 1];  // keys whose values are not finite
+  __shared__ uint8_t v_bad[2][F::kGroups > 1 && !kNibbles ? kTile : 1];  // keys whose values are not finite
   __shared__ int32_t s_dead, s_last, s_r0, s_before, s_tiles0, s_scan[32];
 
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* pbuf = ring + kRing * F::kStage;
   uint8_t* qbuf = pbuf + F::kPBufs * F::kP;
   uint8_t* vring = ring + (kPacked ? 0 : kKs) * F::kStage;  // after K's slots
-  uint8_t* raw = qbuf + F::kQBufs * F::kQ;
+  uint8_t* raw = qbuf + F::kQBufs * F::kQ;  // (8 bits: after it K's slots)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int32_t* dead = &s_dead;
 
@@ -805,7 +834,8 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
     // the self-test of the waits: one kind of barrier expects an arrival more
     const auto more = [&](int kind) { return a.stall == kind ? 1u : 0u; };
     for (int i = 0; i < kKs; ++i) {
-      mbar_init(kfull + i, (kPacked ? 128 : 1) + more(SS_STALL_KEYS));
+      // (8 bits: the copies' bytes, and the lanes' own copies)
+      mbar_init(kfull + i, (kNibbles ? 128 : kBytes ? 33 : 1) + more(SS_STALL_KEYS));
       mbar_init(kempty + i, 1);
     }
     for (int i = 0; i < kVs; ++i) {
@@ -827,8 +857,8 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
     for (int i = 0; i < F::kQBufs; ++i) mbar_init(qfree + i, 1);
     if (kPacked)
       for (int i = 0; i < F::kRawStages; ++i) {
-        mbar_init(rfull + i, 33 + more(SS_STALL_PACKED));  // the copies' bytes, and the lanes' own copies
-        mbar_init(rempty + i, 256);
+        mbar_init(rfull + i, (kNibbles ? 33 : 1) + more(SS_STALL_PACKED));  // the copies' bytes, and the lanes' own copies
+        mbar_init(rempty + i, kNibbles ? 256 : 128);
       }
     for (int i = 0; i < 2; ++i) mbar_init(written + i, F::kGroups > 1 ? F::kSoft - 128 : 1);
     mbar_init(&drain[0], 1);
@@ -837,7 +867,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
     s_r0 = s_before = 0;
     fence_barrier_init();
   }
-  if (F::kGroups > 1 && !kPacked && tid < kTile) v_bad[0][tid] = v_bad[1][tid] = 0;
+  if (F::kGroups > 1 && !kNibbles && tid < kTile) v_bad[0][tid] = v_bad[1][tid] = 0;
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_slot)),
                  "r"(F::kTmem)
@@ -974,7 +1004,27 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
                      page < 0 ? a.c.num_pages : page, bar);
           }
         };
-        if constexpr (kPacked) {
+        if constexpr (kBytes) {
+          const int ks = at % kKs, s = at % F::kRawStages;
+          wait(kempty + ks, at / kKs + 1);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(kfull + ks, F::kRaw);
+          __syncwarp();
+          copies(&tm_k, raw_a + (F::kRawStages + ks) * F::kRaw, kfull + ks);
+          // the scales of eight slots per lane, K's and then V's
+          const int p = __shfl_sync(0xffffffffu, page, (8 * (lane & 15)) >> unit_shift);
+          const int slot = (j0 + 8 * (lane & 15)) & ((1 << a.c.page_shift) - 1);
+          const int64_t off = max(p, 0) * a.c.s_page_stride + head * a.c.s_head_stride + (slot >> a.c.block_shift) * 4;
+          async_load4(smem_addr(&scales[at % kInfo][lane]), (lane < 16 ? a.c.ks : a.c.vs) + off, p >= 0);
+          async_arrive(kfull + ks);
+          ++k_tiles;
+          wait(rempty + s, at / F::kRawStages + 1);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(rfull + s, F::kRaw);
+          __syncwarp();
+          copies(&tm_v, raw_a + s * F::kRaw, rfull + s);
+          ++v_tiles;
+        } else if constexpr (kPacked) {
           const int s = at % F::kRawStages;
           wait(rempty + s, at / F::kRawStages + 1);
           if (!ok) break;
@@ -1015,8 +1065,13 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
     // The copies in flight end before this warp does, also where other warps
     // have given up on them (else their users wait for them anyway).
     bool landed = true;
-    if (kPacked) {
-      asm volatile("cp.async.wait_all;" ::: "memory");
+    if (kPacked) asm volatile("cp.async.wait_all;" ::: "memory");
+    if (kBytes) {
+      for (int32_t i = max(0, k_tiles - kKs); i < k_tiles && landed; ++i)
+        landed = wait_drained(kfull + i % kKs, (i / kKs) & 1);
+      for (int32_t i = max(0, v_tiles - F::kRawStages); i < v_tiles && landed; ++i)
+        landed = wait_drained(rfull + i % F::kRawStages, (i / F::kRawStages) & 1);
+    } else if (kPacked) {
       for (int32_t i = max(0, at - F::kRawStages); i < at && landed; ++i)
         landed = wait_drained(rfull + i % F::kRawStages, (i / F::kRawStages) & 1);
     } else {
@@ -1059,7 +1114,15 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          if constexpr (kPacked) {
+          if constexpr (kBytes) {
+            constexpr uint32_t kHiK = kHalves == 2 ? desc_hi(1024, 2) : desc_hi(512, 4);  // rows of 128 or 64 bytes
+            const uint32_t ka = desc_lo(q_a + F::kQBufs * F::kQ + (F::kRawStages + s) * F::kRaw, 16);
+#pragma unroll
+            for (int kk = 0; kk < 2 * kHalves; ++kk)
+              if (kk < k_steps)
+                umma_e4m3(tm + b * kNS, desc(ka + kk * 2, kHiK), desc(qa + kk * 2, kHi), instr_desc_e4m3<kNS>(),
+                          kk > 0 ? 1u : 0u);
+          } else if constexpr (kPacked) {
 #pragma unroll
             for (int kk = 0; kk < 2 * kHalves; ++kk)
               if (kk < k_steps)
@@ -1267,7 +1330,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
         }
       } else {
         if (k > 0) {
-          convert_queries<kLive, 4>(a, items[b], qbuf + qb * F::kQ, row_qsum[b], row_unit[b], 0, 1);
+          convert_queries<kLive, 4, kBytes>(a, items[b], qbuf + qb * F::kQ, row_qsum[kNibbles ? b : 0], row_unit[b], 0, 1);
           proxy_fence();
         } else {
           bar_sync(6, F::kSoft + 32);  // the softmax warps have done it
@@ -1321,7 +1384,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
           constexpr int kWarps = F::kSoft / 32, kEach = kLive >= 8 * kWarps ? 4 : kLive >= 4 * kWarps ? 2 : 1;
           // (given up: there is no item to read; the barrier all the same)
           if (__all_sync(0xffffffffu, wait_or_dead(mfull, 0, dead)))
-            convert_queries<kLive, kEach>(a, items[0], qbuf, row_qsum[0], row_unit[0], st >> 5, kWarps);
+            convert_queries<kLive, kEach, kBytes>(a, items[0], qbuf, row_qsum[0], row_unit[0], st >> 5, kWarps);
           proxy_fence();
           bar_sync(6, F::kSoft + 32);
         }
@@ -1332,10 +1395,10 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
       const bool in = wait_or_dead((kPacked ? qfull : mfull) + b, (k / kNQ) & 1, dead);
       if (bar_any(5, F::kSoft, !in)) break;  // the same decision for every softmax thread
       const Item it = items[b];
-      float l[kCols], cs[kPacked ? kCols : 1];
+      float l[kCols], cs[kNibbles ? kCols : 1];
 #pragma unroll
       for (int n = 0; n < kCols; ++n) l[n] = 0.0f;
-      if (kPacked)
+      if (kNibbles)
 #pragma unroll
         for (int n = 0; n < kCols; ++n) cs[n] = 0.0f;
       bool unset = true;  // thread i of the warpgroup: row i has seen no key yet
@@ -1370,7 +1433,14 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
         float ka = a.scale_log2, kb = 0.0f, sv = 0.0f, wv = 0.0f;
         float big = 0.0f;  // log2 of the key's values, rounded up: 0 where it does not matter
         bool poison = false;
-        if (kPacked) {  // the tensor cores multiplied n / 512 and n - 8
+        bool no_scale = false;  // 8 bits: V's is not finite
+        if (kBytes) {
+          ka = a.scale_log2 * scales[at % kInfo][lt >> 3];
+          sv = scales[at % kInfo][16 + (lt >> 3)];
+          no_scale = !(fabsf(sv) <= 3.0e38f);
+          if (no_scale) sv = 0.0f;
+          big = static_cast<float>(max((__float_as_int(fabsf(sv)) >> 23) - 126, -80));
+        } else if (kPacked) {  // the tensor cores multiplied n / 512 and n - 8
           const uint32_t kp = k_pair[at % kPairs][lt], vp = v_pair[at % kPairs][lt];
           ka = a.scale_log2 * 512.0f * bf16_lo(kp);
           kb = a.scale_log2 * bf16_hi(kp);
@@ -1425,12 +1495,13 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
             vis &= on;
           }
           }
-          if (!kPacked) {
+          if (!kNibbles) {
             // A value that is not finite must not meet a weight of 0: the row
             // of such a key, where not every query sees it, becomes 0 in
             // shared memory, and the queries that do see it get a weight of NaN.
             // Each warpgroup looks at its part of the channels.
             constexpr int kScan = 8 * kHalves / F::kGroups;
+            const int scan0 = F::kGroups > 1 ? wg * kScan : 0;
             const int32_t s = at % kVs;
             wait_or_dead(vfull + s, (at / kVs) & 1, dead);
             const bool all = here && !draft && j <= first_pos && (always || j > last_pos - a.window);
@@ -1438,11 +1509,14 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
               uint4* v = reinterpret_cast<uint4*>(vring + s * F::kStage + lt * 128);
               uint32_t acc = 0;  // 0 times each channel, added up: NaN as soon as one is not finite
 #pragma unroll 4
-              for (int c = wg * kScan; c < (wg + 1) * kScan; ++c) {
+              for (int c = scan0; c < scan0 + kScan; ++c) {
                 const uint4 x = v[(c >> 3) * 1024 + ((c & 7) ^ (lt & 7))];
                 const uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(y[e]), "r"(0u));
+                for (int e = 0; e < 4; ++e) {
+                  if (kBytes) asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(y[e]), "r"(0u));
+                  else asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(y[e]), "r"(0u));
+                }
               }
               poison = (acc & 0x7fff7fffu) != 0;
               if (F::kGroups > 1 && poison) v_bad[sb][lt] = 1;
@@ -1467,13 +1541,15 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
         for (int i = 0; i < kCols; i += 4) {
           const float4 r4 = *reinterpret_cast<const float4*>(nref + h0 + i);
           uint64_t y[2] = {two(r4.x, r4.y), two(r4.z, r4.w)}, z[2] = {two(x[i], x[i + 1]), two(x[i + 2], x[i + 3])};
-          if (kPacked) {
-            const float4 q4 = *reinterpret_cast<const float4*>(&row_qsum[b][c0 + i]);
+          if constexpr (kPacked) {
             const float4 u4 = *reinterpret_cast<const float4*>(&row_unit[b][c0 + i]);
-            y[0] = fma_2(two(kb, kb), two(q4.x, q4.y), y[0]);
-            y[1] = fma_2(two(kb, kb), two(q4.z, q4.w), y[1]);
             z[0] = mul_2(z[0], two(u4.x, u4.y));
             z[1] = mul_2(z[1], two(u4.z, u4.w));
+          }
+          if constexpr (kNibbles) {
+            const float4 q4 = *reinterpret_cast<const float4*>(&row_qsum[b][c0 + i]);
+            y[0] = fma_2(two(kb, kb), two(q4.x, q4.y), y[0]);
+            y[1] = fma_2(two(kb, kb), two(q4.z, q4.w), y[1]);
           }
 #pragma unroll
           for (int e = 0; e < 2; ++e) split(fma_2(z[e], two(ka, ka), y[e]), x[i + 2 * e], x[i + 2 * e + 1]);
@@ -1532,7 +1608,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
             const float g = corr[h0 + i];
             change |= g != 1.0f;
             l[i] *= g;
-            if (kPacked) cs[i] *= g;
+            if (kNibbles) cs[i] *= g;
             x[i] -= shift[h0 + i];
           }
           if (change && t >= F::kStreams) {
@@ -1561,8 +1637,8 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
             float p[2] = {ex2(x[i]), ex2(x[i + 1])};
             const uint64_t p2 = two(p[0], p[1]);
             split(add_2(two(l[i], l[i + 1]), p2), l[i], l[i + 1]);
+            if constexpr (kNibbles) split(fma_2(p2, two(wv, wv), two(cs[i], cs[i + 1])), cs[i], cs[i + 1]);
             if constexpr (kPacked) {
-              split(fma_2(p2, two(wv, wv), two(cs[i], cs[i + 1])), cs[i], cs[i + 1]);
               split(mul_2(p2, two(sv, sv)), p[0], p[1]);
             }
             o4[e] = kPacked ? f16_pair(p[0], p[1]) : bf16_pair(p[0], p[1]);
@@ -1570,7 +1646,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
           const uint32_t off = lt * F::kPitch + ((c0 & 63) + i8 * 8) * 2;
           *reinterpret_cast<uint4*>(pb + (off ^ ((off >> 3) & kSwz))) = make_uint4(o4[0], o4[1], o4[2], o4[3]);
         }
-        if (!kPacked && F::kGroups > 1 && masked) {
+        if (!kNibbles && F::kGroups > 1 && masked) {
           // warpgroup 0 hears what the others found, and writes into their
           // weights once they are there
           poison = false;
@@ -1582,17 +1658,25 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
           }
           uses[sb] += 1;
         }
+        if (kBytes && no_scale) {  // this warpgroup's rows that see the key
+#pragma unroll 1
+          for (int c = c0; c < c0 + kCols; ++c) {
+            const uint32_t off = lt * F::kPitch + (c & 63) * 2;
+            uint8_t* p = pbuf + sb % F::kPBufs * F::kP + (c >> 6) * (kTile * 128);
+            if ((vis >> (c - c0)) & 1u) *reinterpret_cast<uint16_t*>(p + (off ^ ((off >> 3) & kSwz))) = 0x7fffu;
+          }
+        }
         if (poison) {
-          if (!kPacked) {
+          if (!kNibbles) {
             if (F::kGroups > 1) v_bad[sb][lt] = 0;
             uint4* v = reinterpret_cast<uint4*>(vring + at % kVs * F::kStage + lt * 128);
 #pragma unroll 1
             for (int c = 0; c < 8 * kHalves; ++c) v[(c >> 3) * 1024 + (c & 7)] = make_uint4(0u, 0u, 0u, 0u);
           }
-          const int from = kPacked ? c0 : 0, upto = kPacked ? c0 + kCols : kLive;
+          const int from = kNibbles ? c0 : 0, upto = kNibbles ? c0 + kCols : kLive;
 #pragma unroll 1
           for (int c = from; c < upto; ++c) {
-            const bool see = kPacked ? ((vis >> (c - c0)) & 1u) != 0 : sees(c);
+            const bool see = kNibbles ? ((vis >> (c - c0)) & 1u) != 0 : sees(c);
             const uint32_t off = lt * F::kPitch + (c & 63) * 2;
             uint8_t* p = pbuf + sb % F::kPBufs * F::kP + (c >> 6) * (kTile * 128);
             if (see) *reinterpret_cast<uint16_t*>(p + (off ^ ((off >> 3) & kSwz))) = 0x7fffu;
@@ -1615,7 +1699,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
         return lt < kCols ? (part[0][h0 + lt] + part[1][h0 + lt]) + (part[2][h0 + lt] + part[3][h0 + lt]) : 0.0f;
       };
       float sum = over_keys(l), csum = 0.0f;
-      if constexpr (kPacked) {
+      if constexpr (kNibbles) {
         bar_sync(bar, 128);
         csum = over_keys(cs);
       }
@@ -1674,7 +1758,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
             for (int i = 0; i < kStep; ++i)
               if (sums[kN + i0 + i] != 0.0f) o[i] = __fmaf_rn(o1[i], sums[kN + i0 + i], o[i]);
           }
-          if (kPacked)
+          if (kNibbles)
 #pragma unroll
             for (int i = 0; i < kStep; ++i) o[i] += csums[i0 + i];
           if (whole) {
@@ -1806,6 +1890,40 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(qempty + b);
     }
+  } else if constexpr (kBytes) {
+    if constexpr (F::kSplit) regs_fewer<F::kRegsUnpack>();
+    // --------------------------------------------------------- unpacking --
+    // A thread per key, warpgroups that take turns: V as f16, which holds every
+    // e4m3 number, since the weights that it meets need f16's bits.
+    const int key = (tid - 128 - F::kSoft) & 127;
+#pragma unroll 1
+    for (int32_t at = (tid - 128 - F::kSoft) >> 7; at < my_tiles; at += F::kVGroups) {
+      const int32_t rs = at % F::kRawStages, s = at % kVs;
+      if (!__all_sync(0xffffffffu, wait_or_dead(rfull + rs, (at / F::kRawStages) & 1, dead))) break;
+      const uint8_t* src = raw + rs * F::kRaw;
+      uint8_t* dst = vring + s * F::kStage + key * 128;
+      uint4 w4[4 * kHalves];  // 16 channels each
+#pragma unroll
+      for (int c = 0; c < 4 * kHalves; ++c) {
+        const uint32_t off = key * F::kRawRow + c * 16;
+        w4[c] = *reinterpret_cast<const uint4*>(src + (off ^ ((off >> 3) & (kHalves == 2 ? 0x70u : 0x30u))));
+      }
+      if (!__all_sync(0xffffffffu, wait_or_dead(vempty + s, ((at / kVs) & 1) ^ 1u, dead))) break;
+#pragma unroll
+      for (int c = 0; c < 4 * kHalves; ++c) {
+        const uint32_t w[4] = {w4[c].x, w4[c].y, w4[c].z, w4[c].w};
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int x = 2 * c + e;  // 8 channels
+          *reinterpret_cast<uint4*>(dst + (x >> 3) * 16384 + (((x & 7) ^ (key & 7)) << 4)) =
+              make_uint4(f16_of_e4m3(w[2 * e]), f16_of_e4m3(w[2 * e] >> 16), f16_of_e4m3(w[2 * e + 1]),
+                         f16_of_e4m3(w[2 * e + 1] >> 16));
+        }
+      }
+      proxy_fence();
+      mbar_arrive(vfull + s);
+      mbar_arrive(rempty + rs);
+    }
   } else if constexpr (kPacked) {
     if constexpr (F::kSplit) regs_fewer<F::kRegsUnpack>();
     // --------------------------------------------------------- unpacking --
@@ -1904,10 +2022,10 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves>::kThreads, 1)
   }
 }
 
-template <int kLive, bool kPacked, int kHalves>
+template <int kLive, bool kPacked, int kHalves, bool kBytes = false>
 ss_status launch(const AttnArgs& a, cudaStream_t s) {
-  using F = Cfg<kLive, kPacked, kHalves>;
-  const auto kernel = attn_kernel<kLive, kPacked, kHalves, F::kSplit ? F::kRegs : 0>;
+  using F = Cfg<kLive, kPacked, kHalves, kBytes>;
+  const auto kernel = attn_kernel<kLive, kPacked, kHalves, F::kSplit ? F::kRegs : 0, kBytes>;
   const void* fn = reinterpret_cast<const void*>(kernel);
   CUtensorMap mk, mv, mq{};
   const int unit = 1 << (a.c.page_shift < 7 ? a.c.page_shift : 7);

@@ -1,5 +1,6 @@
 // ss_cache.cu -- the paged key/value cache: writing and reading rows (bf16 or
-// 4 bits), and the pages' bookkeeping (reserve, fork, compact, trim).
+// 4 bits; 8 bits are read here, and written by ss_rope.cu), and the pages'
+// bookkeeping (reserve, fork, compact, trim).
 //
 // A row is one token's keys or values of one head.  All of it moves bytes and
 // computes next to nothing, so the floor of every call is its bytes.
@@ -9,15 +10,14 @@
 #include "ss.h"
 #include "ss_cache.h"
 #include "ss_nvtx.h"
+#include "ss_rows.cuh"
 
 namespace ssc {
 using namespace ss;
 
 constexpr int kThreads = 256;
-constexpr int kRowLanes = 16;                     // a row is at most 16 lanes of 8 channels
 constexpr int kGroups = kThreads / kRowLanes;     // rows in flight per CTA
 constexpr int kMostCtas = 4 * 152;                // per request
-constexpr uint32_t kNaN2 = 0x7fc07fc0u;           // a bf16 pair of NaNs
 
 struct AppendArgs {
   CacheView c;
@@ -45,86 +45,6 @@ __device__ __forceinline__ uint32_t divide(uint32_t n, const FastDiv& f) {
   return f.d == 1 ? n : __umulhi(n, f.mul) >> f.shift;
 }
 
-__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {  // bf16 pairs; a NaN stays
-  uint32_t r;
-  asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
-// Eight channels of a row, quantised: the row's low value and step come from
-// the 16 lanes of the row, as the pair (min x, min -x), so that one shuffle and
-// one instruction join two lanes.
-//
-// round((x - m) / s) without a division per channel: with y = x - m and
-// q = y * (1 / s), the remainder y - q s is exact in fp32 (q is off by a few
-// units at most and s has 8 bits), and q + (y - q s) / s is the quotient to
-// within 2^-20 of its last place before the one rounding.  A quotient that is
-// no half differs from every half by more than 1.003 times half a unit (y has
-// 24 bits, s has 8), so it is not rounded onto one: adding 1.5 * 2^23 then
-// leaves the integer, ties to even, in the low bits.
-__device__ __forceinline__ uint32_t quantise8(const uint4 x, bool live, uint32_t lanes, uint32_t& pair) {
-  uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  const uint32_t mn = min2(min2(w[0], w[1]), min2(w[2], w[3]));
-  const uint32_t mx = max2(max2(w[0], w[1]), max2(w[2], w[3])) ^ 0x80008000u;
-  uint32_t both = min2(__byte_perm(mn, mx, 0x5410), __byte_perm(mn, mx, 0x7632));
-  if (!live) both = 0x7f807f80u;
-#pragma unroll
-  for (int o = kRowLanes / 2; o > 0; o >>= 1) both = min2(both, __shfl_xor_sync(lanes, both, o, kRowLanes));
-  float lo = bf16_lo(both);
-  const float range = __fsub_rn(-bf16_hi(both), lo);
-  if (!(range < __int_as_float(0x7f800000))) {  // a NaN, an infinity or too wide
-    pair = kNaN2;
-    return 0;
-  }
-  // the smallest bf16 that is not below range / 15: then 15 steps reach the
-  // highest channel (the division as above)
-  constexpr float kTiny = 1.0e-28f, kUp = 18446744073709551616.0f;
-  float step = range * (1.0f / 15.0f);
-  step = __fmaf_rn(__fmaf_rn(-step, 15.0f, range), 1.0f / 15.0f, step);
-  if (range < kTiny) step = __fdiv_rn(range, 15.0f);
-  step = __uint_as_float((__float_as_uint(step) + 0xffffu) & 0xffff0000u);
-  pair = (__float_as_uint(step) >> 16) | __float_as_uint(lo);  // lo is one of the row's bf16
-  if (step == 0.0f) return 0;
-  if (range < kTiny) {  // keep 1 / step and the remainders in the normal range: all of it times 2^64
-#pragma unroll
-    for (int i = 0; i < 4; ++i) asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(w[i]) : "r"(0x5f805f80u));
-    lo *= kUp;
-    step *= kUp;
-  }
-  const float inv = __fdividef(1.0f, step);
-  const uint64_t low2 = two(-lo, -lo), inv2 = two(inv, inv), step2 = two(-step, -step);
-  constexpr uint32_t kRound = 0x4b400000u;  // 1.5 * 2^23
-  uint32_t out = 0u - 0x11111111u * kRound;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint64_t y = add_2(two(bf16_lo(w[i]), bf16_hi(w[i])), low2), q = mul_2(y, inv2);
-    const uint64_t t = add_2(fma_2(fma_2(q, step2, y), inv2, q), two(__uint_as_float(kRound), __uint_as_float(kRound)));
-    out += (static_cast<uint32_t>(t) << (4 * i)) + (static_cast<uint32_t>(t >> 32) << (16 + 4 * i));
-  }
-  return out;
-}
-
-__device__ __forceinline__ uint4 dequantise8(uint32_t w, uint32_t pair) {
-  const float s = bf16_lo(pair), m = bf16_hi(pair);
-  const uint64_t s2 = two(s, s), m2 = two(m, m), off = two(-8388608.0f, -8388608.0f);
-  uint32_t o[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {  // 2^23 + n, minus 2^23: no conversion
-    const uint64_t n = add_2(two(__uint_as_float(((w >> (4 * i)) & 15u) | 0x4b000000u),
-                                 __uint_as_float(((w >> (16 + 4 * i)) & 15u) | 0x4b000000u)), off);
-    const uint64_t v = fma_2(n, s2, m2);
-    float a, b;
-    split(v, a, b);
-    o[i] = bf16_pair(a, b);
-  }
-  return make_uint4(o[0], o[1], o[2], o[3]);
-}
-
 // A row is (token, K or V, head): 16 lanes of 16 bytes on the bf16 side.  16
 // lanes take kEach consecutive rows of one token (four where the heads are
 // even), so a token's page is looked up once for them and their loads are in
@@ -134,8 +54,10 @@ __device__ __forceinline__ uint4 dequantise8(uint32_t w, uint32_t pair) {
 // by instructions first (72 % of the issue slots: rounding or unpacking, and
 // the addresses), out also by the loads' latency; bf16, 32 x 1-8 tokens: 4.4
 // us, the latency of lengths, table and rows one after the other.
-template <bool kPacked, bool kRead, int kEach>
+template <int kFormat, bool kRead, int kEach>
 __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const AppendArgs a, const FastDiv by_token) {
+  constexpr bool kPacked = kFormat == SS_CACHE_INT4, kBytes = kFormat == SS_CACHE_FP8;
+  static_assert(!kBytes || kRead, "8 bits are written block by block");
   const int r = blockIdx.y;
   const int32_t begin = a.offsets ? a.offsets[r] : r;
   const int32_t end = a.offsets ? a.offsets[r + 1] : r + 1;
@@ -157,8 +79,8 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const AppendArgs a, c
     const int32_t in_page = static_cast<int32_t>(slot) & ((1 << a.c.page_shift) - 1);
     const int32_t page = page_of(a.t, a.c, row, slot);
     const int64_t in_flat = (begin + static_cast<int64_t>(token)) * a.token_stride + lane * 16;
-    const int64_t in_cell = max(page, 0) * a.c.page_stride + in_page * a.c.slot_stride + lane * (kPacked ? 4 : 16);
-    const int64_t in_scale = max(page, 0) * a.c.s_page_stride + in_page * 4;
+    const int64_t in_cell = max(page, 0) * a.c.page_stride + in_page * a.c.slot_stride + lane * (kPacked ? 4 : kBytes ? 8 : 16);
+    const int64_t in_scale = max(page, 0) * a.c.s_page_stride + (kBytes ? in_page >> a.c.block_shift : in_page) * 4;
     const auto flat = [&](int u) {
       const int32_t head = first + u;
       return head < a.c.heads ? a.k + in_flat + head * a.head_stride : a.v + in_flat + (head - a.c.heads) * a.head_stride;
@@ -185,6 +107,11 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const AppendArgs a, c
       } else if (kPacked) {
         word[u] = *reinterpret_cast<const uint32_t*>(cell(u));
         pair[u] = *scale(u);
+      } else if (kBytes) {
+        const uint2 w = *reinterpret_cast<const uint2*>(cell(u));
+        x[u].x = w.x;
+        x[u].y = w.y;
+        pair[u] = *scale(u);
       } else {
         x[u] = *reinterpret_cast<const uint4*>(cell(u));
       }
@@ -192,7 +119,12 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const AppendArgs a, c
     if (!kRead && page < 0) continue;  // the same for the row's 16 lanes
 #pragma unroll
     for (int u = 0; u < kEach; ++u) {
-      if (kRead) {  // (a step and a low value of 0 give the zeros of a hole)
+      if (kRead) {  // (a step and a low value, or a scale, of 0 give the zeros of a hole)
+        if (kBytes) {
+          float f[8];
+          decode8(make_uint2(x[u].x, x[u].y), __uint_as_float(pair[u]), f);
+          x[u] = make_uint4(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7]));
+        }
         if (live) *reinterpret_cast<uint4*>(flat(u)) = kPacked ? dequantise8(word[u], pair[u]) : x[u];
       } else if (kPacked) {
         const uint32_t w = quantise8(x[u], live, lanes, pair[u]);
@@ -214,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const AppendArgs a, c
   }
 }
 
-static ss_status rows_call(const ss_append_args* args, bool read, cudaStream_t s) {
+ss_status check_append(const ss_append_args* args) {
   if (!args || !check_cache(args->cache) || !check_table(args->pool)) return SS_ERR_INVALID_ARG;
   const ss_append_args& A = *args;
   if (A.layer < 0 || A.layer >= A.cache->num_layers || A.num_requests < 0 || A.num_requests > 65535 ||
@@ -225,6 +157,14 @@ static ss_status rows_call(const ss_append_args* args, bool read, cudaStream_t s
   if (!A.kv_len || !A.out_status || (A.total_tokens > 0 && (!A.k || !A.v)) || !aligned16(A.k) || !aligned16(A.v) || (A.token_stride & 7) != 0 ||
       (A.head_stride & 7) != 0)
     return SS_ERR_INVALID_ARG;
+  if (2ll * (A.token_offsets ? A.max_tokens : 1) * A.cache->num_kv_heads >= (1ll << 31)) return SS_ERR_UNSUPPORTED;
+  return SS_OK;
+}
+
+static ss_status rows_call(const ss_append_args* args, bool read, cudaStream_t s) {
+  const ss_status checked = check_append(args);
+  if (checked != SS_OK || args->num_requests == 0) return checked;
+  const ss_append_args& A = *args;
   AppendArgs a{};
   a.c = view_of(A.cache, A.layer);
   a.t = table_of(A.pool, A.table_rows);
@@ -238,19 +178,19 @@ static ss_status rows_call(const ss_append_args* args, bool read, cudaStream_t s
   a.head_stride = A.head_stride * 2;
   a.status = A.out_status;
   const int64_t rows = 2ll * a.max_tokens * a.c.heads;
-  if (rows >= (1ll << 31)) return SS_ERR_UNSUPPORTED;
   // No more CTAs per request than fill the GPU; they loop over the rest of its
   // rows (4 bits, 4 x 2-6k tokens: 32 us, 35 with a CTA for every 64 rows).
   const bool even = (a.c.heads & 1) == 0;
   const int64_t each = kGroups * (even ? 4 : 2), want = (rows + each - 1) / each;
   const dim3 grid(static_cast<unsigned>(want < 1 ? 1 : want > kMostCtas ? kMostCtas : want), A.num_requests);
   const FastDiv by_token = fast_div(2u * a.c.heads);
-  const bool packed = a.c.format == SS_CACHE_INT4;
-  const auto launch = [&](auto kernel) { kernel<<<grid, kThreads, 0, s>>>(a, by_token); };
-  if (even) launch(packed ? (read ? rows_kernel<true, true, 4> : rows_kernel<true, false, 4>)
-                          : (read ? rows_kernel<false, true, 4> : rows_kernel<false, false, 4>));
-  else launch(packed ? (read ? rows_kernel<true, true, 2> : rows_kernel<true, false, 2>)
-                     : (read ? rows_kernel<false, true, 2> : rows_kernel<false, false, 2>));
+  const auto launch = [&](auto four, auto two) { (even ? four : two)<<<grid, kThreads, 0, s>>>(a, by_token); };
+  constexpr int kBf16 = SS_CACHE_BF16, kInt4 = SS_CACHE_INT4, kFp8 = SS_CACHE_FP8;
+  if (a.c.format == SS_CACHE_FP8) launch(rows_kernel<kFp8, true, 4>, rows_kernel<kFp8, true, 2>);
+  else if (a.c.format == SS_CACHE_INT4 && read) launch(rows_kernel<kInt4, true, 4>, rows_kernel<kInt4, true, 2>);
+  else if (a.c.format == SS_CACHE_INT4) launch(rows_kernel<kInt4, false, 4>, rows_kernel<kInt4, false, 2>);
+  else if (read) launch(rows_kernel<kBf16, true, 4>, rows_kernel<kBf16, true, 2>);
+  else launch(rows_kernel<kBf16, false, 4>, rows_kernel<kBf16, false, 2>);
   return finish(cudaSuccess);
 }
 
@@ -449,7 +389,7 @@ __global__ void __launch_bounds__(kThreads) fork_copy_kernel(const PoolView p, c
   if (slots == 0) return;
   const int32_t src = p.table[parent[i] * p.stride + e], dst = p.table[child[i] * p.stride + e];
   if (src < 0 || src >= c.num_pages || dst < 0 || dst >= c.num_pages) return;
-  const int32_t chunks = (c.format == SS_CACHE_INT4 ? c.dim / 2 : c.dim * 2) / 16;
+  const int32_t chunks = row_bytes(c.format, c.dim) / 16;
   const uint8_t* from = (is_v ? c.v : c.k) + layer * c.layer_stride + src * c.page_stride;
   uint8_t* to = (is_v ? c.v : c.k) + layer * c.layer_stride + dst * c.page_stride;
   const int32_t per_head = slots * chunks, total = per_head * c.heads;
@@ -468,11 +408,12 @@ __global__ void __launch_bounds__(kThreads) fork_copy_kernel(const PoolView p, c
     for (int u = 0; u < 4; ++u)
       if (x0 + u * kThreads < total) *reinterpret_cast<uint4*>(to + at[u]) = v[u];
   }
-  if (c.format == SS_CACHE_INT4) {
+  if (c.format != SS_CACHE_BF16) {
+    const int32_t scales = c.format == SS_CACHE_INT4 ? slots : ((slots - 1) >> c.block_shift) + 1;
     const uint8_t* sf = (is_v ? c.vs : c.ks) + layer * c.s_layer_stride + src * c.s_page_stride;
     uint8_t* st = (is_v ? c.vs : c.ks) + layer * c.s_layer_stride + dst * c.s_page_stride;
-    for (int32_t x = threadIdx.x; x < slots * c.heads; x += kThreads) {
-      const int64_t at = (x / slots) * c.s_head_stride + (x % slots) * 4;
+    for (int32_t x = threadIdx.x; x < scales * c.heads; x += kThreads) {
+      const int64_t at = (x / scales) * c.s_head_stride + (x % scales) * 4;
       *reinterpret_cast<uint32_t*>(st + at) = *reinterpret_cast<const uint32_t*>(sf + at);
     }
   }
@@ -490,6 +431,28 @@ struct CompactArgs {
   int32_t* status;
 };
 
+// What compact does for a request, which every CTA of it finds by itself.
+__device__ __forceinline__ int32_t compact_status(const CompactArgs& a, int i, const int32_t* row, const int32_t* path,
+                                                  int32_t base, int32_t count) {
+  const int32_t verified = a.verified ? a.verified[i] : SS_ROW_OK;
+  int32_t st = SS_ROW_OK;
+  if (verified != SS_ROW_OK) st = verified;
+  else if (!row || base < 0 || count < 0 || count > a.path_stride || base > 0x7ffffffe - count) st = SS_ROW_BAD_PARAM;
+  int bad = 0;
+  if (st == SS_ROW_OK)
+    for (int32_t j = threadIdx.x; j < count; j += kThreads) {
+      const int32_t node = path[j];
+      bad |= node <= (j ? path[j - 1] : 0) || page_of(a.t, a.c, row, static_cast<int64_t>(base) + max(node, 0)) < 0 ||
+             page_of(a.t, a.c, row, static_cast<int64_t>(base) + 1 + j) < 0;
+    }
+  if (__syncthreads_or(bad)) st = SS_ROW_BAD_INDEX;
+  if (blockIdx.y == 0 && threadIdx.x == 0) {
+    a.new_len[i] = (st == SS_ROW_OK) ? base + 1 + count : base;
+    a.status[i] = st;
+  }
+  return st;
+}
+
 constexpr int kPath = 64;  // accepted nodes whose places are held in shared memory at once
 
 // CTA (i, layer): thread t moves the same 16 bytes of every accepted row, in
@@ -501,26 +464,11 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactArgs a) 
   __shared__ int64_t s_from[kPath], s_to[kPath], s_sfrom[kPath], s_sto[kPath];
   const int i = blockIdx.x, layer = blockIdx.y;
   const CacheView& c = a.c;
-  const int32_t base = a.kv_len[i], count = a.accepted[i], verified = a.verified ? a.verified[i] : SS_ROW_OK;
+  const int32_t base = a.kv_len[i], count = a.accepted[i];
   const int32_t* row = table_row(a.t, i);
   const int32_t* path = a.path + static_cast<int64_t>(i) * a.path_stride;
-  int32_t st = SS_ROW_OK;
-  if (verified != SS_ROW_OK) st = verified;
-  else if (!row || base < 0 || count < 0 || count > a.path_stride || base > 0x7ffffffe - count) st = SS_ROW_BAD_PARAM;
-  int bad = 0;
-  if (st == SS_ROW_OK)
-    for (int32_t j = threadIdx.x; j < count; j += kThreads) {
-      const int32_t node = path[j];
-      bad |= node <= (j ? path[j - 1] : 0) || page_of(a.t, c, row, static_cast<int64_t>(base) + max(node, 0)) < 0 ||
-             page_of(a.t, c, row, static_cast<int64_t>(base) + 1 + j) < 0;
-    }
-  if (__syncthreads_or(bad)) st = SS_ROW_BAD_INDEX;
-  if (layer == 0 && threadIdx.x == 0) {
-    a.new_len[i] = (st == SS_ROW_OK) ? base + 1 + count : base;
-    a.status[i] = st;
-  }
-  if (st != SS_ROW_OK) return;
-  const int32_t chunks = (c.format == SS_CACHE_INT4 ? c.dim / 2 : c.dim * 2) / 16;
+  if (compact_status(a, i, row, path, base, count) != SS_ROW_OK) return;
+  const int32_t chunks = row_bytes(c.format, c.dim) / 16;
   const int32_t per = chunks * c.heads, in_page = (1 << c.page_shift) - 1;
   for (int32_t j0 = 0; j0 < count; j0 += kPath) {
     const int32_t m = min(kPath, count - j0);
@@ -556,6 +504,73 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactArgs a) 
           if (s_from[j] >= 0)
             *reinterpret_cast<uint32_t*>(at + s_sto[j]) = *reinterpret_cast<const uint32_t*>(at + s_sfrom[j]);
       }
+  }
+}
+
+// 8 bits: a block into which rows move is encoded anew.  CTA (i, layer) takes
+// the blocks from the first to the last; 16 lanes have one slot of a block (as
+// in ss_rope.cu), kEach heads of K or V at a time.  Sources lie at or behind
+// their places, so those of later blocks lie behind the block being written: a
+// block's reads end at the barrier for its scales, before its writes and the
+// next block's reads.
+__global__ void __launch_bounds__(kThreads) compact_blocks_kernel(const CompactArgs a) {
+  constexpr int kEach = 4;
+  __shared__ uint32_t s_top[3][2 * kEach];
+  const int i = blockIdx.x, layer = blockIdx.y;
+  const CacheView& c = a.c;
+  const int32_t base = a.kv_len[i], count = a.accepted[i];
+  const int32_t* row = table_row(a.t, i);
+  const int32_t* path = a.path + static_cast<int64_t>(i) * a.path_stride;
+  if (compact_status(a, i, row, path, base, count) != SS_ROW_OK || count == 0) return;
+  const int32_t size = 1 << c.block_shift, in_page = (1 << c.page_shift) - 1;
+  const int lane = threadIdx.x % kRowLanes, group = threadIdx.x / kRowLanes;
+  const int slot = group & (size - 1), side = group >> c.block_shift, sides = kGroups >> c.block_shift;
+  const bool live = lane * 8 < c.dim;
+  const int32_t units = 2 * c.heads;
+  if (threadIdx.x < 3 * 2 * kEach) (&s_top[0][0])[threadIdx.x] = 0;
+  __syncthreads();
+  int turn = 0;
+  const int64_t end = static_cast<int64_t>(base) + 1 + count;  // slots
+  for (int64_t b = (static_cast<int64_t>(base) + 1) >> c.block_shift; b <= (end - 1) >> c.block_shift; ++b) {
+    const int64_t at = (b << c.block_shift) + slot, j = at - base - 1;
+    const int64_t from = j < 0 ? at : j < count ? static_cast<int64_t>(base) + path[j] : -1;  // -1: past the rows
+    if (!__syncthreads_or(from >= 0 && from != at)) continue;
+    const int32_t to_page = page_of(a.t, c, row, b << c.block_shift);
+    const int32_t page = from < 0 ? -1 : page_of(a.t, c, row, from);
+    const int64_t to = layer * c.layer_stride + to_page * c.page_stride + (at & in_page) * c.slot_stride + lane * 8;
+    const int64_t src = layer * c.layer_stride + max(page, 0) * c.page_stride + (max(from, int64_t{0}) & in_page) * c.slot_stride + lane * 8;
+    const int64_t to_scale = layer * c.s_layer_stride + to_page * c.s_page_stride + ((at & in_page) >> c.block_shift) * 4;
+    const int64_t src_scale = layer * c.s_layer_stride + max(page, 0) * c.s_page_stride +
+                              ((max(from, int64_t{0}) & in_page) >> c.block_shift) * 4;
+    for (int32_t u0 = side * kEach; u0 - side * kEach < units; u0 += sides * kEach, turn = turn == 2 ? 0 : turn + 1) {
+      float x[kEach][8];
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) {
+        const int32_t u = u0 + e, head = u < c.heads ? u : u - c.heads;
+        const bool there = u < units && page >= 0;
+        uint2 w = make_uint2(0u, 0u);
+        float s = 0.0f;
+        if (there && live) {
+          w = *reinterpret_cast<const uint2*>((u < c.heads ? c.k : c.v) + src + head * c.head_stride);
+          s = *reinterpret_cast<const float*>((u < c.heads ? c.ks : c.vs) + src_scale + head * c.s_head_stride);
+        }
+        decode8(w, s, x[e]);
+        const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(finite_top(x[e])));
+        if ((threadIdx.x & 31) == 0 && top != 0) atomicMax(&s_top[turn][side * kEach + e], top);
+      }
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) {
+        const int32_t u = u0 + e, head = u < c.heads ? u : u - c.heads;
+        const Scale8 f = scale8(__uint_as_float(s_top[turn][side * kEach + e]));
+        if (u >= units || page < 0) continue;
+        if (live) *reinterpret_cast<uint2*>((u < c.heads ? c.k : c.v) + to + head * c.head_stride) = encode8(x[e], f.inv);
+        if (j == count - 1 || slot == size - 1)
+          if (lane == 0) *reinterpret_cast<float*>((u < c.heads ? c.ks : c.vs) + to_scale + head * c.s_head_stride) = f.s;
+      }
+      // (the maxima of the batch before have been read before the barrier)
+      if (threadIdx.x < 2 * kEach) s_top[turn == 0 ? 2 : turn - 1][threadIdx.x] = 0;
+    }
   }
 }
 
@@ -760,6 +775,8 @@ extern "C" {
 
 ss_status ss_cache_append(const ss_append_args* args, ss_stream_t stream) {
   SS_NVTX_RANGE("ss_cache_append");
+  if (args && args->cache && args->cache->format == SS_CACHE_FP8)
+    return ssc::append_blocks(args, reinterpret_cast<cudaStream_t>(stream));
   return ssc::rows_call(args, false, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -819,7 +836,8 @@ ss_status ss_pages_compact(const ss_page_pool* pool, const ss_kv_cache* cache, i
   a.verified = verify_status;
   a.new_len = new_len;
   a.status = out_status;
-  compact_kernel<<<dim3(n, cache->num_layers), kThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
+  const auto kernel = cache->format == SS_CACHE_FP8 ? compact_blocks_kernel : compact_kernel;
+  kernel<<<dim3(n, cache->num_layers), kThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
   return finish(cudaSuccess);
 }
 

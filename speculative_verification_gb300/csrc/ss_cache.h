@@ -13,6 +13,7 @@ void set_last_cuda_error(int32_t e);  // ss_kernel.cu: the value ss_last_cuda_er
 // ss_kv_cache with the layer's base pointers and the page size as a shift.
 struct CacheView {
   int32_t format, num_pages, heads, dim, page_shift;
+  int32_t block_shift;  // 8 bits: slots that share a scale
   uint8_t* k;
   uint8_t* v;
   int64_t layer_stride, page_stride, head_stride, slot_stride;
@@ -31,15 +32,21 @@ struct TableView {
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Bytes of one row of one head (without its scales).
+__host__ __device__ inline int32_t row_bytes(int32_t format, int32_t dim) {
+  return format == SS_CACHE_INT4 ? dim / 2 : format == SS_CACHE_FP8 ? dim : 2 * dim;
+}
+
 inline bool check_cache(const ss_kv_cache* c) {
   if (!c) return false;
-  if (c->format != SS_CACHE_BF16 && c->format != SS_CACHE_INT4) return false;
+  if (c->format != SS_CACHE_BF16 && c->format != SS_CACHE_INT4 && c->format != SS_CACHE_FP8) return false;
   if (c->num_layers < 1 || c->num_pages < 1 || c->num_kv_heads < 1 || c->num_kv_heads > 65535) return false;
   if (c->page_size < 8 || c->page_size > 1024 || (c->page_size & (c->page_size - 1)) != 0) return false;
-  const bool packed = c->format == SS_CACHE_INT4;
-  if (c->head_dim < (packed ? 32 : 8) || c->head_dim > 128 || c->head_dim % (packed ? 32 : 8) != 0) return false;
+  const bool packed = c->format == SS_CACHE_INT4, bytes = c->format == SS_CACHE_FP8;
+  const int32_t unit = packed ? 32 : bytes ? 16 : 8;
+  if (c->head_dim < unit || c->head_dim > 128 || c->head_dim % unit != 0) return false;
   if (!c->k || !c->v || !aligned16(c->k) || !aligned16(c->v)) return false;
-  const int64_t row = packed ? c->head_dim / 2 : 2 * c->head_dim;
+  const int64_t row = row_bytes(c->format, c->head_dim);
   // a tensor copy's strides are multiples of 16 bytes below 2^40
   for (int64_t s : {c->layer_stride, c->page_stride, c->head_stride, c->slot_stride})
     if (s < row || (s & 15) != 0 || s >= (1ll << 40)) return false;
@@ -47,6 +54,14 @@ inline bool check_cache(const ss_kv_cache* c) {
     if (!c->k_scale || !c->v_scale || !aligned16(c->k_scale) || !aligned16(c->v_scale)) return false;
     for (int64_t s : {c->scale_layer_stride, c->scale_page_stride, c->scale_head_stride})
       if (s < 4ll * c->page_size || (s & 15) != 0 || s >= (1ll << 40)) return false;
+  }
+  if (bytes) {
+    if (!c->k_scale || !c->v_scale || (reinterpret_cast<uintptr_t>(c->k_scale) & 3u) != 0 ||
+        (reinterpret_cast<uintptr_t>(c->v_scale) & 3u) != 0)
+      return false;
+    const int64_t page = 4ll * (c->page_size < SS_FP8_BLOCK ? 1 : c->page_size / SS_FP8_BLOCK);
+    for (int64_t s : {c->scale_layer_stride, c->scale_page_stride, c->scale_head_stride})
+      if (s < page || (s & 3) != 0 || s >= (1ll << 40)) return false;
   }
   return true;
 }
@@ -68,7 +83,8 @@ inline CacheView view_of(const ss_kv_cache* c, int32_t layer) {
   v.page_stride = c->page_stride;
   v.head_stride = c->head_stride;
   v.slot_stride = c->slot_stride;
-  if (c->format == SS_CACHE_INT4) {
+  v.block_shift = v.page_shift < 4 ? v.page_shift : 4;  // SS_FP8_BLOCK, or a page of 8
+  if (c->format != SS_CACHE_BF16) {
     v.ks = static_cast<uint8_t*>(c->k_scale) + layer * c->scale_layer_stride;
     v.vs = static_cast<uint8_t*>(c->v_scale) + layer * c->scale_layer_stride;
     v.s_layer_stride = c->scale_layer_stride;
@@ -87,6 +103,15 @@ inline TableView table_of(const ss_page_pool* p, const int32_t* rows) {
   t.max_pages = p->max_pages;
   return t;
 }
+
+}  // namespace ss
+
+namespace ssc {
+ss_status check_append(const ss_append_args* args);  // ss_cache.cu: the append and read calls' arguments
+ss_status append_blocks(const ss_append_args* args, cudaStream_t s);  // ss_rope.cu: ss_cache_append into 8 bits
+}  // namespace ssc
+
+namespace ss {
 
 inline ss_status finish(cudaError_t e) {
   if (e == cudaSuccess) e = cudaGetLastError();

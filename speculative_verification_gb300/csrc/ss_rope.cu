@@ -1,0 +1,510 @@
+// ss_rope.cu -- rotary positions (ss_rope), the same with the cache's append in
+// one launch (ss_rope_append), and the append into 8 bits, whose blocks of slots
+// are written as a whole.
+//
+// The mathematics.  A pair (x, y) of a head's channels at position p becomes
+// (m (x cos a - y sin a), m (y cos a + x sin a)), a = 2 pi p t.  t is a 64-bit
+// fraction of a turn, so p t modulo one turn is one integer product, exact at
+// any position; its upper 32 bits, as a signed fraction of half a turn, are what
+// sincospif takes.  In 8 bits the rows of a block (16 slots of one head) share a
+// power of two by their largest value (ss_rows.cuh).
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <initializer_list>
+
+#include "ss.h"
+#include "ss_cache.h"
+#include "ss_nvtx.h"
+#include "ss_rows.cuh"
+
+namespace ssc {
+
+constexpr int kThreads = 256;
+constexpr int kGroups = kThreads / kRowLanes;  // rows in flight per CTA, and tokens of a chunk
+constexpr int kNone = -1;                      // no cache: keys go to an array as the queries do
+constexpr int kAppend8 = SS_CACHE_FP8;
+constexpr int kPairs = 64;
+
+struct StepArgs {
+  CacheView c;
+  TableView t;
+  int32_t max_tokens, total_tokens;
+  const int32_t* offsets;
+  const int32_t* kv_len;
+  const int32_t* parents;
+  const int32_t* positions;
+  const uint64_t* turns;
+  int32_t half, layout;  // pairs; ss_rope_layout
+  float magnitude;
+  int32_t dim, q_heads, kv_heads, chunk_shift;
+  const uint8_t* q;
+  uint8_t* q_out;
+  const uint8_t* k;
+  uint8_t* k_out;
+  const uint8_t* v;
+  int64_t q_token, q_head, q_out_token, q_out_head;  // bytes
+  int64_t k_token, k_head, k_out_token, k_out_head;  // (v's are k's)
+  int32_t* status;
+};
+
+// What one lane needs to turn its 8 channels: out = x c + partner s, partner
+// the other channel of the pair, s with its sign.
+struct Turn {
+  float c[8], s[8];
+  uint32_t on;  // channels that turn
+};
+
+// kAny: halves whose pairs do not lie 8 channels next to 8 channels.
+template <bool kAny>
+__device__ __forceinline__ Turn turn_of(const StepArgs& a, const float* cos_of, const float* sin_of, int lane) {
+  Turn t;
+  t.on = 0;
+  const int c0 = lane * 8, rot = 2 * a.half;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int ch = c0 + i;
+    const bool second = a.layout == SS_ROPE_HALVES ? ch >= a.half : i & 1;
+    int pair = a.layout == SS_ROPE_HALVES ? (second ? ch - a.half : ch) : ch >> 1;
+    if (ch >= rot) pair = 0;
+    t.c[i] = cos_of[pair];
+    t.s[i] = second ? sin_of[pair] : -sin_of[pair];
+    t.on |= static_cast<uint32_t>(ch < rot) << i;
+  }
+  return t;
+}
+
+// One row's 8 channels, turned.  All 16 lanes of the row call it.  `row` is the
+// row in global memory, read again where lanes' channels do not pair up (kAny).
+template <bool kAny>
+__device__ __forceinline__ uint4 turned(const StepArgs& a, const Turn& t, const uint4& x, const uint8_t* row, int lane,
+                                        uint32_t lanes) {
+  float v[8], p[8];
+  floats_of(x, v);
+  if (a.layout == SS_ROPE_INTERLEAVED) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) p[i] = v[i ^ 1];
+  } else if (!kAny) {
+    const int other = lane * 8 < a.half ? lane + a.half / 8 : lane - a.half / 8;  // past rot_dim: not used
+    const uint4 y = make_uint4(__shfl_sync(lanes, x.x, other, kRowLanes), __shfl_sync(lanes, x.y, other, kRowLanes),
+                               __shfl_sync(lanes, x.z, other, kRowLanes), __shfl_sync(lanes, x.w, other, kRowLanes));
+    floats_of(y, p);
+  } else {
+    const uint16_t* at = reinterpret_cast<const uint16_t*>(row);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int ch = lane * 8 + i;
+      p[i] = 0.0f;
+      if (ch < 2 * a.half) p[i] = __uint_as_float(static_cast<uint32_t>(at[ch < a.half ? ch + a.half : ch - a.half]) << 16);
+    }
+    __syncwarp(lanes);  // read before any lane writes the row's place (which may be the row)
+  }
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float lo = __fmaf_rn(v[2 * i], t.c[2 * i], p[2 * i] * t.s[2 * i]);
+    const float hi = __fmaf_rn(v[2 * i + 1], t.c[2 * i + 1], p[2 * i + 1] * t.s[2 * i + 1]);
+    const uint32_t both = bf16_pair(lo, hi);
+    const uint32_t mask = ((t.on >> (2 * i)) & 1u ? 0xffffu : 0u) | ((t.on >> (2 * i + 1)) & 1u ? 0xffff0000u : 0u);
+    o[i] = (both & mask) | (w[i] & ~mask);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// CTA (x, r, z): chunk x of request r's tokens (those of 16 slots, of 8 where a
+// page has 8), and of their rows each gridDim.z-th.  The sines and cosines of
+// the chunk's tokens are computed once, in shared memory; then 16 lanes take a
+// token's rows of all heads, whose turns stay in registers.  Rows of 8 bits: 16
+// lanes per slot of the block, those that hold rows from before among them.
+template <int kFormat, bool kRope, bool kAny>
+__global__ void __launch_bounds__(kThreads) step_kernel(const StepArgs a) {
+  constexpr bool kBlocks = kFormat == SS_CACHE_FP8;
+  constexpr int kEach = 4;
+  __shared__ __align__(16) float s_cos[kRope ? kGroups : 1][kPairs], s_sin[kRope ? kGroups : 1][kPairs];
+  __shared__ int32_t s_up[kRope ? SS_TREE_MAX_NODES : 1], s_depth[kRope ? SS_TREE_MAX_NODES : 1];
+  __shared__ uint32_t s_top[3][2 * kEach];
+  const int tid = threadIdx.x, r = blockIdx.y;
+  const int32_t begin = a.offsets ? a.offsets[r] : r;
+  const int32_t stop = a.offsets ? a.offsets[r + 1] : r + 1;
+  const int32_t base = a.kv_len ? a.kv_len[r] : 0;
+  const int32_t* row = kFormat == kNone ? nullptr : table_row(a.t, r);
+  const int32_t n = stop - begin;
+  const bool tree = kRope && a.parents;
+  const bool ok = (kFormat == kNone || row) && base >= 0 && begin >= 0 && begin <= stop && stop <= a.total_tokens &&
+                  n <= a.max_tokens && !(tree && n > SS_TREE_MAX_NODES);
+  if (!ok) {
+    if (blockIdx.x == 0 && blockIdx.z == 0 && tid == 0) a.status[r] = SS_ROW_BAD_PARAM;
+    return;
+  }
+  if (blockIdx.x == 0 && blockIdx.z == 0) {  // the status: parents, and does every slot have a page?
+    int missing = 0, bad = 0;
+    if (kFormat != kNone && n > 0) {
+      const int64_t last = (static_cast<int64_t>(base) + n - 1) >> a.c.page_shift;
+      for (int64_t e = (base >> a.c.page_shift) + tid; e <= last; e += kThreads)
+        missing |= e >= a.t.max_pages || row[e] < 0 || row[e] >= a.c.num_pages;
+    }
+    if (tree && tid > 0 && tid < n) bad = a.parents[begin + tid] < 0 || a.parents[begin + tid] >= tid;
+    if (kFormat != kNone) missing = __syncthreads_or(missing);
+    if (tree) bad = __syncthreads_or(bad);
+    if (tid == 0) a.status[r] = bad ? SS_ROW_BAD_PARAM : missing ? SS_ROW_BAD_INDEX : SS_ROW_OK;
+  }
+  // the chunk's tokens t0 .. t1 - 1; its first slot is token `from`
+  const int32_t size = 1 << a.chunk_shift;
+  const int64_t from = kFormat == kNone ? static_cast<int64_t>(blockIdx.x) << a.chunk_shift
+                                        : (((base >> a.chunk_shift) + static_cast<int64_t>(blockIdx.x)) << a.chunk_shift) - base;
+  const int32_t t0 = static_cast<int32_t>(from < 0 ? 0 : from < n ? from : n);
+  const int32_t t1 = static_cast<int32_t>(from + size < n ? from + size : n);
+  const int32_t tokens = t1 - t0;
+  if (tokens <= 0) return;
+  const int lane = tid % kRowLanes, group = tid / kRowLanes;
+  const uint32_t lanes = 0xffffu << (tid & 16);
+  const bool live = lane * 8 < a.dim;
+  if (kBlocks && tid < 3 * 2 * kEach) (&s_top[0][0])[tid] = 0;
+  if constexpr (kRope) {
+    if (tree) {  // depths by jumps of 1, 2, 4 .. parents
+      if (tid < SS_TREE_MAX_NODES) {
+        const int32_t p = tid > 0 && tid < n ? a.parents[begin + tid] : 0;
+        s_up[tid] = p < 0 || p >= tid ? 0 : p;
+        s_depth[tid] = tid > 0;
+      }
+#pragma unroll 1
+      for (int i = 0; i < 6; ++i) {
+        __syncthreads();
+        int32_t up = 0, depth = 0;
+        if (tid < SS_TREE_MAX_NODES) {
+          up = s_up[s_up[tid]];
+          depth = s_depth[tid] + s_depth[s_up[tid]];
+        }
+        __syncthreads();
+        if (tid < SS_TREE_MAX_NODES) {
+          s_up[tid] = up;
+          s_depth[tid] = depth;
+        }
+      }
+      __syncthreads();
+    }
+    for (int i = tid; i < tokens * a.half; i += kThreads) {
+      const int token = i / a.half, pair = i - token * a.half;
+      const int64_t at = a.positions ? a.positions[begin + t0 + token]
+                                     : static_cast<int64_t>(base) + (tree ? s_depth[t0 + token] : t0 + token);
+      const uint64_t turn = static_cast<uint64_t>(at) * a.turns[pair];
+      float s, c;
+      sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 4.656612873077393e-10f, &s, &c);
+      s_cos[token][pair] = a.magnitude * c;
+      s_sin[token][pair] = a.magnitude * s;
+    }
+  }
+  if (kRope || kBlocks) __syncthreads();
+
+  // ---- rows by themselves: queries, and keys and values but in 8 bits
+  if constexpr (kRope) {
+    const int per = kGroups / tokens;  // groups of 16 lanes per token
+    const int token = group % tokens, first = group / tokens;
+    const int32_t heads = a.q_heads + (kBlocks ? 0 : kFormat == kNone ? a.kv_heads : 2 * a.kv_heads);
+    if (first < per) {
+      const Turn t = turn_of<kAny>(a, s_cos[token], s_sin[token], lane);
+      const int64_t at = static_cast<int64_t>(begin) + t0 + token;
+      int32_t page = -1, in_page = 0;
+      if (kFormat != kNone && !kBlocks) {
+        const int64_t slot = static_cast<int64_t>(base) + t0 + token;
+        page = page_of(a.t, a.c, row, slot);
+        in_page = static_cast<int32_t>(slot) & ((1 << a.c.page_shift) - 1);
+      }
+      const auto source = [&](int32_t h) {
+        const int32_t k = h - a.q_heads, v = k - a.kv_heads;
+        return k < 0 ? a.q + at * a.q_token + h * a.q_head
+                     : (v < 0 ? a.k + k * a.k_head : a.v + v * a.k_head) + at * a.k_token;
+      };
+      const int32_t step = per * gridDim.z;
+      for (int32_t h0 = first + per * blockIdx.z; h0 < heads; h0 += step * kEach) {
+        uint4 x[kEach];
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) {
+          const int32_t h = h0 + e * step;
+          x[e] = make_uint4(0u, 0u, 0u, 0u);
+          if (h < heads && live) x[e] = *reinterpret_cast<const uint4*>(source(h) + lane * 16);
+        }
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) {
+          const int32_t h = h0 + e * step, k = h - a.q_heads, v = k - a.kv_heads;
+          if (h >= heads) break;
+          const uint4 y = v < 0 ? turned<kAny>(a, t, x[e], source(h), lane, lanes) : x[e];
+          if (k < 0 || kFormat == kNone) {
+            uint8_t* to = k < 0 ? a.q_out + at * a.q_out_token + h * a.q_out_head
+                                : a.k_out + at * a.k_out_token + k * a.k_out_head;
+            if (live) *reinterpret_cast<uint4*>(to + lane * 16) = y;
+            continue;
+          }
+          if constexpr (kFormat != kNone && !kBlocks) {
+            const int32_t head = v < 0 ? k : v;
+            const int64_t cell = max(page, 0) * a.c.page_stride + head * a.c.head_stride + in_page * a.c.slot_stride;
+            uint8_t* to = (v < 0 ? a.c.k : a.c.v) + cell;
+            if (kFormat == SS_CACHE_INT4) {
+              uint32_t pair;
+              const uint32_t w = quantise8(y, live, lanes, pair);
+              if (page < 0) continue;
+              if (live) *reinterpret_cast<uint32_t*>(to + lane * 4) = w;
+              if (lane == 0)
+                *reinterpret_cast<uint32_t*>((v < 0 ? a.c.ks : a.c.vs) + max(page, 0) * a.c.s_page_stride +
+                                             head * a.c.s_head_stride + in_page * 4) = pair;
+            } else if (live && page >= 0) {
+              *reinterpret_cast<uint4*>(to + lane * 16) = y;
+            }
+          }
+        }
+      }
+    }
+  }
+
+  // ---- a block of 8 bits: 16 lanes per slot, kEach heads of K or V at a time
+  if constexpr (kBlocks) {
+    const int64_t first_slot = base + from;
+    const int32_t page = page_of(a.t, a.c, row, first_slot);  // a block lies in one page
+    if (page < 0) return;
+    const int slot = group & (size - 1), side = group >> a.chunk_shift, sides = kGroups >> a.chunk_shift;
+    const int64_t i = from + slot;  // the slot's token
+    const bool fresh = i >= t0 && i < t1, kept = i < 0;
+    const int64_t at = static_cast<int64_t>(begin) + (fresh ? i : 0);
+    const int32_t in_page = static_cast<int32_t>(first_slot) & ((1 << a.c.page_shift) - 1);
+    const int64_t cell = page * a.c.page_stride + (in_page + slot) * a.c.slot_stride + lane * 8;
+    const int64_t scale = page * a.c.s_page_stride + (in_page >> a.chunk_shift) * 4;
+    Turn t;
+    if constexpr (kRope) t = turn_of<kAny>(a, s_cos[fresh ? i - t0 : 0], s_sin[fresh ? i - t0 : 0], lane);
+    const int32_t units = 2 * a.kv_heads, batch = sides * kEach, step = batch * gridDim.z;
+    int turn = 0;
+    for (int32_t u0 = blockIdx.z * batch; u0 < units; u0 += step, turn = turn == 2 ? 0 : turn + 1) {
+      uint4 x[kEach];
+      float old[kEach];
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) {
+        const int32_t u = u0 + side * kEach + e, head = u < a.kv_heads ? u : u - a.kv_heads;
+        x[e] = make_uint4(0u, 0u, 0u, 0u);
+        old[e] = 0.0f;
+        if (u >= units || !live) continue;
+        if (fresh) {
+          x[e] = *reinterpret_cast<const uint4*>((u < a.kv_heads ? a.k : a.v) + at * a.k_token + head * a.k_head + lane * 16);
+        } else if (kept) {
+          const uint2 w = *reinterpret_cast<const uint2*>((u < a.kv_heads ? a.c.k : a.c.v) + cell + head * a.c.head_stride);
+          x[e].x = w.x;
+          x[e].y = w.y;
+          old[e] = *reinterpret_cast<const float*>((u < a.kv_heads ? a.c.ks : a.c.vs) + scale + head * a.c.s_head_stride);
+        }
+      }
+      const auto values = [&](int e, float (&f)[8]) {
+        if (kept) decode8(make_uint2(x[e].x, x[e].y), old[e], f);
+        else floats_of(x[e], f);
+      };
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) {
+        const int32_t u = u0 + side * kEach + e;
+        if constexpr (kRope)
+          if (fresh && u < a.kv_heads)
+            x[e] = turned<kAny>(a, t, x[e], a.k + at * a.k_token + u * a.k_head, lane, lanes);
+        float f[8];
+        values(e, f);
+        __syncwarp();
+        const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(finite_top(f)));
+        if ((tid & 31) == 0 && top != 0) atomicMax(&s_top[turn][side * kEach + e], top);
+      }
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) {
+        const int32_t u = u0 + side * kEach + e, head = u < a.kv_heads ? u : u - a.kv_heads;
+        if (u >= units || !(fresh || kept)) continue;
+        const Scale8 to = scale8(__uint_as_float(s_top[turn][side * kEach + e]));
+        float f[8];
+        values(e, f);
+        if (live) *reinterpret_cast<uint2*>((u < a.kv_heads ? a.c.k : a.c.v) + cell + head * a.c.head_stride) = encode8(f, to.inv);
+        if (lane == 0 && i == t1 - 1)
+          *reinterpret_cast<float*>((u < a.kv_heads ? a.c.ks : a.c.vs) + scale + head * a.c.s_head_stride) = to.s;
+      }
+      // the batch before's maxima were read before this batch's barrier; they are needed again in two batches
+      if (tid < 2 * kEach) s_top[turn == 0 ? 2 : turn - 1][tid] = 0;
+    }
+  }
+}
+
+// ------------------------------------------------------------------- host --
+
+static bool aligned_strides(std::initializer_list<int64_t> strides) {
+  for (int64_t s : strides)
+    if ((s & 7) != 0) return false;
+  return true;
+}
+
+static bool check_table_of_turns(const ss_rope_table* t, int32_t dim) {
+  return t && t->turns && (reinterpret_cast<uintptr_t>(t->turns) & 7u) == 0 && t->rot_dim >= 2 && (t->rot_dim & 1) == 0 &&
+         t->rot_dim <= dim && (t->layout == SS_ROPE_HALVES || t->layout == SS_ROPE_INTERLEAVED) && isfinite(t->magnitude);
+}
+
+static void take_rope(StepArgs* a, const ss_rope_table* t) {
+  a->turns = t->turns;
+  a->half = t->rot_dim / 2;
+  a->layout = t->layout;
+  a->magnitude = t->magnitude;
+}
+
+// As many CTAs per chunk as there are SMs to spare, up to one for every four
+// heads of K or V (or rows by themselves).
+static unsigned splits(int64_t chunks, int64_t rows) {
+  const int64_t spare = (2 * 152 + chunks - 1) / chunks, most = rows < 4 ? 1 : rows / 4;
+  const int64_t z = spare < most ? spare : most;
+  return static_cast<unsigned>(z < 1 ? 1 : z > 64 ? 64 : z);
+}
+
+template <int kFormat, bool kRope>
+static ss_status launch_step(const StepArgs& a, int32_t num_requests, cudaStream_t s) {
+  const int64_t size = 1ll << a.chunk_shift;
+  // n tokens touch at most ceil((n + size - 1) / size) blocks of slots
+  const int64_t x = kFormat == kNone ? (a.max_tokens + size - 1) / size : (a.max_tokens + 2 * size - 2) / size;
+  const int64_t rows = kFormat == SS_CACHE_FP8 ? 2ll * a.kv_heads : a.q_heads + 2ll * a.kv_heads;
+  const dim3 grid(static_cast<unsigned>(x < 1 ? 1 : x), num_requests, splits((x < 1 ? 1 : x) * num_requests, rows));
+  if constexpr (kRope) {
+    if (a.layout == SS_ROPE_HALVES && a.half % 8 != 0) {
+      step_kernel<kFormat, true, true><<<grid, kThreads, 0, s>>>(a);
+      return finish(cudaSuccess);
+    }
+  }
+  step_kernel<kFormat, kRope, false><<<grid, kThreads, 0, s>>>(a);
+  return finish(cudaSuccess);
+}
+
+static void take_append(StepArgs* a, const ss_append_args& A) {
+  a->c = view_of(A.cache, A.layer);
+  a->t = table_of(A.pool, A.table_rows);
+  a->max_tokens = A.token_offsets ? A.max_tokens : 1;
+  a->total_tokens = A.total_tokens;
+  a->offsets = A.token_offsets;
+  a->kv_len = A.kv_len;
+  a->dim = a->c.dim;
+  a->kv_heads = a->c.heads;
+  a->chunk_shift = a->c.format == SS_CACHE_FP8 ? a->c.block_shift : 4;
+  a->k = static_cast<const uint8_t*>(A.k);
+  a->v = static_cast<const uint8_t*>(A.v);
+  a->k_token = A.token_stride * 2;
+  a->k_head = A.head_stride * 2;
+  a->status = A.out_status;
+}
+
+ss_status append_blocks(const ss_append_args* args, cudaStream_t s) {
+  const ss_status checked = check_append(args);
+  if (checked != SS_OK || args->num_requests == 0) return checked;
+  StepArgs a{};
+  take_append(&a, *args);
+  return launch_step<kAppend8, false>(a, args->num_requests, s);
+}
+
+}  // namespace ssc
+
+extern "C" {
+
+ss_status ss_rope_turns(int32_t rot_dim, double base, int32_t scaling, double factor, double length, double low,
+                        double high, uint64_t* turns) {
+  SS_NVTX_RANGE("ss_rope_turns");
+  if (!turns || rot_dim < 2 || rot_dim > 128 || (rot_dim & 1) != 0 || !isfinite(base) || !(base > 0.0))
+    return SS_ERR_INVALID_ARG;
+  if (scaling != SS_ROPE_PLAIN && scaling != SS_ROPE_LINEAR && scaling != SS_ROPE_BY_PARTS) return SS_ERR_INVALID_ARG;
+  if (scaling != SS_ROPE_PLAIN && (!isfinite(factor) || !(factor > 0.0))) return SS_ERR_INVALID_ARG;
+  if (scaling == SS_ROPE_BY_PARTS && (!isfinite(length) || !(length > 0.0) || !isfinite(high) || !(low >= 0.0) || !(high > low)))
+    return SS_ERR_INVALID_ARG;
+  constexpr double kTau = 6.283185307179586;
+  uint64_t out[64];
+  for (int32_t i = 0; i < rot_dim / 2; ++i) {
+    double f = pow(base, -2.0 * i / rot_dim);
+    if (scaling == SS_ROPE_LINEAR) f /= factor;
+    if (scaling == SS_ROPE_BY_PARTS) {
+      double g = (length * f / kTau - low) / (high - low);
+      g = g < 0.0 ? 0.0 : g > 1.0 ? 1.0 : g;
+      f = f * g + f / factor * (1.0 - g);
+    }
+    const double turn = f / kTau;  // of which a position is at most half
+    if (!(turn <= 0.5)) return SS_ERR_INVALID_ARG;
+    out[i] = static_cast<uint64_t>(ldexp(turn, 64) + 0.5);
+  }
+  for (int32_t i = 0; i < rot_dim / 2; ++i) turns[i] = out[i];
+  return SS_OK;
+}
+
+ss_status ss_rope(const ss_rope_args* args, ss_stream_t stream) {
+  SS_NVTX_RANGE("ss_rope");
+  using namespace ssc;
+  if (!args) return SS_ERR_INVALID_ARG;
+  const ss_rope_args& A = *args;
+  if (A.head_dim < 8 || A.head_dim > 128 || A.head_dim % 8 != 0 || !check_table_of_turns(A.rope, A.head_dim) ||
+      A.num_requests < 0 || A.num_requests > 65535 || A.max_tokens < 0 || A.total_tokens < 0 || A.num_heads < 0 ||
+      A.num_heads > 65535 || A.num_kv_heads < 0 || A.num_kv_heads > 65535 || (A.parents && A.positions))
+    return SS_ERR_INVALID_ARG;
+  if (!A.token_offsets && A.total_tokens < A.num_requests) return SS_ERR_INVALID_ARG;
+  if (A.num_requests == 0) return SS_OK;
+  const bool any = A.total_tokens > 0;
+  if ((!A.kv_len && !A.positions) || !A.out_status || (any && A.num_heads > 0 && A.q && !A.q_out) ||
+      (any && A.num_kv_heads > 0 && A.k && !A.k_out) || !aligned16(A.q) || !aligned16(A.q_out) || !aligned16(A.k) ||
+      !aligned16(A.k_out) ||
+      !aligned_strides({A.q_token_stride, A.q_head_stride, A.q_out_token_stride, A.q_out_head_stride, A.k_token_stride,
+                        A.k_head_stride, A.k_out_token_stride, A.k_out_head_stride}))
+    return SS_ERR_INVALID_ARG;
+  StepArgs a{};
+  take_rope(&a, A.rope);
+  a.max_tokens = A.token_offsets ? A.max_tokens : 1;
+  a.total_tokens = A.total_tokens;
+  a.offsets = A.token_offsets;
+  a.kv_len = A.positions ? nullptr : A.kv_len;
+  a.parents = A.parents;
+  a.positions = A.positions;
+  a.dim = A.head_dim;
+  a.q_heads = A.q ? A.num_heads : 0;
+  a.kv_heads = A.k ? A.num_kv_heads : 0;
+  a.chunk_shift = 4;
+  a.q = static_cast<const uint8_t*>(A.q);
+  a.q_out = static_cast<uint8_t*>(A.q_out);
+  a.k = static_cast<const uint8_t*>(A.k);
+  a.k_out = static_cast<uint8_t*>(A.k_out);
+  a.q_token = A.q_token_stride * 2;
+  a.q_head = A.q_head_stride * 2;
+  a.q_out_token = A.q_out_token_stride * 2;
+  a.q_out_head = A.q_out_head_stride * 2;
+  a.k_token = A.k_token_stride * 2;
+  a.k_head = A.k_head_stride * 2;
+  a.k_out_token = A.k_out_token_stride * 2;
+  a.k_out_head = A.k_out_head_stride * 2;
+  a.status = A.out_status;
+  return launch_step<kNone, true>(a, A.num_requests, reinterpret_cast<cudaStream_t>(stream));
+}
+
+ss_status ss_rope_append(const ss_rope_append_args* args, ss_stream_t stream) {
+  SS_NVTX_RANGE("ss_rope_append");
+  using namespace ssc;
+  if (!args) return SS_ERR_INVALID_ARG;
+  const ss_status checked = check_append(args->append);
+  if (checked != SS_OK) return checked;
+  const ss_rope_append_args& A = *args;
+  const ss_append_args& B = *A.append;
+  if (!check_table_of_turns(A.rope, B.cache->head_dim) || A.num_heads < 0 || A.num_heads > 65535 || (A.parents && A.positions))
+    return SS_ERR_INVALID_ARG;
+  if (B.num_requests == 0) return SS_OK;
+  if ((B.total_tokens > 0 && A.num_heads > 0 && (!A.q || !A.q_out)) || !aligned16(A.q) || !aligned16(A.q_out) ||
+      !aligned_strides({A.q_token_stride, A.q_head_stride, A.q_out_token_stride, A.q_out_head_stride}))
+    return SS_ERR_INVALID_ARG;
+  StepArgs a{};
+  take_append(&a, B);
+  take_rope(&a, A.rope);
+  a.parents = A.parents;
+  a.positions = A.positions;
+  a.q_heads = A.num_heads;
+  a.q = static_cast<const uint8_t*>(A.q);
+  a.q_out = static_cast<uint8_t*>(A.q_out);
+  a.q_token = A.q_token_stride * 2;
+  a.q_head = A.q_head_stride * 2;
+  a.q_out_token = A.q_out_token_stride * 2;
+  a.q_out_head = A.q_out_head_stride * 2;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  switch (a.c.format) {
+    case SS_CACHE_BF16: return launch_step<SS_CACHE_BF16, true>(a, B.num_requests, s);
+    case SS_CACHE_INT4: return launch_step<SS_CACHE_INT4, true>(a, B.num_requests, s);
+    default: return launch_step<SS_CACHE_FP8, true>(a, B.num_requests, s);
+  }
+}
+
+}  // extern "C"

@@ -218,6 +218,60 @@ class ss_attention_args(C.Structure):
     ]
 
 
+class ss_rope_table(C.Structure):
+    _fields_ = [
+        ("turns", C.c_void_p),
+        ("rot_dim", C.c_int32),
+        ("layout", C.c_int32),
+        ("magnitude", C.c_float),
+    ]
+
+
+class ss_rope_args(C.Structure):
+    _fields_ = [
+        ("rope", C.POINTER(ss_rope_table)),
+        ("num_requests", C.c_int32),
+        ("max_tokens", C.c_int32),
+        ("total_tokens", C.c_int32),
+        ("head_dim", C.c_int32),
+        ("token_offsets", C.c_void_p),
+        ("kv_len", C.c_void_p),
+        ("parents", C.c_void_p),
+        ("positions", C.c_void_p),
+        ("num_heads", C.c_int32),
+        ("num_kv_heads", C.c_int32),
+        ("q", C.c_void_p),
+        ("q_out", C.c_void_p),
+        ("q_token_stride", C.c_int64),
+        ("q_head_stride", C.c_int64),
+        ("q_out_token_stride", C.c_int64),
+        ("q_out_head_stride", C.c_int64),
+        ("k", C.c_void_p),
+        ("k_out", C.c_void_p),
+        ("k_token_stride", C.c_int64),
+        ("k_head_stride", C.c_int64),
+        ("k_out_token_stride", C.c_int64),
+        ("k_out_head_stride", C.c_int64),
+        ("out_status", C.c_void_p),
+    ]
+
+
+class ss_rope_append_args(C.Structure):
+    _fields_ = [
+        ("rope", C.POINTER(ss_rope_table)),
+        ("append", C.POINTER(ss_append_args)),
+        ("parents", C.c_void_p),
+        ("positions", C.c_void_p),
+        ("num_heads", C.c_int32),
+        ("q", C.c_void_p),
+        ("q_out", C.c_void_p),
+        ("q_token_stride", C.c_int64),
+        ("q_head_stride", C.c_int64),
+        ("q_out_token_stride", C.c_int64),
+        ("q_out_head_stride", C.c_int64),
+    ]
+
+
 # Every symbol include/ss.h declares, with its ctypes signature.
 SIGNATURES = {
     "ss_workspace_size": ([C.c_int32, C.c_int32], C.c_size_t),
@@ -249,6 +303,9 @@ SIGNATURES = {
     "ss_cache_attention": ([C.POINTER(ss_attention_args), C.c_void_p, C.c_size_t, C.c_void_p], C.c_int),
     "ss_selftest_attention_timeout": ([C.POINTER(ss_attention_args), C.c_int32, C.c_void_p, C.c_size_t, C.c_void_p],
                                       C.c_int),
+    "ss_rope_turns": ([C.c_int32, C.c_double, C.c_int32] + [C.c_double] * 4 + [C.c_void_p], C.c_int),
+    "ss_rope": ([C.POINTER(ss_rope_args), C.c_void_p], C.c_int),
+    "ss_rope_append": ([C.POINTER(ss_rope_append_args), C.c_void_p], C.c_int),
     "ss_pages_reserve": ([C.POINTER(ss_page_pool), C.c_int32] + [C.c_void_p] * 5, C.c_int),
     "ss_pages_fork": ([C.POINTER(ss_page_pool), C.POINTER(ss_kv_cache), C.c_int32] + [C.c_void_p] * 5, C.c_int),
     "ss_pages_compact": ([C.POINTER(ss_page_pool), C.POINTER(ss_kv_cache), C.c_int32] + [C.c_void_p] * 3 +
@@ -584,6 +641,7 @@ def _packer(cls):
 
 
 _POOL, _APPEND, _ATTENTION = _packer(ss_page_pool), _packer(ss_append_args), _packer(ss_attention_args)
+_ROPE, _ROPE_APPEND = _packer(ss_rope_args), _packer(ss_rope_append_args)
 _quick = {}
 
 
@@ -597,31 +655,39 @@ def _quick_call(name, argtypes):
     return fn
 
 
+#: Slots of a page that share a scale in an 8-bit cache.
+SS_FP8_BLOCK = 16
+
+
 class KVCache:
     """The keys and values of a model's layers in pages (ss_kv_cache).
 
     k, v: [layers, pages, kv heads, page size, head dim] bf16; or, packed in
     4 bits, [..., head dim / 2] uint8 with k_scale and v_scale
     [layers, pages, kv heads, page size, 2] bf16 holding each row's (step,
-    low).  Any strides with contiguous rows, the same for k and v.
+    low); or in 8 bits, [..., head dim] float8_e4m3fn with k_scale and v_scale
+    [layers, pages, kv heads, page size / 16] (one for a page of 8) float32
+    holding each block's scale.  Any strides with contiguous rows, the same for
+    k and v.
     """
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         import torch
-        packed = k_scale is not None
+        fp8 = k.dtype == torch.float8_e4m3fn
+        packed = k_scale is not None and not fp8
         self.device = k.get_device()  # -1: the host; the calls refuse it
-        want = torch.uint8 if packed else torch.bfloat16
+        want = k.dtype if fp8 else torch.uint8 if packed else torch.bfloat16
         for t in (k, v):
             if t.dim() != 5 or t.dtype != want or t.shape != k.shape or t.stride() != k.stride() or t.stride(4) != 1 or \
                     t.get_device() != self.device:
                 raise SSError("KVCache: want k and v as [layers, pages, kv heads, page size, row] %s tensors of the same "
                               "shape and strides with contiguous rows, on one device" % want)
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.format = "int4" if packed else "bf16"
+        self.format = "fp8" if fp8 else "int4" if packed else "bf16"
         layers, self.num_pages, self.num_kv_heads, self.page_size, row = k.shape
         self.num_layers, self.head_dim = layers, row * 2 if packed else row
         es = k.element_size()
-        c = ss_kv_cache(1 if packed else 0, layers, self.num_pages, self.num_kv_heads, self.page_size, self.head_dim,
+        c = ss_kv_cache(_FORMATS[self.format], layers, self.num_pages, self.num_kv_heads, self.page_size, self.head_dim,
                         k.data_ptr(), v.data_ptr(), *(_span(k, i) * es for i in range(4)))
         if packed:
             for t in (k_scale, v_scale):
@@ -631,9 +697,22 @@ class KVCache:
                                   "tensors of the same strides, a page's pairs next to each other, on k's device")
             c.k_scale, c.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
             c.scale_layer_stride, c.scale_page_stride, c.scale_head_stride = (_span(k_scale, i) * 2 for i in range(3))
+        if fp8:
+            blocks = max(1, self.page_size // SS_FP8_BLOCK)
+            for t in (k_scale, v_scale):
+                if t is None or t.dtype != torch.float32 or t.shape != (*k.shape[:3], blocks) or \
+                        t.stride() != k_scale.stride() or (blocks > 1 and t.stride(3) != 1) or \
+                        t.get_device() != self.device:
+                    raise SSError("KVCache: want k_scale and v_scale as [layers, pages, kv heads, %d] float32 tensors of "
+                                  "the same strides, a page's scales next to each other, on k's device" % blocks)
+            c.k_scale, c.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
+            c.scale_layer_stride, c.scale_page_stride, c.scale_head_stride = (_span(k_scale, i) * 4 for i in range(3))
         self.struct = c
         self.ref = C.pointer(c)
         self.address = C.addressof(c)
+
+
+_FORMATS = {"bf16": 0, "int4": 1, "fp8": 2}
 
 
 def _span(t, i):
@@ -650,8 +729,13 @@ def alloc_cache(layers, pages, kv_heads, page_size, head_dim, format="bf16", dev
     shape = (layers, pages, kv_heads, page_size)
     if format == "bf16":
         return KVCache(*(torch.zeros(*shape, head_dim, dtype=torch.bfloat16, device=device) for _ in range(2)))
+    if format == "fp8":
+        blocks = max(1, page_size // SS_FP8_BLOCK)
+        return KVCache(*(torch.zeros(*shape, head_dim, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
+                         for _ in range(2)),
+                       *(torch.zeros(*shape[:3], blocks, dtype=torch.float32, device=device) for _ in range(2)))
     if format != "int4":
-        raise SSError("alloc_cache: format is 'bf16' or 'int4'")
+        raise SSError("alloc_cache: format is 'bf16', 'int4' or 'fp8'")
     return KVCache(*(torch.zeros(*shape, head_dim // 2, dtype=torch.uint8, device=device) for _ in range(2)),
                    *(torch.zeros(*shape, 2, dtype=torch.bfloat16, device=device) for _ in range(2)))
 
@@ -704,21 +788,27 @@ def _with_table(packer, page_table, cache, int32):
     return buf, C.addressof(buf) + packer.size
 
 
-def _rows_call(name, cache, layer, k, v, page_table, kv_len, status, token_offsets, max_tokens, table_rows, stream):
-    import torch
+def _pack_rows(torch, buf, at, table, cache, layer, k, v, kv_len, status, token_offsets, max_tokens, table_rows):
+    """The arguments of an append or read call (ss_append_args) into buf."""
     n, i32, shape, dev = kv_len.numel(), torch.int32, k.shape, cache.device
-    stride, handle = k.stride(), _raw_stream(torch, stream, dev)
+    stride = k.stride()
     if k.dtype is not torch.bfloat16 or v.dtype is not torch.bfloat16 or k.get_device() != dev or v.get_device() != dev or \
             len(shape) != 3 or v.shape != shape or v.stride() != stride or stride[2] != 1 or \
             shape[1] != cache.num_kv_heads or shape[2] != cache.head_dim:
         raise SSError("want k and v as [tokens, %d, %d] bf16 tensors of the same strides with contiguous rows on cuda:%d"
                       % (cache.num_kv_heads, cache.head_dim, dev))
-    buf, table = _with_table(_APPEND, page_table, cache, i32)
-    _APPEND.pack_into(buf, 0, cache.address, table, layer, n, 1 if max_tokens is None else max_tokens, shape[0],
+    _APPEND.pack_into(buf, at, cache.address, table, layer, n, 1 if max_tokens is None else max_tokens, shape[0],
                       0 if token_offsets is None else _want(token_offsets, dev, "token_offsets", i32, (n + 1,)),
                       0 if table_rows is None else _want(table_rows, dev, "table_rows", i32, (n,)),
                       _want(kv_len, dev, "kv_len", i32), k.data_ptr(), v.data_ptr(), stride[0], stride[1],
                       _want(status, dev, "status", i32, (n,)))
+
+
+def _rows_call(name, cache, layer, k, v, page_table, kv_len, status, token_offsets, max_tokens, table_rows, stream):
+    import torch
+    handle = _raw_stream(torch, stream, cache.device)
+    buf, table = _with_table(_APPEND, page_table, cache, torch.int32)
+    _pack_rows(torch, buf, 0, table, cache, layer, k, v, kv_len, status, token_offsets, max_tokens, table_rows)
     _check(_quick_call(name, [C.c_char_p, C.c_void_p])(buf, handle))
 
 
@@ -737,6 +827,102 @@ def ss_cache_read(cache, layer, k, v, page_table, kv_len, status, *, token_offse
     """The inverse of ss_cache_append: k and v are written."""
     _rows_call("ss_cache_read", cache, layer, k, v, page_table, kv_len, status, token_offsets, max_tokens, table_rows,
                stream)
+
+
+class Rope:
+    """Rotary positions for heads of head_dim channels (ss_rope_table): the
+    first rot_dim channels (None: all) in pairs, by "halves" or "interleaved",
+    with the frequencies base^(-2i / rot_dim), scaled: None, "linear" (by
+    1 / factor) or "by_parts" (pairs that turn less than `low` times within
+    `length` positions by 1 / factor, those above `high` not at all); sines and
+    cosines times magnitude.  turns: the frequencies in turns, [rot_dim / 2]
+    int64 (the bits of 64-bit fractions) on the device; a tensor of one's own
+    may be passed instead of what they are made from."""
+
+    def __init__(self, head_dim, rot_dim=None, base=10000.0, layout="halves", scaling=None, factor=1.0, length=0.0,
+                 low=1.0, high=4.0, magnitude=1.0, turns=None, device="cuda"):
+        import torch
+        self.head_dim, self.rot_dim = head_dim, head_dim if rot_dim is None else rot_dim
+        if layout not in _LAYOUTS or scaling not in _SCALINGS or not 2 <= self.rot_dim <= head_dim or self.rot_dim % 2:
+            raise SSError("Rope: layout is 'halves' or 'interleaved', scaling None, 'linear' or 'by_parts', rot_dim even "
+                          "in [2, head_dim]")
+        if turns is None:
+            table = np.empty(self.rot_dim // 2, np.uint64)
+            _check(load().ss_rope_turns(self.rot_dim, base, _SCALINGS[scaling], factor, length, low, high,
+                                        table.ctypes.data_as(C.c_void_p)))
+            turns = torch.from_numpy(table.view(np.int64)).to(device)
+        if turns.dtype != torch.int64 or turns.shape != (self.rot_dim // 2,) or not turns.is_contiguous():
+            raise SSError("Rope: want turns as a contiguous [%d] int64 tensor" % (self.rot_dim // 2))
+        self.turns, self.device = turns, turns.get_device()
+        self.struct = ss_rope_table(turns.data_ptr(), self.rot_dim, _LAYOUTS[layout], magnitude)
+        self.ref = C.pointer(self.struct)
+        self.address = C.addressof(self.struct)
+
+
+_LAYOUTS = {"halves": 0, "interleaved": 1}
+_SCALINGS = {None: 0, "linear": 1, "by_parts": 2}
+
+
+def _turned(torch, name, x, out, dim, dev):
+    """Pointers, strides and heads of an array and of where it goes turned."""
+    if x is None and out is None:
+        return 0, 0, 0, 0, 0, 0, 0, 0
+    if x is None or out is None or x.dtype is not torch.bfloat16 or out.dtype is not torch.bfloat16 or \
+            x.get_device() != dev or out.get_device() != dev or x.dim() != 3 or out.shape != x.shape or \
+            x.shape[2] != dim or x.stride(2) != 1 or out.stride(2) != 1:
+        raise SSError("want %s and %s_out as [tokens, heads, %d] bf16 tensors with contiguous rows on cuda:%d"
+                      % (name, name, dim, dev))
+    return (x.data_ptr(), out.data_ptr(), x.stride(0), x.stride(1), out.stride(0), out.stride(1), x.shape[1], x.shape[0])
+
+
+def ss_rope(rope, q, q_out, k, k_out, kv_len, status, *, token_offsets=None, max_tokens=None, parents=None,
+            positions=None, stream=None):
+    """The new tokens' queries and keys [tokens, heads, head dim], turned by
+    their positions (see include/ss.h): kv_len and the token's number, or with
+    parents its depth in the request's draft tree, or positions [tokens].  q_out
+    and k_out may be q and k; q and q_out, or k and k_out, may be None."""
+    import torch
+    i32, n, dev = torch.int32, status.numel(), rope.device
+    handle = _raw_stream(torch, stream, dev)
+    qs, ks = (_turned(torch, *x, rope.head_dim, dev) for x in (("q", q, q_out), ("k", k, k_out)))
+    total = qs[7] if q is not None else ks[7]
+    if q is not None and k is not None and qs[7] != ks[7]:
+        raise SSError("want as many tokens of k as of q")
+    buf = C.create_string_buffer(_ROPE.size)
+    _ROPE.pack_into(buf, 0, rope.address, n, 1 if max_tokens is None else max_tokens, total, rope.head_dim,
+                    0 if token_offsets is None else _want(token_offsets, dev, "token_offsets", i32, (n + 1,)),
+                    0 if kv_len is None else _want(kv_len, dev, "kv_len", i32, (n,)),
+                    0 if parents is None else _want(parents, dev, "parents", i32, (total,)),
+                    0 if positions is None else _want(positions, dev, "positions", i32, (total,)),
+                    qs[6], ks[6], *qs[:6], *ks[:6], _want(status, dev, "status", i32))
+    _check(_quick_call("ss_rope", [C.c_char_p, C.c_void_p])(buf, handle))
+
+
+def ss_rope_append(rope, cache, layer, q, q_out, k, v, page_table, kv_len, status, *, token_offsets=None,
+                   max_tokens=None, table_rows=None, parents=None, positions=None, stream=None):
+    """ss_rope on q and k, and ss_cache_append of the turned keys and of v, in
+    one launch (see include/ss.h).  k is not written; q_out may be q; q and
+    q_out may be None."""
+    import torch
+    i32, dev = torch.int32, cache.device
+    handle = _raw_stream(torch, stream, dev)
+    if rope.device != dev or rope.head_dim != cache.head_dim:
+        raise SSError("rope: want a Rope for the cache's heads of %d channels on its device" % cache.head_dim)
+    qs, total = _turned(torch, "q", q, q_out, cache.head_dim, dev), k.shape[0]
+    if q is not None and qs[7] != total:
+        raise SSError("want as many tokens of k as of q")
+    at = _ROPE_APPEND.size
+    buf, table = _with_table(_BOTH, page_table, cache, i32)
+    _pack_rows(torch, buf, at, table, cache, layer, k, v, kv_len, status, token_offsets, max_tokens, table_rows)
+    _ROPE_APPEND.pack_into(buf, 0, rope.address, C.addressof(buf) + at,
+                           0 if parents is None else _want(parents, dev, "parents", i32, (total,)),
+                           0 if positions is None else _want(positions, dev, "positions", i32, (total,)), qs[6], *qs[:6])
+    _check(_quick_call("ss_rope_append", [C.c_char_p, C.c_void_p])(buf, handle))
+
+
+class _BOTH:
+    """A buffer's room for ss_rope_append_args and the ss_append_args behind."""
+    size = _ROPE_APPEND.size + _APPEND.size
 
 
 def ss_attention_workspace_size():
