@@ -69,6 +69,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "ss.h"
 #include "ss_cache.h"
@@ -99,6 +100,7 @@ constexpr float kUnset = 3.0e38f;         // in a piece: minus the reference of 
 template <bool kPacked> constexpr float kSlack = kPacked ? 15.0f : 16.0f;
 constexpr float kDeep = 32.0f;
 constexpr float kTop = 8.0f;
+constexpr int kMostExtra = 3;             // Cfg::kExtra at most
 constexpr int kSlotFloats = 128 * 130;    // one piece: up to 128 rows of 128 channels, r and l
 
 struct AttnArgs {
@@ -151,6 +153,7 @@ struct Item {
   int32_t base, qbegin;
   int32_t cta0, cta1, piece;      // the CTAs that share the item; this CTA's piece
   int32_t pad;
+  int64_t start;                  // where the item begins in the line of all tiles
   const int32_t* row;
 };
 
@@ -161,31 +164,43 @@ template <int kLive, bool kPacked, int kHalves, bool kBytes>
 struct Cfg {
   static constexpr bool kNibbles = kPacked && !kBytes;
   static constexpr int kN = kLive < 16 ? 16 : kLive;
-  static constexpr int kNS = kPacked ? 2 * kLive : kN;
-  static constexpr int kGroups = kLive <= 16 ? 1 : kLive == 32 ? 2 : kPacked ? 2 : 4;  // softmax warpgroups
+  // 8 bits, from 32 rows on: one column per row, both parts of the queries summed
+  // into it (below, twice the MMAs would be what a tile costs)
+  static constexpr bool kOneCol = kBytes && kLive >= 32;
+  static constexpr int kNS = kPacked && !kOneCol ? 2 * kLive : kN;
+  static constexpr int kGroups = kLive <= 16 ? 1 : kLive == 32 || kNibbles ? 2 : 4;  // softmax warpgroups of a tile
   static constexpr int kCols = kLive / kGroups;              // rows per softmax thread
-  // 4 bits, few rows: two warpgroups take turns at the tiles, each with a sum
-  // and an accumulator of its own, joined at the item's end.  What a tile asks
-  // of one is mostly latency then (1300 clocks, where copying it takes 750).
-  static constexpr int kStreams = kPacked && kLive <= 16 ? 2 : 1;
+  // 4 bits, few rows, and 8 bits: two sets of warpgroups take turns at the tiles,
+  // each with a sum and an accumulator of its own, joined at the item's end.  What
+  // a tile asks of one is mostly latency (1300 clocks for few rows of 4 bits, where
+  // copying it takes 750; 8 bits, 64 rows: @@).
+  static constexpr int kStreams = kPacked && kLive <= (kBytes ? 32 : 16) ? 2 : 1;
   static constexpr int kSoft = 128 * kGroups * kStreams;
   static constexpr int kPerTile = kSoft / kStreams;          // softmax threads of one tile
   // 4 bits: one warpgroup unpacks K; V, twice the work, has two that take turns
   // where the softmax leaves the registers.  8 bits: K is used as it is.
   static constexpr int kVGroups = kLive <= 16 ? 2 : 1;
   static constexpr int kUnpack = kPacked ? 128 * (kNibbles + kVGroups) : 0;
+  // ... and from there on the softmax warps convert the next item's queries at the
+  // end of one (a prompt's items are short: one warp takes longer for 64 rows than
+  // all of their tiles)
+  static constexpr bool kConv = kBytes && kLive >= 32;
+  // What an item costs beyond its tiles, in tiles: with it the line is cut into
+  // parts that take equally long (4.2 us an item, 1.4 a tile: 2 x 4096 prompt, where
+  // CTAs had 25 to 60 items, @@)
+  static constexpr int kExtra = kConv ? 3 : 0;
   static constexpr int kThreads = 128 + kSoft + kUnpack;
   // Registers per thread by warpgroup where one size does not fit all: the
   // launch's kThreads x kRegs are shared out again (all or none of them).
   static constexpr int kRegs = kThreads > 640 ? 80 : kThreads > 512 ? 96 : kThreads > 384 ? 128 : 168;
   static constexpr bool kSplit = kPacked || kLive == 128;
-  static constexpr int kRegs0 = kStreams == 2 ? 56 : 64;                                   // copies, MMAs, queries
-  static constexpr int kRegsSoft = kBytes ? (kStreams == 2 ? 128 : 184) : !kPacked || kStreams == 2 ? 104 : kLive >= 64 ? 152 : 136;
-  static constexpr int kRegsUnpack = kBytes ? 80 : kLive >= 64 ? 56 : 72;
+  static constexpr int kRegs0 = kBytes ? (kLive <= 16 ? 96 : kLive == 32 ? 56 : 40) : kStreams == 2 ? 56 : 64;                                   // copies, MMAs, queries
+  static constexpr int kRegsSoft = kBytes ? (kLive <= 16 ? 104 : kLive == 32 ? 88 : 96) : !kPacked || kStreams == 2 ? 104 : kLive >= 64 ? 152 : 136;
+  static constexpr int kRegsUnpack = kBytes ? (kLive <= 16 ? 88 : kLive == 32 ? 72 : 56) : kLive >= 64 ? 56 : 72;
   static_assert(!kSplit || kRegs0 + kSoft / 128 * kRegsSoft + kUnpack / 128 * kRegsUnpack <= kThreads / 128 * kRegs,
                 "a warpgroup would wait for registers for ever");
   static constexpr int kStage = kHalves * 16384;             // 128 keys x 64 channels x 2 bytes per half
-  static constexpr int kQ = kPacked ? kNS * 128 : kHalves * kN * 128;
+  static constexpr int kQ = kPacked ? 2 * kLive * 128 : kHalves * kN * 128;
   static constexpr int kNQ = 2;                              // items prepared ahead
   static constexpr int kQBufs = kLive >= 128 ? 1 : 2;        // of which with their queries
   static constexpr int kPitch = kN >= 64 ? 128 : kN * 2;     // bytes per key of a P block
@@ -366,9 +381,10 @@ __device__ __forceinline__ constexpr uint32_t instr_desc(bool mn) {
          (static_cast<uint32_t>(128 >> 4) << 24);
 }
 
-template <int kN>
+// (e5m2: B's numbers are)
+template <int kN, bool kE5m2 = false>
 __device__ __forceinline__ constexpr uint32_t instr_desc_e4m3() {
-  return (1u << 4) | (static_cast<uint32_t>(kN >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
+  return (1u << 4) | (kE5m2 ? 1u << 10 : 0u) | (static_cast<uint32_t>(kN >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
 }
 
 // True in one lane of the warp.  Inside `if (elect_one())` the compiler knows
@@ -541,6 +557,11 @@ __device__ __forceinline__ uint32_t e4m3_pair(float a, float b) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
   return r;
 }
+__device__ __forceinline__ uint32_t e5m2_pair(float a, float b) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
 __device__ __forceinline__ uint32_t f16_of_e4m3(uint32_t pair) {
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(pair)));
@@ -639,7 +660,7 @@ __device__ __forceinline__ Request request_of(const AttnArgs& a, int32_t r) {
     const uint32_t all = min(q.base + q.n, a.table_end);
     const uint32_t keys = a.window > 0 ? min(all, a.window + 2u * kTile) + min(static_cast<uint32_t>(a.sinks), all) : all;
     const uint32_t blocks = (static_cast<uint32_t>(q.n * a.group - 1) >> (31 - __clz(a.block_rows))) + 1;
-    q.ok = (static_cast<uint64_t>(blocks) * (keys / kTile + 3)) >> 31 == 0;
+    q.ok = (static_cast<uint64_t>(blocks) * (keys / kTile + 3 + kMostExtra)) >> 31 == 0;
   }
   if (!q.ok) q.n = 0;
   return q;
@@ -712,20 +733,25 @@ __device__ __forceinline__ int32_t add_tiles(int32_t x, int32_t y) {
   return static_cast<int32_t>(min(static_cast<uint32_t>(x) + static_cast<uint32_t>(y), 0x7fffffffu));
 }
 
-// Tiles of one kv head of a request; the lanes of a warp share its blocks.
+// Tiles of one kv head of a request, and kExtra for each item; the lanes of a
+// warp share its blocks.
+template <int kExtra>
 __device__ __forceinline__ int32_t request_tiles(const AttnArgs& a, const Request& q, int32_t block0, int32_t step) {
   int32_t sum = 0;
 #pragma unroll 1
   for (int32_t row0 = block0 * a.block_rows; row0 < q.n * a.group; row0 += step * a.block_rows)
-    sum += span_of(a, q, row0).tiles;
+    sum += span_of(a, q, row0).tiles + kExtra;
   return sum;
 }
 
 // The queries of an item over a cache of 4 or 8 bits: row n as unit (hi + lo / 32), both
 // e4m3, unit a power of two by the row's largest channel: q's 8 bits are 4 + 4,
-// so this is exact but for channels below 2^-15 of the largest.  16 lanes per
-// row, 8 channels each; a warp has 2 kEach rows in flight.
-template <int kLive, int kEach, bool kBytes>
+// so this is exact but for channels below 2^-15 of the largest.  kOneCol: unit
+// (hi + lo), lo e5m2: what 4 bits leave of 8 is at most 8 units of the eighth,
+// for which 3 bits are enough; channels below 2^-13 of the largest are off by
+// 2^-21 of it at most.  16 lanes per row, 8 channels each; a warp has 2 kEach rows
+// in flight.
+template <int kLive, int kEach, bool kBytes, bool kOneCol>
 __device__ __forceinline__ void convert_queries(const AttnArgs& a, const Item& it, uint8_t* q, float* qsum, float* unit,
                                                 int warp, int warps) {
   const int lane = threadIdx.x & 31, ch = lane & 15;
@@ -776,7 +802,8 @@ __device__ __forceinline__ void convert_queries(const AttnArgs& a, const Item& i
         const float p0 = v[c] * scale, p1 = v[d] * scale;
         const uint32_t h = e4m3_pair(p0, p1);
         const float2 back = e4m3_floats(h);
-        const uint32_t r = e4m3_pair((p0 - back.x) * 32.0f, (p1 - back.y) * 32.0f);
+        const uint32_t r = kOneCol ? e5m2_pair(p0 - back.x, p1 - back.y)
+                                   : e4m3_pair((p0 - back.x) * 32.0f, (p1 - back.y) * 32.0f);
         hi[i >> 1] |= h << (16 * (i & 1));
         lo[i >> 1] |= r << (16 * (i & 1));
       }
@@ -851,7 +878,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves, kBytes>::kThreads
     }
     for (int i = 0; i < kNQ; ++i) {
       mbar_init(mfull + i, 32 + more(SS_STALL_ITEMS));
-      mbar_init(qfull + i, 32 + more(SS_STALL_QUERIES));
+      mbar_init(qfull + i, (F::kConv ? F::kSoft : 32) + more(SS_STALL_QUERIES));
       mbar_init(qempty + i, 1 + F::kSoft / 32);
     }
     for (int i = 0; i < F::kQBufs; ++i) mbar_init(qfree + i, 1);
@@ -860,7 +887,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves, kBytes>::kThreads
         mbar_init(rfull + i, (kNibbles ? 33 : 1) + more(SS_STALL_PACKED));  // the copies' bytes, and the lanes' own copies
         mbar_init(rempty + i, kNibbles ? 256 : 128);
       }
-    for (int i = 0; i < 2; ++i) mbar_init(written + i, F::kGroups > 1 ? F::kSoft - 128 : 1);
+    for (int i = 0; i < 2; ++i) mbar_init(written + i, F::kGroups > 1 ? F::kPerTile - 128 : 1);
     mbar_init(&drain[0], 1);
     mbar_init(&drain[1], 1);
     s_dead = 0;
@@ -883,13 +910,13 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves, kBytes>::kThreads
 #pragma unroll 1
     for (int32_t r = tid; r < a.num_requests; r += F::kThreads) {
       const Request q = request_of(a, r);
-      weights[r] = request_tiles(a, q, 0, 1);
+      weights[r] = request_tiles<F::kExtra>(a, q, 0, 1);
     }
   } else {
 #pragma unroll 1
     for (int32_t r = warp; r < a.num_requests; r += F::kThreads / 32) {
       const Request q = request_of(a, r);
-      const int32_t w = __reduce_add_sync(0xffffffffu, request_tiles(a, q, lane, 32));
+      const int32_t w = __reduce_add_sync(0xffffffffu, request_tiles<F::kExtra>(a, q, lane, 32));
       if (lane == 0) weights[r] = w;
     }
   }
@@ -945,7 +972,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves, kBytes>::kThreads
     if (warp == 0) {
     // ---------------------------------------------------- tensor copies --
     const int32_t unit_shift = min(a.c.page_shift, 7), units = kTile >> unit_shift;
-    const int32_t tiles_all = __shfl_sync(0xffffffffu, my_tiles, 0);
+    const int32_t tiles_all = F::kExtra ? 0x7fffffff : __shfl_sync(0xffffffffu, my_tiles, 0);  // (or until an item of none)
     const uint32_t ring_a = smem_addr(ring);
     const uint32_t vring_a = ring_a + (kPacked ? 0 : kKs) * F::kStage;
     const uint32_t raw_a = ring_a + kRing * F::kStage + F::kPBufs * F::kP + F::kQBufs * F::kQ;
@@ -963,6 +990,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves, kBytes>::kThreads
       const Item& it = items[b];
       const auto same = [](int32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
       const int32_t tiles = same(it.tiles), tile0 = same(it.tile0), nsink = same(it.nsink), sink_end = same(it.sink_end);
+      if (F::kExtra && tiles == 0) break;
       const int32_t origin = same(it.origin), end = same(it.end), head = same(it.head);
       const int32_t* row = it.row;
       // 64 entries of the page table from the next tile's on, two per lane,
@@ -1089,7 +1117,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves, kBytes>::kThreads
     // of its own, so that one's waits pass under the other's MMAs.
     constexpr uint32_t kHi = desc_hi(1024, 2);
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-    const int32_t tiles_all = __shfl_sync(0xffffffffu, my_tiles, 0);
+    const int32_t tiles_all = F::kExtra ? 0x7fffffff : __shfl_sync(0xffffffffu, my_tiles, 0);
     const uint32_t ring_a = smem_addr(ring);
     const uint32_t q_a = ring_a + kRing * F::kStage + F::kPBufs * F::kP;
     const int k_steps = kPacked ? (a.c.dim + 31) / 32 : (a.c.dim + 15) / 16;
@@ -1101,6 +1129,10 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves, kBytes>::kThreads
 #pragma unroll 1
     for (int32_t k = 0; at < tiles_all && ok; ++k) {
       const int qb = k % kNQ;
+      if constexpr (F::kExtra) {
+        wait(mfull + qb, k / kNQ);
+        if (!ok || __shfl_sync(0xffffffffu, items[qb].tiles, 0) == 0) break;
+      }
       wait(qfull + qb, k / kNQ);
       if (!ok) break;
       const int32_t tiles = __shfl_sync(0xffffffffu, items[qb].tiles, 0);
@@ -1122,6 +1154,12 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves, kBytes>::kThreads
               if (kk < k_steps)
                 umma_e4m3(tm + b * kNS, desc(ka + kk * 2, kHiK), desc(qa + kk * 2, kHi), instr_desc_e4m3<kNS>(),
                           kk > 0 ? 1u : 0u);
+            if constexpr (F::kOneCol)
+#pragma unroll
+              for (int kk = 0; kk < 2 * kHalves; ++kk)
+                if (kk < k_steps)
+                  umma_e4m3(tm + b * kNS, desc(ka + kk * 2, kHiK), desc(qa + (kLive * 128 >> 4) + kk * 2, kHi),
+                            instr_desc_e4m3<kNS, true>(), 1u);
           } else if constexpr (kPacked) {
 #pragma unroll
             for (int kk = 0; kk < 2 * kHalves; ++kk)
@@ -1154,7 +1192,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves, kBytes>::kThreads
     // ---------------------------------------- second product, O^T += V^T P^T --
     constexpr uint32_t kHiV = desc_hi(1024, 2), kHiP = desc_hi(8 * F::kPitch, kN >= 64 ? 2u : kN == 32 ? 4u : 6u);
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-    const int32_t tiles_all = __shfl_sync(0xffffffffu, my_tiles, 0);
+    const int32_t tiles_all = F::kExtra ? 0x7fffffff : __shfl_sync(0xffffffffu, my_tiles, 0);
     const uint32_t ring_a = smem_addr(ring);
     const uint32_t p_a = ring_a + kRing * F::kStage, v_a = ring_a + (kPacked ? 0 : kKs) * F::kStage;
     bool ok = true;
@@ -1168,6 +1206,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves, kBytes>::kThreads
       wait(mfull + qb, k / kNQ);
       if (!ok) break;
       const int32_t tiles = __shfl_sync(0xffffffffu, items[qb].tiles, 0);
+      if (F::kExtra && tiles == 0) break;
       wait(oempty + (k & 1), (k >> 1) + 1);
 #pragma unroll 1
       for (int32_t t = 0; t < tiles; ++t, ++at) {
@@ -1209,7 +1248,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves, kBytes>::kThreads
 #pragma unroll 1
     for (;; row0 += 32 * kLive) {  // the block that holds it: 32 blocks at a time
       const int32_t mine_row = row0 + lane * kLive;
-      const int32_t n = mine_row < q.n * a.group ? span_of(a, q, mine_row).tiles : 0;
+      const int32_t n = mine_row < q.n * a.group ? span_of(a, q, mine_row).tiles + F::kExtra : 0;
       int32_t sum = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -1230,11 +1269,34 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves, kBytes>::kThreads
     int32_t q_items = 0;  // whose queries are issued
     int32_t tree_of = -1, node_deep[2];
     uint64_t node_path[2];
+    const auto next_item = [&]() {  // what begins at `start`
+      skip = 0;
+      row0 += kLive;
+      if (row0 >= q.n * a.group) {
+        row0 = 0;
+        if (++head == a.c.heads) {
+          head = 0;
+          do {
+            q = request_of(a, ++r);
+          } while (q.n == 0);
+        }
+      }
+      s = span_of(a, q, row0);
+    };
 #pragma unroll 1
-    for (int32_t k = 0; left > 0; ++k) {
+    for (int32_t k = 0; F::kExtra || left > 0; ++k) {
       const int b = k % kNQ;
       if (!__all_sync(0xffffffffu, wait_item(qempty + b, ((k / kNQ) & 1) ^ 1u, dead))) break;
-      const int32_t rows = min(kLive, q.n * a.group - row0), take = min(left, s.tiles - skip);
+      // this CTA's part of the item's place in the line: kExtra, then the tiles
+      const int32_t part = min(left, s.tiles + F::kExtra - skip);
+      const int32_t tile0 = max(skip - F::kExtra, 0), take = max(skip + part - F::kExtra, 0) - tile0;
+      if constexpr (F::kExtra)
+        if (take == 0) {  // no more: an item without tiles
+          if (lane == 0) items[b].tiles = 0;
+          mbar_arrive(mfull + b);
+          break;
+        }
+      const int32_t rows = min(kLive, q.n * a.group - row0);
       if (lane == 0) {
         Item it;
         it.r = r;
@@ -1242,7 +1304,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves, kBytes>::kThreads
         it.row0 = row0;
         it.rows = rows;
         it.tiles = take;
-        it.tile0 = skip;
+        it.tile0 = tile0;
         it.all = s.tiles;
         it.nsink = s.nsink;
         it.sink_end = s.sink_end;
@@ -1250,10 +1312,11 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves, kBytes>::kThreads
         it.end = s.end;
         it.base = q.base;
         it.qbegin = q.qbegin;
-        it.cta0 = static_cast<int32_t>(((start + 1) * ctas - 1) / total);
-        it.cta1 = static_cast<int32_t>(((start + s.tiles) * ctas - 1) / total);
-        it.piece = (start + skip == lo) ? 0 : 1;
+        it.cta0 = static_cast<int32_t>(((start + F::kExtra + 1) * ctas - 1) / total);
+        it.cta1 = static_cast<int32_t>(((start + F::kExtra + s.tiles) * ctas - 1) / total);
+        it.piece = start <= lo ? 0 : 1;  // the CTA's first item?
         it.pad = 0;
+        it.start = start;
         it.row = q.row;
         items[b] = it;
       }
@@ -1308,8 +1371,17 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves, kBytes>::kThreads
       mbar_arrive(mfull + b);
       __syncwarp();
       const int qb = k % F::kQBufs;
-      if (!__all_sync(0xffffffffu, wait_item(qfree + qb, ((k / F::kQBufs) & 1) ^ 1u, dead))) break;
-      if constexpr (!kPacked) {
+      if constexpr (!F::kConv)
+        if (!__all_sync(0xffffffffu, wait_item(qfree + qb, ((k / F::kQBufs) & 1) ^ 1u, dead))) break;
+      if constexpr (F::kConv) {  // (the softmax warps' work, from L2)
+#pragma unroll 1
+        for (int n = lane; n < 2 * rows; n += 32) {
+          const int32_t token = token_of(a, row0 + (n >> 1)), h = head * a.group + (row0 + (n >> 1) - token * a.group);
+          if ((n & 1) * 64 < a.c.dim)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(a.q + (static_cast<int64_t>(q.qbegin) + token) * a.q_token +
+                                                          h * a.q_head + (n & 1) * 128));
+        }
+      } else if constexpr (!kPacked) {
         // by tensor copies: the block's tokens times the group's heads in one
         // box where blocks start at tokens, else row by row
         uint8_t* dst = qbuf + qb * F::kQ;
@@ -1330,30 +1402,23 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves, kBytes>::kThreads
         }
       } else {
         if (k > 0) {
-          convert_queries<kLive, 4, kBytes>(a, items[b], qbuf + qb * F::kQ, row_qsum[kNibbles ? b : 0], row_unit[b], 0, 1);
+          convert_queries<kLive, 4, kBytes, F::kOneCol>(a, items[b], qbuf + qb * F::kQ, row_qsum[kNibbles ? b : 0], row_unit[b], 0,
+                                                        1);
           proxy_fence();
         } else {
           bar_sync(6, F::kSoft + 32);  // the softmax warps have done it
         }
       }
-      mbar_arrive(qfull + b);
+      if constexpr (!F::kConv) mbar_arrive(qfull + b);
       q_items = k + 1;
-      // the next item
-      left -= take;
-      if (left == 0) break;
-      start += s.tiles;
-      skip = 0;
-      row0 += kLive;
-      if (row0 >= q.n * a.group) {
-        row0 = 0;
-        if (++head == a.c.heads) {
-          head = 0;
-          do {
-            q = request_of(a, ++r);
-          } while (q.n == 0);
-        }
+      left -= part;
+      if (left == 0) {
+        if (!F::kExtra) break;
+        skip += part;  // nothing is taken of what is left of it
+        continue;
       }
-      s = span_of(a, q, row0);
+      start += s.tiles + F::kExtra;
+      next_item();
     }
     if constexpr (!kPacked) {  // their copies end before this warp does
       bool landed = true;
@@ -1364,8 +1429,8 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves, kBytes>::kThreads
     if constexpr (F::kSplit) regs_more<F::kRegsSoft>();
     // ---------------------------------------------------------- softmax --
     const int st = tid - 128, wg = st >> 7, lt = st & 127, wq = warp & 3;
-    const int stream = F::kStreams == 2 ? wg : 0;
-    const int c0 = F::kStreams == 2 ? 0 : wg * kCols;             // this warpgroup's rows
+    const int stream = wg / F::kGroups, part_of = wg % F::kGroups;
+    const int c0 = part_of * kCols;                               // this warpgroup's rows
     const int h0 = stream * kN + c0;                              // their state
     const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;  // this warp's tensor-memory lanes
     const int bar = 1 + wg;                                       // its barrier
@@ -1377,24 +1442,36 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves, kBytes>::kThreads
     constexpr uint32_t kSwz = kN >= 64 ? 0x70u : kN == 32 ? 0x30u : 0x10u;  // P's swizzle
     int32_t done = 0;  // tiles of the items before
     uint32_t uses[2] = {0, 0};  // of written
-    for (int32_t k = 0; done < my_tiles; ++k) {
+    const auto convert = [&](int32_t k) {  // item k's queries, by all softmax warps
+      constexpr int kWarps = F::kSoft / 32, kEach = kLive >= 8 * kWarps ? 4 : kLive >= 4 * kWarps ? 2 : 1;
+      const int b = k % kNQ;
+      convert_queries<kLive, kEach, kBytes, F::kOneCol>(a, items[b], qbuf + k % F::kQBufs * F::kQ, row_qsum[kNibbles ? b : 0],
+                                                        row_unit[b], st >> 5, kWarps);
+    };
+    bool none = false;  // kConv: no item is left, or a wait for it has given up
+    for (int32_t k = 0; F::kExtra || done < my_tiles; ++k) {
       const int b = k % kNQ;
       if constexpr (kPacked)
         if (k == 0) {  // the first item's queries, for which everyone waits, by all of these warps
-          constexpr int kWarps = F::kSoft / 32, kEach = kLive >= 8 * kWarps ? 4 : kLive >= 4 * kWarps ? 2 : 1;
           // (given up: there is no item to read; the barrier all the same)
-          if (__all_sync(0xffffffffu, wait_or_dead(mfull, 0, dead)))
-            convert_queries<kLive, kEach, kBytes>(a, items[0], qbuf, row_qsum[0], row_unit[0], st >> 5, kWarps);
+          const bool there = __all_sync(0xffffffffu, wait_or_dead(mfull, 0, dead));
+          if constexpr (F::kConv) none = !there || items[0].tiles == 0;
+          if (there && !none) convert(0);
           proxy_fence();
-          bar_sync(6, F::kSoft + 32);
+          if constexpr (F::kConv) {
+            if (!none) mbar_arrive(qfull);
+          } else {
+            bar_sync(6, F::kSoft + 32);
+          }
         }
       // The rows' references start at 0: before the barrier, behind which every
       // warp reads them (the last item's readers have passed barriers since).
       if (lt < kCols) nref[h0 + lt] = 0.0f;
       // (4 bits: the rows' sums and units come with the queries)
-      const bool in = wait_or_dead((kPacked ? qfull : mfull) + b, (k / kNQ) & 1, dead);
-      if (bar_any(5, F::kSoft, !in)) break;  // the same decision for every softmax thread
-      const Item it = items[b];
+      const bool in = none || wait_or_dead((kPacked ? qfull : mfull) + b, (k / kNQ) & 1, dead);
+      if (bar_any(5, F::kSoft, !in || none)) break;  // the same decision for every softmax thread
+      // (8 bits: read where it is needed, registers are short)
+      std::conditional_t<F::kConv, const Item&, const Item> it = items[b];
       float l[kCols], cs[kNibbles ? kCols : 1];
 #pragma unroll
       for (int n = 0; n < kCols; ++n) l[n] = 0.0f;
@@ -1407,6 +1484,12 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves, kBytes>::kThreads
       const int32_t first_pos = it.base + (tree ? 0 : token_of(a, it.row0));
       const int32_t last_pos = it.base + token_of(a, it.row0 + it.rows - 1);  // of a tree: at most
       const int32_t first_off = it.row0 - token_of(a, it.row0) * a.group;     // rows of the first token in blocks before
+      // 8 bits: the item's tiles of which every row sees every key are clear0 .. clear1 - 1 (pages apart)
+      int32_t clear0 = 0, clear1 = 0;
+      if constexpr (F::kConv) {
+        clear0 = it.nsink + (a.window > 0 ? max(0, ((last_pos - a.window - it.origin) >> 7) + 1) : 0);
+        clear1 = it.nsink + (((tree ? it.base - 1 : first_pos) - (kTile - 1) - it.origin) >> 7) + 1;
+      }
 #pragma unroll 1
       for (int32_t t = F::kStreams == 2 ? (done ^ stream) & 1 : 0; t < it.tiles; t += F::kStreams) {
         const int32_t at = done + t;
@@ -1422,13 +1505,13 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves, kBytes>::kThreads
         constexpr int kPart = !kPacked ? 8 : kCols < 16 ? kCols : 16;
         float x[kCols], low[kPart];
         tmem_get(tmem + sb * kNS + c0 + lanes, x);
-        if constexpr (kPacked) tmem_get(tmem + sb * kNS + kLive + c0 + lanes, low);
+        if constexpr (kPacked && !F::kOneCol) tmem_get(tmem + sb * kNS + kLive + c0 + lanes, low);
         // (Where the wait has given up the copies' warp may write it now: the
         // threads need not agree on it, and nothing that they do together
         // depends on it.)
         const uint32_t there = *reinterpret_cast<volatile uint32_t*>(info + at % kInfo);
         // does some row miss some key of the tile?
-        const bool masked = sink || there != every || j0 + kTile - 1 > (tree ? it.base - 1 : first_pos) ||
+        const bool masked = F::kConv ? there != every || n < clear0 || n >= clear1 : sink || there != every || j0 + kTile - 1 > (tree ? it.base - 1 : first_pos) ||
                             (a.window > 0 && j0 <= last_pos - a.window);
         float ka = a.scale_log2, kb = 0.0f, sv = 0.0f, wv = 0.0f;
         float big = 0.0f;  // log2 of the key's values, rounded up: 0 where it does not matter
@@ -1501,7 +1584,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves, kBytes>::kThreads
             // shared memory, and the queries that do see it get a weight of NaN.
             // Each warpgroup looks at its part of the channels.
             constexpr int kScan = 8 * kHalves / F::kGroups;
-            const int scan0 = F::kGroups > 1 ? wg * kScan : 0;
+            const int scan0 = part_of * kScan;
             const int32_t s = at % kVs;
             wait_or_dead(vfull + s, (at / kVs) & 1, dead);
             const bool all = here && !draft && j <= first_pos && (always || j > last_pos - a.window);
@@ -1525,7 +1608,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves, kBytes>::kThreads
         }
         // x_nj - r_n of this key, every row
         tmem_wait(x);
-        if constexpr (kPacked) {
+        if constexpr (kPacked && !F::kOneCol) {
 #pragma unroll
           for (int i0 = 0; i0 < kCols; i0 += kPart) {
             if (i0 > 0) tmem_get(tmem + sb * kNS + kLive + c0 + i0 + lanes, low);
@@ -1650,7 +1733,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves, kBytes>::kThreads
           // warpgroup 0 hears what the others found, and writes into their
           // weights once they are there
           poison = false;
-          if (wg != 0) {
+          if (part_of != 0) {
             mbar_arrive(&written[sb]);
           } else {
             wait_or_dead(&written[sb], uses[sb] & 1, dead);
@@ -1685,6 +1768,15 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves, kBytes>::kThreads
         proxy_fence();
         tc_fence_before();
         mbar_arrive(pfull + sb);
+      }
+      if constexpr (F::kConv) {  // the next item's queries, while the last product ends
+        const int32_t n = k + 1;
+        none = !__all_sync(0xffffffffu, wait_item(mfull + n % kNQ, (n / kNQ) & 1, dead)) || items[n % kNQ].tiles == 0;
+        if (!none) {
+          if (__all_sync(0xffffffffu, wait_or_dead(qfree + n % F::kQBufs, ((n / F::kQBufs) & 1) ^ 1u, dead))) convert(n);
+          proxy_fence();
+          mbar_arrive(qfull + n % kNQ);
+        }
       }
       // ---- the item's end: sums over the keys, then the rows
       done += it.tiles;
@@ -1724,24 +1816,25 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves, kBytes>::kThreads
         tc_fence_before();  // each warpgroup reads both accumulators
         bar_sync(5, F::kSoft);
         tc_fence_after();
-        if (st < kCols) {
-          const float n0 = part[0][st], n1 = part[0][kN + st], s0 = part[1][st], s1 = part[1][kN + st];
+        if (stream == 0 && lt < kCols) {
+          const int c = c0 + lt;
+          const float n0 = part[0][c], n1 = part[0][kN + c], s0 = part[1][c], s1 = part[1][kN + c];
           const float top = fminf(n0, n1);
           const float g0 = n0 == kUnset ? (s0 == 0.0f ? 0.0f : 1.0f) : ex2(top - n0);
           const float g1 = n1 == kUnset ? (s1 == 0.0f ? 0.0f : 1.0f) : ex2(top - n1);
           sum = __fmaf_rn(g0, s0, g1 * s1);
           const float inv = !whole ? 1.0f : sum == 0.0f ? 0.0f : __fdividef(1.0f, sum);
-          nref[st] = top;
-          sums[st] = g0 * inv;
-          sums[kN + st] = g1 * inv;
-          csums[st] = __fmaf_rn(g0, part[2][st], g1 * part[2][kN + st]) * inv;
+          nref[c] = top;
+          sums[c] = g0 * inv;
+          sums[kN + c] = g1 * inv;
+          csums[c] = __fmaf_rn(g0, part[2][c], g1 * part[2][kN + c]) * inv;
           unset = top == kUnset;
         }
         bar_sync(5, F::kSoft);
       }
       // this warpgroup's rows of the result, scaled
       constexpr int kOut = kCols / F::kStreams;
-      const int r0 = F::kStreams == 2 ? wg * kOut : c0;
+      const int r0 = c0 + stream * kOut;
       if (wq * 32 < kHalves * 64 && r0 < rows) {
         // eight rows at a time, in a loop: the code is fetched once per item
         constexpr int kStep = kOut < 8 ? kOut : 8;
@@ -1805,8 +1898,8 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves, kBytes>::kThreads
           // piece p is CTA cta0 + p's first, but for the first CTA, whose
           // second piece it is unless the item starts where the CTA starts
           __threadfence();
-          const int64_t item_start = (it.piece == 0 ? lo : hi - it.tiles) - it.tile0;
-          const int32_t first_piece = item_start == total * it.cta0 / ctas ? 0 : 1;
+          const int64_t item_start = F::kExtra ? it.start : (it.piece == 0 ? lo : hi - it.tiles) - it.tile0;
+          const int32_t first_piece = item_start <= total * it.cta0 / ctas ? 0 : 1;
           const float* base = a.pieces + static_cast<int64_t>(it.cta0) * 2 * kSlotFloats;
           const auto piece_at = [&](int32_t p) {
             return base + (static_cast<int64_t>(p) * 2 + (p == 0 ? first_piece : 0)) * kSlotFloats;
@@ -1896,8 +1989,17 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves, kBytes>::kThreads
     // A thread per key, warpgroups that take turns: V as f16, which holds every
     // e4m3 number, since the weights that it meets need f16's bits.
     const int key = (tid - 128 - F::kSoft) & 127;
+    int32_t upto = 0, k = 0;  // the end of the items so far
 #pragma unroll 1
-    for (int32_t at = (tid - 128 - F::kSoft) >> 7; at < my_tiles; at += F::kVGroups) {
+    for (int32_t at = (tid - 128 - F::kSoft) >> 7; F::kExtra || at < my_tiles; at += F::kVGroups) {
+      if constexpr (F::kExtra)
+        if (at == upto) {  // the next item
+          if (!__all_sync(0xffffffffu, wait_item(mfull + k % kNQ, (k / kNQ) & 1, dead))) break;
+          const int32_t tiles = items[k % kNQ].tiles;
+          if (tiles == 0) break;
+          upto += tiles;
+          ++k;
+        }
       const int32_t rs = at % F::kRawStages, s = at % kVs;
       if (!__all_sync(0xffffffffu, wait_or_dead(rfull + rs, (at / F::kRawStages) & 1, dead))) break;
       const uint8_t* src = raw + rs * F::kRaw;
@@ -2011,7 +2113,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves, kBytes>::kThreads
 #pragma unroll 1
     for (int32_t r = s_r0; r < a.num_requests && upto * a.c.heads < hi; ++r) {
       const Request q = request_of(a, r);
-      upto += request_tiles(a, q, 0, 1);
+      upto += request_tiles<F::kExtra>(a, q, 0, 1);
       if (q.n > 0) atomicExch(a.status + r, SS_ROW_TIMEOUT);
     }
   }
