@@ -50,65 +50,81 @@ struct StepArgs {
 };
 
 // What one lane needs to turn its 8 channels: out = x c + partner s, partner
-// the other channel of the pair, s with its sign.
+// the other channel of the pair, s with its sign; two channels at a time.
 struct Turn {
-  float c[8], s[8];
+  uint64_t c[4], s[4];
   uint32_t on;  // channels that turn
 };
 
-// kAny: halves whose pairs do not lie 8 channels next to 8 channels.
-template <bool kAny>
+// kOdd: pairs that do not come eight by eight (halves of rot_dim not in
+// multiples of 8 channels, interleaved ones that end inside a lane's channels).
 __device__ __forceinline__ Turn turn_of(const StepArgs& a, const float* cos_of, const float* sin_of, int lane) {
   Turn t;
   t.on = 0;
   const int c0 = lane * 8, rot = 2 * a.half;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int ch = c0 + i;
-    const bool second = a.layout == SS_ROPE_HALVES ? ch >= a.half : i & 1;
-    int pair = a.layout == SS_ROPE_HALVES ? (second ? ch - a.half : ch) : ch >> 1;
-    if (ch >= rot) pair = 0;
-    t.c[i] = cos_of[pair];
-    t.s[i] = second ? sin_of[pair] : -sin_of[pair];
-    t.on |= static_cast<uint32_t>(ch < rot) << i;
+  for (int i = 0; i < 4; ++i) {
+    float c[2], s[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int ch = c0 + 2 * i + e;
+      const bool second = a.layout == SS_ROPE_HALVES ? ch >= a.half : e == 1;
+      int pair = a.layout == SS_ROPE_HALVES ? (second ? ch - a.half : ch) : ch >> 1;
+      if (ch >= rot) pair = 0;
+      c[e] = cos_of[pair];
+      s[e] = second ? sin_of[pair] : -sin_of[pair];
+      t.on |= static_cast<uint32_t>(ch < rot) << (2 * i + e);
+    }
+    t.c[i] = two(c[0], c[1]);
+    t.s[i] = two(s[0], s[1]);
   }
   return t;
 }
 
 // One row's 8 channels, turned.  All 16 lanes of the row call it.  `row` is the
-// row in global memory, read again where lanes' channels do not pair up (kAny).
-template <bool kAny>
+// row in global memory, read again where lanes' channels do not pair up (kOdd).
+template <bool kOdd>
 __device__ __forceinline__ uint4 turned(const StepArgs& a, const Turn& t, const uint4& x, const uint8_t* row, int lane,
                                         uint32_t lanes) {
-  float v[8], p[8];
-  floats_of(x, v);
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint64_t p[4];
   if (a.layout == SS_ROPE_INTERLEAVED) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) p[i] = v[i ^ 1];
-  } else if (!kAny) {
+    for (int i = 0; i < 4; ++i) p[i] = two(bf16_hi(w[i]), bf16_lo(w[i]));
+  } else if (!kOdd) {
     const int other = lane * 8 < a.half ? lane + a.half / 8 : lane - a.half / 8;  // past rot_dim: not used
-    const uint4 y = make_uint4(__shfl_sync(lanes, x.x, other, kRowLanes), __shfl_sync(lanes, x.y, other, kRowLanes),
-                               __shfl_sync(lanes, x.z, other, kRowLanes), __shfl_sync(lanes, x.w, other, kRowLanes));
-    floats_of(y, p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t y = __shfl_sync(lanes, w[i], other, kRowLanes);
+      p[i] = two(bf16_lo(y), bf16_hi(y));
+    }
   } else {
     const uint16_t* at = reinterpret_cast<const uint16_t*>(row);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int ch = lane * 8 + i;
-      p[i] = 0.0f;
-      if (ch < 2 * a.half) p[i] = __uint_as_float(static_cast<uint32_t>(at[ch < a.half ? ch + a.half : ch - a.half]) << 16);
+    for (int i = 0; i < 4; ++i) {
+      float v[2] = {0.0f, 0.0f};
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int ch = lane * 8 + 2 * i + e;
+        if (ch < 2 * a.half)
+          v[e] = __uint_as_float(static_cast<uint32_t>(at[ch < a.half ? ch + a.half : ch - a.half]) << 16);
+      }
+      p[i] = two(v[0], v[1]);
     }
     __syncwarp(lanes);  // read before any lane writes the row's place (which may be the row)
   }
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
   uint32_t o[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float lo = __fmaf_rn(v[2 * i], t.c[2 * i], p[2 * i] * t.s[2 * i]);
-    const float hi = __fmaf_rn(v[2 * i + 1], t.c[2 * i + 1], p[2 * i + 1] * t.s[2 * i + 1]);
-    const uint32_t both = bf16_pair(lo, hi);
-    const uint32_t mask = ((t.on >> (2 * i)) & 1u ? 0xffffu : 0u) | ((t.on >> (2 * i + 1)) & 1u ? 0xffff0000u : 0u);
-    o[i] = (both & mask) | (w[i] & ~mask);
+    float lo, hi;
+    split(fma_2(two(bf16_lo(w[i]), bf16_hi(w[i])), t.c[i], mul_2(p[i], t.s[i])), lo, hi);
+    o[i] = bf16_pair(lo, hi);
+    if (kOdd) {
+      const uint32_t mask = ((t.on >> (2 * i)) & 1u ? 0xffffu : 0u) | ((t.on >> (2 * i + 1)) & 1u ? 0xffff0000u : 0u);
+      o[i] = (o[i] & mask) | (w[i] & ~mask);
+    } else if (t.on == 0) {
+      o[i] = w[i];
+    }
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
@@ -118,14 +134,16 @@ __device__ __forceinline__ uint4 turned(const StepArgs& a, const Turn& t, const 
 // the chunk's tokens are computed once, in shared memory; then 16 lanes take a
 // token's rows of all heads, whose turns stay in registers.  Rows of 8 bits: 16
 // lanes per slot of the block, those that hold rows from before among them.
-template <int kFormat, bool kRope, bool kAny>
-__global__ void __launch_bounds__(kThreads) step_kernel(const StepArgs a) {
+template <int kFormat, bool kRope, bool kOdd>
+__global__ void __launch_bounds__(kThreads, kOdd ? 2 : !kRope ? 5 : kFormat == SS_CACHE_FP8 || kFormat == SS_CACHE_INT4 ? 3 : 4) step_kernel(const StepArgs a) {
   constexpr bool kBlocks = kFormat == SS_CACHE_FP8;
   constexpr int kEach = 4;
   __shared__ __align__(16) float s_cos[kRope ? kGroups : 1][kPairs], s_sin[kRope ? kGroups : 1][kPairs];
-  __shared__ int32_t s_up[kRope ? SS_TREE_MAX_NODES : 1], s_depth[kRope ? SS_TREE_MAX_NODES : 1];
-  __shared__ uint32_t s_top[3][2 * kEach];
+  __shared__ int32_t s_depth[kRope ? SS_TREE_MAX_NODES : 1];
+  __shared__ __align__(16) uint32_t s_top[3][2 * kEach];
+  __shared__ uint64_t s_turns[kRope ? kPairs : 1];
   const int tid = threadIdx.x, r = blockIdx.y;
+  if (kRope && tid < a.half) s_turns[tid] = a.turns[tid];
   const int32_t begin = a.offsets ? a.offsets[r] : r;
   const int32_t stop = a.offsets ? a.offsets[r + 1] : r + 1;
   const int32_t base = a.kv_len ? a.kv_len[r] : 0;
@@ -162,34 +180,67 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const StepArgs a) {
   const uint32_t lanes = 0xffffu << (tid & 16);
   const bool live = lane * 8 < a.dim;
   if (kBlocks && tid < 3 * 2 * kEach) (&s_top[0][0])[tid] = 0;
+  // rows by themselves (below): 16 lanes have a token's rows first, first + step, ..
+  const int per = kGroups / tokens;  // groups of 16 lanes per token
+  const int token = group % tokens, first = group / tokens < per ? group / tokens + per * blockIdx.z : 0x3fffffff;
+  const int32_t heads = !kRope ? 0 : a.q_heads + (kBlocks ? 0 : kFormat == kNone ? a.kv_heads : 2 * a.kv_heads);
+  const int64_t at_row = static_cast<int64_t>(begin) + t0 + token;
+  const uint8_t* of_q = a.q + at_row * a.q_token + lane * 16;
+  const uint8_t* of_k = a.k + at_row * a.k_token + lane * 16 - a.q_heads * a.k_head;
+  const uint8_t* of_v = a.v + at_row * a.k_token + lane * 16 - (a.q_heads + a.kv_heads) * a.k_head;
+  const int32_t step = per * gridDim.z;
+  const auto source = [&](int32_t h) {
+    return (h < a.q_heads ? of_q : h < a.q_heads + a.kv_heads || kFormat == kNone ? of_k : of_v) +
+           h * (h < a.q_heads ? a.q_head : a.k_head);
+  };
+  uint4 x[kEach];
+  const auto load = [&](int32_t h0) {
+#pragma unroll
+    for (int e = 0; e < kEach; ++e)
+      if (h0 + e * step < heads && live) x[e] = *reinterpret_cast<const uint4*>(source(h0 + e * step));
+  };
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) x[e] = make_uint4(0u, 0u, 0u, 0u);
+  // 8 bits: the block's page
+  const int64_t first_slot = base + from;
+  const int32_t block_page = kBlocks ? page_of(a.t, a.c, row, first_slot) : -1;  // a block lies in one page
   if constexpr (kRope) {
-    if (tree) {  // depths by jumps of 1, 2, 4 .. parents
-      if (tid < SS_TREE_MAX_NODES) {
-        const int32_t p = tid > 0 && tid < n ? a.parents[begin + tid] : 0;
-        s_up[tid] = p < 0 || p >= tid ? 0 : p;
-        s_depth[tid] = tid > 0;
-      }
-#pragma unroll 1
-      for (int i = 0; i < 6; ++i) {
-        __syncthreads();
-        int32_t up = 0, depth = 0;
-        if (tid < SS_TREE_MAX_NODES) {
-          up = s_up[s_up[tid]];
-          depth = s_depth[tid] + s_depth[s_up[tid]];
+    load(first);  // on their way while the angles are computed
+    if (tree) {  // depths by jumps of 1, 2, 4 .. parents: a warp, nodes i and i + 32 in lane i
+      if (tid < 32) {
+        int32_t up[2], depth[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int32_t node = tid + 32 * h, p = node > 0 && node < n ? a.parents[begin + node] : 0;
+          up[h] = p < 0 || p >= node ? 0 : p;
+          depth[h] = node > 0;
         }
-        __syncthreads();
-        if (tid < SS_TREE_MAX_NODES) {
-          s_up[tid] = up;
-          s_depth[tid] = depth;
+#pragma unroll
+        for (int i = 0; i < 6; ++i) {
+          int32_t far[2], more[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int32_t u0 = __shfl_sync(0xffffffffu, up[0], up[h] & 31), u1 = __shfl_sync(0xffffffffu, up[1], up[h] & 31);
+            const int32_t d0 = __shfl_sync(0xffffffffu, depth[0], up[h] & 31), d1 = __shfl_sync(0xffffffffu, depth[1], up[h] & 31);
+            far[h] = up[h] < 32 ? u0 : u1;
+            more[h] = up[h] < 32 ? d0 : d1;
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            up[h] = far[h];
+            depth[h] += more[h];
+          }
         }
+        s_depth[tid] = depth[0];
+        s_depth[tid + 32] = depth[1];
       }
-      __syncthreads();
     }
+    __syncthreads();
     for (int i = tid; i < tokens * a.half; i += kThreads) {
       const int token = i / a.half, pair = i - token * a.half;
       const int64_t at = a.positions ? a.positions[begin + t0 + token]
                                      : static_cast<int64_t>(base) + (tree ? s_depth[t0 + token] : t0 + token);
-      const uint64_t turn = static_cast<uint64_t>(at) * a.turns[pair];
+      const uint64_t turn = static_cast<uint64_t>(at) * s_turns[pair];
       float s, c;
       sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 4.656612873077393e-10f, &s, &c);
       s_cos[token][pair] = a.magnitude * c;
@@ -200,40 +251,23 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const StepArgs a) {
 
   // ---- rows by themselves: queries, and keys and values but in 8 bits
   if constexpr (kRope) {
-    const int per = kGroups / tokens;  // groups of 16 lanes per token
-    const int token = group % tokens, first = group / tokens;
-    const int32_t heads = a.q_heads + (kBlocks ? 0 : kFormat == kNone ? a.kv_heads : 2 * a.kv_heads);
-    if (first < per) {
-      const Turn t = turn_of<kAny>(a, s_cos[token], s_sin[token], lane);
-      const int64_t at = static_cast<int64_t>(begin) + t0 + token;
+    if (first < heads) {
+      const Turn t = turn_of(a, s_cos[token], s_sin[token], lane);
       int32_t page = -1, in_page = 0;
       if (kFormat != kNone && !kBlocks) {
         const int64_t slot = static_cast<int64_t>(base) + t0 + token;
         page = page_of(a.t, a.c, row, slot);
         in_page = static_cast<int32_t>(slot) & ((1 << a.c.page_shift) - 1);
       }
-      const auto source = [&](int32_t h) {
-        const int32_t k = h - a.q_heads, v = k - a.kv_heads;
-        return k < 0 ? a.q + at * a.q_token + h * a.q_head
-                     : (v < 0 ? a.k + k * a.k_head : a.v + v * a.k_head) + at * a.k_token;
-      };
-      const int32_t step = per * gridDim.z;
-      for (int32_t h0 = first + per * blockIdx.z; h0 < heads; h0 += step * kEach) {
-        uint4 x[kEach];
-#pragma unroll
-        for (int e = 0; e < kEach; ++e) {
-          const int32_t h = h0 + e * step;
-          x[e] = make_uint4(0u, 0u, 0u, 0u);
-          if (h < heads && live) x[e] = *reinterpret_cast<const uint4*>(source(h) + lane * 16);
-        }
+      for (int32_t h0 = first;;) {
 #pragma unroll
         for (int e = 0; e < kEach; ++e) {
           const int32_t h = h0 + e * step, k = h - a.q_heads, v = k - a.kv_heads;
           if (h >= heads) break;
-          const uint4 y = v < 0 ? turned<kAny>(a, t, x[e], source(h), lane, lanes) : x[e];
+          const uint4 y = v < 0 ? turned<kOdd>(a, t, x[e], source(h) - lane * 16, lane, lanes) : x[e];
           if (k < 0 || kFormat == kNone) {
-            uint8_t* to = k < 0 ? a.q_out + at * a.q_out_token + h * a.q_out_head
-                                : a.k_out + at * a.k_out_token + k * a.k_out_head;
+            uint8_t* to = k < 0 ? a.q_out + at_row * a.q_out_token + h * a.q_out_head
+                                : a.k_out + at_row * a.k_out_token + k * a.k_out_head;
             if (live) *reinterpret_cast<uint4*>(to + lane * 16) = y;
             continue;
           }
@@ -254,71 +288,100 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const StepArgs a) {
             }
           }
         }
+        h0 += step * kEach;
+        if (h0 >= heads) break;
+        load(h0);
       }
     }
   }
 
-  // ---- a block of 8 bits: 16 lanes per slot, kEach heads of K or V at a time
+  // ---- a block of 8 bits: 16 lanes per slot, kEach heads of K or V at a time.
+  // Bound by instructions: what a batch of heads shares is computed once, the
+  // maxima of its heads leave a warp together.
   if constexpr (kBlocks) {
-    const int64_t first_slot = base + from;
-    const int32_t page = page_of(a.t, a.c, row, first_slot);  // a block lies in one page
+    const int32_t page = block_page;
     if (page < 0) return;
     const int slot = group & (size - 1), side = group >> a.chunk_shift, sides = kGroups >> a.chunk_shift;
     const int64_t i = from + slot;  // the slot's token
     const bool fresh = i >= t0 && i < t1, kept = i < 0;
-    const int64_t at = static_cast<int64_t>(begin) + (fresh ? i : 0);
     const int32_t in_page = static_cast<int32_t>(first_slot) & ((1 << a.c.page_shift) - 1);
-    const int64_t cell = page * a.c.page_stride + (in_page + slot) * a.c.slot_stride + lane * 8;
-    const int64_t scale = page * a.c.s_page_stride + (in_page >> a.chunk_shift) * 4;
+    const int64_t in_flat = (static_cast<int64_t>(begin) + (fresh ? i : 0)) * a.k_token + lane * 16;
+    const int64_t in_cell = page * a.c.page_stride + (in_page + slot) * a.c.slot_stride + lane * 8;
+    const int64_t in_scale = page * a.c.s_page_stride + (in_page >> a.chunk_shift) * 4;
     Turn t;
-    if constexpr (kRope) t = turn_of<kAny>(a, s_cos[fresh ? i - t0 : 0], s_sin[fresh ? i - t0 : 0], lane);
-    const int32_t units = 2 * a.kv_heads, batch = sides * kEach, step = batch * gridDim.z;
+    if constexpr (kRope) t = turn_of(a, s_cos[fresh ? i - t0 : 0], s_sin[fresh ? i - t0 : 0], lane);
+    const int32_t batch = sides * kEach, batches = (a.kv_heads + batch - 1) / batch;  // of K, and of V
     int turn = 0;
-    for (int32_t u0 = blockIdx.z * batch; u0 < units; u0 += step, turn = turn == 2 ? 0 : turn + 1) {
-      uint4 x[kEach];
+    for (int32_t n0 = blockIdx.z; n0 < 2 * batches; n0 += gridDim.z, turn = turn == 2 ? 0 : turn + 1) {
+      const bool is_v = n0 >= batches;
+      const int32_t head0 = (is_v ? n0 - batches : n0) * batch + side * kEach, more = a.kv_heads - head0;  // heads left
+      const uint8_t* src = (is_v ? a.v : a.k) + in_flat + head0 * a.k_head;
+      uint8_t* cell = (is_v ? a.c.v : a.c.k) + in_cell + head0 * a.c.head_stride;
+      float* scale = reinterpret_cast<float*>((is_v ? a.c.vs : a.c.ks) + in_scale + head0 * a.c.s_head_stride);
+      const auto scale_of = [&](int e) {
+        return reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(scale) + e * a.c.s_head_stride);
+      };
       float old[kEach];
 #pragma unroll
       for (int e = 0; e < kEach; ++e) {
-        const int32_t u = u0 + side * kEach + e, head = u < a.kv_heads ? u : u - a.kv_heads;
         x[e] = make_uint4(0u, 0u, 0u, 0u);
         old[e] = 0.0f;
-        if (u >= units || !live) continue;
+        if (e >= more || !live) continue;
         if (fresh) {
-          x[e] = *reinterpret_cast<const uint4*>((u < a.kv_heads ? a.k : a.v) + at * a.k_token + head * a.k_head + lane * 16);
+          x[e] = *reinterpret_cast<const uint4*>(src + e * a.k_head);
         } else if (kept) {
-          const uint2 w = *reinterpret_cast<const uint2*>((u < a.kv_heads ? a.c.k : a.c.v) + cell + head * a.c.head_stride);
+          const uint2 w = *reinterpret_cast<const uint2*>(cell + e * a.c.head_stride);
           x[e].x = w.x;
           x[e].y = w.y;
-          old[e] = *reinterpret_cast<const float*>((u < a.kv_heads ? a.c.ks : a.c.vs) + scale + head * a.c.s_head_stride);
+          old[e] = *scale_of(e);
         }
       }
-      const auto values = [&](int e, float (&f)[8]) {
-        if (kept) decode8(make_uint2(x[e].x, x[e].y), old[e], f);
-        else floats_of(x[e], f);
-      };
+      uint32_t mine = 0;
+      bool odd = false;  // a value is not finite
 #pragma unroll
       for (int e = 0; e < kEach; ++e) {
-        const int32_t u = u0 + side * kEach + e;
         if constexpr (kRope)
-          if (fresh && u < a.kv_heads)
-            x[e] = turned<kAny>(a, t, x[e], a.k + at * a.k_token + u * a.k_head, lane, lanes);
-        float f[8];
-        values(e, f);
+          if (fresh && !is_v && e < more) x[e] = turned<kOdd>(a, t, x[e], src - lane * 16 + e * a.k_head, lane, lanes);
+        uint32_t top;
+        if (kept) {
+          float f[8];
+          decode8(make_uint2(x[e].x, x[e].y), old[e], f);
+          top = __float_as_uint(finite_top(f));
+        } else {
+          top = magnitude(x[e]);
+          if (__builtin_expect(top >= 0x7f80u, 0)) {
+            float f[8];
+            floats_of(x[e], f);
+            top = __float_as_uint(finite_top(f)) >> 16;
+            odd = true;
+          }
+          top <<= 16;
+        }
         __syncwarp();
-        const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(finite_top(f)));
-        if ((tid & 31) == 0 && top != 0) atomicMax(&s_top[turn][side * kEach + e], top);
+        top = __reduce_max_sync(0xffffffffu, top);
+        if ((tid & 31) == e) mine = top;
       }
+      if ((tid & 31) < kEach && mine != 0) atomicMax(&s_top[turn][side * kEach + (tid & 31)], mine);
       __syncthreads();
+      const uint4 tops = *reinterpret_cast<const uint4*>(&s_top[turn][side * kEach]);
+      if (fresh || kept) {
+        const uint32_t top[kEach] = {tops.x, tops.y, tops.z, tops.w};
 #pragma unroll
-      for (int e = 0; e < kEach; ++e) {
-        const int32_t u = u0 + side * kEach + e, head = u < a.kv_heads ? u : u - a.kv_heads;
-        if (u >= units || !(fresh || kept)) continue;
-        const Scale8 to = scale8(__uint_as_float(s_top[turn][side * kEach + e]));
-        float f[8];
-        values(e, f);
-        if (live) *reinterpret_cast<uint2*>((u < a.kv_heads ? a.c.k : a.c.v) + cell + head * a.c.head_stride) = encode8(f, to.inv);
-        if (lane == 0 && i == t1 - 1)
-          *reinterpret_cast<float*>((u < a.kv_heads ? a.c.ks : a.c.vs) + scale + head * a.c.s_head_stride) = to.s;
+        for (int e = 0; e < kEach; ++e) {
+          if (e >= more) break;
+          const Scale8 to = scale8(__uint_as_float(top[e]));
+          uint2 w;
+          if (kept || odd) {
+            float f[8];
+            if (kept) decode8(make_uint2(x[e].x, x[e].y), old[e], f);
+            else floats_of(x[e], f);
+            w = encode8(f, to.inv);
+          } else {
+            w = encode8(x[e], to.inv);
+          }
+          if (live) *reinterpret_cast<uint2*>(cell + e * a.c.head_stride) = w;
+          if (lane == 0 && i == t1 - 1) *scale_of(e) = to.s;
+        }
       }
       // the batch before's maxima were read before this batch's barrier; they are needed again in two batches
       if (tid < 2 * kEach) s_top[turn == 0 ? 2 : turn - 1][tid] = 0;
@@ -346,10 +409,10 @@ static void take_rope(StepArgs* a, const ss_rope_table* t) {
   a->magnitude = t->magnitude;
 }
 
-// As many CTAs per chunk as there are SMs to spare, up to one for every four
-// heads of K or V (or rows by themselves).
+// As many CTAs per chunk as the GPU has room for, up to one for every four rows
+// of a token.
 static unsigned splits(int64_t chunks, int64_t rows) {
-  const int64_t spare = (2 * 152 + chunks - 1) / chunks, most = rows < 4 ? 1 : rows / 4;
+  const int64_t spare = (4 * 152 + chunks - 1) / chunks, most = rows < 4 ? 1 : rows / 4;
   const int64_t z = spare < most ? spare : most;
   return static_cast<unsigned>(z < 1 ? 1 : z > 64 ? 64 : z);
 }
@@ -359,10 +422,10 @@ static ss_status launch_step(const StepArgs& a, int32_t num_requests, cudaStream
   const int64_t size = 1ll << a.chunk_shift;
   // n tokens touch at most ceil((n + size - 1) / size) blocks of slots
   const int64_t x = kFormat == kNone ? (a.max_tokens + size - 1) / size : (a.max_tokens + 2 * size - 2) / size;
-  const int64_t rows = kFormat == SS_CACHE_FP8 ? 2ll * a.kv_heads : a.q_heads + 2ll * a.kv_heads;
+  const int64_t rows = a.q_heads + (kFormat == kNone ? 1ll : 2ll) * a.kv_heads;
   const dim3 grid(static_cast<unsigned>(x < 1 ? 1 : x), num_requests, splits((x < 1 ? 1 : x) * num_requests, rows));
   if constexpr (kRope) {
-    if (a.layout == SS_ROPE_HALVES && a.half % 8 != 0) {
+    if (a.half % (a.layout == SS_ROPE_HALVES ? 8 : 4) != 0) {
       step_kernel<kFormat, true, true><<<grid, kThreads, 0, s>>>(a);
       return finish(cudaSuccess);
     }

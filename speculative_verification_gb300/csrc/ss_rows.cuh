@@ -151,6 +151,13 @@ __device__ __forceinline__ void decode8(uint2 w, float s, float (&x)[8]) {
   }
 }
 
+// The largest magnitude of eight bf16 values, as bits (0x7f80 and up: one is not
+// finite): magnitudes compare as integers, in pairs.
+__device__ __forceinline__ uint32_t magnitude(const uint4& x) {
+  const uint32_t m = __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu), __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
+  return max(m & 0xffffu, m >> 16);
+}
+
 __device__ __forceinline__ void floats_of(const uint4& w, float (&x)[8]) {
   const uint32_t v[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -158,6 +165,22 @@ __device__ __forceinline__ void floats_of(const uint4& w, float (&x)[8]) {
     x[2 * i] = bf16_lo(v[i]);
     x[2 * i + 1] = bf16_hi(v[i]);
   }
+}
+
+// Finite bf16 values.
+__device__ __forceinline__ uint2 encode8(const uint4& x, float inv) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  const uint64_t inv2 = two(inv, inv);
+  uint32_t o[2] = {0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a, b;
+    split(mul_2(two(bf16_lo(w[i]), bf16_hi(w[i])), inv2), a, b);
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+    o[i >> 1] |= static_cast<uint32_t>(r) << (16 * (i & 1));
+  }
+  return make_uint2(o[0], o[1]);
 }
 
 }  // namespace ssc

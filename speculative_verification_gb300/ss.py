@@ -863,16 +863,19 @@ _LAYOUTS = {"halves": 0, "interleaved": 1}
 _SCALINGS = {None: 0, "linear": 1, "by_parts": 2}
 
 
-def _turned(torch, name, x, out, dim, dev):
+def _turned(bf16, name, x, out, dim, dev):
     """Pointers, strides and heads of an array and of where it goes turned."""
     if x is None and out is None:
-        return 0, 0, 0, 0, 0, 0, 0, 0
-    if x is None or out is None or x.dtype is not torch.bfloat16 or out.dtype is not torch.bfloat16 or \
-            x.get_device() != dev or out.get_device() != dev or x.dim() != 3 or out.shape != x.shape or \
-            x.shape[2] != dim or x.stride(2) != 1 or out.stride(2) != 1:
-        raise SSError("want %s and %s_out as [tokens, heads, %d] bf16 tensors with contiguous rows on cuda:%d"
-                      % (name, name, dim, dev))
-    return (x.data_ptr(), out.data_ptr(), x.stride(0), x.stride(1), out.stride(0), out.stride(1), x.shape[1], x.shape[0])
+        return (0, 0, 0, 0, 0, 0), 0, None
+    if x is not None and out is not None and x.dtype is bf16 and out.dtype is bf16 and x.get_device() == dev and \
+            out.get_device() == dev:
+        shape, (token, head, one) = x.shape, x.stride() if len(x.shape) == 3 else (0, 0, 0)
+        if one == 1 and shape[2] == dim and out.shape == shape:
+            token_out, head_out, one = out.stride()
+            if one == 1:
+                return (x.data_ptr(), out.data_ptr(), token, head, token_out, head_out), shape[1], shape[0]
+    raise SSError("want %s and %s_out as [tokens, heads, %d] bf16 tensors with contiguous rows on cuda:%d"
+                  % (name, name, dim, dev))
 
 
 def ss_rope(rope, q, q_out, k, k_out, kv_len, status, *, token_offsets=None, max_tokens=None, parents=None,
@@ -882,20 +885,21 @@ def ss_rope(rope, q, q_out, k, k_out, kv_len, status, *, token_offsets=None, max
     parents its depth in the request's draft tree, or positions [tokens].  q_out
     and k_out may be q and k; q and q_out, or k and k_out, may be None."""
     import torch
-    i32, n, dev = torch.int32, status.numel(), rope.device
+    i32, bf16, n, dev, dim = torch.int32, torch.bfloat16, status.numel(), rope.device, rope.head_dim
     handle = _raw_stream(torch, stream, dev)
-    qs, ks = (_turned(torch, *x, rope.head_dim, dev) for x in (("q", q, q_out), ("k", k, k_out)))
-    total = qs[7] if q is not None else ks[7]
-    if q is not None and k is not None and qs[7] != ks[7]:
+    qs, heads, total = _turned(bf16, "q", q, q_out, dim, dev)
+    ks, kv_heads, tokens = _turned(bf16, "k", k, k_out, dim, dev)
+    if total is None:
+        total = tokens or 0
+    elif tokens is not None and tokens != total:
         raise SSError("want as many tokens of k as of q")
-    buf = C.create_string_buffer(_ROPE.size)
-    _ROPE.pack_into(buf, 0, rope.address, n, 1 if max_tokens is None else max_tokens, total, rope.head_dim,
-                    0 if token_offsets is None else _want(token_offsets, dev, "token_offsets", i32, (n + 1,)),
-                    0 if kv_len is None else _want(kv_len, dev, "kv_len", i32, (n,)),
-                    0 if parents is None else _want(parents, dev, "parents", i32, (total,)),
-                    0 if positions is None else _want(positions, dev, "positions", i32, (total,)),
-                    qs[6], ks[6], *qs[:6], *ks[:6], _want(status, dev, "status", i32))
-    _check(_quick_call("ss_rope", [C.c_char_p, C.c_void_p])(buf, handle))
+    args = _ROPE.pack(rope.address, n, 1 if max_tokens is None else max_tokens, total, dim,
+                      0 if token_offsets is None else _want(token_offsets, dev, "token_offsets", i32, (n + 1,)),
+                      0 if kv_len is None else _want(kv_len, dev, "kv_len", i32, (n,)),
+                      0 if parents is None else _want(parents, dev, "parents", i32, (total,)),
+                      0 if positions is None else _want(positions, dev, "positions", i32, (total,)),
+                      heads, kv_heads, *qs, *ks, _want(status, dev, "status", i32))
+    _check(_quick_call("ss_rope", [C.c_char_p, C.c_void_p])(args, handle))
 
 
 def ss_rope_append(rope, cache, layer, q, q_out, k, v, page_table, kv_len, status, *, token_offsets=None,
@@ -908,15 +912,16 @@ def ss_rope_append(rope, cache, layer, q, q_out, k, v, page_table, kv_len, statu
     handle = _raw_stream(torch, stream, dev)
     if rope.device != dev or rope.head_dim != cache.head_dim:
         raise SSError("rope: want a Rope for the cache's heads of %d channels on its device" % cache.head_dim)
-    qs, total = _turned(torch, "q", q, q_out, cache.head_dim, dev), k.shape[0]
-    if q is not None and qs[7] != total:
+    qs, heads, tokens = _turned(torch.bfloat16, "q", q, q_out, cache.head_dim, dev)
+    total = k.shape[0]
+    if tokens is not None and tokens != total:
         raise SSError("want as many tokens of k as of q")
     at = _ROPE_APPEND.size
     buf, table = _with_table(_BOTH, page_table, cache, i32)
     _pack_rows(torch, buf, at, table, cache, layer, k, v, kv_len, status, token_offsets, max_tokens, table_rows)
     _ROPE_APPEND.pack_into(buf, 0, rope.address, C.addressof(buf) + at,
                            0 if parents is None else _want(parents, dev, "parents", i32, (total,)),
-                           0 if positions is None else _want(positions, dev, "positions", i32, (total,)), qs[6], *qs[:6])
+                           0 if positions is None else _want(positions, dev, "positions", i32, (total,)), heads, *qs)
     _check(_quick_call("ss_rope_append", [C.c_char_p, C.c_void_p])(buf, handle))
 
 
