@@ -6,7 +6,8 @@ each.  The prompt is cached once and its pages are shared by the
 continuations (ss_pages_fork); every step then
 
   ss_pages_reserve      pages for the draft tree's tokens
-  per layer             ss_cache_append, ss_cache_attention (tree mask, window)
+  per layer             ss_cache_append, or with rotary positions ss_rope_append,
+                        and ss_cache_attention (tree mask, window)
   ss_tree_verify        the accepted path and one token of the target's
   ss_commit_accepted    the emitted tokens into the token buffer
   ss_pages_compact      the accepted nodes' rows next to each other
@@ -15,7 +16,7 @@ continuations (ss_pages_fork); every step then
 without a device-to-host copy in the loop.  The drafts are uniform random
 tokens (their q says so), so the verified text follows the target model.
 
-    python examples/tree_decode.py [--format bf16|int4] [--steps N]
+    python examples/tree_decode.py [--format bf16|int4|fp8] [--rotary] [--steps N]
 """
 import argparse
 import os
@@ -30,7 +31,8 @@ from speculative_verification_gb300 import ss  # noqa: E402
 class Decoder:
     """Attention layers without an MLP: as much of a model as the calls need."""
 
-    def __init__(self, vocab=512, layers=3, heads=8, kv_heads=2, dim=64, positions=2048, window=96, sinks=4, seed=0):
+    def __init__(self, vocab=512, layers=3, heads=8, kv_heads=2, dim=64, positions=2048, window=96, sinks=4, seed=0,
+                 rotary=False):
         g = torch.Generator().manual_seed(seed)
 
         def weight(*shape, scale):
@@ -44,9 +46,12 @@ class Decoder:
         self.qkv = [weight(width, (heads + 2 * kv_heads) * dim, scale=width ** -0.5) for _ in range(layers)]
         self.out = [weight(width, width, scale=width ** -0.5) for _ in range(layers)]
         self.head = weight(width, vocab, scale=2.0 * width ** -0.5)
+        # positions learned and added, or three quarters of each head turned by them
+        self.rope = ss.Rope(dim, rot_dim=dim * 3 // 4, layout="interleaved") if rotary else None
 
     def embedded(self, tokens, positions):
-        return self.embed[tokens.long()] + self.place[positions.long()]
+        x = self.embed[tokens.long()]
+        return x if self.rope else x + self.place[positions.long()]
 
     def project(self, layer, x):
         """The queries, keys and values of a layer."""
@@ -58,8 +63,12 @@ class Decoder:
         x = self.embedded(tokens, positions)
         for layer in range(self.layers):
             q, k, v = self.project(layer, x)
-            ss.ss_cache_append(cache, layer, k, v, pool.page_table, kv_len, status, token_offsets=offsets,
-                               max_tokens=most, table_rows=attention.get("table_rows"))
+            rows = dict(token_offsets=offsets, max_tokens=most, table_rows=attention.get("table_rows"))
+            if self.rope:  # (the queries in place: the tree gives each node its depth)
+                ss.ss_rope_append(self.rope, cache, layer, q, q, k, v, pool.page_table, kv_len, status,
+                                  parents=attention.get("parents"), **rows)
+            else:
+                ss.ss_cache_append(cache, layer, k, v, pool.page_table, kv_len, status, **rows)
             o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
             ss.ss_cache_attention(cache, layer, q, o, pool.page_table, kv_len, workspace, status, query_offsets=offsets,
                                   max_queries=most, window=self.window, sinks=self.sinks, **attention)
@@ -157,12 +166,13 @@ def decode(model, prompts, samples=2, steps=6, nodes=12, page=16, format="bf16",
 
 def main():
     ap = argparse.ArgumentParser(description=__doc__.split("\n\n")[0])
-    ap.add_argument("--format", default="bf16", choices=("bf16", "int4"))
+    ap.add_argument("--format", default="bf16", choices=("bf16", "int4", "fp8"))
+    ap.add_argument("--rotary", action="store_true")
     ap.add_argument("--steps", type=int, default=6)
     args = ap.parse_args()
     g = torch.Generator().manual_seed(5)
     prompts = [torch.randint(512, (m,), generator=g).tolist() for m in (7, 150, 64)]
-    texts, lengths, _, pool, bad = decode(Decoder(), prompts, steps=args.steps, format=args.format)
+    texts, lengths, _, pool, bad = decode(Decoder(rotary=args.rotary), prompts, steps=args.steps, format=args.format)
     for i, t in enumerate(texts):
         m = len(prompts[i // 2])
         print("prompt %d, continuation %d: %d tokens in %d steps: %s" % (i // 2, i % 2, len(t) - m, args.steps, t[m:]))

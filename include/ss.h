@@ -647,7 +647,7 @@ ss_status ss_cache_read(const ss_append_args* args, ss_stream_t stream);
  * Sums and softmax statistics are held in fp32; the weights are rounded to
  * bf16 (4 and 8 bits: to f16, in which those 2^22 and more below the query's
  * largest lose bits and those 2^33 below it are 0) before they meet the values.
- * (4 and 8 bits: queries' channels below 2^-15 of the row's largest lose bits.)
+ * Queries meet 4- and 8-bit keys to 2^-21 of a row's largest channel at least.
  * Results are right for values up to 2^110 over the query's number of keys
  * (4 and 8 bits: 2^100) in magnitude; values below 2^-80 may count as 0.  The result
  * does not depend on timing: the work is split over the SMs by the lengths

@@ -165,15 +165,17 @@ struct Cfg {
   static constexpr bool kNibbles = kPacked && !kBytes;
   static constexpr int kN = kLive < 16 ? 16 : kLive;
   // 8 bits, from 32 rows on: one column per row, both parts of the queries summed
-  // into it (below, twice the MMAs would be what a tile costs)
+  // into it by twice the MMAs, which spares the softmax the sum (48 x 1-8 drafts
+  // 289 -> 257 us, with the queries' conversion below).  Fewer rows are bound by the copies.
   static constexpr bool kOneCol = kBytes && kLive >= 32;
   static constexpr int kNS = kPacked && !kOneCol ? 2 * kLive : kN;
   static constexpr int kGroups = kLive <= 16 ? 1 : kLive == 32 || kNibbles ? 2 : 4;  // softmax warpgroups of a tile
   static constexpr int kCols = kLive / kGroups;              // rows per softmax thread
-  // 4 bits, few rows, and 8 bits: two sets of warpgroups take turns at the tiles,
-  // each with a sum and an accumulator of its own, joined at the item's end.  What
-  // a tile asks of one is mostly latency (1300 clocks for few rows of 4 bits, where
-  // copying it takes 750; 8 bits, 64 rows: @@).
+  // 4 and 8 bits, few rows: two sets of warpgroups take turns at the tiles, each
+  // with a sum and an accumulator of its own, joined at the item's end.  What a
+  // tile asks of one is mostly latency then (4 bits: 1300 clocks, where copying it
+  // takes 750).  8 bits, 64 rows: two sets of two spill their registers (394 us, 48 x
+  // 1-8 drafts; four warpgroups on one tile 248).
   static constexpr int kStreams = kPacked && kLive <= (kBytes ? 32 : 16) ? 2 : 1;
   static constexpr int kSoft = 128 * kGroups * kStreams;
   static constexpr int kPerTile = kSoft / kStreams;          // softmax threads of one tile
@@ -182,12 +184,12 @@ struct Cfg {
   static constexpr int kVGroups = kLive <= 16 ? 2 : 1;
   static constexpr int kUnpack = kPacked ? 128 * (kNibbles + kVGroups) : 0;
   // ... and from there on the softmax warps convert the next item's queries at the
-  // end of one (a prompt's items are short: one warp takes longer for 64 rows than
-  // all of their tiles)
+  // end of one: a prompt's items are short, and one warp takes longer for 64 rows
+  // than all of their tiles (2 x 4096 prompt 1138 -> 680 us)
   static constexpr bool kConv = kBytes && kLive >= 32;
   // What an item costs beyond its tiles, in tiles: with it the line is cut into
-  // parts that take equally long (4.2 us an item, 1.4 a tile: 2 x 4096 prompt, where
-  // CTAs had 25 to 60 items, @@)
+  // parts that take equally long (4.2 us an item, 1.4 a tile; 2 x 4096 prompt, where
+  // CTAs had 25 to 60 items: 583 -> 525 us; 2 instead of 3: 540)
   static constexpr int kExtra = kConv ? 3 : 0;
   static constexpr int kThreads = 128 + kSoft + kUnpack;
   // Registers per thread by warpgroup where one size does not fit all: the
@@ -979,6 +981,8 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves, kBytes>::kThreads
     int32_t at = 0, k = 0;  // tile, item
     bool ok = true;
     int32_t k_tiles = 0, v_tiles = 0;  // issued
+    uint32_t kslot = 0, kphase = 0, rslot = 0, rphase = 0;  // 8 bits: the next tile's slots
+    const uint32_t scales_a = kBytes ? smem_addr(&scales[0][kBytes ? lane : 0]) : 0;
     const auto wait = [&](uint64_t* bar, int32_t use) {
       if (ok) ok = __all_sync(0xffffffffu, wait_or_dead(bar, use & 1, dead));
     };
@@ -992,6 +996,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves, kBytes>::kThreads
       const int32_t tiles = same(it.tiles), tile0 = same(it.tile0), nsink = same(it.nsink), sink_end = same(it.sink_end);
       if (F::kExtra && tiles == 0) break;
       const int32_t origin = same(it.origin), end = same(it.end), head = same(it.head);
+      const uint8_t* scale_at = kBytes ? (lane < 16 ? a.c.ks : a.c.vs) + head * a.c.s_head_stride : nullptr;
       const int32_t* row = it.row;
       // 64 entries of the page table from the next tile's on, two per lane,
       // loaded a tile or more before their use: a load per tile, waited for,
@@ -1032,7 +1037,44 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves, kBytes>::kThreads
                      page < 0 ? a.c.num_pages : page, bar);
           }
         };
-        if constexpr (kBytes) {
+        if constexpr (kBytes && !F::kConv) {
+          // This warp's own work is what a tile of few rows costs beside its
+          // bytes: one wait for both slots, one block of copies (32 x 1 token over
+          // 8-64k 381 -> 370 us; 64 rows, with fewer slots, are no faster with it).
+          const int32_t p = __shfl_sync(0xffffffffu, page, (8 * (lane & 15)) >> unit_shift);
+          const int32_t slot = u & ((1 << a.c.page_shift) - 1), to = page < 0 ? a.c.num_pages : page;  // filled with zeros
+          const int32_t block = ((j0 + 8 * (lane & 15)) & ((1 << a.c.page_shift) - 1)) >> a.c.block_shift;
+          const uint8_t* from = scale_at + max(p, 0) * a.c.s_page_stride + block * 4;
+          const bool free = mbar_try_wait(kempty + kslot, kphase ^ 1u) & mbar_try_wait(rempty + rslot, rphase ^ 1u);
+          if (__builtin_expect(!__all_sync(0xffffffffu, free), 0)) {
+            if (ok) ok = __all_sync(0xffffffffu, wait_or_dead(kempty + kslot, kphase ^ 1u, dead));
+            if (ok) ok = __all_sync(0xffffffffu, wait_or_dead(rempty + rslot, rphase ^ 1u, dead));
+            if (!ok) break;
+          }
+          if (lane == 0) {
+            mbar_arrive_expect_tx(kfull + kslot, F::kRaw);
+            mbar_arrive_expect_tx(rfull + rslot, F::kRaw);
+          }
+          __syncwarp();
+          if (lane < units) {
+            const uint32_t in = (lane << unit_shift) * F::kRawRow;
+            tma_4d(raw_a + (F::kRawStages + kslot) * F::kRaw + in, &tm_k, 0, slot, head, to, kfull + kslot);
+            tma_4d(raw_a + rslot * F::kRaw + in, &tm_v, 0, slot, head, to, rfull + rslot);
+          }
+          // the scales of eight slots per lane, K's and then V's
+          async_load4(scales_a + (at % kInfo) * 128, from, p >= 0);
+          async_arrive(kfull + kslot);
+          ++k_tiles;
+          ++v_tiles;
+          if (++kslot == kKs) {
+            kslot = 0;
+            kphase ^= 1u;
+          }
+          if (++rslot == F::kRawStages) {
+            rslot = 0;
+            rphase ^= 1u;
+          }
+        } else if constexpr (kBytes) {
           const int ks = at % kKs, s = at % F::kRawStages;
           wait(kempty + ks, at / kKs + 1);
           if (!ok) break;

@@ -773,26 +773,33 @@ def alloc_pool(rows, entries, pages, page_size, device="cuda"):
 def _with_table(packer, page_table, cache, int32):
     """A buffer for a call's arguments, with the ss_page_pool of a bare page
     table behind them, and the address of the page table's structure."""
+    size = packer.size
+    buffer = _buffers.get(size)
+    if buffer is None:
+        buffer = _buffers[size] = C.c_char * (size + _POOL.size)
+    buf = buffer()
     if isinstance(page_table, PagePool):
         if page_table.device != cache.device or page_table.page_size != cache.page_size:
             raise SSError("page_table: want a pool of the cache's page size on its device")
-        return C.create_string_buffer(packer.size), page_table.address
-    if page_table.dtype is not int32 or page_table.dim() != 2 or page_table.stride(1) != 1 or \
-            page_table.get_device() != cache.device:
+        return buf, page_table.address
+    shape, stride = page_table.shape, page_table.stride()
+    if page_table.dtype is not int32 or len(shape) != 2 or stride[1] != 1 or page_table.get_device() != cache.device:
         raise SSError("page_table: want a PagePool or a [rows, entries] int32 tensor with contiguous rows on the cache's "
                       "device")
-    rows, entries = page_table.shape
-    buf = C.create_string_buffer(packer.size + _POOL.size)
-    _POOL.pack_into(buf, packer.size, rows, entries, page_table.stride(0) if rows > 1 else entries,
-                    page_table.data_ptr(), cache.num_pages, cache.page_size, 0, 0, 0)
-    return buf, C.addressof(buf) + packer.size
+    rows, entries = shape
+    _POOL.pack_into(buf, size, rows, entries, stride[0] if rows > 1 else entries, page_table.data_ptr(), cache.num_pages,
+                    cache.page_size, 0, 0, 0)
+    return buf, C.addressof(buf) + size
+
+
+_buffers = {}  # types of the calls' argument buffers, by the arguments' size
 
 
 def _pack_rows(torch, buf, at, table, cache, layer, k, v, kv_len, status, token_offsets, max_tokens, table_rows):
     """The arguments of an append or read call (ss_append_args) into buf."""
-    n, i32, shape, dev = kv_len.numel(), torch.int32, k.shape, cache.device
+    n, i32, bf16, shape, dev = kv_len.numel(), torch.int32, torch.bfloat16, k.shape, cache.device
     stride = k.stride()
-    if k.dtype is not torch.bfloat16 or v.dtype is not torch.bfloat16 or k.get_device() != dev or v.get_device() != dev or \
+    if k.dtype is not bf16 or v.dtype is not bf16 or k.get_device() != dev or v.get_device() != dev or \
             len(shape) != 3 or v.shape != shape or v.stride() != stride or stride[2] != 1 or \
             shape[1] != cache.num_kv_heads or shape[2] != cache.head_dim:
         raise SSError("want k and v as [tokens, %d, %d] bf16 tensors of the same strides with contiguous rows on cuda:%d"

@@ -201,3 +201,90 @@ def test_the_plain_append_and_compact():
     got = c.values(1, 1, slice(0, 5))
     want = held[[0, 1, 2, 4, 6]]
     assert np.abs(got - want).max() <= 2.0 ** -10 * c.s[1, 1, 0] * 8 + 2.0 ** -4 * np.abs(want).max()
+
+
+# ------------------------------------------------------------ the binding --
+
+from tests.test_cache_binding import Elsewhere, Host, calls, half, ints, moved, on, pools  # noqa: E402, F401
+
+
+def eight_tensors(page=16):
+    shape = (1, 4, 2, page)
+    data = lambda: on(torch.zeros(*shape, 64, dtype=torch.uint8).view(torch.float8_e4m3fn))  # noqa: E731
+    scale = lambda: on(torch.zeros(1, 4, 2, max(1, page // 16)))  # noqa: E731
+    return dict(k=data(), v=data(), k_scale=scale(), v_scale=scale())
+
+
+def a_rope(device_of=lambda t: t, dim=64):
+    return ss.Rope(dim, turns=device_of(on(torch.zeros(dim // 2, dtype=torch.int64))))
+
+
+def rope(t):
+    a = dict(q=half(3, 4, 64), q_out=half(3, 4, 64), k=half(3, 2, 64), k_out=half(3, 2, 64), kv_len=ints(3), status=ints(3),
+             token_offsets=ints(4), parents=ints(3))
+    a.update(t)
+    r = a.pop("rope", None) or a_rope()
+    ss.ss_rope(r, *(a.pop(x) for x in ("q", "q_out", "k", "k_out", "kv_len", "status")), max_tokens=1, **a)
+
+
+def step(t):
+    a = dict(q=half(3, 4, 64), q_out=half(3, 4, 64), k=half(3, 2, 64), v=half(3, 2, 64), page_table=ints(3, 2), kv_len=ints(3),
+             status=ints(3), token_offsets=ints(4), table_rows=ints(3), positions=ints(3))
+    a.update(t)
+    r, c = a.pop("rope", None) or a_rope(), a.pop("cache", None) or ss.KVCache(**eight_tensors())
+    ss.ss_rope_append(r, c, 0, *(a.pop(x) for x in ("q", "q_out", "k", "v", "page_table", "kv_len", "status")), max_tokens=1, **a)
+
+
+@pytest.mark.parametrize("call,name,arguments", [
+    (rope, "ss_rope", "q q_out k k_out kv_len status token_offsets parents positions"),
+    (step, "ss_rope_append", "q q_out k v page_table kv_len status token_offsets table_rows parents positions")])
+def test_every_argument_is_asked_for_its_gpu(calls, call, name, arguments):  # noqa: F811
+    call({})
+    assert calls == [name]
+    shapes = {"q": half(3, 4, 64), "q_out": half(3, 4, 64), "k": half(3, 2, 64), "k_out": half(3, 2, 64), "v": half(3, 2, 64),
+              "page_table": ints(3, 2), "token_offsets": ints(4)}
+    for x in arguments.split():
+        for cls in (Host, Elsewhere):
+            with pytest.raises(ss.SSError):
+                call({x: moved(shapes.get(x, ints(3)), cls)})
+    for cls in (Host, Elsewhere):
+        with pytest.raises(ss.SSError):
+            call({"rope": a_rope(lambda t: moved(t, cls))})
+        if call is step:
+            there = ss.KVCache(**{k: moved(t, cls) for k, t in eight_tensors().items()})
+            with pytest.raises(ss.SSError):
+                call({"cache": there})
+    assert calls == [name]
+
+
+def test_arguments_of_other_shapes_and_types(calls):  # noqa: F811
+    for call, t in ((rope, dict(q=half(3, 4, 32))), (rope, dict(q_out=half(3, 5, 64))), (rope, dict(q_out=None)), (rope, dict(k=None)),
+                    (rope, dict(q=half(3, 64, 4).transpose(1, 2))), (rope, dict(q=half(4, 4, 64), q_out=half(4, 4, 64))),
+                    (rope, dict(parents=ints(4))), (rope, dict(kv_len=ints(2))), (rope, dict(token_offsets=ints(3))),
+                    (rope, dict(q=half(3, 256))), (rope, dict(k=half(3, 2, 64).float())), (rope, dict(positions=half(3))),
+                    (step, dict(rope=a_rope(dim=128))), (step, dict(q=half(2, 4, 64), q_out=half(2, 4, 64))),
+                    (step, dict(v=half(3, 3, 64))), (step, dict(k=half(3, 2, 32), v=half(3, 2, 32))), (step, dict(q_out=None)),
+                    (step, dict(page_table=ss.PagePool(page_size=32, **pools())))):
+        with pytest.raises(ss.SSError):
+            call(t)
+    assert not calls
+    rope(dict(q=None, q_out=None))
+    rope(dict(k=None, k_out=None, kv_len=None, positions=ints(3), parents=None))
+    step(dict(q=None, q_out=None, page_table=ss.PagePool(page_size=16, **pools())))
+    assert calls == ["ss_rope", "ss_rope", "ss_rope_append"]
+
+
+def test_caches_of_8_bits():
+    for page in (8, 16, 64):
+        c = ss.KVCache(**eight_tensors(page))
+        assert c.format == "fp8" and c.struct.format == 2 and c.head_dim == 64 and c.struct.slot_stride == 64
+        assert c.struct.scale_head_stride == 4 * max(1, page // 16)
+    for kw in (dict(k_scale=on(torch.zeros(1, 4, 2, 2))), dict(k_scale=None), dict(v_scale=None), dict(v=half(1, 4, 2, 16, 64)),
+               dict(k_scale=on(torch.zeros(1, 4, 2, 1, dtype=torch.float64))), dict(v_scale=moved(on(torch.zeros(1, 4, 2, 1)), Host)),
+               dict(v_scale=on(torch.zeros(1, 2, 4, 1).transpose(1, 2)))):
+        with pytest.raises(ss.SSError):
+            ss.KVCache(**{**eight_tensors(), **kw})
+    with pytest.raises(ss.SSError):
+        ss.alloc_cache(1, 2, 2, 16, 64, "e4m3", device="cpu")
+    c = ss.alloc_cache(2, 3, 2, 32, 48, "fp8", device="cpu")
+    assert c.k.shape == (2, 3, 2, 32, 48) and c.v_scale.shape == (2, 3, 2, 2) and c.device == -1
