@@ -95,6 +95,36 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const AppendArgs a, c
       return reinterpret_cast<uint32_t*>(head < a.c.heads ? a.c.ks + in_scale + head * a.c.s_head_stride
                                                           : a.c.vs + in_scale + (head - a.c.heads) * a.c.s_head_stride);
     };
+    if constexpr (kBytes) {
+      // (bound by instructions: the rows of K, or of V, a step apart)
+      const bool is_v = first >= static_cast<uint32_t>(a.c.heads);
+      if (is_v || first + kEach <= static_cast<uint32_t>(a.c.heads)) {
+        const int32_t head = is_v ? first - a.c.heads : first;
+        const uint8_t* from = (is_v ? a.c.v : a.c.k) + in_cell + head * a.c.head_stride;
+        const uint8_t* scales = (is_v ? a.c.vs : a.c.ks) + in_scale + head * a.c.s_head_stride;
+        uint8_t* to = (is_v ? a.v : a.k) + in_flat + head * a.head_stride;
+        uint2 w[kEach];
+        float s[kEach];
+#pragma unroll
+        for (int u = 0; u < kEach; ++u) {
+          w[u] = make_uint2(0u, 0u);
+          s[u] = 0.0f;
+          if (live && page >= 0) {
+            w[u] = *reinterpret_cast<const uint2*>(from + u * a.c.head_stride);
+            s[u] = *reinterpret_cast<const float*>(scales + u * a.c.s_head_stride);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < kEach; ++u) {
+          float f[8];
+          decode8(w[u], s[u], f);
+          if (live)
+            *reinterpret_cast<uint4*>(to + u * a.head_stride) =
+                make_uint4(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7]));
+        }
+        continue;
+      }
+    }
     uint4 x[kEach];
     uint32_t word[kEach], pair[kEach];
 #pragma unroll

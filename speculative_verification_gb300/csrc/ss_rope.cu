@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, kOdd ? 2 : !kRope ? 5 : kFormat == S
     if (page < 0) return;
     const int slot = group & (size - 1), side = group >> a.chunk_shift, sides = kGroups >> a.chunk_shift;
     const int64_t i = from + slot;  // the slot's token
-    const bool fresh = i >= t0 && i < t1, kept = i < 0;
+    const bool fresh = i >= t0 && i < t1, kept = i < 0, had = from < 0;  // had: some slots hold rows from before
     const int32_t in_page = static_cast<int32_t>(first_slot) & ((1 << a.c.page_shift) - 1);
     const int64_t in_flat = (static_cast<int64_t>(begin) + (fresh ? i : 0)) * a.k_token + lane * 16;
     const int64_t in_cell = page * a.c.page_stride + (in_page + slot) * a.c.slot_stride + lane * 8;
@@ -325,63 +325,75 @@ __global__ void __launch_bounds__(kThreads, kOdd ? 2 : !kRope ? 5 : kFormat == S
 #pragma unroll
       for (int e = 0; e < kEach; ++e) {
         x[e] = make_uint4(0u, 0u, 0u, 0u);
-        old[e] = 0.0f;
-        if (e >= more || !live) continue;
-        if (fresh) {
-          x[e] = *reinterpret_cast<const uint4*>(src + e * a.k_head);
-        } else if (kept) {
-          const uint2 w = *reinterpret_cast<const uint2*>(cell + e * a.c.head_stride);
-          x[e].x = w.x;
-          x[e].y = w.y;
-          old[e] = *scale_of(e);
-        }
+        if (fresh && live && e < more) x[e] = *reinterpret_cast<const uint4*>(src + e * a.k_head);
       }
-      uint32_t mine = 0;
-      bool odd = false;  // a value is not finite
-#pragma unroll
-      for (int e = 0; e < kEach; ++e) {
-        if constexpr (kRope)
-          if (fresh && !is_v && e < more) x[e] = turned<kOdd>(a, t, x[e], src - lane * 16 + e * a.k_head, lane, lanes);
-        uint32_t top;
-        if (kept) {
-          float f[8];
-          decode8(make_uint2(x[e].x, x[e].y), old[e], f);
-          top = __float_as_uint(finite_top(f));
-        } else {
-          top = magnitude(x[e]);
-          if (__builtin_expect(top >= 0x7f80u, 0)) {
-            float f[8];
-            floats_of(x[e], f);
-            top = __float_as_uint(finite_top(f)) >> 16;
-            odd = true;
-          }
-          top <<= 16;
-        }
-        __syncwarp();
-        top = __reduce_max_sync(0xffffffffu, top);
-        if ((tid & 31) == e) mine = top;
-      }
-      if ((tid & 31) < kEach && mine != 0) atomicMax(&s_top[turn][side * kEach + (tid & 31)], mine);
-      __syncthreads();
-      const uint4 tops = *reinterpret_cast<const uint4*>(&s_top[turn][side * kEach]);
-      if (fresh || kept) {
-        const uint32_t top[kEach] = {tops.x, tops.y, tops.z, tops.w};
+      if (had) {
 #pragma unroll
         for (int e = 0; e < kEach; ++e) {
-          if (e >= more) break;
-          const Scale8 to = scale8(__uint_as_float(top[e]));
-          uint2 w;
-          if (kept || odd) {
-            float f[8];
-            if (kept) decode8(make_uint2(x[e].x, x[e].y), old[e], f);
-            else floats_of(x[e], f);
-            w = encode8(f, to.inv);
-          } else {
-            w = encode8(x[e], to.inv);
+          old[e] = 0.0f;
+          if (kept && live && e < more) {
+            const uint2 w = *reinterpret_cast<const uint2*>(cell + e * a.c.head_stride);
+            x[e].x = w.x;
+            x[e].y = w.y;
+            old[e] = *scale_of(e);
           }
-          if (live) *reinterpret_cast<uint2*>(cell + e * a.c.head_stride) = w;
-          if (lane == 0 && i == t1 - 1) *scale_of(e) = to.s;
         }
+      }
+      if constexpr (kRope)
+        if (fresh && !is_v) {
+#pragma unroll
+          for (int e = 0; e < kEach; ++e)
+            if (e < more) x[e] = turned<kOdd>(a, t, x[e], src - lane * 16 + e * a.k_head, lane, lanes);
+        }
+      uint32_t top[kEach], most = 0;
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) {
+        top[e] = magnitude(x[e]) << 16;
+        if (!kept) most = max(most, top[e]);
+      }
+      const bool odd = most >= 0x7f800000u;  // a value is not finite
+      if (had || odd) {
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) {
+          float f[8];
+          if (kept) decode8(make_uint2(x[e].x, x[e].y), old[e], f);
+          else floats_of(x[e], f);
+          top[e] = __float_as_uint(finite_top(f));
+        }
+      }
+      __syncwarp();
+      uint32_t mine = 0;
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) {
+        const uint32_t m = __reduce_max_sync(0xffffffffu, top[e]);
+        if ((tid & 31) == e) mine = m;
+      }
+      if ((tid & 31) < kEach && mine != 0) atomicMax(&s_top[turn][side * kEach + (tid & 31)], mine);
+      const bool slow = __syncthreads_or(odd) || had;
+      const uint4 tops = *reinterpret_cast<const uint4*>(&s_top[turn][side * kEach]);
+      const Scale8 to[kEach] = {scale8(__uint_as_float(tops.x)), scale8(__uint_as_float(tops.y)),
+                                scale8(__uint_as_float(tops.z)), scale8(__uint_as_float(tops.w))};
+      const bool row_here = live && (fresh || kept);
+      if (!slow) {
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) {
+          const uint2 w = encode8(x[e], to[e].inv);
+          if (row_here && e < more) *reinterpret_cast<uint2*>(cell + e * a.c.head_stride) = w;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) {
+          float f[8];
+          if (kept) decode8(make_uint2(x[e].x, x[e].y), old[e], f);
+          else floats_of(x[e], f);
+          const uint2 w = encode8(f, to[e].inv);
+          if (row_here && e < more) *reinterpret_cast<uint2*>(cell + e * a.c.head_stride) = w;
+        }
+      }
+      if (lane == 0 && i == t1 - 1) {
+#pragma unroll
+        for (int e = 0; e < kEach; ++e)
+          if (e < more) *scale_of(e) = to[e].s;
       }
       // the batch before's maxima were read before this batch's barrier; they are needed again in two batches
       if (tid < 2 * kEach) s_top[turn == 0 ? 2 : turn - 1][tid] = 0;

@@ -146,8 +146,7 @@ __device__ __forceinline__ void decode8(uint2 w, float s, float (&x)[8]) {
     asm("{\n\t.reg .f16 l, u;\n\tmov.b32 {l, u}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, u;\n\t}"
         : "=f"(x[2 * h]), "=f"(x[2 * h + 1])
         : "r"(f));
-    x[2 * h] *= s;
-    x[2 * h + 1] *= s;
+    split(mul_2(two(x[2 * h], x[2 * h + 1]), two(s, s)), x[2 * h], x[2 * h + 1]);
   }
 }
 
