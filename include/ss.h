@@ -778,8 +778,8 @@ ss_status ss_pages_trim(const ss_page_pool* pool, int32_t n, const int32_t* tabl
  *   a = 2 pi p turns[i];
  * the other channels stay.  turns are fractions of a full turn per position in
  * units of 2^-64 (0.64 fixed point): p turns[i] modulo 2^64 is exact in integer
- * arithmetic, so far positions lose nothing.  Angles are rounded to 2^-24 of
- * half a turn, the products and sums held in fp32, the result rounded to bf16.
+ * arithmetic, so far positions lose nothing.  Cosines and sines are rounded to
+ * fp32, products and sums held in it, the result rounded to bf16.
  *
  * ss_rope_turns fills turns (HOST memory, rot_dim / 2 entries; to be copied to
  * the device once) for the frequencies f_i = base^(-2i / rot_dim), scaled:
@@ -845,8 +845,11 @@ typedef struct {
 ss_status ss_rope(const ss_rope_args* args, ss_stream_t stream);
 
 /* ss_rope_append: ss_rope on the queries and keys, and ss_cache_append of the
- * turned keys (as bf16 has them) and of the values, in one launch: the cache
- * holds what the two calls would leave there, the turned keys go nowhere else.
+ * turned keys (as bf16 has them) and of the values, in one launch: the turned
+ * keys go nowhere else.  A cache of bf16 holds what the two calls would leave
+ * there.  Keys for 8 or 4 bits are summed to about 2^-33 of |x| + |y| before
+ * their rounding to bf16: here and there, next to ties, a unit of bf16 apart
+ * from ss_rope's, which in those formats could have become a step.
  * `append` describes the requests, k and v; k is not written.  out_status
  * (append's): the larger of both calls' codes; SS_ROW_BAD_PARAM for a request
  * that either refuses: nothing of it is touched. */

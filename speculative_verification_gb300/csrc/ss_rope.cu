@@ -5,8 +5,15 @@
 // The mathematics.  A pair (x, y) of a head's channels at position p becomes
 // (m (x cos a - y sin a), m (y cos a + x sin a)), a = 2 pi p t.  t is a 64-bit
 // fraction of a turn, so p t modulo one turn is one integer product, exact at
-// any position; its upper 32 bits, as a signed fraction of half a turn, are what
-// sincospif takes.  In 8 bits the rows of a block (16 slots of one head) share a
+// any position.  Its upper 8 bits, rounded, are one of 256 angles A whose sine
+// and cosine are tabled in two parts; with the rest d, |d| <= pi / 256, and the
+// first terms of its series,
+//   cos(A + d) = cos A + (cos A (cos d - 1) - sin A sin d), likewise the sine,
+// where what is added is small, so that both come out to 2^-34, as two floats.
+// Rotations are fp32 sums of the first.  Those of keys that go into a cache of 8
+// or 4 bits take the second too and carry their remainders, so that they are
+// rounded to bf16 as the exact sums are: there a unit of bf16 may become a step
+// of the cache.  In 8 bits the rows of a block (16 slots of one head) share a
 // power of two by their largest value (ss_rows.cuh).
 #include <cuda_runtime.h>
 #include <math.h>
@@ -49,6 +56,55 @@ struct StepArgs {
   int32_t* status;
 };
 
+// Cosines and sines of 2 pi k / 256, as the sum of two floats each.
+struct Circle {
+  float4 at[256];
+  static constexpr double series(double x, double first, int n) {  // sum of (-1)^i x^(2i+n) / (2i+n)!
+    double term = first, sum = first;
+    for (int i = 1; i < 14; ++i) {
+      term *= -x * x / ((2 * i + n) * (2 * i + n - 1));
+      sum += term;
+    }
+    return sum;
+  }
+  constexpr Circle() : at() {
+    for (int k = 0; k < 256; ++k) {
+      const int q = (k + 32) / 64, left = k - 64 * q;  // quadrant, and -32 .. 31 of it
+      const double x = left * (6.283185307179586 / 256.0);
+      const double c = series(x, 1.0, 0), s = series(x, x, 1);
+      const double cs = q % 4 == 0 ? c : q % 4 == 1 ? -s : q % 4 == 2 ? -c : s;
+      const double sn = q % 4 == 0 ? s : q % 4 == 1 ? c : q % 4 == 2 ? -s : -c;
+      at[k].x = static_cast<float>(cs);
+      at[k].y = static_cast<float>(cs - static_cast<double>(at[k].x));
+      at[k].z = static_cast<float>(sn);
+      at[k].w = static_cast<float>(sn - static_cast<double>(at[k].z));
+    }
+  }
+};
+__device__ const Circle kCircle = Circle();
+
+// The cosine and sine of a fraction of a turn times a magnitude: each a float
+// and what is left of it.
+__device__ __forceinline__ void circle(uint64_t turn, float magnitude, float2& c, float2& s) {
+  const uint32_t k = static_cast<uint32_t>((turn + (1ull << 55)) >> 56);  // modulo 256
+  const int32_t left = static_cast<int32_t>(static_cast<int64_t>(turn - (static_cast<uint64_t>(k) << 56)) >> 24);
+  constexpr double kUnit = 6.283185307179586 / 1099511627776.0;  // 2 pi / 2^40
+  constexpr float kHigh = static_cast<float>(kUnit), kLow = static_cast<float>(kUnit - static_cast<double>(kHigh));
+  const float n = static_cast<float>(left & ~0xff), m = static_cast<float>(left & 0xff), d = n * kHigh;
+  const float rest = __fmaf_rn(n, kHigh, -d) + __fmaf_rn(n, kLow, m * kHigh);  // the angle less d
+  const float d2 = d * d, sd = __fmaf_rn(d * d2, -1.0f / 6.0f, rest), cd = d2 * __fmaf_rn(d2, 1.0f / 24.0f, -0.5f);
+  const float4 a = kCircle.at[k & 255u];
+  // hi + lo + (first + left of it) d + first sd + hi cd
+  const auto sum = [&](float hi, float lo, float first, float first_lo) {
+    const float f = first * d, h = hi + f, t = h - hi;
+    const float l = ((hi - (h - t)) + (f - t)) + (__fmaf_rn(first, d, -f) + __fmaf_rn(first, sd, __fmaf_rn(first_lo, d, __fmaf_rn(hi, cd, lo))));
+    const float p = magnitude * h, e = __fmaf_rn(magnitude, h, -p) + magnitude * l, r = p + e;
+    return make_float2(r, e - (r - p));
+  };
+  c = sum(a.x, a.y, -a.z, -a.w);
+  s = sum(a.z, a.w, a.x, a.y);
+}
+
 // What one lane needs to turn its 8 channels: out = x c + partner s, partner
 // the other channel of the pair, s with its sign; two channels at a time.
 struct Turn {
@@ -81,11 +137,17 @@ __device__ __forceinline__ Turn turn_of(const StepArgs& a, const float* cos_of, 
   return t;
 }
 
+// The places of a channel's word in a token's row of what cosines and sines
+// leave: a lane's 8 in two reads without conflicts.
+__device__ __forceinline__ int low_at(int ch) { return (ch & 4) * 16 + (ch >> 3) * 4 + (ch & 3); }
+
 // One row's 8 channels, turned.  All 16 lanes of the row call it.  `row` is the
 // row in global memory, read again where lanes' channels do not pair up (kOdd).
-template <bool kOdd>
+// kClose: sums to about 2^-33 of |x c| + |partner s| before they are rounded, with
+// `low`, what the floats c and s leave (cosine's below, sine's above in a word).
+template <bool kOdd, bool kClose>
 __device__ __forceinline__ uint4 turned(const StepArgs& a, const Turn& t, const uint4& x, const uint8_t* row, int lane,
-                                        uint32_t lanes) {
+                                        uint32_t lanes, const uint4* low) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
   uint64_t p[4];
   if (a.layout == SS_ROPE_INTERLEAVED) {
@@ -114,11 +176,40 @@ __device__ __forceinline__ uint4 turned(const StepArgs& a, const Turn& t, const 
     __syncwarp(lanes);  // read before any lane writes the row's place (which may be the row)
   }
   uint32_t o[4];
+  bool exact = false;
+  if constexpr (kClose) {
+    const uint4 l0 = low[lane], l1 = low[lane + kRowLanes];
+    const uint32_t l[8] = {l0.x, l0.y, l0.z, l0.w, l1.x, l1.y, l1.z, l1.w};
+    const uint64_t minus = two(-1.0f, -1.0f);
+    uint64_t all = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      // sum = a + b with a = v c, b = p s: what the sum took of either (sum - b; the
+      // rest), and what is left of them
+      const uint64_t v = two(bf16_lo(w[i]), bf16_hi(w[i])), b = mul_2(p[i], t.s[i]), sum = fma_2(v, t.c[i], b);
+      const uint64_t of_a = fma_2(b, minus, sum), less_a = fma_2(sum, minus, b), less_b = fma_2(sum, minus, of_a);
+      // the sine's low part keeps the cosine's bits below its own: 2^-8 of 2^-25
+      const uint64_t left = add_2(fma_2(v, two(bf16_lo(l[2 * i]), bf16_lo(l[2 * i + 1])), fma_2(v, t.c[i], less_a)),
+                                  fma_2(p[i], two(__uint_as_float(l[2 * i]), __uint_as_float(l[2 * i + 1])), fma_2(p[i], t.s[i], less_b)));
+      all = add_2(all, left);
+      float lo, hi;
+      split(add_2(sum, left), lo, hi);
+      o[i] = bf16_pair(lo, hi);
+    }
+    float lo, hi;
+    split(all, lo, hi);
+    exact = fabsf(lo + hi) < INFINITY;  // else something is not finite, and what is left of it no number
+  }
+  if (!exact) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float lo, hi;
+      split(fma_2(two(bf16_lo(w[i]), bf16_hi(w[i])), t.c[i], mul_2(p[i], t.s[i])), lo, hi);
+      o[i] = bf16_pair(lo, hi);
+    }
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    float lo, hi;
-    split(fma_2(two(bf16_lo(w[i]), bf16_hi(w[i])), t.c[i], mul_2(p[i], t.s[i])), lo, hi);
-    o[i] = bf16_pair(lo, hi);
     if (kOdd) {
       const uint32_t mask = ((t.on >> (2 * i)) & 1u ? 0xffffu : 0u) | ((t.on >> (2 * i + 1)) & 1u ? 0xffff0000u : 0u);
       o[i] = (o[i] & mask) | (w[i] & ~mask);
@@ -136,11 +227,12 @@ __device__ __forceinline__ uint4 turned(const StepArgs& a, const Turn& t, const 
 // lanes per slot of the block, those that hold rows from before among them.
 template <int kFormat, bool kRope, bool kOdd>
 __global__ void __launch_bounds__(kThreads, kOdd ? 2 : !kRope ? 5 : kFormat == SS_CACHE_FP8 || kFormat == SS_CACHE_INT4 ? 3 : 4) step_kernel(const StepArgs a) {
-  constexpr bool kBlocks = kFormat == SS_CACHE_FP8;
+  constexpr bool kBlocks = kFormat == SS_CACHE_FP8, kClose = kRope && (kBlocks || kFormat == SS_CACHE_INT4);
   constexpr int kEach = 4;
   __shared__ __align__(16) float s_cos[kRope ? kGroups : 1][kPairs], s_sin[kRope ? kGroups : 1][kPairs];
   __shared__ int32_t s_depth[kRope ? SS_TREE_MAX_NODES : 1];
   __shared__ __align__(16) uint32_t s_top[3][2 * kEach];
+  __shared__ __align__(16) uint32_t s_low[kClose ? kGroups : 1][2 * kPairs];
   __shared__ uint64_t s_turns[kRope ? kPairs : 1];
   const int tid = threadIdx.x, r = blockIdx.y;
   if (kRope && tid < a.half) s_turns[tid] = a.turns[tid];
@@ -241,10 +333,16 @@ __global__ void __launch_bounds__(kThreads, kOdd ? 2 : !kRope ? 5 : kFormat == S
       const int64_t at = a.positions ? a.positions[begin + t0 + token]
                                      : static_cast<int64_t>(base) + (tree ? s_depth[t0 + token] : t0 + token);
       const uint64_t turn = static_cast<uint64_t>(at) * s_turns[pair];
-      float s, c;
-      sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 4.656612873077393e-10f, &s, &c);
-      s_cos[token][pair] = a.magnitude * c;
-      s_sin[token][pair] = a.magnitude * s;
+      float2 c, s;
+      circle(turn, a.magnitude, c, s);
+      s_cos[token][pair] = c.x;
+      s_sin[token][pair] = s.x;
+      if constexpr (kClose) {
+        const int ch = a.layout == SS_ROPE_HALVES ? pair : 2 * pair, partner = a.layout == SS_ROPE_HALVES ? pair + a.half : ch + 1;
+        const uint32_t low = bf16_pair(c.y, s.y);
+        s_low[token][low_at(ch)] = low ^ 0x80000000u;
+        s_low[token][low_at(partner)] = low;
+      }
     }
   }
   if (kRope || kBlocks) __syncthreads();
@@ -264,7 +362,11 @@ __global__ void __launch_bounds__(kThreads, kOdd ? 2 : !kRope ? 5 : kFormat == S
         for (int e = 0; e < kEach; ++e) {
           const int32_t h = h0 + e * step, k = h - a.q_heads, v = k - a.kv_heads;
           if (h >= heads) break;
-          const uint4 y = v < 0 ? turned<kOdd>(a, t, x[e], source(h) - lane * 16, lane, lanes) : x[e];
+          uint4 y = x[e];
+          if (kClose && !kBlocks && k >= 0 && v < 0)
+            y = turned<kOdd, kClose>(a, t, y, source(h) - lane * 16, lane, lanes, reinterpret_cast<const uint4*>(s_low[kClose ? token : 0]));
+          else if (v < 0)
+            y = turned<kOdd, false>(a, t, y, source(h) - lane * 16, lane, lanes, nullptr);
           if (k < 0 || kFormat == kNone) {
             uint8_t* to = k < 0 ? a.q_out + at_row * a.q_out_token + h * a.q_out_head
                                 : a.k_out + at_row * a.k_out_token + k * a.k_out_head;
@@ -343,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, kOdd ? 2 : !kRope ? 5 : kFormat == S
         if (fresh && !is_v) {
 #pragma unroll
           for (int e = 0; e < kEach; ++e)
-            if (e < more) x[e] = turned<kOdd>(a, t, x[e], src - lane * 16 + e * a.k_head, lane, lanes);
+            if (e < more) x[e] = turned<kOdd, kClose>(a, t, x[e], src - lane * 16 + e * a.k_head, lane, lanes, reinterpret_cast<const uint4*>(s_low[i - t0]));
         }
       uint32_t top[kEach], most = 0;
 #pragma unroll
@@ -433,9 +535,11 @@ template <int kFormat, bool kRope>
 static ss_status launch_step(const StepArgs& a, int32_t num_requests, cudaStream_t s) {
   const int64_t size = 1ll << a.chunk_shift;
   // n tokens touch at most ceil((n + size - 1) / size) blocks of slots
-  const int64_t x = kFormat == kNone ? (a.max_tokens + size - 1) / size : (a.max_tokens + 2 * size - 2) / size;
+  const int64_t n = a.max_tokens < a.total_tokens ? a.max_tokens : a.total_tokens;  // a generous max_tokens costs nothing
+  const int64_t x = kFormat == kNone ? (n + size - 1) / size : (n + 2 * size - 2) / size;
   const int64_t rows = a.q_heads + (kFormat == kNone ? 1ll : 2ll) * a.kv_heads;
-  const dim3 grid(static_cast<unsigned>(x < 1 ? 1 : x), num_requests, splits((x < 1 ? 1 : x) * num_requests, rows));
+  const int64_t wide = x < 1 ? 1 : x;
+  const dim3 grid(static_cast<unsigned>(wide), num_requests, splits(wide * num_requests, rows));
   if constexpr (kRope) {
     if (a.half % (a.layout == SS_ROPE_HALVES ? 8 : 4) != 0) {
       step_kernel<kFormat, true, true><<<grid, kThreads, 0, s>>>(a);

@@ -5,7 +5,10 @@ Tolerances.  A turned channel is one bf16 rounding (2^-8 of it at most) of fp32
 sums: the angle is off by 2^-25 of half a turn (2^-23.3 radians), sine and
 cosine by two units of 2^-24, magnitude, product and sum by one each, so by less
 than 2^-21 of |x| + |y| times the magnitude.  What is cached in 8 bits is
-defined bit by bit.
+defined bit by bit.  Keys on their way into 8 or 4 bits are bf16 roundings of
+sums that are off by 2^-33 of |x| + |y|: compared bit by bit with the 64-bit
+sums' after an assertion that none of these lies that near to where a rounding
+turns.
 """
 import random
 
@@ -41,6 +44,21 @@ def check_turned(got, x, at, rope, layout, magnitude, what=""):
     err = np.abs(np32(got) - want)
     assert (err <= 2.0 ** -8 * np.abs(want) + 2.0 ** -21 * both * abs(magnitude)).all(), (what, err.max())
     assert np.array_equal(np32(got)[..., 2 * h:], np32(x)[..., 2 * h:])
+
+
+def keys_to_cache(x, at, rope, layout, magnitude):
+    """The keys that ss_rope_append puts into 8 or 4 bits, from 64-bit sums."""
+    table = [int(v) for v in rope.turns.cpu().numpy().view(np.uint64)]
+    x64 = np32(x).astype(np.float64)
+    want = P.turn(x64, at, table, rope.rot_dim, layout, magnitude)
+    h = rope.rot_dim // 2
+    a, b = (slice(0, h), slice(h, 2 * h)) if layout == "halves" else (slice(0, 2 * h, 2), slice(1, 2 * h, 2))
+    off = np.zeros_like(want)
+    off[..., a] = off[..., b] = 2.0 ** -33 * abs(magnitude) * (np.abs(x64[..., a]) + np.abs(x64[..., b]))
+    off[np.array(at) == 0] = 0.0  # cosine 1 and sine 0 are exact, and so are two products that one of them takes part in
+    y, low, high = (R.bf16((want + d).astype(np.float32)) for d in (0, -off, off))
+    assert np.array_equal(low, high)
+    return torch.from_numpy(y).to(torch.bfloat16).cuda()
 
 
 SHAPES = [  # dim, rot_dim, heads, kv heads
@@ -354,15 +372,23 @@ def test_rope_append_is_the_two_calls(ss, fmt, page, dim, rot, heads, kv, layout
     q, k, v = (x[:total] for x in (qkv[:, :heads], qkv[:, heads:heads + kv], qkv[:, heads + kv:]))
     at = {}
     if mode == "tree":
-        at["parents"] = ints([p for n in news for p in (random_parents(pr, n) if n else [])])
-    if mode == "positions":
-        at["positions"] = ints(rng.integers(-2 ** 31, 2 ** 31, total).tolist())
+        trees = [random_parents(pr, n) if n else [] for n in news]
+        at["parents"], places = ints(sum(trees, [])), P.positions(lens, news, trees)
+    elif mode == "positions":
+        places = rng.integers(-2 ** 31, 2 ** 31, total).tolist()
+        at["positions"] = ints(places)
+    else:
+        places = P.positions(lens, news)
     rows = {} if mode == "one" else dict(token_offsets=ints(offsets), max_tokens=max(news))
     t, n, st, st2 = ints(table), ints(lens), ints([-1] * 5), ints([-1] * 5)
-    # the two calls
+    # the two calls (8 and 4 bits: with the keys from closer sums)
     q_want, turned = torch.empty(total, heads, dim, dtype=torch.bfloat16, device="cuda"), torch.empty_like(k)
     before = [x.clone() for x in parts(cache)]
     ss.ss_rope(rope, *((q, q_want) if heads else (None, None)), k, turned, n, st, **rows, **at)
+    if fmt != "bf16":
+        close = keys_to_cache(k, places, rope, layout, 0.75)
+        assert (np.abs(np32(close) - np32(turned)) <= 2.0 ** -7 * np.abs(np32(close)) + 2.0 ** -19).all()
+        turned = close
     ss.ss_cache_append(cache, 0, *(x.contiguous() for x in (turned, v)), t, n, st2, **rows)
     assert st.tolist() == [0] * 5 and st2.tolist() == [0] * 5
     want = [x.clone() for x in parts(cache)]
@@ -538,3 +564,65 @@ def test_all_calls_on_the_longest_rows(ss):
     assert (np.abs(np32(back) - want) <= (2.0 ** -4 + 2.0 ** -7) * np.abs(want) + 2.0 ** -15).all()
     err = np.abs(np32(back_v) - np32(v))
     assert (err <= 2.0 ** -4 * np.abs(np32(v)) + 2.0 ** -15).all()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "int4", "fp8"])
+def test_long_chunks_and_generous_limits(ss, fmt):
+    """Many chunks of tokens of a request; limits far above the numbers of tokens."""
+    rng = np.random.default_rng(11)
+    lens, news, heads, page, dim = [5, 70], [21000, 3], 1, 64, 64
+    need = [-(-(a + b) // page) for a, b in zip(lens, news)]
+    perm = rng.permutation(sum(need)).tolist()
+    table = ints([[perm.pop() for _ in range(n)] + [-1] * (max(need) - n) for n in need])
+    cache = any_cache(ss, rng, fmt, sum(need), heads, page, dim)
+    before = [x.clone() for x in parts(cache)]
+    rope = ss.Rope(dim, base=1e6)
+    q, k, v = (half(rng, sum(news), h, dim) for h in (2, 1, 1))
+    out, turned, st = torch.empty_like(q), torch.empty_like(k), ints([-1] * 2)
+    kw = dict(token_offsets=ints(offsets_of(news)), max_tokens=200000)
+    ss.ss_rope(rope, q, out, k, turned, ints(lens), st, **kw)
+    assert st.tolist() == [0, 0]
+    at = P.positions(lens, news)
+    check_turned(out, q, at, rope, "halves", 1.0)
+    ss.ss_cache_append(cache, 0, turned, v, table, ints(lens), st, **kw)
+    assert st.tolist() == [0, 0]
+    want = [x.clone() for x in parts(cache)]
+    if fmt == "fp8":
+        plain = [P.Cache8(x[0].cpu().numpy(), s[0].cpu().numpy()) for x, s in ((before[0], before[2]), (before[1], before[3]))]
+        for x, w in ((turned, plain[0]), (v, plain[1])):
+            x = np32(x).astype(np.float64)
+            for r, a in enumerate(lens):
+                w.append(table[r].tolist(), a, x[offsets_of(news)[r]:offsets_of(news)[r + 1]])
+        same8(cache, plain)
+    def again():
+        for x, y in zip(parts(cache), before):
+            x.copy_(y)
+
+    if fmt != "bf16":  # (in 1.3 million keys some lie next to where a rounding turns: as with limits that fit)
+        again()
+        ss.ss_rope_append(rope, cache, 0, q, torch.empty_like(q), k, v, table, ints(lens), st, **dict(kw, max_tokens=21000))
+        want = [x.clone() for x in parts(cache)]
+    again()
+    out2 = torch.empty_like(q)
+    ss.ss_rope_append(rope, cache, 0, q, out2, k, v, table, ints(lens), st, **kw)
+    assert st.tolist() == [0, 0] and torch.equal(out, out2)
+    for x, y in zip(parts(cache), want):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+def test_two_calls_at_once(ss):
+    """Two streams, each with requests of its own in one cache: the blocks are apart."""
+    p = Rows(ss, 21, [3, 40, 0, 17], [500, 300, 77, 130], 4, 16, 128)
+    want = plain8(p.cache)
+    p.plain(want)
+    half_of = [slice(0, 2), slice(2, 4)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    lens, table, st = ints(p.lens), ints(p.table), [ints([-1, -1]) for _ in range(2)]
+    off = [ints(p.offsets[h.start:h.stop + 1]) for h in half_of]
+    torch.cuda.synchronize()
+    for s, h, o, t in zip(streams, half_of, off, st):
+        ss.ss_cache_append(p.cache, 0, p.k, p.v, table, lens[h], t, token_offsets=o, max_tokens=500,
+                           table_rows=ints([h.start, h.start + 1]), stream=s)
+    torch.cuda.synchronize()
+    assert [t.tolist() for t in st] == [[0, 0], [0, 0]]
+    same8(p.cache, want)
