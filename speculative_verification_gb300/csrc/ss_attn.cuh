@@ -36,7 +36,16 @@
 // the references then also count the keys' magnitudes and keep the largest
 // weight near f16's upper end (kSlack, kTop).
 //
-// Roundings: P to bf16 (4 bits: p s_v to f16, whose 11 bits leave only the
+// 8 bits.  A row stands for s n, n e4m3, s a power of two for 16 slots of a head.
+// The keys' e4m3 numbers are the A operand as they lie in the cache.  A bf16
+// query is split into unit (hi + lo): hi e4m3, of what is left lo e4m3 too
+// (8 and 16 rows, a column of its own) or e5m2 (from 32 rows on, in the same
+// column), so the products lose next to nothing; s_k enters in fp32.  Values
+// become f16 (exact), the weights p s_v in f16 meet them, as for 4 bits.  A
+// block whose scale is not finite, or an element that is NaN, is a value that
+// is not finite in this kernel's sense: taken out where some row does not see it.
+//
+// Roundings: P to bf16 (4 and 8 bits: p s_v to f16, whose 11 bits leave only the
 // result's own rounding to see; weights 2^22 below a row's largest and smaller
 // lose bits, 2^33 below it they are 0), the result to bf16; everything else is
 // fp32 (sums of p on the unrounded values).
@@ -51,7 +60,7 @@
 // Warps: 0 tensor copies (one box per page and 64 channels, straight from the
 // page table), 1 the first and 2 the second product's tcgen05.mma, 3 the next
 // item's queries and masks, then the softmax warps (128 threads per 8 to 32
-// rows) and for 4 bits those that unpack.
+// rows) and for 4 and 8 bits those that unpack.
 //
 // Measured on one GB300, and what bounds it: bf16, 32 requests of 1-8 drafts
 // over 1-32k tokens (32 heads on 8, dim 128): 244 us, 6.68 TB/s, the cache's
@@ -62,7 +71,11 @@
 // 8-64k: 365 us, 3.43 TB/s, 1390 clocks a tile, the unpacking's and the waits'
 // latency; 48 x 1-8 drafts, 64 rows, of which 44 % are without a query: 325 us,
 // instruction issue (54 % of the slots).  One token of one request: 12 us, all
-// latency.
+// latency.  8 bits, 32 x 1 token over 8-64k: 362 us, 6.5 TB/s, the cache's
+// bytes; 48 x 1-8 drafts over 1-16k, 64 rows: 246 us (floor 125), the softmax
+// chain and the copying warp's spilled registers; 16 trees over 2-12k, dim 64:
+// 118 us, 2 x 4096-token prompt chunks in a window: 529 us, both by the chain:
+// 1.4 us a tile and 4.2 an item.
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>

@@ -52,8 +52,9 @@ __device__ __forceinline__ uint32_t divide(uint32_t n, const FastDiv& f) {
 // grid's width further.  4 x 2-6k tokens, 8 heads of 128 channels: 4 bits in
 // 32.6 us (67 with a division per channel), out in 21.6 (4.4 TB/s), both bound
 // by instructions first (72 % of the issue slots: rounding or unpacking, and
-// the addresses), out also by the loads' latency; bf16, 32 x 1-8 tokens: 4.4
-// us, the latency of lengths, table and rows one after the other.
+// the addresses), out also by the loads' latency; 8 bits out in 18.9 (7.0 TB/s with
+// what L2 holds); bf16, 32 x 1-8 tokens: 4.4 us, the latency of lengths, table and
+// rows one after the other.
 template <int kFormat, bool kRead, int kEach>
 __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const AppendArgs a, const FastDiv by_token) {
   constexpr bool kPacked = kFormat == SS_CACHE_INT4, kBytes = kFormat == SS_CACHE_FP8;

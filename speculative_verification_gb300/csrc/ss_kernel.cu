@@ -3445,6 +3445,6 @@ const char* ss_status_string(ss_status status) {
   return "unknown status";
 }
 
-const char* ss_version(void) { return "ss 0.6.0 (sm_103a)"; }
+const char* ss_version(void) { return "ss 0.7.0 (sm_103a)"; }
 
 }  // extern "C"

@@ -226,7 +226,7 @@ __device__ __forceinline__ uint4 turned(const StepArgs& a, const Turn& t, const 
 // token's rows of all heads, whose turns stay in registers.  Rows of 8 bits: 16
 // lanes per slot of the block, those that hold rows from before among them.
 template <int kFormat, bool kRope, bool kOdd>
-__global__ void __launch_bounds__(kThreads, kOdd ? 2 : !kRope ? 5 : kFormat == SS_CACHE_FP8 || kFormat == SS_CACHE_INT4 ? 3 : 4) step_kernel(const StepArgs a) {
+__global__ void __launch_bounds__(kThreads, kOdd ? 2 : !kRope ? 5 : kFormat > SS_CACHE_BF16 ? 3 : 4) step_kernel(const StepArgs a) {
   constexpr bool kBlocks = kFormat == SS_CACHE_FP8, kClose = kRope && (kBlocks || kFormat == SS_CACHE_INT4);
   constexpr int kEach = 4;
   __shared__ __align__(16) float s_cos[kRope ? kGroups : 1][kPairs], s_sin[kRope ? kGroups : 1][kPairs];
