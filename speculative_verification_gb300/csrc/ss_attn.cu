@@ -127,7 +127,9 @@ static ss_status attention(const ss_attention_args* args, int32_t stall, void* w
   // Rows per item: the rows that a request can have, up to what the kernel
   // holds.  More rows per item read the cache fewer times; unused rows cost
   // tensor-core and softmax time (clocks a tile, bf16: 2550 for 8 rows, where the
-  // copy bounds it, 2900 for 128; 4 bits: 1390 for 8, 2700 for 64).
+  // copy bounds it, 2900 for 128; 4 bits: 1390 for 8, 2700 for 64).  8 bits, 64
+  // rows against 32: 48 x 1-8 drafts 250 us, 293; 16 trees 125, 164; 2 x 4096
+  // prompt 529, 797; a kernel of 128 spills its registers (670 and more).
   const int64_t rows = static_cast<int64_t>(a.max_queries) * a.group;
   const int32_t most = a.c.format == SS_CACHE_BF16 ? 128 : 64;
   a.block_rows = 8;

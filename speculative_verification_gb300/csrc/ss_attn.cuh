@@ -202,8 +202,12 @@ struct Cfg {
   static constexpr bool kConv = kBytes && kLive >= 32;
   // What an item costs beyond its tiles, in tiles: with it the line is cut into
   // parts that take equally long (4.2 us an item, 1.4 a tile; 2 x 4096 prompt, where
-  // CTAs had 25 to 60 items: 583 -> 525 us; 2 instead of 3: 540)
-  static constexpr int kExtra = kConv ? 3 : 0;
+  // CTAs had 25 to 60 items: 583 -> 525 us; 2 instead of 3: 540).  Where CTAs have
+  // few tiles it also keeps the end of one item and the start of the next, each
+  // with its piece to leave, from the same CTA (4 x 1-3 tokens over 1-2k: 22.4 ->
+  // 16.3 us; over 3-6k 24.3 -> 16.9, with 1 or 2 19.5 and more).  The roles then
+  // end at an item without tiles, as none knows how many tiles its CTA has.
+  static constexpr int kExtra = kBytes ? 3 : 0;
   static constexpr int kThreads = 128 + kSoft + kUnpack;
   // Registers per thread by warpgroup where one size does not fit all: the
   // launch's kThreads x kRegs are shared out again (all or none of them).
@@ -894,7 +898,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves, kBytes>::kThreads
     for (int i = 0; i < kNQ; ++i) {
       mbar_init(mfull + i, 32 + more(SS_STALL_ITEMS));
       mbar_init(qfull + i, (F::kConv ? F::kSoft : 32) + more(SS_STALL_QUERIES));
-      mbar_init(qempty + i, 1 + F::kSoft / 32);
+      mbar_init(qempty + i, 1 + F::kSoft / 32 + (F::kExtra && F::kVGroups > 1 ? F::kUnpack / 32 : 0));
     }
     for (int i = 0; i < F::kQBufs; ++i) mbar_init(qfree + i, 1);
     if (kPacked)
@@ -1349,6 +1353,10 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves, kBytes>::kThreads
         if (take == 0) {  // no more: an item without tiles
           if (lane == 0) items[b].tiles = 0;
           mbar_arrive(mfull + b);
+          if constexpr (!F::kConv) {  // what the softmax warps wait for
+            if (k == 0) bar_sync(6, F::kSoft + 32);
+            mbar_arrive(qfull + b);
+          }
           break;
         }
       const int32_t rows = min(kLive, q.n * a.group - row0);
@@ -1503,14 +1511,15 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves, kBytes>::kThreads
       convert_queries<kLive, kEach, kBytes, F::kOneCol>(a, items[b], qbuf + k % F::kQBufs * F::kQ, row_qsum[kNibbles ? b : 0],
                                                         row_unit[b], st >> 5, kWarps);
     };
-    bool none = false;  // kConv: no item is left, or a wait for it has given up
+    bool none = false;  // kExtra: no item is left, or (kConv) a wait for it has given up
     for (int32_t k = 0; F::kExtra || done < my_tiles; ++k) {
       const int b = k % kNQ;
       if constexpr (kPacked)
         if (k == 0) {  // the first item's queries, for which everyone waits, by all of these warps
           // (given up: there is no item to read; the barrier all the same)
           const bool there = __all_sync(0xffffffffu, wait_or_dead(mfull, 0, dead));
-          if constexpr (F::kConv) none = !there || items[0].tiles == 0;
+          if constexpr (F::kExtra) none = there && items[0].tiles == 0;
+          if constexpr (F::kConv) none = none || !there;
           if (there && !none) convert(0);
           proxy_fence();
           if constexpr (F::kConv) {
@@ -1524,6 +1533,7 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves, kBytes>::kThreads
       if (lt < kCols) nref[h0 + lt] = 0.0f;
       // (4 bits: the rows' sums and units come with the queries)
       const bool in = none || wait_or_dead((kPacked ? qfull : mfull) + b, (k / kNQ) & 1, dead);
+      if constexpr (F::kExtra && !F::kConv) none = none || (in && items[b].tiles == 0);
       if (bar_any(5, F::kSoft, !in || none)) break;  // the same decision for every softmax thread
       // (8 bits: read where it is needed, registers are short)
       std::conditional_t<F::kConv, const Item&, const Item> it = items[b];
@@ -2047,14 +2057,23 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves, kBytes>::kThreads
     int32_t upto = 0, k = 0;  // the end of the items so far
 #pragma unroll 1
     for (int32_t at = (tid - 128 - F::kSoft) >> 7; F::kExtra || at < my_tiles; at += F::kVGroups) {
-      if constexpr (F::kExtra)
-        if (at == upto) {  // the next item
-          if (!__all_sync(0xffffffffu, wait_item(mfull + k % kNQ, (k / kNQ) & 1, dead))) break;
-          const int32_t tiles = items[k % kNQ].tiles;
-          if (tiles == 0) break;
+      if constexpr (F::kExtra) {
+        bool more = true;
+        while (more && at >= upto) {  // the next item
+          const int b = k++ % kNQ;
+          more = __all_sync(0xffffffffu, wait_item(mfull + b, ((k - 1) / kNQ) & 1, dead));
+          if (!more) break;
+          const int32_t tiles = items[b].tiles;
+          // (warpgroups that take turns may fall behind by items of which they have no tile)
+          if (F::kVGroups > 1) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(qempty + b);
+          }
+          more = tiles != 0;
           upto += tiles;
-          ++k;
         }
+        if (!more) break;
+      }
       const int32_t rs = at % F::kRawStages, s = at % kVs;
       if (!__all_sync(0xffffffffu, wait_or_dead(rfull + rs, (at / F::kRawStages) & 1, dead))) break;
       const uint8_t* src = raw + rs * F::kRaw;

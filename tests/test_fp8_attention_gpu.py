@@ -156,6 +156,15 @@ def test_many_items_for_every_block_of_rows(ss, workspace, group, dim):
     Problem8(ss, 40, lens, [1] * len(lens), 2 * group, 2, dim, 16).check(ss, workspace)
 
 
+@pytest.mark.parametrize("heads,news", [(4, 1), (8, 3), (40, 1), (16, 5)])
+@pytest.mark.parametrize("longest", [100, 300])
+def test_items_of_few_tiles(ss, workspace, heads, news, longest):
+    """Many items a CTA, of a tile each: not every warpgroup that unpacks values has one."""
+    rng = random.Random(longest)
+    lens = [rng.randint(longest - 100, longest) for _ in range(400)]
+    Problem8(ss, 41, lens, [news] * len(lens), heads, 2, 64, 32).check(ss, workspace)
+
+
 @pytest.mark.parametrize("order", ["pshd", "hpsd", "shpd"])
 def test_cache_layouts(ss, workspace, order):
     Problem8(ss, 22, [100, 300], [2, 5], 4, 2, 64, 16, order=order).check(ss, workspace)
