@@ -307,6 +307,8 @@ __global__ void __launch_bounds__(kThreads, kOdd ? 2 : !kRope ? 5 : kFormat > SS
   const int32_t block_page = kBlocks ? page_of(a.t, a.c, row, first_slot) : -1;  // a block lies in one page
   if constexpr (kRope) {
     load(first);  // on their way while the angles are computed
+    if constexpr (kClose && kOdd)  // a lane's channels that do not turn take part in its sums' check
+      for (int i = tid; i < kGroups * 2 * kPairs; i += kThreads) (&s_low[0][0])[i] = 0;
     if (tree) {  // depths by jumps of 1, 2, 4 .. parents: a warp, nodes i and i + 32 in lane i
       if (tid < 32) {
         int32_t up[2], depth[2];
