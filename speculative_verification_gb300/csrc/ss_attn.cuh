@@ -72,10 +72,10 @@
 // latency; 48 x 1-8 drafts, 64 rows, of which 44 % are without a query: 325 us,
 // instruction issue (54 % of the slots).  One token of one request: 12 us, all
 // latency.  8 bits, 32 x 1 token over 8-64k: 362 us, 6.5 TB/s, the cache's
-// bytes; 48 x 1-8 drafts over 1-16k, 64 rows: 246 us (floor 125), the softmax
-// chain and the copying warp's spilled registers; 16 trees over 2-12k, dim 64:
-// 118 us, 2 x 4096-token prompt chunks in a window: 529 us, both by the chain:
-// 1.4 us a tile and 4.2 an item.
+// bytes; 48 x 1-8 drafts over 1-16k, 64 rows: 246 us (floor 125); 16 trees over
+// 2-12k, dim 64: 118 us; 2 x 4096-token prompt chunks in a window: 525 us; by a
+// tile's chain through its roles, 1.4 us, and 4.2 an item.  The softmax is a fifth
+// of it (199, 96 and 436 without its arithmetic).
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>
