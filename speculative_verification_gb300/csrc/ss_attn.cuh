@@ -213,8 +213,9 @@ struct Cfg {
   // launch's kThreads x kRegs are shared out again (all or none of them).
   static constexpr int kRegs = kThreads > 640 ? 80 : kThreads > 512 ? 96 : kThreads > 384 ? 128 : 168;
   static constexpr bool kSplit = kPacked || kLive == 128;
-  static constexpr int kRegs0 = kBytes ? (kLive <= 16 ? 96 : kLive == 32 ? 56 : 40) : kStreams == 2 ? 56 : 64;                                   // copies, MMAs, queries
-  static constexpr int kRegsSoft = kBytes ? (kLive <= 16 ? 104 : kLive == 32 ? 88 : 96) : !kPacked || kStreams == 2 ? 104 : kLive >= 64 ? 152 : 136;
+  static constexpr int kRegs0 = kBytes ? (kLive <= 16 ? 96 : kLive == 32 ? 56 : 40) : kStreams == 2 ? 56 : 64;  // copies, MMAs, queries
+  static constexpr int kRegsSoft = kBytes ? (kLive <= 16 ? 104 : kLive == 32 ? 88 : 96)
+                                   : !kPacked || kStreams == 2 ? 104 : kLive >= 64 ? 152 : 136;
   static constexpr int kRegsUnpack = kBytes ? (kLive <= 16 ? 88 : kLive == 32 ? 72 : 56) : kLive >= 64 ? 56 : 72;
   static_assert(!kSplit || kRegs0 + kSoft / 128 * kRegsSoft + kUnpack / 128 * kRegsUnpack <= kThreads / 128 * kRegs,
                 "a warpgroup would wait for registers for ever");
@@ -1576,8 +1577,9 @@ __global__ void __launch_bounds__(Cfg<kLive, kPacked, kHalves, kBytes>::kThreads
         // depends on it.)
         const uint32_t there = *reinterpret_cast<volatile uint32_t*>(info + at % kInfo);
         // does some row miss some key of the tile?
-        const bool masked = F::kConv ? there != every || n < clear0 || n >= clear1 : sink || there != every || j0 + kTile - 1 > (tree ? it.base - 1 : first_pos) ||
-                            (a.window > 0 && j0 <= last_pos - a.window);
+        const bool masked = F::kConv ? there != every || n < clear0 || n >= clear1
+                                     : sink || there != every || j0 + kTile - 1 > (tree ? it.base - 1 : first_pos) ||
+                                           (a.window > 0 && j0 <= last_pos - a.window);
         float ka = a.scale_log2, kb = 0.0f, sv = 0.0f, wv = 0.0f;
         float big = 0.0f;  // log2 of the key's values, rounded up: 0 where it does not matter
         bool poison = false;

@@ -569,7 +569,8 @@ __global__ void __launch_bounds__(kThreads) compact_blocks_kernel(const CompactA
     const int32_t to_page = page_of(a.t, c, row, b << c.block_shift);
     const int32_t page = from < 0 ? -1 : page_of(a.t, c, row, from);
     const int64_t to = layer * c.layer_stride + to_page * c.page_stride + (at & in_page) * c.slot_stride + lane * 8;
-    const int64_t src = layer * c.layer_stride + max(page, 0) * c.page_stride + (max(from, int64_t{0}) & in_page) * c.slot_stride + lane * 8;
+    const int64_t src = layer * c.layer_stride + max(page, 0) * c.page_stride +
+                        (max(from, int64_t{0}) & in_page) * c.slot_stride + lane * 8;
     const int64_t to_scale = layer * c.s_layer_stride + to_page * c.s_page_stride + ((at & in_page) >> c.block_shift) * 4;
     const int64_t src_scale = layer * c.s_layer_stride + max(page, 0) * c.s_page_stride +
                               ((max(from, int64_t{0}) & in_page) >> c.block_shift) * 4;

@@ -98,7 +98,8 @@ __device__ __forceinline__ void circle(uint64_t turn, float magnitude, float2& c
   // hi + lo + (first + left of it) d + first sd + hi cd
   const auto sum = [&](float hi, float lo, float first, float first_lo) {
     const float f = first * d, h = hi + f, t = h - hi;
-    const float l = ((hi - (h - t)) + (f - t)) + (__fmaf_rn(first, d, -f) + __fmaf_rn(first, sd, __fmaf_rn(first_lo, d, __fmaf_rn(hi, cd, lo))));
+    const float small = __fmaf_rn(first, sd, __fmaf_rn(first_lo, d, __fmaf_rn(hi, cd, lo)));
+    const float l = ((hi - (h - t)) + (f - t)) + (__fmaf_rn(first, d, -f) + small);
     const float p = magnitude * h, e = __fmaf_rn(magnitude, h, -p) + magnitude * l, r = p + e;
     return make_float2(r, e - (r - p));
   };
@@ -375,7 +376,8 @@ __global__ void __launch_bounds__(kThreads, kOdd ? 2 : !kRope ? 5 : kFormat > SS
           if (h >= heads) break;
           uint4 y = x[e];
           if (kClose && !kBlocks && k >= 0 && v < 0)
-            y = turned<kOdd, kClose>(a, t, y, source(h) - lane * 16, lane, lanes, reinterpret_cast<const uint4*>(s_low[kClose ? token : 0]));
+            y = turned<kOdd, kClose>(a, t, y, source(h) - lane * 16, lane, lanes,
+                                     reinterpret_cast<const uint4*>(s_low[kClose ? token : 0]));
           else if (v < 0)
             y = turned<kOdd, false>(a, t, y, source(h) - lane * 16, lane, lanes, nullptr);
           if (k < 0 || kFormat == kNone) {
@@ -456,7 +458,9 @@ __global__ void __launch_bounds__(kThreads, kOdd ? 2 : !kRope ? 5 : kFormat > SS
         if (fresh && !is_v) {
 #pragma unroll
           for (int e = 0; e < kEach; ++e)
-            if (e < more) x[e] = turned<kOdd, kClose>(a, t, x[e], src - lane * 16 + e * a.k_head, lane, lanes, reinterpret_cast<const uint4*>(s_low[i - t0]));
+            if (e < more)
+              x[e] = turned<kOdd, kClose>(a, t, x[e], src - lane * 16 + e * a.k_head, lane, lanes,
+                                          reinterpret_cast<const uint4*>(s_low[i - t0]));
         }
       uint32_t top[kEach], most = 0;
 #pragma unroll
