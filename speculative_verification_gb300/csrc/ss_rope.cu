@@ -538,10 +538,14 @@ static void take_rope(StepArgs* a, const ss_rope_table* t) {
   a->magnitude = t->magnitude;
 }
 
-// As many CTAs per chunk as the GPU has room for, up to one for every four rows
-// of a token.
-static unsigned splits(int64_t chunks, int64_t rows) {
-  const int64_t spare = (4 * 152 + chunks - 1) / chunks, most = rows < 4 ? 1 : rows / 4;
+// As many CTAs per chunk as give every SM `each` of them, up to one for every four rows of
+// a token.  Three or four an SM: with keys and values that are encoded, whose CTAs
+// are longer, four (2 x 4096 tokens into 8 bits 60 us, 64 with three; 4 bits 69 and
+// 77; 32 trees into 8 bits 17.0 and 17.2); else three, as each computes the angles
+// again (bf16 51 and 48, half as many tokens 30.2 and 27.7; ss_rope of 4096 tokens
+// 16.3 and 15.3).
+static unsigned splits(int64_t chunks, int64_t rows, int64_t each) {
+  const int64_t spare = (each * 152 + chunks - 1) / chunks, most = rows < 4 ? 1 : rows / 4;
   const int64_t z = spare < most ? spare : most;
   return static_cast<unsigned>(z < 1 ? 1 : z > 64 ? 64 : z);
 }
@@ -554,7 +558,7 @@ static ss_status launch_step(const StepArgs& a, int32_t num_requests, cudaStream
   const int64_t x = kFormat == kNone ? (n + size - 1) / size : (n + 2 * size - 2) / size;
   const int64_t rows = a.q_heads + (kFormat == kNone ? 1ll : 2ll) * a.kv_heads;
   const int64_t wide = x < 1 ? 1 : x;
-  const dim3 grid(static_cast<unsigned>(wide), num_requests, splits(wide * num_requests, rows));
+  const dim3 grid(static_cast<unsigned>(wide), num_requests, splits(wide * num_requests, rows, kFormat > SS_CACHE_BF16 ? 4 : 3));
   if constexpr (kRope) {
     if (a.half % (a.layout == SS_ROPE_HALVES ? 8 : 4) != 0) {
       step_kernel<kFormat, true, true><<<grid, kThreads, 0, s>>>(a);
