@@ -656,11 +656,12 @@ ss_status ss_cache_read(const ss_append_args* args, ss_stream_t stream);
  * out_status: SS_ROW_BAD_PARAM (a count outside [0, max_queries], with parents
  * above SS_TREE_MAX_NODES, query rows outside [0, total_queries), a negative
  * kv_len, kv_len plus the count above 2^31 - 256, a table row outside the
- * table, about 2^31 or more tiles of 128 keys by up to 128 rows in one kv head:
- * the request's rows are not written; or a parent outside [0, i): the
+ * table, about 2^31 or more tiles of 128 keys by up to 128 rows in one kv head
+ * (4 and 8 bits: 64 rows; 8 bits: three tiles more count for each block of
+ * rows): the request's rows are not written; or a parent outside [0, i): the
  * node is taken as a child of the root), SS_ROW_BAD_INDEX (slots beyond the
- * table: they are holes), SS_ROW_LIMIT (about 2^31 or more such tiles in all
- * requests, fewer with more than 64 kv heads: no rows are written),
+ * table: they are holes), SS_ROW_LIMIT (about 2^31 or more such tiles, counted
+ * alike, in all requests, fewer with more than 64 kv heads: no rows are written),
  * SS_ROW_TIMEOUT (a bounded wait gave up: the request's rows are undefined, and
  * the workspace must be zeroed again; until then every call with it reports
  * this for its requests).

@@ -113,7 +113,7 @@ constexpr float kUnset = 3.0e38f;         // in a piece: minus the reference of 
 template <bool kPacked> constexpr float kSlack = kPacked ? 15.0f : 16.0f;
 constexpr float kDeep = 32.0f;
 constexpr float kTop = 8.0f;
-constexpr int kMostExtra = 3;             // Cfg::kExtra at most
+constexpr int kExtra8 = 3;                // Cfg::kExtra of 8 bits
 constexpr int kSlotFloats = 128 * 130;    // one piece: up to 128 rows of 128 channels, r and l
 
 struct AttnArgs {
@@ -123,6 +123,7 @@ struct AttnArgs {
   uint32_t group_mul, group_shift;  // n / group = (n * group_mul >> 32) >> group_shift, n < 2^31
   int32_t block_rows;  // rows of an item (the kernel's kLive)
   int32_t table_end;   // slots of a table row, at most 2^31 - 1
+  int32_t extra_tiles; // Cfg::kExtra: tiles that an item counts beyond its own
   int32_t few_tiles;   // the requests' tiles for one head stay below 2^31, whatever the lengths
   int32_t most_tiles;  // that a call may have for one head
   const int32_t* offsets;
@@ -207,7 +208,7 @@ struct Cfg {
   // with its piece to leave, from the same CTA (4 x 1-3 tokens over 1-2k: 22.4 ->
   // 16.3 us; over 3-6k 24.3 -> 16.9, with 1 or 2 19.5 and more).  The roles then
   // end at an item without tiles, as none knows how many tiles its CTA has.
-  static constexpr int kExtra = kBytes ? 3 : 0;
+  static constexpr int kExtra = kBytes ? kExtra8 : 0;
   static constexpr int kThreads = 128 + kSoft + kUnpack;
   // Registers per thread by warpgroup where one size does not fit all: the
   // launch's kThreads x kRegs are shared out again (all or none of them).
@@ -680,7 +681,7 @@ __device__ __forceinline__ Request request_of(const AttnArgs& a, int32_t r) {
     const uint32_t all = min(q.base + q.n, a.table_end);
     const uint32_t keys = a.window > 0 ? min(all, a.window + 2u * kTile) + min(static_cast<uint32_t>(a.sinks), all) : all;
     const uint32_t blocks = (static_cast<uint32_t>(q.n * a.group - 1) >> (31 - __clz(a.block_rows))) + 1;
-    q.ok = (static_cast<uint64_t>(blocks) * (keys / kTile + 3 + kMostExtra)) >> 31 == 0;
+    q.ok = (static_cast<uint64_t>(blocks) * (keys / kTile + 3 + a.extra_tiles)) >> 31 == 0;
   }
   if (!q.ok) q.n = 0;
   return q;
