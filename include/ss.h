@@ -543,9 +543,10 @@ typedef enum {
                        with 448 s >= |x| for every finite value x of the block's rows, and n = x / s rounded to
                        nearest even (a power of two: the scale costs no bit of x); a value that is not finite
                        becomes the NaN of e4m3 and counts for no scale.  The rows of a block are those up to the
-                       request's last token: rows that were there before are read with the old scale and
-                       written again with the new one, rows past them are left.  So a row's small values are
-                       held to 2^-10 s, half of e4m3's smallest step, s by the largest value beside it.
+                       request's last token: rows that were there before are read with the old scale (s n as
+                       fp32 has it) and written again with the new one, rows past them are left.  So a row's
+                       small values are held to 2^-10 s, half of e4m3's smallest step, s by the largest value
+                       beside it.
                        Attention and the reading calls take any scales.  The scale arrays hold s per block. */
 } ss_cache_format;
 
@@ -595,8 +596,8 @@ typedef struct {
 
 /* ss_cache_append writes the new tokens' keys and values of one layer (k and
  * v are read); ss_cache_read reads the same rows back as bf16 (k and v are
- * written; 4-bit values s * n + m and 8-bit values s * n rounded once).
- * Request r has the rows
+ * written; 8-bit values s * n are rounded once, with any scale; 4-bit values
+ * are the bf16 of s * n + m as fp32 has it).  Request r has the rows
  * token_offsets[r] .. token_offsets[r + 1] - 1 of k and v, at the slots from
  * kv_len[r].  out_status: SS_ROW_BAD_PARAM (a count outside [0, max_tokens],
  * rows outside [0, total_tokens), a negative kv_len or a table row outside the

@@ -117,11 +117,8 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const AppendArgs a, c
         }
 #pragma unroll
         for (int u = 0; u < kEach; ++u) {
-          float f[8];
-          decode8(w[u], s[u], f);
-          if (live)
-            *reinterpret_cast<uint4*>(to + u * a.head_stride) =
-                make_uint4(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7]));
+          const uint4 y = read8(w[u], s[u]);
+          if (live) *reinterpret_cast<uint4*>(to + u * a.head_stride) = y;
         }
         continue;
       }
@@ -151,11 +148,7 @@ __global__ void __launch_bounds__(kThreads, 4) rows_kernel(const AppendArgs a, c
 #pragma unroll
     for (int u = 0; u < kEach; ++u) {
       if (kRead) {  // (a step and a low value, or a scale, of 0 give the zeros of a hole)
-        if (kBytes) {
-          float f[8];
-          decode8(make_uint2(x[u].x, x[u].y), __uint_as_float(pair[u]), f);
-          x[u] = make_uint4(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7]));
-        }
+        if (kBytes) x[u] = read8(make_uint2(x[u].x, x[u].y), __uint_as_float(pair[u]));
         if (live) *reinterpret_cast<uint4*>(flat(u)) = kPacked ? dequantise8(word[u], pair[u]) : x[u];
       } else if (kPacked) {
         const uint32_t w = quantise8(x[u], live, lanes, pair[u]);

@@ -150,6 +150,25 @@ __device__ __forceinline__ void decode8(uint2 w, float s, float (&x)[8]) {
   }
 }
 
+// What eight bytes stand for, in bf16, rounded once.  By a power of two the product
+// is exact in fp32; by another scale it has up to 28 bits and is rounded to odd (toward
+// zero, the last bit set where something is left), so that the rounding to bf16
+// knows on which side of a tie it lay.
+__device__ __forceinline__ uint4 read8(uint2 w, float s) {
+  float f[8];
+  if ((__float_as_uint(s) & 0x7fffffu) == 0) {
+    decode8(w, s, f);
+  } else {
+    decode8(w, 1.0f, f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t down = __float_as_uint(__fmul_rd(f[i], s)), up = __float_as_uint(__fmul_ru(f[i], s));
+      f[i] = __uint_as_float(min(down, up) | static_cast<uint32_t>(down != up));
+    }
+  }
+  return make_uint4(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7]));
+}
+
 // The largest magnitude of eight bf16 values, as bits (0x7f80 and up: one is not
 // finite): magnitudes compare as integers, in pairs.
 __device__ __forceinline__ uint32_t magnitude(const uint4& x) {
