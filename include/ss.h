@@ -854,8 +854,12 @@ ss_status ss_rope(const ss_rope_args* args, ss_stream_t stream);
  * and there, next to ties, a unit of bf16 apart from ss_rope's, which in those
  * formats could have become a step.
  * `append` describes the requests, k and v; k is not written.  out_status
- * (append's): the larger of both calls' codes; SS_ROW_BAD_PARAM for a request
- * that either refuses: nothing of it is touched. */
+ * (append's): the larger of both calls' codes.  SS_ROW_BAD_PARAM thus has two
+ * meanings: a request that either call refuses, of which nothing is touched
+ * (counts, rows, kv_len or table row as they say there); or one with a parent
+ * outside [0, i), which is done like any other, that node as a child of the
+ * root: its queries, keys, values and (8 bits) its blocks' earlier rows are
+ * written, but for tokens without a page, of which this code says nothing. */
 typedef struct {
   const ss_rope_table* rope;
   const ss_append_args* append;
