@@ -546,12 +546,27 @@ typedef enum {
                        request's last token: rows that were there before are read with the old scale (s n as
                        fp32 has it) and written again with the new one, rows past them are left.  So a row's
                        small values are held to 2^-10 s, half of e4m3's smallest step, s by the largest value
-                       beside it.
+                       beside it; and for good, whatever becomes of that value: see "8 bits and drafts".
                        Attention and the reading calls take any scales.  The scale arrays hold s per block. */
 } ss_cache_format;
 
 /* Slots of a page that share a scale in an SS_CACHE_FP8 cache. */
 #define SS_FP8_BLOCK 16
+
+/* 8 bits and drafts.  A draft shares its block's scale with the rows before it and
+ * beside it, the last emitted tokens and the other branches of a tree among
+ * them.  A draft's value that is finite and more than 2^14 times as large as a
+ * small one of those rows takes bits from it in the step in which the draft is
+ * tried, and these do not come back when the draft is rejected: a later append
+ * or ss_pages_compact gives the block a smaller scale again, of the values as
+ * they are by then.  So what a row holds, and with it the text, can depend on
+ * the drafts that were tried.  The bound: a value x that was in a block with
+ * scales up to s is held to 2^-4 |x| + 2^-9 s.  Rows of blocks that were full
+ * before the step are not touched, and the bf16 and 4-bit formats, whose rows are
+ * apart, know none of this.  Who wants it for 8 bits too tries the drafts in a
+ * fork (ss_pages_fork copies the page that is partly filled), gives the fork's
+ * pages back (ss_pages_trim to length 0) and appends the accepted tokens to
+ * the row that was forked: it then holds what a run without those drafts does. */
 
 /* One cache: [num_layers][num_pages][num_kv_heads][page_size] rows of K and of
  * V in any order of those four (strides in bytes, the same for K and V). */
@@ -640,8 +655,9 @@ ss_status ss_cache_read(const ss_append_args* args, ss_stream_t stream);
  * keys at positions > p - window or < sinks (a draft key of a tree is at its
  * node's position).  A query that sees nothing (holes) gets out = 0 and
  * lse = -infinity.  Keys and values that a query does not see never reach its
- * result, whatever they hold (8 bits: nor does a NaN or an infinity in a scale
- * that only they have).  A query that sees a NaN or an infinity gets
+ * result, whatever the cache holds there (8 bits: nor does a NaN or an infinity
+ * in a scale that only they have; what their append did to the rows beside them
+ * is another matter, see "8 bits and drafts").  A query that sees a NaN or an infinity gets
  * results that are not finite or, for an infinite key, weights of 0 and 1
  * (lse stays finite where only a value is not).
  *
