@@ -865,10 +865,10 @@ ss_status ss_rope(const ss_rope_args* args, ss_stream_t stream);
 /* ss_rope_append: ss_rope on the queries and keys, and ss_cache_append of the
  * turned keys (as bf16 has them) and of the values, in one launch: the turned
  * keys go nowhere else.  A cache of bf16 holds what the two calls would leave
- * there.  Keys for 8 or 4 bits are summed to about 2^-33 of |x| + |y| before
- * their rounding to bf16 (but in a row with a value that is not finite): here
- * and there, next to ties, a unit of bf16 apart from ss_rope's, which in those
- * formats could have become a step.
+ * there.  Keys for 8 or 4 bits are summed to 2^-32 of magnitude (|x| + |y|)
+ * before they are rounded to fp32 and from there to bf16 (but in a row with a
+ * value that is not finite): here and there, next to ties, a unit of bf16
+ * apart from ss_rope's, which in those formats could have become a step.
  * `append` describes the requests, k and v; k is not written.  out_status
  * (append's): the larger of both calls' codes.  SS_ROW_BAD_PARAM thus has two
  * meanings: a request that either call refuses, of which nothing is touched

@@ -146,7 +146,9 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
   return r;
 }
 
-// Two fp32 operations in one instruction.
+// Two fp32 operations in one instruction.  A mul_2 and an add_2 behind it become one
+// fused step, in spite of their .rn: where each has to round, use __fmul_rn and
+// __fadd_rn, which stay apart.
 __device__ __forceinline__ uint64_t two(float a, float b) {
   return static_cast<uint64_t>(__float_as_uint(b)) << 32 | __float_as_uint(a);
 }

@@ -11,11 +11,12 @@
 //   cos(A + d) = cos A + (cos A (cos d - 1) - sin A sin d), likewise the sine,
 // where what is added is small, so that both come out to 2^-34, as two floats.
 // Rotations are fp32 sums of the first.  Those of keys that go into a cache of 8
-// or 4 bits take the second too and carry their remainders, so that they are
-// rounded to bf16 as the exact sums are: there a unit of bf16 may become a step
-// of the cache (one key in some 20,000 is rounded the other way in fp32).  It costs
-// 16 registers a thread, and would cost 10 us of a prompt's 64 in bf16.  In 8 bits the rows of a block (16 slots of one head) share a
-// power of two by their largest value (ss_rows.cuh).
+// or 4 bits take the second too and carry their remainders (2^-32 of magnitude
+// (|x| + |y|)), so that they are rounded to fp32, and from there to bf16, as the exact
+// sums are: there a unit of bf16 may become a step of the cache (one key in some
+// 20,000 is rounded the other way in plain fp32).  It costs 16 registers a thread.
+// In 8 bits the rows of a block (16 slots of one head) share a power of two by
+// their largest value (ss_rows.cuh).
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -91,17 +92,19 @@ __device__ __forceinline__ void circle(uint64_t turn, float magnitude, float2& c
   const int32_t left = static_cast<int32_t>(static_cast<int64_t>(turn - (static_cast<uint64_t>(k) << 56)) >> 24);
   constexpr double kUnit = 6.283185307179586 / 1099511627776.0;  // 2 pi / 2^40
   constexpr float kHigh = static_cast<float>(kUnit), kLow = static_cast<float>(kUnit - static_cast<double>(kHigh));
-  const float n = static_cast<float>(left & ~0xff), m = static_cast<float>(left & 0xff), d = n * kHigh;
+  const float n = static_cast<float>(left & ~0xff), m = static_cast<float>(left & 0xff), d = __fmul_rn(n, kHigh);
   const float rest = __fmaf_rn(n, kHigh, -d) + __fmaf_rn(n, kLow, m * kHigh);  // the angle less d
   const float d2 = d * d, sd = __fmaf_rn(d * d2, -1.0f / 6.0f, rest), cd = d2 * __fmaf_rn(d2, 1.0f / 24.0f, -0.5f);
   const float4 a = kCircle.at[k & 255u];
   // hi + lo + (first + left of it) d + first sd + hi cd
   const auto sum = [&](float hi, float lo, float first, float first_lo) {
-    const float f = first * d, h = hi + f, t = h - hi;
+    // (each rounding is said: none of these may be joined with another)
+    const float f = __fmul_rn(first, d), h = __fadd_rn(hi, f), t = __fsub_rn(h, hi);
     const float small = __fmaf_rn(first, sd, __fmaf_rn(first_lo, d, __fmaf_rn(hi, cd, lo)));
-    const float l = ((hi - (h - t)) + (f - t)) + (__fmaf_rn(first, d, -f) + small);
-    const float p = magnitude * h, e = __fmaf_rn(magnitude, h, -p) + magnitude * l, r = p + e;
-    return make_float2(r, e - (r - p));
+    const float l =
+        __fadd_rn(__fadd_rn(__fsub_rn(hi, __fsub_rn(h, t)), __fsub_rn(f, t)), __fadd_rn(__fmaf_rn(first, d, -f), small));
+    const float p = __fmul_rn(magnitude, h), e = __fmaf_rn(magnitude, l, __fmaf_rn(magnitude, h, -p)), r = __fadd_rn(p, e);
+    return make_float2(r, __fsub_rn(e, __fsub_rn(r, p)));
   };
   c = sum(a.x, a.y, -a.z, -a.w);
   s = sum(a.z, a.w, a.x, a.y);
@@ -145,8 +148,9 @@ __device__ __forceinline__ int low_at(int ch) { return (ch & 4) * 16 + (ch >> 3)
 
 // One row's 8 channels, turned.  All 16 lanes of the row call it.  `row` is the
 // row in global memory, read again where lanes' channels do not pair up (kOdd).
-// kClose: sums to about 2^-33 of |x c| + |partner s| before they are rounded, with
-// `low`, what the floats c and s leave (cosine's below, sine's above in a word).
+// kClose: sums to 2^-32 of magnitude (|x| + |partner|) before they are rounded, to fp32 and
+// to bf16, with `low`, what the floats c and s leave (cosine's below, sine's above in a
+// word): these are known to 2^-34.3 of the magnitude, and rounded to bf16 by 2^-33 of it.
 template <bool kOdd, bool kClose>
 __device__ __forceinline__ uint4 turned(const StepArgs& a, const Turn& t, const uint4& x, const uint8_t* row, int lane,
                                         uint32_t lanes, const uint4* low) {
@@ -182,20 +186,37 @@ __device__ __forceinline__ uint4 turned(const StepArgs& a, const Turn& t, const 
   if constexpr (kClose) {
     const uint4 l0 = low[lane], l1 = low[lane + kRowLanes];
     const uint32_t l[8] = {l0.x, l0.y, l0.z, l0.w, l1.x, l1.y, l1.z, l1.w};
-    const uint64_t minus = two(-1.0f, -1.0f);
     uint64_t all = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      // sum = a + b with a = v c, b = p s: what the sum took of either (sum - b; the
-      // rest), and what is left of them
-      const uint64_t v = two(bf16_lo(w[i]), bf16_hi(w[i])), b = mul_2(p[i], t.s[i]), sum = fma_2(v, t.c[i], b);
-      const uint64_t of_a = fma_2(b, minus, sum), less_a = fma_2(sum, minus, b), less_b = fma_2(sum, minus, of_a);
-      // the sine's low part keeps the cosine's bits below its own: 2^-8 of 2^-25
-      const uint64_t left = add_2(fma_2(v, two(bf16_lo(l[2 * i]), bf16_lo(l[2 * i + 1])), fma_2(v, t.c[i], less_a)),
-                                  fma_2(p[i], two(__uint_as_float(l[2 * i]), __uint_as_float(l[2 * i + 1])), fma_2(p[i], t.s[i], less_b)));
+      // sum = a + b of two fp32 numbers, the rounded products: then what the sum took of
+      // either (sum - b; the rest) is exact, and with it what is left of v c and p s (of
+      // a sum in one fused step, whose bits may end below b's, it is not).  One float at
+      // a time: of products and sums of two at once the compiler makes fused steps,
+      // whatever their roundings are said to be (fp8 prompt 49.4 us in a graph with such
+      // steps, 51.6; 53.4 with two at once and products kept apart by adding a -0 that
+      // the compiler does not know, which takes more registers).
+      float c[2], s[2], q[2], sum[2], less_a[2], less_b[2];
+      split(t.c[i], c[0], c[1]);
+      split(t.s[i], s[0], s[1]);
+      split(p[i], q[0], q[1]);
+      const float x2[2] = {bf16_lo(w[i]), bf16_hi(w[i])};
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float b = __fmul_rn(q[e], s[e]);
+        sum[e] = __fadd_rn(__fmul_rn(x2[e], c[e]), b);
+        less_a[e] = __fsub_rn(b, sum[e]);
+        less_b[e] = -__fadd_rn(sum[e], less_a[e]);
+      }
+      const uint64_t v = two(x2[0], x2[1]);
+      // (the sine's low part with the cosine's bits below: rounded with them)
+      const uint64_t of_x = fma_2(v, t.c[i], two(less_a[0], less_a[1]));
+      const uint64_t of_p = fma_2(p[i], t.s[i], two(less_b[0], less_b[1]));
+      const uint64_t left = add_2(fma_2(v, two(bf16_lo(l[2 * i]), bf16_lo(l[2 * i + 1])), of_x),
+                                  fma_2(p[i], two(__uint_as_float(l[2 * i]), __uint_as_float(l[2 * i + 1])), of_p));
       all = add_2(all, left);
       float lo, hi;
-      split(add_2(sum, left), lo, hi);
+      split(add_2(two(sum[0], sum[1]), left), lo, hi);
       o[i] = bf16_pair(lo, hi);
     }
     float lo, hi;
@@ -351,7 +372,10 @@ __global__ void __launch_bounds__(kThreads, kOdd ? 2 : !kRope ? 5 : kFormat > SS
       s_sin[token][pair] = s.x;
       if constexpr (kClose) {
         const int ch = a.layout == SS_ROPE_HALVES ? pair : 2 * pair, partner = a.layout == SS_ROPE_HALVES ? pair + a.half : ch + 1;
-        const uint32_t low = bf16_pair(c.y, s.y);
+        // the cosine's low part as bf16 below; above it what brings the word, as a float, nearest to the sine's
+        const uint32_t lower = bf16_pair(c.y, 0.0f), sine = __float_as_uint(s.y);
+        const int32_t upper = static_cast<int32_t>(sine & 0x7fffffffu) + 0x8000 - static_cast<int32_t>(lower);
+        const uint32_t low = (sine & 0x80000000u) | (static_cast<uint32_t>(max(upper, 0)) & 0x7fff0000u) | lower;
         s_low[token][low_at(ch)] = low ^ 0x80000000u;
         s_low[token][low_at(partner)] = low;
       }
