@@ -62,20 +62,21 @@
 // item's queries and masks, then the softmax warps (128 threads per 8 to 32
 // rows) and for 4 and 8 bits those that unpack.
 //
-// Measured on one GB300, and what bounds it: bf16, 32 requests of 1-8 drafts
-// over 1-32k tokens (32 heads on 8, dim 128): 244 us, 6.68 TB/s, the cache's
-// bytes.  2 x 4096-token prompt chunks in a window of 1024: 313 us, 412
-// TFLOP/s; 16 trees over 2-12k tokens, dim 64: 85 us; both by the chain of one
-// tile's softmax, 2900 clocks for 128 x 128 weights (the powers alone take
-// 1024), in which all softmax warps are in one phase.  4 bits, 32 x 1 token over
-// 8-64k: 365 us, 3.43 TB/s, 1390 clocks a tile, the unpacking's and the waits'
-// latency; 48 x 1-8 drafts, 64 rows, of which 44 % are without a query: 325 us,
-// instruction issue (54 % of the slots).  One token of one request: 12 us, all
-// latency.  8 bits, 32 x 1 token over 8-64k: 362 us, 6.5 TB/s, the cache's
-// bytes; 48 x 1-8 drafts over 1-16k, 64 rows: 246 us (floor 125); 16 trees over
-// 2-12k, dim 64: 118 us; 2 x 4096-token prompt chunks in a window: 525 us; by a
-// tile's chain through its roles, 1.4 us, and 4.2 an item.  The softmax is a fifth
-// of it (199, 96 and 436 without its arithmetic).
+// Measured on one GB300 (calls in sequence unless said otherwise), and what
+// bounds it: bf16, 32 requests of 1-8 drafts over 1-32k tokens (32 heads on 8,
+// dim 128): 244 us, 6.68 TB/s, the cache's bytes.  2 x 4096-token prompt chunks
+// in a window of 1024: 313 us, 412 TFLOP/s; 16 trees over 2-12k tokens, dim 64:
+// 85 us; both by the chain of one tile's softmax, 2900 clocks for 128 x 128
+// weights (the powers alone take 1024), in which all softmax warps are in one
+// phase.  4 bits, 32 x 1 token over 8-64k: 365 us, 3.43 TB/s, 1390 clocks a
+// tile, the unpacking's and the waits' latency; 48 x 1-8 drafts, 64 rows, of
+// which 44 % are without a query: 325 us, instruction issue (54 % of the slots).
+// One token of one request: 12 us, all latency.  8 bits, 32 x 1 token over
+// 8-64k: 362 us, 6.5 TB/s, the cache's bytes; 48 x 1-8 drafts over 1-16k, 64
+// rows: 246 us (floor 125); 16 trees over 2-12k, dim 64: 118 us; 2 x 4096-token
+// prompt chunks in a window: 525 us; by a tile's chain through its roles, 1.4
+// us, and 4.2 an item.  The softmax is a fifth of it (199, 96 and 436 without
+// its arithmetic).
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -204,10 +205,10 @@ struct Cfg {
   // What an item costs beyond its tiles, in tiles: with it the line is cut into
   // parts that take equally long (4.2 us an item, 1.4 a tile; 2 x 4096 prompt, where
   // CTAs had 25 to 60 items: 583 -> 525 us; 2 instead of 3: 540).  Where CTAs have
-  // few tiles it also keeps the end of one item and the start of the next, each
-  // with its piece to leave, from the same CTA (4 x 1-3 tokens over 1-2k: 22.4 ->
-  // 16.3 us; over 3-6k 24.3 -> 16.9, with 1 or 2 19.5 and more).  The roles then
-  // end at an item without tiles, as none knows how many tiles its CTA has.
+  // few tiles it also keeps the end of one item and the start of the next, each with
+  // its piece to leave, from the same CTA (in a graph, 4 x 1-3 tokens over 1-2k:
+  // 22.4 -> 16.3 us; over 3-6k 24.3 -> 16.9, with 1 or 2 19.5 and more).  The roles
+  // then end at an item without tiles, as none knows how many tiles its CTA has.
   static constexpr int kExtra = kBytes ? kExtra8 : 0;
   static constexpr int kThreads = 128 + kSoft + kUnpack;
   // Registers per thread by warpgroup where one size does not fit all: the

@@ -536,7 +536,9 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactArgs a) 
 // in ss_rope.cu), kEach heads of K or V at a time.  Sources lie at or behind
 // their places, so those of later blocks lie behind the block being written: a
 // block's reads end at the barrier for its scales, before its writes and the
-// next block's reads.
+// next block's reads.  64 requests, 32 layers, up to 7 accepted rows: 69 us in a graph
+// (bf16 9.7), 94 alone after a flush of L2: all rows of the blocks are read and
+// written, block after block with a barrier for each four heads.
 __global__ void __launch_bounds__(kThreads) compact_blocks_kernel(const CompactArgs a) {
   constexpr int kEach = 4;
   __shared__ uint32_t s_top[3][2 * kEach];

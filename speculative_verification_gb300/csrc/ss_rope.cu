@@ -117,8 +117,6 @@ struct Turn {
   uint32_t on;  // channels that turn
 };
 
-// kOdd: pairs that do not come eight by eight (halves of rot_dim not in
-// multiples of 8 channels, interleaved ones that end inside a lane's channels).
 __device__ __forceinline__ Turn turn_of(const StepArgs& a, const float* cos_of, const float* sin_of, int lane) {
   Turn t;
   t.on = 0;
@@ -146,8 +144,10 @@ __device__ __forceinline__ Turn turn_of(const StepArgs& a, const float* cos_of, 
 // leave: a lane's 8 in two reads without conflicts.
 __device__ __forceinline__ int low_at(int ch) { return (ch & 4) * 16 + (ch >> 3) * 4 + (ch & 3); }
 
-// One row's 8 channels, turned.  All 16 lanes of the row call it.  `row` is the
-// row in global memory, read again where lanes' channels do not pair up (kOdd).
+// One row's 8 channels, turned.  All 16 lanes of the row call it.
+// kOdd: pairs that do not come eight by eight (halves of rot_dim not in multiples of
+// 8 channels, interleaved ones that end inside a lane's channels).  `row` is the row
+// in global memory, read again where lanes' channels do not pair up.
 // kClose: sums to 2^-32 of magnitude (|x| + |partner|) before they are rounded, to fp32 and
 // to bf16, with `low`, what the floats c and s leave (cosine's below, sine's above in a
 // word): these are known to 2^-34.3 of the magnitude, and rounded to bf16 by 2^-33 of it.
@@ -249,13 +249,14 @@ __device__ __forceinline__ uint4 turned(const StepArgs& a, const Turn& t, const 
 // token's rows of all heads, whose turns stay in registers.  Rows of 8 bits: 16
 // lanes per slot of the block, those that hold rows from before among them.
 //
-// Alone, cold: 4 x 4096 tokens, 32 heads on 8, 64 of 128 channels turned: 53 us,
-// 6.3 TB/s, loads' latency and 56 % of the issue slots; 2 x 4096 tokens into bf16:
-// 39 us, 61 % of the slots (100 to 126 instructions for two rows).  Without turns, 4
-// x 2-6k tokens into 8 bits: 21 us, 64 % of the slots.  32 trees of 9-48 nodes into 8
-// bits: 15.6 us, barriers and latency.  Registers set the CTAs of an SM: four where
-// 64 of them do, three with the keys' close sums (at 64 they spill: 67 -> 70 us for
-// the prompt when it had them), five without turns.
+// One cold launch under ncu (whose writes may still be in L2 at its end): 4 x 4096
+// tokens, 32 heads on 8, 64 of 128 channels turned: 53 us, loads' latency and 56 % of
+// the issue slots; 2 x 4096 tokens into bf16: 39 us, 61 % of the slots (100 to 126
+// instructions for two rows).  Without turns, 4 x 2-6k tokens into 8 bits: 21 us, 64 %
+// of the slots.  32 trees of 9-48 nodes into 8 bits: 16.8 us, barriers and latency.
+// In a graph, the append alone: 2 x 4096 tokens into bf16 38 us, 8 bits 52, 4 bits 60;
+// the 32 trees 13.4.  Registers set the CTAs of an SM: four where 64 of them do, three
+// with the keys' close sums (80, which already spill), five without turns.
 template <int kFormat, bool kRope, bool kOdd>
 __global__ void __launch_bounds__(kThreads, kOdd ? 2 : !kRope ? 5 : kFormat > SS_CACHE_BF16 ? 3 : 4) step_kernel(const StepArgs a) {
   constexpr bool kBlocks = kFormat == SS_CACHE_FP8, kClose = kRope && (kBlocks || kFormat == SS_CACHE_INT4);
@@ -564,10 +565,9 @@ static void take_rope(StepArgs* a, const ss_rope_table* t) {
 
 // As many CTAs per chunk as give every SM `each` of them, up to one for every four rows of
 // a token.  Three or four an SM: with keys and values that are encoded, whose CTAs
-// are longer, four (2 x 4096 tokens into 8 bits 60 us, 64 with three; 4 bits 69 and
-// 77; 32 trees into 8 bits 17.0 and 17.2); else three, as each computes the angles
-// again (bf16 51 and 48, half as many tokens 30.2 and 27.7; ss_rope of 4096 tokens
-// 16.3 and 15.3).
+// are longer, four (in a graph, 2 x 4096 tokens into 8 bits 51.7 us, 55.5 with three; 4
+// bits 59.5 and 68.0; 32 trees into 8 bits 13.4 and 13.8); else three, as each computes
+// the angles again (bf16 39.5 with four and 37.8, half as many tokens 22.7 and 20.5).
 static unsigned splits(int64_t chunks, int64_t rows, int64_t each) {
   const int64_t spare = (each * 152 + chunks - 1) / chunks, most = rows < 4 ? 1 : rows / 4;
   const int64_t z = spare < most ? spare : most;
