@@ -665,6 +665,8 @@ ss_status ss_cache_read(const ss_append_args* args, ss_stream_t stream);
  * bf16 (4 and 8 bits: to f16, in which those 2^22 and more below the query's
  * largest lose bits and those 2^33 below it are 0) before they meet the values.
  * Queries meet 4- and 8-bit keys to 2^-21 of a row's largest channel at least.
+ * lse is held to some units of 2^-24 of its size, and with 4 and 8 bits of log2 of
+ * the values' magnitude too, which a row's reference counts there.
  * Results are right for values up to 2^110 over the query's number of keys
  * (4 and 8 bits: 2^100) in magnitude; values below 2^-80 may count as 0.  The result
  * does not depend on timing: the work is split over the SMs by the lengths
